@@ -66,10 +66,8 @@
 // over through mbarriers, so one that gives up leaves no other waiting on a
 // hardware barrier (the FP8 stagers' named barrier is reached by all four
 // stager warps on every path).
-#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cudaTypedefs.h>
 
 #include <atomic>
 #include <climits>
@@ -78,6 +76,7 @@
 
 #include "hs_internal.cuh"
 #include "hs_tc.cuh"
+#include "hs_tmap.cuh"
 
 namespace {
 
@@ -135,15 +134,6 @@ struct Cfg {
     static_assert(SMEM_ALLOC <= 232448, "shared memory");
 };
 
-// Programmatic dependent launch: this grid may start while the previous kernel
-// on the stream (the step's resolve) is still running; a thread waits here for
-// that kernel's completion and memory before reading anything it wrote.
-__device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-// Lets the next kernel on the stream (the split merge) be scheduled early.
-__device__ __forceinline__ void grid_dep_launch() {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
 struct DecParams {
     const int32_t *resolved, *topk, *req_ids, *ctx;
     const float *gscale;        // gathered row scales (FP8, gathered rows)
@@ -158,130 +148,6 @@ struct DecParams {
     int tpl;  // lists per request: list b is token b % tpl of request b / tpl
     float scale_log2;
 };
-
-__device__ __forceinline__ void st_shared_v4(uint32_t a, uint32_t x, uint32_t y, uint32_t z,
-                                             uint32_t w) {
-    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
-                 : "memory");
-}
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(a)
-                 : "memory");
-    return v;
-}
-__device__ __forceinline__ float4 ld_shared_f4(uint32_t a) {
-    float4 v;
-    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(a)
-                 : "memory");
-    return v;
-}
-// TMEM load of 32 columns whose registers only become valid after the wait;
-// the wait takes them as operands so no use can be scheduled before it.
-#define HS_TMEM_LD32(taddr, r)                                                                    \
-    asm volatile(                                                                                 \
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"  \
-        "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"        \
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),    \
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),             \
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),          \
-          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),          \
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),          \
-          "=r"(r[31])                                                                             \
-        : "r"(taddr)                                                                              \
-        : "memory")
-#define HS_TMEM_WAIT_LD32(r)                                                                      \
-    asm volatile("tcgen05.wait::ld.sync.aligned;"                                                 \
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),        \
-                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),      \
-                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),  \
-                   "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),  \
-                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),  \
-                   "+r"(r[30]), "+r"(r[31])::"memory")
-// TMEM store of 32 (16) columns of 32-bit words from this thread's lane.
-#define HS_TMEM_ST32(taddr, r)                                                                    \
-    asm volatile(                                                                                 \
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"   \
-        "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"      \
-        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),           \
-        "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),          \
-        "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),      \
-        "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),      \
-        "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])                               \
-        : "memory")
-#define HS_TMEM_ST16(taddr, r)                                                                    \
-    asm volatile(                                                                                 \
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"   \
-        "%13,%14,%15,%16};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]),  \
-        "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),           \
-        "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])                                           \
-        : "memory")
-
-// A box of a 4-D tensor map (coordinates innermost first).
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, int c0, int c1, int c2, int c3,
-                                            uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
-        : "memory");
-}
-
-// Shared memory to a box of a 3-D tensor map (bulk async group of this thread).
-__device__ __forceinline__ void tma_store_3d(const void *tmap, uint32_t src, int c0, int c1, int c2) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
-            reinterpret_cast<uint64_t>(tmap)),
-        "r"(src), "r"(c0), "r"(c1), "r"(c2)
-        : "memory");
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<uint32_t *>(&h);
-}
-
-// Four e4m3 codes (the bytes of w, lowest first) to four BF16 values, exactly.
-// A code's sign, four exponent bits and three mantissa bits, placed at the
-// BF16 sign, the low four exponent bits and the top three mantissa bits, form
-// a BF16 whose value is the code's times 2^-120: a normal code 2^(e-7)(1+m/8)
-// becomes 2^(e-127)(1+m/8), a subnormal code 2^-6 (m/8) the BF16 subnormal
-// 2^-126 (m/8). Multiplying by 2^120 (exact) gives the code's value.
-__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t w, uint32_t &lo, uint32_t &hi) {
-    const uint32_t t0 = __byte_perm(w, 0u, 0x1404);  // bytes (c1, 0, c0, 0), high to low
-    const uint32_t t1 = __byte_perm(w, 0u, 0x3424);  // bytes (c3, 0, c2, 0)
-    uint32_t a = (t0 & 0x80008000u) | ((t0 >> 4) & 0x07F007F0u);
-    uint32_t b = (t1 & 0x80008000u) | ((t1 >> 4) & 0x07F007F0u);
-    const uint32_t two120 = 0x7B807B80u;  // (2^120, 2^120) in BF16
-    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(two120));
-    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(b) : "r"(two120));
-    lo = a;
-    hi = b;
-}
-
-// One kind::f16 MMA with A from TMEM; the B descriptor comes as two 32-bit
-// halves (only the low half changes between the MMAs of one operand walk) and
-// the accumulate flag is a constant, so that issuing costs a few instructions.
-template <bool ACC>
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t blo, uint32_t bhi,
-                                       uint32_t idesc) {
-    if (ACC)
-        asm volatile(
-            "{\n .reg .b64 bd;\n mov.b64 bd, {%2, %3};\n"
-            " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], bd, %4, 1;\n}\n" ::"r"(d),
-            "r"(a), "r"(blo), "r"(bhi), "r"(idesc)
-            : "memory");
-    else
-        asm volatile(
-            "{\n .reg .b64 bd;\n mov.b64 bd, {%2, %3};\n"
-            " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], bd, %4, 0;\n}\n" ::"r"(d),
-            "r"(a), "r"(blo), "r"(bhi), "r"(idesc)
-            : "memory");
-}
 
 // S = Q K^T over this CTA's 288 depth columns: the four value chunks (A = Q
 // chunk c at TMEM columns aq + 32 c, B = local chunk c) and its half of the
@@ -1115,19 +981,6 @@ struct Plan {
     size_t ws_o_bytes, ws_bytes;
 };
 
-int sm_count() {
-    static std::atomic<int> cached[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
-    int n = cached[dev].load(std::memory_order_relaxed);
-    if (!n) {
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-            n = 148;
-        cached[dev].store(n, std::memory_order_relaxed);
-    }
-    return n;
-}
-
 Plan make_plan(int B, int T, int H, int K) {
     Plan pl{};
     pl.M = T * H;
@@ -1147,35 +1000,6 @@ Plan make_plan(int B, int T, int H, int K) {
         pl.ws_bytes = pl.ws_o_bytes + ((rows * sizeof(float) + 255) & ~size_t(255));
     }
     return pl;
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    if (!fn) {
-        void *f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                             &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    }
-    return fn;
-}
-
-// Map [batch][rows][inner] (rank 3) or [rows][inner] (rank 2, batch 1) with a
-// (box_inner x box_rows) box.
-bool make_map(CUtensorMap *m, CUtensorMapDataType dt, const void *ptr, uint64_t inner,
-              uint64_t rows, uint64_t batch, uint64_t row_bytes, uint32_t box_inner,
-              uint32_t box_rows, CUtensorMapSwizzle sw, uint32_t rank = 3) {
-    auto fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[3] = {inner, rows, batch};
-    cuuint64_t strides[2] = {row_bytes, row_bytes * rows};
-    cuuint32_t box[3] = {box_inner, box_rows, 1};
-    cuuint32_t es[3] = {1, 1, 1};
-    return fn(m, dt, rank, const_cast<void *>(ptr), dims, strides, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Rows of 9 chunks of 64 elements, as a 4-D map (element, row, chunk,

@@ -2,6 +2,8 @@
 // tensor memory (TMEM) and tcgen05 MMA. Written from the PTX ISA.
 #pragma once
 
+#include <cuda_bf16.h>
+
 #include <cstdint>
 
 namespace hs {
@@ -230,6 +232,155 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
     asm volatile(
         "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
         : "memory");
+}
+
+// ---------------------------------------------------------------- dependent launch
+// Programmatic dependent launch: this grid may start while the previous kernel
+// on the stream (the step's resolve) is still running; a thread waits here for
+// that kernel's completion and memory before reading anything it wrote.
+__device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the next kernel on the stream (the split merge) be scheduled early.
+__device__ __forceinline__ void grid_dep_launch() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// ---------------------------------------------------------------- shared memory, TMEM words, conversions
+__device__ __forceinline__ void st_shared_v4(uint32_t a, uint32_t x, uint32_t y, uint32_t z,
+                                             uint32_t w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
+                 : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(a)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_shared_f4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(a)
+                 : "memory");
+    return v;
+}
+// TMEM load of 32 columns whose registers only become valid after the wait;
+// the wait takes them as operands so no use can be scheduled before it.
+#define HS_TMEM_LD32(taddr, r)                                                                    \
+    asm volatile(                                                                                 \
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"  \
+        "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"        \
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),    \
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),             \
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),          \
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),          \
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),          \
+          "=r"(r[31])                                                                             \
+        : "r"(taddr)                                                                              \
+        : "memory")
+#define HS_TMEM_WAIT_LD32(r)                                                                      \
+    asm volatile("tcgen05.wait::ld.sync.aligned;"                                                 \
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),        \
+                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),      \
+                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),  \
+                   "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),  \
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),  \
+                   "+r"(r[30]), "+r"(r[31])::"memory")
+#define HS_TMEM_LD16(taddr, r)                                                                    \
+    asm volatile(                                                                                 \
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"  \
+        "%14,%15}, [%16];"                                                                        \
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),    \
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),             \
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])                                                   \
+        : "r"(taddr)                                                                              \
+        : "memory")
+#define HS_TMEM_WAIT_LD16(r)                                                                      \
+    asm volatile("tcgen05.wait::ld.sync.aligned;"                                                 \
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),        \
+                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),      \
+                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory")
+// TMEM store of 32 (16) columns of 32-bit words from this thread's lane.
+#define HS_TMEM_ST32(taddr, r)                                                                    \
+    asm volatile(                                                                                 \
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"   \
+        "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"      \
+        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),           \
+        "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),          \
+        "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),      \
+        "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),      \
+        "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])                               \
+        : "memory")
+#define HS_TMEM_ST16(taddr, r)                                                                    \
+    asm volatile(                                                                                 \
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"   \
+        "%13,%14,%15,%16};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]),  \
+        "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),           \
+        "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])                                           \
+        : "memory")
+
+// A box of a 4-D tensor map (coordinates innermost first).
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, int c0, int c1, int c2, int c3,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+        : "memory");
+}
+
+// Shared memory to a box of a 3-D tensor map (bulk async group of this thread).
+__device__ __forceinline__ void tma_store_3d(const void *tmap, uint32_t src, int c0, int c1, int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+            reinterpret_cast<uint64_t>(tmap)),
+        "r"(src), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t *>(&h);
+}
+
+// Four e4m3 codes (the bytes of w, lowest first) to four BF16 values, exactly.
+// A code's sign, four exponent bits and three mantissa bits, placed at the
+// BF16 sign, the low four exponent bits and the top three mantissa bits, form
+// a BF16 whose value is the code's times 2^-120: a normal code 2^(e-7)(1+m/8)
+// becomes 2^(e-127)(1+m/8), a subnormal code 2^-6 (m/8) the BF16 subnormal
+// 2^-126 (m/8). Multiplying by 2^120 (exact) gives the code's value.
+__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    const uint32_t t0 = __byte_perm(w, 0u, 0x1404);  // bytes (c1, 0, c0, 0), high to low
+    const uint32_t t1 = __byte_perm(w, 0u, 0x3424);  // bytes (c3, 0, c2, 0)
+    uint32_t a = (t0 & 0x80008000u) | ((t0 >> 4) & 0x07F007F0u);
+    uint32_t b = (t1 & 0x80008000u) | ((t1 >> 4) & 0x07F007F0u);
+    const uint32_t two120 = 0x7B807B80u;  // (2^120, 2^120) in BF16
+    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(two120));
+    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(b) : "r"(two120));
+    lo = a;
+    hi = b;
+}
+
+// One kind::f16 MMA with A from TMEM; the B descriptor comes as two 32-bit
+// halves (only the low half changes between the MMAs of one operand walk) and
+// the accumulate flag is a constant, so that issuing costs a few instructions.
+template <bool ACC>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t blo, uint32_t bhi,
+                                       uint32_t idesc) {
+    if (ACC)
+        asm volatile(
+            "{\n .reg .b64 bd;\n mov.b64 bd, {%2, %3};\n"
+            " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], bd, %4, 1;\n}\n" ::"r"(d),
+            "r"(a), "r"(blo), "r"(bhi), "r"(idesc)
+            : "memory");
+    else
+        asm volatile(
+            "{\n .reg .b64 bd;\n mov.b64 bd, {%2, %3};\n"
+            " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], bd, %4, 0;\n}\n" ::"r"(d),
+            "r"(a), "r"(blo), "r"(bhi), "r"(idesc)
+            : "memory");
 }
 
 }  // namespace tc
