@@ -14,6 +14,10 @@
  * (hs_resolve_topk_union, hs_sparse_mla_decode_per_token), several layers'
  * pools resolved in one launch (hs_resolve_topk_layers), and the residency
  * transitions around the path (hs_active_copy, hs_demote_cold_pages).
+ * Around it: new tokens' rows into the cache (hs_append_rows), the pages a
+ * query token attends to chosen by a cheap score (hs_page_means,
+ * hs_select_pages), and attention over whole pages, for lists of them and for
+ * trees of drafted tokens (hs_page_mla_decode, hs_page_mla_decode_per_token).
  *
  * Conventions
  *  - Streams are cudaStream_t values passed as void* (NULL = legacy stream).
@@ -306,6 +310,107 @@ hs_status hs_active_copy(hs_pool_t pool, int32_t n, const int32_t *d_req, const 
 hs_status hs_demote_cold_pages(hs_pool_t pool, int32_t n, const int32_t *d_req,
                                const int32_t *d_keep_tail, int32_t *d_freed, int32_t *d_n_freed,
                                void *stream);
+
+/* ---- new rows, and pages chosen and attended to as wholes ----------------
+ *      No allocation and no host synchronisation; launch shapes depend on the
+ *      integer arguments alone, so every call can be captured in a CUDA graph.
+ *      The pool's device must be the current one. Request ids, lists and masks
+ *      are read on the device at each launch. -------------------------------- */
+
+/* Puts the latent rows of new tokens into the cache: row k of request
+ * d_req_ids[b] (k = 0 .. T-1) goes to position d_start[b] + k, or, with d_start
+ * NULL, to ctx_len - T + k (the convention of the decode's query tokens).
+ *   d_rows   bf16 [B][T][576], 16-byte aligned
+ *   d_index  int32 [B][T] or NULL: row k is d_rows[b][d_index[b][k]]; -1 puts
+ *            nothing there. So a verified draft's accepted path, or ragged
+ *            chunks of prompt, go in with one call. NULL: row k is d_rows[b][k].
+ * The row goes to every tier that holds the position: its page's GPU block, the
+ * page's host copy, and the position's hot slot. BF16 pools take it as it is.
+ * FP8 pools take scale = max(max|x| / 448, 2^-126) and the e4m3 codes of
+ * x / scale (quotients rounded to 32 bits, then to nearest even); a row that
+ * holds an infinity or NaN gets scale NaN and so reads as NaN.
+ * Context lengths are not changed; rows of other positions are left as they
+ * were. The request ids are distinct. A position outside [0, max_ctx) or an
+ * index outside [-1, T) is skipped (HS_DEVERR_INDEX_RANGE), as is a position
+ * whose page has neither a GPU block nor a host copy (HS_DEVERR_BAD_PAGE) and
+ * a bad request id (HS_DEVERR_BAD_REQUEST). Order it with hs_active_copy of the
+ * same pages. Requires T >= 1. */
+hs_status hs_append_rows(hs_pool_t pool, int32_t B, int32_t T, const void *d_rows,
+                         const int32_t *d_req_ids, const int32_t *d_start,
+                         const int32_t *d_index, void *stream);
+
+/* Mean rows: for each of n pairs (d_req[i], d_page[i]) the mean of the page's
+ * rows at positions below ctx_len (sums in f32; zeros when there is none) goes
+ * to d_means [max_requests][max_pages][576] (bf16, 16-byte aligned, owned by
+ * the caller) at [d_req[i]][d_page[i]]; other entries are left as they were.
+ * A page without a GPU block is read from its host copy. A pair out of range,
+ * or whose page has neither, is skipped (HS_DEVERR_BAD_PAGE). */
+hs_status hs_page_means(hs_pool_t pool, int32_t n, const int32_t *d_req, const int32_t *d_page,
+                        void *d_means, void *stream);
+
+/* Chooses N pages per query token. Query token t of request b sits at position
+ * L_b - T + t; its candidates are the pages that hold a position up to its own.
+ * The score of page p is max_h q[b][t][h] . means[req][p]. If there are more
+ * than N candidates, the first n_first and the last n_last are kept and the
+ * others taken by descending score, equal scores by ascending page, until
+ * there are N. The choice is that of the exact sums (products of BF16 values
+ * summed in 64 bits), not of 32-bit ones; a NaN product counts as minus
+ * infinity.
+ *   d_q        bf16 [B][T][H][576];  d_means as hs_page_means writes them
+ *   d_tree     uint64 [B][T] or NULL: as in hs_page_mla_decode; with it every
+ *              page below ctx_len is a candidate for every query token
+ *   d_pages    int32 [B][T][N] out: ascending page numbers, -1 behind the last
+ *   d_topk_idx int32 [B][T][N*64] out or NULL: the positions in those pages that
+ *              the query token sees, in order, -1 in the others' places: the
+ *              lists that hs_resolve_topk_union takes when pages are not resident
+ *   d_workspace / ws_bytes: hs_select_workspace_bytes(pool, B, T) bytes, 256-byte
+ *              aligned; calls that overlap need one each
+ * The scores are exact in time only near the border, so means or queries with
+ * infinities or NaN (whose scores say nothing in 32 bits) make a call slow, not
+ * wrong. Requires 1 <= N <= 1024 (HS_ERR_CAPACITY above), n_first + n_last <= N,
+ * T <= 32767 (64 with a tree), H <= 65535, T*H <= 2^22, B <= 65535; q and means
+ * 16-byte aligned. */
+hs_status hs_select_pages(hs_pool_t pool, int32_t B, int32_t T, int32_t H, int32_t N,
+                          int32_t n_first, int32_t n_last, const void *d_q, const void *d_means,
+                          const int32_t *d_req_ids, const uint64_t *d_tree, int32_t *d_pages,
+                          int32_t *d_topk_idx, void *d_workspace, size_t ws_bytes, void *stream);
+size_t hs_select_workspace_bytes(hs_pool_t pool, int32_t B, int32_t T);
+
+/* MLA decode over whole pages, read in place from their GPU blocks.
+ *   d_pages int32 [B][N]: each request's pages, in any order, -1 = no page; a
+ *           page listed twice counts twice. NULL: every page below ctx_len, and
+ *           N is the number of pages the launch is planned for (0: max_pages);
+ *           longer and shorter contexts are served all the same
+ *   d_tree  uint64 [B][T] or NULL. NULL: query token t sees positions up to its
+ *           own, L_b - T + t (a chain). Otherwise the last T positions are the
+ *           nodes of a draft: query token t sees every position below L_b - T,
+ *           and node i iff bit i of d_tree[b][t] is set (its ancestors and
+ *           itself; T <= 64, higher bits are ignored)
+ *   d_q, d_out, d_lse, sm_scale: as in hs_sparse_mla_decode; a query row that
+ *           sees nothing gets out 0 and lse -inf
+ *   d_workspace / ws_bytes: hs_page_decode_workspace_bytes(B, T, H, N) bytes (N as
+ *           passed, max_pages for 0), 256-byte aligned, may be NULL when that is 0;
+ *           calls that overlap need one each
+ * What a row that no query may see holds does not matter. An entry outside the
+ * context is skipped (HS_DEVERR_INDEX_RANGE), as is a page without a GPU block
+ * (HS_DEVERR_BAD_PAGE: resolve its positions with hs_resolve_topk_union
+ * instead); a bad request id attends to nothing (HS_DEVERR_BAD_REQUEST).
+ * Requires B <= 65535, 1 <= T <= 32767, H*T <= 128*65535; q and out 16-byte
+ * aligned. */
+hs_status hs_page_mla_decode(hs_pool_t pool, int32_t B, int32_t T, int32_t H, int32_t N,
+                             const void *d_q, const int32_t *d_pages, const int32_t *d_req_ids,
+                             const uint64_t *d_tree, float sm_scale, void *d_out, float *d_lse,
+                             void *d_workspace, size_t ws_bytes, void *stream);
+size_t hs_page_decode_workspace_bytes(int32_t B, int32_t T, int32_t H, int32_t N);
+
+/* hs_page_mla_decode with one list of pages per query token (those that
+ * hs_select_pages chose): d_pages int32 [B][T][N], not NULL. The workspace needs
+ * hs_page_decode_workspace_bytes(B * T, 1, H, N) bytes. Requires B * T <= 65535. */
+hs_status hs_page_mla_decode_per_token(hs_pool_t pool, int32_t B, int32_t T, int32_t H, int32_t N,
+                                       const void *d_q, const int32_t *d_pages,
+                                       const int32_t *d_req_ids, const uint64_t *d_tree,
+                                       float sm_scale, void *d_out, float *d_lse,
+                                       void *d_workspace, size_t ws_bytes, void *stream);
 
 /* Failure-detection check: launches one device wait on a barrier phase that
  * nothing completes, bounded by limit_us (1 .. 2,000,000) exactly like the

@@ -36,7 +36,9 @@ EXPORTED = [
     "hs_decode_workspace_bytes", "hs_status_string", "hs_sparse_mla_decode_static_ws",
     "hs_pool_check_bounded_wait", "hs_resolve_topk_union", "hs_sparse_mla_decode_per_token",
     "hs_layer_group_create", "hs_layer_group_destroy", "hs_resolve_topk_layers",
-    "hs_active_copy", "hs_demote_cold_pages",
+    "hs_active_copy", "hs_demote_cold_pages", "hs_append_rows", "hs_page_means",
+    "hs_select_pages", "hs_select_workspace_bytes", "hs_page_mla_decode",
+    "hs_page_decode_workspace_bytes", "hs_page_mla_decode_per_token",
 ]
 HS_STATIC_DECODE_WS_BYTES = 24 << 20
 
@@ -109,6 +111,16 @@ def load() -> C.CDLL:
         "hs_sparse_mla_decode_per_token": ([vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp,
                                             C.c_float, vp, vp, vp, sz, vp], i32),
         "hs_pool_check_bounded_wait": ([vp, C.c_uint32, vp], i32),
+        "hs_append_rows": ([vp, i32, i32, vp, vp, vp, vp, vp], i32),
+        "hs_page_means": ([vp, i32, vp, vp, vp, vp], i32),
+        "hs_select_pages": ([vp, i32, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, sz,
+                             vp], i32),
+        "hs_select_workspace_bytes": ([vp, i32, i32], sz),
+        "hs_page_mla_decode": ([vp, i32, i32, i32, i32, vp, vp, vp, vp, C.c_float, vp, vp, vp,
+                                sz, vp], i32),
+        "hs_page_decode_workspace_bytes": ([i32, i32, i32, i32], sz),
+        "hs_page_mla_decode_per_token": ([vp, i32, i32, i32, i32, vp, vp, vp, vp, C.c_float, vp,
+                                          vp, vp, sz, vp], i32),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -138,6 +150,25 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+def _arg(name: str, t, dtype: str, *shape, optional: bool = False) -> int | None:
+    """Device pointer of a CUDA tensor whose type (a torch dtype's name) and shape
+    are checked first (-1 in `shape`: any size): the kernels read it by both."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if str(t.dtype) != "torch." + dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if len(t.shape) != len(shape) or any(w not in (-1, n) for n, w in zip(t.shape, shape)):
+        raise ValueError(f"{name}: expected shape {list(shape)}, got {list(t.shape)}")
+    return _ptr(t)
+
+
+def _ws(workspace):
+    return (0 if workspace is None else workspace.numel() * workspace.element_size(),
+            _ptr(workspace))
+
+
 def _stream(stream) -> int | None:
     import torch
     if stream is None:
@@ -146,14 +177,15 @@ def _stream(stream) -> int | None:
 
 
 class _CudaArray:
-    def __init__(self, ptr: int, shape, typestr: str):
+    def __init__(self, ptr: int, shape, typestr: str, owner):
+        self.owner = owner  # a tensor over the pool's memory keeps the pool
         self.__cuda_array_interface__ = {"shape": tuple(shape), "typestr": typestr,
                                          "data": (ptr, False), "version": 3, "strides": None}
 
 
-def _device_view(ptr: int, shape, typestr: str):
+def _device_view(ptr: int, shape, typestr: str, owner=None):
     import torch
-    return torch.as_tensor(_CudaArray(ptr, shape, typestr), device="cuda")
+    return torch.as_tensor(_CudaArray(ptr, shape, typestr, owner), device="cuda")
 
 
 # ------------------------------------------------------------- C ABI functions
@@ -271,6 +303,86 @@ def hs_sparse_mla_decode_static_ws(pool: int, q, gathered, gathered_scale, resol
         _ptr(topk_idx), _ptr(req_ids), float(sm_scale), _ptr(out), _ptr(lse), _stream(stream)))
 
 
+def hs_append_rows(pool: int, rows, req_ids, start=None, index=None, stream=None):
+    """New tokens' rows into the cache (see hs.h). rows bf16 [B][T][576]; req_ids
+    int32 [B]; start int32 [B] or None (ctx_len - T); index int32 [B][T] or None."""
+    B, T = rows.shape[0], rows.shape[1]
+    _check("hs_append_rows", load().hs_append_rows(
+        pool, B, T, _arg("rows", rows, "bfloat16", B, T, 576), _arg("req_ids", req_ids, "int32", B),
+        _arg("start", start, "int32", B, optional=True),
+        _arg("index", index, "int32", B, T, optional=True), _stream(stream)))
+
+
+def hs_page_means(pool: int, req, page, means, stream=None):
+    """Mean rows of pages (see hs.h). req, page int32 [n]; means bf16
+    [max_requests][max_pages][576]."""
+    n = req.shape[0]
+    cfg = hs_pool_config()
+    _check("hs_pool_get_config", load().hs_pool_get_config(pool, C.byref(cfg)))
+    _check("hs_page_means", load().hs_page_means(
+        pool, n, _arg("req", req, "int32", n), _arg("page", page, "int32", n),
+        _arg("means", means, "bfloat16", cfg.max_requests, (cfg.max_ctx + 63) // 64, 576),
+        _stream(stream)))
+
+
+def hs_select_workspace_bytes(pool: int, B: int, T: int) -> int:
+    return load().hs_select_workspace_bytes(pool, B, T)
+
+
+def hs_select_pages(pool: int, q, means, req_ids, pages, n_first: int = 1, n_last: int = 1,
+                    tree=None, topk_idx=None, workspace=None, stream=None):
+    """Pages of the highest score for each query token (see hs.h). q bf16
+    [B][T][H][576]; means as hs_page_means; pages int32 [B][T][N] out; tree int64
+    [B][T] or None; topk_idx int32 [B][T][N*64] out or None; workspace uint8 tensor
+    of hs_select_workspace_bytes."""
+    B, T, H = q.shape[:3]
+    N = pages.shape[-1]
+    cfg = hs_pool_config()
+    _check("hs_pool_get_config", load().hs_pool_get_config(pool, C.byref(cfg)))
+    ws, wp = _ws(workspace)
+    _check("hs_select_pages", load().hs_select_pages(
+        pool, B, T, H, N, n_first, n_last, _arg("q", q, "bfloat16", B, T, H, 576),
+        _arg("means", means, "bfloat16", cfg.max_requests, (cfg.max_ctx + 63) // 64, 576),
+        _arg("req_ids", req_ids, "int32", B), _arg("tree", tree, "int64", B, T, optional=True),
+        _arg("pages", pages, "int32", B, T, N),
+        _arg("topk_idx", topk_idx, "int32", B, T, N * 64, optional=True), wp, ws, _stream(stream)))
+
+
+def hs_page_decode_workspace_bytes(B: int, T: int, H: int, N: int) -> int:
+    return load().hs_page_decode_workspace_bytes(B, T, H, N)
+
+
+def hs_page_mla_decode(pool: int, q, pages, req_ids, tree, sm_scale: float, out, lse,
+                       workspace=None, stream=None, n_pages: int = 0):
+    """MLA decode over whole pages (see hs.h). q bf16 [B][T][H][576]; pages int32
+    [B][N], or None for every page (planned for n_pages, 0: max_pages); tree int64
+    [B][T] or None; out bf16 [B][T][H][512]; lse float32 [B][T][H]."""
+    B, T, H = q.shape[:3]
+    N = n_pages if pages is None else pages.shape[-1]
+    ws, wp = _ws(workspace)
+    _check("hs_page_mla_decode", load().hs_page_mla_decode(
+        pool, B, T, H, N, _arg("q", q, "bfloat16", B, T, H, 576),
+        _arg("pages", pages, "int32", B, N, optional=True), _arg("req_ids", req_ids, "int32", B),
+        _arg("tree", tree, "int64", B, T, optional=True), float(sm_scale),
+        _arg("out", out, "bfloat16", B, T, H, 512), _arg("lse", lse, "float32", B, T, H), wp, ws,
+        _stream(stream)))
+
+
+def hs_page_mla_decode_per_token(pool: int, q, pages, req_ids, tree, sm_scale: float, out, lse,
+                                 workspace=None, stream=None):
+    """hs_page_mla_decode with one list per query token: pages int32 [B][T][N];
+    workspace of hs_page_decode_workspace_bytes(B*T, 1, H, N) bytes."""
+    B, T, H = q.shape[:3]
+    N = pages.shape[-1]
+    ws, wp = _ws(workspace)
+    _check("hs_page_mla_decode_per_token", load().hs_page_mla_decode_per_token(
+        pool, B, T, H, N, _arg("q", q, "bfloat16", B, T, H, 576),
+        _arg("pages", pages, "int32", B, T, N), _arg("req_ids", req_ids, "int32", B),
+        _arg("tree", tree, "int64", B, T, optional=True), float(sm_scale),
+        _arg("out", out, "bfloat16", B, T, H, 512), _arg("lse", lse, "float32", B, T, H), wp, ws,
+        _stream(stream)))
+
+
 # ------------------------------------------------------------- convenience
 class Pool:
     """Owns one hs_pool handle; methods map one-to-one onto the C ABI."""
@@ -355,12 +467,12 @@ class Pool:
     # storage views (zero-copy)
     def gpu_rows(self):
         n = self.cfg.n_gpu_blocks * 64
-        return _device_view(load().hs_gpu_rows(self.handle), (n, self.row_bytes), "|u1")
+        return _device_view(load().hs_gpu_rows(self.handle), (n, self.row_bytes), "|u1", self)
 
     def gpu_scales(self):
         if not self.fp8:
             return None
-        return _device_view(load().hs_gpu_scales(self.handle), (self.cfg.n_gpu_blocks * 64,), "<f4")
+        return _device_view(load().hs_gpu_scales(self.handle), (self.cfg.n_gpu_blocks * 64,), "<f4", self)
 
     def host_rows(self) -> np.ndarray | None:
         p = load().hs_host_rows(self.handle)
@@ -381,25 +493,25 @@ class Pool:
         p = load().hs_host_rows_device(self.handle)
         if not p:
             return None
-        return _device_view(p, (self.cfg.n_host_blocks * 64, self.row_bytes), "|u1")
+        return _device_view(p, (self.cfg.n_host_blocks * 64, self.row_bytes), "|u1", self)
 
     def host_scales_device(self):
         p = load().hs_host_scales_device(self.handle)
         if not p:
             return None
-        return _device_view(p, (self.cfg.n_host_blocks * 64,), "<f4")
+        return _device_view(p, (self.cfg.n_host_blocks * 64,), "<f4", self)
 
     def tables(self) -> dict:
         t, R, C_ = self._tables, self.cfg.max_requests, self.cfg.hot_rows
         return {
-            "page_table": _device_view(t.page_table, (R, self.max_pages, 2), "<i4"),
-            "hot_blocks": _device_view(t.hot_blocks, (R, C_ // 64), "<i4"),
-            "slot_tag": _device_view(t.slot_tag, (R, C_), "<i4"),
-            "slot_stamp": _device_view(t.slot_stamp, (R, C_), "<i4"),
-            "lru_order": _device_view(t.lru_order, (R, C_), "<i4"),
-            "pos_to_slot": _device_view(t.pos_to_slot, (R, self.cfg.max_ctx), "<i4"),
-            "clock": _device_view(t.clock, (R,), "<i4"),
-            "ctx_len": _device_view(t.ctx_len, (R,), "<i4"),
+            "page_table": _device_view(t.page_table, (R, self.max_pages, 2), "<i4", self),
+            "hot_blocks": _device_view(t.hot_blocks, (R, C_ // 64), "<i4", self),
+            "slot_tag": _device_view(t.slot_tag, (R, C_), "<i4", self),
+            "slot_stamp": _device_view(t.slot_stamp, (R, C_), "<i4", self),
+            "lru_order": _device_view(t.lru_order, (R, C_), "<i4", self),
+            "pos_to_slot": _device_view(t.pos_to_slot, (R, self.cfg.max_ctx), "<i4", self),
+            "clock": _device_view(t.clock, (R,), "<i4", self),
+            "ctx_len": _device_view(t.ctx_len, (R,), "<i4", self),
         }
 
     # hot path
@@ -422,3 +534,25 @@ class Pool:
                                     req_ids, sm_scale, out, lse, workspace=None, stream=None):
         hs_sparse_mla_decode_per_token(self.handle, q, gathered, gathered_scale, resolved,
                                        topk_idx, req_ids, sm_scale, out, lse, workspace, stream)
+
+    # new rows, page selection, attention over pages
+    def append_rows(self, rows, req_ids, start=None, index=None, stream=None):
+        hs_append_rows(self.handle, rows, req_ids, start, index, stream)
+
+    def page_means(self, req, page, means, stream=None):
+        hs_page_means(self.handle, req, page, means, stream)
+
+    def select_pages(self, q, means, req_ids, pages, n_first=1, n_last=1, tree=None,
+                     topk_idx=None, workspace=None, stream=None):
+        hs_select_pages(self.handle, q, means, req_ids, pages, n_first, n_last, tree, topk_idx,
+                        workspace, stream)
+
+    def page_mla_decode(self, q, pages, req_ids, tree, sm_scale, out, lse, workspace=None,
+                        stream=None, n_pages=0):
+        hs_page_mla_decode(self.handle, q, pages, req_ids, tree, sm_scale, out, lse, workspace,
+                           stream, n_pages)
+
+    def page_mla_decode_per_token(self, q, pages, req_ids, tree, sm_scale, out, lse,
+                                  workspace=None, stream=None):
+        hs_page_mla_decode_per_token(self.handle, q, pages, req_ids, tree, sm_scale, out, lse,
+                                     workspace, stream)
