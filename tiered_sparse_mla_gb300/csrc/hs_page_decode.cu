@@ -2,35 +2,55 @@
 // cores: a list of pages per query token or per request, or all of a request's
 // pages, with the drafted tokens a chain or a tree.
 //
-// One 64-row page is one key tile: its rows lie together in the pool, so TMA
-// brings them as boxes of 64 rows x 64 columns with no per-row ids.
-//   S[128 x 64] = Q[128 x 576] K^T,  O[128 x 512] += P V,  V = K[:, 0:512].
+// A 64-row page lies together in the pool, so TMA brings it as boxes of 64 rows x
+// 64 columns with no per-row ids. Per step, two pages (128 keys):
+//   S[128 x 128] = Q[128 x 576] K^T,  O[128 x 512] += P V,  V = K[:, 0:512].
 //
-// Work unit: (list, 128 query rows, split of the list), run by two CTAs. CTA h
-// holds O for the value columns [256 h, 256 h + 256) and both compute the whole
-// of S: 832 instead of 544 columns of depth per key, but no exchange of scores
-// between the two. O takes 256 of the 512 TMEM columns, S 64, P 32 and five of
-// the nine 64-column chunks of Q the other 160; Q's other four stay in shared
-// memory (the MMA reads A from either).
-//   warp 0      producer: Q, then per page five boxes of the columns that only
-//               S needs (the other CTA's value columns and the 64 rope columns)
-//               and one of this CTA's four value chunks, which stay until PV;
-//   warp 1      MMA issuer: S_j = Q K_j^T, then O += P_{j-1} V_{j-1}: the pipe
-//               works on the latter while the softmax warps read S_j;
-//   warps 4-7   softmax, one thread per query row: mask, online softmax with a
-//               conditional rescale, P to TMEM; then the epilogue;
-//   warps 8-15  (FP8) converters: e4m3 codes of each landed chunk to BF16, the
-//               chunks alternating between two groups of four warps.
-// FP8: the codes become BF16 exactly; a row's fp32 scale multiplies its scores
-// in f32 and its probability before that is rounded to BF16 (the MMA's operand
-// type; the probabilities' sum is that of the unrounded ones).
+// Work unit: (list, 128 query rows, split of the list), run by a cluster of two
+// CTAs whose tensor cores work as one (cta_group::2): CTA r holds the query rows
+// [64 r, 64 r + 64) with their S (64 TMEM columns), O (256) and six of the nine
+// 64-column chunks of Q (192; the other three stay in shared memory), and no
+// score leaves its CTA. With M = 128 over two CTAs the accumulator of CTA r has
+// row i in lane i for the first half of the MMA's columns and in lane 64 + i for
+// the second; A in tensor memory is wanted in both.
+//   K: CTA r supplies the keys of page r of the step, all nine chunks, through a
+//      ring of chunk slots that S frees at once;
+//   V: CTA r supplies the value columns 128 r + {0..127, 256..383} of both pages,
+//      loaded apart (the second reading comes from L2) into a buffer that PV frees.
+// An MMA of 128 keys takes 45 clocks (256 value columns: 64), so a step is
+// 36 x 45 + 16 x 64 = 2.7k clocks; an earlier form, one CTA per half of the value
+// columns and both computing S, was bound by the issue of its 80 smaller MMAs per
+// 128 keys and by their operands' shared-memory reads.
+// Roles in each CTA:
+//   warps 0, 3  producers: the K chunks and the V chunks of each step by TMA;
+//   warp 1      (CTA 0) MMA issuer for both CTAs: S_j = Q K_j^T, then
+//               O += P_{j-1} V_{j-1}, during which the softmax reads S_j;
+//   warps 4-11  softmax: thread = (row, page of the step, half of its keys): mask,
+//               online softmax with a conditional rescale, P as BF16 to shared
+//               memory; epilogue;
+//   warps 12-19 (FP8) converters: the e4m3 codes of the landed chunks to F16, four
+//               warps for K's chunks and four for V's.
+// FP8: the MMAs run on F16, which every e4m3 code is exactly and to which the
+// hardware converts two codes per instruction (24 against 72 clocks per 16 codes
+// and warp for placing BF16 bits with integer instructions, which bound the loop).
+//   Q: the CTA's BF16 values times a power of two that brings the largest to
+//      [2^14, 2^15): exact down to 2^-29 of that largest, off by at most 2^-40 of
+//      it below.
+//   P: in log2 units, t = score + log2|scale| is the weight of a row's codes; a
+//      query row keeps a reference for t as it does for the scores, and
+//      P = 2^7 exp2(t - reference) <= 2^15. F16 rounds it by at most 2^-11 of it or
+//      2^-32 of the row's largest. The probabilities' sum has the unrounded ones.
+//   Warp 2 turns each step's scales into the two numbers per key that the softmax
+//   uses (scale times the scores' factor, log2|scale|).
 // Every wait is bounded; on expiry the kernel sets HS_DEVERR_TIMEOUT, drains its
 // own copies and MMAs and returns.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include <cfloat>
 #include <climits>
 #include <cstdint>
+#include <type_traits>
 
 #include "hs_internal.cuh"
 #include "hs_tc.cuh"
@@ -42,39 +62,51 @@ using namespace hs::tc;
 using hs::kDim;
 using hs::kPage;
 
-constexpr int BM = 128, BN = kPage;
-constexpr int QCH = BM * 128;   // a 64-column chunk of Q
-constexpr int KCH = BN * 128;   // a 64-column chunk of a page, BF16
-constexpr int CCH = BN * 64;    // the same as e4m3 codes
-constexpr int NX = 5, NVC = 4;  // chunks that only S needs; chunks of this CTA's value columns
-constexpr int NSM = 128;        // softmax threads
-constexpr int NT_RING = 4;      // tiles whose page number and scales are held
-constexpr float TAU2 = 8.f;     // rescale threshold, log2 units: P <= 2^8
-constexpr uint32_t TM_O = 0, TM_S = 256, TM_P = 320, TM_Q = 352;
+constexpr int BM = 128, RM = 64;  // query rows per work unit, per CTA
+constexpr int CH = 64 * 128;      // 64 rows (of Q, of a page, of P) x 64 BF16 columns
+constexpr int CCH = 64 * 64;      // 64 rows x 64 e4m3 codes
+constexpr int NK = 9, NVC = 4;    // K chunks of a page; V chunks of a page in this CTA
+constexpr int NQT = 6;            // chunks of Q in tensor memory
+constexpr int NTI = 3;            // steps whose page numbers and scales are held
+constexpr int NSW = 8;             // softmax warps
+constexpr float TAU2 = 8.f;       // rescale threshold, log2 units: P <= 2^8
+constexpr uint32_t TM_O = 0, TM_S = 256, TM_Q = 320;
 
 template <bool FP8>
 struct PCfg {
-    static constexpr int THREADS = FP8 ? 512 : 256;
-    static constexpr int NV = FP8 ? 2 : 3;   // stages of value chunks
-    static constexpr int NXS = FP8 ? 6 : 8;  // slots of the other chunks
-    static constexpr int NC = FP8 ? 11 : 1;  // slots of codes
+    static constexpr int THREADS = 128 + 32 * NSW + (FP8 ? 256 : 0);
+    static constexpr int NV = 2;              // V's buffers: two steps; FP8: the two halves of one step's columns
+    static constexpr int NXS = FP8 ? 6 : 7;   // slots of K chunks
+    static constexpr int GK = FP8 ? 3 : 1;    // K chunks per barrier (converted together)
+    static constexpr int GV = 4;              // FP8: V chunks converted together (half the columns)
+    static constexpr int NXG = NXS / GK;      // groups of K chunks
+    static constexpr int NCK = FP8 ? 3 : 0;   // groups of K codes
+    static constexpr int NCV = FP8 ? 2 : 0;   // groups of V codes
+    static constexpr int NC = NCK + NCV;
+    static constexpr int RK = FP8 ? NCK : NXG, RV = FP8 ? NCV : NV;  // the producers' rings
     static constexpr int OFF_Q = 0;
-    static constexpr int OFF_V = OFF_Q + NVC * QCH;
-    static constexpr int OFF_X = OFF_V + NV * NVC * KCH;
-    static constexpr int OFF_C = OFF_X + NXS * KCH;
-    static constexpr int OFF_SC = OFF_C + (FP8 ? NC * CCH : 0);        // f32 [NT_RING][64]
-    static constexpr int OFF_PG = OFF_SC + (FP8 ? NT_RING * BN * 4 : 0);  // int32 [NT_RING]
-    static constexpr int OFF_BAR = OFF_PG + NT_RING * 4;
-    static constexpr int B_QFULL = 0, B_QREADY = 1, B_SFULL = 2, B_SFREE = 3, B_PFULL = 4,
-                         B_PVDONE = 5, B_DRAIN = 6, B_TFULL = 7, B_TFREE = B_TFULL + NT_RING,
-                         B_VFULL = B_TFREE + NT_RING, B_VFREE = B_VFULL + NV,
-                         B_XFULL = B_VFREE + NV, B_XFREE = B_XFULL + NXS,
-                         B_CFULL = B_XFREE + NXS, B_CFREE = B_CFULL + NC, NBAR = B_CFREE + NC;
-    static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;  // TMEM base, abort flag, tiles, first tile
-    static constexpr int SMEM = OFF_MISC + 16;
+    static constexpr int OFF_P = OFF_Q + (NK - NQT) * CH;  // [2 pages] rows x keys
+    static constexpr int OFF_V = OFF_P + 2 * CH;           // [steps][2 pages][NVC]
+    static constexpr int OFF_X = OFF_V + (FP8 ? 1 : 2) * 2 * NVC * CH;
+    static constexpr int OFF_C = OFF_X + NXS * CH;
+    static constexpr int OFF_SC = OFF_C + (NCK * GK + NCV * GV) * CCH;    // f32 [NTI][2][64] scores' factors
+    static constexpr int OFF_SP = OFF_SC + (FP8 ? NTI * 2 * 64 * 4 : 0);  // f32 [NTI][2][64] log2|scale|
+    static constexpr int OFF_XM = OFF_SP + (FP8 ? NTI * 2 * 64 * 4 : 0);  // f32 [softmax threads], FP8: twice
+    static constexpr int OFF_PG = OFF_XM + (FP8 ? 2 : 1) * 32 * NSW * 4;                           // int32 [NTI][2]
+    static constexpr int OFF_NEG = OFF_PG + NTI * 8;                      // int32 [NTI] some scale is negative
+    static constexpr int OFF_BAR = (OFF_NEG + NTI * 4 + 7) & ~7;
+    static constexpr int B_QFULL = 0, B_QDONE = 1, B_QREADY = 2, B_SFULL = 3, B_SFREE = 4, B_PFULL = 5,
+                         B_PVDONE = 6, B_DRAIN = 7, B_TFULL = 8, B_TFREE = B_TFULL + NTI,
+                         B_TREADY = B_TFREE + NTI, B_VFULL = B_TREADY + NTI, B_VFREE = B_VFULL + NV, B_XFULL = B_VFREE + NV,
+                         B_XFREE = B_XFULL + NXG, B_CFULL = B_XFREE + NXG, B_CFREE = B_CFULL + NC,
+                         NBAR = B_CFREE + NC;
+    static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;  // TMEM base, abort flag, steps, first entry, end, Q's power
+    static constexpr int SMEM = OFF_MISC + 32;
     static constexpr int SMEM_ALLOC = SMEM + 1024;
-    static_assert(OFF_BAR % 8 == 0 && OFF_MISC % 4 == 0, "alignment");
-    static_assert(NX * QCH <= OFF_C - OFF_V, "staging of Q");
+    static constexpr int OFF_QST = OFF_V + (FP8 ? 0 : 1) * 2 * NVC * CH;  // Q is staged in the last V stage
+    static_assert(OFF_BAR % 8 == 0 && OFF_SC % 16 == 0, "alignment");
+    static_assert(NQT * CH <= 2 * NVC * CH, "staging of Q");
+    static_assert(OFF_SC - OFF_V >= RM * 512 * 4, "staging of O");
     static_assert(SMEM_ALLOC <= 232448, "shared memory");
 };
 
@@ -84,14 +116,87 @@ struct PageParams {
     const int2 *table;
     const uint64_t *tree;  // [B][T] or null
     const float *scales;   // FP8: the pool's row scales
-    __nv_bfloat16 *out;
-    float *lse, *ws_o, *ws_lse;
+    float *lse, *ws_lse;
     uint32_t *err;
     int T, H, N, M, lists, nsplit, max_req, max_pages, zero_block;
     int tpl;               // lists per request: list i is token i % tpl of request i / tpl
     float scale_log2;
 };
 
+// ---------------------------------------------------------------- two CTAs' tensor cores as one
+__device__ __forceinline__ void tmem_alloc2(uint32_t dst_smem, uint32_t ncols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// Arrives on the barrier at this offset in both CTAs once every MMA issued so far is done.
+__device__ __forceinline__ void commit_both(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+// One MMA; descriptors as two 32-bit halves (the high one is shared), A from
+// shared memory or from tensor memory.
+__device__ __forceinline__ void mma2_ss(uint32_t d, uint32_t alo, uint32_t blo, uint32_t hi, uint32_t idesc,
+                                        uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %5, 0;\n mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %4, p;\n}\n" ::"r"(d),
+        "r"(alo), "r"(blo), "r"(hi), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma2_ts(uint32_t d, uint32_t a, uint32_t blo, uint32_t hi, uint32_t idesc,
+                                        uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n mov.b64 b, {%2, %3};\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(blo), "r"(hi), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// A box into this CTA's shared memory whose bytes complete on a barrier of either CTA.
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const void *tmap, int c0, int c1, int c2, uint32_t cluster_bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(cluster_bar)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred P;\n elect.sync _|P, 0xffffffff;\n selp.u32 %0, 1, 0, P;\n}\n" : "=r"(p));
+    return p;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+// Two BF16 values times 2^k (as a float) to F16.
+__device__ __forceinline__ uint32_t bf16x2_to_f16(uint32_t w, float pow2) {
+    return pack_f16(__uint_as_float(w << 16) * pow2, __uint_as_float(w & 0xffff0000u) * pow2);
+}
+// Four e4m3 codes to F16, exactly; with V, the NaN codes (rows that no query
+// sees may hold any byte) become a finite value.
+template <bool V>
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+    if (V) {
+        const uint32_t most = 0x5f805f80u;  // 480, above every code
+        asm("min.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(most));
+        asm("min.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(most));
+    }
+}
 // f32 bulk copy of one page's scales into shared memory
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
     asm volatile(
@@ -99,63 +204,113 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
         "l"(src), "r"(bytes), "r"(bar)
         : "memory");
 }
+// Two f32 operations in one instruction.
+__device__ __forceinline__ void mul2(float &a, float &b, float c, float d) {
+    asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n mul.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
+        : "+f"(a), "+f"(b)
+        : "f"(c), "f"(d));
+}
+__device__ __forceinline__ void add2(float &a, float &b, float c, float d) {
+    asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
+        : "+f"(a), "+f"(b)
+        : "f"(c), "f"(d));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// Whether any of the softmax threads says so (named barrier 1).
+__device__ __forceinline__ bool any_softmax(bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.red.or.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(r)
+        : "r"((uint32_t)x), "n"(32 * NSW)
+        : "memory");
+    return r != 0;
+}
+
+// O's 128 columns from `at` in this thread's lane times alpha. Out of line: it
+// runs where a row's reference grows, and inside the loop it costs the scores'
+// registers.
+__device__ __noinline__ void rescale_o(uint32_t at, float alpha) {
+#pragma unroll 1
+    for (int c = 0; c < 128; c += 32) {
+        uint32_t o[32];
+        HS_TMEM_LD32(at + c, o);
+        HS_TMEM_WAIT_LD32(o);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+        HS_TMEM_ST32(at + c, o);
+    }
+    tmem_wait_st();
+}
 
 template <bool FP8>
 __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
 page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k1,
-                   const __grid_constant__ CUtensorMap tm_k4, const PageParams p) {
+                   const __grid_constant__ CUtensorMap tm_k2, const __grid_constant__ CUtensorMap tm_o,
+                   const PageParams p) {
     using C = PCfg<FP8>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = hs::smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *smem = smem_raw + (base - raw);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int half = blockIdx.x & 1, split = blockIdx.x >> 1, mt = blockIdx.y, list = blockIdx.z;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int rank = static_cast<int>(hs::cluster_ctarank());
+    const int split = blockIdx.x >> 1, mt = blockIdx.y, list = blockIdx.z;
     volatile int32_t *misc = reinterpret_cast<volatile int32_t *>(smem + C::OFF_MISC);
     volatile int32_t *ring_pg = reinterpret_cast<volatile int32_t *>(smem + C::OFF_PG);
     auto bar = [&](int i) { return base + C::OFF_BAR + 8u * (uint32_t)i; };
+    // the same barrier in CTA 0, whose warp 1 issues the MMAs
+    auto lead = [&](int i) { return hs::dsmem_map(smem + C::OFF_BAR + 8 * i, 0); };
     auto fail = [&]() {
         misc[1] = 1;
         atomicOr(p.err, HS_DEVERR_TIMEOUT);
     };
 
+    if (threadIdx.x == 0) {
+        mbar_init(bar(C::B_QFULL), 1);
+        mbar_init(bar(C::B_QDONE), NSW);
+        mbar_init(bar(C::B_QREADY), 2 * NSW);  // both CTAs' softmax warps
+        mbar_init(bar(C::B_SFULL), 1);
+        mbar_init(bar(C::B_SFREE), 2 * NSW);
+        mbar_init(bar(C::B_PFULL), 2 * NSW);
+        mbar_init(bar(C::B_PVDONE), 1);
+        mbar_init(bar(C::B_DRAIN), 1);
+        for (int i = 0; i < NTI; ++i) {
+            mbar_init(bar(C::B_TFULL + i), 1);
+            mbar_init(bar(C::B_TFREE + i), NSW);
+            mbar_init(bar(C::B_TREADY + i), 1);
+        }
+        for (int i = 0; i < C::NV; ++i) {
+            mbar_init(bar(C::B_VFULL + i), FP8 ? 8 : 1);  // FP8: four converter warps of each CTA
+            mbar_init(bar(C::B_VFREE + i), 1);
+        }
+        for (int i = 0; i < C::NXG; ++i) {
+            mbar_init(bar(C::B_XFULL + i), FP8 ? 8 : 1);  // FP8: four converter warps of each CTA
+            mbar_init(bar(C::B_XFREE + i), 1);
+        }
+        for (int i = 0; i < C::NC; ++i) {
+            mbar_init(bar(C::B_CFULL + i), 1);
+            mbar_init(bar(C::B_CFREE + i), 4);
+        }
+        misc[1] = 0;
+        fence_mbar_init();
+        fence_proxy_async();
+        // Q by TMA at once: its barrier is this CTA's own
+        mbar_expect_tx(bar(C::B_QFULL), NK * CH);
+        for (int i = 0; i < NK; ++i)
+            tma_load_3d(i < NQT ? base + C::OFF_QST + i * CH : base + C::OFF_Q + (i - NQT) * CH, &tm_q, 64 * i,
+                        mt * BM + RM * rank, list, bar(C::B_QFULL));
+    }
     const int req = p.req[list / p.tpl];
     const bool req_ok = req >= 0 && req < p.max_req;
     const int L = req_ok ? p.ctx[req] : 0;
     const int npages = L <= 0 ? 0 : (L - 1) / kPage + 1;
     const int32_t *entries = p.pages ? p.pages + (size_t)list * p.N : nullptr;
-
-    if (threadIdx.x == 32) {
-        mbar_init(bar(C::B_QFULL), 1);
-        mbar_init(bar(C::B_QREADY), NSM);
-        mbar_init(bar(C::B_SFULL), 1);
-        mbar_init(bar(C::B_SFREE), NSM);
-        mbar_init(bar(C::B_PFULL), NSM);
-        mbar_init(bar(C::B_PVDONE), 1);
-        mbar_init(bar(C::B_DRAIN), 1);
-        for (int i = 0; i < NT_RING; ++i) {
-            mbar_init(bar(C::B_TFULL + i), 1);
-            mbar_init(bar(C::B_TFREE + i), NSM);
-        }
-        for (int i = 0; i < C::NV; ++i) {
-            mbar_init(bar(C::B_VFULL + i), FP8 ? 128 * NVC : 1);
-            mbar_init(bar(C::B_VFREE + i), 1);
-        }
-        for (int i = 0; i < C::NXS; ++i) {
-            mbar_init(bar(C::B_XFULL + i), FP8 ? 128 : 1);
-            mbar_init(bar(C::B_XFREE + i), 1);
-        }
-        for (int i = 0; i < C::NC; ++i) {
-            mbar_init(bar(C::B_CFULL + i), 1);
-            mbar_init(bar(C::B_CFREE + i), 128);
-        }
-        misc[1] = 0;
-        fence_mbar_init();
-        prefetch_tmap(&tm_q);
-        prefetch_tmap(&tm_k1);
-        if (!FP8) prefetch_tmap(&tm_k4);
-    }
-    if (warp == 0) {
+    if (warp == 2) {
         // the list's end: past its last entry that names a page
         int end = npages;
         if (entries) {
@@ -165,182 +320,253 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             end = __reduce_max_sync(0xffffffffu, end);
         }
         if (lane == 0) {
-            const int a = (int)((long long)end * split / p.nsplit);
-            misc[2] = (int)((long long)end * (split + 1) / p.nsplit) - a;
-            misc[3] = a;
+            // splits begin at even entries: a step is two pages
+            const long long steps = (end + 1) / 2;
+            const int a = (int)(steps * split / p.nsplit), z = (int)(steps * (split + 1) / p.nsplit);
+            misc[2] = z - a;
+            misc[3] = 2 * a;
+            misc[4] = end;
         }
     }
-    if (warp == 1) tmem_alloc(base + C::OFF_MISC, 512);
+    if (warp == 1) tmem_alloc2(base + C::OFF_MISC, 512);
     tc_fence_before();
     __syncthreads();
+    cluster_sync_all();  // both CTAs' barriers and tensor memory are there
     tc_fence_after();
+    grid_dep_launch();
     const uint32_t tmem = static_cast<uint32_t>(misc[0]);
-    const int ntiles = misc[2], first = misc[3];
-    // chunk i of the order in which a page's chunks are used
-    auto chunk_of = [&](int i) { return i < 4 ? 4 * (1 - half) + i : (i == 4 ? 8 : 4 * half + i - 5); };
+    const int nsteps = misc[2], first = misc[3], end = misc[4];
 
-    if (warp == 0) {
-        // ------------------------------------------------------------ producer
-        if (ntiles > 0) {
-            if (lane == 0) {
-                mbar_expect_tx(bar(C::B_QFULL), 9 * QCH);
-                for (int i = 0; i < 9; ++i)
-                    tma_load_3d(i < NX ? base + C::OFF_V + i * QCH : base + C::OFF_Q + (i - NX) * QCH, &tm_q,
-                                64 * chunk_of(i), mt * BM, list, bar(C::B_QFULL));
-            }
-            // page number and block of the next 32 entries, one per lane
-            uint32_t bad = 0;
-            auto fetch = [&](int i0, int &pg, int &blk) {
-                const int i = i0 + lane;
-                pg = -1;
-                blk = p.zero_block;
-                if (i < ntiles) {
-                    const int x = entries ? entries[first + i] : first + i;
-                    if (x < -1 || x >= npages) {
-                        bad |= HS_DEVERR_INDEX_RANGE;
-                    } else if (x >= 0) {
-                        const int g = p.table[(size_t)req * p.max_pages + x].x;
-                        if (g >= 0) {
-                            pg = x;
-                            blk = g;
-                        } else {
-                            bad |= HS_DEVERR_BAD_PAGE;  // not resident: the entry is skipped
-                        }
-                    }
-                }
-            };
-            int pg, blk, npg, nblk;
-            fetch(0, npg, nblk);
-            int ux = 0, uc = 0, tiles_done = 0;  // chunk loads and tiles begun
-            bool ok = true;
-            for (int j = 0; j < ntiles && ok; ++j) {
-                if (j % 32 == 0) {
-                    pg = npg;
-                    blk = nblk;
-                    fetch(j + 32, npg, nblk);
-                }
-                const int tpg = __shfl_sync(0xffffffffu, pg, j & 31), tblk = __shfl_sync(0xffffffffu, blk, j & 31);
-                if (lane == 0) {
-                    const int row0 = tblk * kPage;
-                    const int ti = j % NT_RING;
-                    ok = mbar_wait(bar(C::B_TFREE + ti), ((uint32_t)(j / NT_RING) & 1u) ^ 1u) && !misc[1];
-                    if (ok) {
-                        ring_pg[ti] = tpg;
-                        if (FP8) {
-                            mbar_expect_tx(bar(C::B_TFULL + ti), BN * 4);
-                            bulk_load(base + C::OFF_SC + ti * BN * 4, p.scales + (size_t)row0, BN * 4, bar(C::B_TFULL + ti));
-                        } else {
-                            mbar_arrive(bar(C::B_TFULL + ti));
-                        }
-                        tiles_done = j + 1;
-                    }
-                    if (FP8) {
-                        for (int i = 0; i < 9 && ok; ++i, ++uc) {
-                            const int s = uc % C::NC;
-                            ok = mbar_wait(bar(C::B_CFREE + s), ((uint32_t)(uc / C::NC) & 1u) ^ 1u) && !misc[1];
-                            if (!ok) break;
-                            mbar_expect_tx(bar(C::B_CFULL + s), CCH);
-                            tma_load_3d(base + C::OFF_C + s * CCH, &tm_k1, 0, row0, chunk_of(i), bar(C::B_CFULL + s));
-                        }
+    if (warp == 0 || warp == 3) {
+        // ------------------------------------------------------------ producers
+        // warp 0: page numbers, scales, K; warp 3: V. Each looks up the pages'
+        // blocks itself, 32 entries at a time, one per lane, ahead of their use.
+        const bool kw = warp == 0;
+        uint32_t bad = 0;
+        auto fetch = [&](int i0, int &pg, int &blk) {
+            const int i = first + i0 + lane;
+            pg = -1;
+            blk = p.zero_block;
+            if (i < end && i < first + 2 * nsteps) {
+                const int x = entries ? entries[i] : i;
+                if (x < -1 || x >= npages) {
+                    bad |= HS_DEVERR_INDEX_RANGE;
+                } else if (x >= 0) {
+                    const int g = p.table[(size_t)req * p.max_pages + x].x;
+                    if (g >= 0) {
+                        pg = x;
+                        blk = g;
                     } else {
-                        for (int i = 0; i < NX && ok; ++i, ++ux) {
-                            const int s = ux % C::NXS;
-                            ok = mbar_wait(bar(C::B_XFREE + s), ((uint32_t)(ux / C::NXS) & 1u) ^ 1u) && !misc[1];
-                            if (!ok) break;
-                            mbar_expect_tx(bar(C::B_XFULL + s), KCH);
-                            tma_load_3d(base + C::OFF_X + s * KCH, &tm_k1, 0, row0, chunk_of(i), bar(C::B_XFULL + s));
-                        }
-                        const int s = j % C::NV;
-                        if (ok && j == 0) ok = mbar_wait(bar(C::B_QREADY), 0);  // Q was staged there
-                        if (ok) ok = mbar_wait(bar(C::B_VFREE + s), ((uint32_t)(j / C::NV) & 1u) ^ 1u) && !misc[1];
-                        if (ok) {
-                            mbar_expect_tx(bar(C::B_VFULL + s), NVC * KCH);
-                            tma_load_3d(base + C::OFF_V + s * NVC * KCH, &tm_k4, 0, row0, 4 * half, bar(C::B_VFULL + s));
-                            uc = j + 1;
-                        }
+                        bad |= HS_DEVERR_BAD_PAGE;  // not resident: the entry is skipped
                     }
                 }
-                ok = __shfl_sync(0xffffffffu, ok, 0);
             }
-            if (!ok && lane == 0) {
-                fail();
-                // the copies begun have landed before the CTA may end
-                mbar_wait(bar(C::B_QFULL), 0);
+        };
+        int pg, blk, npg, nblk;
+        fetch(0, npg, nblk);
+        int ul = 0, ut = 0;  // loads and steps begun
+        bool ok = true;
+        for (int j = 0; j < nsteps && ok; ++j) {
+            if (j % 16 == 0) {
+                pg = npg;
+                blk = nblk;
+                fetch(2 * j + 32, npg, nblk);
+            }
+            const int src = 2 * (j % 16);
+            const int pg0 = __shfl_sync(0xffffffffu, pg, src), pg1 = __shfl_sync(0xffffffffu, pg, src + 1);
+            const int row0 = __shfl_sync(0xffffffffu, blk, src) * kPage;
+            const int row1 = __shfl_sync(0xffffffffu, blk, src + 1) * kPage;
+            if (lane == 0 && kw) {
+                const int own = rank ? row1 : row0, ti = j % NTI;
+                ok = mbar_wait_inline(bar(C::B_TFREE + ti), ((uint32_t)(j / NTI) & 1u) ^ 1u);
+                if (ok) {
+                    ring_pg[2 * ti] = pg0;
+                    ring_pg[2 * ti + 1] = pg1;
+                    if (FP8) {
+                        const uint32_t sc = base + C::OFF_SC + ti * 512;
+                        mbar_expect_tx(bar(C::B_TFULL + ti), 512);
+                        bulk_load(sc, p.scales + (size_t)row0, 256, bar(C::B_TFULL + ti));
+                        bulk_load(sc + 256, p.scales + (size_t)row1, 256, bar(C::B_TFULL + ti));
+                    } else {
+                        mbar_arrive(bar(C::B_TFULL + ti));
+                    }
+                    ut = j + 1;
+                }
+                for (int i = 0; i < NK && ok; i += C::GK, ++ul) {
+                    const int s = ul % C::RK;
+                    const uint32_t ph = ((uint32_t)(ul / C::RK) & 1u) ^ 1u;
+                    if (FP8) {
+                        ok = mbar_wait_inline(bar(C::B_CFREE + s), ph);
+                        if (!ok) break;
+                        mbar_expect_tx(bar(C::B_CFULL + s), C::GK * CCH);
+                        tma_load_3d(base + C::OFF_C + s * C::GK * CCH, &tm_k1, 0, own, i, bar(C::B_CFULL + s));
+                    } else {
+                        ok = mbar_wait_inline(bar(C::B_XFREE + s), ph);
+                        if (!ok) break;
+                        // both CTAs' bytes complete on CTA 0's barrier
+                        if (rank == 0) mbar_expect_tx(bar(C::B_XFULL + s), 2 * CH);
+                        tma_load_pair(base + C::OFF_X + s * CH, &tm_k1, 0, own, i, lead(C::B_XFULL + s));
+                    }
+                }
+            } else if (lane == 0) {
                 if (FP8) {
-                    for (int i = tiles_done - 1; i >= 0 && i >= tiles_done - NT_RING; --i)
-                        mbar_wait(bar(C::B_TFULL + i % NT_RING), (uint32_t)(i / NT_RING) & 1u);
-                    for (int i = uc - 1; i >= 0 && i >= uc - C::NC; --i)
-                        mbar_wait(bar(C::B_CFULL + i % C::NC), (uint32_t)(i / C::NC) & 1u);
+                    for (int i = 0; i < 2 && ok; ++i, ++ul) {  // half the columns: two chunks of either page
+                        const int cs = C::NCK + ul % C::RV;
+                        const uint32_t dst = base + C::OFF_C + (C::NCK * C::GK + (ul % C::RV) * C::GV) * CCH;
+                        ok = mbar_wait_inline(bar(C::B_CFREE + cs), ((uint32_t)(ul / C::RV) & 1u) ^ 1u);
+                        if (!ok) break;
+                        mbar_expect_tx(bar(C::B_CFULL + cs), C::GV * CCH);
+                        tma_load_3d(dst, &tm_k2, 0, row0, 4 * i + 2 * rank, bar(C::B_CFULL + cs));
+                        tma_load_3d(dst + 2 * CCH, &tm_k2, 0, row1, 4 * i + 2 * rank, bar(C::B_CFULL + cs));
+                    }
                 } else {
-                    for (int i = ux - 1; i >= 0 && i >= ux - C::NXS; --i)
-                        mbar_wait(bar(C::B_XFULL + i % C::NXS), (uint32_t)(i / C::NXS) & 1u);
-                    for (int i = uc - 1; i >= 0 && i >= uc - C::NV; --i)
-                        mbar_wait(bar(C::B_VFULL + i % C::NV), (uint32_t)(i / C::NV) & 1u);
+                    const int s = j % C::RV;
+                    if (j == 1) ok = mbar_wait_inline(bar(C::B_QDONE), 0);  // Q was staged there
+                    if (ok) ok = mbar_wait_inline(bar(C::B_VFREE + s), ((uint32_t)(j / C::RV) & 1u) ^ 1u);
+                    if (ok) {
+                        const uint32_t dst = base + C::OFF_V + s * 2 * NVC * CH;
+                        mbar_expect_tx(bar(C::B_VFULL + s), 2 * NVC * CH);
+                        tma_load_3d(dst, &tm_k2, 0, row0, 2 * rank, bar(C::B_VFULL + s));
+                        tma_load_3d(dst + 2 * CH, &tm_k2, 0, row0, 4 + 2 * rank, bar(C::B_VFULL + s));
+                        tma_load_3d(dst + 4 * CH, &tm_k2, 0, row1, 2 * rank, bar(C::B_VFULL + s));
+                        tma_load_3d(dst + 6 * CH, &tm_k2, 0, row1, 4 + 2 * rank, bar(C::B_VFULL + s));
+                        ul = j + 1;
+                    }
                 }
             }
-            bad = __reduce_or_sync(0xffffffffu, bad);
-            if (bad && lane == 0) atomicOr(p.err, bad);
+            ok = __shfl_sync(0xffffffffu, ok, 0);
         }
-        if (lane == 0 && !req_ok) atomicOr(p.err, HS_DEVERR_BAD_REQUEST);
+        if (lane == 0) {
+            // the copies begun have landed before the CTA may end
+            if (kw) mbar_wait_inline(bar(C::B_QFULL), 0);
+            if (!ok) {
+                fail();
+                const int ring = kw ? C::RK : C::RV;
+                const int b0 = FP8 ? (kw ? C::B_CFULL : C::B_CFULL + C::NCK) : (kw ? C::B_XFULL : C::B_VFULL);
+                for (int i = ul - 1; (FP8 || !kw || rank == 0) && i >= 0 && i >= ul - ring; --i)
+                    mbar_wait_inline(bar(b0 + i % ring), (uint32_t)(i / ring) & 1u);
+                for (int i = ut - 1; FP8 && kw && i >= 0 && i >= ut - NTI; --i)
+                    mbar_wait_inline(bar(C::B_TFULL + i % NTI), (uint32_t)(i / NTI) & 1u);
+            }
+        }
+        bad = __reduce_or_sync(0xffffffffu, bad);
+        if (lane == 0 && kw) {
+            if (!req_ok) bad |= HS_DEVERR_BAD_REQUEST;
+            if (bad) atomicOr(p.err, bad);
+        }
     } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA issuer
-        if (lane == 0 && ntiles > 0) {
-            constexpr uint32_t ID_QK = idesc_f16(1u, 0, BM, BN), ID_PV = idesc_f16(1u, 1, BM, 256);
-            bool ok = mbar_wait(bar(C::B_QREADY), 0);
+        // ------------------------------------------------------------ MMA issuer (CTA 0)
+        if (rank == 0 && nsteps > 0) {
+            constexpr uint32_t ID_QK = idesc_f16(FP8 ? 0u : 1u, 0, BM, 128), ID_PV = idesc_f16(FP8 ? 0u : 1u, 1, BM, 256);
+            const uint64_t dk = desc_sw128(base, 16, 1024), dv = desc_sw128(base, CH, 1024);
+            const uint32_t hi = (uint32_t)(dk >> 32), klo = (uint32_t)dk, vlo = (uint32_t)dv;
+            const uint32_t leader = elect_one();
+            bool ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_QREADY), 0));
             tc_fence_after();
-            const uint64_t dq = desc_sw128(base + C::OFF_Q, 16, 1024);
             auto pv = [&](int j) {
-                ok = mbar_wait(bar(C::B_PFULL), (uint32_t)j & 1u) && !misc[1];
+                ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_PFULL), (uint32_t)j & 1u));
                 if (!ok) return;
                 tc_fence_after();
-                const int s = j % C::NV;
-                const uint64_t v = desc_sw128(base + C::OFF_V + s * NVC * KCH, KCH, 1024);
+                const uint32_t v = vlo + ((C::OFF_V + (FP8 ? 0 : j % C::NV) * 2 * NVC * CH) >> 4);
+                const uint32_t a = klo + (C::OFF_P >> 4);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)  // 16 keys: 8 columns of P, 2 KB of V
-                    mma_f16_ts(tmem + TM_O, tmem + TM_P + 8u * k, v + (uint64_t)(128 * k), ID_PV, (j | k) != 0);
-                mma_commit(bar(C::B_VFREE + s));
-                mma_commit(bar(C::B_PVDONE));
-            };
-            int ux = 0;
-            for (int j = 0; j < ntiles && ok; ++j) {
-                if (j > 0) ok = mbar_wait(bar(C::B_SFREE), (uint32_t)(j - 1) & 1u);
-                if (!ok) break;
-                tc_fence_after();
-                for (int i = 0; i < NX && ok; ++i, ++ux) {
-                    const int s = ux % C::NXS;
-                    ok = mbar_wait(bar(C::B_XFULL + s), (uint32_t)(ux / C::NXS) & 1u) && !misc[1];
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t kd = desc_sw128(base + C::OFF_X + s * KCH, 16, 1024);
+                for (int nh = 0; nh < 2; ++nh) {  // 256 value columns each
+                    if (FP8) {  // each half is there, and free again, by itself
+                        ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_VFULL + nh), (uint32_t)j & 1u));
+                        if (!ok) return;
+                        tc_fence_after();
+                    }
+                    if (leader) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_f16_ts(tmem + TM_S, tmem + TM_Q + 32u * i + 8u * k, kd + 2 * k, ID_QK, (i | k) != 0);
-                    mma_commit(bar(C::B_XFREE + s));
+                        for (int pgi = 0; pgi < 2; ++pgi)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)  // 16 keys: 32 bytes of P, 2 KB of V
+                                mma2_ss(tmem + TM_O + 128u * nh, a + ((pgi * CH + 32 * k) >> 4),
+                                        v + ((pgi * NVC * CH + nh * 2 * CH + 2048 * k) >> 4), hi, ID_PV,
+                                        (j | pgi | k) != 0);
+                        if (FP8) commit_both(bar(C::B_VFREE + nh));
+                        if (!FP8 && nh == 1) commit_both(bar(C::B_VFREE + j % C::NV));
+                        if (nh == 1) commit_both(bar(C::B_PVDONE));
+                    }
+                    __syncwarp();
                 }
-                const int s = j % C::NV;
-                if (ok) ok = mbar_wait(bar(C::B_VFULL + s), (uint32_t)(j / C::NV) & 1u) && !misc[1];
-                if (!ok) break;
+                __syncwarp();
+            };
+            int s = 0;
+            uint32_t ph = 0;
+            for (int j = 0; j < nsteps && ok; ++j) {
+                if (j > 0) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_SFREE), (uint32_t)(j - 1) & 1u));
                 tc_fence_after();
-                const uint64_t vd = desc_sw128(base + C::OFF_V + s * NVC * KCH, 16, 1024);
 #pragma unroll
-                for (int i = 0; i < NVC; ++i)
+                for (int c = 0; c < NK; ++c) {
+                    const int g = c % C::GK;  // the chunk within its barrier's group
+                    if (g == 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_XFULL + s), ph));
+                    if (ok) {
+                        if (g == 0) tc_fence_after();
+                        const uint32_t kd = klo + ((C::OFF_X + (s * C::GK + g) * CH) >> 4);
+                        if (leader) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_f16(tmem + TM_S, dq + (uint64_t)((i * QCH + 32 * k) >> 4),
-                                vd + (uint64_t)((i * KCH + 32 * k) >> 4), ID_QK, 1u);
-                mma_commit(bar(C::B_SFULL));
+                            for (int k = 0; k < 4; ++k) {
+                                if (c < NQT)
+                                    mma2_ts(tmem + TM_S, tmem + TM_Q + 32u * c + 8u * k, kd + 2 * k, hi, ID_QK, (c | k) != 0);
+                                else
+                                    mma2_ss(tmem + TM_S, klo + ((C::OFF_Q + (c - NQT) * CH + 32 * k) >> 4), kd + 2 * k, hi,
+                                            ID_QK, 1u);
+                            }
+                            if (g == C::GK - 1) commit_both(bar(C::B_XFREE + s));
+                        }
+                        __syncwarp();
+                    }
+                    if (g == C::GK - 1 && ++s == C::NXG) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                if (leader) commit_both(bar(C::B_SFULL));
+                __syncwarp();
                 if (j > 0) pv(j - 1);
             }
-            if (ok) pv(ntiles - 1);
-            if (!ok) fail();
-            mma_commit(bar(C::B_DRAIN));
-            mbar_wait(bar(C::B_DRAIN), 0);
+            if (ok) pv(nsteps - 1);
+            if (!ok && lane == 0) fail();
+            if (leader) {
+                // every MMA issued has finished before shared and tensor memory go
+                asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                                 bar(C::B_DRAIN))
+                             : "memory");
+                mbar_wait_inline(bar(C::B_DRAIN), 0);
+            }
+            __syncwarp();
         }
-    } else if (warp >= 4 && warp < 8) {
+    } else if (FP8 && warp == 2) {
+        // ------------------------------------------------------------ the keys' factors
+        bool ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_QDONE), 0));
+        // four keys per lane; c takes Q's power back
+        const float c = p.scale_log2 * __int_as_float(misc[5]);
+        for (int j = 0; j < nsteps; ++j) {
+            const int ti = j % NTI;
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_TFULL + ti), (uint32_t)(j / NTI) & 1u));
+            if (!ok) break;
+            const uint32_t at = base + C::OFF_SC + ti * 512 + lane * 16;
+            const float4 f = ld_shared_f4(at);
+            st_shared_v4(at, __float_as_uint(f.x * c), __float_as_uint(f.y * c), __float_as_uint(f.z * c),
+                         __float_as_uint(f.w * c));
+            st_shared_v4(at + C::OFF_SP - C::OFF_SC, __float_as_uint(__log2f(fabsf(f.x))), __float_as_uint(__log2f(fabsf(f.y))),
+                         __float_as_uint(__log2f(fabsf(f.z))), __float_as_uint(__log2f(fabsf(f.w))));
+            const bool neg = __any_sync(0xffffffffu, f.x < 0.f || f.y < 0.f || f.z < 0.f || f.w < 0.f);
+            if (lane == 0) reinterpret_cast<volatile int32_t *>(smem + C::OFF_NEG)[ti] = neg;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::B_TREADY + ti));
+        }
+        if (!ok && lane == 0) fail();
+    } else if (warp >= 4 && warp < 4 + NSW) {
         // ------------------------------------------------------------ softmax, epilogue
-        const int wq = warp & 3, row = wq * 32 + lane;
+        // warp w reaches the tensor memory lanes 32 (w % 4) .. + 31
+        const int wq = warp & 3, hf = (warp - 4) >> 2, tid = hf * 128 + wq * 32 + lane;
+        const int row = tid & 63, kh = wq >> 1;  // query row of this CTA; page of the step
+        constexpr int KT = 32;                   // keys per thread: 32 hf .. of the page
         const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
-        const int mg = mt * BM + row;
+        const int mg = mt * BM + RM * rank + row;
         const bool vrow = mg < p.M;
         const int b = list / p.tpl;
         const int nt = p.T * p.tpl;  // query tokens of the request
@@ -351,145 +577,258 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             tree = p.tree[(size_t)b * nt + t];
             if (nt < 64) tree &= (1ull << nt) - 1;
         }
-        bool ok = true;
-        float m2 = -INFINITY, l = 0.f;
-        if (ntiles > 0) {
-            ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_QFULL), 0));
+        float *xm = reinterpret_cast<float *>(smem + C::OFF_XM);
+        const uint32_t lead_sfree = lead(C::B_SFREE), lead_pfull = lead(C::B_PFULL), lead_qready = lead(C::B_QREADY);
+        // What the MMAs read was written through this CTA's shared or tensor memory
+        // and fenced for the async proxy by its writers: the arrive needs no
+        // cluster-scope release, which takes 1-2k clocks a time.
+        auto arrive_lead = [&](uint32_t cluster_bar) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive_peer(cluster_bar);
+        };
+        bool ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_QFULL), 0));
+        auto q_at = [&](int i) { return base + (i < NQT ? C::OFF_QST + i * CH : C::OFF_Q + (i - NQT) * CH) + row * 128; };
+        float q_pow = 1.f;
+        if (FP8) {
+            // the largest finite magnitude of the CTA's rows, as BF16 bits
+            uint32_t m = 0;
             if (ok) {
-#pragma unroll 1
-                for (int i = 0; i < NX; ++i) {
-                    uint32_t w[32];
+                auto fin = [](uint32_t w) {
+                    const uint32_t x = w & 0x7fff7fffu;
+                    return x & __vcmpltu2(x, 0x7f807f80u);
+                };
+                for (int i = 2 * hf + kh; i < NK; i += 4)
 #pragma unroll
                     for (int u = 0; u < 8; ++u) {
-                        const uint4 v = ld_shared_v4(base + C::OFF_V + i * QCH + row * 128 + ((u ^ (row & 7)) << 4));
-                        w[4 * u] = v.x;
-                        w[4 * u + 1] = v.y;
-                        w[4 * u + 2] = v.z;
-                        w[4 * u + 3] = v.w;
+                        const uint4 v = ld_shared_v4(q_at(i) + ((u ^ (row & 7)) << 4));
+                        m = __vmaxu2(m, __vmaxu2(__vmaxu2(fin(v.x), fin(v.y)), __vmaxu2(fin(v.z), fin(v.w))));
                     }
-                    HS_TMEM_ST32(tmem + lane_off + TM_Q + 32u * i, w);
-                }
-                tmem_wait_st();
             }
-            fence_proxy_async();  // the staging space is refilled by TMA next
-            tc_fence_before();
-            mbar_arrive(bar(C::B_QREADY));
+            m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+            if (lane == 0) xm[warp - 4] = __uint_as_float(m << 16);
+            named_bar_sync(1, 32 * NSW);
+            float top = 0.f;
+#pragma unroll
+            for (int e = 0; e < NSW; ++e) top = fmaxf(top, xm[e]);
+            named_bar_sync(1, 32 * NSW);
+            const int k = min(141 - (int)(__float_as_uint(top) >> 23), 126);
+            q_pow = __uint_as_float((uint32_t)(k + 127) << 23);
+            if (tid == 0) misc[5] = (127 - k) << 23;
         }
-        for (int j = 0; j < ntiles; ++j) {
-            const int ti = j % NT_RING;
-            float s[BN];
+        if (ok && nsteps > 0) {
+#pragma unroll 1
+            for (int i = hf; i < NQT; i += 2) {
+                uint32_t w[32];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const uint4 v = ld_shared_v4(q_at(i) + ((u ^ (row & 7)) << 4));
+                    w[4 * u] = FP8 ? bf16x2_to_f16(v.x, q_pow) : v.x;
+                    w[4 * u + 1] = FP8 ? bf16x2_to_f16(v.y, q_pow) : v.y;
+                    w[4 * u + 2] = FP8 ? bf16x2_to_f16(v.z, q_pow) : v.z;
+                    w[4 * u + 3] = FP8 ? bf16x2_to_f16(v.w, q_pow) : v.w;
+                }
+                HS_TMEM_ST32(tmem + lane_off + TM_Q + 32u * i, w);
+            }
+            if (FP8) {  // the chunks that stay in shared memory, in place, a quarter per thread
+#pragma unroll
+                for (int i = NQT; i < NK; ++i)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const uint32_t at = q_at(i) + (((4 * hf + 2 * kh + u) ^ (row & 7)) << 4);
+                        const uint4 v = ld_shared_v4(at);
+                        st_shared_v4(at, bf16x2_to_f16(v.x, q_pow), bf16x2_to_f16(v.y, q_pow),
+                                     bf16x2_to_f16(v.z, q_pow), bf16x2_to_f16(v.w, q_pow));
+                    }
+            }
+            tmem_wait_st();
+        }
+        fence_proxy_async();  // the staging space is refilled next
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::B_QDONE));
+        arrive_lead(lead_qready);
+
+        float m2 = -INFINITY, l = 0.f;
+        float mp = -INFINITY;  // FP8: P's reference
+        for (int j = 0; j < nsteps; ++j) {
+            const int ti = j % NTI;
+            float s[KT];
+            const uint32_t sc_at = base + C::OFF_SC + ti * 512 + kh * 256 + hf * 128;
+            const uint32_t sp_at = base + C::OFF_SP + ti * 512 + kh * 256 + hf * 128;
             if (ok)
-                ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_TFULL + ti), (uint32_t)(j / NT_RING) & 1u) &&
-                                                 mbar_wait(bar(C::B_SFULL), (uint32_t)j & 1u) && !misc[1]);
+                ok = __all_sync(0xffffffffu, mbar_wait_inline(bar((FP8 ? C::B_TREADY : C::B_TFULL) + ti), (uint32_t)(j / NTI) & 1u) &&
+                                                 mbar_wait_inline(bar(C::B_SFULL), (uint32_t)j & 1u));
             if (ok) {
                 tc_fence_after();
-                uint32_t ra[32], rb[32];
-                HS_TMEM_LD32(tmem + lane_off + TM_S, ra);
-                HS_TMEM_LD32(tmem + lane_off + TM_S + 32, rb);
+                uint32_t ra[32];
+                HS_TMEM_LD32(tmem + lane_off + TM_S + 32u * hf, ra);
                 HS_TMEM_WAIT_LD32(ra);
-                HS_TMEM_WAIT_LD32(rb);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    s[e] = __uint_as_float(ra[e]) * p.scale_log2;
-                    s[32 + e] = __uint_as_float(rb[e]) * p.scale_log2;
+                for (int e = 0; e < KT; e += 4) {
+                    const float4 f = FP8 ? ld_shared_f4(sc_at + 4 * e) : make_float4(p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[e + i] = __uint_as_float(ra[e + i]);
+                    mul2(s[e], s[e + 1], f.x, f.y);
+                    mul2(s[e + 2], s[e + 3], f.z, f.w);
                 }
             }
             tc_fence_before();
-            mbar_arrive(bar(C::B_SFREE));  // S_{j+1} may be written
-            uint32_t pk[BN / 2];
-            bool need = false;
-            float alpha = 1.f;
+            arrive_lead(lead_sfree);  // S_{j+1} may be written
+            const int pg = ok ? ring_pg[2 * ti + kh] : -1;
+            // the keys that this row sees, as bits
+            const long long base_pos = (long long)pg * kPage;
+            const bool tail = pg >= 0 && base_pos + kPage > draft;  // some row may not see some key
+            float tmax = -INFINITY, pmax = -INFINITY;
+            uint32_t mine = ~0u;
+            if (pg < 0) {
+                mine = 0;
+            } else if (tail) {
+                uint64_t seen;
+                const long long d = draft - base_pos;  // < 64
+                if (p.tree) {
+                    if (d >= 0)
+                        seen = ((1ull << d) - 1) | (tree << d);
+                    else
+                        seen = d > -64 ? tree >> -d : 0ull;
+                } else {
+                    const long long n = d + t + 1;
+                    seen = n >= 64 ? ~0ull : (n <= 0 ? 0ull : (1ull << n) - 1);
+                }
+                mine = (uint32_t)(seen >> (KT * hf));
+            }
+            const bool hide = !__all_sync(0xffffffffu, mine == ~0u);
             if (ok) {
-                const int pg = ring_pg[ti];
-                const uint32_t sc_at = base + C::OFF_SC + ti * BN * 4;
+                if (hide) {
+#pragma unroll
+                    for (int e = 0; e < KT; ++e) s[e] = (mine >> e) & 1u ? s[e] : -INFINITY;
+                }
+                float mx[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    mx[e] = max3(s[e], s[e + 4], s[e + 8]);
+                    mx[e] = max3(mx[e], s[e + 12], s[e + 16]);
+                    mx[e] = max3(mx[e], s[e + 20], s[e + 24]);
+                    mx[e] = fmaxf(mx[e], s[e + 28]);
+                }
+                tmax = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
                 if (FP8) {
+                    // scores plus log2|scale|; a hidden row's scale may be anything
+                    float pm[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                    for (int e = 0; e < BN / 4; ++e) {
-                        const float4 f = ld_shared_f4(sc_at + 16 * e);
-                        s[4 * e] *= f.x;
-                        s[4 * e + 1] *= f.y;
-                        s[4 * e + 2] *= f.z;
-                        s[4 * e + 3] *= f.w;
-                    }
-                }
-                // the keys that this row sees, as bits
-                const long long base_pos = (long long)pg * kPage;
-                const bool tail = pg >= 0 && base_pos + kPage > draft;  // some row may not see some key
-                uint64_t seen = ~0ull;
-                if (pg < 0) {
-                    seen = 0;
-                } else if (tail) {
-                    const long long d = draft - base_pos;  // < 64
-                    if (p.tree) {
-                        if (d >= 0)
-                            seen = ((1ull << d) - 1) | (tree << d);
-                        else
-                            seen = d > -64 ? tree >> -d : 0ull;
-                    } else {
-                        const long long n = d + t + 1;
-                        seen = n >= 64 ? ~0ull : (n <= 0 ? 0ull : (1ull << n) - 1);
-                    }
-                }
-                if (!__all_sync(0xffffffffu, seen == ~0ull)) {
-                    const uint32_t lo = (uint32_t)seen, hi = (uint32_t)(seen >> 32);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        s[e] = (lo >> e) & 1u ? s[e] : -INFINITY;
-                        s[32 + e] = (hi >> e) & 1u ? s[32 + e] : -INFINITY;
-                    }
-                }
-                float mx[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    mx[e] = fmaxf(fmaxf(s[e], s[e + 8]), fmaxf(s[e + 16], s[e + 24]));
-                    mx[e] = fmaxf(mx[e], fmaxf(fmaxf(s[e + 32], s[e + 40]), fmaxf(s[e + 48], s[e + 56])));
-                }
-#pragma unroll
-                for (int w = 4; w >= 1; w >>= 1)
-#pragma unroll
-                    for (int e = 0; e < w; ++e) mx[e] = fmaxf(mx[e], mx[e + w]);
-                const float tmax = mx[0];
-                if (j == 0) {
-                    m2 = tmax;
-                } else if (tmax > m2 + TAU2) {
-                    need = true;
-                    alpha = exp2f(m2 - tmax);
-                    l *= alpha;
-                    m2 = tmax;
-                }
-                const float mref = m2 == -INFINITY ? 0.f : m2;
-                float ls[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int e = 0; e < BN / 4; ++e) {
-                    float a0 = exp2f(s[4 * e] - mref), a1 = exp2f(s[4 * e + 1] - mref);
-                    float a2 = exp2f(s[4 * e + 2] - mref), a3 = exp2f(s[4 * e + 3] - mref);
-                    ls[e & 3] += (a0 + a1) + (a2 + a3);
-                    if (FP8) {
-                        float4 f = ld_shared_f4(sc_at + 16 * e);
-                        if (tail) {  // a row that is not seen may have any scale
-                            f.x = fabsf(f.x) <= FLT_MAX ? f.x : 0.f;
-                            f.y = fabsf(f.y) <= FLT_MAX ? f.y : 0.f;
-                            f.z = fabsf(f.z) <= FLT_MAX ? f.z : 0.f;
-                            f.w = fabsf(f.w) <= FLT_MAX ? f.w : 0.f;
+                    for (int e = 0; e < KT; e += 4) {
+                        const float4 f = ld_shared_f4(sp_at + 4 * e);
+                        float t0 = s[e], t1 = s[e + 1], t2 = s[e + 2], t3 = s[e + 3];
+                        add2(t0, t1, f.x, f.y);
+                        add2(t2, t3, f.z, f.w);
+                        if (hide) {
+                            t0 = (mine >> e) & 1u ? t0 : -INFINITY;
+                            t1 = (mine >> (e + 1)) & 1u ? t1 : -INFINITY;
+                            t2 = (mine >> (e + 2)) & 1u ? t2 : -INFINITY;
+                            t3 = (mine >> (e + 3)) & 1u ? t3 : -INFINITY;
                         }
-                        a0 *= f.x;
-                        a1 *= f.y;
-                        a2 *= f.z;
-                        a3 *= f.w;
+                        pm[0] = max3(pm[0], t0, t1);
+                        pm[1] = max3(pm[1], t2, t3);
                     }
-                    pk[2 * e] = pack_bf16(a0, a1);
-                    pk[2 * e + 1] = pack_bf16(a2, a3);
+                    pmax = fmaxf(pm[0], pm[1]);
                 }
-                l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+            }
+            // A row's four threads share its references: where some row of the CTA
+            // outgrows its own, the rows' four maxima meet in shared memory.
+            float alpha = 1.f;
+            auto outgrown = [](float x, float ref) { return x > ref + TAU2 || (ref == -INFINITY && x != -INFINITY); };
+            const bool grow = any_softmax(outgrown(tmax, m2) || (FP8 && outgrown(pmax, mp)));
+            if (grow) {
+                xm[tid] = tmax;
+                if (FP8) xm[32 * NSW + tid] = pmax;
+                named_bar_sync(1, 32 * NSW);
+                auto of_row = [&](int o) {
+                    return fmaxf(fmaxf(xm[o + row], xm[o + row + 64]), fmaxf(xm[o + row + 128], xm[o + row + 192]));
+                };
+                const float both = of_row(0), pboth = FP8 ? of_row(32 * NSW) : 0.f;
+                named_bar_sync(1, 32 * NSW);  // read before the next writes
+                if (outgrown(both, m2)) {
+                    alpha = exp2f(m2 - both);  // 0 where the row had seen nothing
+                    l *= alpha;
+                    m2 = both;
+                }
+                if (FP8) {
+                    alpha = 1.f;
+                    if (outgrown(pboth, mp)) {
+                        alpha = exp2f(mp - pboth);
+                        mp = pboth;
+                    }
+                }
+            }
+            uint32_t pk[KT / 2];
+            if (ok) {
+                const float mneg = m2 == -INFINITY ? 0.f : -m2, pneg = mp == -INFINITY ? 0.f : 7.f - mp;
+                float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+#pragma unroll
+                for (int e = 0; e < KT; e += 4) {
+                    float a0 = s[e], a1 = s[e + 1], a2 = s[e + 2], a3 = s[e + 3];
+                    add2(a0, a1, mneg, mneg);
+                    add2(a2, a3, mneg, mneg);
+                    a0 = ex2(a0);
+                    a1 = ex2(a1);
+                    a2 = ex2(a2);
+                    a3 = ex2(a3);
+                    add2(l0, l1, a0, a1);
+                    add2(l2, l3, a2, a3);
+                    if (FP8) {
+                        const float4 f = ld_shared_f4(sp_at + 4 * e);
+                        a0 = f.x;
+                        a1 = f.y;
+                        a2 = f.z;
+                        a3 = f.w;
+                        add2(a0, a1, pneg, pneg);
+                        add2(a2, a3, pneg, pneg);
+                        add2(a0, a1, s[e], s[e + 1]);
+                        add2(a2, a3, s[e + 2], s[e + 3]);
+                        pk[e / 2] = pack_f16(ex2(a0), ex2(a1));
+                        pk[e / 2 + 1] = pack_f16(ex2(a2), ex2(a3));
+                    } else {
+                        pk[e / 2] = pack_bf16(a0, a1);
+                        pk[e / 2 + 1] = pack_bf16(a2, a3);
+                    }
+                }
+                l += (l0 + l1) + (l2 + l3);
+                if (FP8 && hide) {
+                    // a hidden row's scale may be NaN
+#pragma unroll
+                    for (int e = 0; e < KT / 2; ++e)
+                        pk[e] &= ((mine >> (2 * e)) & 1u ? 0xffffu : 0u) | ((mine >> (2 * e + 1)) & 1u ? 0xffff0000u : 0u);
+                }
+                if (FP8 && reinterpret_cast<volatile int32_t *>(smem + C::OFF_NEG)[ti]) {
+#pragma unroll
+                    for (int e = 0; e < KT; e += 4) {  // signs of the scales
+                        const float4 f = ld_shared_f4(sc_at + 4 * e);
+                        pk[e / 2] ^= ((__float_as_uint(f.x) >> 16) & 0x8000u) | (__float_as_uint(f.y) & 0x80000000u);
+                        pk[e / 2 + 1] ^= ((__float_as_uint(f.z) >> 16) & 0x8000u) | (__float_as_uint(f.w) & 0x80000000u);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::B_TFREE + ti));
+            // P and O are free once the previous PV is done; BF16: this CTA's V has
+            // landed (FP8: its converters tell the MMA issuer themselves)
+            if (ok && j > 0) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_PVDONE), (uint32_t)(j - 1) & 1u));
+            if (ok && !FP8)
+                ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_VFULL + j % C::NV), (uint32_t)(j / C::NV) & 1u));
+            if (ok) {
+                tc_fence_after();
+                const uint32_t pr = base + C::OFF_P + kh * CH + row * 128;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    st_shared_v4(pr + (((c + 4 * hf) ^ (row & 7)) << 4), pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
                 if (tail && !FP8) {
                     // A row that some query does not see may hold infinities or
-                    // NaN, and 0 x NaN would reach that query's sum: they become
-                    // zeros here (S_j is done with them; a query that does see
-                    // them has them in its scores).
-                    const uint32_t v0 = base + C::OFF_V + (j % C::NV) * NVC * KCH + row * 16;
+                    // NaN, and 0 x NaN would reach that query's sum: in V they
+                    // become zeros (a query that does see them has them in its
+                    // scores). The page's 32 KB, by its 128 threads.
+                    const uint32_t v0 = base + C::OFF_V + (j % C::NV) * 2 * NVC * CH + kh * NVC * CH + (row + 64 * hf) * 16;
 #pragma unroll 4
                     for (int u = 0; u < 16; ++u) {
-                        uint4 v = ld_shared_v4(v0 + 2048 * u);
+                        const uint4 v = ld_shared_v4(v0 + 2048 * u);
                         uint32_t w[4] = {v.x, v.y, v.z, v.w};
                         bool hit = false;
 #pragma unroll
@@ -500,56 +839,45 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         }
                         if (hit) st_shared_v4(v0 + 2048 * u, w[0], w[1], w[2], w[3]);
                     }
-                    fence_proxy_async();
                 }
-                // P and O are free once the previous PV is done
-                if (j > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_PVDONE), (uint32_t)(j - 1) & 1u));
-            }
-            mbar_arrive(bar(C::B_TFREE + ti));
-            if (ok) {
-                tc_fence_after();
-                HS_TMEM_ST32(tmem + lane_off + TM_P, pk);
-                if (__any_sync(0xffffffffu, need)) {
-#pragma unroll 1
-                    for (int cc = 0; cc < 8; ++cc) {
-                        uint32_t o[32];
-                        const uint32_t at = tmem + lane_off + TM_O + 32 * cc;
-                        HS_TMEM_LD32(at, o);
-                        HS_TMEM_WAIT_LD32(o);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                        HS_TMEM_ST32(at, o);
-                    }
-                }
-                tmem_wait_st();
+                fence_proxy_async();
+                if (grow && j > 0 && __any_sync(0xffffffffu, alpha != 1.f))
+                    rescale_o(tmem + lane_off + TM_O + 128u * hf, alpha);
             }
             tc_fence_before();
-            mbar_arrive(bar(C::B_PFULL));
+            arrive_lead(lead_pfull);
         }
-        if (ok && ntiles > 0) {
-            ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_PVDONE), (uint32_t)(ntiles - 1) & 1u));
+        if (ok && nsteps > 0) {
+            ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_PVDONE), (uint32_t)(nsteps - 1) & 1u));
             tc_fence_after();
         }
-        if (!ok) fail();
+        if (!ok && lane == 0) fail();
+        // the row's sum over its four threads' keys
+        xm[tid] = l;
+        named_bar_sync(1, 32 * NSW);
+        l = (xm[row] + xm[row + 64]) + (xm[row + 128] + xm[row + 192]);
         // rows that see nothing: out 0, lse -inf
-        const float inv = l == 0.f ? 0.f : __fdividef(1.f, l);
+        const float inv = l == 0.f ? 0.f : __fdividef(FP8 ? (mp == -INFINITY ? 0.f : ex2(mp - m2 - 7.f)) : 1.f, l);
         const bool one = p.nsplit == 1;
-        if (ok && (one || ntiles > 0)) {
-            const size_t orow = one ? (size_t)list * p.M + mg : ((size_t)split * p.lists + list) * p.M + mg;
+        if (ok && (one || nsteps > 0)) {
+            // O / l through shared memory, idle by now, in 32-row boxes of 128
+            // swizzled bytes per row: this thread's value columns are
+            // 256 hf + 128 kh + (0..127). Rows past M are clipped by the map.
+            const int wr = wq & 1;  // which 32 rows
+            const uint32_t st0 = base + C::OFF_V + wr * 4096 + (uint32_t)(row & 31) * 128u;
 #pragma unroll 1
-            for (int cc = 0; cc < 8; ++cc) {
+            for (int cc = 0; cc < 4; ++cc) {
                 uint32_t o[32];
-                if (ntiles > 0) {
-                    HS_TMEM_LD32(tmem + lane_off + TM_O + 32 * cc, o);
+                if (nsteps > 0) {
+                    HS_TMEM_LD32(tmem + lane_off + TM_O + 128 * hf + 32 * cc, o);
                     HS_TMEM_WAIT_LD32(o);
                 } else {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = 0u;
                 }
-                if (!vrow) continue;
-                const size_t at = orow * 512 + 256 * half + 32 * cc;
+                const int col = 256 * hf + 128 * kh + 32 * cc;
                 if (one) {
-                    uint4 *d = reinterpret_cast<uint4 *>(p.out + at);
+                    const uint32_t at = st0 + (uint32_t)(col >> 6) * 8192u;
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
                         uint32_t w[4];
@@ -557,75 +885,124 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         for (int e = 0; e < 4; ++e)
                             w[e] = pack_bf16(__uint_as_float(o[8 * u + 2 * e]) * inv,
                                              __uint_as_float(o[8 * u + 2 * e + 1]) * inv);
-                        d[u] = make_uint4(w[0], w[1], w[2], w[3]);
+                        const int c = ((col & 32) >> 3) + u;
+                        st_shared_v4(at + (uint32_t)((c ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
                     }
                 } else {
                     // partials stay f32: a third rounding to BF16 would show next to
                     // those of P and of the output
-                    float4 *d = reinterpret_cast<float4 *>(p.ws_o + at);
+                    const uint32_t at = st0 + (uint32_t)(col >> 5) * 8192u;
 #pragma unroll
                     for (int u = 0; u < 8; ++u)
-                        d[u] = make_float4(__uint_as_float(o[4 * u]) * inv, __uint_as_float(o[4 * u + 1]) * inv,
-                                           __uint_as_float(o[4 * u + 2]) * inv, __uint_as_float(o[4 * u + 3]) * inv);
+                        st_shared_v4(at + (uint32_t)((u ^ (row & 7)) << 4), __float_as_uint(__uint_as_float(o[4 * u]) * inv),
+                                     __float_as_uint(__uint_as_float(o[4 * u + 1]) * inv),
+                                     __float_as_uint(__uint_as_float(o[4 * u + 2]) * inv),
+                                     __float_as_uint(__uint_as_float(o[4 * u + 3]) * inv));
                 }
             }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+                const int wide = one ? 64 : 32;
+                const int z = one ? list : split * p.lists + list;
+                const int c0 = 256 * hf + 128 * kh;
+                for (int c = c0; c < c0 + 128; c += wide)
+                    tma_store_3d(&tm_o, base + C::OFF_V + (uint32_t)(c / wide) * 8192u + wr * 4096, c,
+                                 mt * BM + RM * rank + 32 * wr, z);
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                // the stores have read shared memory before the CTA may end
+                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            }
+            __syncwarp();
         }
-        if (vrow && half == 0) {
+        if (vrow && kh == 0 && hf == 0) {
             const float lse = (!ok || l == 0.f) ? -INFINITY : (m2 + __log2f(l)) * 0.69314718055994531f;
             if (one)
                 p.lse[(size_t)list * p.M + mg] = lse;
             else
                 p.ws_lse[((size_t)split * p.lists + list) * p.M + mg] = lse;
         }
-    } else if (FP8 && warp >= 8) {
+    } else if (FP8 && warp >= 4 + NSW) {
         // ------------------------------------------------------------ converters
-        const int grp = (warp - 8) >> 2, tid = threadIdx.x & 127;
-        bool ok = ntiles > 0 && __all_sync(0xffffffffu, mbar_wait(bar(C::B_QREADY), 0));  // Q was staged there
-        const int total = 9 * ntiles;
-        for (int u = grp; u < total; u += 2) {
-            const int j = u / 9, i = u % 9, cs = u % C::NC;
-            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_CFULL + cs), (uint32_t)(u / C::NC) & 1u) && !misc[1]);
-            uint4 w[2];
-            if (ok) {
-                w[0] = ld_shared_v4(base + C::OFF_C + cs * CCH + 16 * tid);
-                w[1] = ld_shared_v4(base + C::OFF_C + cs * CCH + 16 * (tid + 128));
-            }
-            mbar_arrive(bar(C::B_CFREE + cs));
-            uint32_t dst, full;
-            if (i < NX) {
-                const int ux = NX * j + i, s = ux % C::NXS;
-                if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_XFREE + s), ((uint32_t)(ux / C::NXS) & 1u) ^ 1u));
-                dst = base + C::OFF_X + s * KCH;
-                full = bar(C::B_XFULL + s);
-            } else {
-                const int s = j % C::NV;
-                if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_VFREE + s), ((uint32_t)(j / C::NV) & 1u) ^ 1u));
-                dst = base + C::OFF_V + (s * NVC + i - NX) * KCH;
-                full = bar(C::B_VFULL + s);
-            }
-            if (ok) {
+        const bool kw = warp < 8 + NSW;
+        const int tid = threadIdx.x & 127;
+        // V's space held the staged Q
+        bool ok = kw || __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_QDONE), 0));
+        // A group of chunks at a time: the next group's codes are loaded while this
+        // one's stores are fenced.
+        auto convert = [&](auto is_k) {
+            constexpr bool K = decltype(is_k)::value;
+            constexpr int G = K ? C::GK : C::GV, ring = K ? C::NCK : C::NCV, c0 = K ? 0 : C::NCK;
+            const int total = (K ? NK / G : 2) * nsteps;
+            uint4 w[G][2];
+            int cs = 0, xs = 0;
+            uint32_t cph = 0, xph = 1;
+            auto load = [&]() {
+                if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_CFULL + c0 + cs), cph));
+                const uint32_t src = base + C::OFF_C + ((K ? 0 : C::NCK * C::GK) + cs * G) * CCH + 16 * tid;
+                if (ok) {
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int un = tid + 128 * k, key = un >> 2, part = un & 3;
-                    uint32_t o[8];
-                    e4m3x4_to_bf16(w[k].x, o[0], o[1]);
-                    e4m3x4_to_bf16(w[k].y, o[2], o[3]);
-                    e4m3x4_to_bf16(w[k].z, o[4], o[5]);
-                    e4m3x4_to_bf16(w[k].w, o[6], o[7]);
-                    st_shared_v4(dst + key * 128 + (((2 * part) ^ (key & 7)) << 4), o[0], o[1], o[2], o[3]);
-                    st_shared_v4(dst + key * 128 + (((2 * part + 1) ^ (key & 7)) << 4), o[4], o[5], o[6], o[7]);
+                    for (int g = 0; g < G; ++g) {
+                        w[g][0] = ld_shared_v4(src + g * CCH);
+                        w[g][1] = ld_shared_v4(src + g * CCH + 2048);
+                    }
                 }
+            };
+            if (total > 0) load();
+#pragma unroll 1
+            for (int i = 0; i < total; ++i) {
+                if (ok)
+                    ok = __all_sync(0xffffffffu, K ? mbar_wait_inline(bar(C::B_XFREE + xs), xph)
+                                                   : mbar_wait_inline(bar(C::B_VFREE + (i & 1)), ((uint32_t)(i >> 1) & 1u) ^ 1u));
+                if (ok) {
+                    const uint32_t dst = base + (K ? C::OFF_X + xs * G * CH : C::OFF_V + (i & 1) * 2 * CH) + (tid >> 2) * 128;
+                    const int key = (tid >> 2) & 7, part = 2 * (tid & 3);  // rows key and key + 32: the same swizzle
+#pragma unroll
+                    for (int g = 0; g < G; ++g)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            // K: the chunks in turn; V: two of the first page, two of the second
+                            const uint32_t at = dst + (K ? g : (g >> 1) * NVC + (g & 1)) * CH + k * 4096;
+                            uint32_t o[8];
+                            e4m3x4_to_f16<!K>(w[g][k].x, o[0], o[1]);
+                            e4m3x4_to_f16<!K>(w[g][k].y, o[2], o[3]);
+                            e4m3x4_to_f16<!K>(w[g][k].z, o[4], o[5]);
+                            e4m3x4_to_f16<!K>(w[g][k].w, o[6], o[7]);
+                            st_shared_v4(at + ((part ^ key) << 4), o[0], o[1], o[2], o[3]);
+                            st_shared_v4(at + (((part + 1) ^ key) << 4), o[4], o[5], o[6], o[7]);
+                        }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::B_CFREE + c0 + cs));
+                if (++cs == ring) {
+                    cs = 0;
+                    cph ^= 1u;
+                }
+                if (i + 1 < total) load();
                 fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_peer(lead(K ? C::B_XFULL + xs : C::B_VFULL + (i & 1)));
+                if (K && ++xs == C::NXG) {
+                    xs = 0;
+                    xph ^= 1u;
+                }
             }
-            mbar_arrive(full);
+        };
+        if constexpr (FP8) {
+            static_assert(NK % C::GK == 0 && NVC == C::GV && C::NXS % C::GK == 0, "groups of chunks");
+            if (kw)
+                convert(std::true_type{});
+            else
+                convert(std::false_type{});
         }
-        if (!ok && ntiles > 0) fail();
+        if (!ok && lane == 0) fail();
     }
 
     tc_fence_before();
     __syncthreads();
+    cluster_sync_all();  // no CTA leaves while the other's MMAs or arrivals may reach it
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem, 512);
+    if (warp == 1) tmem_dealloc2(tmem, 512);
 }
 
 // Joins the splits: out = sum_s w_s O_s / sum_s w_s, w_s = exp(lse_s - max), in
@@ -633,6 +1010,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 __global__ void __launch_bounds__(256)
 page_combine_kernel(const float *__restrict__ ws_o, const float *__restrict__ ws_lse, int nsplit, int rows,
                     __nv_bfloat16 *__restrict__ out, float *__restrict__ lse) {
+    grid_dep_wait();  // the splits' partials
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int64_t row = i >> 7;
     const int c = (int)(i & 127) * 4;
@@ -672,20 +1050,20 @@ struct PagePlan {
 };
 
 // Splits of a list of N pages: the count that a model of the launch makes
-// shortest. A page takes a CTA about 1 us, a CTA's start and epilogue 5 us, a
-// second launch 3 us and the partials' write and read about 5 MB per us.
+// shortest. Two pages take a pair of CTAs about 1.6 us, their start and epilogue
+// 6 us, a second launch 2 us and the partials' write and read about 5 MB per us.
 PagePlan page_plan(int64_t lists, int64_t T, int64_t H, int64_t N) {
     PagePlan pl{};
     pl.M = (int)(T * H);
     pl.mtiles = (pl.M + BM - 1) / BM;
     const int64_t sms = sm_count(), units = lists * pl.mtiles * 2;
-    const int64_t most = N < 128 ? N : 128;
+    const int64_t steps = (N + 1) / 2, most = steps < 128 ? steps : 128;
     double best = 1e300;
     pl.nsplit = 1;
     for (int64_t ns = 1; ns <= most; ++ns) {
         const double waves = (double)((units * ns + sms - 1) / sms);
-        double t = waves * ((double)((N + ns - 1) / ns) * 1.0 + 5.0);
-        if (ns > 1) t += 3.0 + (double)ns * lists * pl.M * 512 * 8 / 5e6;
+        double t = waves * ((double)((steps + ns - 1) / ns) * 1.6 + 6.0);
+        if (ns > 1) t += 2.0 + (double)ns * lists * pl.M * 512 * 8 / 5e6;
         if (t < best * 0.98) {
             best = t;
             pl.nsplit = (int)ns;
@@ -707,7 +1085,7 @@ bool make_page_map(CUtensorMap *m, bool fp8, const void *rows, uint64_t n_rows, 
     const cuuint64_t rb = fp8 ? kDim : 2 * kDim;
     cuuint64_t dims[3] = {64, n_rows, 9};
     cuuint64_t strides[2] = {rb, rb / 9};
-    cuuint32_t box[3] = {64, (cuuint32_t)BN, nchunks};
+    cuuint32_t box[3] = {64, (cuuint32_t)kPage, nchunks};
     cuuint32_t es[3] = {1, 1, 1};
     return fn(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
               const_cast<void *>(rows), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -717,7 +1095,7 @@ bool make_page_map(CUtensorMap *m, bool fp8, const void *rows, uint64_t n_rows, 
 
 template <bool FP8>
 hs_status launch_pages(dim3 grid, int dev, cudaStream_t s, const CUtensorMap &tq, const CUtensorMap &k1,
-                       const CUtensorMap &k4, const PageParams &p) {
+                       const CUtensorMap &k2, const CUtensorMap &to, const PageParams &p) {
     static std::atomic<int> state[64];
     if (dev < 0 || dev >= 64) return HS_ERR_UNSUPPORTED;
     if (state[dev].load(std::memory_order_acquire) != 1) {
@@ -725,8 +1103,19 @@ hs_status launch_pages(dim3 grid, int dev, cudaStream_t s, const CUtensorMap &tq
                                          PCfg<FP8>::SMEM_ALLOC));
         state[dev].store(1, std::memory_order_release);
     }
-    page_decode_kernel<FP8><<<grid, PCfg<FP8>::THREADS, PCfg<FP8>::SMEM_ALLOC, s>>>(tq, k1, k4, p);
-    return cudaGetLastError() == cudaSuccess ? HS_OK : HS_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(PCfg<FP8>::THREADS, 1, 1);
+    cfg.dynamicSmemBytes = PCfg<FP8>::SMEM_ALLOC;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, page_decode_kernel<FP8>, tq, k1, k2, to, p) == cudaSuccess ? HS_OK : HS_ERR_CUDA;
 }
 
 // `lists` lists of T query tokens each; tpl > 1 (with T = 1): lists / tpl
@@ -751,11 +1140,17 @@ hs_status page_entry(hs_pool_t pool, int64_t lists, int32_t T, int32_t tpl, int3
     if (pl.nsplit > 1 && (!d_workspace || ws_bytes < pl.ws_bytes || ((uintptr_t)d_workspace & 255u)))
         return HS_ERR_INVALID_ARG;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    CUtensorMap tq, k1, k4;
+    CUtensorMap tq, k1, k2, to;
     const uint64_t rows = (uint64_t)(pool->cfg.n_gpu_blocks + 1) * kPage;
-    if (!make_map(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d_q, kDim, pl.M, lists, 2 * kDim, 64, BM,
+    if (!make_map(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d_q, kDim, pl.M, lists, 2 * kDim, 64, RM,
                   CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_page_map(&k1, fp8, pool->d_rows, rows, 1) || !make_page_map(&k4, fp8, pool->d_rows, rows, NVC))
+        !make_page_map(&k1, fp8, pool->d_rows, rows, fp8 ? PCfg<true>::GK : 1) || !make_page_map(&k2, fp8, pool->d_rows, rows, 2))
+        return HS_ERR_CUDA;
+    // the output (one split), or the splits' f32 partials
+    const bool one = pl.nsplit == 1;
+    if (!make_map(&to, one ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                  one ? d_out : d_workspace, 512, pl.M, (uint64_t)lists * pl.nsplit, one ? 1024 : 2048, one ? 64 : 32,
+                  32, CU_TENSOR_MAP_SWIZZLE_128B))
         return HS_ERR_CUDA;
     PageParams p{};
     p.pages = d_pages;
@@ -764,9 +1159,7 @@ hs_status page_entry(hs_pool_t pool, int64_t lists, int32_t T, int32_t tpl, int3
     p.table = reinterpret_cast<const int2 *>(pool->d_page);
     p.tree = d_tree;
     p.scales = pool->d_scales;
-    p.out = static_cast<__nv_bfloat16 *>(d_out);
     p.lse = d_lse;
-    p.ws_o = pl.nsplit > 1 ? static_cast<float *>(d_workspace) : nullptr;
     p.ws_lse = pl.nsplit > 1 ? reinterpret_cast<float *>(static_cast<uint8_t *>(d_workspace) + pl.ws_o_bytes)
                              : nullptr;
     p.err = pool->d_err;
@@ -782,13 +1175,23 @@ hs_status page_entry(hs_pool_t pool, int64_t lists, int32_t T, int32_t tpl, int3
     p.tpl = tpl;
     p.scale_log2 = sm_scale * 1.4426950408889634f;
     const dim3 grid(2 * pl.nsplit, pl.mtiles, (unsigned)lists);
-    const hs_status st = fp8 ? launch_pages<true>(grid, dev, s, tq, k1, k4, p)
-                             : launch_pages<false>(grid, dev, s, tq, k1, k4, p);
+    const hs_status st = fp8 ? launch_pages<true>(grid, dev, s, tq, k1, k2, to, p)
+                             : launch_pages<false>(grid, dev, s, tq, k1, k2, to, p);
     if (st != HS_OK || pl.nsplit == 1) return st;
     const int n = (int)(lists * pl.M);
-    page_combine_kernel<<<(unsigned)(((int64_t)n * 128 + 255) / 256), 256, 0, s>>>(p.ws_o, p.ws_lse, pl.nsplit, n,
-                                                                                   p.out, d_lse);
-    return cudaGetLastError() == cudaSuccess ? HS_OK : HS_ERR_CUDA;
+    cudaLaunchConfig_t cc = {};
+    cc.gridDim = dim3((unsigned)(((int64_t)n * 128 + 255) / 256), 1, 1);
+    cc.blockDim = dim3(256, 1, 1);
+    cc.stream = s;
+    cudaLaunchAttribute ca[1];
+    ca[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    ca[0].val.programmaticStreamSerializationAllowed = 1;
+    cc.attrs = ca;
+    cc.numAttrs = 1;
+    return cudaLaunchKernelEx(&cc, page_combine_kernel, (const float *)d_workspace, (const float *)p.ws_lse, pl.nsplit, n,
+                              static_cast<__nv_bfloat16 *>(d_out), d_lse) == cudaSuccess
+               ? HS_OK
+               : HS_ERR_CUDA;
 }
 
 }  // namespace

@@ -67,6 +67,18 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
     return mbar_try(bar, parity) || mbar_wait_slow(bar, parity, limit_ns);
 }
 
+// The same wait without a call: where many registers are live the call's
+// convention would spill them on the way to every wait.
+__device__ __forceinline__ bool mbar_wait_inline(uint32_t bar, uint32_t parity) {
+    if (mbar_try(bar, parity)) return true;
+    const uint64_t t0 = globaltimer();
+    bool ok;
+    do {
+        ok = mbar_try(bar, parity);
+    } while (!ok && globaltimer() - t0 <= 2000000000ull);
+    return ok;
+}
+
 // Cluster-scope variants: waits that acquire what a peer CTA released, and an
 // arrive on a barrier in a peer CTA's shared memory (address from mapa).
 __device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity) {
