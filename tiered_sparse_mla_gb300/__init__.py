@@ -152,27 +152,50 @@ def _ptr(t) -> int | None:
 
 def _arg(name: str, t, dtype: str, *shape, optional: bool = False) -> int | None:
     """Device pointer of a CUDA tensor whose type (a torch dtype's name) and shape
-    are checked first (-1 in `shape`: any size): the kernels read it by both."""
-    if t is None:
-        if optional:
-            return None
+    are checked first: the kernels read it by both."""
+    if t is None and optional:
+        return None
+    # one look at a tensor that is as it should be: a call takes a few microseconds
+    try:
+        if t.shape == shape and t.dtype is _dtypes[dtype] and t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except (AttributeError, KeyError):
+        pass
+    import torch
+    if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name}: expected a CUDA tensor")
-    if str(t.dtype) != "torch." + dtype:
+    _dtypes[dtype] = getattr(torch, dtype)
+    if t.dtype is not _dtypes[dtype]:
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
-    if len(t.shape) != len(shape) or any(w not in (-1, n) for n, w in zip(t.shape, shape)):
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {list(shape)}, got {list(t.shape)}")
     return _ptr(t)
 
 
+_dtypes: dict = {}
+
+
 def _ws(workspace):
-    return (0 if workspace is None else workspace.numel() * workspace.element_size(),
-            _ptr(workspace))
+    if workspace is None:
+        return 0, None
+    return workspace.numel() * workspace.element_size(), _ptr(workspace)
+
+
+_raw_stream = None
 
 
 def _stream(stream) -> int | None:
-    import torch
     if stream is None:
-        stream = torch.cuda.current_stream()
+        global _raw_stream
+        if _raw_stream is None:
+            import torch
+            # the current stream's handle, without a Stream object for it
+            get_dev = getattr(torch._C, "_cuda_getDevice", None)
+            get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            if get is None or get_dev is None or not torch.cuda.is_initialized():
+                return torch.cuda.current_stream().cuda_stream
+            _raw_stream = lambda: get(get_dev())
+        return _raw_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
@@ -313,16 +336,19 @@ def hs_append_rows(pool: int, rows, req_ids, start=None, index=None, stream=None
         _arg("index", index, "int32", B, T, optional=True), _stream(stream)))
 
 
+def _means_shape(pool: int):
+    cfg = hs_pool_config()
+    _check("hs_pool_get_config", load().hs_pool_get_config(pool, C.byref(cfg)))
+    return cfg.max_requests, (cfg.max_ctx + 63) // 64, 576
+
+
 def hs_page_means(pool: int, req, page, means, stream=None):
     """Mean rows of pages (see hs.h). req, page int32 [n]; means bf16
     [max_requests][max_pages][576]."""
     n = req.shape[0]
-    cfg = hs_pool_config()
-    _check("hs_pool_get_config", load().hs_pool_get_config(pool, C.byref(cfg)))
     _check("hs_page_means", load().hs_page_means(
         pool, n, _arg("req", req, "int32", n), _arg("page", page, "int32", n),
-        _arg("means", means, "bfloat16", cfg.max_requests, (cfg.max_ctx + 63) // 64, 576),
-        _stream(stream)))
+        _arg("means", means, "bfloat16", *_means_shape(pool)), _stream(stream)))
 
 
 def hs_select_workspace_bytes(pool: int, B: int, T: int) -> int:
@@ -337,12 +363,10 @@ def hs_select_pages(pool: int, q, means, req_ids, pages, n_first: int = 1, n_las
     of hs_select_workspace_bytes."""
     B, T, H = q.shape[:3]
     N = pages.shape[-1]
-    cfg = hs_pool_config()
-    _check("hs_pool_get_config", load().hs_pool_get_config(pool, C.byref(cfg)))
     ws, wp = _ws(workspace)
     _check("hs_select_pages", load().hs_select_pages(
         pool, B, T, H, N, n_first, n_last, _arg("q", q, "bfloat16", B, T, H, 576),
-        _arg("means", means, "bfloat16", cfg.max_requests, (cfg.max_ctx + 63) // 64, 576),
+        _arg("means", means, "bfloat16", *_means_shape(pool)),
         _arg("req_ids", req_ids, "int32", B), _arg("tree", tree, "int64", B, T, optional=True),
         _arg("pages", pages, "int32", B, T, N),
         _arg("topk_idx", topk_idx, "int32", B, T, N * 64, optional=True), wp, ws, _stream(stream)))

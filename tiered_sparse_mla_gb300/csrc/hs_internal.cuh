@@ -47,6 +47,8 @@ struct hs_pool {
     int32_t *d_lru = nullptr, *d_p2s = nullptr, *d_clock = nullptr, *d_ctx = nullptr;
     uint32_t *d_err = nullptr;
     int32_t *h_hot_blocks = nullptr;  // host shadow of hot_blocks (lease state)
+    alignas(64) unsigned char page_maps[2][128];  // tensor maps of the rows (attention over pages)
+    bool page_maps_made = false;
 
     hs::DevPool dev() const {
         hs::DevPool p;

@@ -166,6 +166,10 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const void *tmap, in
         "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(cluster_bar)
         : "memory");
 }
+// All threads of both CTAs have come here; orders no memory by itself.
+__device__ __forceinline__ void cluster_sync_relaxed() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 __device__ __forceinline__ uint32_t elect_one() {
     uint32_t p;
     asm volatile("{\n .reg .pred P;\n elect.sync _|P, 0xffffffff;\n selp.u32 %0, 1, 0, P;\n}\n" : "=r"(p));
@@ -264,13 +268,22 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     volatile int32_t *ring_pg = reinterpret_cast<volatile int32_t *>(smem + C::OFF_PG);
     auto bar = [&](int i) { return base + C::OFF_BAR + 8u * (uint32_t)i; };
     // the same barrier in CTA 0, whose warp 1 issues the MMAs
-    auto lead = [&](int i) { return hs::dsmem_map(smem + C::OFF_BAR + 8 * i, 0); };
+    const uint32_t lead0 = hs::dsmem_map(smem + C::OFF_BAR, 0);
+    auto lead = [&](int i) { return lead0 + 8u * (uint32_t)i; };
     auto fail = [&]() {
         misc[1] = 1;
         atomicOr(p.err, HS_DEVERR_TIMEOUT);
     };
 
-    if (threadIdx.x == 0) {
+    // The loads that lead to the first copy, as early and as parallel as they go:
+    // entries and request, then the table (its bounds do not need the context's
+    // length) and the length.
+    const int32_t *entries = p.pages ? p.pages + (size_t)list * p.N : nullptr;
+    const bool loader = warp == 0 || warp == 3;
+    int e0 = -1;  // entry `lane`
+    if (loader && entries && lane < p.N) e0 = entries[lane];
+    const int req = p.req[list / p.tpl];
+    if (threadIdx.x == 32) {
         mbar_init(bar(C::B_QFULL), 1);
         mbar_init(bar(C::B_QDONE), NSW);
         mbar_init(bar(C::B_QREADY), 2 * NSW);  // both CTAs' softmax warps
@@ -305,65 +318,71 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             tma_load_3d(i < NQT ? base + C::OFF_QST + i * CH : base + C::OFF_Q + (i - NQT) * CH, &tm_q, 64 * i,
                         mt * BM + RM * rank, list, bar(C::B_QFULL));
     }
-    const int req = p.req[list / p.tpl];
     const bool req_ok = req >= 0 && req < p.max_req;
     const int L = req_ok ? p.ctx[req] : 0;
-    const int npages = L <= 0 ? 0 : (L - 1) / kPage + 1;
-    const int32_t *entries = p.pages ? p.pages + (size_t)list * p.N : nullptr;
-    if (warp == 2) {
+    const int2 *table = p.table + (size_t)(req_ok ? req : 0) * p.max_pages;
+    int nsteps = 0, first = 0, end = 0, npages = 0;
+    uint32_t bad = 0;
+    // page number and block of the entries from i0 on, one per lane
+    auto fetch = [&](int i0, int &pg, int &blk) {
+        const int i = first + i0 + lane;
+        const bool in = i < end && i < first + 2 * nsteps;
+        const int kept = __shfl_sync(0xffffffffu, e0, i & 31);
+        int x = -1, g = -1;
+        if (in) x = entries ? (i < 32 ? kept : entries[i]) : i;
+        if (x >= 0 && x < p.max_pages) g = table[x].x;
+        pg = -1;
+        blk = p.zero_block;
+        if (x < -1 || x >= npages) {
+            bad |= HS_DEVERR_INDEX_RANGE;
+        } else if (x >= 0) {
+            if (g >= 0) {
+                pg = x;
+                blk = g;
+            } else {
+                bad |= HS_DEVERR_BAD_PAGE;  // not resident: the entry is skipped
+            }
+        }
+    };
+    int npg = -1, nblk = p.zero_block;
+    if (loader) {
         // the list's end: past its last entry that names a page
-        int end = npages;
         if (entries) {
-            end = 0;
-            for (int i = lane; i < p.N; i += 32)
+            end = e0 != -1 ? lane + 1 : 0;
+            for (int i = lane + 32; i < p.N; i += 32)
                 if (entries[i] != -1) end = i + 1;
             end = __reduce_max_sync(0xffffffffu, end);
+        } else {
+            end = L <= 0 ? 0 : (L - 1) / kPage + 1;
         }
-        if (lane == 0) {
-            // splits begin at even entries: a step is two pages
-            const long long steps = (end + 1) / 2;
-            const int a = (int)(steps * split / p.nsplit), z = (int)(steps * (split + 1) / p.nsplit);
-            misc[2] = z - a;
-            misc[3] = 2 * a;
-            misc[4] = end;
-        }
+        // splits begin at even entries: a step is two pages
+        const long long steps = (end + 1) / 2;
+        const int z = (int)(steps * (split + 1) / p.nsplit);
+        first = (int)(steps * split / p.nsplit);
+        nsteps = z - first;
+        first *= 2;
+        npages = L <= 0 ? 0 : (L - 1) / kPage + 1;
+        fetch(0, npg, nblk);
+        if (warp == 0 && lane == 0) misc[2] = nsteps;
     }
-    if (warp == 1) tmem_alloc2(base + C::OFF_MISC, 512);
+    if (warp == 2) tmem_alloc2(base + C::OFF_MISC, 512);
     tc_fence_before();
     __syncthreads();
-    cluster_sync_all();  // both CTAs' barriers and tensor memory are there
+    // Both CTAs' barriers and tensor memory are there. What the peer needs of this
+    // CTA are its barriers, released by the fence above: a releasing arrive would
+    // wait for everything in flight (measured 3k clocks).
+    cluster_sync_relaxed();
     tc_fence_after();
     grid_dep_launch();
     const uint32_t tmem = static_cast<uint32_t>(misc[0]);
-    const int nsteps = misc[2], first = misc[3], end = misc[4];
+    nsteps = misc[2];
 
-    if (warp == 0 || warp == 3) {
+    if (loader) {
         // ------------------------------------------------------------ producers
         // warp 0: page numbers, scales, K; warp 3: V. Each looks up the pages'
-        // blocks itself, 32 entries at a time, one per lane, ahead of their use.
+        // blocks itself, 32 entries at a time, ahead of their use.
         const bool kw = warp == 0;
-        uint32_t bad = 0;
-        auto fetch = [&](int i0, int &pg, int &blk) {
-            const int i = first + i0 + lane;
-            pg = -1;
-            blk = p.zero_block;
-            if (i < end && i < first + 2 * nsteps) {
-                const int x = entries ? entries[i] : i;
-                if (x < -1 || x >= npages) {
-                    bad |= HS_DEVERR_INDEX_RANGE;
-                } else if (x >= 0) {
-                    const int g = p.table[(size_t)req * p.max_pages + x].x;
-                    if (g >= 0) {
-                        pg = x;
-                        blk = g;
-                    } else {
-                        bad |= HS_DEVERR_BAD_PAGE;  // not resident: the entry is skipped
-                    }
-                }
-            }
-        };
-        int pg, blk, npg, nblk;
-        fetch(0, npg, nblk);
+        int pg, blk;
         int ul = 0, ut = 0;  // loads and steps begun
         bool ok = true;
         for (int j = 0; j < nsteps && ok; ++j) {
@@ -1000,9 +1019,9 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 
     tc_fence_before();
     __syncthreads();
-    cluster_sync_all();  // no CTA leaves while the other's MMAs or arrivals may reach it
+    cluster_sync_relaxed();  // no CTA leaves while the other's MMAs or arrivals may reach it
     tc_fence_after();
-    if (warp == 1) tmem_dealloc2(tmem, 512);
+    if (warp == 2) tmem_dealloc2(tmem, 512);
 }
 
 // Joins the splits: out = sum_s w_s O_s / sum_s w_s, w_s = exp(lse_s - max), in
@@ -1140,12 +1159,20 @@ hs_status page_entry(hs_pool_t pool, int64_t lists, int32_t T, int32_t tpl, int3
     if (pl.nsplit > 1 && (!d_workspace || ws_bytes < pl.ws_bytes || ((uintptr_t)d_workspace & 255u)))
         return HS_ERR_INVALID_ARG;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    CUtensorMap tq, k1, k2, to;
+    CUtensorMap tq, to;
     const uint64_t rows = (uint64_t)(pool->cfg.n_gpu_blocks + 1) * kPage;
     if (!make_map(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d_q, kDim, pl.M, lists, 2 * kDim, 64, RM,
-                  CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_page_map(&k1, fp8, pool->d_rows, rows, fp8 ? PCfg<true>::GK : 1) || !make_page_map(&k2, fp8, pool->d_rows, rows, 2))
+                  CU_TENSOR_MAP_SWIZZLE_128B))
         return HS_ERR_CUDA;
+    // the pool's own maps, once
+    static_assert(sizeof(pool->page_maps[0]) == sizeof(CUtensorMap), "size of a tensor map");
+    CUtensorMap *maps = reinterpret_cast<CUtensorMap *>(pool->page_maps);
+    if (!pool->page_maps_made) {
+        if (!make_page_map(&maps[0], fp8, pool->d_rows, rows, fp8 ? PCfg<true>::GK : 1) ||
+            !make_page_map(&maps[1], fp8, pool->d_rows, rows, 2))
+            return HS_ERR_CUDA;
+        pool->page_maps_made = true;
+    }
     // the output (one split), or the splits' f32 partials
     const bool one = pl.nsplit == 1;
     if (!make_map(&to, one ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
@@ -1175,8 +1202,8 @@ hs_status page_entry(hs_pool_t pool, int64_t lists, int32_t T, int32_t tpl, int3
     p.tpl = tpl;
     p.scale_log2 = sm_scale * 1.4426950408889634f;
     const dim3 grid(2 * pl.nsplit, pl.mtiles, (unsigned)lists);
-    const hs_status st = fp8 ? launch_pages<true>(grid, dev, s, tq, k1, k2, to, p)
-                             : launch_pages<false>(grid, dev, s, tq, k1, k2, to, p);
+    const hs_status st = fp8 ? launch_pages<true>(grid, dev, s, tq, maps[0], maps[1], to, p)
+                             : launch_pages<false>(grid, dev, s, tq, maps[0], maps[1], to, p);
     if (st != HS_OK || pl.nsplit == 1) return st;
     const int n = (int)(lists * pl.M);
     cudaLaunchConfig_t cc = {};
