@@ -123,58 +123,6 @@ struct PageParams {
     float scale_log2;
 };
 
-// ---------------------------------------------------------------- two CTAs' tensor cores as one
-__device__ __forceinline__ void tmem_alloc2(uint32_t dst_smem, uint32_t ncols) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t ncols) {
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
-}
-// Arrives on the barrier at this offset in both CTAs once every MMA issued so far is done.
-__device__ __forceinline__ void commit_both(uint32_t bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-            bar),
-        "h"((uint16_t)3)
-        : "memory");
-}
-// One MMA; descriptors as two 32-bit halves (the high one is shared), A from
-// shared memory or from tensor memory.
-__device__ __forceinline__ void mma2_ss(uint32_t d, uint32_t alo, uint32_t blo, uint32_t hi, uint32_t idesc,
-                                        uint32_t acc) {
-    asm volatile(
-        "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %5, 0;\n mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n"
-        " tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %4, p;\n}\n" ::"r"(d),
-        "r"(alo), "r"(blo), "r"(hi), "r"(idesc), "r"(acc)
-        : "memory");
-}
-__device__ __forceinline__ void mma2_ts(uint32_t d, uint32_t a, uint32_t blo, uint32_t hi, uint32_t idesc,
-                                        uint32_t acc) {
-    asm volatile(
-        "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n mov.b64 b, {%2, %3};\n"
-        " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d),
-        "r"(a), "r"(blo), "r"(hi), "r"(idesc), "r"(acc)
-        : "memory");
-}
-// A box into this CTA's shared memory whose bytes complete on a barrier of either CTA.
-__device__ __forceinline__ void tma_load_pair(uint32_t dst, const void *tmap, int c0, int c1, int c2, uint32_t cluster_bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2"
-        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(cluster_bar)
-        : "memory");
-}
-// All threads of both CTAs have come here; orders no memory by itself.
-__device__ __forceinline__ void cluster_sync_relaxed() {
-    asm volatile("barrier.cluster.arrive.relaxed.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t elect_one() {
-    uint32_t p;
-    asm volatile("{\n .reg .pred P;\n elect.sync _|P, 0xffffffff;\n selp.u32 %0, 1, 0, P;\n}\n" : "=r"(p));
-    return p;
-}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -218,11 +166,6 @@ __device__ __forceinline__ void add2(float &a, float &b, float c, float d) {
     asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
         : "+f"(a), "+f"(b)
         : "f"(c), "f"(d));
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
 }
 // Whether any of the softmax threads says so (named barrier 1).
 __device__ __forceinline__ bool any_softmax(bool x) {

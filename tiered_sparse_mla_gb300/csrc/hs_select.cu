@@ -30,73 +30,98 @@ __host__ __device__ __forceinline__ int pages_of(int tokens) {
 }
 
 // ---------------------------------------------------------------- scores
-// One CTA per (128 pages, request). The pages are the MMA's M rows, the query
-// rows (token x head) its N columns, so that the maximum over heads runs along
-// the registers of the one thread that owns a page. Chunks of 64 depth columns
-// stream through a ring (pages 16 KB, query rows up to 32 KB a stage); two CTAs
-// share an SM, so one's loads cover the other's epilogue.
-constexpr int SP = 128;          // pages per tile
+// Work unit: (request, group of whole query tokens of at most 256 rows, range of
+// page tiles), run by two CTAs whose tensor cores work as one (cta_group::2,
+// M = 256, N up to 256): pages are the MMA's M rows, 128 per CTA, so that the
+// maximum over heads runs along the registers of the one thread that owns a page,
+// and query rows its N columns, half of them supplied by either CTA. The queries
+// stay in shared memory (144 KB a CTA) and the pages stream past once through a
+// ring of 16 KB chunks; the scores of one tile are reduced while the next is
+// multiplied (two accumulators). One MMA of 256 x 256 x 16 takes 128 clocks, so
+// 256 rows per pass need 4.6k clocks per tile of 256 pages and fewer rows are bound
+// by the pages' bytes. An earlier form, one CTA per 128 pages with the queries
+// streamed past each tile, moved 6x the pages' bytes from L2 and took 3x as long.
+//   warp 0      producer;  warp 1 (CTA 0) MMA issuer;
+//   warps 2-5   the pages' |c|^2, from the chunks as they land; their arrival is
+//               what the MMA issuer waits for;
+//   warps 6-9   maxima over heads, one thread per page.
+constexpr int SP = 256;          // pages per tile (two CTAs)
 constexpr int NCH = kDim / 64;   // depth chunks
-constexpr int ST = 192;          // threads: producer, MMA, four epilogue warps
-constexpr int MAXN = 256;        // query rows per group
-constexpr int MAXST = 5;         // ring stages
-constexpr int A_BYTES = SP * 128;
-constexpr int RING_BYTES = 98304;
-constexpr int SCORE_SMEM = RING_BYTES + 1024 + 256;
+constexpr int ST = 320;
+constexpr int MAXN = 256;        // query rows per pass
+constexpr int NST = 4;           // ring stages
+constexpr int A_BYTES = 128 * 128;
+constexpr int OFF_RING = NCH * 128 * 128;
+constexpr int OFF_SBAR = OFF_RING + NST * A_BYTES;
+constexpr int SCORE_SMEM = OFF_SBAR + 256 + 1024;
+static_assert(SCORE_SMEM <= 232448, "shared memory");
 
 struct ScoreParams {
     const int32_t *req, *ctx;
     float *s1;       // [B*T][Pp] best head's score
-    uint32_t *s2;    // [B*T][Pp] second best (BF16, rounded up) << 16 | best head
-    float *cn;       // [B][Pp]   |c_p|^2
+    float *cn, *cm;  // [B][Pp] |c_p|^2; [B][Pp / 32] the largest of 32 pages (infinite if one is not finite)
     uint32_t *err;
-    int T, H, M, N, groups, nst, Pp, max_req;
+    int T, H, tpg, groups, splits;  // tokens per group; groups of tokens; splits of the tiles
+    int hpc, N;                     // heads per pass (H, or 256 at most); N: query rows of a pass, rounded up
+    int Pp, max_req;
 };
 
-__global__ void __launch_bounds__(ST, 2)
+__global__ void __launch_bounds__(ST, 1)
 score_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_q,
              const ScoreParams p) {
     extern __shared__ uint8_t smem_raw[];
     grid_dep_launch();
-    const int b = blockIdx.y, tile = blockIdx.x;
+    const int rank = static_cast<int>(hs::cluster_ctarank());
+    const int unit = blockIdx.x >> 1, split = unit % p.splits, g = (unit / p.splits) % p.groups;
+    const int b = unit / (p.splits * p.groups);
     const int r = p.req[b];
-    if (r < 0 || r >= p.max_req) return;
-    const int pages = pages_of(p.ctx[r]);
-    if (tile * SP >= pages) return;
+    if (r < 0 || r >= p.max_req) return;  // both CTAs alike
+    const int pages = pages_of(p.ctx[r]), tiles = (pages + SP - 1) / SP;
+    const int t_lo = (int)((long long)tiles * split / p.splits);
+    const int nt = (int)((long long)tiles * (split + 1) / p.splits) - t_lo;
+    if (nt == 0) return;
     const uint32_t raw = hs::smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *smem = smem_raw + (base - raw);
-    volatile int32_t *misc = reinterpret_cast<volatile int32_t *>(smem + RING_BYTES);
-    auto bar = [&](int i) { return base + RING_BYTES + 16u + 8u * (uint32_t)i; };
-    constexpr int B_FULL = 0, B_EMPTY = MAXST, B_NREAD = 2 * MAXST, B_DFULL = 3 * MAXST,
-                  B_DEMPTY = B_DFULL + 1, B_DRAIN = B_DEMPTY + 1, NB = B_DRAIN + 1;
+    volatile int32_t *misc = reinterpret_cast<volatile int32_t *>(smem + OFF_SBAR);
+    constexpr int B_QFULL = 0, B_QFREE = 1, B_FULL = 2, B_READY = B_FULL + NST, B_FREE = B_READY + NST,
+                  B_DFULL = B_FREE + NST, B_DFREE = B_DFULL + 2, B_DRAIN = B_DFREE + 2, NB = B_DRAIN + 1;
     static_assert(16 + 8 * NB <= 256, "barriers");
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t stage = A_BYTES + p.N * 128;
-    const int uses = p.groups * NCH;
+    auto bar = [&](int i) { return base + OFF_SBAR + 16u + 8u * (uint32_t)i; };
+    const uint32_t lead0 = hs::dsmem_map(smem + OFF_SBAR + 16, 0);
+    auto lead = [&](int i) { return lead0 + 8u * (uint32_t)i; };
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int passes = (p.H + p.hpc - 1) / p.hpc;  // one, unless a token has more than 256 heads
+    const int total = passes * nt;
     auto fail = [&]() {
         misc[1] = 1;
         atomicOr(p.err, HS_DEVERR_TIMEOUT);
     };
     uint32_t cols = 32;
-    while ((int)cols < p.N) cols <<= 1;
+    while ((int)cols < 2 * p.N) cols <<= 1;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < p.nst; ++i) {
+        mbar_init(bar(B_QFULL), 1);
+        mbar_init(bar(B_QFREE), 1);
+        for (int i = 0; i < NST; ++i) {
             mbar_init(bar(B_FULL + i), 1);
-            mbar_init(bar(B_EMPTY + i), 1);
-            mbar_init(bar(B_NREAD + i), 4);
+            mbar_init(bar(B_READY + i), 8);
+            mbar_init(bar(B_FREE + i), 1);
         }
-        mbar_init(bar(B_DFULL), 1);
-        mbar_init(bar(B_DEMPTY), 4);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(B_DFULL + i), 1);
+            mbar_init(bar(B_DFREE + i), 8);
+        }
         mbar_init(bar(B_DRAIN), 1);
         misc[1] = 0;
         fence_mbar_init();
+        fence_proxy_async();
         prefetch_tmap(&tm_c);
         prefetch_tmap(&tm_q);
     }
-    if (warp == 1) tmem_alloc(base + RING_BYTES, cols);
+    if (warp == 1) tmem_alloc2(base + OFF_SBAR, cols);
     tc_fence_before();
     __syncthreads();
+    cluster_sync_relaxed();
     tc_fence_after();
     const uint32_t tmem = static_cast<uint32_t>(misc[0]);
 
@@ -105,119 +130,175 @@ score_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ C
         if (lane == 0) {
             int issued = 0;
             bool ok = true;
-            for (int u = 0; u < uses && ok; ++u) {
-                const int s = u % p.nst;
-                const uint32_t ph = (uint32_t)(u / p.nst) & 1u;
-                ok = mbar_wait(bar(B_EMPTY + s), ph ^ 1u) && !misc[1];
-                // a stage of the first group is also read by the norms
-                if (ok && u >= p.nst && u - p.nst < NCH) ok = mbar_wait(bar(B_NREAD + s), ph ^ 1u);
+            for (int k = 0; k < passes && ok; ++k) {
+                // the queries of a pass: this CTA's half of the rows, all chunks
+                if (k > 0) ok = mbar_wait_inline(bar(B_QFREE), (uint32_t)(k - 1) & 1u);
                 if (!ok) break;
-                const int g = u / NCH, c = u % NCH;
-                mbar_expect_tx(bar(B_FULL + s), stage);
-                tma_load_3d(base + s * stage, &tm_c, 64 * c, tile * SP, r, bar(B_FULL + s));
-                tma_load_3d(base + s * stage + A_BYTES, &tm_q, 64 * c, g * p.N, b, bar(B_FULL + s));
-                ++issued;
+                if (rank == 0) mbar_expect_tx(bar(B_QFULL), NCH * p.N * 128);
+                const int row = g * p.tpg * p.H + k * p.hpc + rank * (p.N / 2);
+                for (int c = 0; c < NCH; ++c)
+                    tma_load_pair(base + c * (p.N / 2) * 128, &tm_q, 64 * c, row, b, lead(B_QFULL));
+                for (int i = 0; i < nt && ok; ++i)
+                    for (int c = 0; c < NCH && ok; ++c, ++issued) {
+                        const int s = issued % NST;
+                        ok = mbar_wait_inline(bar(B_FREE + s), ((uint32_t)(issued / NST) & 1u) ^ 1u);
+                        if (!ok) break;
+                        mbar_expect_tx(bar(B_FULL + s), A_BYTES);
+                        tma_load_3d(base + OFF_RING + s * A_BYTES, &tm_c, 64 * c, (t_lo + i) * SP + 128 * rank, r,
+                                    bar(B_FULL + s));
+                    }
             }
             if (!ok) {
                 fail();
-                for (int u = issued - 1; u >= 0 && u >= issued - p.nst; --u)
-                    mbar_wait(bar(B_FULL + u % p.nst), (uint32_t)(u / p.nst) & 1u);
+                for (int u = issued - 1; u >= 0 && u >= issued - NST; --u)
+                    mbar_wait_inline(bar(B_FULL + u % NST), (uint32_t)(u / NST) & 1u);
             }
         }
     } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
+        // ------------------------------------------------------------ MMA issuer (CTA 0)
+        if (rank == 0) {
             const uint32_t idesc = idesc_f16(1u, 0, SP, p.N);
+            const uint64_t d0 = desc_sw128(base, 16, 1024);
+            const uint32_t hi = (uint32_t)(d0 >> 32), lo = (uint32_t)d0;
+            const uint32_t leader = elect_one();
+            const uint32_t qch = (uint32_t)(p.N / 2) * 128u;
             bool ok = true;
-            for (int u = 0; u < uses && ok; ++u) {
-                const int s = u % p.nst, g = u / NCH, c = u % NCH;
-                if (c == 0 && g > 0) ok = mbar_wait(bar(B_DEMPTY), (uint32_t)(g - 1) & 1u);
-                ok = ok && mbar_wait(bar(B_FULL + s), (uint32_t)(u / p.nst) & 1u) && !misc[1];
+            int u = 0;
+            for (int i = 0; i < total && ok; ++i) {
+                if (i % nt == 0) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(B_QFULL), (uint32_t)(i / nt) & 1u));
+                if (ok && i >= 2)
+                    ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(B_DFREE + (i & 1)), ((uint32_t)(i >> 1) & 1u) ^ 1u));
                 if (!ok) break;
-                tc_fence_after();
-                const uint64_t a = desc_sw128(base + s * stage, 16, 1024);
-                const uint64_t q = desc_sw128(base + s * stage + A_BYTES, 16, 1024);
+                const uint32_t d = tmem + (uint32_t)((i & 1) * p.N);
+                for (int c = 0; c < NCH && ok; ++c, ++u) {
+                    const int s = u % NST;
+                    ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(B_READY + s), (uint32_t)(u / NST) & 1u));
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (leader) {
+                        const uint32_t a = lo + ((OFF_RING + s * A_BYTES) >> 4), q = lo + ((c * qch) >> 4);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_f16(tmem, a + 2 * k, q + 2 * k, idesc, (c | k) != 0);
-                mma_commit(bar(B_EMPTY + s));
-                if (c == NCH - 1) mma_commit(bar(B_DFULL));
-            }
-            if (!ok) fail();
-            mma_commit(bar(B_DRAIN));
-            mbar_wait(bar(B_DRAIN), 0);
-        }
-    } else {
-        // ------------------------------------------------------------ norms, epilogue
-        const int wq = warp & 3, row = wq * 32 + lane;
-        const int page = tile * SP + row;
-        bool ok = true;
-        // |c_p|^2 of this thread's page, from the chunks as they pass
-        float cn = 0.f;
-        for (int u = 0; u < NCH; ++u) {
-            const int s = u % p.nst;
-            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(B_FULL + s), (uint32_t)(u / p.nst) & 1u) &&
-                                                     !misc[1]);
-            if (ok) {
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const uint4 v = ld_shared_v4(base + s * stage + row * 128 + ((c ^ (row & 7)) << 4));
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float lo = __uint_as_float(w[e] << 16), hi = __uint_as_float(w[e] & 0xffff0000u);
-                        cn = fmaf(lo, lo, cn);
-                        cn = fmaf(hi, hi, cn);
+                        for (int k = 0; k < 4; ++k) mma2_ss(d, a + 2 * k, q + 2 * k, hi, idesc, (c | k) != 0);
+                        commit_both(bar(B_FREE + s));
                     }
+                    __syncwarp();
                 }
+                if (!ok) break;
+                if (leader) {
+                    commit_both(bar(B_DFULL + (i & 1)));
+                    if (i % nt == nt - 1) commit_both(bar(B_QFREE));
+                }
+                __syncwarp();
+            }
+            if (!ok && lane == 0) fail();
+            if (leader) {
+                asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                                 bar(B_DRAIN))
+                             : "memory");
+                mbar_wait_inline(bar(B_DRAIN), 0);
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_NREAD + s));
         }
-        if (ok && page < pages) p.cn[(size_t)b * p.Pp + page] = cn;
-        int t = 0, h = 0, arg = 0;
-        float m1 = -INFINITY, m2 = -INFINITY;
+    } else if (warp < 6) {
+        // ------------------------------------------------------------ norms
+        const int row = (warp - 2) * 32 + lane;
+        const bool first_group = g == 0;
+        bool ok = true;
+        int u = 0;
+        for (int i = 0; i < total; ++i) {
+            float n4[4] = {0.f, 0.f, 0.f, 0.f};
+            const bool need = first_group && i < nt;
+            for (int c = 0; c < NCH; ++c, ++u) {
+                const int s = u % NST;
+                if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(B_FULL + s), (uint32_t)(u / NST) & 1u));
+                if (ok && need) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint4 v = ld_shared_v4(base + OFF_RING + s * A_BYTES + row * 128 + ((k ^ (row & 7)) << 4));
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float x = __uint_as_float(w[e] << 16), y = __uint_as_float(w[e] & 0xffff0000u);
+                            n4[e] = fmaf(y, y, fmaf(x, x, n4[e]));
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive_peer(lead(B_READY + s));
+            }
+            const int page = (t_lo + i % nt) * SP + 128 * rank + row;
+            if (ok && need) {
+                const bool in = page < pages;
+                const float cn = (n4[0] + n4[1]) + (n4[2] + n4[3]);
+                float m = in ? (cn <= FLT_MAX ? cn : INFINITY) : 0.f;
+                m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+                if (in) p.cn[(size_t)b * p.Pp + page] = cn;
+                if (in && lane == 0) p.cm[((size_t)b * p.Pp + page) / 32] = m;
+            }
+        }
+        if (!ok && lane == 0) fail();
+    } else {
+        // ------------------------------------------------------------ maxima over heads
+        const int wq = warp & 3, row = wq * 32 + lane;
         const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
-        for (int g = 0; g < p.groups; ++g) {
-            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(B_DFULL), (uint32_t)g & 1u) && !misc[1]);
+        bool ok = true;
+        for (int i = 0; i < total; ++i) {
+            const int k = i / nt, page = (t_lo + i % nt) * SP + 128 * rank + row;
+            const int h0 = k * p.hpc, hn = min(p.hpc, p.H - h0);  // heads of this pass
+            const int t0 = g * p.tpg, tn = min(p.tpg, p.T - t0);
+            const int rows = tn * hn;
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(B_DFULL + (i & 1)), (uint32_t)(i >> 1) & 1u));
             if (ok) {
                 tc_fence_after();
-                const int left = min(p.N, p.M - g * p.N);
-                for (int c0 = 0; c0 < left; c0 += 16) {
-                    uint32_t d[16];
-                    HS_TMEM_LD16(tmem + lane_off + c0, d);
-                    HS_TMEM_WAIT_LD16(d);
+                int t = t0, h = 0;
+                float m = -INFINITY;
+                const uint32_t d0 = tmem + lane_off + (uint32_t)((i & 1) * p.N);
+                auto flush = [&]() {
+                    if (page < pages) {
+                        float *at = p.s1 + ((size_t)b * p.T + t) * p.Pp + page;
+                        *at = k > 0 ? fmaxf(*at, m) : m;  // this thread stored the earlier heads' itself
+                    }
+                    m = -INFINITY;
+                    h = 0;
+                    ++t;
+                };
+                for (int c0 = 0; c0 < rows; c0 += 32) {
+                    uint32_t d[32];
+                    HS_TMEM_LD32(d0 + c0, d);
+                    HS_TMEM_WAIT_LD32(d);
+                    auto f = [&](int e) { return __uint_as_float(d[e]); };
+                    if ((hn & 7) == 0) {
+                        // a token's heads end at multiples of eight columns
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        if (c0 + e >= left) break;
-                        const float v = __uint_as_float(d[e]);
-                        m2 = fmaxf(m2, fminf(m1, v));
-                        arg = v > m1 ? h : arg;
-                        m1 = fmaxf(m1, v);
-                        if (++h == p.H) {
-                            if (page < pages) {
-                                const size_t at = ((size_t)b * p.T + t) * p.Pp + page;
-                                p.s1[at] = m1;
-                                // rounded up: its distance to the best is never overstated
-                                p.s2[at] = ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_ru(m2)) << 16) | (uint32_t)arg;
+                        for (int e = 0; e < 32; e += 8) {
+                            if (c0 + e < rows) {
+                                m = max3(m, max3(f(e), f(e + 1), f(e + 2)),
+                                         max3(f(e + 3), max3(f(e + 4), f(e + 5), f(e + 6)), f(e + 7)));
+                                if ((h += 8) == hn) flush();
                             }
-                            m1 = m2 = -INFINITY;
-                            h = arg = 0;
-                            ++t;
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            if (c0 + e < rows) {
+                                m = fmaxf(m, f(e));
+                                if (++h == hn) flush();
+                            }
                         }
                     }
                 }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_DEMPTY));
+            if (lane == 0) mbar_arrive_peer(lead(B_DFREE + (i & 1)));
         }
-        if (!ok) fail();
+        if (!ok && lane == 0) fail();
     }
     tc_fence_before();
     __syncthreads();
+    cluster_sync_relaxed();  // no CTA leaves while the other's MMAs or arrivals may reach it
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem, cols);
+    if (warp == 1) tmem_dealloc2(tmem, cols);
 }
 
 // ---------------------------------------------------------------- selection
@@ -231,14 +312,14 @@ constexpr int NW = LT / 32;
 constexpr int BINS = 2048;
 constexpr int CAP = 512;       // pages near the border that fit in shared memory
 constexpr int MAXSEL = 1024;   // pages per list
+constexpr int KEEP = 16;       // scores that a thread keeps in registers (16,384 pages)
 
 struct SelectParams {
     const int32_t *req, *ctx;
     const uint64_t *tree;            // [B][T] or null
     const __nv_bfloat16 *q, *means;  // [B][T][H][576], [max_req][max_pages][576]
     float *s1;
-    uint32_t *s2;
-    const float *cn;
+    const float *cn, *cm;
     uint64_t *key64;                 // [B*T][Pp] only written when more than CAP pages are near the border
     int32_t *pages, *topk;           // [B][T][N], [B][T][N*64] or null
     uint32_t *err;
@@ -275,6 +356,24 @@ __device__ __forceinline__ double dot64(const __nv_bfloat16 *q, const __nv_bfloa
     return acc;
 }
 
+// The same in 32 bits: off by less than 2^-19 |q||c| (18 products per lane and
+// five additions), well inside E.
+__device__ __forceinline__ float dot32(const __nv_bfloat16 *q, const __nv_bfloat16 *c) {
+    const int lane = threadIdx.x & 31;
+    float x = 0.f, y = 0.f;
+#pragma unroll
+    for (int i = 0; i < kDim / 64; ++i) {
+        const uint32_t a = reinterpret_cast<const uint32_t *>(q)[lane + 32 * i];
+        const uint32_t b = reinterpret_cast<const uint32_t *>(c)[lane + 32 * i];
+        x = fmaf(__uint_as_float(a << 16), __uint_as_float(b << 16), x);
+        y = fmaf(__uint_as_float(a & 0xffff0000u), __uint_as_float(b & 0xffff0000u), y);
+    }
+    x += y;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
 __global__ void __launch_bounds__(LT) select_kernel(const SelectParams p) {
     __shared__ int hist[BINS];
     __shared__ uint32_t lkey[CAP];
@@ -285,7 +384,7 @@ __global__ void __launch_bounds__(LT) select_kernel(const SelectParams p) {
     __shared__ float warp_f[NW];
     __shared__ uint32_t s_lo, s_hi, s_theta;
     __shared__ int s_need, s_bin, s_m, s_nsel, s_unknown;
-    __shared__ float s_qn, s_cn;
+    __shared__ float s_qn, s_cn, s_up, s_dn, s_e2;
     const int list = blockIdx.x, b = list / p.T, t = list % p.T;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int r = p.req[b];
@@ -343,76 +442,103 @@ __global__ void __launch_bounds__(LT) select_kernel(const SelectParams p) {
     }
     if (!all && k > 0) {
         float *s1 = p.s1 + (size_t)list * p.Pp;
-        uint32_t *s2 = p.s2 + (size_t)list * p.Pp;
-        const float *cn = p.cn + (size_t)b * p.Pp;
+        const float *cn = p.cn + (size_t)b * p.Pp, *cm = p.cm + (size_t)b * p.Pp / 32;
         const __nv_bfloat16 *means = p.means + (size_t)r * p.max_pages * kDim;
+        // one reading of the scores, all loads at once
+        float v[KEEP];
+        auto load = [&]() {
+#pragma unroll
+            for (int u = 0; u < KEEP; ++u) {
+                const int i = c0 + tid + u * LT;
+                v[u] = i < c1 ? s1[i] : 0.f;
+            }
+        };
+        auto each = [&](auto f) {
+#pragma unroll
+            for (int u = 0; u < KEEP; ++u) {
+                const int i = c0 + tid + u * LT;
+                if (i < c1) f(i, v[u]);
+            }
+            for (int i = c0 + tid + KEEP * LT; i < c1; i += LT) f(i, s1[i]);
+        };
+        load();
         // a page whose score or norm is not finite says nothing in 32 bits
         auto unknown = [&](float s, float c) { return !(fabsf(s) <= FLT_MAX) || !(c <= FLT_MAX); };
         uint32_t lo = 0xffffffffu, hi = 0u;
-        float cm = 0.f;
+        float cmx = 0.f;
         int unk = 0;
-        for (int i = c0 + tid; i < c1; i += LT) {
-            const float s = s1[i], c = cn[i];
-            if (unknown(s, c)) {
-                unk = 1;
-            } else {
-                const uint32_t key = order32(s);
-                lo = min(lo, key);
-                hi = max(hi, key);
-                cm = fmaxf(cm, c);
-            }
-        }
+        for (int i = tid; i < (n + 31) / 32; i += LT) cmx = fmaxf(cmx, cm[i]);
+        each([&](int, float s) {
+            unk |= !(fabsf(s) <= FLT_MAX);
+            const uint32_t key = order32(s);
+            lo = min(lo, key);
+            hi = max(hi, key);
+        });
+        unk |= cmx > FLT_MAX;
         lo = __reduce_min_sync(0xffffffffu, lo);
         hi = __reduce_max_sync(0xffffffffu, hi);
-        cm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(cm)));  // not negative
+        cmx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(cmx)));  // not negative
         unk = __any_sync(0xffffffffu, unk);
         if (lane == 0) {
             atomicMin(&s_lo, lo);
             atomicMax(&s_hi, hi);
-            atomicMax(reinterpret_cast<int *>(&s_cn), __float_as_int(cm));
+            atomicMax(reinterpret_cast<int *>(&s_cn), __float_as_int(cmx));
             if (unk) s_unknown = 1;
         }
         __syncthreads();
         if (s_unknown) {
             // those pages' scores in 64 bits; what stands for them in 32 is the
-            // rounded sum, with a second best that names no head
+            // rounded sum
+            __syncthreads();
+            if (tid == 0) {
+                s_lo = 0xffffffffu;
+                s_hi = 0u;
+                s_cn = 0.f;
+            }
+            __syncthreads();
             for (int i0 = c0 + warp * 32; i0 < c1; i0 += LT) {
                 const int i = i0 + lane;
-                unsigned todo = __ballot_sync(0xffffffffu, i < c1 && unknown(s1[i < c1 ? i : c0], cn[i < c1 ? i : c0]));
+                float s = i < c1 ? s1[i] : 0.f;
+                const float c = i < c1 ? cn[i] : 0.f;
+                const bool mine = i < c1 && unknown(s, c);
+                unsigned todo = __ballot_sync(0xffffffffu, mine);
                 while (todo) {
-                    const int pg = i0 + __ffs(todo) - 1;
+                    const int who = __ffs(todo) - 1, pg = i0 + who;
                     todo &= todo - 1;
                     double best = -(double)INFINITY;
                     for (int h = 0; h < p.H; ++h) {
                         const double d = dot64(q + (size_t)h * kDim, means + (size_t)pg * kDim);
                         best = d > best ? d : best;
                     }
-                    const float s = __double2float_rn(best);
-                    if (lane == 0) {
+                    if (lane == who) {
+                        s = __double2float_rn(best);
                         s1[pg] = s;
-                        s2[pg] = 0x7f800000u;
-                        const uint32_t key = order32(s);
-                        atomicMin(&s_lo, key);
-                        atomicMax(&s_hi, key);
                     }
+                }
+                if (i < c1) {
+                    const uint32_t key = order32(s);
+                    atomicMin(&s_lo, key);
+                    atomicMax(&s_hi, key);
+                    if (!mine) atomicMax(reinterpret_cast<int *>(&s_cn), __float_as_int(c));
                 }
             }
             __syncthreads();
+            load();
         }
         // ------------------------------------------------ the border's bin
         int need = k;
         lo = s_lo;
         hi = s_hi;
-        int m = 0;
-        for (;;) {
+        int m = c1 - c0;
+        while (m > CAP && lo != hi) {
             const int bits = 32 - __clz((int)(hi - lo));
             const int sh = bits > 11 ? bits - 11 : 0;
             for (int i = tid; i < BINS; i += LT) hist[i] = 0;
             __syncthreads();
-            for (int i = c0 + tid; i < c1; i += LT) {
-                const uint32_t key = order32(s1[i]);
+            each([&](int, float s) {
+                const uint32_t key = order32(s);
                 if (key >= lo && key <= hi) atomicAdd(&hist[(key - lo) >> sh], 1);
-            }
+            });
             __syncthreads();
             // from the top: thread i holds bins BINS-1-2i and the one below
             const int b0 = BINS - 1 - 2 * tid;
@@ -443,7 +569,6 @@ __global__ void __launch_bounds__(LT) select_kernel(const SelectParams p) {
             lo = lo + ((uint32_t)s_bin << sh);
             hi = min(hi, lo + ((sh ? (1u << sh) : 1u) - 1u));
             __syncthreads();
-            if (sh == 0 || m <= CAP) break;
         }
         // the k-th largest score: the need-th of the bin
         if (lo == hi) {
@@ -451,60 +576,71 @@ __global__ void __launch_bounds__(LT) select_kernel(const SelectParams p) {
         } else {
             if (tid == 0) s_m = 0;
             __syncthreads();
-            for (int i = c0 + tid; i < c1; i += LT) {
-                const uint32_t key = order32(s1[i]);
+            each([&](int, float s) {
+                const uint32_t key = order32(s);
                 if (key >= lo && key <= hi) lkey[atomicAdd(&s_m, 1)] = key;
-            }
+            });
             __syncthreads();
             if (tid < m) {
                 int above = 0, equal = 0;
+                const uint32_t mine = lkey[tid];
                 for (int j = 0; j < m; ++j) {
-                    above += lkey[j] > lkey[tid];
-                    equal += lkey[j] == lkey[tid];
+                    above += lkey[j] > mine;
+                    equal += lkey[j] == mine;
                 }
-                if (above < need && above + equal >= need) s_theta = lkey[tid];
+                if (above < need && above + equal >= need) s_theta = mine;
             }
+            __syncthreads();
         }
         if (tid == 0) s_m = 0;
         __syncthreads();
         // ------------------------------------------------ above it, and near it
-        const float theta = from_order32(s_theta);
-        const double e2 = 2.0 * (1.0 / 65536.0) * sqrt((double)s_qn) * sqrt((double)s_cn) * 1.0001;
-        const double slack = e2 + fabs((double)theta) * (1.0 / 4194304.0);
-        const double up = (double)theta + slack, dn = (double)theta - slack;
-        for (int i = c0 + tid; i < c1; i += LT) {
-            const double s = (double)s1[i];
+        // (64-bit arithmetic is 1/64 as fast: one thread's, and the few sums' below)
+        if (tid == 0) {
+            const double theta = (double)from_order32(s_theta);
+            const double e2 = 2.0 * (1.0 / 65536.0) * sqrt((double)s_qn) * sqrt((double)s_cn) * 1.0001;
+            const double slack = e2 + fabs(theta) * (1.0 / 4194304.0);
+            s_up = __double2float_ru(theta + slack);
+            s_dn = __double2float_rd(theta - slack);
+            s_e2 = __double2float_ru(e2);
+        }
+        __syncthreads();
+        const float up = s_up, dn = s_dn, e2 = s_e2;
+        each([&](int i, float s) {
             if (s > up) {
                 sel[atomicAdd(&s_nsel, 1)] = i;
             } else if (!(s < dn)) {
                 const int j = atomicAdd(&s_m, 1);
                 if (j < CAP) lpage[j] = i;
             }
-        }
+        });
         __syncthreads();
         need = k - s_nsel;
         m = s_m;
-        // exact score of a near page: the best head alone where the second best is further off
-        const bool same = e2 == 0.0 && !s_unknown;  // the sums are exact as they are
-        auto ambiguous = [&](int pg) {
-            const float second = __uint_as_float(s2[pg] & 0xffff0000u);
-            return !((double)s1[pg] - (double)second > e2);
-        };
+        const bool same = e2 == 0.f && !s_unknown;  // the sums are exact as they are
         if (m <= CAP) {
             if (m == need) {
                 if (tid < m) sel[s_nsel + tid] = lpage[tid];
             } else {
-                if (tid < m) lk64[tid] = same ? order64((double)s1[lpage[tid]]) : 0ull;
+                if (tid < m) {
+                    lk64[tid] = same ? order64((double)s1[lpage[tid]]) : 0ull;
+                    lkey[tid] = 0u;
+                }
                 __syncthreads();
                 if (!same) {
-                    for (int j = 0; j < m; ++j) {
-                        const int pg = lpage[j];
-                        const bool amb = ambiguous(pg);
-                        const int step = amb ? NW : p.H;
-                        for (int h = amb ? warp : (warp == j % NW ? (int)(s2[pg] & 0xffffu) : p.H); h < p.H; h += step) {
-                            const double d = dot64(q + (size_t)h * kDim, means + (size_t)pg * kDim);
-                            if (lane == 0) atomicMax(&lk64[j], (unsigned long long)order64(d));
-                        }
+                    // every (page, head) in 32 bits, then those near the page's best in 64
+                    const int pairs = m * p.H;
+                    for (int x = warp; x < pairs; x += NW) {
+                        const float d = dot32(q + (size_t)(x % p.H) * kDim, means + (size_t)lpage[x / p.H] * kDim);
+                        if (lane == 0 && d == d) atomicMax(&lkey[x / p.H], order32(d));
+                    }
+                    __syncthreads();
+                    for (int x = warp; x < pairs; x += NW) {
+                        const __nv_bfloat16 *qh = q + (size_t)(x % p.H) * kDim, *c = means + (size_t)lpage[x / p.H] * kDim;
+                        const uint32_t bk = lkey[x / p.H];
+                        if (bk && dot32(qh, c) < from_order32(bk) - e2) continue;
+                        const double d = dot64(qh, c);
+                        if (lane == 0) atomicMax(&lk64[x / p.H], (unsigned long long)order64(d));
                     }
                     __syncthreads();
                 }
@@ -520,16 +656,19 @@ __global__ void __launch_bounds__(LT) select_kernel(const SelectParams p) {
             // memory, the need-th largest by bisection, ties by position
             uint64_t *k64 = p.key64 + (size_t)list * p.Pp;
             for (int i = c0 + warp; i < c1; i += NW) {
-                const double s = (double)s1[i];
+                const float s = s1[i];
                 uint64_t key = 0;
                 if (!(s > up) && !(s < dn)) {
                     if (same) {
-                        key = order64(s);
+                        key = order64((double)s);
                     } else {
-                        const bool amb = ambiguous(i);
-                        const int h0 = amb ? 0 : (int)(s2[i] & 0xffffu), h1 = amb ? p.H : h0 + 1;
-                        for (int h = h0; h < h1; ++h) {
-                            const uint64_t d = order64(dot64(q + (size_t)h * kDim, means + (size_t)i * kDim));
+                        const __nv_bfloat16 *c = means + (size_t)i * kDim;
+                        float best = -INFINITY;
+                        for (int h = 0; h < p.H; ++h) best = fmaxf(best, dot32(q + (size_t)h * kDim, c));
+                        for (int h = 0; h < p.H; ++h) {
+                            const __nv_bfloat16 *qh = q + (size_t)h * kDim;
+                            if (dot32(qh, c) < best - e2) continue;
+                            const uint64_t d = order64(dot64(qh, c));
                             key = d > key ? d : key;
                         }
                     }
@@ -599,7 +738,7 @@ __global__ void __launch_bounds__(LT) select_kernel(const SelectParams p) {
 
 struct Ws {
     int Pp;
-    size_t s1, s2, cn, k64, total;
+    size_t s1, cn, cm, k64, total;
 };
 Ws workspace(const hs_pool *pool, int64_t B, int64_t T) {
     Ws w{};
@@ -607,11 +746,29 @@ Ws workspace(const hs_pool *pool, int64_t B, int64_t T) {
     const size_t lists = (size_t)B * T, row = (size_t)w.Pp;
     auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
     w.s1 = 0;
-    w.s2 = up(lists * row * 4);
-    w.cn = w.s2 + up(lists * row * 4);
-    w.k64 = w.cn + up((size_t)B * row * 4);
+    w.cn = up(lists * row * 4);
+    w.cm = w.cn + up((size_t)B * row * 4);
+    w.k64 = w.cm + up((size_t)B * row / 32 * 4);
     w.total = w.k64 + up(lists * row * 8);
     return w;
+}
+
+// Splits of a request's page tiles: the count that a model of the launch makes
+// shortest. A tile takes a pair of CTAs about 2.8 us (the pages' bytes at the
+// card's rate, or 256 query rows' products), its start and the queries 4 us.
+int score_splits(int64_t items, int64_t tiles) {
+    const int64_t pairs = sm_count() / 2 > 0 ? sm_count() / 2 : 1;
+    double best = 1e300;
+    int splits = 1;
+    for (int64_t n = 1; n <= tiles && (n == 1 || items * n <= 8 * pairs); ++n) {
+        const double waves = (double)((items * n + pairs - 1) / pairs);
+        const double t = waves * ((double)((tiles + n - 1) / n) * 2.8 + 4.0);
+        if (t < best * 0.98) {
+            best = t;
+            splits = (int)n;
+        }
+    }
+    return splits;
 }
 
 hs_status score_attr(int dev) {
@@ -658,27 +815,39 @@ extern "C" hs_status hs_select_pages(hs_pool_t pool, int32_t B, int32_t T, int32
         p.req = d_req_ids;
         p.ctx = pool->d_ctx;
         p.s1 = reinterpret_cast<float *>(ws + w.s1);
-        p.s2 = reinterpret_cast<uint32_t *>(ws + w.s2);
         p.cn = reinterpret_cast<float *>(ws + w.cn);
         p.err = pool->d_err;
+        p.cm = reinterpret_cast<float *>(ws + w.cm);
         p.T = T;
         p.H = H;
-        p.M = T * H;
-        p.groups = (p.M + MAXN - 1) / MAXN;
-        p.N = ((p.M + p.groups - 1) / p.groups + 15) & ~15;
-        p.nst = RING_BYTES / (A_BYTES + p.N * 128);
-        if (p.nst > MAXST) p.nst = MAXST;
+        p.hpc = H < MAXN ? H : MAXN;
+        p.tpg = MAXN / p.hpc < T ? MAXN / p.hpc : T;
+        p.groups = (T + p.tpg - 1) / p.tpg;
+        p.N = (p.tpg * p.hpc + 31) & ~31;
+        p.splits = score_splits((int64_t)B * p.groups, (pool->max_pages + SP - 1) / SP);
         p.Pp = w.Pp;
         p.max_req = pool->cfg.max_requests;
+        const int64_t units = (int64_t)B * p.groups * p.splits;
+        if (2 * units > INT32_MAX) return HS_ERR_INVALID_ARG;
         CUtensorMap tc, tq;
         if (!make_map(&tc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d_means, kDim, pool->max_pages,
-                      pool->cfg.max_requests, 2 * kDim, 64, SP, CU_TENSOR_MAP_SWIZZLE_128B) ||
-            !make_map(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d_q, kDim, p.M, B, 2 * kDim, 64, p.N,
+                      pool->cfg.max_requests, 2 * kDim, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !make_map(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d_q, kDim, (uint64_t)T * H, B, 2 * kDim, 64, p.N / 2,
                       CU_TENSOR_MAP_SWIZZLE_128B))
             return HS_ERR_CUDA;
-        const dim3 grid((pool->max_pages + SP - 1) / SP, B);
-        score_kernel<<<grid, ST, SCORE_SMEM, s>>>(tc, tq, p);
-        if (cudaGetLastError() != cudaSuccess) return HS_ERR_CUDA;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(2 * units), 1, 1);
+        cfg.blockDim = dim3(ST, 1, 1);
+        cfg.dynamicSmemBytes = SCORE_SMEM;
+        cfg.stream = s;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaLaunchKernelEx(&cfg, score_kernel, tc, tq, p) != cudaSuccess) return HS_ERR_CUDA;
     }
     SelectParams p{};
     p.req = d_req_ids;
@@ -687,8 +856,8 @@ extern "C" hs_status hs_select_pages(hs_pool_t pool, int32_t B, int32_t T, int32
     p.q = static_cast<const __nv_bfloat16 *>(d_q);
     p.means = static_cast<const __nv_bfloat16 *>(d_means);
     p.s1 = reinterpret_cast<float *>(ws + w.s1);
-    p.s2 = reinterpret_cast<uint32_t *>(ws + w.s2);
     p.cn = reinterpret_cast<const float *>(ws + w.cn);
+    p.cm = reinterpret_cast<const float *>(ws + w.cm);
     p.key64 = reinterpret_cast<uint64_t *>(ws + w.k64);
     p.pages = d_pages;
     p.topk = d_topk_idx;
