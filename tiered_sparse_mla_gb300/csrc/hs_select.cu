@@ -44,11 +44,13 @@ __host__ __device__ __forceinline__ int pages_of(int tokens) {
 //   warp 0      producer;  warp 1 (CTA 0) MMA issuer;
 //   warps 2-5   the pages' |c|^2, from the chunks as they land; their arrival is
 //               what the MMA issuer waits for;
-//   warps 6-9   maxima over heads, one thread per page.
+//   warps 6-9   maxima over heads, one thread per page, and the group of eight heads
+//               that each is in.
 constexpr int SP = 256;          // pages per tile (two CTAs)
 constexpr int NCH = kDim / 64;   // depth chunks
 constexpr int ST = 320;
 constexpr int MAXN = 256;        // query rows per pass
+constexpr int HG = 8;            // heads per group
 constexpr int NST = 4;           // ring stages
 constexpr int A_BYTES = 128 * 128;
 constexpr int OFF_RING = NCH * 128 * 128;
@@ -59,6 +61,7 @@ static_assert(SCORE_SMEM <= 232448, "shared memory");
 struct ScoreParams {
     const int32_t *req, *ctx;
     float *s1;       // [B*T][Pp] best head's score
+    uint32_t *s2;    // [B*T][Pp] best score of another group of heads (BF16, rounded up) << 16 | group
     float *cn, *cm;  // [B][Pp] |c_p|^2; [B][Pp / 32] the largest of 32 pages (infinite if one is not finite)
     uint32_t *err;
     int T, H, tpg, groups, splits;  // tokens per group; groups of tokens; splits of the tiles
@@ -250,39 +253,59 @@ score_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ C
             if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(B_DFULL + (i & 1)), (uint32_t)(i >> 1) & 1u));
             if (ok) {
                 tc_fence_after();
-                int t = t0, h = 0;
-                float m = -INFINITY;
+                int t = t0, h = 0, arg = 0;
+                float m = -INFINITY, m2 = -INFINITY;  // best group's score and the best of the others
                 const uint32_t d0 = tmem + lane_off + (uint32_t)((i & 1) * p.N);
+                auto group = [&](float x, int g8) {
+                    m2 = fmaxf(m2, fminf(m, x));
+                    arg = x > m ? g8 : arg;
+                    m = fmaxf(m, x);
+                };
                 auto flush = [&]() {
                     if (page < pages) {
-                        float *at = p.s1 + ((size_t)b * p.T + t) * p.Pp + page;
-                        *at = k > 0 ? fmaxf(*at, m) : m;  // this thread stored the earlier heads' itself
+                        const size_t at = ((size_t)b * p.T + t) * p.Pp + page;
+                        arg += h0 / HG;
+                        if (k > 0) {  // with the earlier heads', which this thread stored itself
+                            const float o = p.s1[at];
+                            const uint32_t w = p.s2[at];
+                            m2 = fmaxf(fmaxf(m2, __uint_as_float(w & 0xffff0000u)), fminf(m, o));
+                            arg = m > o ? arg : (int)(w & 0xffffu);
+                            m = fmaxf(m, o);
+                        }
+                        p.s1[at] = m;
+                        // rounded up: its distance to the best is never overstated
+                        p.s2[at] = ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_ru(m2)) << 16) | (uint32_t)arg;
                     }
-                    m = -INFINITY;
-                    h = 0;
+                    m = m2 = -INFINITY;
+                    h = arg = 0;
                     ++t;
                 };
+                float part = -INFINITY;  // heads that do not come in whole groups
                 for (int c0 = 0; c0 < rows; c0 += 32) {
                     uint32_t d[32];
                     HS_TMEM_LD32(d0 + c0, d);
                     HS_TMEM_WAIT_LD32(d);
                     auto f = [&](int e) { return __uint_as_float(d[e]); };
-                    if ((hn & 7) == 0) {
-                        // a token's heads end at multiples of eight columns
+                    if (hn % HG == 0) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
+                        for (int e = 0; e < 32; e += HG) {
                             if (c0 + e < rows) {
-                                m = max3(m, max3(f(e), f(e + 1), f(e + 2)),
-                                         max3(f(e + 3), max3(f(e + 4), f(e + 5), f(e + 6)), f(e + 7)));
-                                if ((h += 8) == hn) flush();
+                                group(fmaxf(max3(f(e), f(e + 1), f(e + 2)),
+                                            max3(f(e + 3), max3(f(e + 4), f(e + 5), f(e + 6)), f(e + 7))),
+                                      h / HG);
+                                if ((h += HG) == hn) flush();
                             }
                         }
                     } else {
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
                             if (c0 + e < rows) {
-                                m = fmaxf(m, f(e));
-                                if (++h == hn) flush();
+                                part = fmaxf(part, f(e));
+                                if (++h % HG == 0 || h == hn) {
+                                    group(part, (h - 1) / HG);
+                                    part = -INFINITY;
+                                }
+                                if (h == hn) flush();
                             }
                         }
                     }
@@ -302,23 +325,25 @@ score_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ C
 }
 
 // ---------------------------------------------------------------- selection
-// One CTA per (request, query token). A histogram of the scores' bits, as
-// integers in the scores' order, finds the border's bin (one pass where the
-// scores are of one magnitude, three at most); the bin's members give the k-th
-// largest score; a last pass collects the pages above the border's interval and
-// those inside it, and the latter are summed again in 64 bits.
-constexpr int LT = 1024;       // threads
-constexpr int NW = LT / 32;
+// One CTA per (request, query token): 1024 threads, or 256 where they can keep
+// all of a request's scores (fewer barrier partners: one list of 64 pages 9.7 ->
+// SELECT_ONE_256 us of this kernel). The scores are read once, as integers in the
+// scores' order. A histogram of them finds the border's bin (one pass where the
+// scores are of one magnitude, three at most), the bin's members give the k-th
+// largest score, and a last pass collects the pages above the border's interval
+// and those inside it; the latter are summed again in 64 bits. That arithmetic is
+// 1/64 as fast as 32-bit: only sums that 32 bits cannot settle are taken so.
 constexpr int BINS = 2048;
 constexpr int CAP = 512;       // pages near the border that fit in shared memory
 constexpr int MAXSEL = 1024;   // pages per list
-constexpr int KEEP = 16;       // scores that a thread keeps in registers (16,384 pages)
+constexpr int KEEP = 16;       // scores that a thread keeps in registers
 
 struct SelectParams {
     const int32_t *req, *ctx;
     const uint64_t *tree;            // [B][T] or null
     const __nv_bfloat16 *q, *means;  // [B][T][H][576], [max_req][max_pages][576]
     float *s1;
+    uint32_t *s2;
     const float *cn, *cm;
     uint64_t *key64;                 // [B*T][Pp] only written when more than CAP pages are near the border
     int32_t *pages, *topk;           // [B][T][N], [B][T][N*64] or null
@@ -333,6 +358,7 @@ __device__ __forceinline__ uint32_t order32(float x) {
 __device__ __forceinline__ float from_order32(uint32_t k) {
     return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
+constexpr uint32_t KEY_MOST = 0xff7fffffu, KEY_LEAST = 0x00800000u;  // of the finite scores
 // NaN ranks with minus infinity
 __device__ __forceinline__ uint64_t order64(double x) {
     if (x != x) x = -(double)INFINITY;
@@ -340,51 +366,74 @@ __device__ __forceinline__ uint64_t order64(double x) {
     return (u >> 63) ? ~u : (u | (1ull << 63));
 }
 
-// q . c in 64 bits, by a warp (every lane gets the sum)
+// q . c to nearly 64 bits, by a warp (every lane gets the sum). Products of BF16
+// values are exact in f32, and sums are kept as a pair of f32 that loses nothing
+// above 2^-45 of the products' sum (Knuth's two-sum); 64-bit arithmetic is 1/64 as
+// fast and only joins the last pair.
 __device__ __forceinline__ double dot64(const __nv_bfloat16 *q, const __nv_bfloat16 *c) {
     const int lane = threadIdx.x & 31;
-    double acc = 0.0;
+    uint32_t a[kDim / 64], b[kDim / 64];
 #pragma unroll
     for (int i = 0; i < kDim / 64; ++i) {
-        const uint32_t a = reinterpret_cast<const uint32_t *>(q)[lane + 32 * i];
-        const uint32_t b = reinterpret_cast<const uint32_t *>(c)[lane + 32 * i];
-        acc = fma((double)__uint_as_float(a << 16), (double)__uint_as_float(b << 16), acc);
-        acc = fma((double)__uint_as_float(a & 0xffff0000u), (double)__uint_as_float(b & 0xffff0000u), acc);
+        a[i] = reinterpret_cast<const uint32_t *>(q)[lane + 32 * i];
+        b[i] = reinterpret_cast<const uint32_t *>(c)[lane + 32 * i];
     }
+    float s = 0.f, r = 0.f;
+    auto add = [&](float x) {
+        const float t = __fadd_rn(s, x), y = __fsub_rn(t, s);
+        r = __fadd_rn(r, __fadd_rn(__fsub_rn(s, __fsub_rn(t, y)), __fsub_rn(x, y)));
+        s = t;
+    };
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+    for (int i = 0; i < kDim / 64; ++i) {
+        add(__fmul_rn(__uint_as_float(a[i] << 16), __uint_as_float(b[i] << 16)));
+        add(__fmul_rn(__uint_as_float(a[i] & 0xffff0000u), __uint_as_float(b[i] & 0xffff0000u)));
+    }
+#pragma unroll 1
+    for (int o = 16; o >= 1; o >>= 1) {
+        const float so = __shfl_xor_sync(0xffffffffu, s, o), ro = __shfl_xor_sync(0xffffffffu, r, o);
+        r = __fadd_rn(r, ro);
+        add(so);
+    }
+    double acc = (double)s + (double)r;
+    if (!(fabs(acc) <= (double)FLT_MAX)) {
+        // infinities, NaN, or products beyond 32 bits: the same in every lane
+        acc = 0.0;
+#pragma unroll 1
+        for (int i = lane; i < kDim; i += 32)
+            acc = fma((double)__bfloat162float(q[i]), (double)__bfloat162float(c[i]), acc);
+#pragma unroll 1
+        for (int o = 16; o >= 1; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+    }
     return acc;
 }
-
-// The same in 32 bits: off by less than 2^-19 |q||c| (18 products per lane and
-// five additions), well inside E.
+// The same in 32 bits: off by less than 2^-19 |q||c|, well inside E.
 __device__ __forceinline__ float dot32(const __nv_bfloat16 *q, const __nv_bfloat16 *c) {
     const int lane = threadIdx.x & 31;
-    float x = 0.f, y = 0.f;
-#pragma unroll
+    float x = 0.f;
+#pragma unroll 3
     for (int i = 0; i < kDim / 64; ++i) {
         const uint32_t a = reinterpret_cast<const uint32_t *>(q)[lane + 32 * i];
         const uint32_t b = reinterpret_cast<const uint32_t *>(c)[lane + 32 * i];
         x = fmaf(__uint_as_float(a << 16), __uint_as_float(b << 16), x);
-        y = fmaf(__uint_as_float(a & 0xffff0000u), __uint_as_float(b & 0xffff0000u), y);
+        x = fmaf(__uint_as_float(a & 0xffff0000u), __uint_as_float(b & 0xffff0000u), x);
     }
-    x += y;
-#pragma unroll
+#pragma unroll 1
     for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
 }
 
+template <int LT>
 __global__ void __launch_bounds__(LT) select_kernel(const SelectParams p) {
+    constexpr int NW = LT / 32, PB = BINS / LT;
     __shared__ int hist[BINS];
     __shared__ uint32_t lkey[CAP];
     __shared__ int lpage[CAP];
     __shared__ unsigned long long lk64[CAP];
     __shared__ int sel[MAXSEL], sorted[MAXSEL];
-    __shared__ int warp_i[NW];
-    __shared__ float warp_f[NW];
+    __shared__ int warp_i[32];
     __shared__ uint32_t s_lo, s_hi, s_theta;
-    __shared__ int s_need, s_bin, s_m, s_nsel, s_unknown;
-    __shared__ float s_qn, s_cn, s_up, s_dn, s_e2;
+    __shared__ int s_need, s_bin, s_m, s_nsel, s_near, s_qn, s_cn;
     const int list = blockIdx.x, b = list / p.T, t = list % p.T;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int r = p.req[b];
@@ -395,112 +444,115 @@ __global__ void __launch_bounds__(LT) select_kernel(const SelectParams p) {
     const int n = end <= 0 ? 0 : pages_of((int)end);  // pages that hold a token this one may see
     const bool all = n <= p.N;
     const int k = p.N - p.n_first - p.n_last;
-    const int c0 = p.n_first, c1 = n - p.n_last;  // candidates (when not all)
+    const int c0 = p.n_first, cnt = n - p.n_last - c0;  // candidates (when not all)
     if (!req_ok && tid == 0) atomicOr(p.err, HS_DEVERR_BAD_REQUEST);
     if (tid == 0) {
-        s_nsel = 0;
-        s_m = 0;
-        s_unknown = 0;
+        s_nsel = s_m = s_near = 0;
         s_lo = 0xffffffffu;
         s_hi = 0u;
-        s_cn = 0.f;
+        s_qn = s_cn = 0;
     }
-    if (!all && k > 0) {
-        // max |q_h|^2; the queries were there before the scores' kernel began
-        float mx = 0.f;
-        for (int h = warp; h < p.H; h += NW) {
-            const uint32_t *qr = reinterpret_cast<const uint32_t *>(q + (size_t)h * kDim);
-            float s = 0.f;
-#pragma unroll
-            for (int i = 0; i < kDim / 64; ++i) {
-                const uint32_t w = qr[lane + 32 * i];
-                const float lo = __uint_as_float(w << 16), hi = __uint_as_float(w & 0xffff0000u);
-                s = fmaf(lo, lo, s);
-                s = fmaf(hi, hi, s);
-            }
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            mx = s == s ? fmaxf(mx, s) : INFINITY;
-            if (mx == INFINITY) break;
-        }
-        if (lane == 0) warp_f[warp] = mx;
-        __syncthreads();
-        if (tid == 0) {
-            float m = 0.f;
-            for (int w = 0; w < NW; ++w) m = fmaxf(m, warp_f[w]);
-            s_qn = m;
-        }
-    }
-    grid_dep_wait();  // the scores
-    __syncthreads();
-
     if (all) {
         for (int i = tid; i < p.N; i += LT) sorted[i] = i < n ? i : -1;
     } else {
         for (int i = tid; i < p.n_first; i += LT) sel[k + i] = i;
         for (int i = tid; i < p.n_last; i += LT) sel[k + p.n_first + i] = n - p.n_last + i;
     }
+    __syncthreads();
     if (!all && k > 0) {
-        float *s1 = p.s1 + (size_t)list * p.Pp;
-        const float *cn = p.cn + (size_t)b * p.Pp, *cm = p.cm + (size_t)b * p.Pp / 32;
-        const __nv_bfloat16 *means = p.means + (size_t)r * p.max_pages * kDim;
-        // one reading of the scores, all loads at once
-        float v[KEEP];
-        auto load = [&]() {
+        // max |q_h|^2; the queries were there before the scores' kernel began
+        float mx = 0.f;
+        for (int h = warp; h < p.H; h += NW) {
+            const uint32_t *qr = reinterpret_cast<const uint32_t *>(q + (size_t)h * kDim);
+            float x = 0.f, y = 0.f;
 #pragma unroll
-            for (int u = 0; u < KEEP; ++u) {
-                const int i = c0 + tid + u * LT;
-                v[u] = i < c1 ? s1[i] : 0.f;
+            for (int i = 0; i < kDim / 64; ++i) {
+                const uint32_t w = qr[lane + 32 * i];
+                const float lo = __uint_as_float(w << 16), hi = __uint_as_float(w & 0xffff0000u);
+                x = fmaf(lo, lo, x);
+                y = fmaf(hi, hi, y);
             }
+            x += y;
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+            mx = x == x ? fmaxf(mx, x) : INFINITY;
+            if (mx == INFINITY) break;
+        }
+        if (lane == 0) atomicMax(&s_qn, __float_as_int(mx));  // not negative
+    }
+    grid_dep_wait();  // the scores
+    if (!all && k > 0) {
+        float *s1 = p.s1 + (size_t)list * p.Pp + c0;
+        uint32_t *s2 = p.s2 + (size_t)list * p.Pp + c0;
+        const float *cn = p.cn + (size_t)b * p.Pp + c0, *cm = p.cm + (size_t)b * p.Pp / 32;
+        const __nv_bfloat16 *means = p.means + ((size_t)r * p.max_pages + c0) * kDim;
+        // one reading of the scores, all loads at once; candidates are numbered from 0
+        uint32_t v[KEEP];
+        auto load = [&]() {
+            float x[KEEP];
+#pragma unroll
+            for (int u = 0; u < KEEP; ++u) x[u] = tid + u * LT < cnt ? s1[tid + u * LT] : 0.f;
+#pragma unroll
+            for (int u = 0; u < KEEP; ++u) v[u] = order32(x[u]);
         };
         auto each = [&](auto f) {
 #pragma unroll
-            for (int u = 0; u < KEEP; ++u) {
-                const int i = c0 + tid + u * LT;
-                if (i < c1) f(i, v[u]);
+            for (int u = 0; u < KEEP; ++u)
+                if (tid + u * LT < cnt) f(tid + u * LT, v[u]);
+            for (int i = tid + KEEP * LT; i < cnt; i += LT) f(i, order32(s1[i]));
+        };
+        // the same for the few that satisfy `is`: little code in the unrolled part
+        // (instructions that run once come from memory)
+        auto pick = [&](auto is, auto f) {
+            uint32_t mask = 0;
+#pragma unroll
+            for (int u = 0; u < KEEP; ++u) mask |= (tid + u * LT < cnt && is(v[u]) ? 1u : 0u) << u;
+            while (mask) {
+                const int i = tid + (__ffs(mask) - 1) * LT;
+                mask &= mask - 1;
+                f(i, order32(s1[i]));
             }
-            for (int i = c0 + tid + KEEP * LT; i < c1; i += LT) f(i, s1[i]);
+            for (int i = tid + KEEP * LT; i < cnt; i += LT) {
+                const uint32_t key = order32(s1[i]);
+                if (is(key)) f(i, key);
+            }
         };
         load();
-        // a page whose score or norm is not finite says nothing in 32 bits
-        auto unknown = [&](float s, float c) { return !(fabsf(s) <= FLT_MAX) || !(c <= FLT_MAX); };
         uint32_t lo = 0xffffffffu, hi = 0u;
         float cmx = 0.f;
-        int unk = 0;
         for (int i = tid; i < (n + 31) / 32; i += LT) cmx = fmaxf(cmx, cm[i]);
-        each([&](int, float s) {
-            unk |= !(fabsf(s) <= FLT_MAX);
-            const uint32_t key = order32(s);
+        each([&](int, uint32_t key) {
             lo = min(lo, key);
             hi = max(hi, key);
         });
-        unk |= cmx > FLT_MAX;
         lo = __reduce_min_sync(0xffffffffu, lo);
         hi = __reduce_max_sync(0xffffffffu, hi);
-        cmx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(cmx)));  // not negative
-        unk = __any_sync(0xffffffffu, unk);
+        cmx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(cmx)));
         if (lane == 0) {
             atomicMin(&s_lo, lo);
             atomicMax(&s_hi, hi);
-            atomicMax(reinterpret_cast<int *>(&s_cn), __float_as_int(cmx));
-            if (unk) s_unknown = 1;
+            atomicMax(&s_cn, __float_as_int(cmx));
         }
         __syncthreads();
-        if (s_unknown) {
+        lo = s_lo;
+        hi = s_hi;
+        // a page whose score or norm is not finite says nothing in 32 bits
+        const bool some_unknown = lo < KEY_LEAST || hi > KEY_MOST || __int_as_float(s_cn) > FLT_MAX;
+        if (some_unknown) {
             // those pages' scores in 64 bits; what stands for them in 32 is the
             // rounded sum
             __syncthreads();
             if (tid == 0) {
                 s_lo = 0xffffffffu;
                 s_hi = 0u;
-                s_cn = 0.f;
+                s_cn = 0;
             }
             __syncthreads();
-            for (int i0 = c0 + warp * 32; i0 < c1; i0 += LT) {
+            for (int i0 = warp * 32; i0 < cnt; i0 += LT) {
                 const int i = i0 + lane;
-                float s = i < c1 ? s1[i] : 0.f;
-                const float c = i < c1 ? cn[i] : 0.f;
-                const bool mine = i < c1 && unknown(s, c);
+                float s = i < cnt ? s1[i] : 0.f;
+                const float c = i < cnt ? cn[i] : 0.f;
+                const bool mine = i < cnt && (!(fabsf(s) <= FLT_MAX) || !(c <= FLT_MAX));
                 unsigned todo = __ballot_sync(0xffffffffu, mine);
                 while (todo) {
                     const int who = __ffs(todo) - 1, pg = i0 + who;
@@ -513,37 +565,39 @@ __global__ void __launch_bounds__(LT) select_kernel(const SelectParams p) {
                     if (lane == who) {
                         s = __double2float_rn(best);
                         s1[pg] = s;
+                        s2[pg] = 0x7f800000u;  // another group's may be as good
                     }
                 }
-                if (i < c1) {
+                if (i < cnt) {
                     const uint32_t key = order32(s);
                     atomicMin(&s_lo, key);
                     atomicMax(&s_hi, key);
-                    if (!mine) atomicMax(reinterpret_cast<int *>(&s_cn), __float_as_int(c));
+                    if (!mine) atomicMax(&s_cn, __float_as_int(c));
                 }
             }
             __syncthreads();
             load();
+            lo = s_lo;
+            hi = s_hi;
         }
         // ------------------------------------------------ the border's bin
-        int need = k;
-        lo = s_lo;
-        hi = s_hi;
-        int m = c1 - c0;
+        int need = k, m = cnt;
         while (m > CAP && lo != hi) {
             const int bits = 32 - __clz((int)(hi - lo));
             const int sh = bits > 11 ? bits - 11 : 0;
             for (int i = tid; i < BINS; i += LT) hist[i] = 0;
             __syncthreads();
-            each([&](int, float s) {
-                const uint32_t key = order32(s);
-                if (key >= lo && key <= hi) atomicAdd(&hist[(key - lo) >> sh], 1);
+            const uint32_t span = hi - lo;
+            each([&](int, uint32_t key) {
+                if (key - lo <= span) atomicAdd(&hist[(key - lo) >> sh], 1);
             });
             __syncthreads();
-            // from the top: thread i holds bins BINS-1-2i and the one below
-            const int b0 = BINS - 1 - 2 * tid;
-            const int h0 = hist[b0], h1 = hist[b0 - 1];
-            int sum = h0 + h1;
+            // from the top: a thread's PB bins, the highest first
+            const int b0 = BINS - 1 - PB * tid;
+            int hb[PB], own = 0;
+#pragma unroll
+            for (int e = 0; e < PB; ++e) own += hb[e] = hist[b0 - e];
+            int sum = own;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int x = __shfl_up_sync(0xffffffffu, sum, o);
@@ -551,17 +605,16 @@ __global__ void __launch_bounds__(LT) select_kernel(const SelectParams p) {
             }
             if (lane == 31) warp_i[warp] = sum;
             __syncthreads();
-            int before = 0;
-            for (int w = 0; w < warp; ++w) before += warp_i[w];
-            const int a = before + sum - h0 - h1;  // members above bin b0
-            if (a < need && a + h0 >= need) {
-                s_bin = b0;
-                s_need = need - a;
-                s_m = h0;
-            } else if (a + h0 < need && a + h0 + h1 >= need) {
-                s_bin = b0 - 1;
-                s_need = need - a - h0;
-                s_m = h1;
+            int above = sum - own;  // members above this thread's bins
+            for (int w = 0; w < warp; ++w) above += warp_i[w];
+#pragma unroll
+            for (int e = 0; e < PB; ++e) {
+                if (above < need && above + hb[e] >= need) {
+                    s_bin = b0 - e;
+                    s_need = need - above;
+                    s_m = hb[e];
+                }
+                above += hb[e];
             }
             __syncthreads();
             need = s_need;
@@ -571,19 +624,19 @@ __global__ void __launch_bounds__(LT) select_kernel(const SelectParams p) {
             __syncthreads();
         }
         // the k-th largest score: the need-th of the bin
-        if (lo == hi) {
-            if (tid == 0) s_theta = lo;
-        } else {
-            if (tid == 0) s_m = 0;
+        if (tid == 0) {
+            s_m = 0;
+            s_theta = lo;
+        }
+        __syncthreads();
+        if (lo != hi) {
+            const uint32_t span = hi - lo;
+            pick([&](uint32_t key) { return key - lo <= span; },
+                 [&](int, uint32_t key) { lkey[atomicAdd(&s_m, 1)] = key; });
             __syncthreads();
-            each([&](int, float s) {
-                const uint32_t key = order32(s);
-                if (key >= lo && key <= hi) lkey[atomicAdd(&s_m, 1)] = key;
-            });
-            __syncthreads();
-            if (tid < m) {
+            for (int i = tid; i < m; i += LT) {
                 int above = 0, equal = 0;
-                const uint32_t mine = lkey[tid];
+                const uint32_t mine = lkey[i];
                 for (int j = 0; j < m; ++j) {
                     above += lkey[j] > mine;
                     equal += lkey[j] == mine;
@@ -592,75 +645,65 @@ __global__ void __launch_bounds__(LT) select_kernel(const SelectParams p) {
             }
             __syncthreads();
         }
-        if (tid == 0) s_m = 0;
-        __syncthreads();
         // ------------------------------------------------ above it, and near it
-        // (64-bit arithmetic is 1/64 as fast: one thread's, and the few sums' below)
-        if (tid == 0) {
-            const double theta = (double)from_order32(s_theta);
-            const double e2 = 2.0 * (1.0 / 65536.0) * sqrt((double)s_qn) * sqrt((double)s_cn) * 1.0001;
-            const double slack = e2 + fabs(theta) * (1.0 / 4194304.0);
-            s_up = __double2float_ru(theta + slack);
-            s_dn = __double2float_rd(theta - slack);
-            s_e2 = __double2float_ru(e2);
-        }
+        // The interval's bounds are rounded outwards; a bound that is NaN (norms
+        // beyond 32 bits) makes every page near.
+        const float theta = from_order32(s_theta);
+        const float e2 = __fmul_ru(2.f / 65536.f * 1.001f, __fmul_ru(__fsqrt_ru(__int_as_float(s_qn)), __fsqrt_ru(__int_as_float(s_cn))));
+        const float slack = __fadd_ru(e2, __fmul_ru(fabsf(theta), 1.f / 4194304.f));
+        const float fup = __fadd_ru(theta, slack), fdn = __fadd_rd(theta, -slack);
+        const uint32_t up = fup == fup ? order32(fup) : 0xffffffffu, dn = fdn == fdn ? order32(fdn) : 0u;
+        pick([&](uint32_t key) { return key >= dn; },
+             [&](int i, uint32_t key) {
+                 if (key > up) {
+                     sel[atomicAdd(&s_nsel, 1)] = c0 + i;
+                 } else {
+                     const int j = atomicAdd(&s_near, 1);
+                     if (j < CAP) lpage[j] = i;
+                 }
+             });
         __syncthreads();
-        const float up = s_up, dn = s_dn, e2 = s_e2;
-        each([&](int i, float s) {
-            if (s > up) {
-                sel[atomicAdd(&s_nsel, 1)] = i;
-            } else if (!(s < dn)) {
-                const int j = atomicAdd(&s_m, 1);
-                if (j < CAP) lpage[j] = i;
-            }
-        });
-        __syncthreads();
-        need = k - s_nsel;
-        m = s_m;
-        const bool same = e2 == 0.f && !s_unknown;  // the sums are exact as they are
-        if (m <= CAP) {
-            if (m == need) {
-                if (tid < m) sel[s_nsel + tid] = lpage[tid];
-            } else {
-                if (tid < m) {
-                    lk64[tid] = same ? order64((double)s1[lpage[tid]]) : 0ull;
-                    lkey[tid] = 0u;
+        const int first = s_nsel;
+        need = k - first;
+        m = s_near;
+        const bool same = e2 == 0.f && !some_unknown;  // the sums are exact as they are
+        if (m == need && m <= CAP) {
+            for (int i = tid; i < m; i += LT) sel[first + i] = c0 + lpage[i];
+        } else if (m <= CAP) {
+            for (int i = tid; i < m; i += LT) lk64[i] = same ? order64((double)s1[lpage[i]]) : 0ull;
+            __syncthreads();
+            if (!same) {
+                // The heads in question: those of the best group, or all where
+                // another group comes near it. A warp takes one at a time.
+                for (int e = 0; e < m; ++e) {
+                    const int pg = lpage[e];
+                    const uint32_t w = s2[pg];
+                    const bool one = s1[pg] - __uint_as_float(w & 0xffff0000u) > e2;
+                    const int h0 = one ? (int)(w & 0xffffu) * HG : 0, hn = one ? min(HG, p.H - h0) : p.H;
+                    // entries begin at different warps, so that they run at once
+                    for (int h = (warp + NW - e * HG % NW) % NW; h < hn; h += NW) {
+                        const double y = dot64(q + (size_t)(h0 + h) * kDim, means + (size_t)pg * kDim);
+                        if (lane == 0) atomicMax(&lk64[e], (unsigned long long)order64(y));
+                    }
                 }
                 __syncthreads();
-                if (!same) {
-                    // every (page, head) in 32 bits, then those near the page's best in 64
-                    const int pairs = m * p.H;
-                    for (int x = warp; x < pairs; x += NW) {
-                        const float d = dot32(q + (size_t)(x % p.H) * kDim, means + (size_t)lpage[x / p.H] * kDim);
-                        if (lane == 0 && d == d) atomicMax(&lkey[x / p.H], order32(d));
-                    }
-                    __syncthreads();
-                    for (int x = warp; x < pairs; x += NW) {
-                        const __nv_bfloat16 *qh = q + (size_t)(x % p.H) * kDim, *c = means + (size_t)lpage[x / p.H] * kDim;
-                        const uint32_t bk = lkey[x / p.H];
-                        if (bk && dot32(qh, c) < from_order32(bk) - e2) continue;
-                        const double d = dot64(qh, c);
-                        if (lane == 0) atomicMax(&lk64[x / p.H], (unsigned long long)order64(d));
-                    }
-                    __syncthreads();
-                }
-                if (tid < m) {
-                    int better = 0;
-                    for (int j = 0; j < m; ++j)
-                        better += lk64[j] > lk64[tid] || (lk64[j] == lk64[tid] && lpage[j] < lpage[tid]);
-                    if (better < need) sel[s_nsel + better] = lpage[tid];
-                }
+            }
+            for (int i = tid; i < m; i += LT) {
+                int better = 0;
+                for (int j = 0; j < m; ++j)
+                    better += lk64[j] > lk64[i] || (lk64[j] == lk64[i] && lpage[j] < lpage[i]);
+                if (better < need) sel[first + better] = c0 + lpage[i];
             }
         } else {
             // very many equal or nearly equal scores: keys of all candidates in
             // memory, the need-th largest by bisection, ties by position
             uint64_t *k64 = p.key64 + (size_t)list * p.Pp;
-            for (int i = c0 + warp; i < c1; i += NW) {
-                const float s = s1[i];
+            for (int i = warp; i < cnt; i += NW) {
+                const uint32_t key32 = order32(s1[i]);
                 uint64_t key = 0;
-                if (!(s > up) && !(s < dn)) {
+                if (key32 >= dn && key32 <= up) {
                     if (same) {
-                        key = order64((double)s);
+                        key = order64((double)s1[i]);
                     } else {
                         const __nv_bfloat16 *c = means + (size_t)i * kDim;
                         float best = -INFINITY;
@@ -668,8 +711,8 @@ __global__ void __launch_bounds__(LT) select_kernel(const SelectParams p) {
                         for (int h = 0; h < p.H; ++h) {
                             const __nv_bfloat16 *qh = q + (size_t)h * kDim;
                             if (dot32(qh, c) < best - e2) continue;
-                            const uint64_t d = order64(dot64(qh, c));
-                            key = d > key ? d : key;
+                            const uint64_t y = order64(dot64(qh, c));
+                            key = y > key ? y : key;
                         }
                     }
                 }
@@ -678,7 +721,7 @@ __global__ void __launch_bounds__(LT) select_kernel(const SelectParams p) {
             __syncthreads();
             auto count = [&](uint64_t at_least) {  // by the whole CTA
                 int c = 0;
-                for (int i = c0 + tid; i < c1; i += LT) c += k64[i] >= at_least;
+                for (int i = tid; i < cnt; i += LT) c += k64[i] >= at_least;
                 c = __reduce_add_sync(0xffffffffu, c);
                 if (lane == 0) warp_i[warp] = c;
                 __syncthreads();
@@ -693,20 +736,18 @@ __global__ void __launch_bounds__(LT) select_kernel(const SelectParams p) {
                 if (count(mid) >= need) tau = mid;
             }
             int room = need - count(tau + 1);  // of those equal to it, the lowest pages
-            const int first = s_nsel;
             if (tid == 0) s_m = 0;
             __syncthreads();
-            for (int i0 = c0; i0 < c1; i0 += LT) {
+            for (int i0 = 0; i0 < cnt; i0 += LT) {
                 const int i = i0 + tid;
-                const uint64_t key = i < c1 ? k64[i] : 0;
+                const uint64_t key = i < cnt ? k64[i] : 0;
                 int total;
-                const int rank = hs::block_scan_flag<LT>(i < c1 && key == tau, warp_i, total);
-                if (i < c1 && (key > tau || (key == tau && rank < room)))
-                    sel[first + atomicAdd(&s_m, 1)] = i;
+                const int rank = hs::block_scan_flag<LT>(i < cnt && key == tau, warp_i, total);
+                if (i < cnt && (key > tau || (key == tau && rank < room)))
+                    sel[first + atomicAdd(&s_m, 1)] = c0 + i;
                 room -= total;
             }
         }
-        __syncthreads();
     }
     __syncthreads();
     if (!all) {
@@ -717,8 +758,8 @@ __global__ void __launch_bounds__(LT) select_kernel(const SelectParams p) {
             for (int j = 0; j < p.N; ++j) at += sel[j] < mine;
             sorted[at] = mine;
         }
+        __syncthreads();
     }
-    __syncthreads();
     for (int i = tid; i < p.N; i += LT) p.pages[(size_t)list * p.N + i] = sorted[i];
     if (p.topk) {
         const uint64_t tree = p.tree ? p.tree[list] : 0;
@@ -738,7 +779,7 @@ __global__ void __launch_bounds__(LT) select_kernel(const SelectParams p) {
 
 struct Ws {
     int Pp;
-    size_t s1, cn, cm, k64, total;
+    size_t s1, s2, cn, cm, k64, total;
 };
 Ws workspace(const hs_pool *pool, int64_t B, int64_t T) {
     Ws w{};
@@ -746,7 +787,8 @@ Ws workspace(const hs_pool *pool, int64_t B, int64_t T) {
     const size_t lists = (size_t)B * T, row = (size_t)w.Pp;
     auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
     w.s1 = 0;
-    w.cn = up(lists * row * 4);
+    w.s2 = up(lists * row * 4);
+    w.cn = w.s2 + up(lists * row * 4);
     w.cm = w.cn + up((size_t)B * row * 4);
     w.k64 = w.cm + up((size_t)B * row / 32 * 4);
     w.total = w.k64 + up(lists * row * 8);
@@ -815,6 +857,7 @@ extern "C" hs_status hs_select_pages(hs_pool_t pool, int32_t B, int32_t T, int32
         p.req = d_req_ids;
         p.ctx = pool->d_ctx;
         p.s1 = reinterpret_cast<float *>(ws + w.s1);
+        p.s2 = reinterpret_cast<uint32_t *>(ws + w.s2);
         p.cn = reinterpret_cast<float *>(ws + w.cn);
         p.err = pool->d_err;
         p.cm = reinterpret_cast<float *>(ws + w.cm);
@@ -856,6 +899,7 @@ extern "C" hs_status hs_select_pages(hs_pool_t pool, int32_t B, int32_t T, int32
     p.q = static_cast<const __nv_bfloat16 *>(d_q);
     p.means = static_cast<const __nv_bfloat16 *>(d_means);
     p.s1 = reinterpret_cast<float *>(ws + w.s1);
+    p.s2 = reinterpret_cast<uint32_t *>(ws + w.s2);
     p.cn = reinterpret_cast<const float *>(ws + w.cn);
     p.cm = reinterpret_cast<const float *>(ws + w.cm);
     p.key64 = reinterpret_cast<uint64_t *>(ws + w.k64);
@@ -872,7 +916,8 @@ extern "C" hs_status hs_select_pages(hs_pool_t pool, int32_t B, int32_t T, int32
     p.max_pages = pool->max_pages;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((int64_t)B * T), 1, 1);
-    cfg.blockDim = dim3(LT, 1, 1);
+    const bool few = pool->max_pages <= KEEP * 256;
+    cfg.blockDim = dim3(few ? 256 : 1024, 1, 1);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     // its first part needs nothing of the scores' kernel
@@ -880,5 +925,5 @@ extern "C" hs_status hs_select_pages(hs_pool_t pool, int32_t B, int32_t T, int32
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pool->max_pages > N && N > n_first + n_last ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, select_kernel, p) == cudaSuccess ? HS_OK : HS_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, few ? select_kernel<256> : select_kernel<1024>, p) == cudaSuccess ? HS_OK : HS_ERR_CUDA;
 }
