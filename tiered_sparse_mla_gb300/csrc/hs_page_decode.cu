@@ -218,14 +218,6 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         atomicOr(p.err, HS_DEVERR_TIMEOUT);
     };
 
-    // The loads that lead to the first copy, as early and as parallel as they go:
-    // entries and request, then the table (its bounds do not need the context's
-    // length) and the length.
-    const int32_t *entries = p.pages ? p.pages + (size_t)list * p.N : nullptr;
-    const bool loader = warp == 0 || warp == 3;
-    int e0 = -1;  // entry `lane`
-    if (loader && entries && lane < p.N) e0 = entries[lane];
-    const int req = p.req[list / p.tpl];
     if (threadIdx.x == 32) {
         mbar_init(bar(C::B_QFULL), 1);
         mbar_init(bar(C::B_QDONE), NSW);
@@ -255,12 +247,27 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         misc[1] = 0;
         fence_mbar_init();
         fence_proxy_async();
+        grid_dep_wait();
         // Q by TMA at once: its barrier is this CTA's own
         mbar_expect_tx(bar(C::B_QFULL), NK * CH);
         for (int i = 0; i < NK; ++i)
             tma_load_3d(i < NQT ? base + C::OFF_QST + i * CH : base + C::OFF_Q + (i - NQT) * CH, &tm_q, 64 * i,
                         mt * BM + RM * rank, list, bar(C::B_QFULL));
     }
+    if (warp == 2) tmem_alloc2(base + C::OFF_MISC, 512);
+    // What the earlier kernels of the stream wrote is read from here on: this grid
+    // may be launched while the last of them still runs. It lets no later grid begin
+    // before it ends: the splits' join, placed on SMs that were done early, kept the
+    // next call's CTAs from theirs (76 x 27 steps: 129 against 144 us a call).
+    grid_dep_wait();
+    // The loads that lead to the first copy, as early and as parallel as they go:
+    // entries and request, then the table (its bounds do not need the context's
+    // length) and the length.
+    const int32_t *entries = p.pages ? p.pages + (size_t)list * p.N : nullptr;
+    const bool loader = warp == 0 || warp == 3;
+    int e0 = -1;  // entry `lane`
+    if (loader && entries && lane < p.N) e0 = entries[lane];
+    const int req = p.req[list / p.tpl];
     const bool req_ok = req >= 0 && req < p.max_req;
     const int L = req_ok ? p.ctx[req] : 0;
     const int2 *table = p.table + (size_t)(req_ok ? req : 0) * p.max_pages;
@@ -308,7 +315,6 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         fetch(0, npg, nblk);
         if (warp == 0 && lane == 0) misc[2] = nsteps;
     }
-    if (warp == 2) tmem_alloc2(base + C::OFF_MISC, 512);
     tc_fence_before();
     __syncthreads();
     // Both CTAs' barriers and tensor memory are there. What the peer needs of this
@@ -316,7 +322,6 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     // wait for everything in flight (measured 3k clocks).
     cluster_sync_relaxed();
     tc_fence_after();
-    grid_dep_launch();
     const uint32_t tmem = static_cast<uint32_t>(misc[0]);
     nsteps = misc[2];
 
@@ -967,42 +972,116 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     if (warp == 2) tmem_dealloc2(tmem, 512);
 }
 
-// Joins the splits: out = sum_s w_s O_s / sum_s w_s, w_s = exp(lse_s - max), in
-// the splits' order. Four columns of a row per thread.
-__global__ void __launch_bounds__(256)
-page_combine_kernel(const float *__restrict__ ws_o, const float *__restrict__ ws_lse, int nsplit, int rows,
-                    __nv_bfloat16 *__restrict__ out, float *__restrict__ lse) {
-    grid_dep_wait();  // the splits' partials
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t row = i >> 7;
-    const int c = (int)(i & 127) * 4;
-    if (row >= rows) return;
-    float mx = -INFINITY;
-    bool nan = false;
-    for (int s = 0; s < nsplit; ++s) {
-        const float v = ws_lse[(size_t)s * rows + row];
-        nan = nan || v != v;
-        mx = fmaxf(mx, v);
-    }
-    float acc[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
-    if (mx != -INFINITY) {
-#pragma unroll 4
-        for (int s = 0; s < nsplit; ++s) {
-            const float v = ws_lse[(size_t)s * rows + row];
-            if (v == -INFINITY) continue;  // that split's partial was not written
-            const float4 o = *reinterpret_cast<const float4 *>(ws_o + ((size_t)s * rows + row) * 512 + c);
-            const float w = exp2f((v - mx) * 1.4426950408889634f);
-            sum += w;
-            acc[0] = fmaf(w, o.x, acc[0]);
-            acc[1] = fmaf(w, o.y, acc[1]);
-            acc[2] = fmaf(w, o.z, acc[2]);
-            acc[3] = fmaf(w, o.w, acc[3]);
-        }
-    }
+// Joins the splits: out = sum_s w_s O_s / sum_s w_s, w_s = exp(lse_s - max), in a
+// fixed order. Four columns of a row per thread; up to FEW splits all loads are
+// issued before the first is used. More splits (long contexts, few rows): a block
+// per row, four groups of threads over every fourth split, joined in shared memory
+// (19 splits of 512 rows: 9 -> COMBINE_MANY us behind the main kernel).
+constexpr int FEW = 4, JG = 4;
+__device__ __forceinline__ void store_joined(__nv_bfloat16 *out, float *lse, int64_t row, int c, const float (&acc)[4],
+                                             float sum, float mx, bool nan) {
     const float inv = nan ? __uint_as_float(0x7fc00000u) : (sum > 0.f ? __fdividef(1.f, sum) : 0.f);
     *reinterpret_cast<uint2 *>(out + row * 512 + c) =
         make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
     if (c == 0) lse[row] = nan ? inv : (sum > 0.f ? mx + __logf(sum) : -INFINITY);
+}
+__device__ __forceinline__ void add_split(float (&acc)[4], float w, float4 o) {
+    acc[0] = fmaf(w, o.x, acc[0]);
+    acc[1] = fmaf(w, o.y, acc[1]);
+    acc[2] = fmaf(w, o.z, acc[2]);
+    acc[3] = fmaf(w, o.w, acc[3]);
+}
+__global__ void __launch_bounds__(256)
+join_few_kernel(const float *__restrict__ ws_o, const float *__restrict__ ws_lse, int nsplit, int rows,
+                __nv_bfloat16 *__restrict__ out, float *__restrict__ lse) {
+    grid_dep_wait();  // the splits' partials
+    grid_dep_launch();
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t row = i >> 7;
+    const int c = (int)(i & 127) * 4;
+    if (row >= rows) return;
+    float v[FEW];
+    float4 o[FEW];
+#pragma unroll
+    for (int s = 0; s < FEW; ++s) {
+        v[s] = -INFINITY;
+        o[s] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (s < nsplit) {
+            v[s] = ws_lse[(size_t)s * rows + row];
+            o[s] = __ldcs(reinterpret_cast<const float4 *>(ws_o + ((size_t)s * rows + row) * 512 + c));
+        }
+    }
+    float mx = -INFINITY;
+    bool nan = false;
+#pragma unroll
+    for (int s = 0; s < FEW; ++s) {
+        nan = nan || v[s] != v[s];
+        mx = fmaxf(mx, v[s]);
+    }
+    float acc[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
+#pragma unroll
+    for (int s = 0; s < FEW; ++s)
+        if (v[s] != -INFINITY) {  // otherwise that split's partial was not written
+            const float w = exp2f((v[s] - mx) * 1.4426950408889634f);
+            sum += w;
+            add_split(acc, w, o[s]);
+        }
+    store_joined(out, lse, row, c, acc, sum, mx, nan);
+}
+__global__ void __launch_bounds__(128 * JG)
+join_many_kernel(const float *__restrict__ ws_o, const float *__restrict__ ws_lse, int nsplit, int rows,
+                 __nv_bfloat16 *__restrict__ out, float *__restrict__ lse) {
+    __shared__ float w[128];
+    __shared__ float4 part[JG - 1][128];
+    __shared__ float s_mx, s_sum;
+    __shared__ int s_nan;
+    grid_dep_wait();
+    grid_dep_launch();
+    const int64_t row = blockIdx.x;
+    const int g = threadIdx.x >> 7, col = threadIdx.x & 127;
+    if (threadIdx.x < 32) {  // the splits' weights, by one warp
+        float v[4], mx = -INFINITY;
+        bool nan = false;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int s = threadIdx.x + 32 * u;
+            v[u] = s < nsplit ? ws_lse[(size_t)s * rows + row] : -INFINITY;
+            nan = nan || v[u] != v[u];
+            mx = fmaxf(mx, v[u]);
+        }
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+        nan = __any_sync(0xffffffffu, nan);
+        float sum = 0.f;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float x = v[u] == -INFINITY ? 0.f : exp2f((v[u] - mx) * 1.4426950408889634f);
+            w[threadIdx.x + 32 * u] = x;
+            sum += x;
+        }
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (threadIdx.x == 0) {
+            s_mx = mx;
+            s_sum = sum;
+            s_nan = nan;
+        }
+    }
+    __syncthreads();
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int s = g; s < nsplit; s += JG) {
+        const float x = w[s];
+        if (x == 0.f) continue;  // nothing was seen there: its partial was not written, or does not count
+        add_split(acc, x, __ldcs(reinterpret_cast<const float4 *>(ws_o + ((size_t)s * rows + row) * 512) + col));
+    }
+    if (g) part[g - 1][col] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    __syncthreads();
+    if (g == 0) {
+#pragma unroll
+        for (int u = 0; u < JG - 1; ++u) add_split(acc, 1.f, part[u][col]);
+        store_joined(out, lse, row, 4 * col, acc, s_sum, s_mx, s_nan != 0);
+    }
 }
 
 // ---------------------------------------------------------------- host side
@@ -1070,13 +1149,15 @@ hs_status launch_pages(dim3 grid, int dev, cudaStream_t s, const CUtensorMap &tq
     cfg.blockDim = dim3(PCfg<FP8>::THREADS, 1, 1);
     cfg.dynamicSmemBytes = PCfg<FP8>::SMEM_ALLOC;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, page_decode_kernel<FP8>, tq, k1, k2, to, p) == cudaSuccess ? HS_OK : HS_ERR_CUDA;
 }
 
@@ -1149,17 +1230,19 @@ hs_status page_entry(hs_pool_t pool, int64_t lists, int32_t T, int32_t tpl, int3
                              : launch_pages<false>(grid, dev, s, tq, maps[0], maps[1], to, p);
     if (st != HS_OK || pl.nsplit == 1) return st;
     const int n = (int)(lists * pl.M);
+    const bool few = pl.nsplit <= FEW;
     cudaLaunchConfig_t cc = {};
-    cc.gridDim = dim3((unsigned)(((int64_t)n * 128 + 255) / 256), 1, 1);
-    cc.blockDim = dim3(256, 1, 1);
+    cc.gridDim = dim3((unsigned)(few ? ((int64_t)n * 128 + 255) / 256 : n), 1, 1);
+    cc.blockDim = dim3(few ? 256 : 128 * JG, 1, 1);
     cc.stream = s;
     cudaLaunchAttribute ca[1];
     ca[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     ca[0].val.programmaticStreamSerializationAllowed = 1;
     cc.attrs = ca;
     cc.numAttrs = 1;
-    return cudaLaunchKernelEx(&cc, page_combine_kernel, (const float *)d_workspace, (const float *)p.ws_lse, pl.nsplit, n,
-                              static_cast<__nv_bfloat16 *>(d_out), d_lse) == cudaSuccess
+    return cudaLaunchKernelEx(&cc, few ? join_few_kernel : join_many_kernel, (const float *)d_workspace,
+                              (const float *)p.ws_lse, pl.nsplit, n, static_cast<__nv_bfloat16 *>(d_out),
+                              d_lse) == cudaSuccess
                ? HS_OK
                : HS_ERR_CUDA;
 }

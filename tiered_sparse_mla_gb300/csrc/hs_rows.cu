@@ -10,6 +10,7 @@
 #include <cstdint>
 
 #include "hs_internal.cuh"
+#include "hs_tc.cuh"
 
 namespace {
 
@@ -71,6 +72,8 @@ __device__ __forceinline__ uint2 quantise8(uint4 v, float scale, float inv) {
 template <bool FP8>
 __global__ void __launch_bounds__(AT) append_kernel(const AppendParams p) {
     constexpr int RB = FP8 ? kDim : 2 * kDim;
+    hs::tc::grid_dep_wait();  // may be launched while the stream's last kernel runs
+    hs::tc::grid_dep_launch();
     const int lane = threadIdx.x & 31, part = lane & 7;
     const int64_t i = (int64_t)blockIdx.x * ARB + (threadIdx.x >> 5) * ARW + (lane >> 3);
     // whole warps run to the shuffles; rows that write nothing have go = false
@@ -188,6 +191,8 @@ means_kernel(const uint8_t *__restrict__ rows, const float *__restrict__ scales,
     constexpr int NR = kPage / G;    // rows per thread: 16, or 8
     constexpr int E = FP8 ? 16 : 8;  // values per piece
     __shared__ float part[G][kDim + 4];
+    hs::tc::grid_dep_wait();
+    hs::tc::grid_dep_launch();
     const int r = req[blockIdx.x], p = pg[blockIdx.x];
     const bool in_range = r >= 0 && r < max_req && p >= 0 && p < max_pages;
     const size_t at = (size_t)(in_range ? r : 0) * max_pages + (in_range ? p : 0);
@@ -253,6 +258,22 @@ means_kernel(const uint8_t *__restrict__ rows, const float *__restrict__ scales,
     }
 }
 
+// A launch that may begin while the stream's previous kernel still runs (the
+// kernels wait for it before they read or write anything).
+template <typename... P, typename... A>
+hs_status launch(void (*kernel)(P...), unsigned grid, int threads, void *stream, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...) == cudaSuccess ? HS_OK : HS_ERR_CUDA;
+}
+
 bool on_pool_device(const hs_pool *pool) {
     int dev = -1;
     return cudaGetDevice(&dev) == cudaSuccess && dev == pool->device;
@@ -290,12 +311,7 @@ extern "C" hs_status hs_append_rows(hs_pool_t pool, int32_t B, int32_t T, const 
     p.C = pool->cfg.hot_rows;
     p.HB = pool->hb;
     const unsigned grid = (unsigned)((n + ARB - 1) / ARB);
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (pool->cfg.dtype == HS_BF16)
-        append_kernel<false><<<grid, AT, 0, s>>>(p);
-    else
-        append_kernel<true><<<grid, AT, 0, s>>>(p);
-    return cudaGetLastError() == cudaSuccess ? HS_OK : HS_ERR_CUDA;
+    return launch(pool->cfg.dtype == HS_BF16 ? append_kernel<false> : append_kernel<true>, grid, AT, stream, p);
 }
 
 extern "C" hs_status hs_page_means(hs_pool_t pool, int32_t n, const int32_t *d_req,
@@ -304,17 +320,8 @@ extern "C" hs_status hs_page_means(hs_pool_t pool, int32_t n, const int32_t *d_r
     if (n == 0) return HS_OK;
     if (!d_req || !d_page || !d_means || ((uintptr_t)d_means & 15u) || !on_pool_device(pool))
         return HS_ERR_INVALID_ARG;
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int2 *pt = reinterpret_cast<const int2 *>(pool->d_page);
-    auto *out = static_cast<__nv_bfloat16 *>(d_means);
-    if (pool->cfg.dtype == HS_BF16)
-        means_kernel<false><<<n, MT, 0, s>>>(pool->d_rows, nullptr, pool->hd_rows, nullptr, pt,
-                                             pool->d_ctx, pool->cfg.max_requests, pool->max_pages,
-                                             d_req, d_page, out, pool->d_err);
-    else
-        means_kernel<true><<<n, MT, 0, s>>>(pool->d_rows, pool->d_scales, pool->hd_rows,
-                                            pool->hd_scales, pt, pool->d_ctx,
-                                            pool->cfg.max_requests, pool->max_pages, d_req, d_page,
-                                            out, pool->d_err);
-    return cudaGetLastError() == cudaSuccess ? HS_OK : HS_ERR_CUDA;
+    return launch(pool->cfg.dtype == HS_BF16 ? means_kernel<false> : means_kernel<true>, (unsigned)n, MT, stream,
+                  pool->d_rows, pool->d_scales, pool->hd_rows, pool->hd_scales,
+                  reinterpret_cast<const int2 *>(pool->d_page), pool->d_ctx, pool->cfg.max_requests, pool->max_pages,
+                  d_req, d_page, static_cast<__nv_bfloat16 *>(d_means), pool->d_err);
 }

@@ -73,6 +73,9 @@ __global__ void __launch_bounds__(ST, 1)
 score_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_q,
              const ScoreParams p) {
     extern __shared__ uint8_t smem_raw[];
+    // launched early, and launching early, but only what comes before is complete:
+    // a later grid may read what this one's predecessors wrote before it waits
+    grid_dep_wait();
     grid_dep_launch();
     const int rank = static_cast<int>(hs::cluster_ctarank());
     const int unit = blockIdx.x >> 1, split = unit % p.splits, g = (unit / p.splits) % p.groups;
@@ -481,6 +484,7 @@ __global__ void __launch_bounds__(LT) select_kernel(const SelectParams p) {
         if (lane == 0) atomicMax(&s_qn, __float_as_int(mx));  // not negative
     }
     grid_dep_wait();  // the scores
+    grid_dep_launch();
     if (!all && k > 0) {
         float *s1 = p.s1 + (size_t)list * p.Pp + c0;
         uint32_t *s2 = p.s2 + (size_t)list * p.Pp + c0;
@@ -883,13 +887,15 @@ extern "C" hs_status hs_select_pages(hs_pool_t pool, int32_t B, int32_t T, int32
         cfg.blockDim = dim3(ST, 1, 1);
         cfg.dynamicSmemBytes = SCORE_SMEM;
         cfg.stream = s;
-        cudaLaunchAttribute attr[1];
+        cudaLaunchAttribute attr[2];
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = 2;
         attr[0].val.clusterDim.y = 1;
         attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
-        cfg.numAttrs = 1;
+        cfg.numAttrs = 2;
         if (cudaLaunchKernelEx(&cfg, score_kernel, tc, tq, p) != cudaSuccess) return HS_ERR_CUDA;
     }
     SelectParams p{};
