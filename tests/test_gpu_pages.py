@@ -509,6 +509,30 @@ def test_attention_over_lists(dtype, B, T, H, N, ctx):
     c.close()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("B,T,H", [(30, 1, 16), (12, 2, 128), (21, 3, 40)])
+def test_attention_of_medium_batches(dtype, B, T, H):
+    """As many lists as leave two splits each: joined inside the clusters. Requests of
+    one page leave a split without any; some rows lie past the last 128-row tile."""
+    lens = [1500 - 47 * b if b % 5 else (1, 64, 70, 0, T)[b % 4] for b in range(B)]
+    c = Cache(dtype, lens, max_ctx=1536)
+    q = normal(80, B, T, H, P.DIM)
+    out, lse = attend(c, q, None)
+    check(c, q, out, lse, lambda b, t: None)
+    rng = np.random.default_rng(81)
+    own = np.full((B, T, 20), -1, np.int32)
+    for b in range(B):
+        n = -(-lens[b] // 64)
+        for t in range(T):
+            k = rng.integers(0, min(n, 20) + 1)
+            own[b, t, :k] = np.sort(rng.permutation(n)[:k])
+    out, lse = attend(c, q, torch.from_numpy(own).cuda(), per_token=True)
+    check(c, q, out, lse, lambda b, t: [p for p in own[b, t] if p >= 0])
+    again = attend(c, q, torch.from_numpy(own).cuda(), per_token=True)
+    assert torch.equal(out.view(torch.int16), again[0].view(torch.int16)) and torch.equal(lse, again[1])
+    c.close()
+
+
 @pytest.mark.parametrize("factor,scale", [(8.0, SCALE), (32.0, SCALE), (2.0 ** -20, SCALE * 2.0 ** 20), (0.0, SCALE)])
 def test_attention_peaked_and_flat(factor, scale):
     for dtype in ("bf16", "fp8"):

@@ -6,8 +6,8 @@
 // 64 columns with no per-row ids. Per step, two pages (128 keys):
 //   S[128 x 128] = Q[128 x 576] K^T,  O[128 x 512] += P V,  V = K[:, 0:512].
 //
-// Work unit: (list, 128 query rows, split of the list), run by a cluster of two
-// CTAs whose tensor cores work as one (cta_group::2): CTA r holds the query rows
+// Work unit: (list, 128 query rows, split of the list), run by a pair of CTAs of a
+// cluster whose tensor cores work as one (cta_group::2): CTA r holds the query rows
 // [64 r, 64 r + 64) with their S (64 TMEM columns), O (256) and six of the nine
 // 64-column chunks of Q (192; the other three stay in shared memory), and no
 // score leaves its CTA. With M = 128 over two CTAs the accumulator of CTA r has
@@ -69,6 +69,7 @@ constexpr int NK = 9, NVC = 4;    // K chunks of a page; V chunks of a page in t
 constexpr int NQT = 6;            // chunks of Q in tensor memory
 constexpr int NTI = 3;            // steps whose page numbers and scales are held
 constexpr int NSW = 8;             // softmax warps
+constexpr uint32_t JOIN_BYTES = RM * 256 * 4 + RM * 4;  // half the columns of a partial, and its lse
 constexpr float TAU2 = 8.f;       // rescale threshold, log2 units: P <= 2^8
 constexpr uint32_t TM_O = 0, TM_S = 256, TM_Q = 320;
 
@@ -77,13 +78,15 @@ struct PCfg {
     static constexpr int THREADS = 128 + 32 * NSW + (FP8 ? 256 : 0);
     static constexpr int NV = 2;              // V's buffers: two steps; FP8: the two halves of one step's columns
     static constexpr int NXS = FP8 ? 6 : 7;   // slots of K chunks
-    static constexpr int GK = FP8 ? 3 : 1;    // K chunks per barrier (converted together)
+    // K chunks per barrier. FP8: three, converted together; BF16: the rope chunk
+    // by itself, then the value chunks in twos (fewer waits and copies to issue)
+    static constexpr int GK = FP8 ? 3 : 2;
     static constexpr int GV = 4;              // FP8: V chunks converted together (half the columns)
-    static constexpr int NXG = NXS / GK;      // groups of K chunks
+    static constexpr int NXG = FP8 ? NXS / GK : 1 + NXS / 2;  // groups of K chunks; BF16: group 0 is the rope's
     static constexpr int NCK = FP8 ? 3 : 0;   // groups of K codes
     static constexpr int NCV = FP8 ? 2 : 0;   // groups of V codes
     static constexpr int NC = NCK + NCV;
-    static constexpr int RK = FP8 ? NCK : NXG, RV = FP8 ? NCV : NV;  // the producers' rings
+    static constexpr int RK = FP8 ? NCK : NXG - 1, RV = FP8 ? NCV : NV;  // the producers' rings
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_P = OFF_Q + (NK - NQT) * CH;  // [2 pages] rows x keys
     static constexpr int OFF_V = OFF_P + 2 * CH;           // [steps][2 pages][NVC]
@@ -96,17 +99,24 @@ struct PCfg {
     static constexpr int OFF_NEG = OFF_PG + NTI * 8;                      // int32 [NTI] some scale is negative
     static constexpr int OFF_BAR = (OFF_NEG + NTI * 4 + 7) & ~7;
     static constexpr int B_QFULL = 0, B_QDONE = 1, B_QREADY = 2, B_SFULL = 3, B_SFREE = 4, B_PFULL = 5,
-                         B_PVDONE = 6, B_DRAIN = 7, B_TFULL = 8, B_TFREE = B_TFULL + NTI,
+                         B_PVDONE = 6, B_DRAIN = 7, B_JOIN = 8, B_TFULL = 9, B_TFREE = B_TFULL + NTI,
                          B_TREADY = B_TFREE + NTI, B_VFULL = B_TREADY + NTI, B_VFREE = B_VFULL + NV, B_XFULL = B_VFREE + NV,
                          B_XFREE = B_XFULL + NXG, B_CFULL = B_XFREE + NXG, B_CFREE = B_CFULL + NC,
                          NBAR = B_CFREE + NC;
     static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;  // TMEM base, abort flag, steps, first entry, end, Q's power
     static constexpr int SMEM = OFF_MISC + 32;
     static constexpr int SMEM_ALLOC = SMEM + 1024;
+    // where box i (32 columns, 64 rows, 8 KB) of the other split's partial lands:
+    // behind the own one, and where Q was
+    static constexpr int NJB = FP8 ? 6 : 7;
+    __device__ static int join_box(int i) {
+        return i < NJB ? OFF_V + RM * 512 * 4 + i * 8192 : OFF_Q + (i - NJB) * 8192;
+    }
     static constexpr int OFF_QST = OFF_V + (FP8 ? 0 : 1) * 2 * NVC * CH;  // Q is staged in the last V stage
     static_assert(OFF_BAR % 8 == 0 && OFF_SC % 16 == 0, "alignment");
     static_assert(NQT * CH <= 2 * NVC * CH, "staging of Q");
     static_assert(OFF_SC - OFF_V >= RM * 512 * 4, "staging of O");
+    static_assert(OFF_SC - OFF_V >= RM * 512 * 4 + NJB * 8192 && (8 - NJB) * 8192 <= OFF_P - OFF_Q, "the other split's partial");
     static_assert(SMEM_ALLOC <= 232448, "shared memory");
 };
 
@@ -116,13 +126,21 @@ struct PageParams {
     const int2 *table;
     const uint64_t *tree;  // [B][T] or null
     const float *scales;   // FP8: the pool's row scales
+    __nv_bfloat16 *out;    // written here when the splits are joined inside the cluster
     float *lse, *ws_lse;
     uint32_t *err;
+    int inside;            // 2: the two splits are joined inside the cluster; or 0
     int T, H, N, M, lists, nsplit, max_req, max_pages, zero_block;
     int tpl;               // lists per request: list i is token i % tpl of request i / tpl
     float scale_log2;
 };
 
+// This CTA's shared memory to another CTA's, completing on a barrier there.
+__device__ __forceinline__ void bulk_push(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "r"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -205,54 +223,46 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *smem = smem_raw + (base - raw);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const int rank = static_cast<int>(hs::cluster_ctarank());
+    // a cluster is one pair of CTAs, or both splits' pairs
+    const uint32_t crank = hs::cluster_ctarank(), pair0 = crank & ~1u;
+    const int rank = static_cast<int>(crank & 1u);
     const int split = blockIdx.x >> 1, mt = blockIdx.y, list = blockIdx.z;
     volatile int32_t *misc = reinterpret_cast<volatile int32_t *>(smem + C::OFF_MISC);
     volatile int32_t *ring_pg = reinterpret_cast<volatile int32_t *>(smem + C::OFF_PG);
     auto bar = [&](int i) { return base + C::OFF_BAR + 8u * (uint32_t)i; };
-    // the same barrier in CTA 0, whose warp 1 issues the MMAs
-    const uint32_t lead0 = hs::dsmem_map(smem + C::OFF_BAR, 0);
+    // the same barrier in the pair's CTA 0, whose warp 1 issues the MMAs
+    const uint32_t lead0 = hs::dsmem_map(smem + C::OFF_BAR, pair0);
+    const uint16_t both = (uint16_t)(3u << pair0);
     auto lead = [&](int i) { return lead0 + 8u * (uint32_t)i; };
     auto fail = [&]() {
         misc[1] = 1;
         atomicOr(p.err, HS_DEVERR_TIMEOUT);
     };
 
-    if (threadIdx.x == 32) {
-        mbar_init(bar(C::B_QFULL), 1);
-        mbar_init(bar(C::B_QDONE), NSW);
-        mbar_init(bar(C::B_QREADY), 2 * NSW);  // both CTAs' softmax warps
-        mbar_init(bar(C::B_SFULL), 1);
-        mbar_init(bar(C::B_SFREE), 2 * NSW);
-        mbar_init(bar(C::B_PFULL), 2 * NSW);
-        mbar_init(bar(C::B_PVDONE), 1);
-        mbar_init(bar(C::B_DRAIN), 1);
-        for (int i = 0; i < NTI; ++i) {
-            mbar_init(bar(C::B_TFULL + i), 1);
-            mbar_init(bar(C::B_TFREE + i), NSW);
-            mbar_init(bar(C::B_TREADY + i), 1);
+    if (warp == 1) {
+        for (int i = lane; i < C::NBAR; i += 32) {
+            uint32_t n = 1;
+            if (i == C::B_QDONE || (i >= C::B_TFREE && i < C::B_TFREE + NTI)) n = NSW;
+            // both CTAs' softmax warps
+            if (i == C::B_QREADY || i == C::B_SFREE || i == C::B_PFULL) n = 2 * NSW;
+            // FP8: four converter warps of each CTA
+            if (FP8 && ((i >= C::B_VFULL && i < C::B_VFREE) || (i >= C::B_XFULL && i < C::B_XFREE))) n = 8;
+            if (FP8 && i >= C::B_CFREE) n = 4;
+            mbar_init(bar(i), n);
         }
-        for (int i = 0; i < C::NV; ++i) {
-            mbar_init(bar(C::B_VFULL + i), FP8 ? 8 : 1);  // FP8: four converter warps of each CTA
-            mbar_init(bar(C::B_VFREE + i), 1);
-        }
-        for (int i = 0; i < C::NXG; ++i) {
-            mbar_init(bar(C::B_XFULL + i), FP8 ? 8 : 1);  // FP8: four converter warps of each CTA
-            mbar_init(bar(C::B_XFREE + i), 1);
-        }
-        for (int i = 0; i < C::NC; ++i) {
-            mbar_init(bar(C::B_CFULL + i), 1);
-            mbar_init(bar(C::B_CFREE + i), 4);
-        }
-        misc[1] = 0;
+        if (lane == 0) misc[1] = 0;
         fence_mbar_init();
         fence_proxy_async();
+        __syncwarp();
         grid_dep_wait();
-        // Q by TMA at once: its barrier is this CTA's own
-        mbar_expect_tx(bar(C::B_QFULL), NK * CH);
-        for (int i = 0; i < NK; ++i)
-            tma_load_3d(i < NQT ? base + C::OFF_QST + i * CH : base + C::OFF_Q + (i - NQT) * CH, &tm_q, 64 * i,
-                        mt * BM + RM * rank, list, bar(C::B_QFULL));
+        if (lane == 0) {  // Q by TMA at once: its barrier is this CTA's own
+            if (p.inside) mbar_expect_tx(bar(C::B_JOIN), JOIN_BYTES);
+            mbar_expect_tx(bar(C::B_QFULL), NK * CH);
+            for (int i = 0; i < NK; ++i)
+                tma_load_3d(i < NQT ? base + C::OFF_QST + i * CH : base + C::OFF_Q + (i - NQT) * CH, &tm_q, 64 * i,
+                            mt * BM + RM * rank, list, bar(C::B_QFULL));
+        }
+        __syncwarp();
     }
     if (warp == 2) tmem_alloc2(base + C::OFF_MISC, 512);
     // What the earlier kernels of the stream wrote is read from here on: this grid
@@ -331,7 +341,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         // blocks itself, 32 entries at a time, ahead of their use.
         const bool kw = warp == 0;
         int pg, blk;
-        int ul = 0, ut = 0;  // loads and steps begun
+        int ul = 0, ut = 0, ux = 0;  // loads, steps and (BF16) rope loads begun
         bool ok = true;
         for (int j = 0; j < nsteps && ok; ++j) {
             if (j % 16 == 0) {
@@ -359,20 +369,28 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     }
                     ut = j + 1;
                 }
-                for (int i = 0; i < NK && ok; i += C::GK, ++ul) {
-                    const int s = ul % C::RK;
-                    const uint32_t ph = ((uint32_t)(ul / C::RK) & 1u) ^ 1u;
-                    if (FP8) {
-                        ok = mbar_wait_inline(bar(C::B_CFREE + s), ph);
+                if (FP8) {
+                    for (int i = 0; i < NK && ok; i += C::GK, ++ul) {
+                        const int s = ul % C::RK;
+                        ok = mbar_wait_inline(bar(C::B_CFREE + s), ((uint32_t)(ul / C::RK) & 1u) ^ 1u);
                         if (!ok) break;
                         mbar_expect_tx(bar(C::B_CFULL + s), C::GK * CCH);
                         tma_load_3d(base + C::OFF_C + s * C::GK * CCH, &tm_k1, 0, own, i, bar(C::B_CFULL + s));
-                    } else {
-                        ok = mbar_wait_inline(bar(C::B_XFREE + s), ph);
+                    }
+                } else {
+                    // both CTAs' bytes complete on CTA 0's barrier
+                    if (ok) ok = mbar_wait_inline(bar(C::B_XFREE), ((uint32_t)j & 1u) ^ 1u);
+                    if (ok) {
+                        if (rank == 0) mbar_expect_tx(bar(C::B_XFULL), 2 * CH);
+                        tma_load_pair(base + C::OFF_X, &tm_k1, 0, own, 8, lead(C::B_XFULL));
+                        ux = j + 1;
+                    }
+                    for (int i = 0; i < 8 && ok; i += 2, ++ul) {
+                        const int s = 1 + ul % C::RK;
+                        ok = mbar_wait_inline(bar(C::B_XFREE + s), ((uint32_t)(ul / C::RK) & 1u) ^ 1u);
                         if (!ok) break;
-                        // both CTAs' bytes complete on CTA 0's barrier
-                        if (rank == 0) mbar_expect_tx(bar(C::B_XFULL + s), 2 * CH);
-                        tma_load_pair(base + C::OFF_X + s * CH, &tm_k1, 0, own, i, lead(C::B_XFULL + s));
+                        if (rank == 0) mbar_expect_tx(bar(C::B_XFULL + s), 4 * CH);
+                        tma_load_pair(base + C::OFF_X + (2 * s - 1) * CH, &tm_k2, 0, own, i, lead(C::B_XFULL + s));
                     }
                 }
             } else if (lane == 0) {
@@ -409,9 +427,10 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (!ok) {
                 fail();
                 const int ring = kw ? C::RK : C::RV;
-                const int b0 = FP8 ? (kw ? C::B_CFULL : C::B_CFULL + C::NCK) : (kw ? C::B_XFULL : C::B_VFULL);
+                const int b0 = FP8 ? (kw ? C::B_CFULL : C::B_CFULL + C::NCK) : (kw ? C::B_XFULL + 1 : C::B_VFULL);
                 for (int i = ul - 1; (FP8 || !kw || rank == 0) && i >= 0 && i >= ul - ring; --i)
                     mbar_wait_inline(bar(b0 + i % ring), (uint32_t)(i / ring) & 1u);
+                if (!FP8 && kw && rank == 0 && ux > 0) mbar_wait_inline(bar(C::B_XFULL), (uint32_t)(ux - 1) & 1u);
                 for (int i = ut - 1; FP8 && kw && i >= 0 && i >= ut - NTI; --i)
                     mbar_wait_inline(bar(C::B_TFULL + i % NTI), (uint32_t)(i / NTI) & 1u);
             }
@@ -451,9 +470,9 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                                 mma2_ss(tmem + TM_O + 128u * nh, a + ((pgi * CH + 32 * k) >> 4),
                                         v + ((pgi * NVC * CH + nh * 2 * CH + 2048 * k) >> 4), hi, ID_PV,
                                         (j | pgi | k) != 0);
-                        if (FP8) commit_both(bar(C::B_VFREE + nh));
-                        if (!FP8 && nh == 1) commit_both(bar(C::B_VFREE + j % C::NV));
-                        if (nh == 1) commit_both(bar(C::B_PVDONE));
+                        if (FP8) commit_both(bar(C::B_VFREE + nh), both);
+                        if (!FP8 && nh == 1) commit_both(bar(C::B_VFREE + j % C::NV), both);
+                        if (nh == 1) commit_both(bar(C::B_PVDONE), both);
                     }
                     __syncwarp();
                 }
@@ -464,33 +483,47 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             for (int j = 0; j < nsteps && ok; ++j) {
                 if (j > 0) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_SFREE), (uint32_t)(j - 1) & 1u));
                 tc_fence_after();
+                auto qk = [&](int c, uint32_t slot, bool fresh) {  // one chunk: four MMAs
+                    const uint32_t kd = klo + ((C::OFF_X + slot * CH) >> 4);
 #pragma unroll
-                for (int c = 0; c < NK; ++c) {
-                    const int g = c % C::GK;  // the chunk within its barrier's group
-                    if (g == 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_XFULL + s), ph));
+                    for (int k = 0; k < 4; ++k) {
+                        if (c < NQT)
+                            mma2_ts(tmem + TM_S, tmem + TM_Q + 32u * c + 8u * k, kd + 2 * k, hi, ID_QK, !(fresh && k == 0));
+                        else
+                            mma2_ss(tmem + TM_S, klo + ((C::OFF_Q + (c - NQT) * CH + 32 * k) >> 4), kd + 2 * k, hi, ID_QK,
+                                    !(fresh && k == 0));
+                    }
+                };
+                if (!FP8) {
+                    if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_XFULL), (uint32_t)j & 1u));
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (leader) {
+                        qk(8, 0, true);
+                        commit_both(bar(C::B_XFREE), both);
+                    }
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int c = 0; c < (FP8 ? NK : 8); c += C::GK) {
+                    const int b0 = (FP8 ? 0 : 1) + s;
+                    if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_XFULL + b0), ph));
                     if (ok) {
-                        if (g == 0) tc_fence_after();
-                        const uint32_t kd = klo + ((C::OFF_X + (s * C::GK + g) * CH) >> 4);
+                        tc_fence_after();
                         if (leader) {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                if (c < NQT)
-                                    mma2_ts(tmem + TM_S, tmem + TM_Q + 32u * c + 8u * k, kd + 2 * k, hi, ID_QK, (c | k) != 0);
-                                else
-                                    mma2_ss(tmem + TM_S, klo + ((C::OFF_Q + (c - NQT) * CH + 32 * k) >> 4), kd + 2 * k, hi,
-                                            ID_QK, 1u);
-                            }
-                            if (g == C::GK - 1) commit_both(bar(C::B_XFREE + s));
+                            for (int g = 0; g < C::GK; ++g) qk(c + g, (FP8 ? s * C::GK : 1 + 2 * s) + g, FP8 && c + g == 0);
+                            commit_both(bar(C::B_XFREE + b0), both);
                         }
                         __syncwarp();
                     }
-                    if (g == C::GK - 1 && ++s == C::NXG) {
+                    if (++s == (FP8 ? C::NXG : C::NXG - 1)) {
                         s = 0;
                         ph ^= 1u;
                     }
                 }
                 if (!ok) break;
-                if (leader) commit_both(bar(C::B_SFULL));
+                if (leader) commit_both(bar(C::B_SFULL), both);
                 __syncwarp();
                 if (j > 0) pv(j - 1);
             }
@@ -711,18 +744,18 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 auto of_row = [&](int o) {
                     return fmaxf(fmaxf(xm[o + row], xm[o + row + 64]), fmaxf(xm[o + row + 128], xm[o + row + 192]));
                 };
-                const float both = of_row(0), pboth = FP8 ? of_row(32 * NSW) : 0.f;
+                const float tall = of_row(0), pall = FP8 ? of_row(32 * NSW) : 0.f;
                 named_bar_sync(1, 32 * NSW);  // read before the next writes
-                if (outgrown(both, m2)) {
-                    alpha = exp2f(m2 - both);  // 0 where the row had seen nothing
+                if (outgrown(tall, m2)) {
+                    alpha = exp2f(m2 - tall);  // 0 where the row had seen nothing
                     l *= alpha;
-                    m2 = both;
+                    m2 = tall;
                 }
                 if (FP8) {
                     alpha = 1.f;
-                    if (outgrown(pboth, mp)) {
-                        alpha = exp2f(mp - pboth);
-                        mp = pboth;
+                    if (outgrown(pall, mp)) {
+                        alpha = exp2f(mp - pall);
+                        mp = pall;
                     }
                 }
             }
@@ -819,6 +852,8 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             tc_fence_after();
         }
         if (!ok && lane == 0) fail();
+        __syncwarp();
+        if (p.inside) cluster_arrive_relaxed();  // what this warp needed of this CTA's memory is used
         // the row's sum over its four threads' keys
         xm[tid] = l;
         named_bar_sync(1, 32 * NSW);
@@ -869,7 +904,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0) {
+            if (lane == 0 && !p.inside) {
                 const int wide = one ? 64 : 32;
                 const int z = one ? list : split * p.lists + list;
                 const int c0 = 256 * hf + 128 * kh;
@@ -882,12 +917,36 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
             __syncwarp();
         }
-        if (vrow && kh == 0 && hf == 0) {
+        if (kh == 0 && hf == 0 && (vrow || p.inside)) {
             const float lse = (!ok || l == 0.f) ? -INFINITY : (m2 + __log2f(l)) * 0.69314718055994531f;
             if (one)
                 p.lse[(size_t)list * p.M + mg] = lse;
-            else
+            else if (!p.inside)
                 p.ws_lse[((size_t)split * p.lists + list) * p.M + mg] = lse;
+            else
+                reinterpret_cast<float *>(smem + C::OFF_P)[row] = lse;  // P is done with
+        }
+        if (p.inside) {
+            // The columns that the other split joins go there, with this split's lse, as
+            // soon as its CTA is done with the memory they land in: four boxes of this
+            // warp's 32 rows (what was not computed is sent too, and not used).
+            cluster_wait();
+            fence_proxy_async();
+            __syncwarp();
+            const uint32_t other = crank ^ 2u;
+            const int wr = wq & 1;
+            if (lane == 0) {
+                const uint32_t theirs = hs::dsmem_map(smem + C::OFF_BAR + 8 * C::B_JOIN, other);
+                if (hf != split) {
+#pragma unroll 1
+                    for (int i = 4 * kh; i < 4 * kh + 4; ++i)
+                        bulk_push(hs::dsmem_map(smem + C::join_box(i) + wr * 4096, other),
+                                  base + C::OFF_V + (uint32_t)(8 * hf + i) * 8192u + wr * 4096, 4096, theirs);
+                }
+                if (kh == 0 && hf == 0)
+                    bulk_push(hs::dsmem_map(smem + C::OFF_P + 1024 + wr * 128, other), base + C::OFF_P + wr * 128, 128, theirs);
+            }
+            __syncwarp();
         }
     } else if (FP8 && warp >= 4 + NSW) {
         // ------------------------------------------------------------ converters
@@ -965,6 +1024,50 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         if (!ok && lane == 0) fail();
     }
 
+    if (p.inside) {
+        // Each CTA joins half the columns of its rows, its own split's with the other's,
+        // w_s = exp(lse_s - max) / sum. No workspace is written or read and no second
+        // grid waits.
+        if (warp < 4 || warp >= 4 + NSW) {
+            __syncwarp();
+            cluster_arrive_relaxed();
+            cluster_wait();
+        }
+        bool ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_JOIN), 0));
+        __syncthreads();
+        if (!ok && lane == 0) fail();
+        const float *lses = reinterpret_cast<const float *>(smem + C::OFF_P);
+        float *wts = reinterpret_cast<float *>(smem + C::OFF_P + 2048);  // [rows]: own, the other's
+        if (threadIdx.x < RM) {
+            const int row = threadIdx.x, mg = mt * BM + RM * rank + row;
+            const float mine = lses[row], theirs = lses[256 + row];
+            const bool nan = mine != mine || theirs != theirs;
+            const float mx = fmaxf(mine, theirs);
+            const float wm = mine == -INFINITY ? 0.f : ex2((mine - mx) * 1.4426950408889634f);
+            const float wt = theirs == -INFINITY ? 0.f : ex2((theirs - mx) * 1.4426950408889634f);
+            const float sum = wm + wt;
+            const float inv = nan ? __uint_as_float(0x7fc00000u) : (sum > 0.f ? __fdividef(1.f, sum) : 0.f);
+            wts[2 * row] = wm * inv;
+            wts[2 * row + 1] = wt * inv;
+            if (split == 0 && mg < p.M)
+                p.lse[(size_t)list * p.M + mg] = nan ? inv : (sum > 0.f ? mx + __logf(sum) : -INFINITY);
+        }
+        __syncthreads();
+#pragma unroll 2
+        for (int i = threadIdx.x; i < RM * 64; i += C::THREADS) {  // four columns each
+            const int row = i >> 6, box = (i >> 3) & 7, mg = mt * BM + RM * rank + row;
+            if (mg >= p.M) continue;
+            const uint32_t at = (uint32_t)((row >> 5) * 4096 + (row & 31) * 128 + (((i & 7) ^ (row & 7)) << 4));
+            const float wm = wts[2 * row], wt = wts[2 * row + 1];
+            float4 m = make_float4(0.f, 0.f, 0.f, 0.f), t = m;
+            // a weight of 0: that split saw nothing and wrote nothing, or does not count
+            if (wm != 0.f) m = ld_shared_f4(base + C::OFF_V + (8 * split + box) * 8192 + at);
+            if (wt != 0.f) t = ld_shared_f4(base + C::join_box(box) + at);
+            *reinterpret_cast<uint2 *>(p.out + ((size_t)list * p.M + mg) * 512 + 256 * split + 4 * (i & 63)) =
+                make_uint2(pack_bf16(m.x * wm + t.x * wt, m.y * wm + t.y * wt),
+                           pack_bf16(m.z * wm + t.z * wt, m.w * wm + t.w * wt));
+        }
+    }
     tc_fence_before();
     __syncthreads();
     cluster_sync_relaxed();  // no CTA leaves while the other's MMAs or arrivals may reach it
@@ -1087,26 +1190,31 @@ join_many_kernel(const float *__restrict__ ws_o, const float *__restrict__ ws_ls
 // ---------------------------------------------------------------- host side
 struct PagePlan {
     int M, mtiles, nsplit;
+    double us;  // the model's time
     size_t ws_o_bytes, ws_bytes;
 };
 
-// Splits of a list of N pages: the count that a model of the launch makes
-// shortest. Two pages take a pair of CTAs about 1.6 us, their start and epilogue
-// 6 us, a second launch 2 us and the partials' write and read about 5 MB per us.
+// A model of the launch's time, in us: two pages take a pair of CTAs about 1.9,
+// their start and epilogue 6.5.
+constexpr double US_STEP = 1.9, US_ENDS = 6.5;
+
+// Splits of a list of N pages joined through the workspace by a second grid: the
+// count that the model makes shortest; the join is 3.5 us and about 5 MB of
+// partials written and read per us.
 PagePlan page_plan(int64_t lists, int64_t T, int64_t H, int64_t N) {
     PagePlan pl{};
     pl.M = (int)(T * H);
     pl.mtiles = (pl.M + BM - 1) / BM;
     const int64_t sms = sm_count(), units = lists * pl.mtiles * 2;
     const int64_t steps = (N + 1) / 2, most = steps < 128 ? steps : 128;
-    double best = 1e300;
+    pl.us = 1e300;
     pl.nsplit = 1;
     for (int64_t ns = 1; ns <= most; ++ns) {
         const double waves = (double)((units * ns + sms - 1) / sms);
-        double t = waves * ((double)((steps + ns - 1) / ns) * 1.6 + 6.0);
-        if (ns > 1) t += 2.0 + (double)ns * lists * pl.M * 512 * 8 / 5e6;
-        if (t < best * 0.98) {
-            best = t;
+        double t = waves * ((double)((steps + ns - 1) / ns) * US_STEP + US_ENDS);
+        if (ns > 1) t += 3.5 + (double)ns * lists * pl.M * 512 * 8 / 5e6;
+        if (t < pl.us * 0.98) {
+            pl.us = t;
             pl.nsplit = (int)ns;
         }
         if (units * ns > 8 * sms) break;
@@ -1134,9 +1242,35 @@ bool make_page_map(CUtensorMap *m, bool fp8, const void *rows, uint64_t n_rows, 
               CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// How many clusters of two pairs of CTAs the device holds at once.
 template <bool FP8>
-hs_status launch_pages(dim3 grid, int dev, cudaStream_t s, const CUtensorMap &tq, const CUtensorMap &k1,
-                       const CUtensorMap &k2, const CUtensorMap &to, const PageParams &p) {
+int clusters_of_four(int dev) {
+    static std::atomic<int> cached[64];
+    int n = cached[dev].load(std::memory_order_acquire);
+    if (n == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(4, 1, 1024);
+        cfg.blockDim = dim3(PCfg<FP8>::THREADS, 1, 1);
+        cfg.dynamicSmemBytes = PCfg<FP8>::SMEM_ALLOC;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 4;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, page_decode_kernel<FP8>, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            n = 0;
+        }
+        n = n > 0 ? n : -1;
+        cached[dev].store(n, std::memory_order_release);
+    }
+    return n;
+}
+
+template <bool FP8>
+hs_status launch_pages(int dev, cudaStream_t s, const CUtensorMap &tq, const CUtensorMap &k1,
+                       const CUtensorMap &k2, const void *d_out, void *ws, const PagePlan &pl, PageParams p) {
     static std::atomic<int> state[64];
     if (dev < 0 || dev >= 64) return HS_ERR_UNSUPPORTED;
     if (state[dev].load(std::memory_order_acquire) != 1) {
@@ -1144,21 +1278,53 @@ hs_status launch_pages(dim3 grid, int dev, cudaStream_t s, const CUtensorMap &tq
                                          PCfg<FP8>::SMEM_ALLOC));
         state[dev].store(1, std::memory_order_release);
     }
+    // Two splits joined inside a cluster, where all clusters run at once and the model
+    // says so: 1.5 us instead of the second grid's 3.5 and the partials' bytes
+    // (32 lists of 2,048 rows: INSIDE against 32.0 us). Four splits in a cluster of
+    // eight CTAs were slower than eight splits and the second grid.
+    if (pl.nsplit > 1) {
+        const int64_t steps = ((p.N < 1 ? p.max_pages : p.N) + 1) / 2, units = (int64_t)p.lists * pl.mtiles;
+        const double t = (double)((steps + 1) / 2) * US_STEP + US_ENDS + 1.5;
+        if (steps >= 2 && t < pl.us && units <= clusters_of_four<FP8>(dev)) p.inside = p.nsplit = 2;
+    }
+    const bool one = p.nsplit == 1;
+    // the output (one split), or the splits' f32 partials
+    CUtensorMap to;
+    if (!make_map(&to, one ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                  one || p.inside ? d_out : ws, 512, pl.M, (uint64_t)p.lists * (one || p.inside ? 1 : p.nsplit),
+                  one ? 1024 : 2048, one ? 64 : 32, 32, CU_TENSOR_MAP_SWIZZLE_128B))
+        return HS_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
+    cfg.gridDim = dim3(2 * p.nsplit, pl.mtiles, (unsigned)p.lists);
     cfg.blockDim = dim3(PCfg<FP8>::THREADS, 1, 1);
     cfg.dynamicSmemBytes = PCfg<FP8>::SMEM_ALLOC;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.x = p.inside ? 2 * p.inside : 2;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, page_decode_kernel<FP8>, tq, k1, k2, to, p) == cudaSuccess ? HS_OK : HS_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, page_decode_kernel<FP8>, tq, k1, k2, to, p) != cudaSuccess) return HS_ERR_CUDA;
+    if (one || p.inside) return HS_OK;
+    const int n = p.lists * pl.M;
+    const bool few = pl.nsplit <= FEW;
+    cudaLaunchConfig_t cc = {};
+    cc.gridDim = dim3((unsigned)(few ? ((int64_t)n * 128 + 255) / 256 : n), 1, 1);
+    cc.blockDim = dim3(few ? 256 : 128 * JG, 1, 1);
+    cc.stream = s;
+    cudaLaunchAttribute ca[1];
+    ca[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    ca[0].val.programmaticStreamSerializationAllowed = 1;
+    cc.attrs = ca;
+    cc.numAttrs = 1;
+    return cudaLaunchKernelEx(&cc, few ? join_few_kernel : join_many_kernel, (const float *)ws, (const float *)p.ws_lse,
+                              pl.nsplit, n, p.out, p.lse) == cudaSuccess
+               ? HS_OK
+               : HS_ERR_CUDA;
 }
 
 // `lists` lists of T query tokens each; tpl > 1 (with T = 1): lists / tpl
@@ -1183,7 +1349,7 @@ hs_status page_entry(hs_pool_t pool, int64_t lists, int32_t T, int32_t tpl, int3
     if (pl.nsplit > 1 && (!d_workspace || ws_bytes < pl.ws_bytes || ((uintptr_t)d_workspace & 255u)))
         return HS_ERR_INVALID_ARG;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    CUtensorMap tq, to;
+    CUtensorMap tq;
     const uint64_t rows = (uint64_t)(pool->cfg.n_gpu_blocks + 1) * kPage;
     if (!make_map(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d_q, kDim, pl.M, lists, 2 * kDim, 64, RM,
                   CU_TENSOR_MAP_SWIZZLE_128B))
@@ -1197,12 +1363,6 @@ hs_status page_entry(hs_pool_t pool, int64_t lists, int32_t T, int32_t tpl, int3
             return HS_ERR_CUDA;
         pool->page_maps_made = true;
     }
-    // the output (one split), or the splits' f32 partials
-    const bool one = pl.nsplit == 1;
-    if (!make_map(&to, one ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
-                  one ? d_out : d_workspace, 512, pl.M, (uint64_t)lists * pl.nsplit, one ? 1024 : 2048, one ? 64 : 32,
-                  32, CU_TENSOR_MAP_SWIZZLE_128B))
-        return HS_ERR_CUDA;
     PageParams p{};
     p.pages = d_pages;
     p.req = d_req_ids;
@@ -1210,6 +1370,7 @@ hs_status page_entry(hs_pool_t pool, int64_t lists, int32_t T, int32_t tpl, int3
     p.table = reinterpret_cast<const int2 *>(pool->d_page);
     p.tree = d_tree;
     p.scales = pool->d_scales;
+    p.out = static_cast<__nv_bfloat16 *>(d_out);
     p.lse = d_lse;
     p.ws_lse = pl.nsplit > 1 ? reinterpret_cast<float *>(static_cast<uint8_t *>(d_workspace) + pl.ws_o_bytes)
                              : nullptr;
@@ -1225,26 +1386,8 @@ hs_status page_entry(hs_pool_t pool, int64_t lists, int32_t T, int32_t tpl, int3
     p.zero_block = (int)pool->cfg.n_gpu_blocks;
     p.tpl = tpl;
     p.scale_log2 = sm_scale * 1.4426950408889634f;
-    const dim3 grid(2 * pl.nsplit, pl.mtiles, (unsigned)lists);
-    const hs_status st = fp8 ? launch_pages<true>(grid, dev, s, tq, maps[0], maps[1], to, p)
-                             : launch_pages<false>(grid, dev, s, tq, maps[0], maps[1], to, p);
-    if (st != HS_OK || pl.nsplit == 1) return st;
-    const int n = (int)(lists * pl.M);
-    const bool few = pl.nsplit <= FEW;
-    cudaLaunchConfig_t cc = {};
-    cc.gridDim = dim3((unsigned)(few ? ((int64_t)n * 128 + 255) / 256 : n), 1, 1);
-    cc.blockDim = dim3(few ? 256 : 128 * JG, 1, 1);
-    cc.stream = s;
-    cudaLaunchAttribute ca[1];
-    ca[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    ca[0].val.programmaticStreamSerializationAllowed = 1;
-    cc.attrs = ca;
-    cc.numAttrs = 1;
-    return cudaLaunchKernelEx(&cc, few ? join_few_kernel : join_many_kernel, (const float *)d_workspace,
-                              (const float *)p.ws_lse, pl.nsplit, n, static_cast<__nv_bfloat16 *>(d_out),
-                              d_lse) == cudaSuccess
-               ? HS_OK
-               : HS_ERR_CUDA;
+    return fp8 ? launch_pages<true>(dev, s, tq, maps[0], maps[1], d_out, d_workspace, pl, p)
+               : launch_pages<false>(dev, s, tq, maps[0], maps[1], d_out, d_workspace, pl, p);
 }
 
 }  // namespace

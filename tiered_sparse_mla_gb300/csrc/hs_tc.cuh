@@ -404,12 +404,13 @@ __device__ __forceinline__ void tmem_alloc2(uint32_t dst_smem, uint32_t ncols) {
 __device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t ncols) {
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
-// Arrives on the barrier at this offset in both CTAs once every MMA issued so far is done.
-__device__ __forceinline__ void commit_both(uint32_t bar) {
+// Arrives on the barrier at this offset in both CTAs of a pair (a mask of cluster
+// ranks) once every MMA issued so far is done.
+__device__ __forceinline__ void commit_both(uint32_t bar, uint16_t mask = 3) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
             bar),
-        "h"((uint16_t)3)
+        "h"(mask)
         : "memory");
 }
 // One MMA; descriptors as two 32-bit halves (the high one is shared), A from
@@ -439,8 +440,13 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const void *tmap, in
         : "memory");
 }
 // All threads of both CTAs have come here; orders no memory by itself.
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync_relaxed() {
-    asm volatile("barrier.cluster.arrive.relaxed.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_arrive_relaxed();
+    cluster_wait();
 }
 __device__ __forceinline__ uint32_t elect_one() {
     uint32_t p;
