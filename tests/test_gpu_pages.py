@@ -356,6 +356,27 @@ def test_select(B, T, H, ctx, N):
     c.close()
 
 
+@pytest.mark.parametrize("B,T,H,long", [(350, 1, 300, 40000), (60, 3, 128, 60000), (33, 2, 16, 20000)])
+def test_select_many_requests(B, T, H, long):
+    """Lists of many lengths laid end to end: empty requests, one page, several tiles of
+    pages, the same request more than once, unknown ones in between."""
+    g = torch.Generator().manual_seed(B)
+    lens = [0, 1, 64, long, long - 12345] + torch.randint(1, 3000, (15,), generator=g).tolist()
+    c = sparse_cache(lens)
+    means = normal(15, c.R, c.P, P.DIM)
+    for r, n in enumerate(lens):
+        means[r, -(-n // 64):] = math.nan
+    q = normal(16, B, T, H, P.DIM)
+    req = torch.randint(-2, c.R + 3, (B,), generator=g).tolist()
+    pages = run_select(c, q, means, 5, req=i32(*req))
+    for b, r in enumerate(req):
+        if 0 <= r < c.R:
+            check_select(c, q[b:b + 1], means, pages[b:b + 1], 1, 2, req=[r])
+        else:
+            assert bool((pages[b] == -1).all())
+    c.close(c.hs.HS_DEVERR_BAD_REQUEST)
+
+
 def test_select_ties_and_near_ties():
     """Equal scores go to the lower page, and scores that differ by less than 32-bit
     sums can tell are told apart."""

@@ -30,17 +30,22 @@ __host__ __device__ __forceinline__ int pages_of(int tokens) {
 }
 
 // ---------------------------------------------------------------- scores
-// Work unit: (request, group of whole query tokens of at most 256 rows, range of
-// page tiles), run by two CTAs whose tensor cores work as one (cta_group::2,
-// M = 256, N up to 256): pages are the MMA's M rows, 128 per CTA, so that the
-// maximum over heads runs along the registers of the one thread that owns a page,
-// and query rows its N columns, half of them supplied by either CTA. The queries
-// stay in shared memory (144 KB a CTA) and the pages stream past once through a
-// ring of 16 KB chunks; the scores of one tile are reduced while the next is
-// multiplied (two accumulators). One MMA of 256 x 256 x 16 takes 128 clocks, so
-// 256 rows per pass need 4.6k clocks per tile of 256 pages and fewer rows are bound
-// by the pages' bytes. An earlier form, one CTA per 128 pages with the queries
-// streamed past each tile, moved 6x the pages' bytes from L2 and took 3x as long.
+// Work unit: a group of whole query tokens of at most 256 rows, the same tokens of
+// every request, and a range of the page tiles of all requests laid end to end, run
+// by two CTAs whose tensor cores work as one (cta_group::2, M = 256, N up to 256):
+// pages are the MMA's M rows, 128 per CTA, so that the maximum over heads runs along
+// the registers of the one thread that owns a page, and query rows its N columns,
+// half of them supplied by either CTA. The queries stay in shared memory (144 KB a
+// CTA) and the pages stream past once through a ring of 16 KB chunks; the scores of
+// one tile are reduced while the next is multiplied (two accumulators). Where a range
+// goes on to the next request, its queries take their places chunk by chunk behind the
+// last tile, so the MMAs hardly pause.
+// Bound: one MMA of 256 x 256 x 16 takes 128 clocks, so 256 rows per pass need 4.6k
+// clocks per tile of 256 pages; fewer rows are bound by the pages' bytes. 16 requests
+// of 16,384 pages with 512 query rows each (155 GFLOP, 302 MB): 99 us, 1.56 PFLOP/s.
+// Measured there: ranges cut at requests, which fill 64 of 76 pairs, 107 us; four ring
+// stages instead of five 105 us; one CTA per 128 pages with the queries streamed past
+// each tile, which moves 6x the pages' bytes from L2, about 300 us.
 //   warp 0      producer;  warp 1 (CTA 0) MMA issuer;
 //   warps 2-5   the pages' |c|^2, from the chunks as they land; their arrival is
 //               what the MMA issuer waits for;
@@ -51,11 +56,11 @@ constexpr int NCH = kDim / 64;   // depth chunks
 constexpr int ST = 320;
 constexpr int MAXN = 256;        // query rows per pass
 constexpr int HG = 8;            // heads per group
-constexpr int NST = 4;           // ring stages
+constexpr int NST = 5;           // ring stages
 constexpr int A_BYTES = 128 * 128;
 constexpr int OFF_RING = NCH * 128 * 128;
 constexpr int OFF_SBAR = OFF_RING + NST * A_BYTES;
-constexpr int SCORE_SMEM = OFF_SBAR + 256 + 1024;
+constexpr int SCORE_SMEM = OFF_SBAR + 384 + 1024;
 static_assert(SCORE_SMEM <= 232448, "shared memory");
 
 struct ScoreParams {
@@ -64,7 +69,7 @@ struct ScoreParams {
     uint32_t *s2;    // [B*T][Pp] best score of another group of heads (BF16, rounded up) << 16 | group
     float *cn, *cm;  // [B][Pp] |c_p|^2; [B][Pp / 32] the largest of 32 pages (infinite if one is not finite)
     uint32_t *err;
-    int T, H, tpg, groups, splits;  // tokens per group; groups of tokens; splits of the tiles
+    int B, T, H, tpg, groups, parts;  // tokens per group; groups of tokens; parts of the tiles
     int hpc, N;                     // heads per pass (H, or 256 at most); N: query rows of a pass, rounded up
     int Pp, max_req;
 };
@@ -78,36 +83,35 @@ score_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ C
     grid_dep_wait();
     grid_dep_launch();
     const int rank = static_cast<int>(hs::cluster_ctarank());
-    const int unit = blockIdx.x >> 1, split = unit % p.splits, g = (unit / p.splits) % p.groups;
-    const int b = unit / (p.splits * p.groups);
-    const int r = p.req[b];
-    if (r < 0 || r >= p.max_req) return;  // both CTAs alike
-    const int pages = pages_of(p.ctx[r]), tiles = (pages + SP - 1) / SP;
-    const int t_lo = (int)((long long)tiles * split / p.splits);
-    const int nt = (int)((long long)tiles * (split + 1) / p.splits) - t_lo;
-    if (nt == 0) return;
+    const int unit = blockIdx.x >> 1, g = unit % p.groups, part = unit / p.groups;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t raw = hs::smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *smem = smem_raw + (base - raw);
     volatile int32_t *misc = reinterpret_cast<volatile int32_t *>(smem + OFF_SBAR);
-    constexpr int B_QFULL = 0, B_QFREE = 1, B_FULL = 2, B_READY = B_FULL + NST, B_FREE = B_READY + NST,
+    volatile int32_t *sums = reinterpret_cast<volatile int32_t *>(smem + OFF_SBAR + 320);
+    constexpr int B_QFULL = 0, B_FULL = B_QFULL + NCH, B_READY = B_FULL + NST, B_FREE = B_READY + NST,
                   B_DFULL = B_FREE + NST, B_DFREE = B_DFULL + 2, B_DRAIN = B_DFREE + 2, NB = B_DRAIN + 1;
-    static_assert(16 + 8 * NB <= 256, "barriers");
-    auto bar = [&](int i) { return base + OFF_SBAR + 16u + 8u * (uint32_t)i; };
-    const uint32_t lead0 = hs::dsmem_map(smem + OFF_SBAR + 16, 0);
+    static_assert(32 + 8 * NB <= 320 && ST / 32 * 4 <= 64, "barriers and sums");
+    auto bar = [&](int i) { return base + OFF_SBAR + 32u + 8u * (uint32_t)i; };
+    const uint32_t lead0 = hs::dsmem_map(smem + OFF_SBAR + 32, 0);
     auto lead = [&](int i) { return lead0 + 8u * (uint32_t)i; };
-    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    // the pages of request b of the list, none if its index is out of range
+    auto pages_at = [&](int b, int &r) {
+        r = b < p.B ? p.req[b] : -1;
+        return r >= 0 && r < p.max_req ? pages_of(p.ctx[r]) : 0;
+    };
+    auto tiles_of = [](int pages) { return (pages + SP - 1) / SP; };
+
     const int passes = (p.H + p.hpc - 1) / p.hpc;  // one, unless a token has more than 256 heads
-    const int total = passes * nt;
     auto fail = [&]() {
         misc[1] = 1;
         atomicOr(p.err, HS_DEVERR_TIMEOUT);
     };
     uint32_t cols = 32;
     while ((int)cols < 2 * p.N) cols <<= 1;
-    if (threadIdx.x == 0) {
-        mbar_init(bar(B_QFULL), 1);
-        mbar_init(bar(B_QFREE), 1);
+    if (threadIdx.x == ST - 32) {  // a warp that finds no requests of its own below unless there are hundreds
+        for (int i = 0; i < NCH; ++i) mbar_init(bar(B_QFULL + i), 1);
         for (int i = 0; i < NST; ++i) {
             mbar_init(bar(B_FULL + i), 1);
             mbar_init(bar(B_READY + i), 8);
@@ -125,39 +129,140 @@ score_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ C
         prefetch_tmap(&tm_q);
     }
     if (warp == 1) tmem_alloc2(base + OFF_SBAR, cols);
+
+    // This pair's range of the requests' tiles, laid end to end, and where it begins.
+    const int per = (p.B + ST - 1) / ST;
+    int mine = 0, own_r = 0, own_pages = 0;
+#pragma unroll 1
+    for (int i = 0; i < per; ++i) {
+        own_pages = pages_at((int)threadIdx.x * per + i, own_r);
+        mine += tiles_of(own_pages);
+    }
+    int before = mine;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += x;
+    }
+    if (lane == 31) sums[warp] = before;
+    before -= mine;
     tc_fence_before();
+    __syncthreads();
+    int all = 0;
+#pragma unroll 1
+    for (int w = 0; w < ST / 32; ++w) {
+        const int x = sums[w];
+        before += w < warp ? x : 0;
+        all += x;
+    }
+    const int even = all / p.parts, odd = all - even * p.parts;
+    const int f0 = even * part + min(part, odd), f1 = f0 + even + (part < odd ? 1 : 0);
+    if (f0 == f1) {
+        if (threadIdx.x == 0) misc[2] = misc[3] = misc[4] = misc[5] = 0;
+    } else if (f0 >= before && f0 < before + mine) {
+        int i = 0, at = before;
+        if (per > 1) {
+            while (i < per - 1) {
+                const int n = tiles_of(pages_at((int)threadIdx.x * per + i, own_r));
+                if (f0 < at + n) break;
+                at += n;
+                ++i;
+            }
+            own_pages = pages_at((int)threadIdx.x * per + i, own_r);
+        }
+        misc[2] = (int)threadIdx.x * per + i;
+        misc[3] = f0 - at;
+        misc[4] = own_r;
+        misc[5] = own_pages;
+    }
     __syncthreads();
     cluster_sync_relaxed();
     tc_fence_after();
     const uint32_t tmem = static_cast<uint32_t>(misc[0]);
 
+    // The range's requests, one after the other: every warp walks them for itself.
+    struct Walk {
+        int b, r, pages, lo, n;  // request, its cache index and pages, first tile, tiles (0: no more)
+        int left;                // tiles of the range behind these
+    };
+    auto take = [&](Walk &w) {
+        const int have = tiles_of(w.pages) - w.lo;
+        w.n = min(w.left, have);
+        w.left -= w.n;
+    };
+    auto start = [&]() {
+        Walk w;
+        w.b = misc[2];
+        w.lo = misc[3];
+        w.r = misc[4];
+        w.pages = misc[5];
+        w.left = f1 - f0;
+        take(w);
+        return w;
+    };
+    auto next = [&](Walk &w) {
+        w.n = w.lo = 0;
+        if (w.left <= 0) return;
+        for (int b0 = w.b + 1; b0 < p.B; b0 += 32) {
+            int r;
+            const int pages = pages_at(b0 + lane, r);
+            const uint32_t some = __ballot_sync(0xffffffffu, pages > 0);
+            if (some) {
+                const int l = __ffs(some) - 1;
+                w.b = b0 + l;
+                w.r = __shfl_sync(0xffffffffu, r, l);
+                w.pages = __shfl_sync(0xffffffffu, pages, l);
+                take(w);
+                return;
+            }
+        }
+    };
+
     if (warp == 0) {
         // ------------------------------------------------------------ producer
-        if (lane == 0) {
-            int issued = 0;
-            bool ok = true;
-            for (int k = 0; k < passes && ok; ++k) {
-                // the queries of a pass: this CTA's half of the rows, all chunks
-                if (k > 0) ok = mbar_wait_inline(bar(B_QFREE), (uint32_t)(k - 1) & 1u);
-                if (!ok) break;
-                if (rank == 0) mbar_expect_tx(bar(B_QFULL), NCH * p.N * 128);
-                const int row = g * p.tpg * p.H + k * p.hpc + rank * (p.N / 2);
-                for (int c = 0; c < NCH; ++c)
-                    tma_load_pair(base + c * (p.N / 2) * 128, &tm_q, 64 * c, row, b, lead(B_QFULL));
-                for (int i = 0; i < nt && ok; ++i)
-                    for (int c = 0; c < NCH && ok; ++c, ++issued) {
-                        const int s = issued % NST;
-                        ok = mbar_wait_inline(bar(B_FREE + s), ((uint32_t)(issued / NST) & 1u) ^ 1u);
-                        if (!ok) break;
-                        mbar_expect_tx(bar(B_FULL + s), A_BYTES);
-                        tma_load_3d(base + OFF_RING + s * A_BYTES, &tm_c, 64 * c, (t_lo + i) * SP + 128 * rank, r,
-                                    bar(B_FULL + s));
-                    }
+        // Queries are loaded once for a request (and pass): chunk by chunk, each as
+        // soon as the last tile of the request before has used its place, which the
+        // ring's wait for a stage NST chunks later has shown.
+        Walk w = start();
+        uint32_t issued = 0, loads = 0;
+        bool ok = true;
+        while (w.n > 0 && ok) {
+            Walk nx = w;
+            next(nx);
+            for (int k = 0; k < passes && ok; ++k, ++loads) {
+                if (lane == 0) {
+                    const bool last = k == passes - 1;
+                    auto load_q = [&](int c, int pass, int b) {
+                        if (rank == 0) mbar_expect_tx(bar(B_QFULL + c), p.N * 128);
+                        tma_load_pair(base + c * (p.N / 2) * 128, &tm_q, 64 * c,
+                                      g * p.tpg * p.H + pass * p.hpc + rank * (p.N / 2), b, lead(B_QFULL + c));
+                    };
+                    for (int i = 0; i < w.n && ok; ++i)
+                        for (int c = 0; c < NCH && ok; ++c, ++issued) {
+                            const uint32_t s = issued % NST;
+                            ok = mbar_wait_inline(bar(B_FREE + s), ((issued / NST) & 1u) ^ 1u);
+                            if (!ok) break;
+                            if (i == 0 && loads == 0)
+                                load_q(c, k, w.b);
+                            else if (i == 0 && c < NST)
+                                load_q(c + NCH - NST, k, w.b);
+                            if (i == w.n - 1 && c >= NST && !(last && nx.n == 0))
+                                load_q(c - NST, last ? 0 : k + 1, last ? nx.b : w.b);
+                            mbar_expect_tx(bar(B_FULL + s), A_BYTES);
+                            tma_load_3d(base + OFF_RING + s * A_BYTES, &tm_c, 64 * c, (w.lo + i) * SP + 128 * rank,
+                                        w.r, bar(B_FULL + s));
+                        }
+                }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
             }
-            if (!ok) {
-                fail();
-                for (int u = issued - 1; u >= 0 && u >= issued - NST; --u)
-                    mbar_wait_inline(bar(B_FULL + u % NST), (uint32_t)(u / NST) & 1u);
+            w = nx;
+        }
+        if (!ok && lane == 0) {
+            // the queries' copies are older than the wait that gave up
+            fail();
+            for (uint32_t u = issued, n = 0; n < NST && u > 0; ++n) {
+                --u;
+                mbar_wait_inline(bar(B_FULL + u % NST), (u / NST) & 1u);
             }
         }
     } else if (warp == 1) {
@@ -169,33 +274,35 @@ score_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ C
             const uint32_t leader = elect_one();
             const uint32_t qch = (uint32_t)(p.N / 2) * 128u;
             bool ok = true;
-            int u = 0;
-            for (int i = 0; i < total && ok; ++i) {
-                if (i % nt == 0) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(B_QFULL), (uint32_t)(i / nt) & 1u));
-                if (ok && i >= 2)
-                    ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(B_DFREE + (i & 1)), ((uint32_t)(i >> 1) & 1u) ^ 1u));
-                if (!ok) break;
-                const uint32_t d = tmem + (uint32_t)((i & 1) * p.N);
-                for (int c = 0; c < NCH && ok; ++c, ++u) {
-                    const int s = u % NST;
-                    ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(B_READY + s), (uint32_t)(u / NST) & 1u));
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (leader) {
-                        const uint32_t a = lo + ((OFF_RING + s * A_BYTES) >> 4), q = lo + ((c * qch) >> 4);
+            uint32_t u = 0, i = 0, loads = 0;
+            for (Walk w = start(); w.n > 0 && ok; next(w))
+                for (int k = 0; k < passes && ok; ++k, ++loads)
+                    for (int j = 0; j < w.n && ok; ++j, ++i) {
+                        if (i >= 2)
+                            ok = __all_sync(0xffffffffu,
+                                            mbar_wait_inline(bar(B_DFREE + (i & 1)), ((i >> 1) & 1u) ^ 1u));
+                        if (!ok) break;
+                        const uint32_t d = tmem + (i & 1) * (uint32_t)p.N;
+                        for (int c = 0; c < NCH && ok; ++c, ++u) {
+                            const uint32_t s = u % NST;
+                            if (j == 0)
+                                ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(B_QFULL + c), loads & 1u));
+                            if (ok)
+                                ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(B_READY + s), (u / NST) & 1u));
+                            if (!ok) break;
+                            tc_fence_after();
+                            if (leader) {
+                                const uint32_t a = lo + ((OFF_RING + s * A_BYTES) >> 4), q = lo + ((c * qch) >> 4);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) mma2_ss(d, a + 2 * k, q + 2 * k, hi, idesc, (c | k) != 0);
-                        commit_both(bar(B_FREE + s));
+                                for (int e = 0; e < 4; ++e) mma2_ss(d, a + 2 * e, q + 2 * e, hi, idesc, (c | e) != 0);
+                                commit_both(bar(B_FREE + s));
+                            }
+                            __syncwarp();
+                        }
+                        if (!ok) break;
+                        if (leader) commit_both(bar(B_DFULL + (i & 1)));
+                        __syncwarp();
                     }
-                    __syncwarp();
-                }
-                if (!ok) break;
-                if (leader) {
-                    commit_both(bar(B_DFULL + (i & 1)));
-                    if (i % nt == nt - 1) commit_both(bar(B_QFREE));
-                }
-                __syncwarp();
-            }
             if (!ok && lane == 0) fail();
             if (leader) {
                 asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
@@ -208,15 +315,15 @@ score_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ C
     } else if (warp < 6) {
         // ------------------------------------------------------------ norms
         const int row = (warp - 2) * 32 + lane;
-        const bool first_group = g == 0;
         bool ok = true;
-        int u = 0;
-        for (int i = 0; i < total; ++i) {
+        uint32_t u = 0;
+        for (Walk w = start(); w.n > 0; next(w))
+        for (int i = 0; i < passes * w.n; ++i) {
             float n4[4] = {0.f, 0.f, 0.f, 0.f};
-            const bool need = first_group && i < nt;
+            const bool need = i < w.n && (w.lo + i) % p.groups == g;  // the groups share this work
             for (int c = 0; c < NCH; ++c, ++u) {
-                const int s = u % NST;
-                if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(B_FULL + s), (uint32_t)(u / NST) & 1u));
+                const uint32_t s = u % NST;
+                if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(B_FULL + s), (u / NST) & 1u));
                 if (ok && need) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
@@ -232,14 +339,14 @@ score_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ C
                 __syncwarp();
                 if (lane == 0) mbar_arrive_peer(lead(B_READY + s));
             }
-            const int page = (t_lo + i % nt) * SP + 128 * rank + row;
             if (ok && need) {
-                const bool in = page < pages;
+                const int page = (w.lo + i) * SP + 128 * rank + row;
+                const bool in = page < w.pages;
                 const float cn = (n4[0] + n4[1]) + (n4[2] + n4[3]);
                 float m = in ? (cn <= FLT_MAX ? cn : INFINITY) : 0.f;
                 m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
-                if (in) p.cn[(size_t)b * p.Pp + page] = cn;
-                if (in && lane == 0) p.cm[((size_t)b * p.Pp + page) / 32] = m;
+                if (in) p.cn[(size_t)w.b * p.Pp + page] = cn;
+                if (in && lane == 0) p.cm[((size_t)w.b * p.Pp + page) / 32] = m;
             }
         }
         if (!ok && lane == 0) fail();
@@ -248,31 +355,34 @@ score_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ C
         const int wq = warp & 3, row = wq * 32 + lane;
         const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
         bool ok = true;
-        for (int i = 0; i < total; ++i) {
-            const int k = i / nt, page = (t_lo + i % nt) * SP + 128 * rank + row;
+        uint32_t i = 0;
+        for (Walk w = start(); w.n > 0; next(w))
+        for (int k = 0; k < passes; ++k)
+        for (int j = 0; j < w.n; ++j, ++i) {
+            const int page = (w.lo + j) * SP + 128 * rank + row;
             const int h0 = k * p.hpc, hn = min(p.hpc, p.H - h0);  // heads of this pass
             const int t0 = g * p.tpg, tn = min(p.tpg, p.T - t0);
             const int rows = tn * hn;
-            if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(B_DFULL + (i & 1)), (uint32_t)(i >> 1) & 1u));
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(B_DFULL + (i & 1)), (i >> 1) & 1u));
             if (ok) {
                 tc_fence_after();
                 int t = t0, h = 0, arg = 0;
                 float m = -INFINITY, m2 = -INFINITY;  // best group's score and the best of the others
-                const uint32_t d0 = tmem + lane_off + (uint32_t)((i & 1) * p.N);
+                const uint32_t d0 = tmem + lane_off + (i & 1) * (uint32_t)p.N;
                 auto group = [&](float x, int g8) {
                     m2 = fmaxf(m2, fminf(m, x));
                     arg = x > m ? g8 : arg;
                     m = fmaxf(m, x);
                 };
                 auto flush = [&]() {
-                    if (page < pages) {
-                        const size_t at = ((size_t)b * p.T + t) * p.Pp + page;
+                    if (page < w.pages) {
+                        const size_t at = ((size_t)w.b * p.T + t) * p.Pp + page;
                         arg += h0 / HG;
                         if (k > 0) {  // with the earlier heads', which this thread stored itself
                             const float o = p.s1[at];
-                            const uint32_t w = p.s2[at];
-                            m2 = fmaxf(fmaxf(m2, __uint_as_float(w & 0xffff0000u)), fminf(m, o));
-                            arg = m > o ? arg : (int)(w & 0xffffu);
+                            const uint32_t x2 = p.s2[at];
+                            m2 = fmaxf(fmaxf(m2, __uint_as_float(x2 & 0xffff0000u)), fminf(m, o));
+                            arg = m > o ? arg : (int)(x2 & 0xffffu);
                             m = fmaxf(m, o);
                         }
                         p.s1[at] = m;
@@ -330,7 +440,7 @@ score_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ C
 // ---------------------------------------------------------------- selection
 // One CTA per (request, query token): 1024 threads, or 256 where they can keep
 // all of a request's scores (fewer barrier partners: one list of 64 pages 9.7 ->
-// SELECT_ONE_256 us of this kernel). The scores are read once, as integers in the
+// SEL256 us of this kernel). The scores are read once, as integers in the
 // scores' order. A histogram of them finds the border's bin (one pass where the
 // scores are of one magnitude, three at most), the bin's members give the k-th
 // largest score, and a last pass collects the pages above the border's interval
@@ -799,22 +909,26 @@ Ws workspace(const hs_pool *pool, int64_t B, int64_t T) {
     return w;
 }
 
-// Splits of a request's page tiles: the count that a model of the launch makes
-// shortest. A tile takes a pair of CTAs about 2.8 us (the pages' bytes at the
-// card's rate, or 256 query rows' products), its start and the queries 4 us.
-int score_splits(int64_t items, int64_t tiles) {
+// Parts that the page tiles of all requests are cut into, each worked through by one
+// pair of CTAs per group: the count that a model of the launch makes shortest. A tile
+// takes a pair about 2.8 us (the pages' bytes at the card's rate, or 256 query rows'
+// products), its start and the queries 4 us. Groups of one part run side by side and
+// share its pages in L2.
+int score_parts(int64_t groups, int64_t tiles) {
     const int64_t pairs = sm_count() / 2 > 0 ? sm_count() / 2 : 1;
     double best = 1e300;
-    int splits = 1;
-    for (int64_t n = 1; n <= tiles && (n == 1 || items * n <= 8 * pairs); ++n) {
-        const double waves = (double)((items * n + pairs - 1) / pairs);
+    int64_t parts = 1;
+    for (int64_t w = 1; w <= 8; ++w) {
+        int64_t n = w * pairs / groups;
+        n = n < 1 ? 1 : (n > tiles ? tiles : n);
+        const double waves = (double)((groups * n + pairs - 1) / pairs);
         const double t = waves * ((double)((tiles + n - 1) / n) * 2.8 + 4.0);
         if (t < best * 0.98) {
             best = t;
-            splits = (int)n;
+            parts = n;
         }
     }
-    return splits;
+    return (int)parts;
 }
 
 hs_status score_attr(int dev) {
@@ -865,17 +979,19 @@ extern "C" hs_status hs_select_pages(hs_pool_t pool, int32_t B, int32_t T, int32
         p.cn = reinterpret_cast<float *>(ws + w.cn);
         p.err = pool->d_err;
         p.cm = reinterpret_cast<float *>(ws + w.cm);
+        p.B = B;
         p.T = T;
         p.H = H;
         p.hpc = H < MAXN ? H : MAXN;
         p.tpg = MAXN / p.hpc < T ? MAXN / p.hpc : T;
         p.groups = (T + p.tpg - 1) / p.tpg;
         p.N = (p.tpg * p.hpc + 31) & ~31;
-        p.splits = score_splits((int64_t)B * p.groups, (pool->max_pages + SP - 1) / SP);
+        const int64_t tiles = (int64_t)B * ((pool->max_pages + SP - 1) / SP);
+        p.parts = score_parts(p.groups, tiles);
+        const int64_t units = (int64_t)p.groups * p.parts;
+        if (2 * units > INT32_MAX || tiles > INT32_MAX) return HS_ERR_INVALID_ARG;
         p.Pp = w.Pp;
         p.max_req = pool->cfg.max_requests;
-        const int64_t units = (int64_t)B * p.groups * p.splits;
-        if (2 * units > INT32_MAX) return HS_ERR_INVALID_ARG;
         CUtensorMap tc, tq;
         if (!make_map(&tc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d_means, kDim, pool->max_pages,
                       pool->cfg.max_requests, 2 * kDim, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
