@@ -353,9 +353,9 @@ hs_status hs_page_means(hs_pool_t pool, int32_t n, const int32_t *d_req, const i
  * The score of page p is max_h q[b][t][h] . means[req][p]. If there are more
  * than N candidates, the first n_first and the last n_last are kept and the
  * others taken by descending score, equal scores by ascending page, until
- * there are N. The choice is that of the exact sums (products of BF16 values
- * summed in 64 bits), not of 32-bit ones; a NaN product counts as minus
- * infinity.
+ * there are N. The choice is that of sums as exact as 64-bit ones (no part above
+ * 2^-45 of the products' sum is lost; products below f32's normal numbers may
+ * count as zero), not of 32-bit ones; a NaN sum counts as minus infinity.
  *   d_q        bf16 [B][T][H][576];  d_means as hs_page_means writes them
  *   d_tree     uint64 [B][T] or NULL: as in hs_page_mla_decode; with it every
  *              page below ctx_len is a candidate for every query token
@@ -365,9 +365,9 @@ hs_status hs_page_means(hs_pool_t pool, int32_t n, const int32_t *d_req, const i
  *              lists that hs_resolve_topk_union takes when pages are not resident
  *   d_workspace / ws_bytes: hs_select_workspace_bytes(pool, B, T) bytes, 256-byte
  *              aligned; calls that overlap need one each
- * The scores are exact in time only near the border, so means or queries with
- * infinities or NaN (whose scores say nothing in 32 bits) make a call slow, not
- * wrong. Requires 1 <= N <= 1024 (HS_ERR_CAPACITY above), n_first + n_last <= N,
+ * Only the sums near the border are taken that exactly. Where 32-bit scores say
+ * nothing (infinities or NaN among the means or queries, hundreds of nearly equal
+ * scores), most pages are, and the call is right but slow. Requires 1 <= N <= 1024 (HS_ERR_CAPACITY above), n_first + n_last <= N,
  * T <= 32767 (64 with a tree), H <= 65535, T*H <= 2^22, B <= 65535; q and means
  * 16-byte aligned. */
 hs_status hs_select_pages(hs_pool_t pool, int32_t B, int32_t T, int32_t H, int32_t N,

@@ -399,6 +399,29 @@ def test_select_ties_and_near_ties():
     c.close()
 
 
+def test_select_where_short_sums_lose_the_most():
+    """One product so large that sums held beside it lose every other one: the scores of
+    two pages are then off by 2^-15.84 |q||c| in opposite directions, and their order in
+    exact sums is the other one."""
+    c = sparse_cache([64 * 600] * 2)
+    small = 2.0 ** -5 * (1 - 2.0 ** -8)
+    means = torch.zeros(2, c.P, P.DIM)
+    means[:, :, 0] = 512.0
+    up, down = means[:, 0].clone(), means[:, 0].clone()
+    up[:, 0] = down[:, 0] = 1024.0
+    up[:, 2:], down[:, 2:] = small, -small
+    down[:, 1] = 35.0 / 32                     # 574 * 2 * small = 35.74 > 35
+    for r, (i, j) in enumerate(((100, 300), (300, 100))):
+        means[r, i], means[r, j] = up[r], down[r]
+    q = torch.ones(2, 1, 8, P.DIM)
+    q[..., 0], q[..., 1] = 1024.0, 32.0
+    q, means = q.to(torch.bfloat16).cuda(), means.to(torch.bfloat16).cuda()
+    pages = run_select(c, q, means, 3, 1, 1)
+    check_select(c, q, means, pages, 1, 1)
+    assert pages[:, 0, 1].tolist() == [100, 300]
+    c.close()
+
+
 def test_select_with_infinities_and_nan():
     c = sparse_cache([64 * 900] * 3)
     means = torch.randn(3, c.P, P.DIM, generator=torch.Generator().manual_seed(11)).to(torch.bfloat16).cuda()

@@ -4,13 +4,15 @@
 // The score of page p for query token t is s = max_h q[t][h] . c_p, c_p the mean
 // row of the page (hs_page_means). The selection is that of the exact sums: the
 // tensor cores' sums are within
-//     E = 2^-16 * max_h |q_h| * max_p |c_p|
-// of them (36 MMAs of depth 16 per score; products of BF16 values are exact in
-// f32, and each MMA adds at most 2^-22 of the sums' largest possible magnitude
-// |q||c|, so 36 * 2^-22 < 2^-16 of it in all), so a page whose score is more
-// than 2 E from the border is in or out, and the few nearer ones are summed
-// again in 64 bits (of which 576 exact products lose nothing that BF16 inputs
-// can tell apart but ties). Equal scores go to the lower page.
+//     E = 2^-15 * max_h |q_h| * max_p |c_p|
+// of them: products of BF16 values are exact, and each of a score's 36 MMAs of depth
+// 16 cuts its 16 products and the sum so far at 2^-25 of the largest's power of two
+// and then rounds the sum to f32, together less than (16 * 2^-25 + 2^-23) |q||c|, so
+// 36 times that, 2^-15.5, in all (2^-15.84 measured with one product of |q||c| and all
+// others just below the cut; 2^-22 to 2^-23 with random ones). A page whose score is
+// more than 2 E from the border is therefore in or out, and the few nearer ones are
+// summed again as pairs of f32. Equal scores go to the lower page. Products below
+// f32's normal numbers may count as zero.
 #include <cfloat>
 #include <climits>
 #include <cstdint>
@@ -439,13 +441,12 @@ score_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ C
 
 // ---------------------------------------------------------------- selection
 // One CTA per (request, query token): 1024 threads, or 256 where they can keep
-// all of a request's scores (fewer barrier partners: one list of 64 pages 9.7 ->
-// SEL256 us of this kernel). The scores are read once, as integers in the
+// all of a request's scores (fewer barrier partners: a call for one list of 64 pages
+// takes 10.9 us instead of 13.6). The scores are read once, as integers in the
 // scores' order. A histogram of them finds the border's bin (one pass where the
 // scores are of one magnitude, three at most), the bin's members give the k-th
 // largest score, and a last pass collects the pages above the border's interval
-// and those inside it; the latter are summed again in 64 bits. That arithmetic is
-// 1/64 as fast as 32-bit: only sums that 32 bits cannot settle are taken so.
+// and those inside it; the latter are summed again (dot64).
 constexpr int BINS = 2048;
 constexpr int CAP = 512;       // pages near the border that fit in shared memory
 constexpr int MAXSEL = 1024;   // pages per list
@@ -763,7 +764,7 @@ __global__ void __launch_bounds__(LT) select_kernel(const SelectParams p) {
         // The interval's bounds are rounded outwards; a bound that is NaN (norms
         // beyond 32 bits) makes every page near.
         const float theta = from_order32(s_theta);
-        const float e2 = __fmul_ru(2.f / 65536.f * 1.001f, __fmul_ru(__fsqrt_ru(__int_as_float(s_qn)), __fsqrt_ru(__int_as_float(s_cn))));
+        const float e2 = __fmul_ru(2.f / 32768.f * 1.001f, __fmul_ru(__fsqrt_ru(__int_as_float(s_qn)), __fsqrt_ru(__int_as_float(s_cn))));
         const float slack = __fadd_ru(e2, __fmul_ru(fabsf(theta), 1.f / 4194304.f));
         const float fup = __fadd_ru(theta, slack), fdn = __fadd_rd(theta, -slack);
         const uint32_t up = fup == fup ? order32(fup) : 0xffffffffu, dn = fdn == fdn ? order32(fdn) : 0u;
