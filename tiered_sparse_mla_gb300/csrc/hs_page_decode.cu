@@ -77,22 +77,20 @@ template <bool FP8>
 struct PCfg {
     static constexpr int THREADS = 128 + 32 * NSW + (FP8 ? 256 : 0);
     static constexpr int NV = 2;              // V's buffers: two steps; FP8: the two halves of one step's columns
-    static constexpr int NXS = FP8 ? 6 : 7;   // slots of K chunks
-    // K chunks per barrier. FP8: three, converted together; BF16: the rope chunk
-    // by itself, then the value chunks in twos (fewer waits and copies to issue)
+    // K chunks per barrier. FP8: three; BF16: the rope chunk by itself, then the
+    // value chunks in twos (fewer waits and copies to issue)
     static constexpr int GK = FP8 ? 3 : 2;
     static constexpr int GV = 4;              // FP8: V chunks converted together (half the columns)
-    static constexpr int NXG = FP8 ? NXS / GK : 1 + NXS / 2;  // groups of K chunks; BF16: group 0 is the rope's
-    static constexpr int NCK = FP8 ? 3 : 0;   // groups of K codes
-    static constexpr int NCV = FP8 ? 2 : 0;   // groups of V codes
-    static constexpr int NC = NCK + NCV;
-    static constexpr int RK = FP8 ? NCK : NXG - 1, RV = FP8 ? NCV : NV;  // the producers' rings
+    static constexpr int NXG = FP8 ? 4 : 4;   // groups of K chunks; BF16: group 0 is the rope's
+    static constexpr int NCV = FP8 ? 4 : 0;   // groups of V codes: two per half of the columns
+    static constexpr int XB = FP8 ? NXG * GK * CCH : (2 * NXG - 1) * CH;  // bytes of K chunks
+    static constexpr int RK = FP8 ? NXG : NXG - 1, RV = FP8 ? NCV : NV;  // the producers' rings
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_P = OFF_Q + (NK - NQT) * CH;  // [2 pages] rows x keys
     static constexpr int OFF_V = OFF_P + 2 * CH;           // [steps][2 pages][NVC]
     static constexpr int OFF_X = OFF_V + (FP8 ? 1 : 2) * 2 * NVC * CH;
-    static constexpr int OFF_C = OFF_X + NXS * CH;
-    static constexpr int OFF_SC = OFF_C + (NCK * GK + NCV * GV) * CCH;    // f32 [NTI][2][64] scores' factors
+    static constexpr int OFF_C = OFF_X + XB;                // FP8: V's codes
+    static constexpr int OFF_SC = OFF_C + NCV * GV * CCH;    // f32 [NTI][2][64] scores' factors
     static constexpr int OFF_SP = OFF_SC + (FP8 ? NTI * 2 * 64 * 4 : 0);  // f32 [NTI][2][64] log2|scale|
     static constexpr int OFF_XM = OFF_SP + (FP8 ? NTI * 2 * 64 * 4 : 0);  // f32 [softmax threads], FP8: twice
     static constexpr int OFF_PG = OFF_XM + (FP8 ? 2 : 1) * 32 * NSW * 4;                           // int32 [NTI][2]
@@ -101,9 +99,9 @@ struct PCfg {
     static constexpr int B_QFULL = 0, B_QDONE = 1, B_QREADY = 2, B_SFULL = 3, B_SFREE = 4, B_PFULL = 5,
                          B_PVDONE = 6, B_DRAIN = 7, B_JOIN = 8, B_TFULL = 9, B_TFREE = B_TFULL + NTI,
                          B_TREADY = B_TFREE + NTI, B_VFULL = B_TREADY + NTI, B_VFREE = B_VFULL + NV, B_XFULL = B_VFREE + NV,
-                         B_XFREE = B_XFULL + NXG, B_CFULL = B_XFREE + NXG, B_CFREE = B_CFULL + NC,
-                         NBAR = B_CFREE + NC;
-    static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;  // TMEM base, abort flag, steps, first entry, end, Q's power
+                         B_XFREE = B_XFULL + NXG, B_CFULL = B_XFREE + NXG, B_CFREE = B_CFULL + NCV,
+                         NBAR = B_CFREE + NCV;
+    static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;  // TMEM base, abort flag, steps
     static constexpr int SMEM = OFF_MISC + 32;
     static constexpr int SMEM_ALLOC = SMEM + 1024;
     // where box i (32 columns, 64 rows, 8 KB) of the other split's partial lands:
@@ -150,22 +148,36 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
-// Two BF16 values times 2^k (as a float) to F16.
-__device__ __forceinline__ uint32_t bf16x2_to_f16(uint32_t w, float pow2) {
-    return pack_f16(__uint_as_float(w << 16) * pow2, __uint_as_float(w & 0xffff0000u) * pow2);
+// Two f32 to e4m3 codes (at most 448; NaN beyond), and what they leave, to codes too.
+__device__ __forceinline__ void e4m3_pieces(float x, float y, uint32_t &p, uint32_t &r) {
+    x = fabsf(x) <= 448.f ? x : __uint_as_float(0x7fffffffu);
+    y = fabsf(y) <= 448.f ? y : __uint_as_float(0x7fffffffu);
+    uint16_t a, b;
+    uint32_t h;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(a) : "f"(y), "f"(x));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(a));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(y - f.y), "f"(x - f.x));
+    p = a;
+    r = b;
 }
-// Four e4m3 codes to F16, exactly; with V, the NaN codes (rows that no query
-// sees may hold any byte) become a finite value.
-template <bool V>
+// Four BF16 values times 2^k (as a float) as the sums of two e4m3 codes each.
+__device__ __forceinline__ void bf16x4_to_e4m3(uint32_t w0, uint32_t w1, float pow2, uint32_t &p, uint32_t &r) {
+    uint32_t p0, p1, r0, r1;
+    e4m3_pieces(__uint_as_float(w0 << 16) * pow2, __uint_as_float(w0 & 0xffff0000u) * pow2, p0, r0);
+    e4m3_pieces(__uint_as_float(w1 << 16) * pow2, __uint_as_float(w1 & 0xffff0000u) * pow2, p1, r1);
+    p = p0 | (p1 << 16);
+    r = r0 | (r1 << 16);
+}
+// Four e4m3 codes to F16, exactly; the NaN codes (rows that no query sees may hold
+// any byte) become a finite value.
 __device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
     asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
         : "=r"(lo), "=r"(hi)
         : "r"(w));
-    if (V) {
-        const uint32_t most = 0x5f805f80u;  // 480, above every code
-        asm("min.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(most));
-        asm("min.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(most));
-    }
+    const uint32_t most = 0x5f805f80u;  // 480, above every code
+    asm("min.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(most));
+    asm("min.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(most));
 }
 // f32 bulk copy of one page's scales into shared memory
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
@@ -246,7 +258,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             // both CTAs' softmax warps
             if (i == C::B_QREADY || i == C::B_SFREE || i == C::B_PFULL) n = 2 * NSW;
             // FP8: four converter warps of each CTA
-            if (FP8 && ((i >= C::B_VFULL && i < C::B_VFREE) || (i >= C::B_XFULL && i < C::B_XFREE))) n = 8;
+            if (FP8 && i >= C::B_VFULL && i < C::B_VFREE) n = 8;
             if (FP8 && i >= C::B_CFREE) n = 4;
             mbar_init(bar(i), n);
         }
@@ -369,16 +381,16 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     }
                     ut = j + 1;
                 }
+                // both CTAs' bytes complete on CTA 0's barrier
                 if (FP8) {
                     for (int i = 0; i < NK && ok; i += C::GK, ++ul) {
                         const int s = ul % C::RK;
-                        ok = mbar_wait_inline(bar(C::B_CFREE + s), ((uint32_t)(ul / C::RK) & 1u) ^ 1u);
+                        ok = mbar_wait_inline(bar(C::B_XFREE + s), ((uint32_t)(ul / C::RK) & 1u) ^ 1u);
                         if (!ok) break;
-                        mbar_expect_tx(bar(C::B_CFULL + s), C::GK * CCH);
-                        tma_load_3d(base + C::OFF_C + s * C::GK * CCH, &tm_k1, 0, own, i, bar(C::B_CFULL + s));
+                        if (rank == 0) mbar_expect_tx(bar(C::B_XFULL + s), 2 * C::GK * CCH);
+                        tma_load_pair(base + C::OFF_X + s * C::GK * CCH, &tm_k1, 0, own, i, lead(C::B_XFULL + s));
                     }
                 } else {
-                    // both CTAs' bytes complete on CTA 0's barrier
                     if (ok) ok = mbar_wait_inline(bar(C::B_XFREE), ((uint32_t)j & 1u) ^ 1u);
                     if (ok) {
                         if (rank == 0) mbar_expect_tx(bar(C::B_XFULL), 2 * CH);
@@ -396,8 +408,8 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             } else if (lane == 0) {
                 if (FP8) {
                     for (int i = 0; i < 2 && ok; ++i, ++ul) {  // half the columns: two chunks of either page
-                        const int cs = C::NCK + ul % C::RV;
-                        const uint32_t dst = base + C::OFF_C + (C::NCK * C::GK + (ul % C::RV) * C::GV) * CCH;
+                        const int cs = ul % C::RV;
+                        const uint32_t dst = base + C::OFF_C + cs * C::GV * CCH;
                         ok = mbar_wait_inline(bar(C::B_CFREE + cs), ((uint32_t)(ul / C::RV) & 1u) ^ 1u);
                         if (!ok) break;
                         mbar_expect_tx(bar(C::B_CFULL + cs), C::GV * CCH);
@@ -427,8 +439,8 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (!ok) {
                 fail();
                 const int ring = kw ? C::RK : C::RV;
-                const int b0 = FP8 ? (kw ? C::B_CFULL : C::B_CFULL + C::NCK) : (kw ? C::B_XFULL + 1 : C::B_VFULL);
-                for (int i = ul - 1; (FP8 || !kw || rank == 0) && i >= 0 && i >= ul - ring; --i)
+                const int b0 = kw ? (FP8 ? C::B_XFULL : C::B_XFULL + 1) : (FP8 ? C::B_CFULL : C::B_VFULL);
+                for (int i = ul - 1; (!kw || rank == 0) && i >= 0 && i >= ul - ring; --i)
                     mbar_wait_inline(bar(b0 + i % ring), (uint32_t)(i / ring) & 1u);
                 if (!FP8 && kw && rank == 0 && ux > 0) mbar_wait_inline(bar(C::B_XFULL), (uint32_t)(ux - 1) & 1u);
                 for (int i = ut - 1; FP8 && kw && i >= 0 && i >= ut - NTI; --i)
@@ -446,6 +458,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             constexpr uint32_t ID_QK = idesc_f16(FP8 ? 0u : 1u, 0, BM, 128), ID_PV = idesc_f16(FP8 ? 0u : 1u, 1, BM, 256);
             const uint64_t dk = desc_sw128(base, 16, 1024), dv = desc_sw128(base, CH, 1024);
             const uint32_t hi = (uint32_t)(dk >> 32), klo = (uint32_t)dk, vlo = (uint32_t)dv;
+            const uint32_t chi = (uint32_t)(desc_sw64(base, 16, 512) >> 32);  // K's codes
             const uint32_t leader = elect_one();
             bool ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_QREADY), 0));
             tc_fence_after();
@@ -484,14 +497,19 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (j > 0) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_SFREE), (uint32_t)(j - 1) & 1u));
                 tc_fence_after();
                 auto qk = [&](int c, uint32_t slot, bool fresh) {  // one chunk: four MMAs
-                    const uint32_t kd = klo + ((C::OFF_X + slot * CH) >> 4);
+                    const uint32_t kd = klo + ((C::OFF_X + slot * (FP8 ? CCH : CH)) >> 4);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if (c < NQT)
-                            mma2_ts(tmem + TM_S, tmem + TM_Q + 32u * c + 8u * k, kd + 2 * k, hi, ID_QK, !(fresh && k == 0));
+                    for (int k = 0; k < 4; ++k) {  // FP8: both pieces of Q with the same 32 codes
+                        const uint32_t tq = tmem + TM_Q + 32u * c + 8u * k, sq = klo + ((C::OFF_Q + (c - NQT) * CH + 32 * k) >> 4);
+                        const bool acc = !(fresh && k == 0);
+                        if (FP8 && c < NQT)
+                            mma2_ts_e4m3(tmem + TM_S, tq, kd + 2 * (k & 1), chi, ID_QK, acc);
+                        else if (FP8)
+                            mma2_ss_e4m3(tmem + TM_S, sq, hi, kd + 2 * (k & 1), chi, ID_QK, acc);
+                        else if (c < NQT)
+                            mma2_ts(tmem + TM_S, tq, kd + 2 * k, hi, ID_QK, acc);
                         else
-                            mma2_ss(tmem + TM_S, klo + ((C::OFF_Q + (c - NQT) * CH + 32 * k) >> 4), kd + 2 * k, hi, ID_QK,
-                                    !(fresh && k == 0));
+                            mma2_ss(tmem + TM_S, sq, kd + 2 * k, hi, ID_QK, acc);
                     }
                 };
                 if (!FP8) {
@@ -540,9 +558,8 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
     } else if (FP8 && warp == 2) {
         // ------------------------------------------------------------ the keys' factors
-        bool ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_QDONE), 0));
-        // four keys per lane; c takes Q's power back
-        const float c = p.scale_log2 * __int_as_float(misc[5]);
+        bool ok = true;
+        const float c = p.scale_log2;  // four keys per lane
         for (int j = 0; j < nsteps; ++j) {
             const int ti = j % NTI;
             if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_TFULL + ti), (uint32_t)(j / NTI) & 1u));
@@ -588,9 +605,9 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         };
         bool ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_QFULL), 0));
         auto q_at = [&](int i) { return base + (i < NQT ? C::OFF_QST + i * CH : C::OFF_Q + (i - NQT) * CH) + row * 128; };
-        float q_pow = 1.f;
+        float q_pow = 1.f, q_back = 1.f;
         if (FP8) {
-            // the largest finite magnitude of the CTA's rows, as BF16 bits
+            // the row's largest finite magnitude, as BF16 bits
             uint32_t m = 0;
             if (ok) {
                 auto fin = [](uint32_t w) {
@@ -604,16 +621,14 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         m = __vmaxu2(m, __vmaxu2(__vmaxu2(fin(v.x), fin(v.y)), __vmaxu2(fin(v.z), fin(v.w))));
                     }
             }
-            m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
-            if (lane == 0) xm[warp - 4] = __uint_as_float(m << 16);
+            xm[tid] = __uint_as_float(max(m & 0xffffu, m >> 16) << 16);
             named_bar_sync(1, 32 * NSW);
-            float top = 0.f;
-#pragma unroll
-            for (int e = 0; e < NSW; ++e) top = fmaxf(top, xm[e]);
+            const uint32_t top = __float_as_uint(fmaxf(fmaxf(xm[row], xm[row + 64]), fmaxf(xm[row + 128], xm[row + 192])));
             named_bar_sync(1, 32 * NSW);
-            const int k = min(141 - (int)(__float_as_uint(top) >> 23), 126);
+            // times 2^k it lies in (224, 448]
+            const int k = min(135 - (int)(top >> 23) - ((top & 0x7fffffu) > 0x600000u), 126);
             q_pow = __uint_as_float((uint32_t)(k + 127) << 23);
-            if (tid == 0) misc[5] = (127 - k) << 23;
+            q_back = __uint_as_float((uint32_t)(127 - k) << 23);
         }
         if (ok && nsteps > 0) {
 #pragma unroll 1
@@ -622,23 +637,37 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
                     const uint4 v = ld_shared_v4(q_at(i) + ((u ^ (row & 7)) << 4));
-                    w[4 * u] = FP8 ? bf16x2_to_f16(v.x, q_pow) : v.x;
-                    w[4 * u + 1] = FP8 ? bf16x2_to_f16(v.y, q_pow) : v.y;
-                    w[4 * u + 2] = FP8 ? bf16x2_to_f16(v.z, q_pow) : v.z;
-                    w[4 * u + 3] = FP8 ? bf16x2_to_f16(v.w, q_pow) : v.w;
+                    if (FP8) {
+                        bf16x4_to_e4m3(v.x, v.y, q_pow, w[2 * u], w[16 + 2 * u]);
+                        bf16x4_to_e4m3(v.z, v.w, q_pow, w[2 * u + 1], w[17 + 2 * u]);
+                    } else {
+                        w[4 * u] = v.x;
+                        w[4 * u + 1] = v.y;
+                        w[4 * u + 2] = v.z;
+                        w[4 * u + 3] = v.w;
+                    }
                 }
                 HS_TMEM_ST32(tmem + lane_off + TM_Q + 32u * i, w);
             }
-            if (FP8) {  // the chunks that stay in shared memory, in place, a quarter per thread
+            if (FP8) {
+                // the chunks that stay in shared memory, in place: three of a row's
+                // four threads take one each
+                const int i = NQT + 2 * hf + kh;
+                if (i < NK) {
+                    uint4 v[8];
 #pragma unroll
-                for (int i = NQT; i < NK; ++i)
+                    for (int u = 0; u < 8; ++u) v[u] = ld_shared_v4(q_at(i) + ((u ^ (row & 7)) << 4));
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const uint32_t at = q_at(i) + (((4 * hf + 2 * kh + u) ^ (row & 7)) << 4);
-                        const uint4 v = ld_shared_v4(at);
-                        st_shared_v4(at, bf16x2_to_f16(v.x, q_pow), bf16x2_to_f16(v.y, q_pow),
-                                     bf16x2_to_f16(v.z, q_pow), bf16x2_to_f16(v.w, q_pow));
+                    for (int u = 0; u < 4; ++u) {
+                        uint32_t w[8];
+                        bf16x4_to_e4m3(v[2 * u].x, v[2 * u].y, q_pow, w[0], w[4]);
+                        bf16x4_to_e4m3(v[2 * u].z, v[2 * u].w, q_pow, w[1], w[5]);
+                        bf16x4_to_e4m3(v[2 * u + 1].x, v[2 * u + 1].y, q_pow, w[2], w[6]);
+                        bf16x4_to_e4m3(v[2 * u + 1].z, v[2 * u + 1].w, q_pow, w[3], w[7]);
+                        st_shared_v4(q_at(i) + ((u ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
+                        st_shared_v4(q_at(i) + (((4 + u) ^ (row & 7)) << 4), w[4], w[5], w[6], w[7]);
                     }
+                }
             }
             tmem_wait_st();
         }
@@ -668,6 +697,10 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     const float4 f = FP8 ? ld_shared_f4(sc_at + 4 * e) : make_float4(p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) s[e + i] = __uint_as_float(ra[e + i]);
+                    if (FP8) {
+                        mul2(s[e], s[e + 1], q_back, q_back);
+                        mul2(s[e + 2], s[e + 3], q_back, q_back);
+                    }
                     mul2(s[e], s[e + 1], f.x, f.y);
                     mul2(s[e + 2], s[e + 3], f.z, f.w);
                 }
@@ -950,76 +983,55 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
     } else if (FP8 && warp >= 4 + NSW) {
         // ------------------------------------------------------------ converters
-        const bool kw = warp < 8 + NSW;
-        const int tid = threadIdx.x & 127;
+        // Four warps for either half of V's columns, one step after the other: the
+        // next step's codes are loaded while this one's stores are fenced.
+        const int half = (warp - 4 - NSW) >> 2, tid = threadIdx.x & 127;
         // V's space held the staged Q
-        bool ok = kw || __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_QDONE), 0));
-        // A group of chunks at a time: the next group's codes are loaded while this
-        // one's stores are fenced.
-        auto convert = [&](auto is_k) {
-            constexpr bool K = decltype(is_k)::value;
-            constexpr int G = K ? C::GK : C::GV, ring = K ? C::NCK : C::NCV, c0 = K ? 0 : C::NCK;
-            const int total = (K ? NK / G : 2) * nsteps;
-            uint4 w[G][2];
-            int cs = 0, xs = 0;
-            uint32_t cph = 0, xph = 1;
-            auto load = [&]() {
-                if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_CFULL + c0 + cs), cph));
-                const uint32_t src = base + C::OFF_C + ((K ? 0 : C::NCK * C::GK) + cs * G) * CCH + 16 * tid;
-                if (ok) {
+        bool ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_QDONE), 0));
+        constexpr int G = C::GV;
+        static_assert(!FP8 || (NVC == G && C::NCV % 2 == 0 && NK % C::GK == 0), "groups of chunks");
+        uint4 w[G][2];
+        auto load = [&](int j) {
+            const int u = 2 * j + half, cs = u % C::RV;
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_CFULL + cs), (uint32_t)(u / C::RV) & 1u));
+            const uint32_t src = base + C::OFF_C + cs * G * CCH + 16 * tid;
+            if (ok) {
 #pragma unroll
-                    for (int g = 0; g < G; ++g) {
-                        w[g][0] = ld_shared_v4(src + g * CCH);
-                        w[g][1] = ld_shared_v4(src + g * CCH + 2048);
-                    }
-                }
-            };
-            if (total > 0) load();
-#pragma unroll 1
-            for (int i = 0; i < total; ++i) {
-                if (ok)
-                    ok = __all_sync(0xffffffffu, K ? mbar_wait_inline(bar(C::B_XFREE + xs), xph)
-                                                   : mbar_wait_inline(bar(C::B_VFREE + (i & 1)), ((uint32_t)(i >> 1) & 1u) ^ 1u));
-                if (ok) {
-                    const uint32_t dst = base + (K ? C::OFF_X + xs * G * CH : C::OFF_V + (i & 1) * 2 * CH) + (tid >> 2) * 128;
-                    const int key = (tid >> 2) & 7, part = 2 * (tid & 3);  // rows key and key + 32: the same swizzle
-#pragma unroll
-                    for (int g = 0; g < G; ++g)
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            // K: the chunks in turn; V: two of the first page, two of the second
-                            const uint32_t at = dst + (K ? g : (g >> 1) * NVC + (g & 1)) * CH + k * 4096;
-                            uint32_t o[8];
-                            e4m3x4_to_f16<!K>(w[g][k].x, o[0], o[1]);
-                            e4m3x4_to_f16<!K>(w[g][k].y, o[2], o[3]);
-                            e4m3x4_to_f16<!K>(w[g][k].z, o[4], o[5]);
-                            e4m3x4_to_f16<!K>(w[g][k].w, o[6], o[7]);
-                            st_shared_v4(at + ((part ^ key) << 4), o[0], o[1], o[2], o[3]);
-                            st_shared_v4(at + (((part + 1) ^ key) << 4), o[4], o[5], o[6], o[7]);
-                        }
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(C::B_CFREE + c0 + cs));
-                if (++cs == ring) {
-                    cs = 0;
-                    cph ^= 1u;
-                }
-                if (i + 1 < total) load();
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_peer(lead(K ? C::B_XFULL + xs : C::B_VFULL + (i & 1)));
-                if (K && ++xs == C::NXG) {
-                    xs = 0;
-                    xph ^= 1u;
+                for (int g = 0; g < G; ++g) {
+                    w[g][0] = ld_shared_v4(src + g * CCH);
+                    w[g][1] = ld_shared_v4(src + g * CCH + 2048);
                 }
             }
         };
-        if constexpr (FP8) {
-            static_assert(NK % C::GK == 0 && NVC == C::GV && C::NXS % C::GK == 0, "groups of chunks");
-            if (kw)
-                convert(std::true_type{});
-            else
-                convert(std::false_type{});
+        if (nsteps > 0) load(0);
+        const uint32_t lead_vfull = lead(C::B_VFULL + half);
+#pragma unroll 1
+        for (int j = 0; j < nsteps; ++j) {
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_VFREE + half), ((uint32_t)j & 1u) ^ 1u));
+            if (ok) {
+                const uint32_t dst = base + C::OFF_V + half * 2 * CH + (tid >> 2) * 128;
+                const int key = (tid >> 2) & 7, part = 2 * (tid & 3);  // rows key and key + 32: the same swizzle
+#pragma unroll
+                for (int g = 0; g < G; ++g)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        // two chunks of the first page, two of the second
+                        const uint32_t at = dst + ((g >> 1) * NVC + (g & 1)) * CH + k * 4096;
+                        uint32_t o[8];
+                        e4m3x4_to_f16(w[g][k].x, o[0], o[1]);
+                        e4m3x4_to_f16(w[g][k].y, o[2], o[3]);
+                        e4m3x4_to_f16(w[g][k].z, o[4], o[5]);
+                        e4m3x4_to_f16(w[g][k].w, o[6], o[7]);
+                        st_shared_v4(at + ((part ^ key) << 4), o[0], o[1], o[2], o[3]);
+                        st_shared_v4(at + (((part + 1) ^ key) << 4), o[4], o[5], o[6], o[7]);
+                    }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::B_CFREE + (2 * j + half) % C::RV));
+            if (j + 1 < nsteps) load(j + 1);
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_peer(lead_vfull);
         }
         if (!ok && lane == 0) fail();
     }
@@ -1228,7 +1240,7 @@ PagePlan page_plan(int64_t lists, int64_t T, int64_t H, int64_t N) {
 }
 
 // [rows][9 chunks][64] seen as (element, row, chunk), boxes of 64 x 64 x n
-bool make_page_map(CUtensorMap *m, bool fp8, const void *rows, uint64_t n_rows, uint32_t nchunks) {
+bool make_page_map(CUtensorMap *m, bool fp8, const void *rows, uint64_t n_rows, uint32_t nchunks, CUtensorMapSwizzle sw) {
     auto fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t rb = fp8 ? kDim : 2 * kDim;
@@ -1238,7 +1250,7 @@ bool make_page_map(CUtensorMap *m, bool fp8, const void *rows, uint64_t n_rows, 
     cuuint32_t es[3] = {1, 1, 1};
     return fn(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
               const_cast<void *>(rows), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+              sw,
               CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1358,8 +1370,10 @@ hs_status page_entry(hs_pool_t pool, int64_t lists, int32_t T, int32_t tpl, int3
     static_assert(sizeof(pool->page_maps[0]) == sizeof(CUtensorMap), "size of a tensor map");
     CUtensorMap *maps = reinterpret_cast<CUtensorMap *>(pool->page_maps);
     if (!pool->page_maps_made) {
-        if (!make_page_map(&maps[0], fp8, pool->d_rows, rows, fp8 ? PCfg<true>::GK : 1) ||
-            !make_page_map(&maps[1], fp8, pool->d_rows, rows, 2))
+        if (!make_page_map(&maps[0], fp8, pool->d_rows, rows, fp8 ? PCfg<true>::GK : 1,
+                           fp8 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !make_page_map(&maps[1], fp8, pool->d_rows, rows, 2,
+                           fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B))
             return HS_ERR_CUDA;
         pool->page_maps_made = true;
     }

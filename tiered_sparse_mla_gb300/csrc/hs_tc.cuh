@@ -214,6 +214,10 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo_byte
     return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo_bytes >> 4) & 0x3FFFu) << 16) |
            ((uint64_t)((sbo_bytes >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
 }
+// The same for rows of 64 bytes (groups of 8 rows: 512 bytes).
+__device__ __forceinline__ uint64_t desc_sw64(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes) {
+    return (desc_sw128(saddr, lbo_bytes, sbo_bytes) & ~(7ull << 61)) | (4ull << 61);
+}
 // Instruction descriptor, kind::f16 with f32 accumulation. ab: 0 = f16, 1 = bf16.
 __host__ __device__ constexpr uint32_t idesc_f16(uint32_t ab, uint32_t b_mn_major, uint32_t M,
                                                  uint32_t N) {
@@ -429,6 +433,24 @@ __device__ __forceinline__ void mma2_ts(uint32_t d, uint32_t a, uint32_t blo, ui
         "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n mov.b64 b, {%2, %3};\n"
         " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d),
         "r"(a), "r"(blo), "r"(hi), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// One MMA of e4m3 codes, depth 32: the instruction descriptor is that of F16 (format
+// 0 of either kind); A and B have layouts of their own.
+__device__ __forceinline__ void mma2_ss_e4m3(uint32_t d, uint32_t alo, uint32_t ahi, uint32_t blo, uint32_t bhi,
+                                             uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %6, 0;\n mov.b64 a, {%1, %2};\n mov.b64 b, {%3, %4};\n"
+        " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %5, p;\n}\n" ::"r"(d),
+        "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma2_ts_e4m3(uint32_t d, uint32_t a, uint32_t blo, uint32_t bhi, uint32_t idesc,
+                                             uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n mov.b64 b, {%2, %3};\n"
+        " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], [%1], b, %4, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(blo), "r"(bhi), "r"(idesc), "r"(acc)
         : "memory");
 }
 // A box into this CTA's shared memory whose bytes complete on a barrier of either CTA.
