@@ -90,12 +90,11 @@ struct PCfg {
     static constexpr int OFF_V = OFF_P + 2 * CH;           // [steps][2 pages][NVC]
     static constexpr int OFF_X = OFF_V + (FP8 ? 1 : 2) * 2 * NVC * CH;
     static constexpr int OFF_C = OFF_X + XB;                // FP8: V's codes
-    static constexpr int OFF_SC = OFF_C + NCV * GV * CCH;    // f32 [NTI][2][64] scores' factors
-    static constexpr int OFF_SP = OFF_SC + (FP8 ? NTI * 2 * 64 * 4 : 0);  // f32 [NTI][2][64] log2|scale|
-    static constexpr int OFF_XM = OFF_SP + (FP8 ? NTI * 2 * 64 * 4 : 0);  // f32 [softmax threads], FP8: twice
-    static constexpr int OFF_PG = OFF_XM + (FP8 ? 2 : 1) * 32 * NSW * 4;                           // int32 [NTI][2]
-    static constexpr int OFF_NEG = OFF_PG + NTI * 8;                      // int32 [NTI] some scale is negative
-    static constexpr int OFF_BAR = (OFF_NEG + NTI * 4 + 7) & ~7;
+    static constexpr int OFF_SC = OFF_C + NCV * GV * CCH;                 // f32 [NTI][2][64] the rows' scales
+    static constexpr int OFF_SP = OFF_SC + (FP8 ? NTI * 2 * 64 * 4 : 0);  // f32 [NTI][4] their largest, by 32 keys
+    static constexpr int OFF_XM = OFF_SP + (FP8 ? NTI * 16 : 0);          // f32 [softmax threads], FP8: twice
+    static constexpr int OFF_PG = OFF_XM + (FP8 ? 2 : 1) * 32 * NSW * 4;  // int32 [NTI][2]
+    static constexpr int OFF_BAR = (OFF_PG + NTI * 8 + 7) & ~7;
     static constexpr int B_QFULL = 0, B_QDONE = 1, B_QREADY = 2, B_SFULL = 3, B_SFREE = 4, B_PFULL = 5,
                          B_PVDONE = 6, B_DRAIN = 7, B_JOIN = 8, B_TFULL = 9, B_TFREE = B_TFULL + NTI,
                          B_TREADY = B_TFREE + NTI, B_VFULL = B_TREADY + NTI, B_VFREE = B_VFULL + NV, B_XFULL = B_VFREE + NV,
@@ -557,21 +556,17 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             __syncwarp();
         }
     } else if (FP8 && warp == 2) {
-        // ------------------------------------------------------------ the keys' factors
+        // ------------------------------------------------------------ the scales' maxima
         bool ok = true;
-        const float c = p.scale_log2;  // four keys per lane
         for (int j = 0; j < nsteps; ++j) {
             const int ti = j % NTI;
             if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_TFULL + ti), (uint32_t)(j / NTI) & 1u));
             if (!ok) break;
-            const uint32_t at = base + C::OFF_SC + ti * 512 + lane * 16;
-            const float4 f = ld_shared_f4(at);
-            st_shared_v4(at, __float_as_uint(f.x * c), __float_as_uint(f.y * c), __float_as_uint(f.z * c),
-                         __float_as_uint(f.w * c));
-            st_shared_v4(at + C::OFF_SP - C::OFF_SC, __float_as_uint(__log2f(fabsf(f.x))), __float_as_uint(__log2f(fabsf(f.y))),
-                         __float_as_uint(__log2f(fabsf(f.z))), __float_as_uint(__log2f(fabsf(f.w))));
-            const bool neg = __any_sync(0xffffffffu, f.x < 0.f || f.y < 0.f || f.z < 0.f || f.w < 0.f);
-            if (lane == 0) reinterpret_cast<volatile int32_t *>(smem + C::OFF_NEG)[ti] = neg;
+            const float4 f = ld_shared_f4(base + C::OFF_SC + ti * 512 + lane * 16);
+            float m = fmaxf(fmaxf(fabsf(f.x), fabsf(f.y)), fmaxf(fabsf(f.z), fabsf(f.w)));
+#pragma unroll
+            for (int o = 4; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if ((lane & 7) == 0) reinterpret_cast<volatile float *>(smem + C::OFF_SP)[4 * ti + (lane >> 3)] = m;
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::B_TREADY + ti));
         }
@@ -678,12 +673,12 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         arrive_lead(lead_qready);
 
         float m2 = -INFINITY, l = 0.f;
-        float mp = -INFINITY;  // FP8: P's reference
+        float cref = 0.f, fac = 0.f;  // FP8: the scales' reference, a power of two, and 16 over it
+        const float row_scale = p.scale_log2 * q_back;
         for (int j = 0; j < nsteps; ++j) {
             const int ti = j % NTI;
             float s[KT];
             const uint32_t sc_at = base + C::OFF_SC + ti * 512 + kh * 256 + hf * 128;
-            const uint32_t sp_at = base + C::OFF_SP + ti * 512 + kh * 256 + hf * 128;
             if (ok)
                 ok = __all_sync(0xffffffffu, mbar_wait_inline(bar((FP8 ? C::B_TREADY : C::B_TFULL) + ti), (uint32_t)(j / NTI) & 1u) &&
                                                  mbar_wait_inline(bar(C::B_SFULL), (uint32_t)j & 1u));
@@ -698,8 +693,8 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
                     for (int i = 0; i < 4; ++i) s[e + i] = __uint_as_float(ra[e + i]);
                     if (FP8) {
-                        mul2(s[e], s[e + 1], q_back, q_back);
-                        mul2(s[e + 2], s[e + 3], q_back, q_back);
+                        mul2(s[e], s[e + 1], row_scale, row_scale);
+                        mul2(s[e + 2], s[e + 3], row_scale, row_scale);
                     }
                     mul2(s[e], s[e + 1], f.x, f.y);
                     mul2(s[e + 2], s[e + 3], f.z, f.w);
@@ -711,7 +706,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             // the keys that this row sees, as bits
             const long long base_pos = (long long)pg * kPage;
             const bool tail = pg >= 0 && base_pos + kPage > draft;  // some row may not see some key
-            float tmax = -INFINITY, pmax = -INFINITY;
+            float tmax = -INFINITY, cmax = 0.f;
             uint32_t mine = ~0u;
             if (pg < 0) {
                 mine = 0;
@@ -745,56 +740,49 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
                 tmax = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
                 if (FP8) {
-                    // scores plus log2|scale|; a hidden row's scale may be anything
-                    float pm[2] = {-INFINITY, -INFINITY};
+                    cmax = reinterpret_cast<volatile float *>(smem + C::OFF_SP)[4 * ti + 2 * kh + hf];
+                    if (hide) {  // a hidden row's scale may be anything
+                        cmax = 0.f;
 #pragma unroll
-                    for (int e = 0; e < KT; e += 4) {
-                        const float4 f = ld_shared_f4(sp_at + 4 * e);
-                        float t0 = s[e], t1 = s[e + 1], t2 = s[e + 2], t3 = s[e + 3];
-                        add2(t0, t1, f.x, f.y);
-                        add2(t2, t3, f.z, f.w);
-                        if (hide) {
-                            t0 = (mine >> e) & 1u ? t0 : -INFINITY;
-                            t1 = (mine >> (e + 1)) & 1u ? t1 : -INFINITY;
-                            t2 = (mine >> (e + 2)) & 1u ? t2 : -INFINITY;
-                            t3 = (mine >> (e + 3)) & 1u ? t3 : -INFINITY;
+                        for (int e = 0; e < KT; e += 4) {
+                            const float4 f = ld_shared_f4(sc_at + 4 * e);
+                            cmax = fmaxf(cmax, (mine >> e) & 1u ? fabsf(f.x) : 0.f);
+                            cmax = fmaxf(cmax, (mine >> (e + 1)) & 1u ? fabsf(f.y) : 0.f);
+                            cmax = fmaxf(cmax, (mine >> (e + 2)) & 1u ? fabsf(f.z) : 0.f);
+                            cmax = fmaxf(cmax, (mine >> (e + 3)) & 1u ? fabsf(f.w) : 0.f);
                         }
-                        pm[0] = max3(pm[0], t0, t1);
-                        pm[1] = max3(pm[1], t2, t3);
                     }
-                    pmax = fmaxf(pm[0], pm[1]);
                 }
             }
             // A row's four threads share its references: where some row of the CTA
             // outgrows its own, the rows' four maxima meet in shared memory.
             float alpha = 1.f;
             auto outgrown = [](float x, float ref) { return x > ref + TAU2 || (ref == -INFINITY && x != -INFINITY); };
-            const bool grow = any_softmax(outgrown(tmax, m2) || (FP8 && outgrown(pmax, mp)));
+            const bool grow = any_softmax(outgrown(tmax, m2) || (FP8 && cmax > 8.f * cref));
             if (grow) {
                 xm[tid] = tmax;
-                if (FP8) xm[32 * NSW + tid] = pmax;
+                if (FP8) xm[32 * NSW + tid] = cmax;
                 named_bar_sync(1, 32 * NSW);
                 auto of_row = [&](int o) {
                     return fmaxf(fmaxf(xm[o + row], xm[o + row + 64]), fmaxf(xm[o + row + 128], xm[o + row + 192]));
                 };
-                const float tall = of_row(0), pall = FP8 ? of_row(32 * NSW) : 0.f;
+                const float tall = of_row(0), call = FP8 ? of_row(32 * NSW) : 0.f;
                 named_bar_sync(1, 32 * NSW);  // read before the next writes
                 if (outgrown(tall, m2)) {
                     alpha = exp2f(m2 - tall);  // 0 where the row had seen nothing
                     l *= alpha;
                     m2 = tall;
                 }
-                if (FP8) {
-                    alpha = 1.f;
-                    if (outgrown(pall, mp)) {
-                        alpha = exp2f(mp - pall);
-                        mp = pall;
-                    }
+                if (FP8 && call > 8.f * cref) {
+                    const uint32_t e = max(__float_as_uint(call) >> 23, 7u);
+                    fac = __uint_as_float((258u - e) << 23);
+                    alpha *= cref * fac * 0.0625f;
+                    cref = __uint_as_float(e << 23);
                 }
             }
             uint32_t pk[KT / 2];
             if (ok) {
-                const float mneg = m2 == -INFINITY ? 0.f : -m2, pneg = mp == -INFINITY ? 0.f : 7.f - mp;
+                const float mneg = m2 == -INFINITY ? 0.f : -m2;
                 float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
 #pragma unroll
                 for (int e = 0; e < KT; e += 4) {
@@ -808,17 +796,13 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     add2(l0, l1, a0, a1);
                     add2(l2, l3, a2, a3);
                     if (FP8) {
-                        const float4 f = ld_shared_f4(sp_at + 4 * e);
-                        a0 = f.x;
-                        a1 = f.y;
-                        a2 = f.z;
-                        a3 = f.w;
-                        add2(a0, a1, pneg, pneg);
-                        add2(a2, a3, pneg, pneg);
-                        add2(a0, a1, s[e], s[e + 1]);
-                        add2(a2, a3, s[e + 2], s[e + 3]);
-                        pk[e / 2] = pack_f16(ex2(a0), ex2(a1));
-                        pk[e / 2 + 1] = pack_f16(ex2(a2), ex2(a3));
+                        float4 f = ld_shared_f4(sc_at + 4 * e);
+                        mul2(f.x, f.y, fac, fac);
+                        mul2(f.z, f.w, fac, fac);
+                        mul2(a0, a1, f.x, f.y);
+                        mul2(a2, a3, f.z, f.w);
+                        pk[e / 2] = pack_f16(a0, a1);
+                        pk[e / 2 + 1] = pack_f16(a2, a3);
                     } else {
                         pk[e / 2] = pack_bf16(a0, a1);
                         pk[e / 2 + 1] = pack_bf16(a2, a3);
@@ -830,14 +814,6 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
                     for (int e = 0; e < KT / 2; ++e)
                         pk[e] &= ((mine >> (2 * e)) & 1u ? 0xffffu : 0u) | ((mine >> (2 * e + 1)) & 1u ? 0xffff0000u : 0u);
-                }
-                if (FP8 && reinterpret_cast<volatile int32_t *>(smem + C::OFF_NEG)[ti]) {
-#pragma unroll
-                    for (int e = 0; e < KT; e += 4) {  // signs of the scales
-                        const float4 f = ld_shared_f4(sc_at + 4 * e);
-                        pk[e / 2] ^= ((__float_as_uint(f.x) >> 16) & 0x8000u) | (__float_as_uint(f.y) & 0x80000000u);
-                        pk[e / 2 + 1] ^= ((__float_as_uint(f.z) >> 16) & 0x8000u) | (__float_as_uint(f.w) & 0x80000000u);
-                    }
                 }
             }
             __syncwarp();
@@ -892,7 +868,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         named_bar_sync(1, 32 * NSW);
         l = (xm[row] + xm[row + 64]) + (xm[row + 128] + xm[row + 192]);
         // rows that see nothing: out 0, lse -inf
-        const float inv = l == 0.f ? 0.f : __fdividef(FP8 ? (mp == -INFINITY ? 0.f : ex2(mp - m2 - 7.f)) : 1.f, l);
+        const float inv = l == 0.f ? 0.f : __fdividef(FP8 ? cref * 0.0625f : 1.f, l);
         const bool one = p.nsplit == 1;
         if (ok && (one || nsteps > 0)) {
             // O / l through shared memory, idle by now, in 32-row boxes of 128
