@@ -147,26 +147,24 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
-// Two f32 to e4m3 codes (at most 448; NaN beyond), and what they leave, to codes too.
-__device__ __forceinline__ void e4m3_pieces(float x, float y, uint32_t &p, uint32_t &r) {
-    x = fabsf(x) <= 448.f ? x : __uint_as_float(0x7fffffffu);
-    y = fabsf(y) <= 448.f ? y : __uint_as_float(0x7fffffffu);
-    uint16_t a, b;
-    uint32_t h;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(a) : "f"(y), "f"(x));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(a));
-    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(y - f.y), "f"(x - f.x));
-    p = a;
-    r = b;
+// Two BF16 values times 2^k (a pair of BF16; at most 448, or NaN) as the sums of two
+// e4m3 codes each. F16 holds the products' eight bits down to 2^-17, the codes'
+// smallest step is 2^-9.
+__device__ __forceinline__ void e4m3_pieces(uint32_t w, uint32_t pow2, uint16_t &p, uint16_t &r) {
+    uint32_t x, h;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(w), "r"(pow2));
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(x) : "f"(__uint_as_float(x & 0xffff0000u)), "f"(__uint_as_float(x << 16)));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(p) : "r"(x));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(p));
+    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(h));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
 }
-// Four BF16 values times 2^k (as a float) as the sums of two e4m3 codes each.
-__device__ __forceinline__ void bf16x4_to_e4m3(uint32_t w0, uint32_t w1, float pow2, uint32_t &p, uint32_t &r) {
-    uint32_t p0, p1, r0, r1;
-    e4m3_pieces(__uint_as_float(w0 << 16) * pow2, __uint_as_float(w0 & 0xffff0000u) * pow2, p0, r0);
-    e4m3_pieces(__uint_as_float(w1 << 16) * pow2, __uint_as_float(w1 & 0xffff0000u) * pow2, p1, r1);
-    p = p0 | (p1 << 16);
-    r = r0 | (r1 << 16);
+__device__ __forceinline__ void bf16x4_to_e4m3(uint32_t w0, uint32_t w1, uint32_t pow2, uint32_t &p, uint32_t &r) {
+    uint16_t p0, p1, r0, r1;
+    e4m3_pieces(w0, pow2, p0, r0);
+    e4m3_pieces(w1, pow2, p1, r1);
+    asm("mov.b32 %0, {%1, %2};" : "=r"(p) : "h"(p0), "h"(p1));
+    asm("mov.b32 %0, {%1, %2};" : "=r"(r) : "h"(r0), "h"(r1));
 }
 // Four e4m3 codes to F16, exactly; the NaN codes (rows that no query sees may hold
 // any byte) become a finite value.
@@ -600,29 +598,35 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         };
         bool ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_QFULL), 0));
         auto q_at = [&](int i) { return base + (i < NQT ? C::OFF_QST + i * CH : C::OFF_Q + (i - NQT) * CH) + row * 128; };
-        float q_pow = 1.f, q_back = 1.f;
+        uint32_t q_pow = 0;   // FP8: the row's power of two, a pair of BF16
+        float q_back = 1.f;
         if (FP8) {
-            // the row's largest finite magnitude, as BF16 bits
-            uint32_t m = 0;
+            uint32_t m = 0;  // the row's largest magnitude; NaN if there is one
             if (ok) {
-                auto fin = [](uint32_t w) {
-                    const uint32_t x = w & 0x7fff7fffu;
-                    return x & __vcmpltu2(x, 0x7f807f80u);
-                };
-                for (int i = 2 * hf + kh; i < NK; i += 4)
 #pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        const uint4 v = ld_shared_v4(q_at(i) + ((u ^ (row & 7)) << 4));
-                        m = __vmaxu2(m, __vmaxu2(__vmaxu2(fin(v.x), fin(v.y)), __vmaxu2(fin(v.z), fin(v.w))));
+                for (int n = 0; n < 3; ++n) {
+                    const int i = 2 * hf + kh + 4 * n;
+                    if (i < NK) {
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) {
+                            const uint4 v = ld_shared_v4(q_at(i) + ((u ^ (row & 7)) << 4));
+                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[e] & 0x7fff7fffu));
+                        }
                     }
+                }
             }
-            xm[tid] = __uint_as_float(max(m & 0xffffu, m >> 16) << 16);
+            // bits of magnitudes are in their order, infinities and NaN above all
+            uint32_t *um = reinterpret_cast<uint32_t *>(smem + C::OFF_XM);
+            um[tid] = max(m & 0xffffu, m >> 16);
             named_bar_sync(1, 32 * NSW);
-            const uint32_t top = __float_as_uint(fmaxf(fmaxf(xm[row], xm[row + 64]), fmaxf(xm[row + 128], xm[row + 192])));
+            const uint32_t top = max(max(um[row], um[row + 64]), max(um[row + 128], um[row + 192]));
             named_bar_sync(1, 32 * NSW);
-            // times 2^k it lies in (224, 448]
-            const int k = min(135 - (int)(top >> 23) - ((top & 0x7fffffu) > 0x600000u), 126);
-            q_pow = __uint_as_float((uint32_t)(k + 127) << 23);
+            // times 2^k it lies in (224, 448]; a row that is not finite becomes NaN
+            const int k = min(135 - (int)(top >> 7) - ((top & 0x7fu) > 0x60u), 126);
+            q_pow = top >= 0x7f80u ? 0x7fc07fc0u : (uint32_t)(k + 127) * 0x00800080u;
             q_back = __uint_as_float((uint32_t)(127 - k) << 23);
         }
         if (ok && nsteps > 0) {
