@@ -587,6 +587,57 @@ def test_attention_peaked_and_flat(factor, scale):
         c.close()
 
 
+def test_attention_fp8_scales_of_many_magnitudes():
+    """Weights are even (a tiny factor), so every row's values count by its scale:
+    scales that grow and fall over the pages, negative ones, zeros, the smallest one."""
+    L = 1300
+    c = Cache("fp8", [L, L, L])
+    g = torch.Generator().manual_seed(82)
+    ramp = torch.linspace(-30, 12, L)
+    for r, e in enumerate((ramp, -ramp - 20, torch.randint(-18, 19, (L,), generator=g).float())):
+        s = torch.exp2(e) * torch.where(torch.rand(L, generator=g) < 0.3, -1.0, 1.0)
+        if r == 2:
+            s[::5], s[1::5] = 0.0, 2.0 ** -126
+        at = torch.tensor([c.row(r, i) for i in range(L)], device="cuda")
+        c.pool.gpu_scales()[at] = s.cuda()
+    q = normal(83, 3, 2, 24, P.DIM)
+    out, lse = attend(c, q, None, scale=2.0 ** -30)
+    check(c, q, out, lse, lambda b, t: None, scale=2.0 ** -30)
+    c.pool.gpu_scales().zero_()
+    out, lse = attend(c, q, None)
+    check(c, q, out, lse, lambda b, t: None)
+    c.close()
+
+
+def test_attention_fp8_queries_with_outliers():
+    """A query's values are the sums of two e4m3 codes each, at a power of two that
+    brings the row's largest to (224, 448]: values of at least 2^-10 of the largest are
+    exact, and smaller ones off by at most half the codes' smallest step, 2^-10 / 224 of
+    the largest. Rows of very different magnitudes do not touch each other."""
+    L = 700
+    c = Cache("fp8", [L])
+    q = normal(84, 1, 2, 32, P.DIM)
+    big = 2.0 ** torch.arange(0, 8).float()
+    for h in range(32):
+        q[0, :, h, 37 * h % 576] = float(big[h % 8]) * 3
+    q[0, 0, 8:16] *= 2.0 ** -40
+    q[0, 0, 16] = 0.0
+    q[0, 0, 17, 5], q[0, 0, 18, 7], q[0, 0, 19, 9] = math.inf, -math.inf, math.nan
+    out, lse = attend(c, q, None)
+    broken = [17, 18, 19]
+    assert bool(torch.isnan(out[0, 0, broken]).all()) and bool(torch.isnan(lse[0, 0, broken]).all())
+    for t in range(2):
+        heads = [h for h in range(32) if t or h not in broken]
+        kv = c.kv(0, torch.arange(L - 1 + t))
+        for h in heads:
+            x = q[0, t, h:h + 1].double()
+            ref = P.attention(x, kv, torch.ones(len(kv), dtype=torch.bool, device="cuda"), SCALE)
+            small = (x[0].abs() < 2.0 ** -10 * x.abs().max()).double()
+            lost = SCALE * float(x.abs().max()) * 2.0 ** -10 / 224 * float((kv.abs() @ small).max())
+            P.check_attention(out[0, t, h:h + 1], lse[0, t, h:h + 1], *ref[:3], ref[3] + lost * 2.0 ** 16, what=f"{t} {h}")
+    c.close()
+
+
 def test_attention_skips_entries_it_cannot_read():
     c = Cache("bf16", [300, 300])
     hs = c.hs

@@ -17,31 +17,41 @@
 //      ring of chunk slots that S frees at once;
 //   V: CTA r supplies the value columns 128 r + {0..127, 256..383} of both pages,
 //      loaded apart (the second reading comes from L2) into a buffer that PV frees.
-// An MMA of 128 keys takes 45 clocks (256 value columns: 64), so a step is
-// 36 x 45 + 16 x 64 = 2.7k clocks; an earlier form, one CTA per half of the value
-// columns and both computing S, was bound by the issue of its 80 smaller MMAs per
-// 128 keys and by their operands' shared-memory reads.
+// Bound: an MMA of 128 keys takes 45 clocks (256 value columns: 64), so a step is
+// 36 x 45 + 16 x 64 = 2.7k clocks, and its shared-memory traffic (the MMAs' operands,
+// the copies, FP8's conversions) about as many at 128 bytes a clock. Measured: BF16
+// 2.8k-3.1k clocks a step (8 x 32 tokens x 128 heads over 16,384 rows: 757 us, 1.39
+// PFLOP/s), FP8 3.2k (4 x 8 tokens x 16 heads over 131,072 rows: 113 us). An earlier
+// form, one CTA per half of the value columns and both computing S, was bound by the
+// issue of its 80 smaller MMAs per 128 keys and by their operands' shared-memory reads.
 // Roles in each CTA:
 //   warps 0, 3  producers: the K chunks and the V chunks of each step by TMA;
 //   warp 1      (CTA 0) MMA issuer for both CTAs: S_j = Q K_j^T, then
 //               O += P_{j-1} V_{j-1}, during which the softmax reads S_j;
 //   warps 4-11  softmax: thread = (row, page of the step, half of its keys): mask,
-//               online softmax with a conditional rescale, P as BF16 to shared
-//               memory; epilogue;
-//   warps 12-19 (FP8) converters: the e4m3 codes of the landed chunks to F16, four
-//               warps for K's chunks and four for V's.
-// FP8: the MMAs run on F16, which every e4m3 code is exactly and to which the
-// hardware converts two codes per instruction (24 against 72 clocks per 16 codes
-// and warp for placing BF16 bits with integer instructions, which bound the loop).
-//   Q: the CTA's BF16 values times a power of two that brings the largest to
-//      [2^14, 2^15): exact down to 2^-29 of that largest, off by at most 2^-40 of
-//      it below.
-//   P: in log2 units, t = score + log2|scale| is the weight of a row's codes; a
-//      query row keeps a reference for t as it does for the scores, and
-//      P = 2^7 exp2(t - reference) <= 2^15. F16 rounds it by at most 2^-11 of it or
-//      2^-32 of the row's largest. The probabilities' sum has the unrounded ones.
-//   Warp 2 turns each step's scales into the two numbers per key that the softmax
-//   uses (scale times the scores' factor, log2|scale|).
+//               online softmax with a conditional rescale, P as BF16 (FP8: F16)
+//               to shared memory; epilogue;
+//   warp 2      (FP8) the largest of the landed scales, by 32 keys;
+//   warps 12-19 (FP8) converters: V's e4m3 codes to F16, four warps for either half
+//               of the columns.
+// FP8: S is taken from the e4m3 codes themselves (kind::f8f6f4), so K needs no
+// conversion (with K's chunks converted to F16 like V's, the shared-memory traffic and
+// the converters' issue made a step 4.0k clocks: 44 against 36 us for 16 x 4 lists of
+// 2,048 rows of 128 heads).
+//   Q: a value times the row's power of two, which brings the row's largest to
+//      (224, 448], is the sum of two e4m3 codes, and an MMA of depth 32 takes either
+//      with the same keys: as many MMAs as one of F16. Values of at least 2^-10 of the
+//      row's largest are exact, smaller ones off by at most 2^-17.8 of that largest. A
+//      row that is not finite becomes NaN.
+//   V: F16, which every code is exactly and to which the hardware converts two codes
+//      per instruction (24 against 72 clocks per 16 codes and warp for placing BF16
+//      bits with integer instructions). Two e4m3 codes per weight would spare this
+//      too, but lose small weights below 2^-10 of the codes' unit.
+//   P: F16, 16 exp2(score - reference) * scale / c, c a power of two that a query row
+//      keeps for the scales as it does the reference for the scores: c is raised where
+//      a scale passes 8 c, so P <= 2^15, exact to 2^-11 of it down to weights of 2^-18
+//      of the largest and off by at most 2^-29 of that below. The probabilities' sum
+//      has the unrounded ones.
 // Every wait is bounded; on expiry the kernel sets HS_DEVERR_TIMEOUT, drains its
 // own copies and MMAs and returns.
 #include <cuda_bf16.h>
@@ -81,7 +91,7 @@ struct PCfg {
     // value chunks in twos (fewer waits and copies to issue)
     static constexpr int GK = FP8 ? 3 : 2;
     static constexpr int GV = 4;              // FP8: V chunks converted together (half the columns)
-    static constexpr int NXG = FP8 ? 4 : 4;   // groups of K chunks; BF16: group 0 is the rope's
+    static constexpr int NXG = 4;             // groups of K chunks; BF16: group 0 is the rope's
     static constexpr int NCV = FP8 ? 4 : 0;   // groups of V codes: two per half of the columns
     static constexpr int XB = FP8 ? NXG * GK * CCH : (2 * NXG - 1) * CH;  // bytes of K chunks
     static constexpr int RK = FP8 ? NXG : NXG - 1, RV = FP8 ? NCV : NV;  // the producers' rings
@@ -1272,7 +1282,7 @@ hs_status launch_pages(int dev, cudaStream_t s, const CUtensorMap &tq, const CUt
     }
     // Two splits joined inside a cluster, where all clusters run at once and the model
     // says so: 1.5 us instead of the second grid's 3.5 and the partials' bytes
-    // (32 lists of 2,048 rows: INSIDE against 32.0 us). Four splits in a cluster of
+    // (32 lists of 2,048 rows, 128 heads: 28.2 against 32.0 us). Four splits in a cluster of
     // eight CTAs were slower than eight splits and the second grid.
     if (pl.nsplit > 1) {
         const int64_t steps = ((p.N < 1 ? p.max_pages : p.N) + 1) / 2, units = (int64_t)p.lists * pl.mtiles;
