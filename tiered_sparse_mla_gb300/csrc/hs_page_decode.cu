@@ -884,7 +884,16 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         // rows that see nothing: out 0, lse -inf
         const float inv = l == 0.f ? 0.f : __fdividef(FP8 ? cref * 0.0625f : 1.f, l);
         const bool one = p.nsplit == 1;
-        if (ok && (one || nsteps > 0)) {
+        // The columns that the other split joins go there as they are staged, once all
+        // CTAs are done with the memory they land in (where nothing was computed, what
+        // is sent is not used).
+        const uint32_t other = crank ^ 2u;
+        uint32_t theirs = 0;
+        if (p.inside) {
+            cluster_wait();
+            theirs = hs::dsmem_map(smem + C::OFF_BAR + 8 * C::B_JOIN, other);
+        }
+        if (p.inside || (ok && (one || nsteps > 0))) {
             // O / l through shared memory, idle by now, in 32-row boxes of 128
             // swizzled bytes per row: this thread's value columns are
             // 256 hf + 128 kh + (0..127). Rows past M are clipped by the map.
@@ -923,9 +932,17 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                                      __float_as_uint(__uint_as_float(o[4 * u + 1]) * inv),
                                      __float_as_uint(__uint_as_float(o[4 * u + 2]) * inv),
                                      __float_as_uint(__uint_as_float(o[4 * u + 3]) * inv));
+                    if (p.inside && hf != split) {
+                        fence_proxy_async();
+                        __syncwarp();
+                        const int box = 4 * kh + cc;
+                        if (lane == 0)
+                            bulk_push(hs::dsmem_map(smem + C::join_box(box) + wr * 4096, other),
+                                      base + C::OFF_V + (uint32_t)(8 * hf + box) * 8192u + wr * 4096, 4096, theirs);
+                    }
                 }
             }
-            fence_proxy_async();
+            if (!p.inside) fence_proxy_async();
             __syncwarp();
             if (lane == 0 && !p.inside) {
                 const int wide = one ? 64 : 32;
@@ -949,26 +966,12 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             else
                 reinterpret_cast<float *>(smem + C::OFF_P)[row] = lse;  // P is done with
         }
-        if (p.inside) {
-            // The columns that the other split joins go there, with this split's lse, as
-            // soon as its CTA is done with the memory they land in: four boxes of this
-            // warp's 32 rows (what was not computed is sent too, and not used).
-            cluster_wait();
+        if (p.inside && kh == 0 && hf == 0) {
             fence_proxy_async();
             __syncwarp();
-            const uint32_t other = crank ^ 2u;
             const int wr = wq & 1;
-            if (lane == 0) {
-                const uint32_t theirs = hs::dsmem_map(smem + C::OFF_BAR + 8 * C::B_JOIN, other);
-                if (hf != split) {
-#pragma unroll 1
-                    for (int i = 4 * kh; i < 4 * kh + 4; ++i)
-                        bulk_push(hs::dsmem_map(smem + C::join_box(i) + wr * 4096, other),
-                                  base + C::OFF_V + (uint32_t)(8 * hf + i) * 8192u + wr * 4096, 4096, theirs);
-                }
-                if (kh == 0 && hf == 0)
-                    bulk_push(hs::dsmem_map(smem + C::OFF_P + 1024 + wr * 128, other), base + C::OFF_P + wr * 128, 128, theirs);
-            }
+            if (lane == 0)
+                bulk_push(hs::dsmem_map(smem + C::OFF_P + 1024 + wr * 128, other), base + C::OFF_P + wr * 128, 128, theirs);
             __syncwarp();
         }
     } else if (FP8 && warp >= 4 + NSW) {
@@ -1038,6 +1041,10 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         bool ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_JOIN), 0));
         __syncthreads();
         if (!ok && lane == 0) fail();
+        __syncwarp();
+        // What was sent has been read, and nothing more comes: the others may end once
+        // this CTA has come here.
+        cluster_arrive_relaxed();
         const float *lses = reinterpret_cast<const float *>(smem + C::OFF_P);
         float *wts = reinterpret_cast<float *>(smem + C::OFF_P + 2048);  // [rows]: own, the other's
         if (threadIdx.x < RM) {
@@ -1055,7 +1062,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 p.lse[(size_t)list * p.M + mg] = nan ? inv : (sum > 0.f ? mx + __logf(sum) : -INFINITY);
         }
         __syncthreads();
-#pragma unroll 2
+#pragma unroll 4
         for (int i = threadIdx.x; i < RM * 64; i += C::THREADS) {  // four columns each
             const int row = i >> 6, box = (i >> 3) & 7, mg = mt * BM + RM * rank + row;
             if (mg >= p.M) continue;
@@ -1072,7 +1079,9 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync_relaxed();  // no CTA leaves while the other's MMAs or arrivals may reach it
+    // no CTA leaves while the other's MMAs or arrivals may reach it
+    if (!p.inside) cluster_arrive_relaxed();
+    cluster_wait();
     tc_fence_after();
     if (warp == 2) tmem_dealloc2(tmem, 512);
 }
