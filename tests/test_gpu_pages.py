@@ -753,6 +753,61 @@ def test_step_eager_captured_and_on_another_stream(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("B,T,H,ctx", [(1, 3, 16, 9000), (30, 1, 16, 1500), (3, 40, 128, 700), (2, 64, 24, 333)])
+def test_plans_of_every_kind_captured_and_at_once(dtype, B, T, H, ctx):
+    """Splits joined by a second kernel, inside a cluster, and no splits: captured and
+    replayed with new queries, masks and lengths; two calls at once on two streams."""
+    c = Cache(dtype, [ctx - 7 * b for b in range(B)])
+    g = torch.Generator().manual_seed(90)
+
+    def trees(n):
+        return torch.randint(-2 ** 63, 2 ** 63 - 1, (n, T), generator=g).cuda()
+
+    def buffers(seed):
+        return {"q": normal(seed, B, T, H, P.DIM), "tree": trees(B), "req": torch.arange(B, **I32),
+                "out": torch.empty(B, T, H, 512, dtype=torch.bfloat16, device="cuda"),
+                "lse": torch.empty(B, T, H, device="cuda"),
+                "ws": torch.empty(max(1, c.hs.hs_page_decode_workspace_bytes(B, T, H, c.P)), dtype=torch.uint8,
+                                  device="cuda")}
+
+    def call(x):
+        c.pool.page_mla_decode(x["q"], None, x["req"], x["tree"], SCALE, x["out"], x["lse"], x["ws"])
+
+    a, b = buffers(91), buffers(92)
+    call(a)
+    torch.cuda.synchronize()
+    check(c, a["q"], a["out"], a["lse"], lambda i, t: None, a["tree"])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(a)
+        call(a)
+    for step in range(2):
+        a["q"].copy_(normal(93 + step, B, T, H, P.DIM))
+        a["tree"].copy_(trees(B))
+        c.set_ctx([n - 1 for n in c.ctx])
+        a["out"].fill_(math.nan)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        check(c, a["q"], a["out"], a["lse"], lambda i, t: None, a["tree"])
+    alone = a["out"].clone(), a["lse"].clone()
+    call(b)
+    torch.cuda.synchronize()
+    other = b["out"].clone(), b["lse"].clone()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(4):
+        with torch.cuda.stream(s1):
+            graph.replay()
+        with torch.cuda.stream(s2):
+            call(b)
+    torch.cuda.synchronize()
+    for got, want in ((a, alone), (b, other)):
+        assert torch.equal(got["out"].view(torch.int16), want[0].view(torch.int16))
+        assert torch.equal(got["lse"], want[1])
+    c.close()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
 def test_selected_positions_through_the_tiered_path(dtype):
     """The selection's positions, resolved as a union and attended to row by row, give
     what attention over the pages gives (same rows, other kernels)."""

@@ -121,6 +121,16 @@ __device__ __forceinline__ uint4 ld_stream_v4(const void *p) {
                  : "l"(p));
     return v;
 }
+// The same for what the stream's previous kernel may still be writing when this one
+// is launched: not through the read-only path.
+__device__ __forceinline__ uint4 ld_once_v4(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
 __device__ __forceinline__ uint4 ld_v4(const void *p) {
     uint4 v;
     asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];\n"

@@ -1093,8 +1093,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 // a block per row with four groups of threads, 0.6 us).
 constexpr int JU = 8;
 __global__ void __launch_bounds__(256)
-join_kernel(const float *__restrict__ ws_o, const float *__restrict__ ws_lse, int nsplit, int rows,
-            __nv_bfloat16 *__restrict__ out, float *__restrict__ lse) {
+join_kernel(const float *ws_o, const float *ws_lse, int nsplit, int rows, __nv_bfloat16 *out, float *lse) {
     grid_dep_wait();  // the splits' partials
     grid_dep_launch();
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;

@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(AT) append_kernel(const AppendParams p) {
     if (go) {
         const uint8_t *s = p.src + ((size_t)b * p.T + from) * (2 * kDim) + part * 16;
 #pragma unroll
-        for (int u = 0; u < 9; ++u) v[u] = hs::ld_stream_v4(s + 128 * u);
+        for (int u = 0; u < 9; ++u) v[u] = hs::ld_once_v4(s + 128 * u);
     } else {
 #pragma unroll
         for (int u = 0; u < 9; ++u) v[u] = make_uint4(0u, 0u, 0u, 0u);
@@ -180,11 +180,9 @@ constexpr int MT = 288;
 
 template <bool FP8>
 __global__ void __launch_bounds__(MT)
-means_kernel(const uint8_t *__restrict__ rows, const float *__restrict__ scales,
-             const uint8_t *__restrict__ host_rows, const float *__restrict__ host_scales,
-             const int2 *__restrict__ page, const int32_t *__restrict__ ctx, int max_req,
-             int max_pages, const int32_t *__restrict__ req, const int32_t *__restrict__ pg,
-             __nv_bfloat16 *__restrict__ means, uint32_t *__restrict__ err) {
+means_kernel(const uint8_t *rows, const float *scales, const uint8_t *host_rows, const float *host_scales,
+             const int2 *page, const int32_t *ctx, int max_req, int max_pages, const int32_t *req,
+             const int32_t *pg, __nv_bfloat16 *means, uint32_t *err) {
     constexpr int RB = FP8 ? kDim : 2 * kDim;
     constexpr int V = RB / 16;       // pieces of a row: 72, or 36
     constexpr int G = MT / V;        // row groups: 4, or 8
@@ -215,7 +213,7 @@ means_kernel(const uint8_t *__restrict__ rows, const float *__restrict__ scales,
         v[u] = make_uint4(0u, 0u, 0u, 0u);
         sc[u] = 0.f;
         if (k < n) {  // rows past the context hold no token and are not read
-            v[u] = hs::ld_stream_v4(src + (size_t)k * RB + piece * 16);
+            v[u] = hs::ld_once_v4(src + (size_t)k * RB + piece * 16);
             if (FP8) sc[u] = (dev ? scales : host_scales)[row0 + k];
         }
     }
@@ -258,8 +256,9 @@ means_kernel(const uint8_t *__restrict__ rows, const float *__restrict__ scales,
     }
 }
 
-// A launch that may begin while the stream's previous kernel still runs (the
-// kernels wait for it before they read or write anything).
+// A launch that may begin while the stream's previous kernel still runs (the kernels
+// wait for it before they read or write anything, and read nothing through the
+// read-only path, which may hold or fetch what was there before).
 template <typename... P, typename... A>
 hs_status launch(void (*kernel)(P...), unsigned grid, int threads, void *stream, A... args) {
     cudaLaunchConfig_t cfg = {};
