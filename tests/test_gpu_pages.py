@@ -577,6 +577,23 @@ def test_attention_of_medium_batches(dtype, B, T, H):
     c.close()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("B,T,H", [(80, 1, 128), (27, 3, 128), (40, 2, 80), (79, 1, 3)])
+def test_attention_of_more_lists_than_fit_at_once(dtype, B, T, H):
+    """Most lists whole, those of the last round in splits: a list may have tiles of both."""
+    lens = [1500 - 17 * b if b % 5 else (1, 64, 70, 0, T)[b % 4] for b in range(B)]
+    c = Cache(dtype, lens, max_ctx=1536)
+    q = normal(85, B, T, H, P.DIM)
+    out, lse = attend(c, q, None)
+    check(c, q, out, lse, lambda b, t: None)
+    tree = torch.randint(-2 ** 63, 2 ** 63 - 1, (B, T), generator=torch.Generator().manual_seed(86)).cuda()
+    out, lse = attend(c, q, None, tree)
+    check(c, q, out, lse, lambda b, t: None, tree)
+    again = attend(c, q, None, tree)
+    assert torch.equal(out.view(torch.int16), again[0].view(torch.int16)) and torch.equal(lse, again[1])
+    c.close()
+
+
 @pytest.mark.parametrize("factor,scale", [(8.0, SCALE), (32.0, SCALE), (2.0 ** -20, SCALE * 2.0 ** 20), (0.0, SCALE)])
 def test_attention_peaked_and_flat(factor, scale):
     for dtype in ("bf16", "fp8"):

@@ -137,7 +137,9 @@ struct PageParams {
     float *lse, *ws_lse;
     uint32_t *err;
     int inside;            // 2: the two splits are joined inside the cluster; or 0
-    int T, H, N, M, lists, nsplit, max_req, max_pages, zero_block;
+    int T, H, N, M, mtiles, nsplit, max_req, max_pages, zero_block;
+    int n_full;            // units (128 query rows of a list) not split; the others are, nsplit ways
+    int ws_list0, ws_lists;  // the lists that the partials' space holds
     int tpl;               // lists per request: list i is token i % tpl of request i / tpl
     float scale_log2;
 };
@@ -235,7 +237,7 @@ template <bool FP8>
 __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
 page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k1,
                    const __grid_constant__ CUtensorMap tm_k2, const __grid_constant__ CUtensorMap tm_o,
-                   const PageParams p) {
+                   const __grid_constant__ CUtensorMap tm_w, const PageParams p) {
     using C = PCfg<FP8>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = hs::smem_addr(smem_raw);
@@ -245,7 +247,11 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     // a cluster is one pair of CTAs, or both splits' pairs
     const uint32_t crank = hs::cluster_ctarank(), pair0 = crank & ~1u;
     const int rank = static_cast<int>(crank & 1u);
-    const int split = blockIdx.x >> 1, mt = blockIdx.y, list = blockIdx.z;
+    // whole units first, then the others' splits
+    const int pair = blockIdx.x >> 1, past = pair - p.n_full;
+    const int nsplit = past < 0 ? 1 : p.nsplit, split = past < 0 ? 0 : past % p.nsplit;
+    const int unit = past < 0 ? pair : p.n_full + past / p.nsplit;
+    const int list = unit / p.mtiles, mt = unit - list * p.mtiles;
     volatile int32_t *misc = reinterpret_cast<volatile int32_t *>(smem + C::OFF_MISC);
     volatile int32_t *ring_pg = reinterpret_cast<volatile int32_t *>(smem + C::OFF_PG);
     auto bar = [&](int i) { return base + C::OFF_BAR + 8u * (uint32_t)i; };
@@ -336,8 +342,8 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         // splits begin at even entries: a step is two pages
         const long long steps = (end + 1) / 2;
-        const int z = (int)(steps * (split + 1) / p.nsplit);
-        first = (int)(steps * split / p.nsplit);
+        const int z = (int)(steps * (split + 1) / nsplit);
+        first = (int)(steps * split / nsplit);
         nsteps = z - first;
         first *= 2;
         npages = L <= 0 ? 0 : (L - 1) / kPage + 1;
@@ -883,7 +889,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         l = (xm[row] + xm[row + 64]) + (xm[row + 128] + xm[row + 192]);
         // rows that see nothing: out 0, lse -inf
         const float inv = l == 0.f ? 0.f : __fdividef(FP8 ? cref * 0.0625f : 1.f, l);
-        const bool one = p.nsplit == 1;
+        const bool one = nsplit == 1;
         // The columns that the other split joins go there as they are staged, once all
         // CTAs are done with the memory they land in (where nothing was computed, what
         // is sent is not used).
@@ -946,10 +952,11 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             __syncwarp();
             if (lane == 0 && !p.inside) {
                 const int wide = one ? 64 : 32;
-                const int z = one ? list : split * p.lists + list;
+                const int z = one ? list : split * p.ws_lists + list - p.ws_list0;
+                const CUtensorMap *to = one ? &tm_o : &tm_w;
                 const int c0 = 256 * hf + 128 * kh;
                 for (int c = c0; c < c0 + 128; c += wide)
-                    tma_store_3d(&tm_o, base + C::OFF_V + (uint32_t)(c / wide) * 8192u + wr * 4096, c,
+                    tma_store_3d(to, base + C::OFF_V + (uint32_t)(c / wide) * 8192u + wr * 4096, c,
                                  mt * BM + RM * rank + 32 * wr, z);
                 asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                 // the stores have read shared memory before the CTA may end
@@ -962,7 +969,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (one)
                 p.lse[(size_t)list * p.M + mg] = lse;
             else if (!p.inside)
-                p.ws_lse[((size_t)split * p.lists + list) * p.M + mg] = lse;
+                p.ws_lse[((size_t)split * p.ws_lists + list - p.ws_list0) * p.M + mg] = lse;
             else
                 reinterpret_cast<float *>(smem + C::OFF_P)[row] = lse;  // P is done with
         }
@@ -1087,17 +1094,19 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 }
 
 // Joins the splits: out = sum_s w_s O_s / sum_s w_s, w_s = exp(lse_s - max), in a
-// fixed order. Four columns of a row per thread, JU splits at a time, whose loads are
-// all issued before the first is used; between them the sums move to the larger
-// maximum (8 splits of 112 rows: 4 and 16 at a time made a call 0.15 and 1.2 us longer;
-// a block per row with four groups of threads, 0.6 us).
-constexpr int JU = 8;
+// fixed order, for the rows from `skip` on of the partials' space. Four columns of a row per
+// thread, JU splits at a time, whose loads are all issued before the first is used;
+// between them the sums move to the larger maximum. JU: 2, 4 or 8, the smallest that
+// takes all splits at once (8 splits of 112 rows: 4 and 16 at a time made a call 0.15 and
+// 1.2 us longer, a block per row with four groups of threads 0.6 us; two splits of
+// 32,768 rows: 8 at a time, whose registers leave fewer threads, 20 us longer than 2).
+template <int JU>
 __global__ void __launch_bounds__(256)
-join_kernel(const float *ws_o, const float *ws_lse, int nsplit, int rows, __nv_bfloat16 *out, float *lse) {
+join_kernel(const float *ws_o, const float *ws_lse, int nsplit, int rows, int skip, __nv_bfloat16 *out, float *lse) {
     grid_dep_wait();  // the splits' partials
     grid_dep_launch();
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t row = i >> 7;
+    const int64_t row = (i >> 7) + skip;
     const int c = (int)(i & 127) * 4;
     if (row >= rows) return;
     float mx = -INFINITY, sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
@@ -1146,38 +1155,50 @@ join_kernel(const float *ws_o, const float *ws_lse, int nsplit, int rows, __nv_b
 
 // ---------------------------------------------------------------- host side
 struct PagePlan {
-    int M, mtiles, nsplit;
+    int M, mtiles, nsplit, n_full, list0;
     double us;  // the model's time
     size_t ws_o_bytes, ws_bytes;
 };
 
-// A model of the launch's time, in us: two pages take a pair of CTAs about 1.9,
-// their start and epilogue 6.5.
-constexpr double US_STEP = 1.9, US_ENDS = 6.5;
+// A model of the launch's time, in us: two pages take a pair of CTAs about 1.6,
+// their start and epilogue 7.
+constexpr double US_STEP = 1.6, US_ENDS = 7.0;
 
 // Splits of a list of N pages joined through the workspace by a second grid: the
 // count that the model makes shortest; the join is 3.5 us and about 5 MB of
-// partials written and read per us.
+// partials written and read per us. Where there are more units than pairs of CTAs at
+// once, those of the last, partly filled round may be split by themselves
+// (8 x 32 tokens of 128 heads, 256 units on 76 pairs, 16,384 rows: MIXED us a call
+// against 757 with all units in two).
 PagePlan page_plan(int64_t lists, int64_t T, int64_t H, int64_t N) {
     PagePlan pl{};
     pl.M = (int)(T * H);
     pl.mtiles = (pl.M + BM - 1) / BM;
-    const int64_t sms = sm_count(), units = lists * pl.mtiles * 2;
+    const int64_t pairs = sm_count() / 2 > 0 ? sm_count() / 2 : 1, units = lists * pl.mtiles;
     const int64_t steps = (N + 1) / 2, most = steps < 128 ? steps : 128;
     pl.us = 1e300;
     pl.nsplit = 1;
-    for (int64_t ns = 1; ns <= most; ++ns) {
-        const double waves = (double)((units * ns + sms - 1) / sms);
-        double t = waves * ((double)((steps + ns - 1) / ns) * US_STEP + US_ENDS);
-        if (ns > 1) t += 3.5 + (double)ns * lists * pl.M * 512 * 8 / 5e6;
-        if (t < pl.us * 0.98) {
-            pl.us = t;
-            pl.nsplit = (int)ns;
-        }
-        if (units * ns > 8 * sms) break;
+    auto rounds = [&](int64_t u, int64_t ns) {
+        return (double)((u * ns + pairs - 1) / pairs) * ((double)((steps + ns - 1) / ns) * US_STEP + US_ENDS);
+    };
+    auto join = [&](int64_t rows, int64_t ns) { return ns > 1 ? 3.5 + (double)ns * rows * 512 * 8 / 5e6 : 0.0; };
+    auto consider = [&](double t, int64_t full, int64_t ns) {
+        if (t >= pl.us * 0.98) return;
+        pl.us = t;
+        pl.nsplit = (int)ns;
+        pl.n_full = (int)full;
+    };
+    for (int64_t ns = 1; ns <= most || ns == 1; ++ns) {
+        consider(rounds(units, ns) + join(lists * pl.M, ns), 0, ns);
+        if (units * ns > 8 * pairs) break;
     }
+    const int64_t rest = units % pairs;
+    if (units > pairs && rest)
+        for (int64_t ns = 2; ns <= most && rest * ns <= 8 * pairs; ++ns)
+            consider(rounds(units - rest, 1) + rounds(rest, ns) + join(rest * BM, ns), units - rest, ns);
+    pl.list0 = pl.n_full / pl.mtiles;
     if (pl.nsplit > 1) {
-        const size_t rows = (size_t)pl.nsplit * lists * pl.M;
+        const size_t rows = (size_t)pl.nsplit * (lists - pl.list0) * pl.M;
         pl.ws_o_bytes = (rows * 512 * sizeof(float) + 255) & ~size_t(255);
         pl.ws_bytes = pl.ws_o_bytes + ((rows * sizeof(float) + 255) & ~size_t(255));
     }
@@ -1227,7 +1248,7 @@ int clusters_of_four(int dev) {
 
 template <bool FP8>
 hs_status launch_pages(int dev, cudaStream_t s, const CUtensorMap &tq, const CUtensorMap &k1,
-                       const CUtensorMap &k2, const void *d_out, void *ws, const PagePlan &pl, PageParams p) {
+                       const CUtensorMap &k2, int64_t units, const void *d_out, void *ws, const PagePlan &pl, PageParams p) {
     static std::atomic<int> state[64];
     if (dev < 0 || dev >= 64) return HS_ERR_UNSUPPORTED;
     if (state[dev].load(std::memory_order_acquire) != 1) {
@@ -1240,19 +1261,25 @@ hs_status launch_pages(int dev, cudaStream_t s, const CUtensorMap &tq, const CUt
     // (32 lists of 2,048 rows, 128 heads: 28.2 against 32.0 us). Four splits in a cluster of
     // eight CTAs were slower than eight splits and the second grid.
     if (pl.nsplit > 1) {
-        const int64_t steps = ((p.N < 1 ? p.max_pages : p.N) + 1) / 2, units = (int64_t)p.lists * pl.mtiles;
+        const int64_t steps = ((p.N < 1 ? p.max_pages : p.N) + 1) / 2;
         const double t = (double)((steps + 1) / 2) * US_STEP + US_ENDS + 1.5;
         if (steps >= 2 && t < pl.us && units <= clusters_of_four<FP8>(dev)) p.inside = p.nsplit = 2;
     }
-    const bool one = p.nsplit == 1;
-    // the output (one split), or the splits' f32 partials
-    CUtensorMap to;
-    if (!make_map(&to, one ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
-                  one || p.inside ? d_out : ws, 512, pl.M, (uint64_t)p.lists * (one || p.inside ? 1 : p.nsplit),
-                  one ? 1024 : 2048, one ? 64 : 32, 32, CU_TENSOR_MAP_SWIZZLE_128B))
+    if (p.inside) p.n_full = 0;
+    const int64_t lists = (int64_t)units / pl.mtiles;
+    // the output (units of one split), and the splits' f32 partials
+    CUtensorMap to, tw;
+    const bool direct = p.nsplit == 1 || p.n_full > 0, split = p.nsplit > 1 && !p.inside;
+    if (direct && !make_map(&to, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d_out, 512, pl.M, lists, 1024, 64, 32,
+                            CU_TENSOR_MAP_SWIZZLE_128B))
         return HS_ERR_CUDA;
+    if (split && !make_map(&tw, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, ws, 512, pl.M, (uint64_t)p.ws_lists * p.nsplit, 2048, 32,
+                           32, CU_TENSOR_MAP_SWIZZLE_128B))
+        return HS_ERR_CUDA;
+    if (!direct) to = split ? tw : tq;  // not used
+    if (!split) tw = to;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * p.nsplit, pl.mtiles, (unsigned)p.lists);
+    cfg.gridDim = dim3((unsigned)(2 * (p.n_full + (units - p.n_full) * p.nsplit)), 1, 1);
     cfg.blockDim = dim3(PCfg<FP8>::THREADS, 1, 1);
     cfg.dynamicSmemBytes = PCfg<FP8>::SMEM_ALLOC;
     cfg.stream = s;
@@ -1265,11 +1292,11 @@ hs_status launch_pages(int dev, cudaStream_t s, const CUtensorMap &tq, const CUt
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, page_decode_kernel<FP8>, tq, k1, k2, to, p) != cudaSuccess) return HS_ERR_CUDA;
-    if (one || p.inside) return HS_OK;
-    const int n = p.lists * pl.M;
+    if (cudaLaunchKernelEx(&cfg, page_decode_kernel<FP8>, tq, k1, k2, to, tw, p) != cudaSuccess) return HS_ERR_CUDA;
+    if (!split) return HS_OK;
+    const int n = p.ws_lists * pl.M, skip = (p.n_full % pl.mtiles) * BM;
     cudaLaunchConfig_t cc = {};
-    cc.gridDim = dim3((unsigned)(((int64_t)n * 128 + 255) / 256), 1, 1);
+    cc.gridDim = dim3((unsigned)(((int64_t)(n - skip) * 128 + 255) / 256), 1, 1);
     cc.blockDim = dim3(256, 1, 1);
     cc.stream = s;
     cudaLaunchAttribute ca[1];
@@ -1277,8 +1304,10 @@ hs_status launch_pages(int dev, cudaStream_t s, const CUtensorMap &tq, const CUt
     ca[0].val.programmaticStreamSerializationAllowed = 1;
     cc.attrs = ca;
     cc.numAttrs = 1;
-    return cudaLaunchKernelEx(&cc, join_kernel, (const float *)ws, (const float *)p.ws_lse,
-                              pl.nsplit, n, p.out, p.lse) == cudaSuccess
+    auto join = p.nsplit <= 2 ? join_kernel<2> : (p.nsplit <= 4 ? join_kernel<4> : join_kernel<8>);
+    const size_t row0 = (size_t)p.ws_list0 * pl.M;
+    return cudaLaunchKernelEx(&cc, join, (const float *)ws, (const float *)p.ws_lse, p.nsplit, n, skip,
+                              p.out + row0 * 512, p.lse + row0) == cudaSuccess
                ? HS_OK
                : HS_ERR_CUDA;
 }
@@ -1337,15 +1366,18 @@ hs_status page_entry(hs_pool_t pool, int64_t lists, int32_t T, int32_t tpl, int3
     p.H = H;
     p.N = N;
     p.M = pl.M;
-    p.lists = (int)lists;
+    p.mtiles = pl.mtiles;
     p.nsplit = pl.nsplit;
+    p.n_full = pl.n_full;
+    p.ws_list0 = pl.list0;
+    p.ws_lists = (int)lists - pl.list0;
     p.max_req = pool->cfg.max_requests;
     p.max_pages = pool->max_pages;
     p.zero_block = (int)pool->cfg.n_gpu_blocks;
     p.tpl = tpl;
     p.scale_log2 = sm_scale * 1.4426950408889634f;
-    return fp8 ? launch_pages<true>(dev, s, tq, maps[0], maps[1], d_out, d_workspace, pl, p)
-               : launch_pages<false>(dev, s, tq, maps[0], maps[1], d_out, d_workspace, pl, p);
+    return fp8 ? launch_pages<true>(dev, s, tq, maps[0], maps[1], lists * pl.mtiles, d_out, d_workspace, pl, p)
+               : launch_pages<false>(dev, s, tq, maps[0], maps[1], lists * pl.mtiles, d_out, d_workspace, pl, p);
 }
 
 }  // namespace
