@@ -110,7 +110,7 @@ struct PCfg {
                          B_TREADY = B_TFREE + NTI, B_VFULL = B_TREADY + NTI, B_VFREE = B_VFULL + NV, B_XFULL = B_VFREE + NV,
                          B_XFREE = B_XFULL + NXG, B_CFULL = B_XFREE + NXG, B_CFREE = B_CFULL + NCV,
                          NBAR = B_CFREE + NCV;
-    static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;  // TMEM base, abort flag, steps
+    static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;  // TMEM base, abort flag, steps, list, tile, split, splits
     static constexpr int SMEM = OFF_MISC + 32;
     static constexpr int SMEM_ALLOC = SMEM + 1024;
     // where box i (32 columns, 64 rows, 8 KB) of the other split's partial lands:
@@ -348,7 +348,13 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         first *= 2;
         npages = L <= 0 ? 0 : (L - 1) / kPage + 1;
         fetch(0, npg, nblk);
-        if (warp == 0 && lane == 0) misc[2] = nsteps;
+        if (warp == 0 && lane == 0) {
+            misc[2] = nsteps;
+            misc[3] = list;
+            misc[4] = mt;
+            misc[5] = split;
+            misc[6] = nsplit;
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -592,12 +598,11 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const int row = tid & 63, kh = wq >> 1;  // query row of this CTA; page of the step
         constexpr int KT = 32;                   // keys per thread: 32 hf .. of the page
         const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
-        const int mg = mt * BM + RM * rank + row;
-        const bool vrow = mg < p.M;
         const int b = list / p.tpl;
         const int nt = p.T * p.tpl;  // query tokens of the request
-        const int t = (vrow ? mg / p.H : 0) + list % p.tpl;
-        const long long draft = (long long)L - nt;  // position of the first query token
+        const int at = mt * BM + RM * rank + row;
+        const int t = (at < p.M ? at / p.H : 0) + list % p.tpl;
+        const int draft = L - nt;  // position of the first query token
         uint64_t tree = 0;
         if (p.tree) {
             tree = p.tree[(size_t)b * nt + t];
@@ -669,19 +674,21 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 // four threads take one each
                 const int i = NQT + 2 * hf + kh;
                 if (i < NK) {
-                    uint4 v[8];
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) v[u] = ld_shared_v4(q_at(i) + ((u ^ (row & 7)) << 4));
+                    uint32_t r[16];  // first pieces go where values have been read
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
-                        uint32_t w[8];
-                        bf16x4_to_e4m3(v[2 * u].x, v[2 * u].y, q_pow, w[0], w[4]);
-                        bf16x4_to_e4m3(v[2 * u].z, v[2 * u].w, q_pow, w[1], w[5]);
-                        bf16x4_to_e4m3(v[2 * u + 1].x, v[2 * u + 1].y, q_pow, w[2], w[6]);
-                        bf16x4_to_e4m3(v[2 * u + 1].z, v[2 * u + 1].w, q_pow, w[3], w[7]);
+                        const uint4 x = ld_shared_v4(q_at(i) + (((2 * u) ^ (row & 7)) << 4));
+                        const uint4 y = ld_shared_v4(q_at(i) + (((2 * u + 1) ^ (row & 7)) << 4));
+                        uint32_t w[4];
+                        bf16x4_to_e4m3(x.x, x.y, q_pow, w[0], r[4 * u]);
+                        bf16x4_to_e4m3(x.z, x.w, q_pow, w[1], r[4 * u + 1]);
+                        bf16x4_to_e4m3(y.x, y.y, q_pow, w[2], r[4 * u + 2]);
+                        bf16x4_to_e4m3(y.z, y.w, q_pow, w[3], r[4 * u + 3]);
                         st_shared_v4(q_at(i) + ((u ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
-                        st_shared_v4(q_at(i) + (((4 + u) ^ (row & 7)) << 4), w[4], w[5], w[6], w[7]);
                     }
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        st_shared_v4(q_at(i) + (((4 + u) ^ (row & 7)) << 4), r[4 * u], r[4 * u + 1], r[4 * u + 2], r[4 * u + 3]);
                 }
             }
             tmem_wait_st();
@@ -724,22 +731,22 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             arrive_lead(lead_sfree);  // S_{j+1} may be written
             const int pg = ok ? ring_pg[2 * ti + kh] : -1;
             // the keys that this row sees, as bits
-            const long long base_pos = (long long)pg * kPage;
-            const bool tail = pg >= 0 && base_pos + kPage > draft;  // some row may not see some key
+            const int base_pos = pg * kPage;
+            const bool tail = pg >= 0 && base_pos > draft - kPage;  // some row may not see some key
             float tmax = -INFINITY, cmax = 0.f;
             uint32_t mine = ~0u;
             if (pg < 0) {
                 mine = 0;
             } else if (tail) {
                 uint64_t seen;
-                const long long d = draft - base_pos;  // < 64
+                const int d = draft - base_pos;  // < 64
                 if (p.tree) {
                     if (d >= 0)
                         seen = ((1ull << d) - 1) | (tree << d);
                     else
                         seen = d > -64 ? tree >> -d : 0ull;
                 } else {
-                    const long long n = d + t + 1;
+                    const int n = d + t + 1;
                     seen = n >= 64 ? ~0ull : (n <= 0 ? 0ull : (1ull << n) - 1);
                 }
                 mine = (uint32_t)(seen >> (KT * hf));
@@ -883,6 +890,12 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         if (!ok && lane == 0) fail();
         __syncwarp();
         if (p.inside) cluster_arrive_relaxed();  // what this warp needed of this CTA's memory is used
+        // Where the rows belong, read again: kept through the loop it would cost the
+        // scores' registers (FP8: 37.8 instead of 35.6 us for 16 x 4 lists of
+        // 2,048 rows).
+        const int list = misc[3], mt = misc[4], split = misc[5], nsplit = misc[6];
+        const int mg = mt * BM + RM * rank + row;
+        const bool vrow = mg < p.M;
         // the row's sum over its four threads' keys
         xm[tid] = l;
         named_bar_sync(1, 32 * NSW);
@@ -1168,7 +1181,7 @@ constexpr double US_STEP = 1.6, US_ENDS = 7.0;
 // count that the model makes shortest; the join is 3.5 us and about 5 MB of
 // partials written and read per us. Where there are more units than pairs of CTAs at
 // once, those of the last, partly filled round may be split by themselves
-// (8 x 32 tokens of 128 heads, 256 units on 76 pairs, 16,384 rows: MIXED us a call
+// (8 x 32 tokens of 128 heads, 256 units on 76 pairs, 16,384 rows: 728 us a call
 // against 757 with all units in two).
 PagePlan page_plan(int64_t lists, int64_t T, int64_t H, int64_t N) {
     PagePlan pl{};
