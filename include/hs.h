@@ -391,6 +391,10 @@ size_t hs_select_workspace_bytes(hs_pool_t pool, int32_t B, int32_t T);
  *   d_workspace / ws_bytes: hs_page_decode_workspace_bytes(B, T, H, N) bytes (N as
  *           passed, max_pages for 0), 256-byte aligned, may be NULL when that is 0;
  *           calls that overlap need one each
+ * FP8 pools: a query row is taken as sums of two e4m3 codes per value at a power of two
+ * of its own: exact for values of at least 2^-10 of the row's largest, others are off by
+ * at most 2^-17.8 of that largest; a row that is not finite gives NaN. BF16 pools take it
+ * as it is.
  * What a row that no query may see holds does not matter. An entry outside the
  * context is skipped (HS_DEVERR_INDEX_RANGE), as is a page without a GPU block
  * (HS_DEVERR_BAD_PAGE: resolve its positions with hs_resolve_topk_union
