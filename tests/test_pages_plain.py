@@ -3,6 +3,7 @@ against each other, and the entry points' host-side refusals (no GPU needed)."""
 import ctypes as C
 import math
 
+import pytest
 import torch
 
 import _pages as P
@@ -78,3 +79,29 @@ def test_entry_points_refuse_a_null_pool_and_plan_without_one():
     assert lib.hs_page_decode_workspace_bytes(0, 1, 16, 4) == 0
     assert lib.hs_page_decode_workspace_bytes(1, 1, 16, 0) == 0
     assert lib.hs_page_decode_workspace_bytes(1, 8, 16, 2048) > 0
+
+
+@pytest.mark.parametrize("devices", [1, 2])
+def test_bindings_refuse_tensors_of_another_device(monkeypatch, devices):
+    import tiered_sparse_mla_gb300 as hs
+
+    class OnDevice(torch.Tensor):
+        is_cuda = True
+        device_index = 0
+
+        def get_device(self):
+            return self.device_index
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "device_count", lambda: devices)
+    monkeypatch.setattr(hs, "_only_device", None)
+    x = torch.zeros(3, dtype=torch.int32).as_subclass(OnDevice)
+    for _ in range(2):  # the first look and the short one
+        assert hs._arg("x", x, "int32", 3) == x.data_ptr()
+        assert hs._ws(x) == (12, x.data_ptr())
+    x.device_index = 1
+    for call in (lambda: hs._arg("x", x, "int32", 3), lambda: hs._ws(x)):
+        with pytest.raises(ValueError, match="device 1"):
+            call()
+    with pytest.raises(ValueError):
+        hs._arg("x", torch.zeros(3, dtype=torch.int32), "int32", 3)

@@ -157,7 +157,8 @@ def _arg(name: str, t, dtype: str, *shape, optional: bool = False) -> int | None
         return None
     # one look at a tensor that is as it should be: a call takes a few microseconds
     try:
-        if t.shape == shape and t.dtype is _dtypes[dtype] and t.is_cuda and t.is_contiguous():
+        if (t.shape == shape and t.dtype is _dtypes[dtype] and t.get_device() == _only_device
+                and t.is_contiguous()):
             return t.data_ptr()
     except (AttributeError, KeyError):
         pass
@@ -169,16 +170,33 @@ def _arg(name: str, t, dtype: str, *shape, optional: bool = False) -> int | None
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {list(shape)}, got {list(t.shape)}")
-    return _ptr(t)
+    return _here(name, t)
 
 
 _dtypes: dict = {}
+_only_device = None  # 0 once seen that the process has one CUDA device
+
+
+def _here(name: str, t) -> int:
+    """Device pointer of a contiguous tensor on the current CUDA device (the library
+    refuses a pool of another one)."""
+    import torch
+    global _only_device
+    p, dev = _ptr(t), torch.cuda.current_device()
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on CUDA device {t.get_device()}, the current one is {dev}")
+    if torch.cuda.device_count() == 1:
+        _only_device = 0
+    return p
 
 
 def _ws(workspace):
     if workspace is None:
         return 0, None
-    return workspace.numel() * workspace.element_size(), _ptr(workspace)
+    n = workspace.numel() * workspace.element_size()
+    if workspace.get_device() == _only_device and workspace.is_contiguous():
+        return n, workspace.data_ptr()
+    return n, _here("workspace", workspace)
 
 
 _raw_stream = None
