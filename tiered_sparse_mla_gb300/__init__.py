@@ -360,13 +360,13 @@ def _means_shape(pool: int):
     return cfg.max_requests, (cfg.max_ctx + 63) // 64, 576
 
 
-def hs_page_means(pool: int, req, page, means, stream=None):
+def hs_page_means(pool: int, req, page, means, stream=None, means_shape=None):
     """Mean rows of pages (see hs.h). req, page int32 [n]; means bf16
-    [max_requests][max_pages][576]."""
+    [max_requests][max_pages][576] (means_shape: that shape, where it is known)."""
     n = req.shape[0]
     _check("hs_page_means", load().hs_page_means(
         pool, n, _arg("req", req, "int32", n), _arg("page", page, "int32", n),
-        _arg("means", means, "bfloat16", *_means_shape(pool)), _stream(stream)))
+        _arg("means", means, "bfloat16", *(means_shape or _means_shape(pool))), _stream(stream)))
 
 
 def hs_select_workspace_bytes(pool: int, B: int, T: int) -> int:
@@ -374,7 +374,7 @@ def hs_select_workspace_bytes(pool: int, B: int, T: int) -> int:
 
 
 def hs_select_pages(pool: int, q, means, req_ids, pages, n_first: int = 1, n_last: int = 1,
-                    tree=None, topk_idx=None, workspace=None, stream=None):
+                    tree=None, topk_idx=None, workspace=None, stream=None, means_shape=None):
     """Pages of the highest score for each query token (see hs.h). q bf16
     [B][T][H][576]; means as hs_page_means; pages int32 [B][T][N] out; tree int64
     [B][T] or None; topk_idx int32 [B][T][N*64] out or None; workspace uint8 tensor
@@ -384,7 +384,7 @@ def hs_select_pages(pool: int, q, means, req_ids, pages, n_first: int = 1, n_las
     ws, wp = _ws(workspace)
     _check("hs_select_pages", load().hs_select_pages(
         pool, B, T, H, N, n_first, n_last, _arg("q", q, "bfloat16", B, T, H, 576),
-        _arg("means", means, "bfloat16", *_means_shape(pool)),
+        _arg("means", means, "bfloat16", *(means_shape or _means_shape(pool))),
         _arg("req_ids", req_ids, "int32", B), _arg("tree", tree, "int64", B, T, optional=True),
         _arg("pages", pages, "int32", B, T, N),
         _arg("topk_idx", topk_idx, "int32", B, T, N * 64, optional=True), wp, ws, _stream(stream)))
@@ -582,12 +582,13 @@ class Pool:
         hs_append_rows(self.handle, rows, req_ids, start, index, stream)
 
     def page_means(self, req, page, means, stream=None):
-        hs_page_means(self.handle, req, page, means, stream)
+        hs_page_means(self.handle, req, page, means, stream,
+                      (self.cfg.max_requests, self.max_pages, 576))
 
     def select_pages(self, q, means, req_ids, pages, n_first=1, n_last=1, tree=None,
                      topk_idx=None, workspace=None, stream=None):
         hs_select_pages(self.handle, q, means, req_ids, pages, n_first, n_last, tree, topk_idx,
-                        workspace, stream)
+                        workspace, stream, (self.cfg.max_requests, self.max_pages, 576))
 
     def page_mla_decode(self, q, pages, req_ids, tree, sm_scale, out, lse, workspace=None,
                         stream=None, n_pages=0):
