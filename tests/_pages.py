@@ -62,8 +62,9 @@ def check_attention(out, lse, ref, ref_lse, mass, reach, what=""):
     weight to BF16 (2^-8 of the weighted mean of |value|). Scores are 32-bit sums:
     their error is taken as 2^-16 of |q||k| (36 MMAs that each cut 16 products and the
     sum so far at 2^-25 of the largest's power of two lose 2^-16 of a product that is
-    all of |q||k|; products of like size are far smaller), which moves a weight by that and the sum of the weights by as much again;
-    exp, the split's join and the division stay below 2^-18."""
+    all of |q||k|; products of like size are far smaller), which moves a weight by that
+    and the sum of the weights by as much again; exp, the split's join and the division
+    stay below 2^-18."""
     e = reach * 2.0 ** -16 + 2.0 ** -18
     tol = 2.0 ** -8 * (ref.abs() + mass) * (1 + 2.0 ** -7) + 2 * e * mass + 1e-30
     d = (out.double() - ref).abs()

@@ -20,8 +20,8 @@
 // Bound: an MMA of 128 keys takes 45 clocks (256 value columns: 64), so a step is
 // 36 x 45 + 16 x 64 = 2.7k clocks, and its shared-memory traffic (the MMAs' operands,
 // the copies, FP8's conversions) about as many at 128 bytes a clock. Measured: BF16
-// 2.8k-3.1k clocks a step (8 x 32 tokens x 128 heads over 16,384 rows: 757 us, 1.39
-// PFLOP/s), FP8 3.2k (4 x 8 tokens x 16 heads over 131,072 rows: 113 us). An earlier
+// 2.8k-3.0k clocks a step (8 x 32 tokens x 128 heads over 16,384 rows: 728 us, 1.44
+// PFLOP/s), FP8 3.2k (4 x 8 tokens x 16 heads over 131,072 rows: 111 us). An earlier
 // form, one CTA per half of the value columns and both computing S, was bound by the
 // issue of its 80 smaller MMAs per 128 keys and by their operands' shared-memory reads.
 // Roles in each CTA:
@@ -49,8 +49,8 @@
 //      too, but lose small weights below 2^-10 of the codes' unit.
 //   P: F16, 16 exp2(score - reference) * scale / c, c a power of two that a query row
 //      keeps for the scales as it does the reference for the scores: c is raised where
-//      a scale passes 8 c, so P <= 2^15, exact to 2^-11 of it down to weights of 2^-18
-//      of the largest and off by at most 2^-29 of that below. The probabilities' sum
+//      a scale passes 8 c, so P <= 2^15, off by at most 2^-11 of it down to weights of
+//      2^-18 of the largest and off by at most 2^-29 of that below. The probabilities' sum
 //      has the unrounded ones.
 // Every wait is bounded; on expiry the kernel sets HS_DEVERR_TIMEOUT, drains its
 // own copies and MMAs and returns.
