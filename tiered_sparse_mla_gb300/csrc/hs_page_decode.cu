@@ -110,7 +110,7 @@ struct PCfg {
                          B_TREADY = B_TFREE + NTI, B_VFULL = B_TREADY + NTI, B_VFREE = B_VFULL + NV, B_XFULL = B_VFREE + NV,
                          B_XFREE = B_XFULL + NXG, B_CFULL = B_XFREE + NXG, B_CFREE = B_CFULL + NCV,
                          NBAR = B_CFREE + NCV;
-    static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;  // TMEM base, abort flag, steps, list, tile, split, splits
+    static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;  // TMEM base, abort flag, steps, list, tile, split, splits, first draft
     static constexpr int SMEM = OFF_MISC + 32;
     static constexpr int SMEM_ALLOC = SMEM + 1024;
     // where box i (32 columns, 64 rows, 8 KB) of the other split's partial lands:
@@ -256,11 +256,11 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     volatile int32_t *ring_pg = reinterpret_cast<volatile int32_t *>(smem + C::OFF_PG);
     auto bar = [&](int i) { return base + C::OFF_BAR + 8u * (uint32_t)i; };
     // the same barrier in the pair's CTA 0, whose warp 1 issues the MMAs
-    const uint32_t lead0 = hs::dsmem_map(smem + C::OFF_BAR, pair0);
+    const uint32_t lead0 = cluster_address(base + C::OFF_BAR, pair0);
     const uint16_t both = (uint16_t)(3u << pair0);
     auto lead = [&](int i) { return lead0 + 8u * (uint32_t)i; };
     auto fail = [&]() {
-        misc[1] = 1;
+        st_shared_b32(base + C::OFF_MISC + 4, 1u);
         atomicOr(p.err, HS_DEVERR_TIMEOUT);
     };
 
@@ -354,6 +354,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             misc[4] = mt;
             misc[5] = split;
             misc[6] = nsplit;
+            misc[7] = L - p.T * p.tpl;
         }
     }
     tc_fence_before();
@@ -598,18 +599,10 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const int row = tid & 63, kh = wq >> 1;  // query row of this CTA; page of the step
         constexpr int KT = 32;                   // keys per thread: 32 hf .. of the page
         const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
-        const int b = list / p.tpl;
-        const int nt = p.T * p.tpl;  // query tokens of the request
-        const int at = mt * BM + RM * rank + row;
-        const int t = (at < p.M ? at / p.H : 0) + list % p.tpl;
-        const int draft = L - nt;  // position of the first query token
-        uint64_t tree = 0;
-        if (p.tree) {
-            tree = p.tree[(size_t)b * nt + t];
-            if (nt < 64) tree &= (1ull << nt) - 1;
-        }
-        float *xm = reinterpret_cast<float *>(smem + C::OFF_XM);
-        const uint32_t lead_sfree = lead(C::B_SFREE), lead_pfull = lead(C::B_PFULL), lead_qready = lead(C::B_QREADY);
+        // 32-bit shared addresses throughout: the loop has no registers to spare
+        const uint32_t xm = base + C::OFF_XM;
+        auto word = [&](int i) { return (int)ld_shared_b32(base + C::OFF_MISC + 4 * i); };
+        auto xm_row = [&](int o) { return xm + 4u * (uint32_t)(o + row); };
         // What the MMAs read was written through this CTA's shared or tensor memory
         // and fenced for the async proxy by its writers: the arrive needs no
         // cluster-scope release, which takes 1-2k clocks a time.
@@ -640,10 +633,10 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
             }
             // bits of magnitudes are in their order, infinities and NaN above all
-            uint32_t *um = reinterpret_cast<uint32_t *>(smem + C::OFF_XM);
-            um[tid] = max(m & 0xffffu, m >> 16);
+            st_shared_b32(xm + 4 * tid, max(m & 0xffffu, m >> 16));
             named_bar_sync(1, 32 * NSW);
-            const uint32_t top = max(max(um[row], um[row + 64]), max(um[row + 128], um[row + 192]));
+            const uint32_t top = max(max(ld_shared_b32(xm_row(0)), ld_shared_b32(xm_row(64))),
+                                     max(ld_shared_b32(xm_row(128)), ld_shared_b32(xm_row(192))));
             named_bar_sync(1, 32 * NSW);
             // times 2^k it lies in (224, 448]; a row that is not finite becomes NaN
             const int k = min(135 - (int)(top >> 7) - ((top & 0x7fu) > 0x60u), 126);
@@ -697,8 +690,22 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::B_QDONE));
-        arrive_lead(lead_qready);
+        arrive_lead(lead(C::B_QREADY));
 
+        // This row's query token and its mask. FP8 looks them up where they are needed:
+        // kept through the loop they would cost the scores' registers.
+        auto token = [&](int &t, uint64_t &tree) {
+            const int list = word(3), at = word(4) * BM + RM * rank + row;
+            t = (at < p.M ? at / p.H : 0) + list % p.tpl;
+            if (p.tree) {
+                const int nt = p.T * p.tpl;  // query tokens of the request, at most 64
+                tree = p.tree[(size_t)(list / p.tpl) * nt + t];
+                if (nt < 64) tree &= (1ull << nt) - 1;
+            }
+        };
+        int t = 0;
+        uint64_t tree = 0;
+        if (!FP8) token(t, tree);
         float m2 = -INFINITY, l = 0.f;
         float cref = 0.f, fac = 0.f;  // FP8: the scales' reference, a power of two, and 16 over it
         const float row_scale = p.scale_log2 * q_back;
@@ -728,18 +735,18 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
             }
             tc_fence_before();
-            arrive_lead(lead_sfree);  // S_{j+1} may be written
-            const int pg = ok ? ring_pg[2 * ti + kh] : -1;
+            arrive_lead(lead(C::B_SFREE));  // S_{j+1} may be written
+            const int pg = ok ? (int)ld_shared_b32(base + C::OFF_PG + 4 * (2 * ti + kh)) : -1;
             // the keys that this row sees, as bits
-            const int base_pos = pg * kPage;
-            const bool tail = pg >= 0 && base_pos > draft - kPage;  // some row may not see some key
+            const int d = word(7) - max(pg, 0) * kPage;  // the first query token's position in the page
+            const bool tail = pg >= 0 && d < kPage;  // some row may not see some key
             float tmax = -INFINITY, cmax = 0.f;
             uint32_t mine = ~0u;
             if (pg < 0) {
                 mine = 0;
             } else if (tail) {
+                if (FP8) token(t, tree);
                 uint64_t seen;
-                const int d = draft - base_pos;  // < 64
                 if (p.tree) {
                     if (d >= 0)
                         seen = ((1ull << d) - 1) | (tree << d);
@@ -767,7 +774,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
                 tmax = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
                 if (FP8) {
-                    cmax = reinterpret_cast<volatile float *>(smem + C::OFF_SP)[4 * ti + 2 * kh + hf];
+                    cmax = ld_shared_f1(base + C::OFF_SP + 4 * (4 * ti + 2 * kh + hf));
                     if (hide) {  // a hidden row's scale may be anything
                         cmax = 0.f;
 #pragma unroll
@@ -787,11 +794,12 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             auto outgrown = [](float x, float ref) { return x > ref + TAU2 || (ref == -INFINITY && x != -INFINITY); };
             const bool grow = any_softmax(outgrown(tmax, m2) || (FP8 && cmax > 8.f * cref));
             if (grow) {
-                xm[tid] = tmax;
-                if (FP8) xm[32 * NSW + tid] = cmax;
+                st_shared_f1(xm + 4 * tid, tmax);
+                if (FP8) st_shared_f1(xm + 4 * (32 * NSW + tid), cmax);
                 named_bar_sync(1, 32 * NSW);
                 auto of_row = [&](int o) {
-                    return fmaxf(fmaxf(xm[o + row], xm[o + row + 64]), fmaxf(xm[o + row + 128], xm[o + row + 192]));
+                    return fmaxf(fmaxf(ld_shared_f1(xm_row(o)), ld_shared_f1(xm_row(o + 64))),
+                                 fmaxf(ld_shared_f1(xm_row(o + 128)), ld_shared_f1(xm_row(o + 192))));
                 };
                 const float tall = of_row(0), call = FP8 ? of_row(32 * NSW) : 0.f;
                 named_bar_sync(1, 32 * NSW);  // read before the next writes
@@ -881,7 +889,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     rescale_o(tmem + lane_off + TM_O + 128u * hf, alpha);
             }
             tc_fence_before();
-            arrive_lead(lead_pfull);
+            arrive_lead(lead(C::B_PFULL));
         }
         if (ok && nsteps > 0) {
             ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_PVDONE), (uint32_t)(nsteps - 1) & 1u));
@@ -893,13 +901,13 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         // Where the rows belong, read again: kept through the loop it would cost the
         // scores' registers (FP8: 37.8 instead of 35.6 us for 16 x 4 lists of
         // 2,048 rows).
-        const int list = misc[3], mt = misc[4], split = misc[5], nsplit = misc[6];
+        const int list = word(3), mt = word(4), split = word(5), nsplit = word(6);
         const int mg = mt * BM + RM * rank + row;
         const bool vrow = mg < p.M;
         // the row's sum over its four threads' keys
-        xm[tid] = l;
+        st_shared_f1(xm + 4 * tid, l);
         named_bar_sync(1, 32 * NSW);
-        l = (xm[row] + xm[row + 64]) + (xm[row + 128] + xm[row + 192]);
+        l = (ld_shared_f1(xm_row(0)) + ld_shared_f1(xm_row(64))) + (ld_shared_f1(xm_row(128)) + ld_shared_f1(xm_row(192)));
         // rows that see nothing: out 0, lse -inf
         const float inv = l == 0.f ? 0.f : __fdividef(FP8 ? cref * 0.0625f : 1.f, l);
         const bool one = nsplit == 1;
@@ -910,7 +918,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         uint32_t theirs = 0;
         if (p.inside) {
             cluster_wait();
-            theirs = hs::dsmem_map(smem + C::OFF_BAR + 8 * C::B_JOIN, other);
+            theirs = cluster_address(bar(C::B_JOIN), other);
         }
         if (p.inside || (ok && (one || nsteps > 0))) {
             // O / l through shared memory, idle by now, in 32-row boxes of 128
@@ -956,25 +964,24 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         __syncwarp();
                         const int box = 4 * kh + cc;
                         if (lane == 0)
-                            bulk_push(hs::dsmem_map(smem + C::join_box(box) + wr * 4096, other),
+                            bulk_push(cluster_address(base + C::join_box(box) + wr * 4096, other),
                                       base + C::OFF_V + (uint32_t)(8 * hf + box) * 8192u + wr * 4096, 4096, theirs);
                     }
                 }
+                if (!p.inside && (!one || (cc & 1))) {  // a box is staged: its store runs behind the next one's
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) {
+                        const int box = one ? col >> 6 : col >> 5;
+                        tma_store_3d(one ? &tm_o : &tm_w, base + C::OFF_V + (uint32_t)box * 8192u + wr * 4096,
+                                     one ? 64 * box : 32 * box, mt * BM + RM * rank + 32 * wr,
+                                     one ? list : split * p.ws_lists + list - p.ws_list0);
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    }
+                }
             }
-            if (!p.inside) fence_proxy_async();
-            __syncwarp();
-            if (lane == 0 && !p.inside) {
-                const int wide = one ? 64 : 32;
-                const int z = one ? list : split * p.ws_lists + list - p.ws_list0;
-                const CUtensorMap *to = one ? &tm_o : &tm_w;
-                const int c0 = 256 * hf + 128 * kh;
-                for (int c = c0; c < c0 + 128; c += wide)
-                    tma_store_3d(to, base + C::OFF_V + (uint32_t)(c / wide) * 8192u + wr * 4096, c,
-                                 mt * BM + RM * rank + 32 * wr, z);
-                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                // the stores have read shared memory before the CTA may end
-                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-            }
+            // the stores have read shared memory before the CTA may end
+            if (lane == 0 && !p.inside) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
             __syncwarp();
         }
         if (kh == 0 && hf == 0 && (vrow || p.inside)) {
@@ -984,14 +991,14 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             else if (!p.inside)
                 p.ws_lse[((size_t)split * p.ws_lists + list - p.ws_list0) * p.M + mg] = lse;
             else
-                reinterpret_cast<float *>(smem + C::OFF_P)[row] = lse;  // P is done with
+                st_shared_f1(base + C::OFF_P + 4 * row, lse);  // P is done with
         }
         if (p.inside && kh == 0 && hf == 0) {
             fence_proxy_async();
             __syncwarp();
             const int wr = wq & 1;
             if (lane == 0)
-                bulk_push(hs::dsmem_map(smem + C::OFF_P + 1024 + wr * 128, other), base + C::OFF_P + wr * 128, 128, theirs);
+                bulk_push(cluster_address(base + C::OFF_P + 1024 + wr * 128, other), base + C::OFF_P + wr * 128, 128, theirs);
             __syncwarp();
         }
     } else if (FP8 && warp >= 4 + NSW) {

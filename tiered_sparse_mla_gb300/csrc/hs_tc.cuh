@@ -274,6 +274,22 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
                  : "memory");
     return v;
 }
+__device__ __forceinline__ uint32_t ld_shared_b32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ float ld_shared_f1(uint32_t a) { return __uint_as_float(ld_shared_b32(a)); }
+__device__ __forceinline__ void st_shared_b32(uint32_t a, uint32_t x) {
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(x) : "memory");
+}
+__device__ __forceinline__ void st_shared_f1(uint32_t a, float x) { st_shared_b32(a, __float_as_uint(x)); }
+// A shared-memory address in another CTA of the cluster.
+__device__ __forceinline__ uint32_t cluster_address(uint32_t a, uint32_t rank) {
+    uint32_t d;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(rank));
+    return d;
+}
 __device__ __forceinline__ float4 ld_shared_f4(uint32_t a) {
     float4 v;
     asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
