@@ -78,14 +78,15 @@ constexpr int CCH = 64 * 64;      // 64 rows x 64 e4m3 codes
 constexpr int NK = 9, NVC = 4;    // K chunks of a page; V chunks of a page in this CTA
 constexpr int NQT = 6;            // chunks of Q in tensor memory
 constexpr int NTI = 3;            // steps whose page numbers and scales are held
-constexpr int NSW = 8;             // softmax warps
+constexpr int NSW = 8;            // softmax warps
+constexpr int NCW = 4;            // FP8: converter warps
 constexpr uint32_t JOIN_BYTES = RM * 256 * 4 + RM * 4;  // half the columns of a partial, and its lse
 constexpr float TAU2 = 8.f;       // rescale threshold, log2 units: P <= 2^8
 constexpr uint32_t TM_O = 0, TM_S = 256, TM_Q = 320;
 
 template <bool FP8>
 struct PCfg {
-    static constexpr int THREADS = 128 + 32 * NSW + (FP8 ? 256 : 0);
+    static constexpr int THREADS = 128 + 32 * NSW + (FP8 ? 32 * NCW : 0);
     static constexpr int NV = 2;              // V's buffers: two steps; FP8: the two halves of one step's columns
     // K chunks per barrier. FP8: three; BF16: the rope chunk by itself, then the
     // value chunks in twos (fewer waits and copies to issue)
@@ -1003,16 +1004,17 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
     } else if (FP8 && warp >= 4 + NSW) {
         // ------------------------------------------------------------ converters
-        // Four warps for either half of V's columns, one step after the other: the
-        // next step's codes are loaded while this one's stores are fenced.
-        const int half = (warp - 4 - NSW) >> 2, tid = threadIdx.x & 127;
+        // Half of V's columns at a time: the next half's codes are loaded while this
+        // one's stores are fenced.
+        const int tid = threadIdx.x & 127;
+        constexpr int BY = NCW / 4;
         // V's space held the staged Q
         bool ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_QDONE), 0));
         constexpr int G = C::GV;
         static_assert(!FP8 || (NVC == G && C::NCV % 2 == 0 && NK % C::GK == 0), "groups of chunks");
         uint4 w[G][2];
-        auto load = [&](int j) {
-            const int u = 2 * j + half, cs = u % C::RV;
+        auto load = [&](int u) {
+            const int cs = u % C::RV;
             if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_CFULL + cs), (uint32_t)(u / C::RV) & 1u));
             const uint32_t src = base + C::OFF_C + cs * G * CCH + 16 * tid;
             if (ok) {
@@ -1023,11 +1025,12 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
             }
         };
-        if (nsteps > 0) load(0);
-        const uint32_t lead_vfull = lead(C::B_VFULL + half);
+        const int u0 = (warp - 4 - NSW) >> 2;
+        if (nsteps > 0) load(u0);
 #pragma unroll 1
-        for (int j = 0; j < nsteps; ++j) {
-            if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_VFREE + half), ((uint32_t)j & 1u) ^ 1u));
+        for (int u = u0; u < 2 * nsteps; u += BY) {
+            const int half = u & 1;
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_VFREE + half), ((uint32_t)(u >> 1) & 1u) ^ 1u));
             if (ok) {
                 const uint32_t dst = base + C::OFF_V + half * 2 * CH + (tid >> 2) * 128;
                 const int key = (tid >> 2) & 7, part = 2 * (tid & 3);  // rows key and key + 32: the same swizzle
@@ -1047,11 +1050,11 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(C::B_CFREE + (2 * j + half) % C::RV));
-            if (j + 1 < nsteps) load(j + 1);
+            if (lane == 0) mbar_arrive(bar(C::B_CFREE + u % C::RV));
+            if (u + BY < 2 * nsteps) load(u + BY);
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0) mbar_arrive_peer(lead_vfull);
+            if (lane == 0) mbar_arrive_peer(lead(C::B_VFULL + half));
         }
         if (!ok && lane == 0) fail();
     }
