@@ -32,8 +32,9 @@
 //               online softmax with a conditional rescale, P as BF16 (FP8: F16)
 //               to shared memory; epilogue;
 //   warp 2      (FP8) the largest of the landed scales, by 32 keys;
-//   warps 12-19 (FP8) converters: V's e4m3 codes to F16, four warps for either half
-//               of the columns.
+//   warps 12-15 (FP8) converters: V's e4m3 codes to F16, half the columns at a time
+//               (four more warps leave the softmax 96 registers: 33.9 -> 34.8 us for 16 x 4
+//               lists of 2,048 rows).
 // FP8: S is taken from the e4m3 codes themselves (kind::f8f6f4), so K needs no
 // conversion (with K's chunks converted to F16 like V's, the shared-memory traffic and
 // the converters' issue made a step 4.0k clocks: 44 against 36 us for 16 x 4 lists of
@@ -111,7 +112,7 @@ struct PCfg {
                          B_TREADY = B_TFREE + NTI, B_VFULL = B_TREADY + NTI, B_VFREE = B_VFULL + NV, B_XFULL = B_VFREE + NV,
                          B_XFREE = B_XFULL + NXG, B_CFULL = B_XFREE + NXG, B_CFREE = B_CFULL + NCV,
                          NBAR = B_CFREE + NCV;
-    static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;  // TMEM base, abort flag, steps, list, tile, split, splits, first draft
+    static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;  // TMEM base, abort flag, steps
     static constexpr int SMEM = OFF_MISC + 32;
     static constexpr int SMEM_ALLOC = SMEM + 1024;
     // where box i (32 columns, 64 rows, 8 KB) of the other split's partial lands:
@@ -349,14 +350,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         first *= 2;
         npages = L <= 0 ? 0 : (L - 1) / kPage + 1;
         fetch(0, npg, nblk);
-        if (warp == 0 && lane == 0) {
-            misc[2] = nsteps;
-            misc[3] = list;
-            misc[4] = mt;
-            misc[5] = split;
-            misc[6] = nsplit;
-            misc[7] = L - p.T * p.tpl;
-        }
+        if (warp == 0 && lane == 0) misc[2] = nsteps;
     }
     tc_fence_before();
     __syncthreads();
@@ -602,7 +596,6 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
         // 32-bit shared addresses throughout: the loop has no registers to spare
         const uint32_t xm = base + C::OFF_XM;
-        auto word = [&](int i) { return (int)ld_shared_b32(base + C::OFF_MISC + 4 * i); };
         auto xm_row = [&](int o) { return xm + 4u * (uint32_t)(o + row); };
         // What the MMAs read was written through this CTA's shared or tensor memory
         // and fenced for the async proxy by its writers: the arrive needs no
@@ -693,20 +686,16 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         if (lane == 0) mbar_arrive(bar(C::B_QDONE));
         arrive_lead(lead(C::B_QREADY));
 
-        // This row's query token and its mask. FP8 looks them up where they are needed:
-        // kept through the loop they would cost the scores' registers.
-        auto token = [&](int &t, uint64_t &tree) {
-            const int list = word(3), at = word(4) * BM + RM * rank + row;
-            t = (at < p.M ? at / p.H : 0) + list % p.tpl;
-            if (p.tree) {
-                const int nt = p.T * p.tpl;  // query tokens of the request, at most 64
-                tree = p.tree[(size_t)(list / p.tpl) * nt + t];
-                if (nt < 64) tree &= (1ull << nt) - 1;
-            }
-        };
-        int t = 0;
+        // this row's query token and its mask
+        const int mg = mt * BM + RM * rank + row;
+        const bool vrow = mg < p.M;
+        const int nt = p.T * p.tpl;  // query tokens of the request
+        const int t = (vrow ? mg / p.H : 0) + list % p.tpl, draft = L - nt;
         uint64_t tree = 0;
-        if (!FP8) token(t, tree);
+        if (p.tree) {
+            tree = p.tree[(size_t)(list / p.tpl) * nt + t];
+            if (nt < 64) tree &= (1ull << nt) - 1;
+        }
         float m2 = -INFINITY, l = 0.f;
         float cref = 0.f, fac = 0.f;  // FP8: the scales' reference, a power of two, and 16 over it
         const float row_scale = p.scale_log2 * q_back;
@@ -739,14 +728,13 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             arrive_lead(lead(C::B_SFREE));  // S_{j+1} may be written
             const int pg = ok ? (int)ld_shared_b32(base + C::OFF_PG + 4 * (2 * ti + kh)) : -1;
             // the keys that this row sees, as bits
-            const int d = word(7) - max(pg, 0) * kPage;  // the first query token's position in the page
+            const int d = draft - max(pg, 0) * kPage;  // the first query token's position in the page
             const bool tail = pg >= 0 && d < kPage;  // some row may not see some key
             float tmax = -INFINITY, cmax = 0.f;
             uint32_t mine = ~0u;
             if (pg < 0) {
                 mine = 0;
             } else if (tail) {
-                if (FP8) token(t, tree);
                 uint64_t seen;
                 if (p.tree) {
                     if (d >= 0)
@@ -899,12 +887,6 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         if (!ok && lane == 0) fail();
         __syncwarp();
         if (p.inside) cluster_arrive_relaxed();  // what this warp needed of this CTA's memory is used
-        // Where the rows belong, read again: kept through the loop it would cost the
-        // scores' registers (FP8: 37.8 instead of 35.6 us for 16 x 4 lists of
-        // 2,048 rows).
-        const int list = word(3), mt = word(4), split = word(5), nsplit = word(6);
-        const int mg = mt * BM + RM * rank + row;
-        const bool vrow = mg < p.M;
         // the row's sum over its four threads' keys
         st_shared_f1(xm + 4 * tid, l);
         named_bar_sync(1, 32 * NSW);
@@ -1004,8 +986,8 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
     } else if (FP8 && warp >= 4 + NSW) {
         // ------------------------------------------------------------ converters
-        // Half of V's columns at a time: the next half's codes are loaded while this
-        // one's stores are fenced.
+        // Half of V's columns at a time; the next half's codes are loaded while its buffer
+        // is still read.
         const int tid = threadIdx.x & 127;
         constexpr int BY = NCW / 4;
         // V's space held the staged Q
@@ -1051,10 +1033,10 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::B_CFREE + u % C::RV));
-            if (u + BY < 2 * nsteps) load(u + BY);
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive_peer(lead(C::B_VFULL + half));
+            if (u + BY < 2 * nsteps) load(u + BY);
         }
         if (!ok && lane == 0) fail();
     }
