@@ -21,7 +21,7 @@
 // 36 x 45 + 16 x 64 = 2.7k clocks, and its shared-memory traffic (the MMAs' operands,
 // the copies, FP8's conversions) about as many at 128 bytes a clock. Measured: BF16
 // 2.8k-3.0k clocks a step (8 x 32 tokens x 128 heads over 16,384 rows: 728 us, 1.44
-// PFLOP/s), FP8 3.2k (4 x 8 tokens x 16 heads over 131,072 rows: 111 us). An earlier
+// PFLOP/s), FP8 2.8k-3.2k (4 x 8 tokens x 16 heads over 131,072 rows: 108 us). An earlier
 // form, one CTA per half of the value columns and both computing S, was bound by the
 // issue of its 80 smaller MMAs per 128 keys and by their operands' shared-memory reads.
 // Roles in each CTA:
@@ -37,8 +37,8 @@
 //               lists of 2,048 rows).
 // FP8: S is taken from the e4m3 codes themselves (kind::f8f6f4), so K needs no
 // conversion (with K's chunks converted to F16 like V's, the shared-memory traffic and
-// the converters' issue made a step 4.0k clocks: 44 against 36 us for 16 x 4 lists of
-// 2,048 rows of 128 heads).
+// the converters' issue made a step 4.0k clocks: 44 us for 16 x 4 lists of 2,048 rows of
+// 128 heads, which now take 33).
 //   Q: a value times the row's power of two, which brings the row's largest to
 //      (224, 448], is the sum of two e4m3 codes, and an MMA of depth 32 takes either
 //      with the same keys: as many MMAs as one of F16. Values of at least 2^-10 of the
