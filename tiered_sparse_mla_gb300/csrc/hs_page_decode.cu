@@ -498,14 +498,15 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                                 mma2_ss(tmem + TM_O + 128u * nh, a + ((pgi * CH + 32 * k) >> 4),
                                         v + ((pgi * NVC * CH + nh * 2 * CH + 2048 * k) >> 4), hi, ID_PV,
                                         (j | pgi | k) != 0);
-                        if (FP8) commit_both(bar(C::B_VFREE + nh), both);
-                        if (!FP8 && nh == 1) commit_both(bar(C::B_VFREE + j % C::NV), both);
+                        if (FP8 && j + 1 < nsteps) commit_both(bar(C::B_VFREE + nh), both);
+                        if (!FP8 && nh == 1 && j + C::NV < nsteps) commit_both(bar(C::B_VFREE + j % C::NV), both);
                         if (nh == 1) commit_both(bar(C::B_PVDONE), both);
                     }
                     __syncwarp();
                 }
                 __syncwarp();
             };
+            constexpr int PER = FP8 ? NK / C::GK : 8 / C::GK;  // groups of K chunks per step
             int s = 0;
             uint32_t ph = 0;
             for (int j = 0; j < nsteps && ok; ++j) {
@@ -533,7 +534,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     tc_fence_after();
                     if (leader) {
                         qk(8, 0, true);
-                        commit_both(bar(C::B_XFREE), both);
+                        if (j + 1 < nsteps) commit_both(bar(C::B_XFREE), both);
                     }
                     __syncwarp();
                 }
@@ -546,7 +547,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         if (leader) {
 #pragma unroll
                             for (int g = 0; g < C::GK; ++g) qk(c + g, (FP8 ? s * C::GK : 1 + 2 * s) + g, FP8 && c + g == 0);
-                            commit_both(bar(C::B_XFREE + b0), both);
+                            if (PER * j + c / C::GK + C::RK < PER * nsteps) commit_both(bar(C::B_XFREE + b0), both);
                         }
                         __syncwarp();
                     }
@@ -684,7 +685,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::B_QDONE));
-        arrive_lead(lead(C::B_QREADY));
+        if (nsteps > 0) arrive_lead(lead(C::B_QREADY));
 
         // this row's query token and its mask
         const int mg = mt * BM + RM * rank + row;
@@ -725,7 +726,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
             }
             tc_fence_before();
-            arrive_lead(lead(C::B_SFREE));  // S_{j+1} may be written
+            if (j + 1 < nsteps) arrive_lead(lead(C::B_SFREE));  // S_{j+1} may be written
             const int pg = ok ? (int)ld_shared_b32(base + C::OFF_PG + 4 * (2 * ti + kh)) : -1;
             // the keys that this row sees, as bits
             const int d = draft - max(pg, 0) * kPage;  // the first query token's position in the page
@@ -1056,7 +1057,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         __syncwarp();
         // What was sent has been read, and nothing more comes: the others may end once
         // this CTA has come here.
-        cluster_arrive_relaxed();
+        cluster_arrive_last(misc[1] != 0);
         const float *lses = reinterpret_cast<const float *>(smem + C::OFF_P);
         float *wts = reinterpret_cast<float *>(smem + C::OFF_P + 2048);  // [rows]: own, the other's
         if (threadIdx.x < RM) {
@@ -1091,8 +1092,11 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     }
     tc_fence_before();
     __syncthreads();
-    // no CTA leaves while the other's MMAs or arrivals may reach it
-    if (!p.inside) cluster_arrive_relaxed();
+    // No CTA leaves while the other's MMAs or arrives may reach it. Every arrive on the
+    // other CTA's barriers is one that it waits for (none is made for a step or a slot
+    // that does not come), so none is on its way any more and the barrier need not
+    // release; after a wait that gave up it does.
+    if (!p.inside) cluster_arrive_last(misc[1] != 0);
     cluster_wait();
     tc_fence_after();
     if (warp == 2) tmem_dealloc2(tmem, 512);

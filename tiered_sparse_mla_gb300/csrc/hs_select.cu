@@ -181,6 +181,7 @@ score_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ C
     cluster_sync_relaxed();
     tc_fence_after();
     const uint32_t tmem = static_cast<uint32_t>(misc[0]);
+    const uint32_t tiles = (uint32_t)(f1 - f0) * (uint32_t)passes;  // that this pair multiplies
 
     // The range's requests, one after the other: every warp walks them for itself.
     struct Walk {
@@ -277,6 +278,7 @@ score_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ C
             const uint32_t qch = (uint32_t)(p.N / 2) * 128u;
             bool ok = true;
             uint32_t u = 0, i = 0, loads = 0;
+            const uint32_t last_u = tiles * NCH;
             for (Walk w = start(); w.n > 0 && ok; next(w))
                 for (int k = 0; k < passes && ok; ++k, ++loads)
                     for (int j = 0; j < w.n && ok; ++j, ++i) {
@@ -297,7 +299,7 @@ score_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ C
                                 const uint32_t a = lo + ((OFF_RING + s * A_BYTES) >> 4), q = lo + ((c * qch) >> 4);
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) mma2_ss(d, a + 2 * e, q + 2 * e, hi, idesc, (c | e) != 0);
-                                commit_both(bar(B_FREE + s));
+                                if (u + NST < last_u) commit_both(bar(B_FREE + s));
                             }
                             __syncwarp();
                         }
@@ -428,13 +430,16 @@ score_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ C
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_peer(lead(B_DFREE + (i & 1)));
+            if (lane == 0 && i + 2 < tiles) mbar_arrive_peer(lead(B_DFREE + (i & 1)));
         }
         if (!ok && lane == 0) fail();
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync_relaxed();  // no CTA leaves while the other's MMAs or arrivals may reach it
+    // No CTA leaves while the other's MMAs or arrives may reach it: every arrive on the
+    // other's barriers is one that it waits for, so none is on its way any more.
+    cluster_arrive_last(misc[1] != 0);
+    cluster_wait();
     tc_fence_after();
     if (warp == 1) tmem_dealloc2(tmem, cols);
 }

@@ -481,6 +481,15 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const void *tmap, in
 __device__ __forceinline__ void cluster_arrive_relaxed() {
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
+// The arrive after which the others may end. Relaxed, it lets what this CTA sent them
+// be overtaken: that is right where they have waited for all of it, and not after a
+// wait that gave up (the same on all threads of the CTA).
+__device__ __forceinline__ void cluster_arrive_last(bool failed) {
+    if (failed)
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    else
+        cluster_arrive_relaxed();
+}
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync_relaxed() {
     cluster_arrive_relaxed();
