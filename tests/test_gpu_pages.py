@@ -626,6 +626,29 @@ def test_attention_fp8_scales_of_many_magnitudes():
     c.close()
 
 
+def test_attention_fp8_keeps_small_weights():
+    """The row that takes almost all of the weight has zeros for values: what is left
+    are values at a weight of e^-18 = 2^-26. F16's smallest step, 2^-24 of a weight kept
+    at 2^10 times itself, puts such a weight off by at most 2^-35 / 2^-26 = 2^-9 of it
+    (times 2^-7 / 0.0074, the scales' reference over the row's): less than a weight's
+    rounding to BF16, which the check allows."""
+    c = Cache("fp8", [2], garbage=False)
+    x = torch.zeros(2, P.DIM)
+    x[0, 512:] = 6.75  # scores 64 * 6.75 / 24 = 18 above those of the other row
+    x[1, :512] = torch.randn(512, generator=torch.Generator().manual_seed(87)).clamp(-3.3, 3.3)
+    x[1, 0] = 3.3
+    codes, scale = P.quantise(x.to(torch.bfloat16))
+    at = torch.tensor([c.row(0, 0), c.row(0, 1)], device="cuda")
+    c.pool.gpu_rows()[at] = codes.view(torch.uint8).cuda()
+    c.pool.gpu_scales()[at] = scale.cuda()
+    q = torch.zeros(1, 1, 16, P.DIM)
+    q[..., 512:] = 1.0
+    q = q.to(torch.bfloat16).cuda()
+    out, lse = attend(c, q, None)
+    check(c, q, out, lse, lambda b, t: None)
+    c.close()
+
+
 def test_attention_fp8_queries_with_outliers():
     """A query's values are the sums of two e4m3 codes each, at a power of two that
     brings the row's largest to (224, 448]: values of at least 2^-10 of the largest are

@@ -48,11 +48,11 @@
 //      per instruction (24 against 72 clocks per 16 codes and warp for placing BF16
 //      bits with integer instructions). Two e4m3 codes per weight would spare this
 //      too, but lose small weights below 2^-10 of the codes' unit.
-//   P: F16, 16 exp2(score - reference) * scale / c, c a power of two that a query row
+//   P: F16, 2^10 exp2(score - reference) * scale / c, c a power of two that a query row
 //      keeps for the scales as it does the reference for the scores: c is raised where
-//      a scale passes 8 c, so P <= 2^15, off by at most 2^-11 of it down to weights of
-//      2^-18 of the largest and off by at most 2^-29 of that below. The probabilities' sum
-//      has the unrounded ones.
+//      a scale passes 2 c, the reference where a score passes it by 4, so P <= 2^15. It
+//      is off by at most 2^-11 of it down to 2^-24 of a weight at both references, and
+//      by at most 2^-35 of that below. The probabilities' sum has the unrounded ones.
 // Every wait is bounded; on expiry the kernel sets HS_DEVERR_TIMEOUT, drains its
 // own copies and MMAs and returns.
 #include <cuda_bf16.h>
@@ -82,7 +82,11 @@ constexpr int NTI = 3;            // steps whose page numbers and scales are hel
 constexpr int NSW = 8;            // softmax warps
 constexpr int NCW = 4;            // FP8: converter warps
 constexpr uint32_t JOIN_BYTES = RM * 256 * 4 + RM * 4;  // half the columns of a partial, and its lse
-constexpr float TAU2 = 8.f;       // rescale threshold, log2 units: P <= 2^8
+// A row's references follow where its scores' maximum passes the old one by this much
+// (log2 units), and FP8's where a scale passes twice its own: P <= 2^8, FP8: 2^15.
+template <bool FP8>
+constexpr float TAU2 = FP8 ? 4.f : 8.f;
+constexpr int P_EXP = 10;  // FP8: a weight at both references is 2^10
 constexpr uint32_t TM_O = 0, TM_S = 256, TM_Q = 320;
 
 template <bool FP8>
@@ -698,7 +702,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (nt < 64) tree &= (1ull << nt) - 1;
         }
         float m2 = -INFINITY, l = 0.f;
-        float cref = 0.f, fac = 0.f;  // FP8: the scales' reference, a power of two, and 16 over it
+        float cref = 0.f, fac = 0.f;  // FP8: the scales' reference, a power of two, and 2^10 over it
         const float row_scale = p.scale_log2 * q_back;
         for (int j = 0; j < nsteps; ++j) {
             const int ti = j % NTI;
@@ -781,8 +785,8 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             // A row's four threads share its references: where some row of the CTA
             // outgrows its own, the rows' four maxima meet in shared memory.
             float alpha = 1.f;
-            auto outgrown = [](float x, float ref) { return x > ref + TAU2 || (ref == -INFINITY && x != -INFINITY); };
-            const bool grow = any_softmax(outgrown(tmax, m2) || (FP8 && cmax > 8.f * cref));
+            auto outgrown = [](float x, float ref) { return x > ref + TAU2<FP8> || (ref == -INFINITY && x != -INFINITY); };
+            const bool grow = any_softmax(outgrown(tmax, m2) || (FP8 && cmax > 2.f * cref));
             if (grow) {
                 st_shared_f1(xm + 4 * tid, tmax);
                 if (FP8) st_shared_f1(xm + 4 * (32 * NSW + tid), cmax);
@@ -798,10 +802,11 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     l *= alpha;
                     m2 = tall;
                 }
-                if (FP8 && call > 8.f * cref) {
-                    const uint32_t e = max(__float_as_uint(call) >> 23, 7u);
-                    fac = __uint_as_float((258u - e) << 23);
-                    alpha *= cref * fac * 0.0625f;
+                if (FP8 && call > 2.f * cref) {
+                    // at least 2^-107: its inverse, and the epilogue's factor, are normal
+                    const uint32_t e = max(__float_as_uint(call) >> 23, 20u);
+                    fac = __uint_as_float((254u + P_EXP - e) << 23);
+                    alpha *= cref * fac * (1.f / (1 << P_EXP));
                     cref = __uint_as_float(e << 23);
                 }
             }
@@ -893,7 +898,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         named_bar_sync(1, 32 * NSW);
         l = (ld_shared_f1(xm_row(0)) + ld_shared_f1(xm_row(64))) + (ld_shared_f1(xm_row(128)) + ld_shared_f1(xm_row(192)));
         // rows that see nothing: out 0, lse -inf
-        const float inv = l == 0.f ? 0.f : __fdividef(FP8 ? cref * 0.0625f : 1.f, l);
+        const float inv = l == 0.f ? 0.f : __fdividef(FP8 ? cref * (1.f / (1 << P_EXP)) : 1.f, l);
         const bool one = nsplit == 1;
         // The columns that the other split joins go there as they are staged, once all
         // CTAs are done with the memory they land in (where nothing was computed, what
