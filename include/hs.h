@@ -393,8 +393,9 @@ size_t hs_select_workspace_bytes(hs_pool_t pool, int32_t B, int32_t T);
  *           calls that overlap need one each
  * FP8 pools: a query row is taken as sums of two e4m3 codes per value at a power of two
  * of its own: exact for values of at least 2^-10 of the row's largest, others are off by
- * at most 2^-17.8 of that largest; a row that is not finite gives NaN. BF16 pools take it
- * as it is.
+ * at most 2^-17.8 of that largest; a row that is not finite gives NaN. Weights times
+ * row scales are rounded to F16 (2^-11 of them, or 2^-34 of the largest weight at the
+ * largest scale). BF16 pools take the query as it is and round weights to BF16 (2^-8).
  * What a row that no query may see holds does not matter. An entry outside the
  * context is skipped (HS_DEVERR_INDEX_RANGE), as is a page without a GPU block
  * (HS_DEVERR_BAD_PAGE: resolve its positions with hs_resolve_topk_union
