@@ -56,7 +56,8 @@ typedef enum {
 } hs_status;
 
 /* Bits of the device error word (hs_pool_get_error). */
-#define HS_DEVERR_INDEX_RANGE 1u  /* position outside [0, ctx_len) (and not -1)   */
+#define HS_DEVERR_INDEX_RANGE 1u  /* position outside [0, ctx_len) (and not -1),
+                                     or a ctx_len past max_ctx                      */
 #define HS_DEVERR_DUPLICATE   2u  /* a missing position repeated in one list      */
 #define HS_DEVERR_NO_HOST     4u  /* non-resident, non-hot row without host copy  */
 #define HS_DEVERR_BAD_REQUEST 8u  /* request id outside [0, max_requests)         */
@@ -314,8 +315,10 @@ hs_status hs_demote_cold_pages(hs_pool_t pool, int32_t n, const int32_t *d_req,
 /* ---- new rows, and pages chosen and attended to as wholes ----------------
  *      No allocation and no host synchronisation; launch shapes depend on the
  *      integer arguments alone, so every call can be captured in a CUDA graph.
- *      The pool's device must be the current one. Request ids, lists and masks
- *      are read on the device at each launch. -------------------------------- */
+ *      The pool's device must be the current one. Request ids, lists, masks and
+ *      context lengths are read on the device at each launch. Means, selection
+ *      and attention take a length past max_ctx (hs_set_ctx_len copies any) as
+ *      max_ctx and set HS_DEVERR_INDEX_RANGE. ---------------------------------- */
 
 /* Puts the latent rows of new tokens into the cache: row k of request
  * d_req_ids[b] (k = 0 .. T-1) goes to position d_start[b] + k, or, with d_start

@@ -1,0 +1,80 @@
+"""Append, page means, page selection and attention over pages where an input is at the
+edge of what the operators accept, or past it. Plain 64-bit forms: tests/_pages.py."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import _pages as P
+from test_gpu_pages import I32, SCALE, Cache, attend, check, check_select, i32, normal, run_select, sparse_cache
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    import __graft_entry__ as g
+    g.build()
+    assert torch.cuda.is_available()
+
+
+# ------------------------------------------------------------------ lengths past max_ctx
+@pytest.mark.parametrize("max_ctx", [4096, 4070])
+def test_select_takes_a_length_past_max_ctx_as_max_ctx(max_ctx):
+    """Lengths come from device memory unchecked. The scores' rows end at max_ctx: a
+    longer length changes no other list's choice and nothing behind the workspace."""
+    hs_lens = [max_ctx, 1000, max_ctx]
+    B, T, H, N = 4, 2, 16, 6
+    c = sparse_cache(hs_lens, max_ctx=max_ctx)
+    means = normal(100, 3, c.P, P.DIM)
+    q = normal(101, B, T, H, P.DIM)
+    req = i32(0, 1, 2, 1)
+    tree = torch.tensor([[1, 3]] * B, dtype=torch.int64, device="cuda")
+    for tr in (None, tree):
+        c.set_ctx(hs_lens)
+        want, want_pos = run_select(c, q, means, N, 1, 2, tr, req, topk=True)
+        check_select(c, q, means, want, 1, 2, tr, req=[0, 1, 2, 1])
+        assert c.pool.get_error() == 0
+        for longer in (max_ctx + 1, max_ctx + 64 * 33, 2 ** 31 - 1):
+            c.pool.set_ctx_lens(i32(longer, 1000, longer))
+            pages = torch.full((B, T, N), -7, **I32)
+            pos = torch.full((B, T, N * 64), -7, **I32)
+            need = c.hs.hs_select_workspace_bytes(c.pool.handle, B, T)
+            ws = torch.full((need + (1 << 20),), 0xA5, dtype=torch.uint8, device="cuda")
+            c.pool.select_pages(q, means, req, pages, 1, 2, tr, pos, ws)
+            assert c.pool.get_error() == c.hs.HS_DEVERR_INDEX_RANGE
+            assert torch.equal(pages, want) and torch.equal(pos, want_pos)
+            assert bool((ws[need:] == 0xA5).all())
+    c.close()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+def test_attention_and_means_take_a_length_past_max_ctx_as_max_ctx(dtype):
+    max_ctx = 330
+    c = Cache(dtype, [max_ctx, 200], max_ctx=max_ctx)
+    q = normal(102, 2, 3, 16, P.DIM)
+    lists = torch.tensor([[5, 0, 3], [2, 1, 3]], **I32)
+    pr, pp = i32(0, 0, 1), i32(5, 2, 3)
+
+    def means():
+        m = torch.zeros(2, c.P, P.DIM, dtype=torch.bfloat16, device="cuda")
+        c.pool.page_means(pr, pp, m)
+        torch.cuda.synchronize()
+        return m
+
+    want = attend(c, q, None), attend(c, q, lists), means()
+    assert c.pool.get_error() == 0
+    for longer in (max_ctx + 1, 64 * 500, 2 ** 31 - 1):
+        c.pool.set_ctx_lens(i32(longer, 200))
+        for i, pages in enumerate((None, lists)):
+            got = attend(c, q, pages)
+            assert c.pool.get_error() == c.hs.HS_DEVERR_INDEX_RANGE
+            assert torch.equal(got[0].view(torch.int16), want[i][0].view(torch.int16)) and torch.equal(got[1], want[i][1])
+        assert torch.equal(means().view(torch.int16), want[2].view(torch.int16))
+        assert c.pool.get_error() == c.hs.HS_DEVERR_INDEX_RANGE
+    c.pool.set_ctx_lens(i32(-5, 200))  # a negative one holds nothing
+    out, lse = attend(c, q, None)
+    assert not out[0].any() and bool((lse[0] == -math.inf).all())
+    check(c, q[1:], out[1:], lse[1:], lambda b, t: None, req=[1])
+    c.close()

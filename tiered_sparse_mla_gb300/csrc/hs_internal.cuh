@@ -85,6 +85,13 @@ struct hs_pool {
 // ---------------------------------------------------------------- PTX helpers
 namespace hs {
 
+// A request's context length as the kernels over pages take it. Lengths that were
+// copied from device memory have not been checked, and what is laid out by page
+// (means, scores, the page table) ends at max_ctx.
+__device__ __forceinline__ int context_within(int len, int max_ctx) {
+    return len < 0 ? 0 : (len < max_ctx ? len : max_ctx);
+}
+
 __device__ __forceinline__ void cluster_arrive() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
 }

@@ -143,7 +143,7 @@ struct PageParams {
     float *lse, *ws_lse;
     uint32_t *err;
     int inside;            // 2: the two splits are joined inside the cluster; or 0
-    int T, H, N, M, mtiles, nsplit, max_req, max_pages, zero_block;
+    int T, H, N, M, mtiles, nsplit, max_req, max_pages, max_ctx, zero_block;
     int n_full;            // units (128 query rows of a list) not split; the others are, nsplit ways
     int ws_list0, ws_lists;  // the lists that the partials' space holds
     int tpl;               // lists per request: list i is token i % tpl of request i / tpl
@@ -310,10 +310,10 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     if (loader && entries && lane < p.N) e0 = entries[lane];
     const int req = p.req[list / p.tpl];
     const bool req_ok = req >= 0 && req < p.max_req;
-    const int L = req_ok ? p.ctx[req] : 0;
+    const int len = req_ok ? p.ctx[req] : 0, L = hs::context_within(len, p.max_ctx);
     const int2 *table = p.table + (size_t)(req_ok ? req : 0) * p.max_pages;
     int nsteps = 0, first = 0, end = 0, npages = 0;
-    uint32_t bad = 0;
+    uint32_t bad = len > p.max_ctx ? HS_DEVERR_INDEX_RANGE : 0u;
     // page number and block of the entries from i0 on, one per lane
     auto fetch = [&](int i0, int &pg, int &blk) {
         const int i = first + i0 + lane;
@@ -1387,6 +1387,7 @@ hs_status page_entry(hs_pool_t pool, int64_t lists, int32_t T, int32_t tpl, int3
     p.ws_lists = (int)lists - pl.list0;
     p.max_req = pool->cfg.max_requests;
     p.max_pages = pool->max_pages;
+    p.max_ctx = pool->cfg.max_ctx;
     p.zero_block = (int)pool->cfg.n_gpu_blocks;
     p.tpl = tpl;
     p.scale_log2 = sm_scale * 1.4426950408889634f;

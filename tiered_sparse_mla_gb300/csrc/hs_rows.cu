@@ -181,7 +181,7 @@ constexpr int MT = 288;
 template <bool FP8>
 __global__ void __launch_bounds__(MT)
 means_kernel(const uint8_t *rows, const float *scales, const uint8_t *host_rows, const float *host_scales,
-             const int2 *page, const int32_t *ctx, int max_req, int max_pages, const int32_t *req,
+             const int2 *page, const int32_t *ctx, int max_req, int max_pages, int max_ctx, const int32_t *req,
              const int32_t *pg, __nv_bfloat16 *means, uint32_t *err) {
     constexpr int RB = FP8 ? kDim : 2 * kDim;
     constexpr int V = RB / 16;       // pieces of a row: 72, or 36
@@ -199,8 +199,9 @@ means_kernel(const uint8_t *rows, const float *scales, const uint8_t *host_rows,
         if (threadIdx.x == 0) atomicOr(err, HS_DEVERR_BAD_PAGE);
         return;
     }
-    const long long left = (long long)ctx[r] - (long long)p * kPage;
-    const int n = left <= 0 ? 0 : (left < kPage ? (int)left : kPage);  // rows that hold a token
+    const int len = ctx[r], left = hs::context_within(len, max_ctx) - p * kPage;
+    const int n = left <= 0 ? 0 : (left < kPage ? left : kPage);  // rows that hold a token
+    if (len > max_ctx && threadIdx.x == 0) atomicOr(err, HS_DEVERR_INDEX_RANGE);
     const bool dev = e.x >= 0;
     const size_t row0 = (size_t)(dev ? e.x : e.y) * kPage;
     const uint8_t *src = (dev ? rows : host_rows) + row0 * RB;
@@ -322,5 +323,5 @@ extern "C" hs_status hs_page_means(hs_pool_t pool, int32_t n, const int32_t *d_r
     return launch(pool->cfg.dtype == HS_BF16 ? means_kernel<false> : means_kernel<true>, (unsigned)n, MT, stream,
                   pool->d_rows, pool->d_scales, pool->hd_rows, pool->hd_scales,
                   reinterpret_cast<const int2 *>(pool->d_page), pool->d_ctx, pool->cfg.max_requests, pool->max_pages,
-                  d_req, d_page, static_cast<__nv_bfloat16 *>(d_means), pool->d_err);
+                  pool->cfg.max_ctx, d_req, d_page, static_cast<__nv_bfloat16 *>(d_means), pool->d_err);
 }

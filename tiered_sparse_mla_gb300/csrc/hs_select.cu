@@ -73,7 +73,7 @@ struct ScoreParams {
     uint32_t *err;
     int B, T, H, tpg, groups, parts;  // tokens per group; groups of tokens; parts of the tiles
     int hpc, N;                     // heads per pass (H, or 256 at most); N: query rows of a pass, rounded up
-    int Pp, max_req;
+    int Pp, max_req, max_ctx;
 };
 
 __global__ void __launch_bounds__(ST, 1)
@@ -101,7 +101,7 @@ score_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ C
     // the pages of request b of the list, none if its index is out of range
     auto pages_at = [&](int b, int &r) {
         r = b < p.B ? p.req[b] : -1;
-        return r >= 0 && r < p.max_req ? pages_of(p.ctx[r]) : 0;
+        return r >= 0 && r < p.max_req ? pages_of(hs::context_within(p.ctx[r], p.max_ctx)) : 0;
     };
     auto tiles_of = [](int pages) { return (pages + SP - 1) / SP; };
 
@@ -467,7 +467,7 @@ struct SelectParams {
     uint64_t *key64;                 // [B*T][Pp] only written when more than CAP pages are near the border
     int32_t *pages, *topk;           // [B][T][N], [B][T][N*64] or null
     uint32_t *err;
-    int T, H, N, n_first, n_last, Pp, max_req, max_pages;
+    int T, H, N, n_first, n_last, Pp, max_req, max_pages, max_ctx;
 };
 
 __device__ __forceinline__ uint32_t order32(float x) {
@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(LT) select_kernel(const SelectParams p) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int r = p.req[b];
     const bool req_ok = r >= 0 && r < p.max_req;
-    const int L = req_ok ? p.ctx[r] : 0;
+    const int len = req_ok ? p.ctx[r] : 0, L = hs::context_within(len, p.max_ctx);
     const __nv_bfloat16 *q = p.q + (size_t)list * p.H * kDim;
     const long long end = p.tree ? (long long)L : (long long)L - p.T + t + 1;
     const int n = end <= 0 ? 0 : pages_of((int)end);  // pages that hold a token this one may see
@@ -565,6 +565,7 @@ __global__ void __launch_bounds__(LT) select_kernel(const SelectParams p) {
     const int k = p.N - p.n_first - p.n_last;
     const int c0 = p.n_first, cnt = n - p.n_last - c0;  // candidates (when not all)
     if (!req_ok && tid == 0) atomicOr(p.err, HS_DEVERR_BAD_REQUEST);
+    if (len > p.max_ctx && tid == 0) atomicOr(p.err, HS_DEVERR_INDEX_RANGE);
     if (tid == 0) {
         s_nsel = s_m = s_near = 0;
         s_lo = 0xffffffffu;
@@ -998,6 +999,7 @@ extern "C" hs_status hs_select_pages(hs_pool_t pool, int32_t B, int32_t T, int32
         if (2 * units > INT32_MAX || tiles > INT32_MAX) return HS_ERR_INVALID_ARG;
         p.Pp = w.Pp;
         p.max_req = pool->cfg.max_requests;
+        p.max_ctx = pool->cfg.max_ctx;
         CUtensorMap tc, tq;
         if (!make_map(&tc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d_means, kDim, pool->max_pages,
                       pool->cfg.max_requests, 2 * kDim, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
@@ -1042,6 +1044,7 @@ extern "C" hs_status hs_select_pages(hs_pool_t pool, int32_t B, int32_t T, int32
     p.Pp = w.Pp;
     p.max_req = pool->cfg.max_requests;
     p.max_pages = pool->max_pages;
+    p.max_ctx = pool->cfg.max_ctx;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((int64_t)B * T), 1, 1);
     const bool few = pool->max_pages <= KEEP * 256;
