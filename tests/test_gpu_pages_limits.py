@@ -78,3 +78,48 @@ def test_attention_and_means_take_a_length_past_max_ctx_as_max_ctx(dtype):
     assert not out[0].any() and bool((lse[0] == -math.inf).all())
     check(c, q[1:], out[1:], lse[1:], lambda b, t: None, req=[1])
     c.close()
+
+
+# ------------------------------------------------------------------ selection: very small values
+@pytest.mark.parametrize("q_exp,c_exp", [(-70, 0), (-90, 0), (0, -70), (0, -90), (-62, -45)])
+def test_select_where_squares_leave_the_normal_range(q_exp, c_exp):
+    """Queries or means whose squares are below f32's smallest normal number, with products
+    above it: a power of two on all of them changes no choice."""
+    c = sparse_cache([64 * 600] * 4)
+    small = 2.0 ** -5 * (1 - 2.0 ** -8)
+    means = torch.zeros(4, c.P, P.DIM)
+    means[:2, :, 0] = 512.0
+    up, down = means[0, 0].clone(), means[0, 0].clone()
+    up[0] = down[0] = 1024.0
+    up[2:], down[2:] = small, -small
+    down[1] = 35.0 / 32
+    for r, (i, j) in enumerate(((100, 300), (300, 100))):  # short sums have these two in the other order
+        means[r, i], means[r, j] = up, down
+    g = torch.Generator().manual_seed(103)
+    base = torch.randn(P.DIM, generator=g) * 64  # large terms that cancel, a small rest
+    means[2] = base
+    means[2, :, 0] = torch.randint(-3, 4, (c.P,), generator=g) * 2.0 ** -9
+    means[3] = torch.randn(c.P, P.DIM, generator=g)
+    q = torch.ones(4, 1, 8, P.DIM)
+    q[:2, ..., 0], q[:2, ..., 1] = 1024.0, 32.0
+    q[2:] = torch.randn(2, 1, 1, P.DIM, generator=g)
+    q[2, ..., 0] = 1.0
+    q, means = (q * 2.0 ** q_exp).to(torch.bfloat16).cuda(), (means * 2.0 ** c_exp).to(torch.bfloat16).cuda()
+    for N in (3, 40):
+        pages = run_select(c, q, means, N, 1, 1)
+        check_select(c, q, means, pages, 1, 1)
+    c.close()
+
+
+def test_select_of_zeros():
+    """Queries or means of exact zeros: equal scores, so the lowest pages."""
+    c = sparse_cache([64 * 5000] * 3)
+    means = normal(104, 3, c.P, P.DIM)
+    means[1] = 0.0
+    means[2, 7::2] = -0.0
+    q = normal(105, 3, 2, 16, P.DIM)
+    q[0] = 0.0
+    q[0, 1, 3] = -0.0
+    for N in (5, 700):
+        check_select(c, q, means, run_select(c, q, means, N), 1, 2)
+    c.close()

@@ -12,7 +12,10 @@
 // others just below the cut; 2^-22 to 2^-23 with random ones). A page whose score is
 // more than 2 E from the border is therefore in or out, and the few nearer ones are
 // summed again as pairs of f32. Equal scores go to the lower page. Products below
-// f32's normal numbers may count as zero.
+// f32's normal numbers may count as zero. Norms and sums may lose what lies below
+// those numbers too: each square at most 2^-126, so 576 of them are added to a norm's
+// square, and E gets 2^-116 more (576 products and 36 sums of at most 2^-126). Only
+// where all queries, or all means, are exactly zero are the sums exact as they are.
 #include <cfloat>
 #include <climits>
 #include <cstdint>
@@ -67,13 +70,16 @@ static_assert(SCORE_SMEM <= 232448, "shared memory");
 
 struct ScoreParams {
     const int32_t *req, *ctx;
+    const uint4 *means;  // [max_req][max_pages] rows of 72
     float *s1;       // [B*T][Pp] best head's score
     uint32_t *s2;    // [B*T][Pp] best score of another group of heads (BF16, rounded up) << 16 | group
-    float *cn, *cm;  // [B][Pp] |c_p|^2; [B][Pp / 32] the largest of 32 pages (infinite if one is not finite)
+    // [B][Pp] |c_p|^2, zero for rows of zeros alone; [B][Pp / 32] the largest of 32 pages
+    // (infinite if one is not finite)
+    float *cn, *cm;
     uint32_t *err;
     int B, T, H, tpg, groups, parts;  // tokens per group; groups of tokens; parts of the tiles
     int hpc, N;                     // heads per pass (H, or 256 at most); N: query rows of a pass, rounded up
-    int Pp, max_req, max_ctx;
+    int Pp, max_req, max_pages, max_ctx;
 };
 
 __global__ void __launch_bounds__(ST, 1)
@@ -346,7 +352,14 @@ score_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ C
             if (ok && need) {
                 const int page = (w.lo + i) * SP + 128 * rank + row;
                 const bool in = page < w.pages;
-                const float cn = (n4[0] + n4[1]) + (n4[2] + n4[3]);
+                float cn = (n4[0] + n4[1]) + (n4[2] + n4[3]);
+                if (in && cn == 0.f) {  // rare: squares below f32's normal numbers, or zeros
+                    const uint4 *c = p.means + ((size_t)w.r * p.max_pages + page) * (2 * kDim / 16);
+                    uint32_t any = 0;
+#pragma unroll 1
+                    for (int k = 0; k < 2 * kDim / 16; ++k) any |= c[k].x | c[k].y | c[k].z | c[k].w;
+                    if (any & 0x7fff7fffu) cn = FLT_MIN;
+                }
                 float m = in ? (cn <= FLT_MAX ? cn : INFINITY) : 0.f;
                 m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
                 if (in) p.cn[(size_t)w.b * p.Pp + page] = cn;
@@ -477,6 +490,8 @@ __device__ __forceinline__ uint32_t order32(float x) {
 __device__ __forceinline__ float from_order32(uint32_t k) {
     return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
+constexpr float NORM_LOST = kDim * FLT_MIN;  // of a norm's square
+constexpr float SUMS_LOST = 2048.f * FLT_MIN;  // of 2 E
 constexpr uint32_t KEY_MOST = 0xff7fffffu, KEY_LEAST = 0x00800000u;  // of the finite scores
 // NaN ranks with minus infinity
 __device__ __forceinline__ uint64_t order64(double x) {
@@ -585,9 +600,11 @@ __global__ void __launch_bounds__(LT) select_kernel(const SelectParams p) {
         for (int h = warp; h < p.H; h += NW) {
             const uint32_t *qr = reinterpret_cast<const uint32_t *>(q + (size_t)h * kDim);
             float x = 0.f, y = 0.f;
+            uint32_t any = 0;
 #pragma unroll
             for (int i = 0; i < kDim / 64; ++i) {
                 const uint32_t w = qr[lane + 32 * i];
+                any |= w & 0x7fff7fffu;
                 const float lo = __uint_as_float(w << 16), hi = __uint_as_float(w & 0xffff0000u);
                 x = fmaf(lo, lo, x);
                 y = fmaf(hi, hi, y);
@@ -595,6 +612,7 @@ __global__ void __launch_bounds__(LT) select_kernel(const SelectParams p) {
             x += y;
 #pragma unroll
             for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+            if (x == 0.f && __any_sync(0xffffffffu, any)) x = FLT_MIN;  // not a row of zeros
             mx = x == x ? fmaxf(mx, x) : INFINITY;
             if (mx == INFINITY) break;
         }
@@ -769,8 +787,10 @@ __global__ void __launch_bounds__(LT) select_kernel(const SelectParams p) {
         // ------------------------------------------------ above it, and near it
         // The interval's bounds are rounded outwards; a bound that is NaN (norms
         // beyond 32 bits) makes every page near.
-        const float theta = from_order32(s_theta);
-        const float e2 = __fmul_ru(2.f / 32768.f * 1.001f, __fmul_ru(__fsqrt_ru(__int_as_float(s_qn)), __fsqrt_ru(__int_as_float(s_cn))));
+        const float theta = from_order32(s_theta), qn = __int_as_float(s_qn), cmost = __int_as_float(s_cn);
+        const bool same = (qn == 0.f || cmost == 0.f) && !some_unknown;  // the sums are exact as they are
+        const float qc = __fmul_ru(__fsqrt_ru(__fadd_ru(qn, NORM_LOST)), __fsqrt_ru(__fadd_ru(cmost, NORM_LOST)));
+        const float e2 = same ? 0.f : __fadd_ru(__fmul_ru(2.f / 32768.f * 1.001f, qc), SUMS_LOST);
         const float slack = __fadd_ru(e2, __fmul_ru(fabsf(theta), 1.f / 4194304.f));
         const float fup = __fadd_ru(theta, slack), fdn = __fadd_rd(theta, -slack);
         const uint32_t up = fup == fup ? order32(fup) : 0xffffffffu, dn = fdn == fdn ? order32(fdn) : 0u;
@@ -787,7 +807,6 @@ __global__ void __launch_bounds__(LT) select_kernel(const SelectParams p) {
         const int first = s_nsel;
         need = k - first;
         m = s_near;
-        const bool same = e2 == 0.f && !some_unknown;  // the sums are exact as they are
         if (m == need && m <= CAP) {
             for (int i = tid; i < m; i += LT) sel[first + i] = c0 + lpage[i];
         } else if (m <= CAP) {
@@ -981,6 +1000,7 @@ extern "C" hs_status hs_select_pages(hs_pool_t pool, int32_t B, int32_t T, int32
         ScoreParams p{};
         p.req = d_req_ids;
         p.ctx = pool->d_ctx;
+        p.means = static_cast<const uint4 *>(d_means);
         p.s1 = reinterpret_cast<float *>(ws + w.s1);
         p.s2 = reinterpret_cast<uint32_t *>(ws + w.s2);
         p.cn = reinterpret_cast<float *>(ws + w.cn);
@@ -999,6 +1019,7 @@ extern "C" hs_status hs_select_pages(hs_pool_t pool, int32_t B, int32_t T, int32
         if (2 * units > INT32_MAX || tiles > INT32_MAX) return HS_ERR_INVALID_ARG;
         p.Pp = w.Pp;
         p.max_req = pool->cfg.max_requests;
+        p.max_pages = pool->max_pages;
         p.max_ctx = pool->cfg.max_ctx;
         CUtensorMap tc, tq;
         if (!make_map(&tc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d_means, kDim, pool->max_pages,
