@@ -123,3 +123,28 @@ def test_select_of_zeros():
     for N in (5, 700):
         check_select(c, q, means, run_select(c, q, means, N), 1, 2)
     c.close()
+
+
+def test_select_weighs_every_head_of_a_page_whose_norm_overflows():
+    """A thousand equal scores of 1, and one page of 1 + 2^-16 by a head whose 32-bit sum
+    says 0 (a pair of 2^30 cancels) next to a head whose sum says 1 - 2^-8."""
+    c = sparse_cache([64 * 1000] * 2)
+    means = torch.zeros(2, c.P, P.DIM)
+    means[..., 3] = 1.0
+    for r, p in enumerate((700, 3)):
+        u = torch.zeros(P.DIM)
+        u[0] = u[128] = 2.0 ** 30
+        u[1], u[64], u[2] = 1.0, 2.0 ** -16, 1 - 2.0 ** -8
+        u[5] = 3e19  # where no query has a value: the square of the norm is infinite
+        means[r, p] = u
+    q = torch.zeros(2, 1, 8, P.DIM)
+    q[..., 3] = 1.0
+    q[:, :, 0, 0], q[:, :, 0, 128] = 1.0, -1.0
+    q[:, :, 0, 1] = q[:, :, 0, 64] = 1.0
+    q[:, :, 1:, 2] = 1.0
+    q, means = q.to(torch.bfloat16).cuda(), means.to(torch.bfloat16).cuda()
+    for N in (1, 4):
+        pages = run_select(c, q, means, N, 0, 0)
+        check_select(c, q, means, pages, 0, 0)
+    assert 700 in pages[0, 0].tolist() and 3 in pages[1, 0].tolist()
+    c.close()

@@ -846,11 +846,14 @@ __global__ void __launch_bounds__(LT) select_kernel(const SelectParams p) {
                         key = order64((double)s1[i]);
                     } else {
                         const __nv_bfloat16 *c = means + (size_t)i * kDim;
+                        // the heads whose 32-bit sums come near the best; all of them
+                        // where e2 does not bound this page's sums
+                        const bool bounded = cn[i] <= FLT_MAX;
                         float best = -INFINITY;
-                        for (int h = 0; h < p.H; ++h) best = fmaxf(best, dot32(q + (size_t)h * kDim, c));
+                        for (int h = 0; h < p.H && bounded; ++h) best = fmaxf(best, dot32(q + (size_t)h * kDim, c));
                         for (int h = 0; h < p.H; ++h) {
                             const __nv_bfloat16 *qh = q + (size_t)h * kDim;
-                            if (dot32(qh, c) < best - e2) continue;
+                            if (bounded && dot32(qh, c) < best - e2) continue;
                             const uint64_t y = order64(dot64(qh, c));
                             key = y > key ? y : key;
                         }
