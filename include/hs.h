@@ -356,9 +356,9 @@ hs_status hs_page_means(hs_pool_t pool, int32_t n, const int32_t *d_req, const i
  * The score of page p is max_h q[b][t][h] . means[req][p]. If there are more
  * than N candidates, the first n_first and the last n_last are kept and the
  * others taken by descending score, equal scores by ascending page, until
- * there are N. The choice is that of sums as exact as 64-bit ones (no part above
- * 2^-45 of the products' sum is lost; products below f32's normal numbers may
- * count as zero), not of 32-bit ones; a NaN sum counts as minus infinity.
+ * there are N. The choice is that of sums as exact as 64-bit ones (less than 2^-50
+ * of the sum of the products' magnitudes is lost; products below f32's normal
+ * numbers may count as zero), not of 32-bit ones; a NaN sum counts as minus infinity.
  *   d_q        bf16 [B][T][H][576];  d_means as hs_page_means writes them
  *   d_tree     uint64 [B][T] or NULL: as in hs_page_mla_decode; with it every
  *              page below ctx_len is a candidate for every query token

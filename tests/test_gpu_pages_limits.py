@@ -148,3 +148,49 @@ def test_select_weighs_every_head_of_a_page_whose_norm_overflows():
         check_select(c, q, means, pages, 0, 0)
     assert 700 in pages[0, 0].tolist() and 3 in pages[1, 0].tolist()
     c.close()
+
+
+# ------------------------------------------------------------------ selection: sums near the border
+def test_select_tells_sums_apart_that_pairs_of_f32_do_not():
+    """A product of 1, nine of nearly 2^-24 and eight of 2^-45 in the places that one lane
+    sums: the eight are half the last place of what the nine leave in the sum's second
+    word. The other page has 2^-43 in their stead, half as much."""
+    c = sparse_cache([64 * 600] * 2)
+    order = [2 * 0 + 64 * i + e for i in range(9) for e in (0, 1)]  # lane 0's products
+    more = torch.zeros(P.DIM)
+    more[order[0]] = 1.0
+    more[order[1:10]] = 2.0 ** -24 * (1 - 2.0 ** -8)
+    less = more.clone()
+    more[order[10:]] = 2.0 ** -45
+    less[order[10]] = 2.0 ** -43
+    means = torch.zeros(2, c.P, P.DIM)
+    for r, (i, j) in enumerate(((100, 300), (300, 100))):
+        means[r, i], means[r, j] = more, less
+    q, means = torch.ones(2, 1, 8, P.DIM).to(torch.bfloat16).cuda(), means.to(torch.bfloat16).cuda()
+    pages = run_select(c, q, means, 3, 1, 1)
+    check_select(c, q, means, pages, 1, 1)
+    assert pages[:, 0, 1].tolist() == [100, 300]
+    c.close()
+
+
+def test_select_keeps_rests_below_the_normal_range():
+    """Products near 2^-113, whose last bits, 2^-127, fall behind a sum of 2^-103: seventeen
+    of those bits against one product of 2^-124."""
+    c = sparse_cache([64 * 600] * 2)
+    lane = [[2 * l + 64 * i + e for i in range(9) for e in (0, 1)] for l in (0, 1)]
+    q = torch.ones(P.DIM)
+    q[lane[0][1:]] = 1 + 2.0 ** -7
+    more, less = torch.zeros(P.DIM), torch.zeros(P.DIM)
+    more[lane[0][0]] = less[lane[1][0]] = 2.0 ** -103
+    more[lane[0][1:]] = (1 + 2.0 ** -7) * 2.0 ** -113    # products (1 + 2^-6 + 2^-14) 2^-113
+    less[lane[1][1:]] = (1 + 2.0 ** -6) * 2.0 ** -113
+    less[4] = 2.0 ** -124
+    means = torch.zeros(2, c.P, P.DIM)
+    for r, (i, j) in enumerate(((100, 300), (300, 100))):
+        means[r, i], means[r, j] = more, less
+    q = q.expand(2, 1, 8, P.DIM).to(torch.bfloat16).cuda()
+    means = means.to(torch.bfloat16).cuda()
+    pages = run_select(c, q, means, 3, 1, 1)
+    check_select(c, q, means, pages, 1, 1)
+    assert pages[:, 0, 1].tolist() == [100, 300]
+    c.close()

@@ -11,7 +11,7 @@
 // 36 times that, 2^-15.5, in all (2^-15.84 measured with one product of |q||c| and all
 // others just below the cut; 2^-22 to 2^-23 with random ones). A page whose score is
 // more than 2 E from the border is therefore in or out, and the few nearer ones are
-// summed again as pairs of f32. Equal scores go to the lower page. Products below
+// summed again, as exactly as in 64 bits. Equal scores go to the lower page. Products below
 // f32's normal numbers may count as zero. Norms and sums may lose what lies below
 // those numbers too: each square at most 2^-126, so 576 of them are added to a norm's
 // square, and E gets 2^-116 more (576 products and 36 sums of at most 2^-126). Only
@@ -500,10 +500,43 @@ __device__ __forceinline__ uint64_t order64(double x) {
     return (u >> 63) ? ~u : (u | (1ull << 63));
 }
 
-// q . c to nearly 64 bits, by a warp (every lane gets the sum). Products of BF16
-// values are exact in f32, and sums are kept as a pair of f32 that loses nothing
-// above 2^-45 of the products' sum (Knuth's two-sum); 64-bit arithmetic is 1/64 as
-// fast and only joins the last pair.
+// f32 arithmetic that keeps numbers below the normal ones (the build flushes them).
+__device__ __forceinline__ float add_full(float a, float b) {
+    float d;
+    asm("add.rn.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float sub_full(float a, float b) {
+    float d;
+    asm("sub.rn.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float mul_full(float a, float b) {
+    float d;
+    asm("mul.rn.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ double to_double(float a) {
+    double d;
+    asm("cvt.f64.f32 %0, %1;" : "=d"(d) : "f"(a));
+    return d;
+}
+// a becomes a + b; returns what its rounding left out, exactly (Knuth's two-sum).
+__device__ __forceinline__ float two_sum(float &a, float b) {
+    const float t = add_full(a, b), y = sub_full(t, a);
+    const float rest = add_full(sub_full(a, sub_full(t, y)), sub_full(b, y));
+    a = t;
+    return rest;
+}
+
+// q . c as exactly as in 64 bits, by a warp (every lane gets the sum). Products of BF16
+// values above f32's smallest numbers are exact in f32, and sums are kept in three words:
+// what a sum's rounding leaves out goes into the second by another two-sum, and what that
+// leaves out into the third. With S the sum of the products' magnitudes, and the adds of
+// the first word 23 deep (18 products of a lane, five joins), of the second 28: the second
+// word stays below 23 x 2^-24 S, the third below 28 x 2^-24 of that, 2^-38 S, and its
+// roundings are below 2^-56 S. With the two of the join in 64 bits, whose arithmetic is
+// 1/64 as fast, less than 2^-50 S is lost. (Two words lose up to 2^-39 S.)
 __device__ __forceinline__ double dot64(const __nv_bfloat16 *q, const __nv_bfloat16 *c) {
     const int lane = threadIdx.x & 31;
     uint32_t a[kDim / 64], b[kDim / 64];
@@ -512,24 +545,21 @@ __device__ __forceinline__ double dot64(const __nv_bfloat16 *q, const __nv_bfloa
         a[i] = reinterpret_cast<const uint32_t *>(q)[lane + 32 * i];
         b[i] = reinterpret_cast<const uint32_t *>(c)[lane + 32 * i];
     }
-    float s = 0.f, r = 0.f;
-    auto add = [&](float x) {
-        const float t = __fadd_rn(s, x), y = __fsub_rn(t, s);
-        r = __fadd_rn(r, __fadd_rn(__fsub_rn(s, __fsub_rn(t, y)), __fsub_rn(x, y)));
-        s = t;
-    };
+    float s = 0.f, r = 0.f, t = 0.f;
+    auto add = [&](float x) { t = add_full(t, two_sum(r, two_sum(s, x))); };
 #pragma unroll
     for (int i = 0; i < kDim / 64; ++i) {
-        add(__fmul_rn(__uint_as_float(a[i] << 16), __uint_as_float(b[i] << 16)));
-        add(__fmul_rn(__uint_as_float(a[i] & 0xffff0000u), __uint_as_float(b[i] & 0xffff0000u)));
+        add(mul_full(__uint_as_float(a[i] << 16), __uint_as_float(b[i] << 16)));
+        add(mul_full(__uint_as_float(a[i] & 0xffff0000u), __uint_as_float(b[i] & 0xffff0000u)));
     }
 #pragma unroll 1
     for (int o = 16; o >= 1; o >>= 1) {
         const float so = __shfl_xor_sync(0xffffffffu, s, o), ro = __shfl_xor_sync(0xffffffffu, r, o);
-        r = __fadd_rn(r, ro);
+        const float to = __shfl_xor_sync(0xffffffffu, t, o);
         add(so);
+        t = add_full(t, add_full(two_sum(r, ro), to));
     }
-    double acc = (double)s + (double)r;
+    double acc = to_double(s) + (to_double(r) + to_double(t));
     if (!(fabs(acc) <= (double)FLT_MAX)) {
         // infinities, NaN, or products beyond 32 bits: the same in every lane
         acc = 0.0;
