@@ -194,3 +194,27 @@ def test_select_keeps_rests_below_the_normal_range():
     check_select(c, q, means, pages, 1, 1)
     assert pages[:, 0, 1].tolist() == [100, 300]
     c.close()
+
+
+# ------------------------------------------------------------------ append
+def test_append_fp8_keeps_the_sign_of_zeros():
+    """Codes equal the definition's, e4m3(x / scale), zeros' signs included, whatever the
+    row's largest magnitude."""
+    n = 96
+    c = Cache("fp8", [n], garbage=False)
+    g = torch.Generator().manual_seed(106)
+    x = torch.randn(n, P.DIM, generator=g)
+    x = torch.where(torch.rand(n, P.DIM, generator=g) < 0.5, x, torch.where(x < 0, -0.0, 0.0))
+    x[:, 1::7] *= 2.0 ** -30  # quotients that round to zero
+    x[:, 3::9] = torch.sign(x[:, 3::9]) * 2.0 ** -130  # subnormal values
+    x[::3] *= 2.0 ** 80
+    x[1::3] *= 2.0 ** -80
+    x[5] = -0.0
+    x = x.to(torch.bfloat16)
+    c.pool.append_rows(x[None].cuda(), i32(0), i32(0))
+    torch.cuda.synchronize()
+    code, s = P.quantise(x)
+    at = torch.tensor([c.row(0, p) for p in range(n)])
+    assert torch.equal(c.pool.gpu_scales().cpu()[at], s)
+    assert torch.equal(c.pool.gpu_rows().cpu()[at], code.view(torch.uint8))
+    c.close()

@@ -46,7 +46,8 @@ struct AppendParams {
 // (Markstein, "Computation of elementary functions on the IBM RISC System/6000
 // processor", 1990, theorem on division with a correctly rounded reciprocal)
 // give the correctly rounded quotient as long as no step leaves the normal
-// range, which the caller ensures; otherwise the divide instruction is used.
+// range, which the caller ensures; otherwise the divide instruction is used. The
+// residual is taken with the other sign: that of a zero is +0, and -0 less +0 stays -0.
 template <bool SAFE>
 __device__ __forceinline__ uint2 quantise8(uint4 v, float scale, float inv) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -58,8 +59,8 @@ __device__ __forceinline__ uint2 quantise8(uint4 v, float scale, float inv) {
         if (SAFE) {
             qa = __fmul_rn(a, inv);
             qb = __fmul_rn(b, inv);
-            qa = __fmaf_rn(__fmaf_rn(-qa, scale, a), inv, qa);
-            qb = __fmaf_rn(__fmaf_rn(-qb, scale, b), inv, qb);
+            qa = __fmaf_rn(-__fmaf_rn(qa, scale, -a), inv, qa);
+            qb = __fmaf_rn(-__fmaf_rn(qb, scale, -b), inv, qb);
         } else {  // subnormal operands kept (the build flushes them elsewhere)
             asm("div.rn.f32 %0, %1, %2;" : "=f"(qa) : "f"(a), "f"(scale));
             asm("div.rn.f32 %0, %1, %2;" : "=f"(qb) : "f"(b), "f"(scale));
