@@ -218,3 +218,18 @@ def test_append_fp8_keeps_the_sign_of_zeros():
     assert torch.equal(c.pool.gpu_scales().cpu()[at], s)
     assert torch.equal(c.pool.gpu_rows().cpu()[at], code.view(torch.uint8))
     c.close()
+
+
+# ------------------------------------------------------------------ attention
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+def test_attention_of_an_unknown_request_reports_nothing_else(dtype):
+    c = Cache(dtype, [300])
+    q = normal(107, 2, 2, 16, P.DIM)
+    lists = torch.tensor([[1, 3, -1], [2, 0, 4]], **I32)
+    for bad in (5, -1):
+        for pages, per_token in ((None, False), (lists, False), (lists[:, None].expand(2, 2, 3).contiguous(), True)):
+            out, lse = attend(c, q, pages, req=i32(bad, 0), per_token=per_token)
+            assert c.pool.get_error() == c.hs.HS_DEVERR_BAD_REQUEST
+            assert not out[0].any() and bool((lse[0] == -math.inf).all())
+            check(c, q[1:], out[1:], lse[1:], lambda b, t: None if pages is None else [2, 0, 4], req=[0])
+    c.close()

@@ -468,7 +468,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         bad = __reduce_or_sync(0xffffffffu, bad);
         if (lane == 0 && kw) {
-            if (!req_ok) bad |= HS_DEVERR_BAD_REQUEST;
+            if (!req_ok) bad = HS_DEVERR_BAD_REQUEST;  // it has no context that an entry could lie outside of
             if (bad) atomicOr(p.err, bad);
         }
     } else if (warp == 1) {

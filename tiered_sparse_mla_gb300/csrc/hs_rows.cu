@@ -46,7 +46,8 @@ struct AppendParams {
 // (Markstein, "Computation of elementary functions on the IBM RISC System/6000
 // processor", 1990, theorem on division with a correctly rounded reciprocal)
 // give the correctly rounded quotient as long as no step leaves the normal
-// range, which the caller ensures; otherwise the divide instruction is used. The
+// range, which the caller ensures; otherwise the divide instruction is used (checked in
+// exact arithmetic for every pair of a value's and a scale's significands). The
 // residual is taken with the other sign: that of a zero is +0, and -0 less +0 stays -0.
 template <bool SAFE>
 __device__ __forceinline__ uint2 quantise8(uint4 v, float scale, float inv) {
