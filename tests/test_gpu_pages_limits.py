@@ -233,3 +233,32 @@ def test_attention_of_an_unknown_request_reports_nothing_else(dtype):
             assert not out[0].any() and bool((lse[0] == -math.inf).all())
             check(c, q[1:], out[1:], lse[1:], lambda b, t: None if pages is None else [2, 0, 4], req=[0])
     c.close()
+
+
+# ------------------------------------------------------------------ means
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+def test_page_means_are_quotients(dtype):
+    """Sums that are exact in f32 over counts that are no powers of two: the mean is half
+    way between two BF16 values and goes to the even one."""
+    lens = [14, 28, 60, 64 + 26]
+    c = Cache(dtype, lens, garbage=False)
+    mid = {14: 345, 28: 345, 60: 293, 26: 413}
+    means = torch.zeros(4, c.P, P.DIM, dtype=torch.bfloat16, device="cuda")
+    want = torch.zeros(4, P.DIM)
+    for r, L in enumerate(lens):
+        n = L % 64
+        m = torch.full((P.DIM,), mid[n])  # odd: m - 1 and m + 1 are BF16 values, m lies between two
+        at = torch.tensor([c.row(r, L - n + i) for i in range(n)], device="cuda")
+        sign = torch.tensor([1, -1]).repeat(n // 2)
+        if dtype == "fp8":  # codes of 1 at those scales
+            c.pool.gpu_rows()[at] = torch.ones(n, P.DIM).to(torch.float8_e4m3fn).view(torch.uint8).cuda()
+            c.pool.gpu_scales()[at] = (mid[n] + sign).float().cuda()
+        else:
+            m += 4 * (torch.arange(P.DIM) % 4)
+            c.pool.gpu_rows()[at] = (m + sign[:, None]).to(torch.bfloat16).view(torch.uint8).cuda()
+        want[r] = m
+    c.pool.page_means(i32(0, 1, 2, 3), i32(0, 0, 0, 1), means)
+    torch.cuda.synchronize()
+    for r, L in enumerate(lens):
+        assert torch.equal(means[r, L // 64].cpu(), want[r].to(torch.bfloat16)), r
+    c.close()

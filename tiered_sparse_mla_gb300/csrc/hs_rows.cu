@@ -177,7 +177,9 @@ __global__ void __launch_bounds__(AT) append_kernel(const AppendParams p) {
 // One CTA per page. A thread owns one 16-byte column piece of the row and every
 // G-th row of the page, all of them loaded before the first is used, so a page
 // (72 KB BF16, 36 KB FP8) is in flight at once; the G partial sums meet in
-// shared memory. Sums in f32 in a fixed order, one rounding to BF16 at the end.
+// shared memory. Sums in f32 in a fixed order, a quotient rounded to f32 (a product with
+// a rounded 1/n puts means half way between two BF16 values on the wrong one), and one
+// rounding to BF16 at the end.
 constexpr int MT = 288;
 
 template <bool FP8>
@@ -246,7 +248,7 @@ means_kernel(const uint8_t *rows, const float *scales, const uint8_t *host_rows,
 #pragma unroll
     for (int j = 0; j < E; ++j) part[g][piece * E + j] = sum[j];
     __syncthreads();
-    const float inv = n > 0 ? __fdiv_rn(1.f, (float)n) : 0.f;
+    const float count = n > 0 ? (float)n : 1.f;
     for (int c = threadIdx.x; c < kDim / 2; c += MT) {
         float a = 0.f, b = 0.f;
 #pragma unroll
@@ -255,7 +257,7 @@ means_kernel(const uint8_t *rows, const float *scales, const uint8_t *host_rows,
             b += part[q][2 * c + 1];
         }
         *reinterpret_cast<__nv_bfloat162 *>(means + at * kDim + 2 * c) =
-            __floats2bfloat162_rn(a * inv, b * inv);
+            __floats2bfloat162_rn(__fdiv_rn(a, count), __fdiv_rn(b, count));
     }
 }
 
