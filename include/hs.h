@@ -396,7 +396,9 @@ size_t hs_select_workspace_bytes(hs_pool_t pool, int32_t B, int32_t T);
  *           calls that overlap need one each
  * FP8 pools: a query row is taken as sums of two e4m3 codes per value at a power of two
  * of its own: exact for values of at least 2^-10 of the row's largest, others are off by
- * at most 2^-17.8 of that largest; a row that is not finite gives NaN. Weights times
+ * at most 2^-17.8 of that largest; a row that is not finite gives NaN. A score is the
+ * codes' sum times the product of sm_scale, that power and the row's scale, which may
+ * count as zero below f32's normal numbers (queries below 2^-112, say). Weights times
  * row scales are rounded to F16 (2^-11 of them, or 2^-34 of the largest weight at the
  * largest scale). BF16 pools take the query as it is and round weights to BF16 (2^-8).
  * What a row that no query may see holds does not matter. An entry outside the

@@ -262,3 +262,27 @@ def test_page_means_are_quotients(dtype):
     for r, L in enumerate(lens):
         assert torch.equal(means[r, L // 64].cpu(), want[r].to(torch.bfloat16)), r
     c.close()
+
+
+@pytest.mark.parametrize("q_exp,row_exp,peak", [(100, -105, 1), (122, -118, 16), (-100, 100, 1)])
+def test_attention_fp8_queries_and_scales_of_opposite_magnitude(q_exp, row_exp, peak):
+    """Scores are ordinary numbers although the query times the codes is not one."""
+    L = 400
+    c = Cache("fp8", [L])
+    at = torch.tensor([c.row(0, i) for i in range(L)], device="cuda")
+    c.pool.gpu_scales()[at] *= 2.0 ** row_exp
+    q = (normal(108, 1, 2, 16, P.DIM).double() * 2.0 ** q_exp).to(torch.bfloat16)
+    scale = peak * SCALE * 2.0 ** -(q_exp + row_exp)
+    out, lse = attend(c, q, None, scale=scale)
+    kv = c.kv(0, torch.arange(L))
+    for t in range(2):
+        k = kv[:L - 1 + t]
+        ref = P.attention(q[0, t].double(), k, torch.ones(len(k), dtype=torch.bool, device="cuda"), scale)
+        # The output is as small or large as the rows: compare it at the rows' magnitude.
+        # What is below 2^-126 may count as zero: each of at most four splits' partials,
+        # their products with the weights, the sum, its quotient and the BF16 value, 11
+        # times 2^-126 at most. The check allows 2^-8 of the mass, so 2^8 times that joins it.
+        lost = 11 * 2.0 ** -126 * 2.0 ** 8
+        P.check_attention((out[0, t].double() * 2.0 ** -row_exp).float(), lse[0, t], ref[0] * 2.0 ** -row_exp, ref[1],
+                          (ref[2] + lost) * 2.0 ** -row_exp, ref[3], what=f"token {t}")
+    c.close()

@@ -718,12 +718,14 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 HS_TMEM_WAIT_LD32(ra);
 #pragma unroll
                 for (int e = 0; e < KT; e += 4) {
-                    const float4 f = FP8 ? ld_shared_f4(sc_at + 4 * e) : make_float4(p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2);
+                    float4 f = FP8 ? ld_shared_f4(sc_at + 4 * e) : make_float4(p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) s[e + i] = __uint_as_float(ra[e + i]);
                     if (FP8) {
-                        mul2(s[e], s[e + 1], row_scale, row_scale);
-                        mul2(s[e + 2], s[e + 3], row_scale, row_scale);
+                        // the two scales first: the codes' sum, up to 2^27, times a large
+                        // row's alone may be beyond f32 where the score is not
+                        mul2(f.x, f.y, row_scale, row_scale);
+                        mul2(f.z, f.w, row_scale, row_scale);
                     }
                     mul2(s[e], s[e + 1], f.x, f.y);
                     mul2(s[e + 2], s[e + 3], f.z, f.w);
