@@ -395,7 +395,7 @@ size_t hs_select_workspace_bytes(hs_pool_t pool, int32_t B, int32_t T);
  *           passed, max_pages for 0), 256-byte aligned, may be NULL when that is 0;
  *           calls that overlap need one each
  * FP8 pools: a query row is taken as sums of two e4m3 codes per value at a power of two
- * of its own: exact for values of at least 2^-10 of the row's largest, others are off by
+ * of its own: exact for values of at least 2^-9.8 of the row's largest, others are off by
  * at most 2^-17.8 of that largest; a row that is not finite gives NaN. A score is the
  * codes' sum times the product of sm_scale, that power and the row's scale, which may
  * count as zero below f32's normal numbers (queries below 2^-112, say). Weights times

@@ -286,3 +286,31 @@ def test_attention_fp8_queries_and_scales_of_opposite_magnitude(q_exp, row_exp, 
         P.check_attention((out[0, t].double() * 2.0 ** -row_exp).float(), lse[0, t], ref[0] * 2.0 ** -row_exp, ref[1],
                           (ref[2] + lost) * 2.0 ** -row_exp, ref[3], what=f"token {t}")
     c.close()
+
+
+@pytest.mark.parametrize("largest", [225.0, 250.0, 256.0, 448.0])
+def test_attention_fp8_small_values_beside_a_large_one(largest):
+    """A query value of at least 2^-9.8 of its row's largest is taken exactly, a smaller one
+    is off by at most 2^-17.8 of the largest. One row of context, 448 where a head has its
+    small value and 0 where it has the large one, so that lse is the score itself."""
+    H = 128
+    c = Cache("fp8", [1], garbage=False)
+    x = torch.zeros(P.DIM)
+    x[:H] = 448.0
+    at = c.row(0, 0)
+    c.pool.gpu_rows()[at] = x.to(torch.float8_e4m3fn).view(torch.uint8).cuda()
+    c.pool.gpu_scales()[at] = 1.0
+    v = torch.arange(128, 256).float()[None] * 2.0 ** torch.tensor([-16.0, -17.0, -18.0])[:, None]  # from 2^-11 to 2^-8
+    v = (v * largest).to(torch.bfloat16).flatten()[torch.randperm(384, generator=torch.Generator().manual_seed(110))]
+    for part in v.view(3, H):
+        q = torch.zeros(1, 1, H, P.DIM, dtype=torch.bfloat16)
+        q[0, 0, torch.arange(H), torch.arange(H)] = part
+        q[..., 575] = largest
+        out, lse = attend(c, q.cuda(), None, scale=1.0)
+        got, want = lse[0, 0].double().cpu() / 448, part.double()
+        off = (got - want).abs()
+        exact = want >= largest * 2.0 ** -9.8
+        assert bool(exact.any()) and not bool(exact.all())
+        # a sum of two products in f32, and lse's two roundings and products with log2(e) and ln(2)
+        assert bool((off <= torch.where(exact, 2.0 ** -20 * want, 2.0 ** -20 * want + 2.0 ** -17.8 * largest)).all())
+    c.close()

@@ -41,9 +41,10 @@
 // 128 heads, which now take 33).
 //   Q: a value times the row's power of two, which brings the row's largest to
 //      (224, 448], is the sum of two e4m3 codes, and an MMA of depth 32 takes either
-//      with the same keys: as many MMAs as one of F16. Values of at least 2^-10 of the
-//      row's largest are exact, smaller ones off by at most 2^-17.8 of that largest. A
-//      row that is not finite becomes NaN.
+//      with the same keys: as many MMAs as one of F16. Values that come to 1/4 or more
+//      are exact, their last bit is at least the codes' smallest step: 2^-9.8 of the
+//      row's largest. Smaller ones are off by at most half that step, 2^-17.8 of that
+//      largest. A row that is not finite becomes NaN.
 //   V: F16, which every code is exactly and to which the hardware converts two codes
 //      per instruction (24 against 72 clocks per 16 codes and warp for placing BF16
 //      bits with integer instructions). Two e4m3 codes per weight would spare this
