@@ -399,8 +399,8 @@ size_t hs_select_workspace_bytes(hs_pool_t pool, int32_t B, int32_t T);
  * at most 2^-17.8 of that largest; a row that is not finite gives NaN. A score is the
  * codes' sum times the product of sm_scale, that power and the row's scale, which may
  * count as zero below f32's normal numbers (queries below 2^-112, say). Weights times
- * row scales are rounded to F16 (2^-11 of them, or 2^-34 of the largest weight at the
- * largest scale). BF16 pools take the query as it is and round weights to BF16 (2^-8).
+ * row scales are rounded to F16 (2^-11 of them, or 2^-31 of the query's largest weight
+ * times scale, or 2^-142 if that is larger). BF16 pools take the query as it is and round weights to BF16 (2^-8).
  * What a row that no query may see holds does not matter. An entry outside the
  * context is skipped (HS_DEVERR_INDEX_RANGE), as is a page without a GPU block
  * (HS_DEVERR_BAD_PAGE: resolve its positions with hs_resolve_topk_union

@@ -314,3 +314,54 @@ def test_attention_fp8_small_values_beside_a_large_one(largest):
         # a sum of two products in f32, and lse's two roundings and products with log2(e) and ln(2)
         assert bool((off <= torch.where(exact, 2.0 ** -20 * want, 2.0 ** -20 * want + 2.0 ** -17.8 * largest)).all())
     c.close()
+
+
+def test_attention_fp8_rows_of_huge_scale_that_do_not_count():
+    """Rows at 2^40 times the others' scale whose weights are nothing leave the others'
+    weights their bits, whether they come before them, between them or behind."""
+    L = 700
+    c = Cache("fp8", [L] * 4, garbage=False)
+    g = torch.Generator().manual_seed(109)
+    q = torch.zeros(4, 1, 16, P.DIM)
+    q[..., :64] = torch.randn(4, 1, 16, 64, generator=g)
+    q[..., 575] = 8.0
+    q = q.to(torch.bfloat16).cuda()
+    rows, scales = c.pool.gpu_rows(), c.pool.gpu_scales()
+
+    def check_all(scale):
+        out, lse = attend(c, q, None, scale=scale)
+        for r in range(4):
+            kv = c.kv(r, range(L))
+            here = torch.tensor([float(scales[c.row(r, i)]) < 1 for i in range(L)], device="cuda")
+            seen = torch.ones(L, dtype=torch.bool, device="cuda")
+            ref = P.attention(q[r, 0].double(), kv, seen, scale)
+            # the huge rows' scores are far below all others, or exactly zero: the error of
+            # a score that counts is that of the others
+            reach = P.attention(q[r, 0].double(), kv[here], seen[here], scale)[3]
+            P.check_attention(out[r, 0], lse[r, 0], *ref[:3], reach, what=f"request {r}")
+
+    for r, where in enumerate((range(0, 40), range(300, 303), range(L - 5, L), (0, 130, 131, 400, 699))):
+        for i in where:
+            x = torch.randn(P.DIM, generator=g)
+            x[575] = -448.0  # far below every other score
+            x[:64] = 0.0
+            at = c.row(r, i)
+            rows[at] = x.to(torch.float8_e4m3fn).view(torch.uint8).cuda()
+            scales[at] = 2.0 ** 33
+    check_all(SCALE)
+    # the first row counts for a moment: the next ones' scores leave it behind
+    for r in range(4):
+        x = torch.randn(P.DIM, generator=g)
+        x[:64] = 0.0
+        x[575] = 0.0
+        at = c.row(r, 1)
+        rows[at] = x.to(torch.float8_e4m3fn).view(torch.uint8).cuda()
+        scales[at] = 2.0 ** 33
+        for i in range(128, L - 5):
+            if float(scales[c.row(r, i)]) < 2.0 ** 30:
+                at = c.row(r, i)
+                v = rows[at].clone()
+                v[575] = 0x7e  # code 448, scores that are larger by 8 * 448 * scale / 24, about 1
+                rows[at] = v
+    check_all(SCALE * 40)
+    c.close()

@@ -50,10 +50,13 @@
 //      bits with integer instructions). Two e4m3 codes per weight would spare this
 //      too, but lose small weights below 2^-10 of the codes' unit.
 //   P: F16, 2^10 exp2(score - reference) * scale / c, c a power of two that a query row
-//      keeps for the scales as it does the reference for the scores: c is raised where
-//      a scale passes 2 c, the reference where a score passes it by 4, so P <= 2^15. It
-//      is off by at most 2^-11 of it down to 2^-24 of a weight at both references, and
-//      by at most 2^-35 of that below. The probabilities' sum has the unrounded ones.
+//      keeps for the weights times scales as it does the reference for the scores. The
+//      reference follows where a score passes it by 4. c is at most 16 times the row's
+//      largest weight times scale so far, so that rows of large scale and little weight
+//      leave the others' their bits, and within that not below half the largest scale
+//      alone, which is cheap to look up: only where a scale passes 2 c, or the reference
+//      moves, are the products themselves looked at. So P <= 2^15; it is off by at most
+//      2^-11 of it, or by 2^-35 c. The probabilities' sum has the unrounded ones.
 // Every wait is bounded; on expiry the kernel sets HS_DEVERR_TIMEOUT, drains its
 // own copies and MMAs and returns.
 #include <cuda_bf16.h>
@@ -83,11 +86,12 @@ constexpr int NTI = 3;            // steps whose page numbers and scales are hel
 constexpr int NSW = 8;            // softmax warps
 constexpr int NCW = 4;            // FP8: converter warps
 constexpr uint32_t JOIN_BYTES = RM * 256 * 4 + RM * 4;  // half the columns of a partial, and its lse
-// A row's references follow where its scores' maximum passes the old one by this much
-// (log2 units), and FP8's where a scale passes twice its own: P <= 2^8, FP8: 2^15.
+// A row's reference follows where its scores' maximum passes the old one by this much
+// (log2 units): P <= 2^8, FP8: 2^15.
 template <bool FP8>
 constexpr float TAU2 = FP8 ? 4.f : 8.f;
 constexpr int P_EXP = 10;  // FP8: a weight at both references is 2^10
+constexpr float C_MOST = 16.f;  // FP8: of the scales' reference, over the largest weight times scale
 constexpr uint32_t TM_O = 0, TM_S = 256, TM_Q = 320;
 
 template <bool FP8>
@@ -110,7 +114,8 @@ struct PCfg {
     static constexpr int OFF_SC = OFF_C + NCV * GV * CCH;                 // f32 [NTI][2][64] the rows' scales
     static constexpr int OFF_SP = OFF_SC + (FP8 ? NTI * 2 * 64 * 4 : 0);  // f32 [NTI][4] their largest, by 32 keys
     static constexpr int OFF_XM = OFF_SP + (FP8 ? NTI * 16 : 0);          // f32 [softmax threads], FP8: twice
-    static constexpr int OFF_PG = OFF_XM + (FP8 ? 2 : 1) * 32 * NSW * 4;  // int32 [NTI][2]
+    static constexpr int OFF_WM = OFF_XM + (FP8 ? 2 : 1) * 32 * NSW * 4;  // f32 [RM] FP8: a row's largest weight times scale
+    static constexpr int OFF_PG = OFF_WM + (FP8 ? RM * 4 : 0);            // int32 [NTI][2]
     static constexpr int OFF_BAR = (OFF_PG + NTI * 8 + 7) & ~7;
     static constexpr int B_QFULL = 0, B_QDONE = 1, B_QREADY = 2, B_SFULL = 3, B_SFREE = 4, B_PFULL = 5,
                          B_PVDONE = 6, B_DRAIN = 7, B_JOIN = 8, B_TFULL = 9, B_TFREE = B_TFULL + NTI,
@@ -704,6 +709,8 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         float m2 = -INFINITY, l = 0.f;
         float cref = 0.f, fac = 0.f;  // FP8: the scales' reference, a power of two, and 2^10 over it
+        const uint32_t wm = base + C::OFF_WM + 4u * (uint32_t)row;
+        if (FP8 && tid < RM) st_shared_f1(wm, 0.f);  // read behind a barrier
         const float row_scale = p.scale_log2 * q_back;
         for (int j = 0; j < nsteps; ++j) {
             const int ti = j % NTI;
@@ -785,8 +792,8 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     }
                 }
             }
-            // A row's four threads share its references: where some row of the CTA
-            // outgrows its own, the rows' four maxima meet in shared memory.
+            // A row's four threads share its references: where some row of the CTA may
+            // outgrow its own, the rows' four maxima meet in shared memory.
             float alpha = 1.f;
             auto outgrown = [](float x, float ref) { return x > ref + TAU2<FP8> || (ref == -INFINITY && x != -INFINITY); };
             const bool grow = any_softmax(outgrown(tmax, m2) || (FP8 && cmax > 2.f * cref));
@@ -805,12 +812,30 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     l *= alpha;
                     m2 = tall;
                 }
-                if (FP8 && call > 2.f * cref) {
-                    // at least 2^-107: its inverse, and the epilogue's factor, are normal
-                    const uint32_t e = max(__float_as_uint(call) >> 23, 20u);
-                    fac = __uint_as_float((254u + P_EXP - e) << 23);
-                    alpha *= cref * fac * (1.f / (1 << P_EXP));
-                    cref = __uint_as_float(e << 23);
+                if (FP8) {
+                    float w = 0.f;  // the largest weight times scale (NaN drops out)
+                    if (ok) {
+                        const float mneg = m2 == -INFINITY ? 0.f : -m2;
+#pragma unroll
+                        for (int e = 0; e < KT; e += 4) {
+                            const float4 f = ld_shared_f4(sc_at + 4 * e);
+                            w = max3(w, ex2(s[e] + mneg) * fabsf(f.x), ex2(s[e + 1] + mneg) * fabsf(f.y));
+                            w = max3(w, ex2(s[e + 2] + mneg) * fabsf(f.z), ex2(s[e + 3] + mneg) * fabsf(f.w));
+                        }
+                    }
+                    st_shared_f1(xm + 4 * tid, w);
+                    named_bar_sync(1, 32 * NSW);
+                    const float most = fmaxf(of_row(0), ld_shared_f1(wm) * alpha);
+                    named_bar_sync(1, 32 * NSW);
+                    if (hf == 0 && kh == 0) st_shared_f1(wm, most);
+                    const float want = fminf(fmaxf(call, most), C_MOST * most);
+                    if (want > 2.f * cref || cref > C_MOST * most) {
+                        // at least 2^-107: its inverse, and the epilogue's factor, are normal
+                        const uint32_t e = max(__float_as_uint(want) >> 23, 20u);
+                        fac = __uint_as_float((254u + P_EXP - e) << 23);
+                        alpha = alpha * cref * fac * (1.f / (1 << P_EXP));
+                        cref = __uint_as_float(e << 23);
+                    }
                 }
             }
             uint32_t pk[KT / 2];
