@@ -405,8 +405,8 @@ size_t hs_select_workspace_bytes(hs_pool_t pool, int32_t B, int32_t T);
  * context is skipped (HS_DEVERR_INDEX_RANGE), as is a page without a GPU block
  * (HS_DEVERR_BAD_PAGE: resolve its positions with hs_resolve_topk_union
  * instead); a bad request id attends to nothing (HS_DEVERR_BAD_REQUEST).
- * Requires B <= 65535, 1 <= T <= 32767, H*T <= 128*65535; q and out 16-byte
- * aligned. */
+ * Requires B <= 65535, 1 <= T <= 32767, H*T <= 128*65535, B*T*H < 2^31; q and out
+ * 16-byte aligned (the workspace's size is 0 for sizes outside of that). */
 hs_status hs_page_mla_decode(hs_pool_t pool, int32_t B, int32_t T, int32_t H, int32_t N,
                              const void *d_q, const int32_t *d_pages, const int32_t *d_req_ids,
                              const uint64_t *d_tree, float sm_scale, void *d_out, float *d_lse,

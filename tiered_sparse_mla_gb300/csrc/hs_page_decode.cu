@@ -1354,15 +1354,19 @@ hs_status launch_pages(int dev, cudaStream_t s, const CUtensorMap &tq, const CUt
                : HS_ERR_CUDA;
 }
 
+// Sizes that the attention takes: a plan's row counts fit 32 bits.
+bool takes(int64_t lists, int64_t T, int64_t H) {
+    return lists >= 0 && lists <= 65535 && T >= 1 && T <= 32767 && H >= 1 && T * H <= (int64_t)BM * 65535 &&
+           lists * T * H <= INT32_MAX;
+}
+
 // `lists` lists of T query tokens each; tpl > 1 (with T = 1): lists / tpl
 // requests whose tpl tokens each have their own list.
 hs_status page_entry(hs_pool_t pool, int64_t lists, int32_t T, int32_t tpl, int32_t H, int32_t N,
                      const void *d_q, const int32_t *d_pages, const int32_t *d_req_ids,
                      const uint64_t *d_tree, float sm_scale, void *d_out, float *d_lse,
                      void *d_workspace, size_t ws_bytes, void *stream) {
-    if (!pool || lists < 0 || lists > 65535 || T < 1 || T > 32767 || H < 1 || N < 0 ||
-        (int64_t)T * H > (int64_t)BM * 65535 || (d_tree && (int64_t)T * tpl > 64))
-        return HS_ERR_INVALID_ARG;
+    if (!pool || !takes(lists, T, H) || N < 0 || (d_tree && (int64_t)T * tpl > 64)) return HS_ERR_INVALID_ARG;
     if (d_pages ? N < 1 : false) return HS_ERR_INVALID_ARG;
     if (lists == 0) return HS_OK;
     if (!d_q || !d_req_ids || !d_out || !d_lse) return HS_ERR_INVALID_ARG;
@@ -1372,7 +1376,6 @@ hs_status page_entry(hs_pool_t pool, int64_t lists, int32_t T, int32_t tpl, int3
     if (dev != pool->device) return HS_ERR_INVALID_ARG;
     const bool fp8 = pool->cfg.dtype == HS_FP8_E4M3_ROWSCALE;
     const PagePlan pl = page_plan(lists, T, H, N < 1 ? pool->max_pages : N);
-    if (lists * pl.M > INT32_MAX) return HS_ERR_INVALID_ARG;
     if (pl.nsplit > 1 && (!d_workspace || ws_bytes < pl.ws_bytes || ((uintptr_t)d_workspace & 255u)))
         return HS_ERR_INVALID_ARG;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1426,7 +1429,7 @@ hs_status page_entry(hs_pool_t pool, int64_t lists, int32_t T, int32_t tpl, int3
 }  // namespace
 
 extern "C" size_t hs_page_decode_workspace_bytes(int32_t B, int32_t T, int32_t H, int32_t N) {
-    if (B < 1 || T < 1 || H < 1 || N < 1) return 0;
+    if (B < 1 || N < 1 || !takes(B, T, H)) return 0;
     return page_plan(B, T, H, N).ws_bytes;
 }
 

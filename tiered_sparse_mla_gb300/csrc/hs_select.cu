@@ -1002,7 +1002,7 @@ hs_status score_attr(int dev) {
 }  // namespace
 
 extern "C" size_t hs_select_workspace_bytes(hs_pool_t pool, int32_t B, int32_t T) {
-    if (!pool || B < 1 || T < 1) return 0;
+    if (!pool || B < 1 || B > 65535 || T < 1 || T > 32767) return 0;
     return workspace(pool, B, T).total;
 }
 
