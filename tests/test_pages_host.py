@@ -25,3 +25,26 @@ def test_workspace_of_the_largest_sizes(hs):
             n = hs.hs_page_decode_workspace_bytes(B, T, H, N)
             # partials of at most 128 splits of all rows
             assert 0 <= n <= 128 * (B * T * H * (512 * 4 + 4) + 512)
+
+
+def test_kernels_launched_early_read_nothing_through_the_read_only_path():
+    """A grid that may begin while the kernel before it still writes (it waits before it
+    reads) must not read those writes through the read-only path, which may hold or fetch
+    what was there before: const __restrict__ parameters, __ldg, ld.global.nc."""
+    import glob
+    import os
+    import re
+    import tiered_sparse_mla_gb300 as pkg
+    found = 0
+    for path in sorted(glob.glob(os.path.join(os.path.dirname(pkg.__file__), "csrc", "*.cu"))):
+        with open(path) as f:
+            text = re.sub(r"//[^\n]*", "", f.read())
+        for kernel in text.split("__global__")[1:]:
+            if "grid_dep_wait()" not in kernel:
+                continue
+            found += 1
+            name = re.search(r"(\w+)\s*\((?!\()", re.sub(r"__launch_bounds__\([^;{]*?\)\s*\n?", "", kernel)).group(1)
+            head = kernel[:kernel.index("{")]
+            assert "__restrict__" not in head, f"{os.path.basename(path)}: {name}"
+            assert not re.search(r"__ldg\(|ld_stream_v4\(|global\.nc", kernel), f"{os.path.basename(path)}: {name}"
+    assert found >= 7

@@ -891,8 +891,8 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 // whole merge is about one round trip to memory, with half as many blocks to
 // place once the decode's CTAs leave their SMs.
 constexpr int CMB_TPT = 2;
-__device__ __forceinline__ void combine_store(__nv_bfloat16 *__restrict__ out, float *__restrict__ lse,
-                                              int row, int c8, const float (&acc)[8], float wsum, float mx) {
+__device__ __forceinline__ void combine_store(__nv_bfloat16 *out, float *lse, int row, int c8,
+                                              const float (&acc)[8], float wsum, float mx) {
     const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
     *reinterpret_cast<uint4 *>(out + (size_t)row * 512 + c8) =
         make_uint4(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv),
@@ -900,9 +900,11 @@ __device__ __forceinline__ void combine_store(__nv_bfloat16 *__restrict__ out, f
     if (c8 == 0) lse[row] = wsum > 0.f ? mx + __logf(wsum) : -INFINITY;
 }
 __global__ void __launch_bounds__(256)
-combine_kernel(const __nv_bfloat16 *__restrict__ ws_o, const float *__restrict__ ws_lse, int nsplit,
-               int rows, __nv_bfloat16 *__restrict__ out, float *__restrict__ lse) {
-    grid_dep_wait();  // the decode grid's partials are complete
+combine_kernel(const __nv_bfloat16 *ws_o, const float *ws_lse, int nsplit, int rows, __nv_bfloat16 *out,
+               float *lse) {
+    // the decode grid's partials are complete; launched while it wrote them, so they are
+    // not read through the read-only path (no __restrict__ here)
+    grid_dep_wait();
     const int t0 = blockIdx.x * 256 + threadIdx.x, stride = gridDim.x * 256;
     constexpr int MAXS = 4;
     if (nsplit <= MAXS) {
