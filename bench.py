@@ -21,6 +21,7 @@ import hashlib
 import json
 import math
 import os
+import re
 import statistics
 import select
 import subprocess
@@ -69,18 +70,40 @@ def _peaks():
     return 6800.0, 1900.0, "fallback"
 
 
+def _headers(path: str, seen=None) -> list:
+    """The headers beside a source that it includes, directly or through one another."""
+    seen = [] if seen is None else seen
+    with open(path) as f:
+        names = re.findall(r'^\s*#\s*include\s+"([^"]+)"', f.read(), re.M)
+    for name in names:
+        h = os.path.join(os.path.dirname(path), name)
+        if os.path.exists(h) and h not in seen:
+            seen.append(h)
+            _headers(h, seen)
+    return seen
+
+
+def _sha(*paths: str) -> str:
+    h = hashlib.sha256()
+    for p in paths:
+        with open(p, "rb") as f:
+            h.update(f.read())
+    return h.hexdigest()[:16]
+
+
 def _traffic(kernel: str, src: str, in_place: bool):
     """DRAM bytes per launch from the committed ncu summary, if the kernel's
-    source is unchanged since the capture and the rows reached attention the
-    same way (in place or gathered) as in the capture (else None)."""
+    source and the headers beside it are unchanged since the capture and the rows
+    reached attention the same way (in place or gathered) as in the capture (else None)."""
     p = os.path.join(ROOT, "profiles", "traffic.json")
     if not os.path.exists(p):
         return None
     d = json.load(open(p)).get(kernel)
     if not d:
         return None
-    sha = hashlib.sha256(open(os.path.join(ROOT, src), "rb").read()).hexdigest()[:16]
-    if d.get("source_sha") != sha or d.get("in_place") != in_place:
+    path = os.path.join(ROOT, src)
+    if d.get("source_sha") != _sha(path) or d.get("headers_sha") != _sha(*sorted(_headers(path))) \
+            or d.get("in_place") != in_place:
         return None
     return d["dram_bytes_per_launch"]
 
