@@ -365,3 +365,136 @@ def test_attention_fp8_rows_of_huge_scale_that_do_not_count():
                 rows[at] = v
     check_all(SCALE * 40)
     c.close()
+
+
+# ------------------------------------------------------------------ sizes
+def small_pool(dtype, n_blocks, max_requests, max_ctx):
+    import tiered_sparse_mla_gb300 as hs
+    return hs, hs.Pool(dtype=hs.HS_FP8_E4M3_ROWSCALE if dtype == "fp8" else hs.HS_BF16, n_gpu_blocks=n_blocks,
+                       n_host_blocks=0, max_requests=max_requests, max_ctx=max_ctx, max_topk=32, hot_rows=64)
+
+
+def one_query(hs, pool, q, pages, req, tree=None):
+    B, T, H = q.shape[:3]
+    out = torch.full((B, T, H, 512), math.nan, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((B, T, H), math.nan, device="cuda")
+    n = hs.hs_page_decode_workspace_bytes(B, T, H, pool.max_pages if pages is None else pages.shape[-1])
+    pool.page_mla_decode(q, pages, req, tree, SCALE, out, lse, torch.empty(max(1, n), dtype=torch.uint8, device="cuda"))
+    torch.cuda.synchronize()
+    return out, lse
+
+
+@pytest.mark.parametrize("dtype,n", [("bf16", 70000), ("fp8", 140000)])
+def test_rows_past_32_bits_of_offset(dtype, n):
+    """Pages at both ends of a pool of more than 2^32 bytes."""
+    L = 150
+    hs, pool = small_pool(dtype, n, 1, 192)
+    blocks = [n - 1, 0, n - 2]
+    pool.page_map_range(0, 0, blocks, [-1] * 3)
+    pool.set_ctx_lens(i32(L))
+    x = normal(120, 1, L, P.DIM)
+    pool.append_rows(x, i32(0))
+    means = torch.zeros(1, 3, P.DIM, dtype=torch.bfloat16, device="cuda")
+    pool.page_means(i32(0, 0, 0), i32(0, 1, 2), means)
+    torch.cuda.synchronize()
+    at = torch.tensor([blocks[i // 64] * 64 + i % 64 for i in range(L)], device="cuda")
+    s = pool.gpu_scales()
+    kv = P.values(pool.gpu_rows()[at], None if s is None else s[at])
+    if dtype == "bf16":
+        assert torch.equal(kv, x[0].double())
+    else:
+        code, scale = P.quantise(x[0].cpu())
+        assert torch.equal(pool.gpu_rows()[at].cpu(), code.view(torch.uint8)) and torch.equal(s[at].cpu(), scale)
+    for p in range(3):
+        v = kv[64 * p:64 * p + 64]
+        tol = 2.0 ** -8 * v.mean(0).abs() + len(v) * 2.0 ** -23 * v.abs().mean(0)
+        assert bool(((means[0, p].double() - v.mean(0)).abs() <= tol).all())
+    q = normal(121, 1, 2, 16, P.DIM)
+    out, lse = one_query(hs, pool, q, None, i32(0))
+    for t in range(2):
+        ref = P.attention(q[0, t].double(), kv[:L - 1 + t], torch.ones(L - 1 + t, dtype=torch.bool, device="cuda"), SCALE)
+        P.check_attention(out[0, t], lse[0, t], *ref)
+    assert pool.get_error() == 0
+    pool.close()
+
+
+def test_select_among_means_past_32_bits_of_offset():
+    """Two requests of two million pages each: 4.8 GB of means."""
+    L = 2 ** 27
+    c = sparse_cache([L - 5, L], max_ctx=L)
+    means = torch.empty(2, c.P, P.DIM, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(122)
+    for r in range(2):
+        means[r].normal_(generator=g)
+    q = normal(123, 2, 2, 8, P.DIM)
+    pages = run_select(c, q, means, 20, 1, 2)
+    check_select(c, q, means, pages, 1, 2)
+    c.close()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+def test_attention_of_the_most_lists(dtype):
+    """65,535 lists of one page each, of three requests in turn."""
+    B, lens = 65535, [100, 128, 65]
+    c = Cache(dtype, lens)
+    q = normal(124, B, 1, 1, P.DIM)
+    req = torch.arange(B, device="cuda") % 3
+    pages = torch.randint(0, 2, (B, 1), generator=torch.Generator().manual_seed(125)).to(torch.int32).cuda()
+    out, lse = attend(c, q, pages, req=req.to(torch.int32))
+    for r in range(3):
+        for p in range(2):
+            mine = (req == r) & (pages[:, 0] == p)
+            kv = c.kv(r, range(64 * p, min(lens[r], 64 * p + 64)))
+            ref = P.attention(q[mine, 0, 0].double(), kv, torch.ones(len(kv), dtype=torch.bool, device="cuda"), SCALE)
+            P.check_attention(out[mine, 0, 0], lse[mine, 0, 0], *ref, what=f"request {r} page {p}")
+    c.close()
+
+
+@pytest.mark.parametrize("dtype,T,H", [("bf16", 32767, 1), ("fp8", 32767, 3), ("bf16", 1, 70000), ("fp8", 2, 40000)])
+def test_attention_of_the_most_rows(dtype, T, H):
+    """As many query tokens as a request may have, each with its own border, and as many
+    heads as need hundreds of tiles; every 997th token, or all."""
+    L = T + 333
+    c = Cache(dtype, [L])
+    q = normal(126, 1, T, H, P.DIM)
+    out, lse = attend(c, q, None)
+    kv = c.kv(0, range(L))
+    for t in sorted({*range(0, T, 997), T - 1}):
+        k = kv[:L - T + t + 1]
+        ref = P.attention(q[0, t].double(), k, torch.ones(len(k), dtype=torch.bool, device="cuda"), SCALE)
+        P.check_attention(out[0, t], lse[0, t], *ref, what=f"token {t}")
+    c.close()
+
+
+@pytest.mark.parametrize("T,H", [(32767, 1), (4, 65535)])
+def test_select_of_the_most_rows(T, H):
+    L = T + 700
+    c = sparse_cache([L])
+    means = normal(127, 1, c.P, P.DIM)
+    q = normal(128, 1, T, H, P.DIM)
+    N = 5
+    pages = run_select(c, q, means, N, 1, 1)
+    m = means[0].double()
+    for t in sorted({*range(0, T, 331), T - 1}):
+        want = P.select(q[0, t].double(), m, -(-(L - T + t + 1) // 64), N, 1, 1)
+        assert pages[0, t].tolist() == want + [-1] * (N - len(want)), t
+    c.close()
+
+
+def test_select_of_the_most_requests():
+    """65,535 lists, of five requests in turn, one of them empty and one unknown."""
+    B, lens = 65535, [700, 64, 0, 1500]
+    c = sparse_cache(lens)
+    means = normal(129, 4, c.P, P.DIM)
+    q = normal(130, B, 1, 2, P.DIM)
+    req = torch.arange(B, device="cuda") % 5
+    pages = run_select(c, q, means, 3, 1, 1, req=req.to(torch.int32))[:, 0]
+    assert bool((pages[req == 4] == -1).all()) and bool((pages[req == 2] == -1).all())
+    assert bool((pages[req == 1] == i32(0, -1, -1)).all())
+    for r in (0, 3):
+        n = -(-lens[r] // 64)
+        s = (q[req == r, 0].double() @ means[r, :n].double().T).amax(1)
+        best = s[:, 1:n - 1].argmax(1) + 1
+        want = torch.stack([torch.zeros_like(best), best, torch.full_like(best, n - 1)], 1)
+        assert torch.equal(pages[req == r].long(), want)
+    c.close(c.hs.HS_DEVERR_BAD_REQUEST)
