@@ -20,8 +20,8 @@
 // Bound: an MMA of 128 keys takes 45 clocks (256 value columns: 64), so a step is
 // 36 x 45 + 16 x 64 = 2.7k clocks, and its shared-memory traffic (the MMAs' operands,
 // the copies, FP8's conversions) about as many at 128 bytes a clock. Measured: BF16
-// 2.8k-3.0k clocks a step (8 x 32 tokens x 128 heads over 16,384 rows: 728 us, 1.44
-// PFLOP/s), FP8 2.8k-3.2k (4 x 8 tokens x 16 heads over 131,072 rows: 108 us). An earlier
+// 2.8k-3.0k clocks a step (8 x 32 tokens x 128 heads over 16,384 rows: 732 us, 1.44
+// PFLOP/s), FP8 2.9k-3.2k (4 x 8 tokens x 16 heads over 131,072 rows: 111 us). An earlier
 // form, one CTA per half of the value columns and both computing S, was bound by the
 // issue of its 80 smaller MMAs per 128 keys and by their operands' shared-memory reads.
 // Roles in each CTA:
@@ -38,7 +38,7 @@
 // FP8: S is taken from the e4m3 codes themselves (kind::f8f6f4), so K needs no
 // conversion (with K's chunks converted to F16 like V's, the shared-memory traffic and
 // the converters' issue made a step 4.0k clocks: 44 us for 16 x 4 lists of 2,048 rows of
-// 128 heads, which now take 33).
+// 128 heads, which now take 34).
 //   Q: a value times the row's power of two, which brings the row's largest to
 //      (224, 448], is the sum of two e4m3 codes, and an MMA of depth 32 takes either
 //      with the same keys: as many MMAs as one of F16. Values that come to 1/4 or more
@@ -1210,7 +1210,7 @@ constexpr double US_STEP = 1.6, US_ENDS = 7.0;
 // count that the model makes shortest; the join is 3.5 us and about 5 MB of
 // partials written and read per us. Where there are more units than pairs of CTAs at
 // once, those of the last, partly filled round may be split by themselves
-// (8 x 32 tokens of 128 heads, 256 units on 76 pairs, 16,384 rows: 728 us a call
+// (8 x 32 tokens of 128 heads, 256 units on 76 pairs, 16,384 rows: 732 us a call
 // against 757 with all units in two).
 PagePlan page_plan(int64_t lists, int64_t T, int64_t H, int64_t N) {
     PagePlan pl{};

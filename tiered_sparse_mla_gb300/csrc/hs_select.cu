@@ -47,7 +47,8 @@ __host__ __device__ __forceinline__ int pages_of(int tokens) {
 // last tile, so the MMAs hardly pause.
 // Bound: one MMA of 256 x 256 x 16 takes 128 clocks, so 256 rows per pass need 4.6k
 // clocks per tile of 256 pages; fewer rows are bound by the pages' bytes. 16 requests
-// of 16,384 pages with 512 query rows each (155 GFLOP, 302 MB): 99 us, 1.56 PFLOP/s.
+// of 16,384 pages with 512 query rows each (155 GFLOP, 302 MB): 92 us by itself, 99 in calls
+// back to back, under which the clock falls: 1.68 and 1.56 PFLOP/s.
 // Measured there: ranges cut at requests, which fill 64 of 76 pairs, 107 us; four ring
 // stages instead of five 105 us; one CTA per 128 pages with the queries streamed past
 // each tile, which moves 6x the pages' bytes from L2, about 300 us.
