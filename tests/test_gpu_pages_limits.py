@@ -498,3 +498,22 @@ def test_select_of_the_most_requests():
         want = torch.stack([torch.zeros_like(best), best, torch.full_like(best, n - 1)], 1)
         assert torch.equal(pages[req == r].long(), want)
     c.close(c.hs.HS_DEVERR_BAD_REQUEST)
+
+
+def test_select_with_heads_of_nan():
+    """Heads that hold a NaN count for nothing; where all of them do, all scores are equal."""
+    c = sparse_cache([64 * 5000, 64 * 700])
+    means = normal(131, 2, c.P, P.DIM)
+    means[1, 700:] = math.nan
+    means[0, 11, 3], means[0, 12, 4], means[1, 5, 6] = math.nan, math.inf, -math.inf
+    q = normal(132, 2, 4, 16, P.DIM)
+    q[:, 1, 3, 100] = math.nan
+    q[:, 2, 1:, 7] = math.nan
+    q[:, 3, :, 0] = math.nan
+    q[0, 2, 2, 9] = math.inf
+    for N in (5, 600):
+        check_select(c, q, means, run_select(c, q, means, N, 1, 2), 1, 2)
+    q[:, :, 0] = 0.0
+    q[:, 0, 1:] = math.nan
+    check_select(c, q, means, run_select(c, q, means, 600, 1, 2), 1, 2)
+    c.close()

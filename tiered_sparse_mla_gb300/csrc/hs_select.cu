@@ -616,7 +616,8 @@ __global__ void __launch_bounds__(LT) select_kernel(const SelectParams p) {
         s_nsel = s_m = s_near = 0;
         s_lo = 0xffffffffu;
         s_hi = 0u;
-        s_qn = s_cn = 0;
+        s_qn = __float_as_int(-1.f);
+        s_cn = 0;
     }
     if (all) {
         for (int i = tid; i < p.N; i += LT) sorted[i] = i < n ? i : -1;
@@ -626,8 +627,9 @@ __global__ void __launch_bounds__(LT) select_kernel(const SelectParams p) {
     }
     __syncthreads();
     if (!all && k > 0) {
-        // max |q_h|^2; the queries were there before the scores' kernel began
-        float mx = 0.f;
+        // max |q_h|^2; the queries were there before the scores' kernel began. A head that
+        // holds a NaN has no sum that counts, so its norm does not either.
+        float mx = -1.f;
         for (int h = warp; h < p.H; h += NW) {
             const uint32_t *qr = reinterpret_cast<const uint32_t *>(q + (size_t)h * kDim);
             float x = 0.f, y = 0.f;
@@ -644,10 +646,11 @@ __global__ void __launch_bounds__(LT) select_kernel(const SelectParams p) {
 #pragma unroll
             for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
             if (x == 0.f && __any_sync(0xffffffffu, any)) x = FLT_MIN;  // not a row of zeros
-            mx = x == x ? fmaxf(mx, x) : INFINITY;
+            mx = fmaxf(mx, x);  // NaN drops out
             if (mx == INFINITY) break;
         }
-        if (lane == 0) atomicMax(&s_qn, __float_as_int(mx));  // not negative
+        // as an integer: the order of those that are not negative, and -1.f below them
+        if (lane == 0) atomicMax(&s_qn, __float_as_int(mx));
     }
     grid_dep_wait();  // the scores
     grid_dep_launch();
@@ -707,7 +710,9 @@ __global__ void __launch_bounds__(LT) select_kernel(const SelectParams p) {
         lo = s_lo;
         hi = s_hi;
         // a page whose score or norm is not finite says nothing in 32 bits
-        const bool some_unknown = lo < KEY_LEAST || hi > KEY_MOST || __int_as_float(s_cn) > FLT_MAX;
+        // (where every head holds a NaN, all scores are minus infinity)
+        const float qn = __int_as_float(s_qn);
+        const bool some_unknown = qn >= 0.f && (lo < KEY_LEAST || hi > KEY_MOST || __int_as_float(s_cn) > FLT_MAX);
         if (some_unknown) {
             // those pages' scores in 64 bits; what stands for them in 32 is the
             // rounded sum
@@ -818,8 +823,8 @@ __global__ void __launch_bounds__(LT) select_kernel(const SelectParams p) {
         // ------------------------------------------------ above it, and near it
         // The interval's bounds are rounded outwards; a bound that is NaN (norms
         // beyond 32 bits) makes every page near.
-        const float theta = from_order32(s_theta), qn = __int_as_float(s_qn), cmost = __int_as_float(s_cn);
-        const bool same = (qn == 0.f || cmost == 0.f) && !some_unknown;  // the sums are exact as they are
+        const float theta = from_order32(s_theta), cmost = __int_as_float(s_cn);
+        const bool same = qn < 0.f || ((qn == 0.f || cmost == 0.f) && !some_unknown);  // the sums are exact as they are
         const float qc = __fmul_ru(__fsqrt_ru(__fadd_ru(qn, NORM_LOST)), __fsqrt_ru(__fadd_ru(cmost, NORM_LOST)));
         const float e2 = same ? 0.f : __fadd_ru(__fmul_ru(2.f / 32768.f * 1.001f, qc), SUMS_LOST);
         const float slack = __fadd_ru(e2, __fmul_ru(fabsf(theta), 1.f / 4194304.f));
