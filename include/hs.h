@@ -17,7 +17,10 @@
  * Around it: new tokens' rows into the cache (hs_append_rows), the pages a
  * query token attends to chosen by a cheap score (hs_page_means,
  * hs_select_pages), and attention over whole pages, for lists of them and for
- * trees of drafted tokens (hs_page_mla_decode, hs_page_mla_decode_per_token).
+ * trees of drafted tokens (hs_page_mla_decode, hs_page_mla_decode_per_token), or
+ * with a sliding window (hs_page_mla_decode_window); the attention weight that pages
+ * get and their eviction by it (hs_page_weights, hs_evict_pages); drafts held
+ * against the target's probabilities (hs_verify_drafts).
  *
  * Conventions
  *  - Streams are cudaStream_t values passed as void* (NULL = legacy stream).
@@ -424,6 +427,107 @@ hs_status hs_page_mla_decode_per_token(hs_pool_t pool, int32_t B, int32_t T, int
                                        const int32_t *d_req_ids, const uint64_t *d_tree,
                                        float sm_scale, void *d_out, float *d_lse,
                                        void *d_workspace, size_t ws_bytes, void *stream);
+
+/* hs_page_mla_decode over every page of the context with a sliding window: a query token at
+ * position x sees, of the positions that it would see there, those above x - window and
+ * those below n_sink (the first tokens, which stay visible).
+ *   d_tree  as in hs_page_mla_decode; a query token that sees s nodes is at position
+ *           x = L_b - T + s - 1. Requires window >= T (HS_ERR_UNSUPPORTED), so that no
+ *           node is out of another's window
+ *   d_workspace / ws_bytes: hs_window_workspace_bytes(pool, B, T, H, window, n_sink) bytes,
+ *           256-byte aligned, may be NULL when that is 0; calls that overlap need one each
+ * Pages that no query token of a request sees are not read and need no GPU block. Layouts,
+ * results, roundings and errors are those of hs_page_mla_decode.
+ * Requires window >= 1, n_sink >= 0. */
+hs_status hs_page_mla_decode_window(hs_pool_t pool, int32_t B, int32_t T, int32_t H, int32_t window,
+                                    int32_t n_sink, const void *d_q, const int32_t *d_req_ids,
+                                    const uint64_t *d_tree, float sm_scale, void *d_out, float *d_lse,
+                                    void *d_workspace, size_t ws_bytes, void *stream);
+size_t hs_window_workspace_bytes(hs_pool_t pool, int32_t B, int32_t T, int32_t H, int32_t window,
+                                 int32_t n_sink);
+
+/* The attention weight that the rows of each page get from the query rows q, as attention
+ * with the given lse hands it out: for page p of request r = d_req_ids[b]
+ *   d_weights[r][p] = decay * d_prior[r][p]
+ *                     + sum over t, h and the page's positions j that query token t sees
+ *                       of exp(sm_scale * q[b][t][h].k_j - lse[b][t][h])
+ *   d_q     bf16 [B][T][H][576];  d_lse float [B][T][H] as the attention wrote it (attention
+ *           to fewer pages makes those pages' weights right, the others' arbitrary); a query
+ *           row whose lse is not finite (it saw nothing, or is not a number) adds nothing
+ *   d_tree  as in hs_page_mla_decode
+ *   d_prior float [max_requests][max_pages]: d_weights itself to add up in place, another
+ *           array (that does not overlap it), or NULL: nothing, as with decay 0, where it is not read
+ *   d_weights float [max_requests][max_pages]: entries of pages that hold a position below
+ *           ctx_len are written, the others left as they were
+ * A page without a GPU block gets no new weight. Request ids are distinct; a bad one is
+ * skipped (HS_DEVERR_BAD_REQUEST). What a row that no query sees holds does not matter. FP8
+ * pools take the query as hs_page_mla_decode does. Sums are in f32, in an order that
+ * depends on the sizes alone.
+ *   d_workspace / ws_bytes: hs_weights_workspace_bytes(pool, B, T, H) bytes, 256-byte aligned,
+ *           may be NULL when that is 0; calls that overlap need one each
+ * Requires B <= 65535, 1 <= T <= 32767 (64 with a tree), H >= 1, T*H <= 2^22; q 16-byte aligned. */
+hs_status hs_page_weights(hs_pool_t pool, int32_t B, int32_t T, int32_t H, const void *d_q,
+                          const float *d_lse, const int32_t *d_req_ids, const uint64_t *d_tree,
+                          float sm_scale, float decay, const float *d_prior, float *d_weights,
+                          void *d_workspace, size_t ws_bytes, void *stream);
+size_t hs_weights_workspace_bytes(hs_pool_t pool, int32_t B, int32_t T, int32_t H);
+
+/* Eviction by weight: request d_req[i] keeps d_budget[i] of its resident pages below ctx_len
+ * on the GPU: the first n_first and the last n_last pages of its context (even if they
+ * are more), then the others by descending weight, equal weights by ascending page; NaN counts
+ * as minus infinity. The others lose their GPU block, their host copies stay.
+ *   d_weights float [max_requests][max_pages] (hs_page_weights)
+ *   d_kept    int32 [n][N] out: the kept pages, ascending, -1 behind them, as
+ *             hs_page_mla_decode takes them; HS_DEVERR_CAPACITY if there are more than N (the
+ *             first N are listed, all are kept)
+ *   d_freed / d_n_freed: the freed GPU blocks, [n][max_pages] and [n], in ascending page order
+ *   flags     HS_EVICT_SAVED_ONLY: pages without a host copy are kept, as the first are;
+ *             HS_EVICT_PLAN: the lists are written and nothing is released
+ * One launch, asynchronous on `stream`; order it with what reads the same requests' pages. The
+ * request ids are distinct. A bad one frees nothing and keeps no page (HS_DEVERR_BAD_REQUEST); a
+ * negative budget frees nothing (HS_DEVERR_BAD_PAGE). */
+#define HS_EVICT_SAVED_ONLY 1u
+#define HS_EVICT_PLAN       2u
+hs_status hs_evict_pages(hs_pool_t pool, int32_t n, int32_t N, int32_t n_first, int32_t n_last,
+                         uint32_t flags, const int32_t *d_req, const int32_t *d_budget,
+                         const float *d_weights, int32_t *d_kept, int32_t *d_freed,
+                         int32_t *d_n_freed, void *stream);
+
+/* ---- drafts against the target's probabilities --------------------------- */
+
+typedef enum { HS_PROB_F32 = 0, HS_PROB_BF16 = 1 } hs_prob_dtype;
+
+/* How much of each request's draft the target accepts, and the token after it, from given
+ * random numbers. Node t = 0 .. T-1 of request b is the token d_tokens[b][t] (that of node 0,
+ * which the last step chose, is not looked at); -1: no token. Row t of d_probs is the target's
+ * distribution of the token after node t.
+ *   d_probs       [B][T] rows of V probabilities (dtype: hs_prob_dtype), probs_ld elements apart
+ *   d_draft_probs [B][T-1] rows, draft_ld apart: row t-1 is the distribution that token t
+ *                 was drawn from; or NULL: the drafted tokens are sure guesses
+ *   d_tree        uint64 [B][T] or NULL, as in hs_page_mla_decode: a node's parent is the last
+ *                 node before it that it sees. NULL: a chain, node t-1 is the parent of t.
+ *                 HS_ERR_UNSUPPORTED together with d_draft_probs
+ *   d_uniform     float [B][T] in [0, 1): [t] decides on node t, [0] draws the next token
+ * From node 0 on, the children of the last accepted node are tried in order: with draft
+ * probabilities the child t with token x stays where u_t * q(x) < p(x), else where u_t * s < p(x),
+ * s being 1 less the probabilities of the children refused before it (a token that an
+ * earlier child had counts as 0). Where none stays, the next token is drawn: from
+ * max(p - q, 0) if a child was refused by draft probabilities, else from p without the refused
+ * children's tokens; if that leaves nothing, from p. It is the first token v at which the sum
+ * of the values up to v exceeds u_0 times the sum of all.
+ *   d_index  int32 [B][T] out: the accepted path's nodes in order (0 first), -1 behind
+ *            them, as hs_append_rows takes them
+ *   d_count  int32 [B] out: how many they are;  d_next int32 [B] out: the next token, -1 (and
+ *            HS_DEVERR_INDEX_RANGE) where p is zero throughout
+ * Values outside [0, 1] and NaN count as the nearest of them and as 0. Sums are in steps of
+ * 2^-62 and exact (they end at 4). A token outside [-1, V) counts as -1 (HS_DEVERR_INDEX_RANGE).
+ * Requires B <= 65535, 1 <= T <= 64, V >= 1, rows at least V apart, pointers aligned to
+ * their elements. The pool gives the device and takes the errors. */
+hs_status hs_verify_drafts(hs_pool_t pool, int32_t B, int32_t T, int32_t V, int32_t dtype,
+                           const void *d_probs, int64_t probs_ld, const void *d_draft_probs,
+                           int64_t draft_ld, const int32_t *d_tokens, const uint64_t *d_tree,
+                           const float *d_uniform, int32_t *d_index, int32_t *d_count,
+                           int32_t *d_next, void *stream);
 
 /* Failure-detection check: launches one device wait on a barrier phase that
  * nothing completes, bounded by limit_us (1 .. 2,000,000) exactly like the

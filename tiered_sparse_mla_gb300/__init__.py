@@ -25,6 +25,8 @@ HS_DEVERR_INDEX_RANGE, HS_DEVERR_DUPLICATE, HS_DEVERR_NO_HOST = 1, 2, 4
 HS_DEVERR_BAD_REQUEST, HS_DEVERR_CAPACITY, HS_DEVERR_TIMEOUT = 8, 16, 32
 HS_DEVERR_BAD_PAGE = 64
 HS_BF16, HS_FP8_E4M3_ROWSCALE = 0, 1
+HS_EVICT_SAVED_ONLY, HS_EVICT_PLAN = 1, 2
+HS_PROB_F32, HS_PROB_BF16 = 0, 1
 
 EXPORTED = [
     "hs_pool_create", "hs_pool_destroy", "hs_pool_get_config", "hs_pool_get_tables",
@@ -39,6 +41,8 @@ EXPORTED = [
     "hs_active_copy", "hs_demote_cold_pages", "hs_append_rows", "hs_page_means",
     "hs_select_pages", "hs_select_workspace_bytes", "hs_page_mla_decode",
     "hs_page_decode_workspace_bytes", "hs_page_mla_decode_per_token",
+    "hs_page_mla_decode_window", "hs_window_workspace_bytes", "hs_page_weights",
+    "hs_weights_workspace_bytes", "hs_evict_pages", "hs_verify_drafts",
 ]
 HS_STATIC_DECODE_WS_BYTES = 24 << 20
 
@@ -121,6 +125,15 @@ def load() -> C.CDLL:
         "hs_page_decode_workspace_bytes": ([i32, i32, i32, i32], sz),
         "hs_page_mla_decode_per_token": ([vp, i32, i32, i32, i32, vp, vp, vp, vp, C.c_float, vp,
                                           vp, vp, sz, vp], i32),
+        "hs_page_mla_decode_window": ([vp, i32, i32, i32, i32, i32, vp, vp, vp, C.c_float, vp, vp,
+                                       vp, sz, vp], i32),
+        "hs_window_workspace_bytes": ([vp, i32, i32, i32, i32, i32], sz),
+        "hs_page_weights": ([vp, i32, i32, i32, vp, vp, vp, vp, C.c_float, C.c_float, vp, vp, vp,
+                             sz, vp], i32),
+        "hs_weights_workspace_bytes": ([vp, i32, i32, i32], sz),
+        "hs_evict_pages": ([vp, i32, i32, i32, i32, C.c_uint32, vp, vp, vp, vp, vp, vp, vp], i32),
+        "hs_verify_drafts": ([vp, i32, i32, i32, i32, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp,
+                              vp], i32),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -425,6 +438,111 @@ def hs_page_mla_decode_per_token(pool: int, q, pages, req_ids, tree, sm_scale: f
         _stream(stream)))
 
 
+def hs_window_workspace_bytes(pool: int, B: int, T: int, H: int, window: int, n_sink: int) -> int:
+    return load().hs_window_workspace_bytes(pool, B, T, H, window, n_sink)
+
+
+def hs_page_mla_decode_window(pool: int, q, req_ids, tree, window: int, n_sink: int,
+                              sm_scale: float, out, lse, workspace=None, stream=None):
+    """hs_page_mla_decode over the last `window` positions and the first n_sink ones (see
+    hs.h); workspace of hs_window_workspace_bytes."""
+    B, T, H = q.shape[:3]
+    ws, wp = _ws(workspace)
+    _check("hs_page_mla_decode_window", load().hs_page_mla_decode_window(
+        pool, B, T, H, window, n_sink, _arg("q", q, "bfloat16", B, T, H, 576),
+        _arg("req_ids", req_ids, "int32", B), _arg("tree", tree, "int64", B, T, optional=True),
+        float(sm_scale), _arg("out", out, "bfloat16", B, T, H, 512),
+        _arg("lse", lse, "float32", B, T, H), wp, ws, _stream(stream)))
+
+
+def _table_shape(pool: int):
+    return _means_shape(pool)[:2]
+
+
+def hs_weights_workspace_bytes(pool: int, B: int, T: int, H: int) -> int:
+    return load().hs_weights_workspace_bytes(pool, B, T, H)
+
+
+def hs_page_weights(pool: int, q, lse, req_ids, tree, sm_scale: float, weights, prior=None,
+                    decay: float = 1.0, workspace=None, stream=None, table_shape=None):
+    """The attention weight that each page gets from the query rows q (see hs.h). q bf16
+    [B][T][H][576]; lse float32 [B][T][H]; weights, prior float32 [max_requests][max_pages]
+    (prior: weights itself, another tensor or None)."""
+    B, T, H = q.shape[:3]
+    shape = table_shape or _table_shape(pool)
+    ws, wp = _ws(workspace)
+    _check("hs_page_weights", load().hs_page_weights(
+        pool, B, T, H, _arg("q", q, "bfloat16", B, T, H, 576), _arg("lse", lse, "float32", B, T, H),
+        _arg("req_ids", req_ids, "int32", B), _arg("tree", tree, "int64", B, T, optional=True),
+        float(sm_scale), float(decay), _arg("prior", prior, "float32", *shape, optional=True),
+        _arg("weights", weights, "float32", *shape), wp, ws, _stream(stream)))
+
+
+def hs_evict_pages(pool: int, req, budget, weights, kept, freed, n_freed, n_first: int = 1,
+                   n_last: int = 1, saved_only: bool = False, plan: bool = False, stream=None,
+                   table_shape=None):
+    """Each request's pages of the least weight lose their GPU block (see hs.h). req, budget,
+    n_freed int32 [n]; weights float32 [max_requests][max_pages]; kept int32 [n][N] and freed
+    int32 [n][max_pages] out. plan: the lists only."""
+    n, N = kept.shape
+    shape = table_shape or _table_shape(pool)
+    flags = (HS_EVICT_SAVED_ONLY if saved_only else 0) | (HS_EVICT_PLAN if plan else 0)
+    _check("hs_evict_pages", load().hs_evict_pages(
+        pool, n, N, n_first, n_last, flags, _arg("req", req, "int32", n),
+        _arg("budget", budget, "int32", n), _arg("weights", weights, "float32", *shape),
+        _arg("kept", kept, "int32", n, N), _arg("freed", freed, "int32", n, shape[1]),
+        _arg("n_freed", n_freed, "int32", n), _stream(stream)))
+
+
+_prob_dtypes: dict = {}
+
+
+def _prob_rows(name: str, t, B: int, rows: int, V: int):
+    """Pointer, distance of rows and hs_prob_dtype of probabilities [B][rows][V], whose rows may
+    lie further apart than V values, all equally far."""
+    import torch
+    if not _prob_dtypes:
+        _prob_dtypes.update({torch.float32: HS_PROB_F32, torch.bfloat16: HS_PROB_BF16})
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if t.dtype not in _prob_dtypes:
+        raise ValueError(f"{name}: expected float32 or bfloat16, got {t.dtype}")
+    if t.shape != (B, rows, V):
+        raise ValueError(f"{name}: expected shape {[B, rows, V]}, got {list(t.shape)}")
+    if t.get_device() != _only_device:
+        dev = torch.cuda.current_device()
+        if t.get_device() != dev:
+            raise ValueError(f"{name}: on CUDA device {t.get_device()}, the current one is {dev}")
+    if B * rows == 0:
+        return None, V, _prob_dtypes[t.dtype]
+    sb, sr, sv = t.stride()
+    ld = sr if rows > 1 else (sb if B > 1 else V)
+    if (V > 1 and sv != 1) or ld < V or (rows > 1 and B > 1 and sb != rows * ld):
+        raise ValueError(f"{name}: expected rows of {V} contiguous values, equally far apart")
+    return t.data_ptr(), ld, _prob_dtypes[t.dtype]
+
+
+def hs_verify_drafts(pool: int, tokens, probs, draft_probs, tree, uniform, index, count, next_token,
+                     stream=None):
+    """The accepted part of each draft and the token after it (see hs.h). tokens int32 [B][T];
+    probs float32 or bfloat16 [B][T][V], draft_probs the same [B][T-1][V] or None (rows of
+    either may be a wider buffer's, [..., :V]); tree int64 [B][T] or None; uniform float32
+    [B][T]; index int32 [B][T], count and next_token int32 [B] out."""
+    B, T = tokens.shape
+    V = probs.shape[-1]
+    pp, ld, kind = _prob_rows("probs", probs, B, T, V)
+    dp, dld = None, 0
+    if draft_probs is not None:
+        dp, dld, dkind = _prob_rows("draft_probs", draft_probs, B, T - 1, V)
+        if dkind != kind:
+            raise ValueError(f"draft_probs: expected {probs.dtype}, got {draft_probs.dtype}")
+    _check("hs_verify_drafts", load().hs_verify_drafts(
+        pool, B, T, V, kind, pp, ld, dp, dld, _arg("tokens", tokens, "int32", B, T),
+        _arg("tree", tree, "int64", B, T, optional=True), _arg("uniform", uniform, "float32", B, T),
+        _arg("index", index, "int32", B, T), _arg("count", count, "int32", B),
+        _arg("next_token", next_token, "int32", B), _stream(stream)))
+
+
 # ------------------------------------------------------------- convenience
 class Pool:
     """Owns one hs_pool handle; methods map one-to-one onto the C ABI."""
@@ -599,3 +717,24 @@ class Pool:
                                   workspace=None, stream=None):
         hs_page_mla_decode_per_token(self.handle, q, pages, req_ids, tree, sm_scale, out, lse,
                                      workspace, stream)
+
+    def page_mla_decode_window(self, q, req_ids, tree, window, n_sink, sm_scale, out, lse,
+                               workspace=None, stream=None):
+        hs_page_mla_decode_window(self.handle, q, req_ids, tree, window, n_sink, sm_scale, out,
+                                  lse, workspace, stream)
+
+    # page weights, eviction, drafts
+    def page_weights(self, q, lse, req_ids, tree, sm_scale, weights, prior=None, decay=1.0,
+                     workspace=None, stream=None):
+        hs_page_weights(self.handle, q, lse, req_ids, tree, sm_scale, weights, prior, decay,
+                        workspace, stream, (self.cfg.max_requests, self.max_pages))
+
+    def evict_pages(self, req, budget, weights, kept, freed, n_freed, n_first=1, n_last=1,
+                    saved_only=False, plan=False, stream=None):
+        hs_evict_pages(self.handle, req, budget, weights, kept, freed, n_freed, n_first, n_last,
+                       saved_only, plan, stream, (self.cfg.max_requests, self.max_pages))
+
+    def verify_drafts(self, tokens, probs, draft_probs, tree, uniform, index, count, next_token,
+                      stream=None):
+        hs_verify_drafts(self.handle, tokens, probs, draft_probs, tree, uniform, index, count,
+                         next_token, stream)

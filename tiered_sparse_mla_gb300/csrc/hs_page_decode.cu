@@ -1,6 +1,7 @@
 // hs_page_decode.cu -- MLA decode over whole pages of the pool, on tcgen05 tensor
 // cores: a list of pages per query token or per request, or all of a request's
-// pages, with the drafted tokens a chain or a tree.
+// pages, with the drafted tokens a chain or a tree; or a sliding window of positions with
+// the first ones beside it.
 //
 // A 64-row page lies together in the pool, so TMA brings it as boxes of 64 rows x
 // 64 columns with no per-row ids. Per step, two pages (128 keys):
@@ -57,6 +58,10 @@
 //      alone, which is cheap to look up: only where a scale passes 2 c, or the reference
 //      moves, are the products themselves looked at. So P <= 2^15; it is off by at most
 //      2^-11 of it, or by 2^-35 c. The probabilities' sum has the unrounded ones.
+// Window (WIN): a query token at position x sees the positions from x - window + 1 on, and
+// those below n_sink. A unit's entries are then the pages that some row of it sees, the first
+// ones and those of its window, found by arithmetic; rows are masked from below too on
+// the few pages where a row's window may begin.
 // Every wait is bounded; on expiry the kernel sets HS_DEVERR_TIMEOUT, drains its
 // own copies and MMAs and returns.
 #include <cuda_bf16.h>
@@ -153,6 +158,7 @@ struct PageParams {
     int n_full;            // units (128 query rows of a list) not split; the others are, nsplit ways
     int ws_list0, ws_lists;  // the lists that the partials' space holds
     int tpl;               // lists per request: list i is token i % tpl of request i / tpl
+    int window, n_sink;    // WIN
     float scale_log2;
 };
 
@@ -245,7 +251,7 @@ __device__ __noinline__ void rescale_o(uint32_t at, float alpha) {
     tmem_wait_st();
 }
 
-template <bool FP8>
+template <bool FP8, bool WIN>
 __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
 page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k1,
                    const __grid_constant__ CUtensorMap tm_k2, const __grid_constant__ CUtensorMap tm_o,
@@ -319,6 +325,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     const int len = req_ok ? p.ctx[req] : 0, L = hs::context_within(len, p.max_ctx);
     const int2 *table = p.table + (size_t)(req_ok ? req : 0) * p.max_pages;
     int nsteps = 0, first = 0, end = 0, npages = 0;
+    int wskip = 0, wsinks = INT_MAX;  // WIN: entries from wsinks on are pages wskip later
     uint32_t bad = len > p.max_ctx ? HS_DEVERR_INDEX_RANGE : 0u;
     // page number and block of the entries from i0 on, one per lane
     auto fetch = [&](int i0, int &pg, int &blk) {
@@ -327,6 +334,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const int kept = __shfl_sync(0xffffffffu, e0, i & 31);
         int x = -1, g = -1;
         if (in) x = entries ? (i < 32 ? kept : entries[i]) : i;
+        if (WIN && in) x = i < wsinks ? i : i + wskip;
         if (x >= 0 && x < p.max_pages) g = table[x].x;
         pg = -1;
         blk = p.zero_block;
@@ -351,6 +359,19 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             end = __reduce_max_sync(0xffffffffu, end);
         } else {
             end = L <= 0 ? 0 : (L - 1) / kPage + 1;
+        }
+        if (WIN && end > 0) {
+            // The positions that some row sees: up to its last token's, and from its first
+            // token's window on (a tree's node may be as high up as the context's end).
+            const int t0 = p.tree ? -1 : mt * BM / p.H, t1 = p.tree ? p.T - 1 : (min(p.M, mt * BM + BM) - 1) / p.H;
+            const int top = L - p.T + t1, low = (int)max((long long)L - p.T + t0 - p.window + 1, 0ll);
+            end = top < 0 ? 0 : top / kPage + 1;
+            const int sinks = min((int)(((long long)p.n_sink + kPage - 1) / kPage), end);
+            if (low / kPage > sinks) {
+                wsinks = sinks;
+                wskip = low / kPage - sinks;
+                end -= wskip;
+            }
         }
         // splits begin at even entries: a step is two pages
         const long long steps = (end + 1) / 2;
@@ -707,6 +728,10 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             tree = p.tree[(size_t)(list / p.tpl) * nt + t];
             if (nt < 64) tree &= (1ull << nt) - 1;
         }
+        // WIN: the row's first position, and the last of its CTA pair's rows' first ones
+        auto from = [&](int at) { return (int)max((long long)draft + at - p.window + 1, 0ll); };
+        const int low = WIN ? from(p.tree ? __popcll(tree) - 1 : t) : 0;
+        const int low_max = WIN ? from(p.tree ? nt - 1 : (min(p.M, mt * BM + BM) - 1) / p.H) : 0;
         float m2 = -INFINITY, l = 0.f;
         float cref = 0.f, fac = 0.f;  // FP8: the scales' reference, a power of two, and 2^10 over it
         const uint32_t wm = base + C::OFF_WM + 4u * (uint32_t)row;
@@ -744,7 +769,9 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const int pg = ok ? (int)ld_shared_b32(base + C::OFF_PG + 4 * (2 * ti + kh)) : -1;
             // the keys that this row sees, as bits
             const int d = draft - max(pg, 0) * kPage;  // the first query token's position in the page
-            const bool tail = pg >= 0 && d < kPage;  // some row may not see some key
+            // WIN: some row's window may begin in the page
+            const bool head = WIN && pg >= 0 && low_max > pg * kPage && p.n_sink - kPage < pg * kPage;
+            const bool tail = (pg >= 0 && d < kPage) || head;  // some row may not see some key
             float tmax = -INFINITY, cmax = 0.f;
             uint32_t mine = ~0u;
             if (pg < 0) {
@@ -752,13 +779,20 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             } else if (tail) {
                 uint64_t seen;
                 if (p.tree) {
-                    if (d >= 0)
+                    if (WIN && d >= 64)
+                        seen = ~0ull;
+                    else if (d >= 0)
                         seen = ((1ull << d) - 1) | (tree << d);
                     else
                         seen = d > -64 ? tree >> -d : 0ull;
                 } else {
                     const int n = d + t + 1;
                     seen = n >= 64 ? ~0ull : (n <= 0 ? 0ull : (1ull << n) - 1);
+                }
+                if (WIN && head) {
+                    const int a = low - pg * kPage, n = p.n_sink - pg * kPage;
+                    const uint64_t on = a >= 64 ? 0ull : (a <= 0 ? ~0ull : ~0ull << a);
+                    seen &= on | (n <= 0 ? 0ull : (1ull << n) - 1);  // n is below 64 here
                 }
                 mine = (uint32_t)(seen >> (KT * hf));
             }
@@ -1263,7 +1297,7 @@ bool make_page_map(CUtensorMap *m, bool fp8, const void *rows, uint64_t n_rows, 
 }
 
 // How many clusters of two pairs of CTAs the device holds at once.
-template <bool FP8>
+template <bool FP8, bool WIN>
 int clusters_of_four(int dev) {
     static std::atomic<int> cached[64];
     int n = cached[dev].load(std::memory_order_acquire);
@@ -1278,7 +1312,7 @@ int clusters_of_four(int dev) {
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&n, page_decode_kernel<FP8>, &cfg) != cudaSuccess) {
+        if (cudaOccupancyMaxActiveClusters(&n, page_decode_kernel<FP8, WIN>, &cfg) != cudaSuccess) {
             cudaGetLastError();
             n = 0;
         }
@@ -1288,13 +1322,13 @@ int clusters_of_four(int dev) {
     return n;
 }
 
-template <bool FP8>
+template <bool FP8, bool WIN>
 hs_status launch_pages(int dev, cudaStream_t s, const CUtensorMap &tq, const CUtensorMap &k1,
                        const CUtensorMap &k2, int64_t units, const void *d_out, void *ws, const PagePlan &pl, PageParams p) {
     static std::atomic<int> state[64];
     if (dev < 0 || dev >= 64) return HS_ERR_UNSUPPORTED;
     if (state[dev].load(std::memory_order_acquire) != 1) {
-        HS_CUDA_TRY(cudaFuncSetAttribute(page_decode_kernel<FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        HS_CUDA_TRY(cudaFuncSetAttribute(page_decode_kernel<FP8, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          PCfg<FP8>::SMEM_ALLOC));
         state[dev].store(1, std::memory_order_release);
     }
@@ -1305,7 +1339,7 @@ hs_status launch_pages(int dev, cudaStream_t s, const CUtensorMap &tq, const CUt
     if (pl.nsplit > 1) {
         const int64_t steps = ((p.N < 1 ? p.max_pages : p.N) + 1) / 2;
         const double t = (double)((steps + 1) / 2) * US_STEP + US_ENDS + 1.5;
-        if (steps >= 2 && t < pl.us && units <= clusters_of_four<FP8>(dev)) p.inside = p.nsplit = 2;
+        if (steps >= 2 && t < pl.us && units <= clusters_of_four<FP8, WIN>(dev)) p.inside = p.nsplit = 2;
     }
     if (p.inside) p.n_full = 0;
     const int64_t lists = (int64_t)units / pl.mtiles;
@@ -1334,7 +1368,7 @@ hs_status launch_pages(int dev, cudaStream_t s, const CUtensorMap &tq, const CUt
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, page_decode_kernel<FP8>, tq, k1, k2, to, tw, p) != cudaSuccess) return HS_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, page_decode_kernel<FP8, WIN>, tq, k1, k2, to, tw, p) != cudaSuccess) return HS_ERR_CUDA;
     if (!split) return HS_OK;
     const int n = p.ws_lists * pl.M, skip = (p.n_full % pl.mtiles) * BM;
     cudaLaunchConfig_t cc = {};
@@ -1360,12 +1394,20 @@ bool takes(int64_t lists, int64_t T, int64_t H) {
            lists * T * H <= INT32_MAX;
 }
 
+// The most pages of a window's unit: those of the window of the unit's first token and of the
+// tokens behind it, at the worst alignment, and those of the first positions.
+int64_t window_pages(const hs_pool *pool, int64_t T, int64_t H, int64_t window, int64_t n_sink) {
+    const int64_t tokens = (BM - 1) / H + 2 < T ? (BM - 1) / H + 2 : T;
+    const int64_t n = (window + tokens + 61) / kPage + 1 + (n_sink + kPage - 1) / kPage;
+    return n < pool->max_pages ? n : pool->max_pages;
+}
+
 // `lists` lists of T query tokens each; tpl > 1 (with T = 1): lists / tpl
-// requests whose tpl tokens each have their own list.
+// requests whose tpl tokens each have their own list. window > 0: N pages a unit at most.
 hs_status page_entry(hs_pool_t pool, int64_t lists, int32_t T, int32_t tpl, int32_t H, int32_t N,
                      const void *d_q, const int32_t *d_pages, const int32_t *d_req_ids,
-                     const uint64_t *d_tree, float sm_scale, void *d_out, float *d_lse,
-                     void *d_workspace, size_t ws_bytes, void *stream) {
+                     const uint64_t *d_tree, int32_t window, int32_t n_sink, float sm_scale, void *d_out,
+                     float *d_lse, void *d_workspace, size_t ws_bytes, void *stream) {
     if (!pool || !takes(lists, T, H) || N < 0 || (d_tree && (int64_t)T * tpl > 64)) return HS_ERR_INVALID_ARG;
     if (d_pages ? N < 1 : false) return HS_ERR_INVALID_ARG;
     if (lists == 0) return HS_OK;
@@ -1421,9 +1463,15 @@ hs_status page_entry(hs_pool_t pool, int64_t lists, int32_t T, int32_t tpl, int3
     p.max_ctx = pool->cfg.max_ctx;
     p.zero_block = (int)pool->cfg.n_gpu_blocks;
     p.tpl = tpl;
+    p.window = window;
+    p.n_sink = n_sink;
     p.scale_log2 = sm_scale * 1.4426950408889634f;
-    return fp8 ? launch_pages<true>(dev, s, tq, maps[0], maps[1], lists * pl.mtiles, d_out, d_workspace, pl, p)
-               : launch_pages<false>(dev, s, tq, maps[0], maps[1], lists * pl.mtiles, d_out, d_workspace, pl, p);
+    const int64_t units = lists * pl.mtiles;
+    if (window > 0)
+        return fp8 ? launch_pages<true, true>(dev, s, tq, maps[0], maps[1], units, d_out, d_workspace, pl, p)
+                   : launch_pages<false, true>(dev, s, tq, maps[0], maps[1], units, d_out, d_workspace, pl, p);
+    return fp8 ? launch_pages<true, false>(dev, s, tq, maps[0], maps[1], units, d_out, d_workspace, pl, p)
+               : launch_pages<false, false>(dev, s, tq, maps[0], maps[1], units, d_out, d_workspace, pl, p);
 }
 
 }  // namespace
@@ -1437,7 +1485,7 @@ extern "C" hs_status hs_page_mla_decode(hs_pool_t pool, int32_t B, int32_t T, in
                                         const void *d_q, const int32_t *d_pages, const int32_t *d_req_ids,
                                         const uint64_t *d_tree, float sm_scale, void *d_out, float *d_lse,
                                         void *d_workspace, size_t ws_bytes, void *stream) {
-    return page_entry(pool, B, T, 1, H, N, d_q, d_pages, d_req_ids, d_tree, sm_scale, d_out, d_lse,
+    return page_entry(pool, B, T, 1, H, N, d_q, d_pages, d_req_ids, d_tree, 0, 0, sm_scale, d_out, d_lse,
                       d_workspace, ws_bytes, stream);
 }
 
@@ -1448,6 +1496,22 @@ extern "C" hs_status hs_page_mla_decode_per_token(hs_pool_t pool, int32_t B, int
                                                   void *d_workspace, size_t ws_bytes, void *stream) {
     // request b's T lists are lists b*T .. b*T+T-1 of one query token each
     if (B < 0 || T < 1 || (int64_t)B * T > 65535 || !d_pages) return HS_ERR_INVALID_ARG;
-    return page_entry(pool, (int64_t)B * T, 1, T, H, N, d_q, d_pages, d_req_ids, d_tree, sm_scale, d_out,
-                      d_lse, d_workspace, ws_bytes, stream);
+    return page_entry(pool, (int64_t)B * T, 1, T, H, N, d_q, d_pages, d_req_ids, d_tree, 0, 0, sm_scale,
+                      d_out, d_lse, d_workspace, ws_bytes, stream);
+}
+
+extern "C" size_t hs_window_workspace_bytes(hs_pool_t pool, int32_t B, int32_t T, int32_t H, int32_t window,
+                                            int32_t n_sink) {
+    if (!pool || B < 1 || !takes(B, T, H) || window < 1 || n_sink < 0) return 0;
+    return page_plan(B, T, H, window_pages(pool, T, H, window, n_sink)).ws_bytes;
+}
+
+extern "C" hs_status hs_page_mla_decode_window(hs_pool_t pool, int32_t B, int32_t T, int32_t H, int32_t window,
+                                               int32_t n_sink, const void *d_q, const int32_t *d_req_ids,
+                                               const uint64_t *d_tree, float sm_scale, void *d_out,
+                                               float *d_lse, void *d_workspace, size_t ws_bytes, void *stream) {
+    if (!pool || !takes(B, T, H) || window < 1 || n_sink < 0) return HS_ERR_INVALID_ARG;
+    if (d_tree && T <= 64 && window < T) return HS_ERR_UNSUPPORTED;  // drafted nodes would leave the window
+    return page_entry(pool, B, T, 1, H, (int32_t)window_pages(pool, T, H, window, n_sink), d_q, nullptr,
+                      d_req_ids, d_tree, window, n_sink, sm_scale, d_out, d_lse, d_workspace, ws_bytes, stream);
 }

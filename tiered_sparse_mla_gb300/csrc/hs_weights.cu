@@ -1,0 +1,703 @@
+// hs_weights.cu -- the attention weight that each page gets, on tcgen05 tensor cores:
+//   W'[r][p] = decay W[r][p] + sum over query rows m and the page's keys j that m sees of
+//              exp(scale q_m.k_j - lse_m).
+// With the attention's lse no running maximum is needed and no product with values: one
+// pass over the keys, whose scores are exponentiated and added up where they arise.
+//
+// Work unit: a group of at most 256 query rows and a range of the key tiles (four pages)
+// of all requests laid end to end, run by two CTAs whose tensor cores work as one
+// (cta_group::2, M = 256): keys are the MMA's M rows, 128 (two pages) per CTA, so that a
+// key's sum runs along the registers of the threads that own it, and query rows its N
+// columns, half of them supplied by either CTA. The queries stay in shared memory (up to
+// 144 KB a CTA), the keys stream past once, and one tile's exponentials run while the next
+// is multiplied (two accumulators). Several groups' sums meet in a second grid.
+//   warp 0      producer: queries where the range comes to another request, key chunks;
+//   warp 1      (CTA 0) MMA issuer;
+//   warps 2-9   per request: the columns' terms (FP8: the queries as codes); per tile:
+//               the sums, thread = key and half of the columns.
+// FP8: scores from the e4m3 codes themselves (kind::f8f6f4). A query value times its row's
+// power of two, which brings the row's largest to (224, 448], is the sum of two codes: exact
+// from 2^-9.8 of that largest on, off by at most 2^-17.8 of it below. The powers of all
+// rows are told to both CTAs.
+// Bound: the keys' bytes, or for 256 rows 36 MMAs of 128 clocks per tile.
+// Every wait is bounded; on expiry the kernel sets HS_DEVERR_TIMEOUT, drains its own
+// copies and MMAs and returns.
+#include <cuda_bf16.h>
+
+#include <atomic>
+#include <climits>
+#include <cstdint>
+
+#include "hs_internal.cuh"
+#include "hs_tc.cuh"
+#include "hs_tmap.cuh"
+
+namespace {
+
+using namespace hs::tc;
+using hs::kDim;
+using hs::kPage;
+
+constexpr int TP = 4;            // pages per tile (two CTAs)
+constexpr int NCH = kDim / 64;   // depth chunks
+constexpr int MAXN = 256;        // query rows per group
+constexpr int NEW = 8;           // warps for the sums
+constexpr int WT = 64 + 32 * NEW;
+constexpr int MAXST = 16;        // ring stages, one chunk of 128 keys each
+constexpr int SMEM_MOST = 232448;
+
+template <bool FP8>
+struct WCfg {
+    static constexpr int STAGE = FP8 ? 128 * 64 : 128 * 128;
+    static constexpr int OFF_B = 0;                               // f32 [256]: -lse, in log2 units
+    static constexpr int OFF_A = OFF_B + MAXN * 4;                // FP8 f32 [2][256]: scale over the row's power
+    static constexpr int OFF_X = OFF_A + (FP8 ? 2 * MAXN * 4 : 0);  // FP8 u32 [256]: halves of the rows' maxima
+    static constexpr int OFF_PS = OFF_X + (FP8 ? MAXN * 4 : 0);   // f32 [2][8]: sums of a tile, by warp
+    static constexpr int OFF_DEAD = OFF_PS + 2 * NEW * 4;         // u32 [8]: columns that add nothing
+    static constexpr int OFF_MISC = OFF_DEAD + 32;                // TMEM base, abort flag
+    static constexpr int OFF_BAR = OFF_MISC + 16;
+    static constexpr int B_QFULL = 0, B_QREADY = 1, B_QFREE = 2, B_TAB = 3, B_DRAIN = 4, B_DFULL = 5, B_DFREE = 7,
+                         B_FULL = 9, B_FREE = B_FULL + MAXST, NBAR = B_FREE + MAXST;
+    static constexpr int HEAD = (OFF_BAR + 8 * NBAR + 15) & ~15;
+    __host__ __device__ static int stages(int N) {
+        const int room = SMEM_MOST - 1024 - HEAD - NCH * (N / 2) * 128, n = room / STAGE;
+        return n < MAXST ? n : MAXST;
+    }
+    static_assert(OFF_BAR % 8 == 0 && OFF_A % 16 == 0, "alignment");
+};
+static_assert((SMEM_MOST - 1024 - WCfg<false>::HEAD - NCH * 128 * 128) / WCfg<false>::STAGE >= 4, "ring");
+static_assert((SMEM_MOST - 1024 - WCfg<true>::HEAD - NCH * 128 * 128) / WCfg<true>::STAGE >= 8, "ring");
+
+struct WeightParams {
+    const int32_t *req, *ctx;
+    const int2 *table;
+    const uint64_t *tree;         // [B][T] or null
+    const float *lse;             // [B][T*H]
+    const float *scales;          // FP8: the pool's row scales
+    const float *prior;           // [max_req][max_pages] or null
+    float *weights;               // [max_req][max_pages]
+    float *part;                  // [groups][B][max_pages] where there are several groups
+    uint32_t *err;
+    int B, T, H, M, groups, parts, N, nst;
+    int max_req, max_pages, max_ctx, zero_block;
+    float scale_log2, decay;
+};
+
+__device__ __forceinline__ int pages_of(int tokens) { return tokens <= 0 ? 0 : (tokens - 1) / kPage + 1; }
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void mul2(float &a, float &b, float c, float d) {
+    asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n mul.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
+        : "+f"(a), "+f"(b)
+        : "f"(c), "f"(d));
+}
+__device__ __forceinline__ void add2(float &a, float &b, float c, float d) {
+    asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
+        : "+f"(a), "+f"(b)
+        : "f"(c), "f"(d));
+}
+// a = a c + e, b = b d + f
+__device__ __forceinline__ void fma2(float &a, float &b, float c, float d, float e, float f) {
+    asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n mov.b64 z, {%4, %5};\n"
+        " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}\n"
+        : "+f"(a), "+f"(b)
+        : "f"(c), "f"(d), "f"(e), "f"(f));
+}
+// Two BF16 values times 2^k (at most 448, or NaN) as the sums of two e4m3 codes each: F16
+// holds the products' eight bits down to 2^-17, the codes' smallest step is 2^-9.
+__device__ __forceinline__ void two_codes(uint32_t w, uint32_t pow2, uint16_t &p, uint16_t &r) {
+    uint32_t x, h;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(w), "r"(pow2));
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(x) : "f"(__uint_as_float(x & 0xffff0000u)), "f"(__uint_as_float(x << 16)));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(p) : "r"(x));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(p));
+    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(h));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
+}
+__device__ __forceinline__ void four_codes(uint32_t w0, uint32_t w1, uint32_t pow2, uint32_t &p, uint32_t &r) {
+    uint16_t p0, p1, r0, r1;
+    two_codes(w0, pow2, p0, r0);
+    two_codes(w1, pow2, p1, r1);
+    asm("mov.b32 %0, {%1, %2};" : "=r"(p) : "h"(p0), "h"(p1));
+    asm("mov.b32 %0, {%1, %2};" : "=r"(r) : "h"(r0), "h"(r1));
+}
+__device__ __forceinline__ void st_cluster_f1(uint32_t a, float x) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(x) : "memory");
+}
+
+template <bool FP8>
+__global__ void __launch_bounds__(WT, 1)
+weight_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q, const WeightParams p) {
+    using C = WCfg<FP8>;
+    extern __shared__ uint8_t smem_raw[];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int rank = static_cast<int>(hs::cluster_ctarank());
+    const int unit = blockIdx.x >> 1, g = unit % p.groups, part = unit / p.groups;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t raw = hs::smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;  // queries, ring, then the small things
+    const uint32_t ring = base + NCH * (uint32_t)(p.N / 2) * 128u, head = ring + (uint32_t)(p.nst * C::STAGE);
+    uint8_t *small = smem_raw + (head - raw);
+    volatile int32_t *misc = reinterpret_cast<volatile int32_t *>(small + C::OFF_MISC);
+    auto bar = [&](int i) { return head + C::OFF_BAR + 8u * (uint32_t)i; };
+    const uint32_t lead0 = cluster_address(head + C::OFF_BAR, 0);
+    auto lead = [&](int i) { return lead0 + 8u * (uint32_t)i; };
+    const uint32_t nst = (uint32_t)p.nst;
+    auto fail = [&]() {
+        misc[1] = 1;
+        atomicOr(p.err, HS_DEVERR_TIMEOUT);
+    };
+    uint32_t cols = 32;
+    while ((int)cols < 2 * p.N) cols <<= 1;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::NBAR; ++i) {
+            uint32_t n = 1;
+            if (i == C::B_QREADY || i == C::B_DFREE || i == C::B_DFREE + 1 || i == C::B_TAB) n = 2 * NEW;  // both CTAs'
+            mbar_init(bar(i), n);
+        }
+        misc[1] = 0;
+        fence_mbar_init();
+        fence_proxy_async();
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_q);
+    }
+    if (warp == 1) tmem_alloc2(head + C::OFF_MISC, cols);
+
+    // The requests' tiles laid end to end: how many, and where this pair's range begins.
+    // Every warp finds that, and walks the range, for itself.
+    uint32_t bad = 0;
+    auto request = [&](int b, int &r) {  // context length of request b of the list
+        r = b < p.B ? p.req[b] : -1;
+        if (r < 0 || r >= p.max_req) {
+            if (b < p.B) bad |= HS_DEVERR_BAD_REQUEST;
+            return 0;
+        }
+        const int len = p.ctx[r];
+        if (len > p.max_ctx) bad |= HS_DEVERR_INDEX_RANGE;
+        return hs::context_within(len, p.max_ctx);
+    };
+    auto tiles_of = [](int pages) { return (pages + TP - 1) / TP; };
+    struct Walk {
+        int b, r, L, lo, n;  // request, its cache index and context, first tile, tiles (0: no more)
+        int left;            // tiles of the range behind these
+    };
+    Walk begin{};
+    int total = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+        int r;
+        const int n = tiles_of(pages_of(request(b0 + lane, r)));
+        total += __reduce_add_sync(0xffffffffu, n);
+    }
+    const int even = total / p.parts, odd = total - even * p.parts;
+    const int f0 = even * part + min(part, odd), f1 = f0 + even + (part < odd ? 1 : 0);
+    auto take = [&](Walk &w) {
+        w.n = min(w.left, tiles_of(pages_of(w.L)) - w.lo);
+        w.left -= w.n;
+    };
+    if (f1 > f0) {
+        int at = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            int r;
+            const int L = request(b0 + lane, r), n = tiles_of(pages_of(L));
+            int incl = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += x;
+            }
+            const uint32_t past = __ballot_sync(0xffffffffu, at + incl > f0);
+            if (past) {
+                const int l = __ffs(past) - 1;
+                begin.b = b0 + l;
+                begin.r = __shfl_sync(0xffffffffu, r, l);
+                begin.L = __shfl_sync(0xffffffffu, L, l);
+                begin.lo = f0 - at - __shfl_sync(0xffffffffu, incl - n, l);
+                begin.left = f1 - f0;
+                take(begin);
+                break;
+            }
+            at += __shfl_sync(0xffffffffu, incl, 31);
+        }
+    }
+    auto next = [&](Walk &w) {
+        w.n = w.lo = 0;
+        if (w.left <= 0) return;
+        for (int b0 = w.b + 1; b0 < p.B; b0 += 32) {
+            int r;
+            const int L = request(b0 + lane, r);
+            const uint32_t some = __ballot_sync(0xffffffffu, L > 0);
+            if (some) {
+                const int l = __ffs(some) - 1;
+                w.b = b0 + l;
+                w.r = __shfl_sync(0xffffffffu, r, l);
+                w.L = __shfl_sync(0xffffffffu, L, l);
+                take(w);
+                return;
+            }
+        }
+    };
+    const uint32_t tiles = (uint32_t)(f1 - f0);  // that this pair multiplies
+    bad = __reduce_or_sync(0xffffffffu, bad);
+    if (bad && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.err, bad);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_relaxed();
+    tc_fence_after();
+    const uint32_t tmem = static_cast<uint32_t>(misc[0]);
+    const uint32_t qch = (uint32_t)(p.N / 2) * 128u;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        Walk w = begin;
+        uint32_t u = 0, seg = 0, qn = 0;
+        bool ok = true;
+        while (w.n > 0 && ok) {
+            Walk nx = w;
+            next(nx);
+            const int2 *table = p.table + (size_t)w.r * p.max_pages;
+            const int pages = pages_of(w.L);
+            if (lane == 0) {
+                // the MMAs of the request before are done with the queries' place
+                if (seg > 0) ok = mbar_wait_inline(bar(C::B_QFREE), (seg - 1) & 1u);
+                if (ok) {
+                    mbar_expect_tx(bar(C::B_QFULL), NCH * qch);
+                    for (int c = 0; c < NCH; ++c)
+                        tma_load_3d(base + c * qch, &tm_q, 64 * c, g * MAXN + rank * (p.N / 2), w.b, bar(C::B_QFULL));
+                    ++qn;
+                }
+            }
+            int blk = 0;
+            for (int i = 0; i < w.n; ++i) {
+                // blocks of this CTA's pages, 16 tiles ahead
+                if (i % 16 == 0) {
+                    const int page = TP * (w.lo + i + (lane >> 1)) + 2 * rank + (lane & 1);
+                    const int x = page < pages ? table[page].x : -1;
+                    blk = x >= 0 ? x : p.zero_block;
+                }
+                const int row0 = __shfl_sync(0xffffffffu, blk, 2 * (i % 16)) * kPage;
+                const int row1 = __shfl_sync(0xffffffffu, blk, 2 * (i % 16) + 1) * kPage;
+                if (lane == 0) {
+                    for (int c = 0; c < NCH && ok; ++c, ++u) {
+                        const uint32_t s = u % nst;
+                        ok = mbar_wait_inline(bar(C::B_FREE + (int)s), ((u / nst) & 1u) ^ 1u);
+                        if (!ok) break;
+                        // both CTAs' bytes complete on CTA 0's barrier
+                        if (rank == 0) mbar_expect_tx(bar(C::B_FULL + (int)s), 2 * C::STAGE);
+                        tma_load_pair(ring + s * C::STAGE, &tm_k, 0, row0, c, lead(C::B_FULL + (int)s));
+                        tma_load_pair(ring + s * C::STAGE + C::STAGE / 2, &tm_k, 0, row1, c, lead(C::B_FULL + (int)s));
+                    }
+                }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
+            }
+            w = nx;
+            ++seg;
+        }
+        if (lane == 0) {
+            // the copies begun have landed before the CTA may end
+            if (qn > 0) mbar_wait_inline(bar(C::B_QFULL), (qn - 1) & 1u);
+            if (!ok) {
+                fail();
+                for (uint32_t k = 0, v = u; rank == 0 && k < nst && v > 0; ++k) {
+                    --v;
+                    mbar_wait_inline(bar(C::B_FULL + (int)(v % nst)), (v / nst) & 1u);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer (CTA 0)
+        if (rank == 0 && tiles > 0) {
+            const uint32_t idesc = idesc_f16(FP8 ? 0u : 1u, 0, 256, p.N);
+            const uint64_t d0 = desc_sw128(base, 16, 1024);
+            const uint32_t hi = (uint32_t)(d0 >> 32), lo = (uint32_t)d0;
+            const uint32_t khi = FP8 ? (uint32_t)(desc_sw64(base, 16, 512) >> 32) : hi;
+            const uint32_t leader = elect_one();
+            bool ok = true;
+            uint32_t u = 0, i = 0, seg = 0;
+            const uint32_t last_u = tiles * NCH;
+            for (Walk w = begin; w.n > 0 && ok; ++seg) {
+                ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_QREADY), seg & 1u));
+                if (!ok) break;
+                for (int j = 0; j < w.n && ok; ++j, ++i) {
+                    if (i >= 2)
+                        ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_DFREE + (int)(i & 1)), ((i >> 1) & 1u) ^ 1u));
+                    if (!ok) break;
+                    const uint32_t d = tmem + (i & 1) * (uint32_t)p.N;
+                    for (int c = 0; c < NCH && ok; ++c, ++u) {
+                        const uint32_t s = u % nst;
+                        ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_FULL + (int)s), (u / nst) & 1u));
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (leader) {
+                            const uint32_t a = lo + ((ring - base + s * C::STAGE) >> 4), q = lo + ((c * qch) >> 4);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                if (FP8)  // both codes of the queries with the same 32 codes of the keys
+                                    mma2_ss_e4m3(d, a + 2 * (e & 1), khi, q + 2 * e, hi, idesc, (c | e) != 0);
+                                else
+                                    mma2_ss(d, a + 2 * e, q + 2 * e, hi, idesc, (c | e) != 0);
+                            }
+                            if (u + nst < last_u) commit_both(bar(C::B_FREE + (int)s));
+                        }
+                        __syncwarp();
+                    }
+                    if (!ok) break;
+                    if (leader) commit_both(bar(C::B_DFULL + (int)(i & 1)));
+                    __syncwarp();
+                }
+                next(w);
+                if (ok && w.n > 0 && leader) commit_both(bar(C::B_QFREE));
+                __syncwarp();
+            }
+            if (!ok && lane == 0) fail();
+            if (leader) {
+                asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                                 bar(C::B_DRAIN))
+                             : "memory");
+                mbar_wait_inline(bar(C::B_DRAIN), 0);
+            }
+            __syncwarp();
+        }
+    } else {
+        // ------------------------------------------------------------ the sums
+        const int wq = warp & 3, hf = (warp - 2) >> 2, tid = (warp - 2) * 32 + lane;
+        const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
+        const int c_lo = hf * (p.N / 2), c_hi = min(c_lo + p.N / 2, p.M - g * MAXN);
+        volatile float *psum = reinterpret_cast<volatile float *>(small + C::OFF_PS);
+        volatile uint32_t *dead = reinterpret_cast<volatile uint32_t *>(small + C::OFF_DEAD);
+        const bool writer = hf == 0 && (wq & 1) == 0 && lane == 0;  // of one page of the tile
+        bool ok = true;
+        uint32_t i = 0, seg = 0;
+        for (Walk w = begin; w.n > 0; next(w), ++seg) {
+            // columns' terms; all warps are done with those of the request before
+            {
+                const int m = g * MAXN + tid;
+                float v = tid < p.N && m < p.M ? p.lse[(size_t)w.b * p.M + m] : 0.f;
+                const bool fin = fabsf(v) < INFINITY;
+                // columns behind the last row too: a key that is not finite makes NaN of them
+                const uint32_t out = __ballot_sync(0xffffffffu, !fin || m >= p.M);
+                if (seg > 0) named_bar_sync(1, 32 * NEW);
+                if (tid < p.N) st_shared_f1(head + C::OFF_B + 4 * tid, fin && m < p.M ? -v * 1.4426950408889634f : -INFINITY);
+                if (lane == 0) dead[warp - 2] = out;
+            }
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_QFULL), seg & 1u));
+            const uint32_t tab = head + C::OFF_A + (seg & 1u) * MAXN * 4;
+            if (FP8) {
+                // thread = (row of this CTA's half, half of its chunks)
+                const int row = tid & 127, half = tid >> 7;
+                const bool in = row < p.N / 2;
+                auto q_at = [&](int c) { return base + c * qch + row * 128; };
+                uint32_t m = 0;  // the row's largest magnitude; NaN if there is one
+                if (ok && in) {
+#pragma unroll 1
+                    for (int c = half; c < NCH; c += 2)
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const uint4 v = ld_shared_v4(q_at(c) + ((k ^ (row & 7)) << 4));
+                            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(x[e] & 0x7fff7fffu));
+                        }
+                }
+                // bits of magnitudes are in their order, infinities and NaN above all
+                st_shared_b32(head + C::OFF_X + 4 * tid, max(m & 0xffffu, m >> 16));
+                named_bar_sync(1, 32 * NEW);
+                const uint32_t top = max(ld_shared_b32(head + C::OFF_X + 4 * row), ld_shared_b32(head + C::OFF_X + 4 * (row + 128)));
+                // times 2^k it lies in (224, 448]; a row that is not finite becomes NaN
+                const int k2 = min(135 - (int)(top >> 7) - ((top & 0x7fu) > 0x60u), 126);
+                const uint32_t pow2 = top >= 0x7f80u ? 0x7fc07fc0u : (uint32_t)(k2 + 127) * 0x00800080u;
+                if (ok && in) {
+#pragma unroll 1
+                    for (int c = half; c < NCH; c += 2) {
+                        uint32_t r[16];  // first codes go where values have been read
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint4 x = ld_shared_v4(q_at(c) + (((2 * k) ^ (row & 7)) << 4));
+                            const uint4 y = ld_shared_v4(q_at(c) + (((2 * k + 1) ^ (row & 7)) << 4));
+                            uint32_t z[4];
+                            four_codes(x.x, x.y, pow2, z[0], r[4 * k]);
+                            four_codes(x.z, x.w, pow2, z[1], r[4 * k + 1]);
+                            four_codes(y.x, y.y, pow2, z[2], r[4 * k + 2]);
+                            four_codes(y.z, y.w, pow2, z[3], r[4 * k + 3]);
+                            st_shared_v4(q_at(c) + ((k ^ (row & 7)) << 4), z[0], z[1], z[2], z[3]);
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            st_shared_v4(q_at(c) + (((4 + k) ^ (row & 7)) << 4), r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+                    }
+                }
+                if (in && half == 0) {
+                    const float a = p.scale_log2 * __uint_as_float((uint32_t)(127 - k2) << 23);
+                    const uint32_t at = tab + 4 * (uint32_t)(rank * (p.N / 2) + row);
+                    st_shared_f1(at, a);
+                    st_cluster_f1(cluster_address(at, (uint32_t)rank ^ 1u), a);
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive_remote(cluster_address(bar(C::B_TAB), 0));
+                    mbar_arrive_remote(cluster_address(bar(C::B_TAB), 1));
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive_peer(lead(C::B_QREADY));
+            if (FP8 && ok) ok = __all_sync(0xffffffffu, mbar_wait_cluster(bar(C::B_TAB), seg & 1u));
+            named_bar_sync(1, 32 * NEW);  // the columns' terms are there
+
+            const int pages = pages_of(w.L), draft = w.L - p.T;
+            const int2 *table = p.table + (size_t)w.r * p.max_pages;
+            auto block_at = [&](int tile) {
+                const int page = TP * tile + 2 * rank + (wq >> 1);
+                return page < pages ? table[page].x : -1;
+            };
+            int blk = block_at(w.lo);
+            for (int j = 0; j < w.n; ++j, ++i) {
+                const int page = TP * (w.lo + j) + 2 * rank + (wq >> 1);
+                const int pos = page * kPage + 32 * (wq & 1) + lane;
+                const bool live = blk >= 0;  // the same in a warp
+                float ks = p.scale_log2;
+                if (FP8 && live) ks = p.scales[(size_t)blk * kPage + 32 * (wq & 1) + lane];
+                const int blk_next = j + 1 < w.n ? block_at(w.lo + j + 1) : -1;
+                float before = 0.f;
+                if (writer && page < pages && p.groups == 1 && p.prior && p.decay != 0.f)
+                    before = p.decay * p.prior[(size_t)w.r * p.max_pages + page];
+                const bool all = (pos | 31) < draft;  // every query token sees these keys
+                if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_DFULL + (int)(i & 1)), (i >> 1) & 1u));
+                float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+                if (ok && live) {
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c0 = c_lo; c0 < c_hi; c0 += 32) {
+                        uint32_t d[32];
+                        HS_TMEM_LD32(tmem + lane_off + (i & 1) * (uint32_t)p.N + c0, d);
+                        HS_TMEM_WAIT_LD32(d);
+                        const uint32_t gone = dead[c0 >> 5];
+                        if (all && gone == 0) {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) {
+                                const float4 b = ld_shared_f4(head + C::OFF_B + 4 * (c0 + e));
+                                float a0 = ks, a1 = ks, a2 = ks, a3 = ks;
+                                if (FP8) {  // the two scales first: their product with a sum may be the only one in range
+                                    const float4 a = ld_shared_f4(tab + 4 * (c0 + e));
+                                    mul2(a0, a1, a.x, a.y);
+                                    mul2(a2, a3, a.z, a.w);
+                                }
+                                float x0 = __uint_as_float(d[e]), x1 = __uint_as_float(d[e + 1]);
+                                float x2 = __uint_as_float(d[e + 2]), x3 = __uint_as_float(d[e + 3]);
+                                fma2(x0, x1, a0, a1, b.x, b.y);
+                                fma2(x2, x3, a2, a3, b.z, b.w);
+                                add2(s0, s1, ex2(x0), ex2(x1));
+                                add2(s2, s3, ex2(x2), ex2(x3));
+                            }
+                        } else {
+                            int m = g * MAXN + c0, t = m / p.H, h = m - t * p.H;
+                            auto sees = [&](int tt) {
+                                if (tt >= p.T || pos >= w.L) return false;
+                                if (!p.tree) return pos <= draft + tt;
+                                const int node = pos - draft;
+                                return node < 0 || ((p.tree[(size_t)w.b * p.T + tt] >> node) & 1) != 0;
+                            };
+                            bool seen = sees(t);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const float b = ld_shared_f1(head + C::OFF_B + 4 * (c0 + e));
+                                const float a = FP8 ? ks * ld_shared_f1(tab + 4 * (c0 + e)) : ks;
+                                const float y = ex2(fmaf(__uint_as_float(d[e]), a, b));
+                                s0 += seen && !((gone >> e) & 1u) ? y : 0.f;
+                                if (++h == p.H) {
+                                    h = 0;
+                                    seen = sees(++t);
+                                }
+                            }
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0 && i + 2 < tiles) mbar_arrive_peer(lead(C::B_DFREE + (int)(i & 1)));
+                float sum = (s0 + s1) + (s2 + s3);
+#pragma unroll
+                for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                const int at = (int)(i & 1) * NEW;
+                if (lane == 0) psum[at + 4 * hf + wq] = sum;
+                named_bar_sync(1, 32 * NEW);
+                if (writer && page < pages && ok) {
+                    const float got = (psum[at + wq] + psum[at + wq + 1]) + (psum[at + 4 + wq] + psum[at + 5 + wq]);
+                    if (p.groups == 1)
+                        p.weights[(size_t)w.r * p.max_pages + page] = before + got;
+                    else
+                        p.part[((size_t)g * p.B + w.b) * p.max_pages + page] = got;
+                }
+                blk = blk_next;
+            }
+        }
+        if (!ok && lane == 0) fail();
+    }
+    tc_fence_before();
+    __syncthreads();
+    // No CTA leaves while the other's MMAs or arrives may reach it: every arrive on the
+    // other's barriers is one that it waits for, so none is on its way any more.
+    cluster_arrive_last(misc[1] != 0);
+    cluster_wait();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc2(tmem, cols);
+}
+
+// The groups' sums of each page, in order. One thread per page.
+__global__ void __launch_bounds__(256)
+weight_join_kernel(const float *part, const int32_t *req, const int32_t *ctx, const float *prior, float *weights, int B,
+                   int groups, int max_req, int max_pages, int max_ctx, float decay) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const int b = blockIdx.y, r = req[b];
+    if (r < 0 || r >= max_req) return;
+    const int pages = pages_of(hs::context_within(ctx[r], max_ctx));
+    for (int page = blockIdx.x * 256 + threadIdx.x; page < pages; page += gridDim.x * 256) {
+        const size_t at = (size_t)r * max_pages + page;
+        float sum = 0.f;
+        for (int g = 0; g < groups; ++g) sum += part[((size_t)g * B + b) * max_pages + page];
+        weights[at] = (prior && decay != 0.f ? decay * prior[at] : 0.f) + sum;
+    }
+}
+
+bool takes(int64_t B, int64_t T, int64_t H) {
+    return B >= 0 && B <= 65535 && T >= 1 && T <= 32767 && H >= 1 && T * H <= (1 << 22);
+}
+int groups_of(int64_t M) { return (int)((M + MAXN - 1) / MAXN); }
+
+// Parts that the key tiles of all requests are cut into, each worked through by one pair of
+// CTAs per group: the count that a model of the launch makes shortest. A tile takes a
+// pair us_tile, its start and the queries 5 us.
+int parts_of(int64_t groups, int64_t tiles, double us_tile) {
+    const int64_t pairs = sm_count() / 2 > 0 ? sm_count() / 2 : 1;
+    double best = 1e300;
+    int64_t parts = 1;
+    for (int64_t w = 1; w <= 8; ++w) {
+        int64_t n = w * pairs / groups;
+        n = n < 1 ? 1 : (n > tiles ? tiles : n);
+        const double waves = (double)((groups * n + pairs - 1) / pairs);
+        const double t = waves * ((double)((tiles + n - 1) / n) * us_tile + 5.0);
+        if (t < best * 0.98) {
+            best = t;
+            parts = n;
+        }
+    }
+    return (int)parts;
+}
+
+// [rows][9 chunks][64] seen as (element, row, chunk), boxes of one page's chunk
+bool make_key_map(CUtensorMap *m, bool fp8, const void *rows, uint64_t n_rows) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t rb = fp8 ? kDim : 2 * kDim;
+    cuuint64_t dims[3] = {64, n_rows, 9};
+    cuuint64_t strides[2] = {rb, rb / 9};
+    cuuint32_t box[3] = {64, (cuuint32_t)kPage, 1};
+    cuuint32_t es[3] = {1, 1, 1};
+    return fn(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(rows),
+              dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              fp8 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool FP8>
+hs_status launch_weights(int dev, cudaStream_t s, const CUtensorMap &tk, const CUtensorMap &tq, const WeightParams &p) {
+    static std::atomic<int> state[64];
+    if (dev < 0 || dev >= 64) return HS_ERR_UNSUPPORTED;
+    if (state[dev].load(std::memory_order_acquire) != 1) {
+        HS_CUDA_TRY(cudaFuncSetAttribute(weight_kernel<FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MOST));
+        state[dev].store(1, std::memory_order_release);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * p.groups * p.parts), 1, 1);
+    cfg.blockDim = dim3(WT, 1, 1);
+    cfg.dynamicSmemBytes = (size_t)(1024 + NCH * (p.N / 2) * 128 + p.nst * WCfg<FP8>::STAGE + WCfg<FP8>::HEAD);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, weight_kernel<FP8>, tk, tq, p) == cudaSuccess ? HS_OK : HS_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" size_t hs_weights_workspace_bytes(hs_pool_t pool, int32_t B, int32_t T, int32_t H) {
+    if (!pool || B < 1 || !takes(B, T, H)) return 0;
+    const int groups = groups_of((int64_t)T * H);
+    return groups == 1 ? 0 : ((size_t)groups * B * pool->max_pages * 4 + 255) & ~(size_t)255;
+}
+
+extern "C" hs_status hs_page_weights(hs_pool_t pool, int32_t B, int32_t T, int32_t H, const void *d_q,
+                                     const float *d_lse, const int32_t *d_req_ids, const uint64_t *d_tree,
+                                     float sm_scale, float decay, const float *d_prior, float *d_weights,
+                                     void *d_workspace, size_t ws_bytes, void *stream) {
+    if (!pool || !takes(B, T, H) || (d_tree && T > 64)) return HS_ERR_INVALID_ARG;
+    if (B == 0) return HS_OK;
+    if (!d_q || !d_lse || !d_req_ids || !d_weights || ((uintptr_t)d_q & 15u)) return HS_ERR_INVALID_ARG;
+    const size_t need = hs_weights_workspace_bytes(pool, B, T, H);
+    if (need && (!d_workspace || ws_bytes < need || ((uintptr_t)d_workspace & 255u))) return HS_ERR_INVALID_ARG;
+    int dev = -1;
+    HS_CUDA_TRY(cudaGetDevice(&dev));
+    if (dev != pool->device) return HS_ERR_INVALID_ARG;
+    const bool fp8 = pool->cfg.dtype == HS_FP8_E4M3_ROWSCALE;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    WeightParams p{};
+    p.req = d_req_ids;
+    p.ctx = pool->d_ctx;
+    p.table = reinterpret_cast<const int2 *>(pool->d_page);
+    p.tree = d_tree;
+    p.lse = d_lse;
+    p.scales = pool->d_scales;
+    p.prior = d_prior;
+    p.weights = d_weights;
+    p.part = need ? static_cast<float *>(d_workspace) : nullptr;
+    p.err = pool->d_err;
+    p.B = B;
+    p.T = T;
+    p.H = H;
+    p.M = T * H;
+    p.groups = groups_of(p.M);
+    p.N = p.M < MAXN ? (p.M + 63) & ~63 : MAXN;
+    p.nst = fp8 ? WCfg<true>::stages(p.N) : WCfg<false>::stages(p.N);
+    const int64_t tiles = (int64_t)B * ((pool->max_pages + TP - 1) / TP);
+    // the keys' bytes at the card's rate, or the products
+    const double us_mma = 2.5 * p.N / 256, us_bytes = (fp8 ? 148e3 : 295e3) / 85e3;
+    p.parts = parts_of(p.groups, tiles, us_mma > us_bytes ? us_mma : us_bytes);
+    if (2ll * p.groups * p.parts > INT32_MAX || tiles > INT32_MAX / 32) return HS_ERR_INVALID_ARG;
+    p.max_req = pool->cfg.max_requests;
+    p.max_pages = pool->max_pages;
+    p.max_ctx = pool->cfg.max_ctx;
+    p.zero_block = (int)pool->cfg.n_gpu_blocks;
+    p.scale_log2 = sm_scale * 1.4426950408889634f;
+    p.decay = decay;
+    CUtensorMap tk, tq;
+    if (!make_key_map(&tk, fp8, pool->d_rows, (uint64_t)(pool->cfg.n_gpu_blocks + 1) * kPage) ||
+        !make_map(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d_q, kDim, (uint64_t)p.M, B, 2 * kDim, 64, p.N / 2,
+                  CU_TENSOR_MAP_SWIZZLE_128B))
+        return HS_ERR_CUDA;
+    const hs_status st = fp8 ? launch_weights<true>(dev, s, tk, tq, p) : launch_weights<false>(dev, s, tk, tq, p);
+    if (st != HS_OK || p.groups == 1) return st;
+    cudaLaunchConfig_t cfg = {};
+    const int64_t blocks = ((int64_t)pool->max_pages + 255) / 256;
+    cfg.gridDim = dim3((unsigned)(blocks < 1024 ? blocks : 1024), (unsigned)B, 1);
+    cfg.blockDim = dim3(256, 1, 1);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, weight_join_kernel, (const float *)p.part, d_req_ids, (const int32_t *)pool->d_ctx,
+                              d_prior, d_weights, (int)B, p.groups, p.max_req, p.max_pages, p.max_ctx, decay) == cudaSuccess
+               ? HS_OK
+               : HS_ERR_CUDA;
+}
