@@ -67,7 +67,7 @@ def clean(x):
 
 
 def fixed(x):
-    return math.floor(Fraction(clean(x)) * 2 ** 62)
+    return math.floor(Fraction(clean(x)) * 2 ** 58)
 
 
 def draw(values, u):

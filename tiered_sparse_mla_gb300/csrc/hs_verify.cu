@@ -13,10 +13,12 @@
 // of 128,000 values, 65.5 MB, whose bytes are the bound, after two dependent loads that
 // say which row it is.
 //
-// Sums are integers: a probability is a multiple of 2^-62 in 64 bits (floats from 2^-38 on
-// are such multiples exactly), so that their order does not matter, and no sum differs
-// between a search's two steps. They saturate near 4, which the sums of
-// probabilities do not reach.
+// A search by sums has to add the same way each time. Here sums are integers of 2^-58: eight
+// values of a lane are cut into digits of f32, multiples of 2^-20 (to which adding and
+// taking away 12 rounds a value in [0, 1]), then of 2^-41, whose sums of eight are exact, and a
+// rest below 2^-42, whose sum is off by less than 2^-60. (Integer shifts, at half
+// the rate of additions and twice as many, made 64 requests of 128,000 values 22.7 us.)
+// Integer sums saturate at 64, which those of probabilities do not reach.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -27,10 +29,11 @@
 
 namespace {
 
-constexpr int VT = 512;          // threads per CTA
+constexpr int VT = 256;          // threads per CTA
 constexpr int NW = VT / 32;
-constexpr int BATCH = 256;       // values that a warp adds up at a time
-constexpr int MAXB = 512;        // sums per CTA: longer slices take several batches for each
+constexpr int BATCH = 256;       // values that a warp takes at a time
+constexpr int UNITS = 16;        // of a warp's run of batches: each lane's sum of each is kept
+constexpr int AHEAD = 16384;     // values that a warp asks into L2 at the start
 constexpr int MAXT = 64;
 constexpr int MAXG = 8;          // CTAs per request
 
@@ -42,7 +45,7 @@ struct VerifyParams {
     int32_t *index, *count, *next;
     uint32_t *err;
     int64_t ld, draft_ld;
-    int T, V, per;  // per: batches for each sum
+    int T, V, per;  // per: batches in a unit
 };
 
 __device__ __forceinline__ uint64_t add_sat(uint64_t a, uint64_t b) {
@@ -53,16 +56,60 @@ __device__ __forceinline__ uint64_t shuffle64(uint64_t x, int src) {
     return (uint64_t)__shfl_sync(0xffffffffu, (unsigned long long)x, src);
 }
 
+// The sum over the lanes up to this one.
+__device__ __forceinline__ uint64_t sum_up(uint64_t x, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t y = (uint64_t)__shfl_up_sync(0xffffffffu, (unsigned long long)x, o);
+        if (lane >= o) x = add_sat(x, y);
+    }
+    return x;
+}
+
 // A probability's bits: NaN and negative ones are 0, ones above 1 are 1.
 __device__ __forceinline__ uint32_t clean(uint32_t b) {
     return b > 0x7f800000u ? 0u : min(b, 0x3f800000u);
 }
-// In units of 2^-62, the rest cut off.
+// In [0, 1]; NaN is 0.
+__device__ __forceinline__ float within(float x) {
+    float y;
+    asm("add.sat.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void add2(float &a, float &b, float c, float d) {
+    asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
+        : "+f"(a), "+f"(b)
+        : "f"(c), "f"(d));
+}
+// Two values' digits: the multiples of 2^-20 and 2^-41, and the rest.
+struct Digits {
+    float h0, h1, m0, m1, l0, l1;
+};
+__device__ __forceinline__ Digits digits_of(float x0, float x1) {
+    constexpr float C1 = 12.f, C2 = 0x1.8p-18f;
+    Digits d;
+    d.h0 = x0, d.h1 = x1;
+    add2(d.h0, d.h1, C1, C1);
+    add2(d.h0, d.h1, -C1, -C1);
+    add2(x0, x1, -d.h0, -d.h1);
+    d.m0 = x0, d.m1 = x1;
+    add2(d.m0, d.m1, C2, C2);
+    add2(d.m0, d.m1, -C2, -C2);
+    d.l0 = x0, d.l1 = x1;
+    add2(d.l0, d.l1, -d.m0, -d.m1);
+    return d;
+}
+// In units of 2^-58, the rest cut off.
 __device__ __forceinline__ uint64_t fixed(uint32_t b) {
-    const uint32_t top = ((b & 0x7fffffu) | 0x800000u) << 7;  // 2^62 for 1.0, with 32 zeros behind it
+    const uint32_t top = ((b & 0x7fffffu) | 0x800000u) << 3;  // 2^58 for 1.0, with 32 zeros behind it
     uint64_t r;
     asm("shr.u64 %0, %1, %2;" : "=l"(r) : "l"((uint64_t)top << 32), "r"(127u - (b >> 23)));  // beyond 63: 0
     return r;
+}
+// A draft's test, u q < p, on u q's two 32-bit words (products below 2^-100 may count as zero).
+__device__ __forceinline__ bool below(float u, float q, float p) {
+    const float hi = __fmul_rn(u, q), lo = __fmaf_rn(u, q, -hi);
+    return hi < p || (hi == p && lo < 0.f);
 }
 template <typename P>
 __device__ __forceinline__ uint32_t bits_at(const void *row, int64_t i);
@@ -87,11 +134,12 @@ __device__ __forceinline__ uint64_t part_of(float u, uint64_t total) {
 // Cluster of gridDim.x CTAs per request (blockIdx.y): each finds the accepted path by
 // itself, adds up its slice of the row, and the one that holds the border draws.
 template <typename P>
-__global__ void __launch_bounds__(VT)
+__global__ void __launch_bounds__(VT, 4)
 verify_kernel(const VerifyParams p) {
     hs::tc::grid_dep_wait();
     hs::tc::grid_dep_launch();
-    __shared__ uint64_t sums[MAXB], totals[MAXG];
+    __shared__ uint64_t sums[NW][UNITS][33];   // of a warp's units, by lane
+    __shared__ uint64_t totals[MAXG * NW], s_path;  // of the cluster's warps
     __shared__ int32_t gone[MAXT];     // refused children's tokens
     __shared__ int32_t s_row, s_minus, s_gone;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -135,9 +183,8 @@ verify_kernel(const VerifyParams p) {
         uint64_t path = 1;
         int end = 0, minus = 0, ngone = 0;
         if (p.draft) {  // a chain: up to the first that has no token or is refused
-            // u q has 48 bits: exact in 64
-            const bool s0 = tok[0] >= 0 && (double)u[0] * (double)qx[0] < (double)px[0];
-            const bool s1 = tok[1] >= 0 && (double)u[1] * (double)qx[1] < (double)px[1];
+            const bool s0 = tok[0] >= 0 && below(u[0], qx[0], px[0]);
+            const bool s1 = tok[1] >= 0 && below(u[1], qx[1], px[1]);
             const uint64_t stop = both(lane > 0 && !s0, !s1);  // nodes from T on have no token
             const uint64_t there = both(tok[0] >= 0, tok[1] >= 0);
             const int n = stop ? __ffsll((long long)stop) - 1 : MAXT;
@@ -145,115 +192,177 @@ verify_kernel(const VerifyParams p) {
             end = n - 1;
             minus = n < 64 && ((there >> n) & 1);
         } else {
-            for (int node = 0; node >= 0;) {
-                uint64_t kids = both(par[0] == node && tok[0] >= 0, par[1] == node && tok[1] >= 0);
-                double left = 1.0;
-                int go = -1;
-                ngone = 0;
-                while (kids && go < 0) {
-                    const int c = __ffsll((long long)kids) - 1;
-                    kids &= kids - 1;
-                    const int x = __shfl_sync(0xffffffffu, c < 32 ? tok[0] : tok[1], c & 31);
-                    float pc = __shfl_sync(0xffffffffu, c < 32 ? px[0] : px[1], c & 31);
-                    const float uc = __shfl_sync(0xffffffffu, c < 32 ? u[0] : u[1], c & 31);
-                    // a token that an earlier child had is gone already
-                    const uint64_t same = both(par[0] == node && tok[0] == x, par[1] == node && tok[1] == x);
-                    if (same & ((1ull << c) - 1)) pc = 0.f;
-                    if ((double)uc * left < (double)pc) {
-                        go = c;
-                    } else {
-                        left = fmax(left - (double)pc, 0.0);
-                        if (lane == 0) gone[ngone] = x;
-                        ++ngone;
-                    }
+            // What each node is held against, all nodes at once: 1 less what its earlier
+            // brothers had, each token once.
+            uint64_t mine[2] = {fixed(__float_as_uint(px[0])), fixed(__float_as_uint(px[1]))};
+            uint64_t left[2] = {1ull << 58, 1ull << 58};
+            if (p.tree && T <= 32) {
+                // brothers by one vote, and as many rounds as a node has earlier ones
+                const uint32_t lower = (1u << lane) - 1u, with = __ballot_sync(0xffffffffu, tok[0] >= 0);
+                uint32_t same = __match_any_sync(0xffffffffu, par[0]) & with & lower;
+                const uint32_t twin = __match_any_sync(0xffffffffu, (unsigned long long)(uint32_t)par[0] << 32 | (uint32_t)tok[0]) & lower;
+                if (tok[0] < 0) same = 0;
+                if (tok[0] >= 0 && twin) {  // gone already
+                    mine[0] = 0;
+                    px[0] = 0.f;
                 }
-                end = node;
-                if (go >= 0) path |= 1ull << go;
-                node = go;
+                while (__any_sync(0xffffffffu, same != 0)) {
+                    const uint64_t mj = shuffle64(mine[0], same ? __ffs(same) - 1 : 0);
+                    if (same) left[0] -= min(left[0], mj);
+                    same &= same - 1;
+                }
+            } else if (p.tree) {
+                auto of = [&](int x0, int x1, int j) { return __shfl_sync(0xffffffffu, j < 32 ? x0 : x1, j & 31); };
+#pragma unroll 1
+                for (int j = 1; j < T; ++j) {
+                    const int pj = of(par[0], par[1], j), tj = of(tok[0], tok[1], j);
+                    if (tj < 0) continue;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        if (j < lane + 32 * k && par[k] == pj && tok[k] == tj) {  // gone already
+                            mine[k] = 0;
+                            px[k] = 0.f;
+                        }
+                }
+#pragma unroll 1
+                for (int j = 1; j < T; ++j) {
+                    const int pj = of(par[0], par[1], j);
+                    const uint64_t mj = shuffle64(j < 32 ? mine[0] : mine[1], j & 31);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        if (j < lane + 32 * k && par[k] == pj) left[k] -= min(left[k], mj);
+                }
             }
+            // probabilities below one step by themselves: 0 < p(x) stays
+            auto stays = [&](int k) {
+                return tok[k] >= 0 && (mine[k] ? part_of(u[k], left[k]) < mine[k] : u[k] * ((float)left[k] * 0x1p-58f) < px[k]);
+            };
+            const bool t0 = stays(0), t1 = stays(1);
+            for (;;) {  // down the first of each node's children that stays
+                const uint64_t kids = both(par[0] == end && t0, par[1] == end && t1);
+                if (!kids) break;
+                end = __ffsll((long long)kids) - 1;
+                path |= 1ull << end;
+            }
+            const uint64_t out = both(par[0] == end && tok[0] >= 0, par[1] == end && tok[1] >= 0);
+            ngone = __popcll(out);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                if ((out >> (lane + 32 * k)) & 1) gone[__popcll(out & ((1ull << (lane + 32 * k)) - 1))] = tok[k];
         }
         if (__any_sync(0xffffffffu, bad) && lane == 0 && rank == 0) atomicOr(p.err, HS_DEVERR_INDEX_RANGE);
         if (lane == 0) {
+            s_path = path;
             s_row = end;
             s_minus = minus;
             s_gone = ngone;
-        }
-        if (rank == 0) {
-            const int n = __popcll(path);
-            if (lane == 0) p.count[b] = n;
-            for (int i = lane; i < T; i += 32) {
-                int at = -1;
-                if (i < n) {  // the i-th node of the path
-                    uint64_t rest = path;
-                    for (int k = 0; k < i; ++k) rest &= rest - 1;
-                    at = __ffsll((long long)rest) - 1;
-                }
-                p.index[(int64_t)b * T + i] = at;
-            }
         }
     }
     __syncthreads();
     const P *row = static_cast<const P *>(p.probs) + ((int64_t)b * T + s_row) * p.ld;
     const P *guess = p.draft && s_minus ? static_cast<const P *>(p.draft) + ((int64_t)b * (T - 1) + s_row) * p.draft_ld : nullptr;
     int ngone = s_gone;
-    const float u0 = p.uniform[(int64_t)b * T];
+    // this warp's run of the row's units
     const int64_t unit = (int64_t)BATCH * p.per, units = (V + unit - 1) / unit;
-    const int first = (int)(units * rank / G), n = (int)(units * (rank + 1) / G) - first;
+    const int me = rank * NW + warp, W = G * NW;
+    const int first = (int)(units * me / W), n = (int)(units * (me + 1) / W) - first;
+    const int64_t v_first = first * unit;
+
+    // its first values into L2 while the first of them are added
+    if (lane < 2 && n > 0) {
+        const int64_t len = min(min((int64_t)n * unit, V - v_first), (int64_t)AHEAD) * (int64_t)sizeof(P);
+        const uint64_t at = (uint64_t)(lane ? guess : row) + (uint64_t)v_first * sizeof(P), a0 = at & ~15ull;
+        if (lane == 0 || guess) hs::tc::prefetch_l2((const void *)a0, (uint32_t)((at + len - a0 + 15) & ~15ull));
+    }
 
     for (int attempt = 0;; ++attempt) {
-        for (int i = warp; i < n; i += NW) {
-            uint64_t sum = 0;
-#pragma unroll 1
-            for (int k = 0; k < p.per; ++k) {
-                const int64_t v0 = (first + i) * unit + (int64_t)k * BATCH;
-                uint32_t x[8], y[8];
+        uint64_t total_lane = 0;
+        struct Values {
+            uint32_t x[8], y[8];
+        };
+        auto load = [&](Values &q, int j) {  // batch j of the run
+            const int64_t v0 = v_first + (int64_t)j * BATCH;
+            if (v0 + BATCH <= V) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) q.x[e] = bits_at<P>(row + v0 + lane, 32 * e);
+                if (guess) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) q.y[e] = bits_at<P>(guess + v0 + lane, 32 * e);
+                }
+            } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const int64_t v = v0 + 32 * e + lane;
-                    x[e] = v < V ? bits_at<P>(row, v) : 0u;
-                    y[e] = guess && v < V ? bits_at<P>(guess, v) : 0u;
-                }
-                // the refused children's tokens among these
-                for (int g = 0; g < ngone; ++g) {
-                    const int64_t at = gone[g] - v0;
-                    if (at >= 0 && at < BATCH && (at & 31) == lane) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) x[e] = (at >> 5) == e ? 0u : x[e];
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t a = clean(x[e]), c = clean(y[e]);
-                    const uint64_t r = a > c ? fixed(a) - fixed(c) : 0ull;
-                    sum = add_sat(sum, r);
+                    q.x[e] = v < V ? bits_at<P>(row, v) : 0u;
+                    q.y[e] = guess && v < V ? bits_at<P>(guess, v) : 0u;
                 }
             }
+        };
+        auto add = [&](Values &q, int j) {  // the lane's sum, at most 8
+            const int64_t v0 = v_first + (int64_t)j * BATCH;
+#pragma unroll 1
+            for (int g = 0; g < ngone; ++g) {  // the refused children's tokens among these
+                const int64_t at = gone[g] - v0;
+                if (at >= 0 && at < BATCH && (at & 31) == lane) {
 #pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) sum = add_sat(sum, (uint64_t)__shfl_xor_sync(0xffffffffu, (unsigned long long)sum, o));
-            if (lane == 0) sums[i] = sum;
+                    for (int e = 0; e < 8; ++e) q.x[e] = (at >> 5) == e ? 0u : q.x[e];
+                }
+            }
+            float h0 = 0.f, h1 = 0.f, m0 = 0.f, m1 = 0.f, l0 = 0.f, l1 = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                const float x0 = within(__uint_as_float(q.x[e])), x1 = within(__uint_as_float(q.x[e + 1]));
+                const Digits d = digits_of(x0, x1);
+                add2(h0, h1, d.h0, d.h1);
+                add2(m0, m1, d.m0, d.m1);
+                add2(l0, l1, d.l0, d.l1);
+                if (guess) {  // where it is the larger, nothing is left: the same digits
+                    const float y0 = fminf(within(__uint_as_float(q.y[e])), x0), y1 = fminf(within(__uint_as_float(q.y[e + 1])), x1);
+                    const Digits f = digits_of(y0, y1);
+                    add2(h0, h1, -f.h0, -f.h1);
+                    add2(m0, m1, -f.m0, -f.m1);
+                    add2(l0, l1, -f.l0, -f.l1);
+                }
+            }
+            const int h = __float2int_rn((h0 + h1) * 0x1p20f), m = __float2int_rn((m0 + m1) * 0x1p41f);
+            const int l = __float2int_rn((l0 + l1) * 0x1p58f);
+            // the digits' signs differ, their sum has none
+            return (uint64_t)max(((int64_t)h << 38) + ((int64_t)m << 17) + l, (int64_t)0);
+        };
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+            uint64_t sum = 0;
+#pragma unroll 1
+            for (int k = 0; k < p.per; ++k) {
+                Values q;
+                load(q, i * p.per + k);
+                sum = add_sat(sum, add(q, i * p.per + k));
+            }
+            sums[warp][i][lane] = sum;
+            total_lane = add_sat(total_lane, sum);
         }
-        __syncthreads();
-        uint64_t mine = 0;  // of lane's sums: 16 in a row
-        if (warp == 0) {
-            for (int k = 0; k < MAXB / 32; ++k) {
-                const int i = lane * (MAXB / 32) + k;
-                mine = add_sat(mine, i < n ? sums[i] : 0ull);
-            }
-            uint64_t all = mine;
+        uint64_t all = total_lane;
 #pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) all = add_sat(all, (uint64_t)__shfl_xor_sync(0xffffffffu, (unsigned long long)all, o));
-            if (lane < G) {
-                const uint32_t at = hs::dsmem_map(&totals[rank], lane);
-                asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(all) : "memory");
-            }
+        for (int o = 16; o >= 1; o >>= 1) all = add_sat(all, (uint64_t)__shfl_xor_sync(0xffffffffu, (unsigned long long)all, o));
+        if (lane < G) {
+            const uint32_t at = hs::dsmem_map(&totals[me], lane);
+            asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(all) : "memory");
         }
         hs::cluster_arrive();
-        hs::cluster_wait();
-        uint64_t before = 0, total = 0;
-        for (int g = 0; g < G; ++g) {
-            if (g == rank) before = total;
-            total = add_sat(total, totals[g]);
+        if (rank == 0 && warp == 1 && attempt == 0) {
+            const uint64_t path = s_path;
+            const int len = __popcll(path);
+            for (int t = lane; t < T; t += 32) {
+                if ((path >> t) & 1) p.index[(int64_t)b * T + __popcll(path & ((1ull << t) - 1))] = t;
+                if (t >= len) p.index[(int64_t)b * T + t] = -1;
+            }
+            if (lane == 0) p.count[b] = len;
         }
+        const float u0 = p.uniform[(int64_t)b * T];
+        hs::cluster_wait();
+        // sums of the cluster's warps, two a lane
+        const uint64_t t0 = 2 * lane < W ? totals[2 * lane] : 0ull, t1 = 2 * lane + 1 < W ? totals[2 * lane + 1] : 0ull;
+        const uint64_t some = sum_up(add_sat(t0, t1), lane), total = shuffle64(some, 31);
         if (total == 0 && attempt == 0 && (guess || ngone)) {
             // nothing is left beside the draft: by the row itself
             guess = nullptr;
@@ -262,56 +371,73 @@ verify_kernel(const VerifyParams p) {
             hs::cluster_wait();
             continue;
         }
-        if (warp != 0) return;
         if (total == 0) {
-            if (rank == 0 && lane == 0) {
+            if (me == 0 && lane == 0) {
                 p.next[b] = -1;
                 atomicOr(p.err, HS_DEVERR_INDEX_RANGE);
             }
             return;
         }
-        const uint64_t border = part_of(u0, total);
-        if (border < before || border - before >= totals[rank]) return;
-        // which lane's sums, which of them, which batch, which lane's values, which value:
-        // each time the first whose inclusive sum passes the border
-        uint64_t rest = border - before;
-        auto locate = [&](uint64_t x) {  // lane; rest becomes what is left in it
-            uint64_t incl = x;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint64_t y = (uint64_t)__shfl_up_sync(0xffffffffu, (unsigned long long)incl, o);
-                if (lane >= o) incl = add_sat(incl, y);
-            }
+        // Which warp's run, which of its units, which batch, which lane's values, which value:
+        // each time the first whose inclusive sum passes the border.
+        uint64_t rest = part_of(u0, total);
+        auto locate = [&](uint64_t incl) {  // lane; rest becomes what is left in it
             const uint32_t past = __ballot_sync(0xffffffffu, incl > rest);
             const int l = past ? __ffs(past) - 1 : -1;
             if (l > 0) rest -= shuffle64(incl, l - 1);
             return l;
         };
-        int l = locate(mine);
-        if (l < 0) return;  // cannot be: the sums are the same ones
-        int i = l * (MAXB / 32);
-        while (i < n - 1 && sums[i] <= rest) rest -= sums[i++];
+        int l = locate(some);
+        if (l < 0) return;  // cannot be: it is less than the total
+        const uint64_t t_first = shuffle64(t0, l);
+        const int w = 2 * l + (rest >= t_first);
+        if (w != me) return;
+        if (w & 1) rest -= t_first;
+        uint64_t mine = 0;  // of unit lane / 2: its even or odd lanes' sums
+        if (lane < 2 * n) {
+#pragma unroll 8
+            for (int k = 0; k < 32; k += 2) mine = add_sat(mine, sums[warp][lane >> 1][k + (lane & 1)]);
+        }
+        mine = add_sat(mine, (uint64_t)__shfl_xor_sync(0xffffffffu, (unsigned long long)mine, 1));
+        l = locate(sum_up(lane & 1 ? 0ull : mine, lane)) >> 1;
+        if (l < 0) return;
+#pragma unroll 1
         for (int k = 0; k < p.per; ++k) {
-            const int64_t v0 = (first + i) * unit + (int64_t)k * BATCH + 8 * lane;
+            const int64_t v0 = v_first + l * unit + (int64_t)k * BATCH + 8 * lane;
+            uint32_t x[8], y[8];
             uint64_t r[8], sum = 0;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int64_t v = v0 + e;
-                uint32_t a = v < V ? clean(bits_at<P>(row, v)) : 0u;
-                const uint32_t c = guess && v < V ? clean(bits_at<P>(guess, v)) : 0u;
-                for (int g = 0; g < ngone; ++g) a = gone[g] == v ? 0u : a;
-                r[e] = a > c ? fixed(a) - fixed(c) : 0ull;
-                sum = add_sat(sum, r[e]);
+                x[e] = v < V ? bits_at<P>(row, v) : 0u;
+                y[e] = guess && v < V ? bits_at<P>(guess, v) : 0u;
             }
-            l = locate(sum);
-            if (l < 0) {  // a later batch: all of this one lies before the border
-                uint64_t all = sum;
+#pragma unroll 1
+            for (int g = 0; g < ngone; ++g) {
+                const int64_t at = gone[g] - v0;
 #pragma unroll
-                for (int o = 16; o >= 1; o >>= 1) all = add_sat(all, (uint64_t)__shfl_xor_sync(0xffffffffu, (unsigned long long)all, o));
-                rest -= all;
+                for (int e = 0; e < 8; ++e) x[e] = at == e ? 0u : x[e];
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t a = clean(x[e]), c = clean(y[e]);
+                r[e] = a > c ? fixed(a) - fixed(c) : 0ull;
+                sum += r[e];
+            }
+            sum = sum_up(sum, lane);
+            int at = locate(sum);
+            if (at < 0 && k + 1 < p.per) {  // a later batch: all of this one lies before the border
+                rest -= min(rest, shuffle64(sum, 31));
                 continue;
             }
-            if (lane == l) {
+            // The values by themselves are cut off at 2^-58 where their sum was not: behind all
+            // of them it is the last one that is there.
+            const bool behind = at < 0;
+            uint32_t some_left = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) some_left |= clean(x[e]) > clean(y[e]) ? 1u << e : 0u;
+            if (behind) at = 31 - __clz((int)__ballot_sync(0xffffffffu, some_left != 0));
+            if (lane == at) {
                 int e = 0;
 #pragma unroll
                 for (int j = 0; j < 7; ++j)
@@ -319,7 +445,7 @@ verify_kernel(const VerifyParams p) {
                         rest -= r[j];
                         ++e;
                     }
-                p.next[b] = (int32_t)(v0 + e);
+                p.next[b] = (int32_t)(v0 + (behind ? 31 - __clz((int)some_left) : e));
             }
             return;
         }
@@ -364,7 +490,8 @@ extern "C" hs_status hs_verify_drafts(hs_pool_t pool, int32_t B, int32_t T, int3
     const int64_t batches = ((int64_t)V + BATCH - 1) / BATCH;
     // CTAs per request: one for as many batches as it has warps, eight at most
     const int G = (int)(batches <= NW ? 1 : (batches <= 2 * NW ? 2 : (batches <= 4 * NW ? 4 : MAXG)));
-    p.per = (int)((batches + (int64_t)G * MAXB - G - 1) / ((int64_t)G * MAXB - G));
+    // a run has at most `UNITS` units: one less, and one for what the division leaves
+    p.per = (int)((batches + (int64_t)G * NW * (UNITS - 1) - 1) / ((int64_t)G * NW * (UNITS - 1)));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)G, (unsigned)B, 1);
     cfg.blockDim = dim3(VT, 1, 1);
