@@ -76,27 +76,38 @@ __device__ __forceinline__ float within(float x) {
     asm("add.sat.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ void add2(float &a, float &b, float c, float d) {
-    asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
-        : "+f"(a), "+f"(b)
-        : "f"(c), "f"(d));
+// Pairs of f32 in one register pair, and operations on both.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t x;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(lo), "f"(hi));
+    return x;
+}
+__device__ __forceinline__ float both_of(uint64_t x) {  // their sum
+    float lo, hi;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+    return lo + hi;
+}
+__device__ __forceinline__ uint64_t plus(uint64_t a, uint64_t b) {
+    uint64_t c;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(c) : "l"(a), "l"(b));
+    return c;
+}
+__device__ __forceinline__ uint64_t less(uint64_t a, uint64_t b) {  // a - b
+    uint64_t c;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(c) : "l"(b), "l"(0xbf800000bf800000ull), "l"(a));
+    return c;
 }
 // Two values' digits: the multiples of 2^-20 and 2^-41, and the rest.
 struct Digits {
-    float h0, h1, m0, m1, l0, l1;
+    uint64_t h, m, l;
 };
-__device__ __forceinline__ Digits digits_of(float x0, float x1) {
-    constexpr float C1 = 12.f, C2 = 0x1.8p-18f;
+__device__ __forceinline__ Digits digits_of(uint64_t x) {
+    constexpr uint64_t C1 = 0x4140000041400000ull, C2 = 0x36c0000036c00000ull, SIGNS = 0x8000000080000000ull;  // 12, 1.5 2^-18
     Digits d;
-    d.h0 = x0, d.h1 = x1;
-    add2(d.h0, d.h1, C1, C1);
-    add2(d.h0, d.h1, -C1, -C1);
-    add2(x0, x1, -d.h0, -d.h1);
-    d.m0 = x0, d.m1 = x1;
-    add2(d.m0, d.m1, C2, C2);
-    add2(d.m0, d.m1, -C2, -C2);
-    d.l0 = x0, d.l1 = x1;
-    add2(d.l0, d.l1, -d.m0, -d.m1);
+    d.h = plus(plus(x, C1), C1 ^ SIGNS);
+    x = less(x, d.h);
+    d.m = plus(plus(x, C2), C2 ^ SIGNS);
+    d.l = less(x, d.m);
     return d;
 }
 // In units of 2^-58, the rest cut off.
@@ -280,19 +291,20 @@ verify_kernel(const VerifyParams p) {
         struct Values {
             uint32_t x[8], y[8];
         };
+        const int whole = (int)((V - v_first) / BATCH);  // batches that lie inside the row
+        const P *row_at = row + v_first + lane, *guess_at = guess + v_first + lane;
         auto load = [&](Values &q, int j) {  // batch j of the run
-            const int64_t v0 = v_first + (int64_t)j * BATCH;
-            if (v0 + BATCH <= V) {
+            if (j < whole) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) q.x[e] = bits_at<P>(row + v0 + lane, 32 * e);
+                for (int e = 0; e < 8; ++e) q.x[e] = bits_at<P>(row_at + (int64_t)j * BATCH, 32 * e);
                 if (guess) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) q.y[e] = bits_at<P>(guess + v0 + lane, 32 * e);
+                    for (int e = 0; e < 8; ++e) q.y[e] = bits_at<P>(guess_at + (int64_t)j * BATCH, 32 * e);
                 }
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const int64_t v = v0 + 32 * e + lane;
+                    const int64_t v = v_first + (int64_t)j * BATCH + 32 * e + lane;
                     q.x[e] = v < V ? bits_at<P>(row, v) : 0u;
                     q.y[e] = guess && v < V ? bits_at<P>(guess, v) : 0u;
                 }
@@ -308,36 +320,39 @@ verify_kernel(const VerifyParams p) {
                     for (int e = 0; e < 8; ++e) q.x[e] = (at >> 5) == e ? 0u : q.x[e];
                 }
             }
-            float h0 = 0.f, h1 = 0.f, m0 = 0.f, m1 = 0.f, l0 = 0.f, l1 = 0.f;
+            Digits all = {0, 0, 0};
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
                 const float x0 = within(__uint_as_float(q.x[e])), x1 = within(__uint_as_float(q.x[e + 1]));
-                const Digits d = digits_of(x0, x1);
-                add2(h0, h1, d.h0, d.h1);
-                add2(m0, m1, d.m0, d.m1);
-                add2(l0, l1, d.l0, d.l1);
+                const Digits d = digits_of(pair(x0, x1));
+                all.h = plus(all.h, d.h);
+                all.m = plus(all.m, d.m);
+                all.l = plus(all.l, d.l);
                 if (guess) {  // where it is the larger, nothing is left: the same digits
-                    const float y0 = fminf(within(__uint_as_float(q.y[e])), x0), y1 = fminf(within(__uint_as_float(q.y[e + 1])), x1);
-                    const Digits f = digits_of(y0, y1);
-                    add2(h0, h1, -f.h0, -f.h1);
-                    add2(m0, m1, -f.m0, -f.m1);
-                    add2(l0, l1, -f.l0, -f.l1);
+                    const Digits f = digits_of(pair(fminf(within(__uint_as_float(q.y[e])), x0),
+                                                    fminf(within(__uint_as_float(q.y[e + 1])), x1)));
+                    all.h = less(all.h, f.h);
+                    all.m = less(all.m, f.m);
+                    all.l = less(all.l, f.l);
                 }
             }
-            const int h = __float2int_rn((h0 + h1) * 0x1p20f), m = __float2int_rn((m0 + m1) * 0x1p41f);
-            const int l = __float2int_rn((l0 + l1) * 0x1p58f);
+            const int h = __float2int_rn(both_of(all.h) * 0x1p20f), m = __float2int_rn(both_of(all.m) * 0x1p41f);
+            const int l = __float2int_rn(both_of(all.l) * 0x1p58f);
             // the digits' signs differ, their sum has none
             return (uint64_t)max(((int64_t)h << 38) + ((int64_t)m << 17) + l, (int64_t)0);
         };
+        int j = 0;
 #pragma unroll 1
         for (int i = 0; i < n; ++i) {
             uint64_t sum = 0;
+            int k = p.per;
 #pragma unroll 1
-            for (int k = 0; k < p.per; ++k) {
+            do {
                 Values q;
-                load(q, i * p.per + k);
-                sum = add_sat(sum, add(q, i * p.per + k));
-            }
+                load(q, j);
+                sum = add_sat(sum, add(q, j));
+                ++j;
+            } while (--k > 0);
             sums[warp][i][lane] = sum;
             total_lane = add_sat(total_lane, sum);
         }
