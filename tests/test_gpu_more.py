@@ -381,7 +381,7 @@ def test_evict(n_first, n_last, saved_only):
     c.close()
 
 
-@pytest.mark.parametrize("pages", [1024, 32768, 32769, 41000, 70000])
+@pytest.mark.parametrize("pages", [512, 513, 1024, 2049, 5000, 32769, 70000, 270000])
 def test_evict_of_long_contexts(pages):
     """More pages than a scan takes at a time, and than keys fit in shared memory."""
     ctx = [pages * 64, pages * 64 - 64 * 17 - 3]

@@ -3,12 +3,16 @@
 //
 // Kept are the first n_first and the last n_last pages of the context, with SAVED_ONLY
 // those without a host copy too, and then the others by descending weight, equal weights by
-// ascending page, until there are `budget`. One CTA per request: the weights become keys
-// whose unsigned order is theirs, three histograms of 11, 11 and 10 bits find the key at the
-// border, and one scan over rows of 32 pages gives every page its place in the two lists:
-// with g pages above the border before it and e on it, a page has min(e, room) + g kept
-// ones before it. Bound: the latencies of the call; 16,384 pages are 12 bytes each, 196 KB,
-// which one CTA reads in two microseconds.
+// ascending page, until there are `budget`. The weights become keys whose unsigned order is
+// theirs. Bound: the latencies of the call; 16,384 pages are 12 bytes each.
+//   512 pages at most: one CTA, a thread per page, which counts the keys before its own;
+//   more: a cluster of CTAs, a slice of the pages each. A histogram of the range that the
+//   keys are in, added over the cluster, gives the bin that the border is in; as soon as
+//   a bin has no more than CANDS keys all CTAs take them and count (mostly after one
+//   histogram). With g pages above the border and e on it before a page, min(e, room) + g
+//   kept ones are before that page, so one exchange of the slices' counts places every page
+//   in the two lists. (16 requests of 16,384 pages: one CTA of 1,024 threads for everything
+//   27 us; a cluster with histograms of 2,048 bins, whose exchange takes 3 us each, 23 us.)
 #include <atomic>
 #include <cstdint>
 
@@ -19,11 +23,12 @@ namespace {
 
 using hs::kPage;
 
-constexpr int ET = 1024;       // threads per CTA
+constexpr int ET = 512;        // threads per CTA
 constexpr int NW = ET / 32;
-constexpr int BINS = 2048;
-constexpr int ROWS = 1024;     // rows of 32 pages per scan
-constexpr int CAP = 40960;     // keys that are kept in shared memory: 2.6 million tokens
+constexpr int BINS = 512;      // one per thread
+constexpr int CANDS = 512;
+constexpr int CAP = 32768;     // keys of a slice that are kept in shared memory
+constexpr int MAXG = 8;
 constexpr uint32_t ABSENT = 0u, MUST = 0xffffffffu;
 
 struct EvictParams {
@@ -44,169 +49,308 @@ __device__ __forceinline__ uint32_t key_of(float w) {
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(ET)
-evict_kernel(const EvictParams p) {
-    hs::tc::grid_dep_wait();
-    hs::tc::grid_dep_launch();
-    extern __shared__ uint32_t keys[];  // [cap]
-    __shared__ uint32_t hist[BINS];
-    __shared__ int32_t above[ROWS], equal[ROWS], all[ROWS];
-    __shared__ int32_t wsum[NW], s_bin, s_over, s_cand, s_must;
-    const int i = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+__device__ __forceinline__ uint32_t key_at(const EvictParams &p, int page, int P, float w, int2 where) {
+    if (where.x < 0) return ABSENT;
+    const bool must = page < p.n_first || page >= P - p.n_last || (p.saved_only && where.y < 0);
+    return must ? MUST : key_of(w);
+}
+// Request i's cache index, or -1 with its outputs written; its pages.
+__device__ __forceinline__ int request_of(const EvictParams &p, int i, bool first, int &P, int &budget) {
     const int r = p.req[i];
-    int32_t *kept = p.kept + (size_t)i * p.N, *freed = p.freed + (size_t)i * p.max_pages;
+    budget = p.budget[i];
     if (r < 0 || r >= p.max_req) {
-        for (int k = tid; k < p.N; k += ET) kept[k] = -1;
-        if (tid == 0) {
-            p.n_freed[i] = 0;
-            atomicOr(p.err, HS_DEVERR_BAD_REQUEST);
+        if (first) {
+            for (int k = threadIdx.x; k < p.N; k += ET) p.kept[(size_t)i * p.N + k] = -1;
+            if (threadIdx.x == 0) {
+                p.n_freed[i] = 0;
+                atomicOr(p.err, HS_DEVERR_BAD_REQUEST);
+            }
         }
-        return;
+        return -1;
     }
     const int len = p.ctx[r], L = hs::context_within(len, p.max_ctx);
-    const int budget = p.budget[i];
-    const int P = L <= 0 ? 0 : (L - 1) / kPage + 1;
-    int2 *table = p.table + (size_t)r * p.max_pages;
-    const float *weights = p.weights + (size_t)r * p.max_pages;
-    auto make = [&](int page, float w, int2 where) {
-        if (where.x < 0) return ABSENT;
-        const bool must = page < p.n_first || page >= P - p.n_last || (p.saved_only && where.y < 0);
-        return must ? MUST : key_of(w);
-    };
-    auto key_at = [&](int page) { return page < p.cap ? keys[page] : make(page, weights[page], table[page]); };
-    if (tid == 0) {
-        s_cand = s_must = 0;
+    P = L <= 0 ? 0 : (L - 1) / kPage + 1;
+    if (first && threadIdx.x == 0) {
         uint32_t bad = len > p.max_ctx ? HS_DEVERR_INDEX_RANGE : 0u;
         if (budget < 0) bad |= HS_DEVERR_BAD_PAGE;
         if (bad) atomicOr(p.err, bad);
     }
-    for (int k = tid; k < BINS; k += ET) hist[k] = 0;
-    __syncthreads();
+    return r;
+}
 
+// At most ET pages: one CTA per request.
+__global__ void __launch_bounds__(ET)
+evict_few_kernel(const EvictParams p) {
+    hs::tc::grid_dep_wait();
+    hs::tc::grid_dep_launch();
+    __shared__ __align__(16) uint32_t keys[ET];
+    __shared__ int32_t warp_kept[NW], warp_all[NW], warp_must[NW];
+    const int i = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int P, budget;
+    const int r = request_of(p, i, true, P, budget);
+    if (r < 0) return;
+    int2 *table = p.table + (size_t)r * p.max_pages;
+    int2 where = make_int2(-1, -1);
+    uint32_t key = ABSENT;
+    if (tid < P) {
+        where = table[tid];
+        key = key_at(p, tid, P, p.weights[(size_t)r * p.max_pages + tid], where);
+    }
+    keys[tid] = key;
+    const int must_n = __popc(__ballot_sync(0xffffffffu, key == MUST));
+    const uint32_t here = __ballot_sync(0xffffffffu, key != ABSENT);
+    if (lane == 0) {
+        warp_must[warp] = must_n;
+        warp_all[warp] = __popc(here);
+    }
+    __syncthreads();
+    int must = 0, cand = 0, all_before = __popc(here & ((1u << lane) - 1u));
+    for (int w = 0; w < NW; ++w) {
+        must += warp_must[w];
+        all_before += w < warp ? warp_all[w] : 0;
+        cand += warp_all[w];
+    }
+    // how many of the pages that need not stay come before this one
+    int rank = 0;
+    if (key != ABSENT && key != MUST) {
+        const uint4 *k4 = reinterpret_cast<const uint4 *>(keys);
+        for (int k = 0; k < P; k += 4) {
+            const uint4 v = k4[k >> 2];
+            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) rank += (x[e] > key && x[e] != MUST) || (x[e] == key && k + e < tid);
+        }
+    }
+    // a negative budget frees nothing
+    const bool stay = key == MUST || (key != ABSENT && (budget < 0 || rank < budget - must));
+    const uint32_t kept = __ballot_sync(0xffffffffu, stay);
+    if (lane == 0) warp_kept[warp] = __popc(kept);
+    __syncthreads();
+    int before = __popc(kept & ((1u << lane) - 1u)), total = 0;
+    for (int w = 0; w < NW; ++w) {
+        before += w < warp ? warp_kept[w] : 0;
+        total += warp_kept[w];
+    }
+    if (stay) {
+        if (before < p.N) p.kept[(size_t)i * p.N + before] = tid;
+    } else if (key != ABSENT) {
+        p.freed[(size_t)i * p.max_pages + all_before - before] = where.x;
+        if (!p.plan) table[tid].x = -1;
+    }
+    for (int k = total + tid; k < p.N; k += ET) p.kept[(size_t)i * p.N + k] = -1;
+    if (tid == 0) {
+        p.n_freed[i] = cand - total;
+        if (total > p.N) atomicOr(p.err, HS_DEVERR_CAPACITY);
+    }
+}
+
+// A cluster of G CTAs per request, a slice of the pages each.
+__global__ void __launch_bounds__(ET)
+evict_kernel(const EvictParams p, const int G) {
+    hs::tc::grid_dep_wait();
+    hs::tc::grid_dep_launch();
+    extern __shared__ uint32_t keys[];  // [cap] of the slice
+    __shared__ uint32_t hist[2][BINS];  // one is read by the others while the next is filled
+    __shared__ uint32_t own[CANDS];     // the slice's candidates
+    __shared__ __align__(16) uint32_t cands[CANDS];
+    __shared__ int32_t wsum[NW][3], s_bin, s_over, s_n;
+    __shared__ uint32_t s_border, s_room, wkey[NW][2];
+    __shared__ int32_t counts[MAXG][4], parts[MAXG][3], lists[MAXG];  // of all CTAs
+    const int i = blockIdx.x / G, rank = (int)hs::cluster_ctarank(), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int P, budget;
+    const int r = request_of(p, i, rank == 0, P, budget);
+    if (r < 0) return;  // the whole cluster
+    int2 *table = p.table + (size_t)r * p.max_pages;
+    const float *weights = p.weights + (size_t)r * p.max_pages;
+    int32_t *kept = p.kept + (size_t)i * p.N, *freed = p.freed + (size_t)i * p.max_pages;
+    const int per = ((P + 32 * G - 1) / (32 * G)) * 32, p0 = min(rank * per, P), n = min(per, P - p0);
+    auto key = [&](int k) {
+        return k < p.cap ? keys[k] : key_at(p, p0 + k, P, weights[p0 + k], table[p0 + k]);
+    };
+    hist[0][tid] = hist[1][tid] = 0;
+    if (tid == 0) s_n = 0;
     int cand = 0, must = 0;
+    uint32_t lo = MUST, hi = ABSENT;  // of the keys that need not stay
 #pragma unroll 4
-    for (int page = tid; page < P; page += ET) {
-        const uint32_t k = make(page, weights[page], table[page]);
-        if (page < p.cap) keys[page] = k;
-        cand += k != ABSENT;
-        must += k == MUST;
+    for (int k = tid; k < n; k += ET) {
+        const uint32_t x = key_at(p, p0 + k, P, weights[p0 + k], table[p0 + k]);
+        if (k < p.cap) keys[k] = x;
+        cand += x != ABSENT;
+        must += x == MUST;
+        if (x != ABSENT && x != MUST) {
+            lo = min(lo, x);
+            hi = max(hi, x);
+        }
     }
     cand = __reduce_add_sync(0xffffffffu, cand);
     must = __reduce_add_sync(0xffffffffu, must);
-    if (lane == 0 && cand) {
-        atomicAdd(&s_cand, cand);
-        atomicAdd(&s_must, must);
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lane == 0) {
+        wsum[warp][0] = cand;
+        wsum[warp][1] = must;
+        wkey[warp][0] = lo;
+        wkey[warp][1] = hi;
     }
     __syncthreads();
+    if (warp == 0) {
+        cand = __reduce_add_sync(0xffffffffu, lane < NW ? wsum[lane][0] : 0);
+        must = __reduce_add_sync(0xffffffffu, lane < NW ? wsum[lane][1] : 0);
+        lo = __reduce_min_sync(0xffffffffu, lane < NW ? wkey[lane][0] : MUST);
+        hi = __reduce_max_sync(0xffffffffu, lane < NW ? wkey[lane][1] : ABSENT);
+        if (lane < G) {
+            hs::dsmem_st(hs::dsmem_map(&counts[rank][0], lane), cand);
+            hs::dsmem_st(hs::dsmem_map(&counts[rank][1], lane), must);
+            hs::dsmem_st(hs::dsmem_map(&counts[rank][2], lane), (int32_t)lo);
+            hs::dsmem_st(hs::dsmem_map(&counts[rank][3], lane), (int32_t)hi);
+        }
+    }
+    hs::cluster_arrive();
+    hs::cluster_wait();
+    cand = must = 0;
+    lo = MUST;
+    hi = ABSENT;
+    for (int g = 0; g < G; ++g) {
+        cand += counts[g][0];
+        must += counts[g][1];
+        lo = min(lo, (uint32_t)counts[g][2]);
+        hi = max(hi, (uint32_t)counts[g][3]);
+    }
     // of the pages that need not stay, the `need` of the largest keys do; a negative budget
     // frees nothing
-    const int others = s_cand - s_must;
-    const int need = budget < 0 ? others : max(budget - s_must, 0);
+    const int others = cand - must, need = budget < 0 ? others : max(budget - must, 0);
     uint32_t border = ABSENT;  // keys above it stay, and of those equal to it the first `room`
     int room = 0;
     if (need == 0) {
         border = MUST - 1;
     } else if (need < others) {
-        int left = need;
-        uint32_t prefix = 0;
+        int left = need, inside = others;  // of the keys in lo .. hi
 #pragma unroll 1
-        for (int d = 0; d < 3; ++d) {
-            const int shift = d == 0 ? 21 : (d == 1 ? 10 : 0), bits = d == 2 ? 10 : 11;
-            for (int page = tid; page < P; page += ET) {
-                const uint32_t k = key_at(page);
-                if (k != ABSENT && k != MUST && (d == 0 || (k >> (shift + bits)) == prefix))
-                    atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1)], 1u);
+        for (int d = 0; lo < hi && inside > CANDS; ++d) {
+            const int wide = 32 - __clz((int)(hi - lo)), shift = wide > 9 ? wide - 9 : 0;
+            uint32_t *h = hist[d & 1];
+            for (int k = tid; k < n; k += ET) {
+                const uint32_t x = key(k);
+                if (x >= lo && x <= hi) atomicAdd(&h[(x - lo) >> shift], 1u);
             }
-            __syncthreads();
-            // bins from the top: thread t has bins 2047 - 2t and 2046 - 2t
-            const int h0 = (int)hist[BINS - 1 - 2 * tid], h1 = (int)hist[BINS - 2 - 2 * tid];
-            int incl = h0 + h1;
+            hs::cluster_arrive();
+            hs::cluster_wait();
+            // bins from the top, one a thread, over all slices
+            int mine = 0;
+#pragma unroll
+            for (int g = 0; g < MAXG; ++g)
+                if (g < G) mine += hs::dsmem_ld(hs::dsmem_map(&h[BINS - 1 - tid], (uint32_t)g));
+            int incl = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, incl, o);
                 if (lane >= o) incl += y;
             }
-            if (lane == 31) wsum[warp] = incl;
+            if (lane == 31) wsum[warp][0] = incl;
+            hist[(d & 1) ^ 1][tid] = 0;  // read by the others before the last barrier
             __syncthreads();
-            const int w = lane < warp ? wsum[lane] : 0;
-            const int over = __reduce_add_sync(0xffffffffu, w) + incl - h0 - h1;  // keys in higher bins
-            if (over < left && over + h0 >= left) {
-                s_bin = BINS - 1 - 2 * tid;
+            const int over = __reduce_add_sync(0xffffffffu, lane < warp ? wsum[lane][0] : 0) + incl - mine;  // in higher bins
+            if (over < left && over + mine >= left) {
+                s_bin = BINS - 1 - tid;
                 s_over = over;
-            } else if (over + h0 < left && over + h0 + h1 >= left) {
-                s_bin = BINS - 2 - 2 * tid;
-                s_over = over + h0;
+                s_n = mine;
             }
-            hist[BINS - 1 - 2 * tid] = hist[BINS - 2 - 2 * tid] = 0;
             __syncthreads();
-            prefix = (prefix << bits) | (uint32_t)s_bin;
+            lo += (uint32_t)s_bin << shift;
+            hi = min(hi, lo + ((1u << shift) - 1u));
             left -= s_over;
+            inside = s_n;
+            __syncthreads();
         }
-        border = prefix;
+        border = lo;  // where one key is left
         room = left;
-    }
-    // border is ABSENT where all stay
-
-    int base_g = 0, base_e = 0, base_a = 0;
-    for (int p0 = 0; p0 < P; p0 += 32 * ROWS) {
-        const int rows = min(ROWS, (P - p0 + 31) / 32);
-        for (int row = warp; row < rows; row += NW) {
-            const int page = p0 + 32 * row + lane;
-            const uint32_t k = page < P ? key_at(page) : ABSENT;
-            const uint32_t g = __ballot_sync(0xffffffffu, k > border);
-            const uint32_t e = __ballot_sync(0xffffffffu, k == border && k != ABSENT);
-            const uint32_t a = __ballot_sync(0xffffffffu, k != ABSENT);
-            if (lane == 0) {
-                above[row] = __popc(g);
-                equal[row] = __popc(e);
-                all[row] = __popc(a);
+        if (lo < hi) {
+            if (tid == 0) s_n = 0;
+            __syncthreads();
+            for (int k = tid; k < n; k += ET) {
+                const uint32_t x = key(k);
+                if (x >= lo && x <= hi) own[atomicAdd(&s_n, 1)] = x;
             }
-        }
-        __syncthreads();
-        if (warp < 3) {  // exclusive sums of the rows, 32 per lane
-            int32_t *v = warp == 0 ? above : (warp == 1 ? equal : all);
-            int mine = 0;
-            for (int k = 0; k < ROWS / 32; ++k) {
-                const int at = k * 32 + lane;
-                // 32 rows at a time: their sums so far
-                int x = at < rows ? v[at] : 0, incl = x;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int y = __shfl_up_sync(0xffffffffu, incl, o);
-                    if (lane >= o) incl += y;
+            __syncthreads();
+            if (tid < G) hs::dsmem_st(hs::dsmem_map(&lists[rank], (uint32_t)tid), s_n);
+            hs::cluster_arrive();
+            hs::cluster_wait();
+            // all slices' candidates: any order, the border is a value
+            cands[tid] = ABSENT;
+            __syncthreads();
+            int at = 0;
+            for (int g = 0; g < G; ++g) {
+                const int m = lists[g];
+                if (tid < m) cands[at + tid] = (uint32_t)hs::dsmem_ld(hs::dsmem_map(&own[tid], (uint32_t)g));
+                at += m;
+            }
+            __syncthreads();
+            if (tid < inside) {
+                const uint32_t x = cands[tid];
+                const uint4 *c4 = reinterpret_cast<const uint4 *>(cands);
+                int more = 0, same = 0;
+                for (int k = 0; k < inside; k += 4) {
+                    const uint4 v = c4[k >> 2];
+                    more += (v.x > x) + (v.y > x) + (v.z > x) + (v.w > x);
+                    same += (v.x == x) + (v.y == x) + (v.z == x) + (v.w == x);
                 }
-                if (at < rows) v[at] = mine + incl - x;
-                mine += __shfl_sync(0xffffffffu, incl, 31);
-                if ((k + 1) * 32 >= rows) break;
+                if (more < left && more + same >= left) {  // equal ones write the same
+                    s_border = x;
+                    s_room = (uint32_t)(left - more);
+                }
             }
-            if (lane == 0) wsum[warp] = mine;
+            __syncthreads();
+            border = s_border;
+            room = (int)s_room;
         }
-        __syncthreads();
-        for (int row = warp; row < rows; row += NW) {
-            const int page = p0 + 32 * row + lane;
-            const uint32_t k = page < P ? key_at(page) : ABSENT;
-            const bool isg = k > border, ise = k == border && k != ABSENT, isa = k != ABSENT;
-            const uint32_t lower = (1u << lane) - 1u;
-            const int g = base_g + above[row] + __popc(__ballot_sync(0xffffffffu, isg) & lower);
-            const int e = base_e + equal[row] + __popc(__ballot_sync(0xffffffffu, ise) & lower);
-            const int a = base_a + all[row] + __popc(__ballot_sync(0xffffffffu, isa) & lower);
-            const int before = g + min(e, room);  // kept pages before this one
-            if (isg || (ise && e < room)) {
-                if (before < p.N) kept[before] = page;
-            } else if (isa) {
-                freed[a - before] = table[page].x;
-                if (!p.plan) table[page].x = -1;
-            }
-        }
-        base_g += wsum[0];
-        base_e += wsum[1];
-        base_a += wsum[2];
-        __syncthreads();
     }
-    const int stay = base_g + min(base_e, room);
-    for (int k = stay + tid; k < p.N; k += ET) kept[k] = -1;
-    if (tid == 0) {
-        p.n_freed[i] = base_a - stay;
+
+    // each warp a run of rows of 32 pages: how many are above the border, on it, there at all
+    const int rows = (n + 31) / 32, row0 = rows * warp / NW, row1 = rows * (warp + 1) / NW;
+    int g_n = 0, e_n = 0, a_n = 0;
+    for (int row = row0; row < row1; ++row) {
+        const int k = 32 * row + lane;
+        const uint32_t x = k < n ? key(k) : ABSENT;
+        g_n += __popc(__ballot_sync(0xffffffffu, x > border));
+        e_n += __popc(__ballot_sync(0xffffffffu, x == border && x != ABSENT));
+        a_n += __popc(__ballot_sync(0xffffffffu, x != ABSENT));
+    }
+    __syncthreads();  // wsum has been read
+    if (lane < 3) wsum[warp][lane] = lane == 0 ? g_n : (lane == 1 ? e_n : a_n);
+    __syncthreads();
+    if (tid < 3 * G) {
+        int sum = 0;
+        for (int w = 0; w < NW; ++w) sum += wsum[w][tid % 3];
+        hs::dsmem_st(hs::dsmem_map(&parts[rank][tid % 3], (uint32_t)(tid / 3)), sum);
+    }
+    hs::cluster_arrive();
+    hs::cluster_wait();  // the last that any CTA reads or writes of another
+    int g = 0, e = 0, a = 0, g_all = 0, e_all = 0, a_all = 0;
+    for (int c = 0; c < G; ++c) {
+        if (c < rank) g += parts[c][0], e += parts[c][1], a += parts[c][2];
+        g_all += parts[c][0], e_all += parts[c][1], a_all += parts[c][2];
+    }
+    for (int w = 0; w < warp; ++w) g += wsum[w][0], e += wsum[w][1], a += wsum[w][2];
+    for (int row = row0; row < row1; ++row) {
+        const int k = 32 * row + lane, page = p0 + k;
+        const uint32_t x = k < n ? key(k) : ABSENT, lower = (1u << lane) - 1u;
+        const bool isg = x > border, ise = x == border && x != ABSENT, isa = x != ABSENT;
+        const uint32_t bg = __ballot_sync(0xffffffffu, isg), be = __ballot_sync(0xffffffffu, ise), ba = __ballot_sync(0xffffffffu, isa);
+        const int on = e + __popc(be & lower), before = g + __popc(bg & lower) + min(on, room);  // kept pages before this one
+        if (isg || (ise && on < room)) {
+            if (before < p.N) kept[before] = page;
+        } else if (isa) {
+            freed[a + __popc(ba & lower) - before] = table[page].x;
+            if (!p.plan) table[page].x = -1;
+        }
+        g += __popc(bg);
+        e += __popc(be);
+        a += __popc(ba);
+    }
+    const int stay = g_all + min(e_all, room);
+    for (int k = stay + rank * ET + tid; k < p.N; k += G * ET) kept[k] = -1;
+    if (rank == 0 && tid == 0) {
+        p.n_freed[i] = a_all - stay;
         if (stay > p.N) atomicOr(p.err, HS_DEVERR_CAPACITY);
     }
 }
@@ -246,18 +390,28 @@ extern "C" hs_status hs_evict_pages(hs_pool_t pool, int32_t n, int32_t N, int32_
     p.max_req = pool->cfg.max_requests;
     p.max_pages = pool->max_pages;
     p.max_ctx = pool->cfg.max_ctx;
-    p.cap = pool->max_pages < CAP ? pool->max_pages : CAP;
+    // CTAs of a cluster: one for 2,048 pages, up to eight
+    const int G = pool->max_pages <= 2048 ? 1 : (pool->max_pages <= 4096 ? 2 : (pool->max_pages <= 8192 ? 4 : MAXG));
+    const bool few = pool->max_pages <= ET;
+    if ((int64_t)n * G > INT32_MAX) return HS_ERR_INVALID_ARG;
+    const int64_t slice = ((int64_t)pool->max_pages + 32 * G - 1) / (32 * G) * 32;
+    p.cap = slice < CAP ? (int)slice : CAP;
     p.saved_only = flags & HS_EVICT_SAVED_ONLY;
     p.plan = flags & HS_EVICT_PLAN;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)n, 1, 1);
+    cfg.gridDim = dim3((unsigned)(few ? n : n * G), 1, 1);
     cfg.blockDim = dim3(ET, 1, 1);
-    cfg.dynamicSmemBytes = (size_t)p.cap * 4;
+    cfg.dynamicSmemBytes = few ? 0 : (size_t)p.cap * 4;
     cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)G;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, evict_kernel, p) == cudaSuccess ? HS_OK : HS_ERR_CUDA;
+    cfg.numAttrs = few ? 1 : 2;
+    return (few ? cudaLaunchKernelEx(&cfg, evict_few_kernel, p) : cudaLaunchKernelEx(&cfg, evict_kernel, p, G)) == cudaSuccess
+               ? HS_OK
+               : HS_ERR_CUDA;
 }
