@@ -224,6 +224,13 @@ __device__ __forceinline__ void add2(float &a, float &b, float c, float d) {
         : "+f"(a), "+f"(b)
         : "f"(c), "f"(d));
 }
+// a and b plus 0 times c and d: NaN where one is not finite
+__device__ __forceinline__ void zeros_of(float &a, float &b, float c, float d) {
+    asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n mov.b64 z, {%4, %4};\n"
+        " fma.rn.f32x2 x, y, z, x;\n mov.b64 {%0, %1}, x;\n}\n"
+        : "+f"(a), "+f"(b)
+        : "f"(c), "f"(d), "f"(0.f));
+}
 // Whether any of the softmax threads says so (named barrier 1).
 __device__ __forceinline__ bool any_softmax(bool x) {
     uint32_t r;
@@ -797,6 +804,14 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 mine = (uint32_t)(seen >> (KT * hf));
             }
             const bool hide = !__all_sync(0xffffffffu, mine == ~0u);
+            // BF16: a key that holds an infinity or NaN has no finite score, with any query
+            bool odd = false;
+            if (!FP8 && ok && tail) {
+                float z0 = 0.f, z1 = 0.f;
+#pragma unroll
+                for (int e = 0; e < KT; e += 2) zeros_of(z0, z1, s[e], s[e + 1]);
+                odd = !(z0 + z1 == 0.f);
+            }
             if (ok) {
                 if (hide) {
 #pragma unroll
@@ -830,8 +845,9 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             // outgrow its own, the rows' four maxima meet in shared memory.
             float alpha = 1.f;
             auto outgrown = [](float x, float ref) { return x > ref + TAU2<FP8> || (ref == -INFINITY && x != -INFINITY); };
-            const bool grow = any_softmax(outgrown(tmax, m2) || (FP8 && cmax > 2.f * cref));
+            const bool grow = any_softmax(outgrown(tmax, m2) || (FP8 && cmax > 2.f * cref) || odd);
             if (grow) {
+                if (!FP8) odd = any_softmax(odd);  // either half of the keys
                 st_shared_f1(xm + 4 * tid, tmax);
                 if (FP8) st_shared_f1(xm + 4 * (32 * NSW + tid), cmax);
                 named_bar_sync(1, 32 * NSW);
@@ -921,11 +937,13 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     st_shared_v4(pr + (((c + 4 * hf) ^ (row & 7)) << 4), pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
-                if (tail && !FP8) {
+                if (!FP8 && tail && odd) {
                     // A row that some query does not see may hold infinities or
                     // NaN, and 0 x NaN would reach that query's sum: in V they
                     // become zeros (a query that does see them has them in its
-                    // scores). The page's 32 KB, by its 128 threads.
+                    // scores). The page's 32 KB, by its 128 threads, where a score says so
+                    // (on every page that some query does not see all of, 4 of the 19 of
+                    // a window of 1,024, 2 x 1,999 tokens of 16 heads took 206 us instead of 145).
                     const uint32_t v0 = base + C::OFF_V + (j % C::NV) * 2 * NVC * CH + kh * NVC * CH + (row + 64 * hf) * 16;
 #pragma unroll 4
                     for (int u = 0; u < 16; ++u) {
