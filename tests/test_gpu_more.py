@@ -294,6 +294,28 @@ def test_weights_with_a_key_that_is_not_finite(dtype):
     c.close()
 
 
+@pytest.mark.parametrize("H", [40, 8, 32])
+def test_weights_with_a_key_of_no_weight_that_is_not_finite(H):
+    """An infinity that every query row meets with a negative value: scores of minus infinity,
+    a finite lse, and no weight."""
+    c = Cache("bf16", [400])
+    q = normal(25, 1, 1, H, P.DIM)
+    q[..., 0] = -1 - q[..., 0].abs()
+    rows = c.pool.gpu_rows()[c.row(0, 100)].view(torch.bfloat16)
+    rows[0] = math.inf
+    lse = lse_of(c, q)
+    assert bool(torch.isfinite(lse).all())
+    w = run_weights(c, q, lse)
+    kv = c.kv(0, range(400))
+    kv[100] = 0
+    seen = torch.ones(1, 400, dtype=torch.bool, device="cuda")
+    seen[0, 100] = False
+    want = M.page_weights(q[0].double(), lse[0].double(), kv, seen, SCALE)
+    tol = M.weights_tolerance(want, q[0].double(), lse[0].double(), kv, SCALE, False)
+    assert bool(((w[0].double() - want).abs() <= tol).all())
+    c.close()
+
+
 def test_weights_fp8_scales_of_many_magnitudes():
     c = Cache("fp8", [640])
     g = torch.Generator().manual_seed(19)

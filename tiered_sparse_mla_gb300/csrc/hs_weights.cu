@@ -27,6 +27,7 @@
 #include <atomic>
 #include <climits>
 #include <cstdint>
+#include <type_traits>
 
 #include "hs_internal.cuh"
 #include "hs_tc.cuh"
@@ -378,8 +379,7 @@ weight_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 const int m = g * MAXN + tid;
                 float v = tid < p.N && m < p.M ? p.lse[(size_t)w.b * p.M + m] : 0.f;
                 const bool fin = fabsf(v) < INFINITY;
-                // columns behind the last row too: a key that is not finite makes NaN of them
-                const uint32_t out = __ballot_sync(0xffffffffu, !fin || m >= p.M);
+                const uint32_t out = __ballot_sync(0xffffffffu, !fin);
                 if (seg > 0) named_bar_sync(1, 32 * NEW);
                 if (tid < p.N) st_shared_f1(head + C::OFF_B + 4 * tid, fin && m < p.M ? -v * 1.4426950408889634f : -INFINITY);
                 if (lane == 0) dead[warp - 2] = out;
@@ -476,7 +476,9 @@ weight_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                         HS_TMEM_LD32(tmem + lane_off + (i & 1) * (uint32_t)p.N + c0, d);
                         HS_TMEM_WAIT_LD32(d);
                         const uint32_t gone = dead[c0 >> 5];
-                        if (all && gone == 0) {
+                        // the columns that count: with a key that is not finite the others hold NaN
+                        const uint32_t live = ~gone & (c_hi - c0 < 32 ? (1u << (c_hi - c0)) - 1u : ~0u);
+                        auto sums = [&](auto whole) {
 #pragma unroll
                             for (int e = 0; e < 32; e += 4) {
                                 const float4 b = ld_shared_f4(head + C::OFF_B + 4 * (c0 + e));
@@ -490,9 +492,21 @@ weight_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                                 float x2 = __uint_as_float(d[e + 2]), x3 = __uint_as_float(d[e + 3]);
                                 fma2(x0, x1, a0, a1, b.x, b.y);
                                 fma2(x2, x3, a2, a3, b.z, b.w);
-                                add2(s0, s1, ex2(x0), ex2(x1));
-                                add2(s2, s3, ex2(x2), ex2(x3));
+                                float y0 = ex2(x0), y1 = ex2(x1), y2 = ex2(x2), y3 = ex2(x3);
+                                if (!decltype(whole)::value) {
+                                    y0 = (live >> e) & 1u ? y0 : 0.f;
+                                    y1 = (live >> (e + 1)) & 1u ? y1 : 0.f;
+                                    y2 = (live >> (e + 2)) & 1u ? y2 : 0.f;
+                                    y3 = (live >> (e + 3)) & 1u ? y3 : 0.f;
+                                }
+                                add2(s0, s1, y0, y1);
+                                add2(s2, s3, y2, y3);
                             }
+                        };
+                        if (all && live == ~0u) {
+                            sums(std::true_type{});
+                        } else if (all) {
+                            sums(std::false_type{});
                         } else {
                             int m = g * MAXN + c0, t = m / p.H, h = m - t * p.H;
                             auto sees = [&](int tt) {
@@ -507,7 +521,7 @@ weight_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                                 const float b = ld_shared_f1(head + C::OFF_B + 4 * (c0 + e));
                                 const float a = FP8 ? ks * ld_shared_f1(tab + 4 * (c0 + e)) : ks;
                                 const float y = ex2(fmaf(__uint_as_float(d[e]), a, b));
-                                s0 += seen && !((gone >> e) & 1u) ? y : 0.f;
+                                s0 += seen && ((live >> e) & 1u) ? y : 0.f;
                                 if (++h == p.H) {
                                     h = 0;
                                     seen = sees(++t);
