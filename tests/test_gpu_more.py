@@ -799,3 +799,36 @@ def test_refusals():
     assert all(bool((x == 7).all()) for x in (kept, freed, n, idx, cnt, nxt))
     long.close()
     c.close()
+
+
+@pytest.mark.parametrize("ctx,T,H,window,n_sink", [
+    ([900, 2], 700, 32, 100, 4), ([3000, 700, 900], 700, 24, 333, 0), ([5000], 1500, 16, 1, 0), ([1301, 1300, 1], 1300, 16, 64, 70),
+    ([2700, 650, 30, 0, 900], 600, 17, 500, 1), ([40, 600, 20000, 64], 600, 16, 5000, 64), ([300] * 160, 3, 40, 128, 2),
+    ([1] * 100 + [0] * 60 + [3000] * 10, 2, 64, 200, 2)])
+def test_window_units_one_after_the_other(ctx, T, H, window, n_sink):
+    """More units than two for each pair of CTAs: long ones, ones of a single step, and empty ones in
+    any order."""
+    B = len(ctx)
+    c = Cache("bf16", ctx)
+    q = normal(26, B, T, H, P.DIM)
+    out, lse = attend_window(c, q, window, n_sink)
+    tokens = sorted({0, 1, T // 3, T // 2, T - 2, T - 1}) if T > 3 else None
+    check_window(c, q, out, lse, window, n_sink, tokens=tokens)
+    for _ in range(3):
+        again = attend_window(c, q, window, n_sink)
+        assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    c.close()
+
+
+def test_window_units_one_after_the_other_with_unknown_requests():
+    B = 200
+    c = Cache("bf16", [500, 90, 0])
+    q = normal(27, B, 1, 128, P.DIM)
+    g = torch.Generator().manual_seed(28)
+    req = torch.randint(-1, 4, (B,), generator=g).to(torch.int32)
+    out, lse = attend_window(c, q, 100, 3, req=req.cuda())
+    known = [b for b in range(B) if 0 <= int(req[b]) < 3]
+    check_window(c, q[known], out[known], lse[known], 100, 3, req=[int(req[b]) for b in known])
+    rest = [b for b in range(B) if b not in known]
+    assert not out[rest].any() and bool((lse[rest] == -math.inf).all())
+    c.close(c.hs.HS_DEVERR_BAD_REQUEST)

@@ -123,7 +123,7 @@ struct PCfg {
     static constexpr int OFF_PG = OFF_WM + (FP8 ? RM * 4 : 0);            // int32 [NTI][2]
     static constexpr int OFF_BAR = (OFF_PG + NTI * 8 + 7) & ~7;
     static constexpr int B_QFULL = 0, B_QDONE = 1, B_QREADY = 2, B_SFULL = 3, B_SFREE = 4, B_PFULL = 5,
-                         B_PVDONE = 6, B_DRAIN = 7, B_JOIN = 8, B_TFULL = 9, B_TFREE = B_TFULL + NTI,
+                         B_PVDONE = 6, B_DRAIN = 7, B_JOIN = 8, B_EFREE = 9, B_TFULL = 10, B_TFREE = B_TFULL + NTI,
                          B_TREADY = B_TFREE + NTI, B_VFULL = B_TREADY + NTI, B_VFREE = B_VFULL + NV, B_XFULL = B_VFREE + NV,
                          B_XFREE = B_XFULL + NXG, B_CFULL = B_XFREE + NXG, B_CFREE = B_CFULL + NCV,
                          NBAR = B_CFREE + NCV;
@@ -159,6 +159,7 @@ struct PageParams {
     int ws_list0, ws_lists;  // the lists that the partials' space holds
     int tpl;               // lists per request: list i is token i % tpl of request i / tpl
     int window, n_sink;    // WIN
+    int units;             // LOOP
     float scale_log2;
 };
 
@@ -258,11 +259,12 @@ __device__ __noinline__ void rescale_o(uint32_t at, float alpha) {
     tmem_wait_st();
 }
 
-template <bool FP8, bool WIN>
+template <bool FP8, bool WIN, bool LOOP>
 __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
 page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k1,
                    const __grid_constant__ CUtensorMap tm_k2, const __grid_constant__ CUtensorMap tm_o,
                    const __grid_constant__ CUtensorMap tm_w, const PageParams p) {
+    static_assert(!LOOP || (!FP8 && WIN), "units one after the other");
     using C = PCfg<FP8>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = hs::smem_addr(smem_raw);
@@ -275,8 +277,8 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     // whole units first, then the others' splits
     const int pair = blockIdx.x >> 1, past = pair - p.n_full;
     const int nsplit = past < 0 ? 1 : p.nsplit, split = past < 0 ? 0 : past % p.nsplit;
-    const int unit = past < 0 ? pair : p.n_full + past / p.nsplit;
-    const int list = unit / p.mtiles, mt = unit - list * p.mtiles;
+    int unit = past < 0 ? pair : p.n_full + past / p.nsplit;
+    int list = unit / p.mtiles, mt = unit - list * p.mtiles;
     volatile int32_t *misc = reinterpret_cast<volatile int32_t *>(smem + C::OFF_MISC);
     volatile int32_t *ring_pg = reinterpret_cast<volatile int32_t *>(smem + C::OFF_PG);
     auto bar = [&](int i) { return base + C::OFF_BAR + 8u * (uint32_t)i; };
@@ -292,7 +294,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     if (warp == 1) {
         for (int i = lane; i < C::NBAR; i += 32) {
             uint32_t n = 1;
-            if (i == C::B_QDONE || (i >= C::B_TFREE && i < C::B_TFREE + NTI)) n = NSW;
+            if (i == C::B_QDONE || i == C::B_EFREE || (i >= C::B_TFREE && i < C::B_TFREE + NTI)) n = NSW;
             // both CTAs' softmax warps
             if (i == C::B_QREADY || i == C::B_SFREE || i == C::B_PFULL) n = 2 * NSW;
             // FP8: four converter warps of each CTA
@@ -328,8 +330,9 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     int e0 = -1;  // entry `lane`
     if (loader && entries && lane < p.N) e0 = entries[lane];
     const int req = p.req[list / p.tpl];
-    const bool req_ok = req >= 0 && req < p.max_req;
-    const int len = req_ok ? p.ctx[req] : 0, L = hs::context_within(len, p.max_ctx);
+    bool req_ok = req >= 0 && req < p.max_req;
+    const int len = req_ok ? p.ctx[req] : 0;
+    int L = hs::context_within(len, p.max_ctx);
     const int2 *table = p.table + (size_t)(req_ok ? req : 0) * p.max_pages;
     int nsteps = 0, first = 0, end = 0, npages = 0;
     int wskip = 0, wsinks = INT_MAX;  // WIN: entries from wsinks on are pages wskip later
@@ -356,6 +359,50 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
         }
     };
+    // WIN: the entries of this unit, from the number of the context's pages in `end`
+    auto window_pages = [&]() {
+        wsinks = INT_MAX;
+        wskip = 0;
+        if (end <= 0) return;
+        // The positions that some row sees: up to its last token's, and from its first
+        // token's window on (a tree's node may be as high up as the context's end).
+        const int t0 = p.tree ? -1 : mt * BM / p.H, t1 = p.tree ? p.T - 1 : (min(p.M, mt * BM + BM) - 1) / p.H;
+        const int top = L - p.T + t1, low = (int)max((long long)L - p.T + t0 - p.window + 1, 0ll);
+        end = top < 0 ? 0 : top / kPage + 1;
+        const int sinks = min((int)(((long long)p.n_sink + kPage - 1) / kPage), end);
+        if (low / kPage > sinks) {
+            wsinks = sinks;
+            wskip = low / kPage - sinks;
+            end -= wskip;
+        }
+    };
+    // LOOP: this pair's units are `gridDim.x / 2` apart. Each role walks them for itself: `it`
+    // counts them and g0 the steps before this one's; the barriers' phases run on. The next
+    // one's request is looked up a unit ahead.
+    int it = 0, g0 = 0, req_next = 0, len_next = 0;
+    auto peek = [&]() {
+        const int u = unit + (int)(gridDim.x >> 1);
+        if (!LOOP || u >= p.units) return;
+        req_next = p.req[u / p.mtiles];
+        len_next = req_next >= 0 && req_next < p.max_req ? p.ctx[req_next] : 0;
+    };
+    auto enter_next = [&]() {  // false: there is none
+        if (!LOOP || unit + (int)(gridDim.x >> 1) >= p.units) return false;
+        unit += (int)(gridDim.x >> 1);
+        list = unit / p.mtiles;
+        mt = unit - list * p.mtiles;
+        req_ok = req_next >= 0 && req_next < p.max_req;
+        L = hs::context_within(len_next, p.max_ctx);
+        table = p.table + (size_t)(req_ok ? req_next : 0) * p.max_pages;
+        if (!req_ok) bad |= HS_DEVERR_BAD_REQUEST;
+        if (len_next > p.max_ctx) bad |= HS_DEVERR_INDEX_RANGE;
+        g0 += nsteps;
+        ++it;
+        npages = end = L <= 0 ? 0 : (L - 1) / kPage + 1;
+        window_pages();
+        nsteps = (end + 1) / 2;
+        return true;
+    };
     int npg = -1, nblk = p.zero_block;
     if (loader) {
         // the list's end: past its last entry that names a page
@@ -367,19 +414,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         } else {
             end = L <= 0 ? 0 : (L - 1) / kPage + 1;
         }
-        if (WIN && end > 0) {
-            // The positions that some row sees: up to its last token's, and from its first
-            // token's window on (a tree's node may be as high up as the context's end).
-            const int t0 = p.tree ? -1 : mt * BM / p.H, t1 = p.tree ? p.T - 1 : (min(p.M, mt * BM + BM) - 1) / p.H;
-            const int top = L - p.T + t1, low = (int)max((long long)L - p.T + t0 - p.window + 1, 0ll);
-            end = top < 0 ? 0 : top / kPage + 1;
-            const int sinks = min((int)(((long long)p.n_sink + kPage - 1) / kPage), end);
-            if (low / kPage > sinks) {
-                wsinks = sinks;
-                wskip = low / kPage - sinks;
-                end -= wskip;
-            }
-        }
+        if (WIN) window_pages();
         // splits begin at even entries: a step is two pages
         const long long steps = (end + 1) / 2;
         const int z = (int)(steps * (split + 1) / nsplit);
@@ -408,7 +443,28 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         int pg, blk;
         int ul = 0, ut = 0, ux = 0;  // loads, steps and (BF16) rope loads begun
         bool ok = true;
+        if (LOOP && !req_ok) bad |= HS_DEVERR_BAD_REQUEST;
+        do {
+        peek();
+        if (LOOP && it > 0) {
+            fetch(0, npg, nblk);
+            if (lane == 0 && !kw) {
+                // Q goes where this unit's first V will: free once the step before the last
+                // is done with it; the chunks that stay, once the last scores are.
+                const int s = g0 % C::NV;
+                ok = mbar_wait_inline(bar(C::B_VFREE + s), ((uint32_t)(g0 / C::NV) & 1u) ^ 1u);
+                if (ok && g0 > 0) ok = mbar_wait_inline(bar(C::B_SFULL), (uint32_t)(g0 - 1) & 1u);
+                if (ok) {
+                    mbar_expect_tx(bar(C::B_QFULL), NK * CH);
+                    for (int i = 0; i < NK; ++i)
+                        tma_load_3d(i < NQT ? base + C::OFF_V + s * 2 * NVC * CH + i * CH : base + C::OFF_Q + (i - NQT) * CH,
+                                    &tm_q, 64 * i, mt * BM + RM * rank, list, bar(C::B_QFULL));
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+        }
         for (int j = 0; j < nsteps && ok; ++j) {
+            const int gj = g0 + j;
             if (j % 16 == 0) {
                 pg = npg;
                 blk = nblk;
@@ -419,8 +475,8 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const int row0 = __shfl_sync(0xffffffffu, blk, src) * kPage;
             const int row1 = __shfl_sync(0xffffffffu, blk, src + 1) * kPage;
             if (lane == 0 && kw) {
-                const int own = rank ? row1 : row0, ti = j % NTI;
-                ok = mbar_wait_inline(bar(C::B_TFREE + ti), ((uint32_t)(j / NTI) & 1u) ^ 1u);
+                const int own = rank ? row1 : row0, ti = gj % NTI;
+                ok = mbar_wait_inline(bar(C::B_TFREE + ti), ((uint32_t)(gj / NTI) & 1u) ^ 1u);
                 if (ok) {
                     ring_pg[2 * ti] = pg0;
                     ring_pg[2 * ti + 1] = pg1;
@@ -432,7 +488,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     } else {
                         mbar_arrive(bar(C::B_TFULL + ti));
                     }
-                    ut = j + 1;
+                    ut = gj + 1;
                 }
                 // both CTAs' bytes complete on CTA 0's barrier
                 if (FP8) {
@@ -444,11 +500,11 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         tma_load_pair(base + C::OFF_X + s * C::GK * CCH, &tm_k1, 0, own, i, lead(C::B_XFULL + s));
                     }
                 } else {
-                    if (ok) ok = mbar_wait_inline(bar(C::B_XFREE), ((uint32_t)j & 1u) ^ 1u);
+                    if (ok) ok = mbar_wait_inline(bar(C::B_XFREE), ((uint32_t)gj & 1u) ^ 1u);
                     if (ok) {
                         if (rank == 0) mbar_expect_tx(bar(C::B_XFULL), 2 * CH);
                         tma_load_pair(base + C::OFF_X, &tm_k1, 0, own, 8, lead(C::B_XFULL));
-                        ux = j + 1;
+                        ux = gj + 1;
                     }
                     for (int i = 0; i < 8 && ok; i += 2, ++ul) {
                         const int s = 1 + ul % C::RK;
@@ -470,9 +526,12 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         tma_load_3d(dst + 2 * CCH, &tm_k2, 0, row1, 4 * i + 2 * rank, bar(C::B_CFULL + cs));
                     }
                 } else {
-                    const int s = j % C::RV;
-                    if (j == 1) ok = mbar_wait_inline(bar(C::B_QDONE), 0);  // Q was staged there
-                    if (ok) ok = mbar_wait_inline(bar(C::B_VFREE + s), ((uint32_t)(j / C::RV) & 1u) ^ 1u);
+                    const int s = gj % C::RV;
+                    if (j == 1 && it == 0) ok = mbar_wait_inline(bar(C::B_QDONE), 0);  // Q was staged there
+                    if (LOOP && j == 0 && it > 0) ok = mbar_wait_inline(bar(C::B_QDONE), (uint32_t)it & 1u);
+                    // the last unit's output was
+                    if (LOOP && j == 1 && it > 0) ok = mbar_wait_inline(bar(C::B_EFREE), (uint32_t)(it - 1) & 1u);
+                    if (ok) ok = mbar_wait_inline(bar(C::B_VFREE + s), ((uint32_t)(gj / C::RV) & 1u) ^ 1u);
                     if (ok) {
                         const uint32_t dst = base + C::OFF_V + s * 2 * NVC * CH;
                         mbar_expect_tx(bar(C::B_VFULL + s), 2 * NVC * CH);
@@ -480,15 +539,30 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         tma_load_3d(dst + 2 * CH, &tm_k2, 0, row0, 4 + 2 * rank, bar(C::B_VFULL + s));
                         tma_load_3d(dst + 4 * CH, &tm_k2, 0, row1, 2 * rank, bar(C::B_VFULL + s));
                         tma_load_3d(dst + 6 * CH, &tm_k2, 0, row1, 4 + 2 * rank, bar(C::B_VFULL + s));
-                        ul = j + 1;
+                        ul = gj + 1;
                     }
                 }
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
         }
+        if (LOOP && lane == 0 && !kw && ok && unit + (int)(gridDim.x >> 1) < p.units) {
+            // Each phase is waited for once, in order: those that short units have left.
+            // (Behind the last unit nothing holds the next phase back.)
+            if (it == 0 && nsteps < 2) ok = mbar_wait_inline(bar(C::B_QDONE), 0);
+            if (it > 0 && nsteps == 0) ok = mbar_wait_inline(bar(C::B_QDONE), (uint32_t)it & 1u);
+            if (ok && it > 0 && nsteps < 2) ok = mbar_wait_inline(bar(C::B_EFREE), (uint32_t)(it - 1) & 1u);
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        } while (ok && enter_next());
+        if (LOOP && lane == 0 && ok) {
+            // what the MMA issuer says of the last loads: on its way until it is here
+            const int ring = kw ? C::RK : C::RV, b0 = kw ? C::B_XFREE + 1 : C::B_VFREE;
+            for (int i = ul - 1; i >= 0 && i >= ul - ring; --i) mbar_wait_inline(bar(b0 + i % ring), (uint32_t)(i / ring) & 1u);
+            if (kw && ux > 0) mbar_wait_inline(bar(C::B_XFREE), (uint32_t)(ux - 1) & 1u);
+        }
         if (lane == 0) {
             // the copies begun have landed before the CTA may end
-            if (kw) mbar_wait_inline(bar(C::B_QFULL), 0);
+            if (LOOP ? !kw : kw) mbar_wait_inline(bar(C::B_QFULL), (uint32_t)it & 1u);
             if (!ok) {
                 fail();
                 const int ring = kw ? C::RK : C::RV;
@@ -502,24 +576,24 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         bad = __reduce_or_sync(0xffffffffu, bad);
         if (lane == 0 && kw) {
-            if (!req_ok) bad = HS_DEVERR_BAD_REQUEST;  // it has no context that an entry could lie outside of
+            if (!LOOP && !req_ok) bad = HS_DEVERR_BAD_REQUEST;  // it has no context that an entry could lie outside of
             if (bad) atomicOr(p.err, bad);
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer (CTA 0)
-        if (rank == 0 && nsteps > 0) {
+        if (rank == 0 && (LOOP || nsteps > 0)) {
             constexpr uint32_t ID_QK = idesc_f16(FP8 ? 0u : 1u, 0, BM, 128), ID_PV = idesc_f16(FP8 ? 0u : 1u, 1, BM, 256);
             const uint64_t dk = desc_sw128(base, 16, 1024), dv = desc_sw128(base, CH, 1024);
             const uint32_t hi = (uint32_t)(dk >> 32), klo = (uint32_t)dk, vlo = (uint32_t)dv;
             const uint32_t chi = (uint32_t)(desc_sw64(base, 16, 512) >> 32);  // K's codes
             const uint32_t leader = elect_one();
-            bool ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_QREADY), 0));
-            tc_fence_after();
+            bool ok = true;
             auto pv = [&](int j) {
-                ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_PFULL), (uint32_t)j & 1u));
+                const int gj = g0 + j;
+                ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_PFULL), (uint32_t)gj & 1u));
                 if (!ok) return;
                 tc_fence_after();
-                const uint32_t v = vlo + ((C::OFF_V + (FP8 ? 0 : j % C::NV) * 2 * NVC * CH) >> 4);
+                const uint32_t v = vlo + ((C::OFF_V + (FP8 ? 0 : gj % C::NV) * 2 * NVC * CH) >> 4);
                 const uint32_t a = klo + (C::OFF_P >> 4);
 #pragma unroll
                 for (int nh = 0; nh < 2; ++nh) {  // 256 value columns each
@@ -537,7 +611,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                                         v + ((pgi * NVC * CH + nh * 2 * CH + 2048 * k) >> 4), hi, ID_PV,
                                         (j | pgi | k) != 0);
                         if (FP8 && j + 1 < nsteps) commit_both(bar(C::B_VFREE + nh), both);
-                        if (!FP8 && nh == 1 && j + C::NV < nsteps) commit_both(bar(C::B_VFREE + j % C::NV), both);
+                        if (!FP8 && nh == 1 && (LOOP || j + C::NV < nsteps)) commit_both(bar(C::B_VFREE + gj % C::NV), both);
                         if (nh == 1) commit_both(bar(C::B_PVDONE), both);
                     }
                     __syncwarp();
@@ -547,8 +621,13 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             constexpr int PER = FP8 ? NK / C::GK : 8 / C::GK;  // groups of K chunks per step
             int s = 0;
             uint32_t ph = 0;
+            do {
+            peek();
+            ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_QREADY), (uint32_t)it & 1u));
+            tc_fence_after();
             for (int j = 0; j < nsteps && ok; ++j) {
-                if (j > 0) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_SFREE), (uint32_t)(j - 1) & 1u));
+                const int gj = g0 + j;
+                if (gj > 0) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_SFREE), (uint32_t)(gj - 1) & 1u));
                 tc_fence_after();
                 auto qk = [&](int c, uint32_t slot, bool fresh) {  // one chunk: four MMAs
                     const uint32_t kd = klo + ((C::OFF_X + slot * (FP8 ? CCH : CH)) >> 4);
@@ -567,12 +646,12 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     }
                 };
                 if (!FP8) {
-                    if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_XFULL), (uint32_t)j & 1u));
+                    if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_XFULL), (uint32_t)gj & 1u));
                     if (!ok) break;
                     tc_fence_after();
                     if (leader) {
                         qk(8, 0, true);
-                        if (j + 1 < nsteps) commit_both(bar(C::B_XFREE), both);
+                        if (LOOP || j + 1 < nsteps) commit_both(bar(C::B_XFREE), both);
                     }
                     __syncwarp();
                 }
@@ -585,7 +664,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         if (leader) {
 #pragma unroll
                             for (int g = 0; g < C::GK; ++g) qk(c + g, (FP8 ? s * C::GK : 1 + 2 * s) + g, FP8 && c + g == 0);
-                            if (PER * j + c / C::GK + C::RK < PER * nsteps) commit_both(bar(C::B_XFREE + b0), both);
+                            if (LOOP || PER * j + c / C::GK + C::RK < PER * nsteps) commit_both(bar(C::B_XFREE + b0), both);
                         }
                         __syncwarp();
                     }
@@ -599,7 +678,11 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 __syncwarp();
                 if (j > 0) pv(j - 1);
             }
-            if (ok) pv(nsteps - 1);
+            if (ok && (!LOOP || nsteps > 0)) pv(nsteps - 1);
+            } while (ok && enter_next());
+            // LOOP: the last arrives of both CTAs are here
+            if (LOOP && ok && g0 + nsteps > 0)
+                ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_SFREE), (uint32_t)(g0 + nsteps - 1) & 1u));
             if (!ok && lane == 0) fail();
             if (leader) {
                 // every MMA issued has finished before shared and tensor memory go
@@ -719,12 +802,17 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
             tmem_wait_st();
         }
-        fence_proxy_async();  // the staging space is refilled next
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(C::B_QDONE));
-        if (nsteps > 0) arrive_lead(lead(C::B_QREADY));
+        auto q_moved = [&]() {
+            fence_proxy_async();  // the staging space is refilled next
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::B_QDONE));
+            if (LOOP || nsteps > 0) arrive_lead(lead(C::B_QREADY));
+        };
+        q_moved();
 
+        do {
+        peek();
         // this row's query token and its mask
         const int mg = mt * BM + RM * rank + row;
         const bool vrow = mg < p.M;
@@ -745,12 +833,12 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         if (FP8 && tid < RM) st_shared_f1(wm, 0.f);  // read behind a barrier
         const float row_scale = p.scale_log2 * q_back;
         for (int j = 0; j < nsteps; ++j) {
-            const int ti = j % NTI;
+            const int gj = g0 + j, ti = gj % NTI;
             float s[KT];
             const uint32_t sc_at = base + C::OFF_SC + ti * 512 + kh * 256 + hf * 128;
             if (ok)
-                ok = __all_sync(0xffffffffu, mbar_wait_inline(bar((FP8 ? C::B_TREADY : C::B_TFULL) + ti), (uint32_t)(j / NTI) & 1u) &&
-                                                 mbar_wait_inline(bar(C::B_SFULL), (uint32_t)j & 1u));
+                ok = __all_sync(0xffffffffu, mbar_wait_inline(bar((FP8 ? C::B_TREADY : C::B_TFULL) + ti), (uint32_t)(gj / NTI) & 1u) &&
+                                                 mbar_wait_inline(bar(C::B_SFULL), (uint32_t)gj & 1u));
             if (ok) {
                 tc_fence_after();
                 uint32_t ra[32];
@@ -772,7 +860,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
             }
             tc_fence_before();
-            if (j + 1 < nsteps) arrive_lead(lead(C::B_SFREE));  // S_{j+1} may be written
+            if (LOOP || j + 1 < nsteps) arrive_lead(lead(C::B_SFREE));  // S_{j+1} may be written
             const int pg = ok ? (int)ld_shared_b32(base + C::OFF_PG + 4 * (2 * ti + kh)) : -1;
             // the keys that this row sees, as bits
             const int d = draft - max(pg, 0) * kPage;  // the first query token's position in the page
@@ -928,9 +1016,9 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (lane == 0) mbar_arrive(bar(C::B_TFREE + ti));
             // P and O are free once the previous PV is done; BF16: this CTA's V has
             // landed (FP8: its converters tell the MMA issuer themselves)
-            if (ok && j > 0) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_PVDONE), (uint32_t)(j - 1) & 1u));
+            if (ok && j > 0) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_PVDONE), (uint32_t)(gj - 1) & 1u));
             if (ok && !FP8)
-                ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_VFULL + j % C::NV), (uint32_t)(j / C::NV) & 1u));
+                ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_VFULL + gj % C::NV), (uint32_t)(gj / C::NV) & 1u));
             if (ok) {
                 tc_fence_after();
                 const uint32_t pr = base + C::OFF_P + kh * CH + row * 128;
@@ -944,7 +1032,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     // scores). The page's 32 KB, by its 128 threads, where a score says so
                     // (on every page that some query does not see all of, 4 of the 19 of
                     // a window of 1,024, 2 x 1,999 tokens of 16 heads took 206 us instead of 145).
-                    const uint32_t v0 = base + C::OFF_V + (j % C::NV) * 2 * NVC * CH + kh * NVC * CH + (row + 64 * hf) * 16;
+                    const uint32_t v0 = base + C::OFF_V + (gj % C::NV) * 2 * NVC * CH + kh * NVC * CH + (row + 64 * hf) * 16;
 #pragma unroll 4
                     for (int u = 0; u < 16; ++u) {
                         const uint4 v = ld_shared_v4(v0 + 2048 * u);
@@ -966,8 +1054,31 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             tc_fence_before();
             arrive_lead(lead(C::B_PFULL));
         }
+        // LOOP: the next unit's Q into tensor memory while the last PV runs, so that its first
+        // scores are multiplied during this unit's epilogue
+        const int g1 = g0 + nsteps;
+        if (LOOP && unit + (int)(gridDim.x >> 1) < p.units) {
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_QFULL), (uint32_t)(it + 1) & 1u));
+            if (ok) {
+#pragma unroll 1
+                for (int i = hf; i < NQT; i += 2) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        const uint4 v = ld_shared_v4(base + C::OFF_V + (g1 % C::NV) * 2 * NVC * CH + i * CH + row * 128 + ((u ^ (row & 7)) << 4));
+                        w[4 * u] = v.x;
+                        w[4 * u + 1] = v.y;
+                        w[4 * u + 2] = v.z;
+                        w[4 * u + 3] = v.w;
+                    }
+                    HS_TMEM_ST32(tmem + lane_off + TM_Q + 32u * i, w);
+                }
+                tmem_wait_st();
+            }
+            q_moved();
+        }
         if (ok && nsteps > 0) {
-            ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_PVDONE), (uint32_t)(nsteps - 1) & 1u));
+            ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_PVDONE), (uint32_t)(g1 - 1) & 1u));
             tc_fence_after();
         }
         if (!ok && lane == 0) fail();
@@ -994,7 +1105,9 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             // swizzled bytes per row: this thread's value columns are
             // 256 hf + 128 kh + (0..127). Rows past M are clipped by the map.
             const int wr = wq & 1;  // which 32 rows
-            const uint32_t st0 = base + C::OFF_V + wr * 4096 + (uint32_t)(row & 31) * 128u;
+            // LOOP: the buffer that the next unit's Q and first V are not in
+            const uint32_t stage = base + C::OFF_V + (LOOP ? ((g1 + 1) % C::NV) * 2 * NVC * CH : 0);
+            const uint32_t st0 = stage + wr * 4096 + (uint32_t)(row & 31) * 128u;
 #pragma unroll 1
             for (int cc = 0; cc < 4; ++cc) {
                 uint32_t o[32];
@@ -1042,7 +1155,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     __syncwarp();
                     if (lane == 0) {
                         const int box = one ? col >> 6 : col >> 5;
-                        tma_store_3d(one ? &tm_o : &tm_w, base + C::OFF_V + (uint32_t)box * 8192u + wr * 4096,
+                        tma_store_3d(one ? &tm_o : &tm_w, stage + (uint32_t)box * 8192u + wr * 4096,
                                      one ? 64 * box : 32 * box, mt * BM + RM * rank + 32 * wr,
                                      one ? list : split * p.ws_lists + list - p.ws_list0);
                         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
@@ -1062,6 +1175,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             else
                 st_shared_f1(base + C::OFF_P + 4 * row, lse);  // P is done with
         }
+        if (LOOP && lane == 0) mbar_arrive(bar(C::B_EFREE));
         if (p.inside && kh == 0 && hf == 0) {
             fence_proxy_async();
             __syncwarp();
@@ -1070,6 +1184,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 bulk_push(cluster_address(base + C::OFF_P + 1024 + wr * 128, other), base + C::OFF_P + wr * 128, 128, theirs);
             __syncwarp();
         }
+        } while (enter_next());
     } else if (FP8 && warp >= 4 + NSW) {
         // ------------------------------------------------------------ converters
         // Half of V's columns at a time; the next half's codes are loaded while its buffer
@@ -1254,6 +1369,8 @@ struct PagePlan {
     size_t ws_o_bytes, ws_bytes;
 };
 
+int64_t pairs_at_once() { return sm_count() / 2 > 0 ? sm_count() / 2 : 1; }
+
 // A model of the launch's time, in us: two pages take a pair of CTAs about 1.6,
 // their start and epilogue 7.
 constexpr double US_STEP = 1.6, US_ENDS = 7.0;
@@ -1268,7 +1385,7 @@ PagePlan page_plan(int64_t lists, int64_t T, int64_t H, int64_t N) {
     PagePlan pl{};
     pl.M = (int)(T * H);
     pl.mtiles = (pl.M + BM - 1) / BM;
-    const int64_t pairs = sm_count() / 2 > 0 ? sm_count() / 2 : 1, units = lists * pl.mtiles;
+    const int64_t pairs = pairs_at_once(), units = lists * pl.mtiles;
     const int64_t steps = (N + 1) / 2, most = steps < 128 ? steps : 128;
     pl.us = 1e300;
     pl.nsplit = 1;
@@ -1330,7 +1447,7 @@ int clusters_of_four(int dev) {
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&n, page_decode_kernel<FP8, WIN>, &cfg) != cudaSuccess) {
+        if (cudaOccupancyMaxActiveClusters(&n, page_decode_kernel<FP8, WIN, false>, &cfg) != cudaSuccess) {
             cudaGetLastError();
             n = 0;
         }
@@ -1340,13 +1457,13 @@ int clusters_of_four(int dev) {
     return n;
 }
 
-template <bool FP8, bool WIN>
+template <bool FP8, bool WIN, bool LOOP>
 hs_status launch_pages(int dev, cudaStream_t s, const CUtensorMap &tq, const CUtensorMap &k1,
                        const CUtensorMap &k2, int64_t units, const void *d_out, void *ws, const PagePlan &pl, PageParams p) {
     static std::atomic<int> state[64];
     if (dev < 0 || dev >= 64) return HS_ERR_UNSUPPORTED;
     if (state[dev].load(std::memory_order_acquire) != 1) {
-        HS_CUDA_TRY(cudaFuncSetAttribute(page_decode_kernel<FP8, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        HS_CUDA_TRY(cudaFuncSetAttribute(page_decode_kernel<FP8, WIN, LOOP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          PCfg<FP8>::SMEM_ALLOC));
         state[dev].store(1, std::memory_order_release);
     }
@@ -1374,6 +1491,10 @@ hs_status launch_pages(int dev, cudaStream_t s, const CUtensorMap &tq, const CUt
     if (!split) tw = to;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * (p.n_full + (units - p.n_full) * p.nsplit)), 1, 1);
+    if (LOOP) {
+        cfg.gridDim.x = (unsigned)(2 * pairs_at_once());
+        p.units = (int)units;
+    }
     cfg.blockDim = dim3(PCfg<FP8>::THREADS, 1, 1);
     cfg.dynamicSmemBytes = PCfg<FP8>::SMEM_ALLOC;
     cfg.stream = s;
@@ -1386,7 +1507,7 @@ hs_status launch_pages(int dev, cudaStream_t s, const CUtensorMap &tq, const CUt
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, page_decode_kernel<FP8, WIN>, tq, k1, k2, to, tw, p) != cudaSuccess) return HS_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, page_decode_kernel<FP8, WIN, LOOP>, tq, k1, k2, to, tw, p) != cudaSuccess) return HS_ERR_CUDA;
     if (!split) return HS_OK;
     const int n = p.ws_lists * pl.M, skip = (p.n_full % pl.mtiles) * BM;
     cudaLaunchConfig_t cc = {};
@@ -1420,6 +1541,22 @@ int64_t window_pages(const hs_pool *pool, int64_t T, int64_t H, int64_t window, 
     return n < pool->max_pages ? n : pool->max_pages;
 }
 
+// Windows over BF16 rows with two units or more for each pair of CTAs: a pair takes them one
+// after the other and none is split. The next unit's queries and keys come, and its first
+// scores are multiplied, during the last one's end: 2 x 1,999 tokens of 16 heads, windows of
+// 1,024, LOOP_US against 145 us with a launch of its own for each unit (which takes 3 of a
+// unit's 20 us, and nothing runs while it ends).
+PagePlan window_plan(bool fp8, int64_t lists, int64_t T, int64_t H, int64_t N, bool &loop) {
+    const int64_t mtiles = (T * H + BM - 1) / BM;
+    loop = !fp8 && lists * mtiles >= 2 * pairs_at_once();
+    if (!loop) return page_plan(lists, T, H, N);
+    PagePlan pl{};
+    pl.M = (int)(T * H);
+    pl.mtiles = (int)mtiles;
+    pl.nsplit = 1;
+    return pl;
+}
+
 // `lists` lists of T query tokens each; tpl > 1 (with T = 1): lists / tpl
 // requests whose tpl tokens each have their own list. window > 0: N pages a unit at most.
 hs_status page_entry(hs_pool_t pool, int64_t lists, int32_t T, int32_t tpl, int32_t H, int32_t N,
@@ -1435,7 +1572,8 @@ hs_status page_entry(hs_pool_t pool, int64_t lists, int32_t T, int32_t tpl, int3
     HS_CUDA_TRY(cudaGetDevice(&dev));
     if (dev != pool->device) return HS_ERR_INVALID_ARG;
     const bool fp8 = pool->cfg.dtype == HS_FP8_E4M3_ROWSCALE;
-    const PagePlan pl = page_plan(lists, T, H, N < 1 ? pool->max_pages : N);
+    bool loop = false;
+    const PagePlan pl = window > 0 ? window_plan(fp8, lists, T, H, N, loop) : page_plan(lists, T, H, N < 1 ? pool->max_pages : N);
     if (pl.nsplit > 1 && (!d_workspace || ws_bytes < pl.ws_bytes || ((uintptr_t)d_workspace & 255u)))
         return HS_ERR_INVALID_ARG;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1485,11 +1623,9 @@ hs_status page_entry(hs_pool_t pool, int64_t lists, int32_t T, int32_t tpl, int3
     p.n_sink = n_sink;
     p.scale_log2 = sm_scale * 1.4426950408889634f;
     const int64_t units = lists * pl.mtiles;
-    if (window > 0)
-        return fp8 ? launch_pages<true, true>(dev, s, tq, maps[0], maps[1], units, d_out, d_workspace, pl, p)
-                   : launch_pages<false, true>(dev, s, tq, maps[0], maps[1], units, d_out, d_workspace, pl, p);
-    return fp8 ? launch_pages<true, false>(dev, s, tq, maps[0], maps[1], units, d_out, d_workspace, pl, p)
-               : launch_pages<false, false>(dev, s, tq, maps[0], maps[1], units, d_out, d_workspace, pl, p);
+    auto launch = window > 0 ? (fp8 ? launch_pages<true, true, false> : (loop ? launch_pages<false, true, true> : launch_pages<false, true, false>))
+                             : (fp8 ? launch_pages<true, false, false> : launch_pages<false, false, false>);
+    return launch(dev, s, tq, maps[0], maps[1], units, d_out, d_workspace, pl, p);
 }
 
 }  // namespace
@@ -1521,7 +1657,8 @@ extern "C" hs_status hs_page_mla_decode_per_token(hs_pool_t pool, int32_t B, int
 extern "C" size_t hs_window_workspace_bytes(hs_pool_t pool, int32_t B, int32_t T, int32_t H, int32_t window,
                                             int32_t n_sink) {
     if (!pool || B < 1 || !takes(B, T, H) || window < 1 || n_sink < 0) return 0;
-    return page_plan(B, T, H, window_pages(pool, T, H, window, n_sink)).ws_bytes;
+    bool loop;
+    return window_plan(pool->cfg.dtype == HS_FP8_E4M3_ROWSCALE, B, T, H, window_pages(pool, T, H, window, n_sink), loop).ws_bytes;
 }
 
 extern "C" hs_status hs_page_mla_decode_window(hs_pool_t pool, int32_t B, int32_t T, int32_t H, int32_t window,
