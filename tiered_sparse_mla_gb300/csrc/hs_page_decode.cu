@@ -160,6 +160,7 @@ struct PageParams {
     int tpl;               // lists per request: list i is token i % tpl of request i / tpl
     int window, n_sink;    // WIN
     int units;             // LOOP
+    const uint8_t *q;
     float scale_log2;
 };
 
@@ -359,47 +360,62 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
         }
     };
-    // WIN: the entries of this unit, from the number of the context's pages in `end`
-    auto window_pages = [&]() {
-        wsinks = INT_MAX;
-        wskip = 0;
-        if (end <= 0) return;
+    // WIN: a unit's entries, of the context's pages `e`; the others are left out
+    auto window_pages = [&](int len_u, int mt_u, int &e, int &sinks_u, int &skip_u) {
+        sinks_u = INT_MAX;
+        skip_u = 0;
+        if (e <= 0) return;
         // The positions that some row sees: up to its last token's, and from its first
         // token's window on (a tree's node may be as high up as the context's end).
-        const int t0 = p.tree ? -1 : mt * BM / p.H, t1 = p.tree ? p.T - 1 : (min(p.M, mt * BM + BM) - 1) / p.H;
-        const int top = L - p.T + t1, low = (int)max((long long)L - p.T + t0 - p.window + 1, 0ll);
-        end = top < 0 ? 0 : top / kPage + 1;
-        const int sinks = min((int)(((long long)p.n_sink + kPage - 1) / kPage), end);
+        const int t0 = p.tree ? -1 : mt_u * BM / p.H, t1 = p.tree ? p.T - 1 : (min(p.M, mt_u * BM + BM) - 1) / p.H;
+        const int top = len_u - p.T + t1, low = (int)max((long long)len_u - p.T + t0 - p.window + 1, 0ll);
+        e = top < 0 ? 0 : top / kPage + 1;
+        const int sinks = min((int)(((long long)p.n_sink + kPage - 1) / kPage), e);
         if (low / kPage > sinks) {
-            wsinks = sinks;
-            wskip = low / kPage - sinks;
-            end -= wskip;
+            sinks_u = sinks;
+            skip_u = low / kPage - sinks;
+            e -= skip_u;
         }
     };
-    // LOOP: this pair's units are `gridDim.x / 2` apart. Each role walks them for itself: `it`
-    // counts them and g0 the steps before this one's; the barriers' phases run on. The next
-    // one's request is looked up a unit ahead.
+    // LOOP: this pair's units are `apart`. Each role walks them for itself: `it` counts them and
+    // g0 the steps before this one's; the barriers' phases run on. The next one is looked up
+    // (peek), and worked out (look), while this one runs.
+    const int apart = (int)(gridDim.x >> 1);
     int it = 0, g0 = 0, req_next = 0, len_next = 0;
+    struct {
+        int list, mt, L, end, npages, sinks, skip;
+        bool there, ok;
+    } nx{};
     auto peek = [&]() {
-        const int u = unit + (int)(gridDim.x >> 1);
-        if (!LOOP || u >= p.units) return;
-        req_next = p.req[u / p.mtiles];
+        nx.there = LOOP && unit + apart < p.units;
+        if (!nx.there) return;
+        nx.list = (unit + apart) / p.mtiles;
+        req_next = p.req[nx.list];
         len_next = req_next >= 0 && req_next < p.max_req ? p.ctx[req_next] : 0;
     };
-    auto enter_next = [&]() {  // false: there is none
-        if (!LOOP || unit + (int)(gridDim.x >> 1) >= p.units) return false;
-        unit += (int)(gridDim.x >> 1);
-        list = unit / p.mtiles;
-        mt = unit - list * p.mtiles;
-        req_ok = req_next >= 0 && req_next < p.max_req;
-        L = hs::context_within(len_next, p.max_ctx);
-        table = p.table + (size_t)(req_ok ? req_next : 0) * p.max_pages;
-        if (!req_ok) bad |= HS_DEVERR_BAD_REQUEST;
+    auto look = [&]() {
+        if (!nx.there) return;
+        nx.mt = unit + apart - nx.list * p.mtiles;
+        nx.ok = req_next >= 0 && req_next < p.max_req;
+        if (!nx.ok) bad |= HS_DEVERR_BAD_REQUEST;
         if (len_next > p.max_ctx) bad |= HS_DEVERR_INDEX_RANGE;
+        nx.L = hs::context_within(len_next, p.max_ctx);
+        nx.npages = nx.end = nx.L <= 0 ? 0 : (nx.L - 1) / kPage + 1;
+        window_pages(nx.L, nx.mt, nx.end, nx.sinks, nx.skip);
+    };
+    auto enter = [&]() {  // false: there is no next one
+        if (!nx.there) return false;
+        unit += apart;
+        list = nx.list;
+        mt = nx.mt;
+        L = nx.L;
+        table = p.table + (size_t)(nx.ok ? req_next : 0) * p.max_pages;
         g0 += nsteps;
         ++it;
-        npages = end = L <= 0 ? 0 : (L - 1) / kPage + 1;
-        window_pages();
+        npages = nx.npages;
+        end = nx.end;
+        wsinks = nx.sinks;
+        wskip = nx.skip;
         nsteps = (end + 1) / 2;
         return true;
     };
@@ -414,7 +430,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         } else {
             end = L <= 0 ? 0 : (L - 1) / kPage + 1;
         }
-        if (WIN) window_pages();
+        if (WIN) window_pages(L, mt, end, wsinks, wskip);
         // splits begin at even entries: a step is two pages
         const long long steps = (end + 1) / 2;
         const int z = (int)(steps * (split + 1) / nsplit);
@@ -446,6 +462,11 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         if (LOOP && !req_ok) bad |= HS_DEVERR_BAD_REQUEST;
         do {
         peek();
+        if (LOOP && nx.there && !kw && lane == 1) {
+            // the next unit's Q into L2, so that it comes at once when there is a place for it
+            const int row0 = (unit + apart - nx.list * p.mtiles) * BM + RM * rank, n = min(RM, p.M - row0);
+            if (n > 0) prefetch_l2(p.q + ((size_t)nx.list * p.M + row0) * (2 * kDim), (uint32_t)n * (2 * kDim));
+        }
         if (LOOP && it > 0) {
             fetch(0, npg, nblk);
             if (lane == 0 && !kw) {
@@ -545,7 +566,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
         }
-        if (LOOP && lane == 0 && !kw && ok && unit + (int)(gridDim.x >> 1) < p.units) {
+        if (LOOP && lane == 0 && !kw && ok && nx.there) {
             // Each phase is waited for once, in order: those that short units have left.
             // (Behind the last unit nothing holds the next phase back.)
             if (it == 0 && nsteps < 2) ok = mbar_wait_inline(bar(C::B_QDONE), 0);
@@ -553,7 +574,8 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (ok && it > 0 && nsteps < 2) ok = mbar_wait_inline(bar(C::B_EFREE), (uint32_t)(it - 1) & 1u);
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
-        } while (ok && enter_next());
+        look();
+        } while (ok && enter());
         if (LOOP && lane == 0 && ok) {
             // what the MMA issuer says of the last loads: on its way until it is here
             const int ring = kw ? C::RK : C::RV, b0 = kw ? C::B_XFREE + 1 : C::B_VFREE;
@@ -678,8 +700,9 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 __syncwarp();
                 if (j > 0) pv(j - 1);
             }
+            look();
             if (ok && (!LOOP || nsteps > 0)) pv(nsteps - 1);
-            } while (ok && enter_next());
+            } while (ok && enter());
             // LOOP: the last arrives of both CTAs are here
             if (LOOP && ok && g0 + nsteps > 0)
                 ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_SFREE), (uint32_t)(g0 + nsteps - 1) & 1u));
@@ -811,22 +834,35 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         };
         q_moved();
 
+        const int tpl = LOOP ? 1 : p.tpl;
+        auto token_of = [&](int g) { return g < p.M ? g / p.H : 0; };
+        int t_row = token_of(mt * BM + RM * rank + row), t_end = WIN ? (min(p.M, mt * BM + BM) - 1) / p.H : 0;
+        bool owed = false;  // LOOP: the last unit's output may still be read from shared memory
+        auto pay = [&]() {
+            if (!LOOP || !owed) return;
+            if (lane == 0) {
+                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                mbar_arrive(bar(C::B_EFREE));
+            }
+            __syncwarp();
+            owed = false;
+        };
         do {
         peek();
         // this row's query token and its mask
         const int mg = mt * BM + RM * rank + row;
         const bool vrow = mg < p.M;
-        const int nt = p.T * p.tpl;  // query tokens of the request
-        const int t = (vrow ? mg / p.H : 0) + list % p.tpl, draft = L - nt;
+        const int nt = p.T * tpl;  // query tokens of the request
+        const int t = t_row + list % tpl, draft = L - nt;
         uint64_t tree = 0;
         if (p.tree) {
-            tree = p.tree[(size_t)(list / p.tpl) * nt + t];
+            tree = p.tree[(size_t)(list / tpl) * nt + t];
             if (nt < 64) tree &= (1ull << nt) - 1;
         }
         // WIN: the row's first position, and the last of its CTA pair's rows' first ones
         auto from = [&](int at) { return (int)max((long long)draft + at - p.window + 1, 0ll); };
         const int low = WIN ? from(p.tree ? __popcll(tree) - 1 : t) : 0;
-        const int low_max = WIN ? from(p.tree ? nt - 1 : (min(p.M, mt * BM + BM) - 1) / p.H) : 0;
+        const int low_max = WIN ? from(p.tree ? nt - 1 : t_end) : 0;
         float m2 = -INFINITY, l = 0.f;
         float cref = 0.f, fac = 0.f;  // FP8: the scales' reference, a power of two, and 2^10 over it
         const uint32_t wm = base + C::OFF_WM + 4u * (uint32_t)row;
@@ -861,6 +897,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
             tc_fence_before();
             if (LOOP || j + 1 < nsteps) arrive_lead(lead(C::B_SFREE));  // S_{j+1} may be written
+            if (j == 0) pay();
             const int pg = ok ? (int)ld_shared_b32(base + C::OFF_PG + 4 * (2 * ti + kh)) : -1;
             // the keys that this row sees, as bits
             const int d = draft - max(pg, 0) * kPage;  // the first query token's position in the page
@@ -1057,7 +1094,11 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         // LOOP: the next unit's Q into tensor memory while the last PV runs, so that its first
         // scores are multiplied during this unit's epilogue
         const int g1 = g0 + nsteps;
-        if (LOOP && unit + (int)(gridDim.x >> 1) < p.units) {
+        pay();
+        if (LOOP && nx.there) {
+            look();
+            t_row = token_of(nx.mt * BM + RM * rank + row);
+            t_end = (min(p.M, nx.mt * BM + BM) - 1) / p.H;
             if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_QFULL), (uint32_t)(it + 1) & 1u));
             if (ok) {
 #pragma unroll 1
@@ -1163,7 +1204,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
             }
             // the stores have read shared memory before the CTA may end
-            if (lane == 0 && !p.inside) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            if (!LOOP && lane == 0 && !p.inside) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
             __syncwarp();
         }
         if (kh == 0 && hf == 0 && (vrow || p.inside)) {
@@ -1175,7 +1216,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             else
                 st_shared_f1(base + C::OFF_P + 4 * row, lse);  // P is done with
         }
-        if (LOOP && lane == 0) mbar_arrive(bar(C::B_EFREE));
+        owed = LOOP;
         if (p.inside && kh == 0 && hf == 0) {
             fence_proxy_async();
             __syncwarp();
@@ -1184,7 +1225,8 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 bulk_push(cluster_address(base + C::OFF_P + 1024 + wr * 128, other), base + C::OFF_P + wr * 128, 128, theirs);
             __syncwarp();
         }
-        } while (enter_next());
+        } while (enter());
+        pay();
     } else if (FP8 && warp >= 4 + NSW) {
         // ------------------------------------------------------------ converters
         // Half of V's columns at a time; the next half's codes are loaded while its buffer
@@ -1620,6 +1662,7 @@ hs_status page_entry(hs_pool_t pool, int64_t lists, int32_t T, int32_t tpl, int3
     p.zero_block = (int)pool->cfg.n_gpu_blocks;
     p.tpl = tpl;
     p.window = window;
+    p.q = static_cast<const uint8_t *>(d_q);
     p.n_sink = n_sink;
     p.scale_log2 = sm_scale * 1.4426950408889634f;
     const int64_t units = lists * pl.mtiles;
