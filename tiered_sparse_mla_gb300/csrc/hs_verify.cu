@@ -9,9 +9,11 @@
 // refused children. The drawn token is the first v whose r(0) + .. + r(v) passes u_0 times
 // the sum of all.
 //
-// Only one row of V values (two with a draft's) is read in full for a request: 64 requests
-// of 128,000 values, 65.5 MB, whose bytes are the bound, after two dependent loads that
-// say which row it is.
+// Only one row of V values (two with a draft's) is read in full for a request, a run of it
+// by each warp of a cluster: 64 requests of 128,000 values, 65.5 MB, 17 us, 10 of them the
+// bytes at the copy rate, 1.5 before them two dependent loads that say which row it is, 4
+// behind them the slowest CTA and the search. (The whole runs asked into L2 at the start:
+// 19.7 us. Copies of 16 bytes through shared memory, 30 us: twice the instructions.)
 //
 // A search by sums has to add the same way each time. Here sums are integers of 2^-58: eight
 // values of a lane are cut into digits of f32, multiples of 2^-20 (to which adding and
@@ -33,7 +35,6 @@ constexpr int VT = 256;          // threads per CTA
 constexpr int NW = VT / 32;
 constexpr int BATCH = 256;       // values that a warp takes at a time
 constexpr int UNITS = 16;        // of a warp's run of batches: each lane's sum of each is kept
-constexpr int AHEAD = 16384;     // values that a warp asks into L2 at the start
 constexpr int MAXT = 64;
 constexpr int MAXG = 8;          // CTAs per request
 
@@ -279,82 +280,97 @@ verify_kernel(const VerifyParams p) {
     const int first = (int)(units * me / W), n = (int)(units * (me + 1) / W) - first;
     const int64_t v_first = first * unit;
 
-    // its first values into L2 while the first of them are added
-    if (lane < 2 && n > 0) {
-        const int64_t len = min(min((int64_t)n * unit, V - v_first), (int64_t)AHEAD) * (int64_t)sizeof(P);
-        const uint64_t at = (uint64_t)(lane ? guess : row) + (uint64_t)v_first * sizeof(P), a0 = at & ~15ull;
-        if (lane == 0 || guess) hs::tc::prefetch_l2((const void *)a0, (uint32_t)((at + len - a0 + 15) & ~15ull));
-    }
-
     for (int attempt = 0;; ++attempt) {
         uint64_t total_lane = 0;
-        struct Values {
-            uint32_t x[8], y[8];
-        };
         const int whole = (int)((V - v_first) / BATCH);  // batches that lie inside the row
-        const P *row_at = row + v_first + lane, *guess_at = guess + v_first + lane;
-        auto load = [&](Values &q, int j) {  // batch j of the run
+        auto load = [&](uint32_t (&x)[8], const P *from, int j) {  // batch j of the run
+            const P *at = from + v_first + (int64_t)j * BATCH + lane;
             if (j < whole) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) q.x[e] = bits_at<P>(row_at + (int64_t)j * BATCH, 32 * e);
-                if (guess) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) q.y[e] = bits_at<P>(guess_at + (int64_t)j * BATCH, 32 * e);
-                }
+                for (int e = 0; e < 8; ++e) x[e] = bits_at<P>(at, 32 * e);
             } else {
+                const int64_t left = V - (v_first + (int64_t)j * BATCH) - lane;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int64_t v = v_first + (int64_t)j * BATCH + 32 * e + lane;
-                    q.x[e] = v < V ? bits_at<P>(row, v) : 0u;
-                    q.y[e] = guess && v < V ? bits_at<P>(guess, v) : 0u;
-                }
+                for (int e = 0; e < 8; ++e) x[e] = 32 * e < left ? bits_at<P>(at, 32 * e) : 0u;
             }
         };
-        auto add = [&](Values &q, int j) {  // the lane's sum, at most 8
+        auto leave_out = [&](uint32_t (&x)[8], int j) {  // the refused children's tokens
             const int64_t v0 = v_first + (int64_t)j * BATCH;
 #pragma unroll 1
-            for (int g = 0; g < ngone; ++g) {  // the refused children's tokens among these
+            for (int g = 0; g < ngone; ++g) {
                 const int64_t at = gone[g] - v0;
                 if (at >= 0 && at < BATCH && (at & 31) == lane) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) q.x[e] = (at >> 5) == e ? 0u : q.x[e];
+                    for (int e = 0; e < 8; ++e) x[e] = (at >> 5) == e ? 0u : x[e];
                 }
             }
+        };
+        auto sum_of = [&](const Digits &all) {  // the lane's, at most 8; the digits' signs differ, their sum has none
+            const int h = __float2int_rn(both_of(all.h) * 0x1p20f), m = __float2int_rn(both_of(all.m) * 0x1p41f);
+            const int l = __float2int_rn(both_of(all.l) * 0x1p58f);
+            return (uint64_t)max(((int64_t)h << 38) + ((int64_t)m << 17) + l, (int64_t)0);
+        };
+        auto plain = [&](const uint32_t (&x)[8]) {
             Digits all = {0, 0, 0};
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
-                const float x0 = within(__uint_as_float(q.x[e])), x1 = within(__uint_as_float(q.x[e + 1]));
-                const Digits d = digits_of(pair(x0, x1));
+                const Digits d = digits_of(pair(within(__uint_as_float(x[e])), within(__uint_as_float(x[e + 1]))));
                 all.h = plus(all.h, d.h);
                 all.m = plus(all.m, d.m);
                 all.l = plus(all.l, d.l);
-                if (guess) {  // where it is the larger, nothing is left: the same digits
-                    const Digits f = digits_of(pair(fminf(within(__uint_as_float(q.y[e])), x0),
-                                                    fminf(within(__uint_as_float(q.y[e + 1])), x1)));
-                    all.h = less(all.h, f.h);
-                    all.m = less(all.m, f.m);
-                    all.l = less(all.l, f.l);
-                }
             }
-            const int h = __float2int_rn(both_of(all.h) * 0x1p20f), m = __float2int_rn(both_of(all.m) * 0x1p41f);
-            const int l = __float2int_rn(both_of(all.l) * 0x1p58f);
-            // the digits' signs differ, their sum has none
-            return (uint64_t)max(((int64_t)h << 38) + ((int64_t)m << 17) + l, (int64_t)0);
+            return sum_of(all);
         };
-        int j = 0;
-#pragma unroll 1
-        for (int i = 0; i < n; ++i) {
-            uint64_t sum = 0;
-            int k = p.per;
-#pragma unroll 1
-            do {
-                Values q;
-                load(q, j);
-                sum = add_sat(sum, add(q, j));
-                ++j;
-            } while (--k > 0);
+        auto beside = [&](const uint32_t (&x)[8], const uint32_t (&y)[8]) {
+            Digits all = {0, 0, 0};
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                const float x0 = within(__uint_as_float(x[e])), x1 = within(__uint_as_float(x[e + 1]));
+                const Digits d = digits_of(pair(x0, x1));
+                // where the draft's is the larger, nothing is left: the same digits
+                const Digits f = digits_of(pair(fminf(within(__uint_as_float(y[e])), x0), fminf(within(__uint_as_float(y[e + 1])), x1)));
+                all.h = less(plus(all.h, d.h), f.h);
+                all.m = less(plus(all.m, d.m), f.m);
+                all.l = less(plus(all.l, d.l), f.l);
+            }
+            return sum_of(all);
+        };
+        uint32_t x[8], y[8];
+        auto keep = [&](int i, uint64_t sum) {
             sums[warp][i][lane] = sum;
             total_lane = add_sat(total_lane, sum);
+        };
+        if (guess || p.per > 1) {
+            int j = 0;
+#pragma unroll 1
+            for (int i = 0; i < n; ++i) {
+                uint64_t sum = 0;
+                int k = p.per;
+#pragma unroll 1
+                do {
+                    load(x, row, j);
+                    if (guess) {
+                        load(y, guess, j);
+                        sum = add_sat(sum, beside(x, y));
+                    } else {
+                        leave_out(x, j);
+                        sum = add_sat(sum, plain(x));
+                    }
+                    ++j;
+                } while (--k > 0);
+                keep(i, sum);
+            }
+        } else {  // two batches at a time
+#pragma unroll 1
+            for (int i = 0; i < n; i += 2) {
+                load(x, row, i);
+                if (i + 1 < n) load(y, row, i + 1);
+                leave_out(x, i);
+                keep(i, plain(x));
+                if (i + 1 == n) break;
+                leave_out(y, i + 1);
+                keep(i + 1, plain(y));
+            }
         }
         uint64_t all = total_lane;
 #pragma unroll
