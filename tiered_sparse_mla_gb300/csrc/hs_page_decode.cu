@@ -461,120 +461,120 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         bool ok = true;
         if (LOOP && !req_ok) bad |= HS_DEVERR_BAD_REQUEST;
         do {
-        peek();
-        if (LOOP && nx.there && !kw && lane == 1) {
-            // the next unit's Q into L2, so that it comes at once when there is a place for it
-            const int row0 = (unit + apart - nx.list * p.mtiles) * BM + RM * rank, n = min(RM, p.M - row0);
-            if (n > 0) prefetch_l2(p.q + ((size_t)nx.list * p.M + row0) * (2 * kDim), (uint32_t)n * (2 * kDim));
-        }
-        if (LOOP && it > 0) {
-            fetch(0, npg, nblk);
-            if (lane == 0 && !kw) {
-                // Q goes where this unit's first V will: free once the step before the last
-                // is done with it; the chunks that stay, once the last scores are.
-                const int s = g0 % C::NV;
-                ok = mbar_wait_inline(bar(C::B_VFREE + s), ((uint32_t)(g0 / C::NV) & 1u) ^ 1u);
-                if (ok && g0 > 0) ok = mbar_wait_inline(bar(C::B_SFULL), (uint32_t)(g0 - 1) & 1u);
-                if (ok) {
-                    mbar_expect_tx(bar(C::B_QFULL), NK * CH);
-                    for (int i = 0; i < NK; ++i)
-                        tma_load_3d(i < NQT ? base + C::OFF_V + s * 2 * NVC * CH + i * CH : base + C::OFF_Q + (i - NQT) * CH,
-                                    &tm_q, 64 * i, mt * BM + RM * rank, list, bar(C::B_QFULL));
+            peek();
+            if (LOOP && nx.there && !kw && lane == 1) {
+                // the next unit's Q into L2, so that it comes at once when there is a place for it
+                const int row0 = (unit + apart - nx.list * p.mtiles) * BM + RM * rank, n = min(RM, p.M - row0);
+                if (n > 0) prefetch_l2(p.q + ((size_t)nx.list * p.M + row0) * (2 * kDim), (uint32_t)n * (2 * kDim));
+            }
+            if (LOOP && it > 0) {
+                fetch(0, npg, nblk);
+                if (lane == 0 && !kw) {
+                    // Q goes where this unit's first V will: free once the step before the last
+                    // is done with it; the chunks that stay, once the last scores are.
+                    const int s = g0 % C::NV;
+                    ok = mbar_wait_inline(bar(C::B_VFREE + s), ((uint32_t)(g0 / C::NV) & 1u) ^ 1u);
+                    if (ok && g0 > 0) ok = mbar_wait_inline(bar(C::B_SFULL), (uint32_t)(g0 - 1) & 1u);
+                    if (ok) {
+                        mbar_expect_tx(bar(C::B_QFULL), NK * CH);
+                        for (int i = 0; i < NK; ++i)
+                            tma_load_3d(i < NQT ? base + C::OFF_V + s * 2 * NVC * CH + i * CH : base + C::OFF_Q + (i - NQT) * CH,
+                                        &tm_q, 64 * i, mt * BM + RM * rank, list, bar(C::B_QFULL));
+                    }
                 }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
             }
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-        }
-        for (int j = 0; j < nsteps && ok; ++j) {
-            const int gj = g0 + j;
-            if (j % 16 == 0) {
-                pg = npg;
-                blk = nblk;
-                fetch(2 * j + 32, npg, nblk);
-            }
-            const int src = 2 * (j % 16);
-            const int pg0 = __shfl_sync(0xffffffffu, pg, src), pg1 = __shfl_sync(0xffffffffu, pg, src + 1);
-            const int row0 = __shfl_sync(0xffffffffu, blk, src) * kPage;
-            const int row1 = __shfl_sync(0xffffffffu, blk, src + 1) * kPage;
-            if (lane == 0 && kw) {
-                const int own = rank ? row1 : row0, ti = gj % NTI;
-                ok = mbar_wait_inline(bar(C::B_TFREE + ti), ((uint32_t)(gj / NTI) & 1u) ^ 1u);
-                if (ok) {
-                    ring_pg[2 * ti] = pg0;
-                    ring_pg[2 * ti + 1] = pg1;
+            for (int j = 0; j < nsteps && ok; ++j) {
+                const int gj = g0 + j;
+                if (j % 16 == 0) {
+                    pg = npg;
+                    blk = nblk;
+                    fetch(2 * j + 32, npg, nblk);
+                }
+                const int src = 2 * (j % 16);
+                const int pg0 = __shfl_sync(0xffffffffu, pg, src), pg1 = __shfl_sync(0xffffffffu, pg, src + 1);
+                const int row0 = __shfl_sync(0xffffffffu, blk, src) * kPage;
+                const int row1 = __shfl_sync(0xffffffffu, blk, src + 1) * kPage;
+                if (lane == 0 && kw) {
+                    const int own = rank ? row1 : row0, ti = gj % NTI;
+                    ok = mbar_wait_inline(bar(C::B_TFREE + ti), ((uint32_t)(gj / NTI) & 1u) ^ 1u);
+                    if (ok) {
+                        ring_pg[2 * ti] = pg0;
+                        ring_pg[2 * ti + 1] = pg1;
+                        if (FP8) {
+                            const uint32_t sc = base + C::OFF_SC + ti * 512;
+                            mbar_expect_tx(bar(C::B_TFULL + ti), 512);
+                            bulk_load(sc, p.scales + (size_t)row0, 256, bar(C::B_TFULL + ti));
+                            bulk_load(sc + 256, p.scales + (size_t)row1, 256, bar(C::B_TFULL + ti));
+                        } else {
+                            mbar_arrive(bar(C::B_TFULL + ti));
+                        }
+                        ut = gj + 1;
+                    }
+                    // both CTAs' bytes complete on CTA 0's barrier
                     if (FP8) {
-                        const uint32_t sc = base + C::OFF_SC + ti * 512;
-                        mbar_expect_tx(bar(C::B_TFULL + ti), 512);
-                        bulk_load(sc, p.scales + (size_t)row0, 256, bar(C::B_TFULL + ti));
-                        bulk_load(sc + 256, p.scales + (size_t)row1, 256, bar(C::B_TFULL + ti));
+                        for (int i = 0; i < NK && ok; i += C::GK, ++ul) {
+                            const int s = ul % C::RK;
+                            ok = mbar_wait_inline(bar(C::B_XFREE + s), ((uint32_t)(ul / C::RK) & 1u) ^ 1u);
+                            if (!ok) break;
+                            if (rank == 0) mbar_expect_tx(bar(C::B_XFULL + s), 2 * C::GK * CCH);
+                            tma_load_pair(base + C::OFF_X + s * C::GK * CCH, &tm_k1, 0, own, i, lead(C::B_XFULL + s));
+                        }
                     } else {
-                        mbar_arrive(bar(C::B_TFULL + ti));
+                        if (ok) ok = mbar_wait_inline(bar(C::B_XFREE), ((uint32_t)gj & 1u) ^ 1u);
+                        if (ok) {
+                            if (rank == 0) mbar_expect_tx(bar(C::B_XFULL), 2 * CH);
+                            tma_load_pair(base + C::OFF_X, &tm_k1, 0, own, 8, lead(C::B_XFULL));
+                            ux = gj + 1;
+                        }
+                        for (int i = 0; i < 8 && ok; i += 2, ++ul) {
+                            const int s = 1 + ul % C::RK;
+                            ok = mbar_wait_inline(bar(C::B_XFREE + s), ((uint32_t)(ul / C::RK) & 1u) ^ 1u);
+                            if (!ok) break;
+                            if (rank == 0) mbar_expect_tx(bar(C::B_XFULL + s), 4 * CH);
+                            tma_load_pair(base + C::OFF_X + (2 * s - 1) * CH, &tm_k2, 0, own, i, lead(C::B_XFULL + s));
+                        }
                     }
-                    ut = gj + 1;
-                }
-                // both CTAs' bytes complete on CTA 0's barrier
-                if (FP8) {
-                    for (int i = 0; i < NK && ok; i += C::GK, ++ul) {
-                        const int s = ul % C::RK;
-                        ok = mbar_wait_inline(bar(C::B_XFREE + s), ((uint32_t)(ul / C::RK) & 1u) ^ 1u);
-                        if (!ok) break;
-                        if (rank == 0) mbar_expect_tx(bar(C::B_XFULL + s), 2 * C::GK * CCH);
-                        tma_load_pair(base + C::OFF_X + s * C::GK * CCH, &tm_k1, 0, own, i, lead(C::B_XFULL + s));
-                    }
-                } else {
-                    if (ok) ok = mbar_wait_inline(bar(C::B_XFREE), ((uint32_t)gj & 1u) ^ 1u);
-                    if (ok) {
-                        if (rank == 0) mbar_expect_tx(bar(C::B_XFULL), 2 * CH);
-                        tma_load_pair(base + C::OFF_X, &tm_k1, 0, own, 8, lead(C::B_XFULL));
-                        ux = gj + 1;
-                    }
-                    for (int i = 0; i < 8 && ok; i += 2, ++ul) {
-                        const int s = 1 + ul % C::RK;
-                        ok = mbar_wait_inline(bar(C::B_XFREE + s), ((uint32_t)(ul / C::RK) & 1u) ^ 1u);
-                        if (!ok) break;
-                        if (rank == 0) mbar_expect_tx(bar(C::B_XFULL + s), 4 * CH);
-                        tma_load_pair(base + C::OFF_X + (2 * s - 1) * CH, &tm_k2, 0, own, i, lead(C::B_XFULL + s));
-                    }
-                }
-            } else if (lane == 0) {
-                if (FP8) {
-                    for (int i = 0; i < 2 && ok; ++i, ++ul) {  // half the columns: two chunks of either page
-                        const int cs = ul % C::RV;
-                        const uint32_t dst = base + C::OFF_C + cs * C::GV * CCH;
-                        ok = mbar_wait_inline(bar(C::B_CFREE + cs), ((uint32_t)(ul / C::RV) & 1u) ^ 1u);
-                        if (!ok) break;
-                        mbar_expect_tx(bar(C::B_CFULL + cs), C::GV * CCH);
-                        tma_load_3d(dst, &tm_k2, 0, row0, 4 * i + 2 * rank, bar(C::B_CFULL + cs));
-                        tma_load_3d(dst + 2 * CCH, &tm_k2, 0, row1, 4 * i + 2 * rank, bar(C::B_CFULL + cs));
-                    }
-                } else {
-                    const int s = gj % C::RV;
-                    if (j == 1 && it == 0) ok = mbar_wait_inline(bar(C::B_QDONE), 0);  // Q was staged there
-                    if (LOOP && j == 0 && it > 0) ok = mbar_wait_inline(bar(C::B_QDONE), (uint32_t)it & 1u);
-                    // the last unit's output was
-                    if (LOOP && j == 1 && it > 0) ok = mbar_wait_inline(bar(C::B_EFREE), (uint32_t)(it - 1) & 1u);
-                    if (ok) ok = mbar_wait_inline(bar(C::B_VFREE + s), ((uint32_t)(gj / C::RV) & 1u) ^ 1u);
-                    if (ok) {
-                        const uint32_t dst = base + C::OFF_V + s * 2 * NVC * CH;
-                        mbar_expect_tx(bar(C::B_VFULL + s), 2 * NVC * CH);
-                        tma_load_3d(dst, &tm_k2, 0, row0, 2 * rank, bar(C::B_VFULL + s));
-                        tma_load_3d(dst + 2 * CH, &tm_k2, 0, row0, 4 + 2 * rank, bar(C::B_VFULL + s));
-                        tma_load_3d(dst + 4 * CH, &tm_k2, 0, row1, 2 * rank, bar(C::B_VFULL + s));
-                        tma_load_3d(dst + 6 * CH, &tm_k2, 0, row1, 4 + 2 * rank, bar(C::B_VFULL + s));
-                        ul = gj + 1;
+                } else if (lane == 0) {
+                    if (FP8) {
+                        for (int i = 0; i < 2 && ok; ++i, ++ul) {  // half the columns: two chunks of either page
+                            const int cs = ul % C::RV;
+                            const uint32_t dst = base + C::OFF_C + cs * C::GV * CCH;
+                            ok = mbar_wait_inline(bar(C::B_CFREE + cs), ((uint32_t)(ul / C::RV) & 1u) ^ 1u);
+                            if (!ok) break;
+                            mbar_expect_tx(bar(C::B_CFULL + cs), C::GV * CCH);
+                            tma_load_3d(dst, &tm_k2, 0, row0, 4 * i + 2 * rank, bar(C::B_CFULL + cs));
+                            tma_load_3d(dst + 2 * CCH, &tm_k2, 0, row1, 4 * i + 2 * rank, bar(C::B_CFULL + cs));
+                        }
+                    } else {
+                        const int s = gj % C::RV;
+                        if (j == 1 && it == 0) ok = mbar_wait_inline(bar(C::B_QDONE), 0);  // Q was staged there
+                        if (LOOP && j == 0 && it > 0) ok = mbar_wait_inline(bar(C::B_QDONE), (uint32_t)it & 1u);
+                        // the last unit's output was
+                        if (LOOP && j == 1 && it > 0) ok = mbar_wait_inline(bar(C::B_EFREE), (uint32_t)(it - 1) & 1u);
+                        if (ok) ok = mbar_wait_inline(bar(C::B_VFREE + s), ((uint32_t)(gj / C::RV) & 1u) ^ 1u);
+                        if (ok) {
+                            const uint32_t dst = base + C::OFF_V + s * 2 * NVC * CH;
+                            mbar_expect_tx(bar(C::B_VFULL + s), 2 * NVC * CH);
+                            tma_load_3d(dst, &tm_k2, 0, row0, 2 * rank, bar(C::B_VFULL + s));
+                            tma_load_3d(dst + 2 * CH, &tm_k2, 0, row0, 4 + 2 * rank, bar(C::B_VFULL + s));
+                            tma_load_3d(dst + 4 * CH, &tm_k2, 0, row1, 2 * rank, bar(C::B_VFULL + s));
+                            tma_load_3d(dst + 6 * CH, &tm_k2, 0, row1, 4 + 2 * rank, bar(C::B_VFULL + s));
+                            ul = gj + 1;
+                        }
                     }
                 }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+            }
+            if (LOOP && lane == 0 && !kw && ok && nx.there) {
+                // Each phase is waited for once, in order: those that short units have left.
+                // (Behind the last unit nothing holds the next phase back.)
+                if (it == 0 && nsteps < 2) ok = mbar_wait_inline(bar(C::B_QDONE), 0);
+                if (it > 0 && nsteps == 0) ok = mbar_wait_inline(bar(C::B_QDONE), (uint32_t)it & 1u);
+                if (ok && it > 0 && nsteps < 2) ok = mbar_wait_inline(bar(C::B_EFREE), (uint32_t)(it - 1) & 1u);
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
-        }
-        if (LOOP && lane == 0 && !kw && ok && nx.there) {
-            // Each phase is waited for once, in order: those that short units have left.
-            // (Behind the last unit nothing holds the next phase back.)
-            if (it == 0 && nsteps < 2) ok = mbar_wait_inline(bar(C::B_QDONE), 0);
-            if (it > 0 && nsteps == 0) ok = mbar_wait_inline(bar(C::B_QDONE), (uint32_t)it & 1u);
-            if (ok && it > 0 && nsteps < 2) ok = mbar_wait_inline(bar(C::B_EFREE), (uint32_t)(it - 1) & 1u);
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        look();
+            look();
         } while (ok && enter());
         if (LOOP && lane == 0 && ok) {
             // what the MMA issuer says of the last loads: on its way until it is here
@@ -644,64 +644,64 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             int s = 0;
             uint32_t ph = 0;
             do {
-            peek();
-            ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_QREADY), (uint32_t)it & 1u));
-            tc_fence_after();
-            for (int j = 0; j < nsteps && ok; ++j) {
-                const int gj = g0 + j;
-                if (gj > 0) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_SFREE), (uint32_t)(gj - 1) & 1u));
+                peek();
+                ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_QREADY), (uint32_t)it & 1u));
                 tc_fence_after();
-                auto qk = [&](int c, uint32_t slot, bool fresh) {  // one chunk: four MMAs
-                    const uint32_t kd = klo + ((C::OFF_X + slot * (FP8 ? CCH : CH)) >> 4);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {  // FP8: both pieces of Q with the same 32 codes
-                        const uint32_t tq = tmem + TM_Q + 32u * c + 8u * k, sq = klo + ((C::OFF_Q + (c - NQT) * CH + 32 * k) >> 4);
-                        const bool acc = !(fresh && k == 0);
-                        if (FP8 && c < NQT)
-                            mma2_ts_e4m3(tmem + TM_S, tq, kd + 2 * (k & 1), chi, ID_QK, acc);
-                        else if (FP8)
-                            mma2_ss_e4m3(tmem + TM_S, sq, hi, kd + 2 * (k & 1), chi, ID_QK, acc);
-                        else if (c < NQT)
-                            mma2_ts(tmem + TM_S, tq, kd + 2 * k, hi, ID_QK, acc);
-                        else
-                            mma2_ss(tmem + TM_S, sq, kd + 2 * k, hi, ID_QK, acc);
-                    }
-                };
-                if (!FP8) {
-                    if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_XFULL), (uint32_t)gj & 1u));
-                    if (!ok) break;
+                for (int j = 0; j < nsteps && ok; ++j) {
+                    const int gj = g0 + j;
+                    if (gj > 0) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_SFREE), (uint32_t)(gj - 1) & 1u));
                     tc_fence_after();
-                    if (leader) {
-                        qk(8, 0, true);
-                        if (LOOP || j + 1 < nsteps) commit_both(bar(C::B_XFREE), both);
-                    }
-                    __syncwarp();
-                }
+                    auto qk = [&](int c, uint32_t slot, bool fresh) {  // one chunk: four MMAs
+                        const uint32_t kd = klo + ((C::OFF_X + slot * (FP8 ? CCH : CH)) >> 4);
 #pragma unroll
-                for (int c = 0; c < (FP8 ? NK : 8); c += C::GK) {
-                    const int b0 = (FP8 ? 0 : 1) + s;
-                    if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_XFULL + b0), ph));
-                    if (ok) {
+                        for (int k = 0; k < 4; ++k) {  // FP8: both pieces of Q with the same 32 codes
+                            const uint32_t tq = tmem + TM_Q + 32u * c + 8u * k, sq = klo + ((C::OFF_Q + (c - NQT) * CH + 32 * k) >> 4);
+                            const bool acc = !(fresh && k == 0);
+                            if (FP8 && c < NQT)
+                                mma2_ts_e4m3(tmem + TM_S, tq, kd + 2 * (k & 1), chi, ID_QK, acc);
+                            else if (FP8)
+                                mma2_ss_e4m3(tmem + TM_S, sq, hi, kd + 2 * (k & 1), chi, ID_QK, acc);
+                            else if (c < NQT)
+                                mma2_ts(tmem + TM_S, tq, kd + 2 * k, hi, ID_QK, acc);
+                            else
+                                mma2_ss(tmem + TM_S, sq, kd + 2 * k, hi, ID_QK, acc);
+                        }
+                    };
+                    if (!FP8) {
+                        if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_XFULL), (uint32_t)gj & 1u));
+                        if (!ok) break;
                         tc_fence_after();
                         if (leader) {
-#pragma unroll
-                            for (int g = 0; g < C::GK; ++g) qk(c + g, (FP8 ? s * C::GK : 1 + 2 * s) + g, FP8 && c + g == 0);
-                            if (LOOP || PER * j + c / C::GK + C::RK < PER * nsteps) commit_both(bar(C::B_XFREE + b0), both);
+                            qk(8, 0, true);
+                            if (LOOP || j + 1 < nsteps) commit_both(bar(C::B_XFREE), both);
                         }
                         __syncwarp();
                     }
-                    if (++s == (FP8 ? C::NXG : C::NXG - 1)) {
-                        s = 0;
-                        ph ^= 1u;
+#pragma unroll
+                    for (int c = 0; c < (FP8 ? NK : 8); c += C::GK) {
+                        const int b0 = (FP8 ? 0 : 1) + s;
+                        if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_XFULL + b0), ph));
+                        if (ok) {
+                            tc_fence_after();
+                            if (leader) {
+#pragma unroll
+                                for (int g = 0; g < C::GK; ++g) qk(c + g, (FP8 ? s * C::GK : 1 + 2 * s) + g, FP8 && c + g == 0);
+                                if (LOOP || PER * j + c / C::GK + C::RK < PER * nsteps) commit_both(bar(C::B_XFREE + b0), both);
+                            }
+                            __syncwarp();
+                        }
+                        if (++s == (FP8 ? C::NXG : C::NXG - 1)) {
+                            s = 0;
+                            ph ^= 1u;
+                        }
                     }
+                    if (!ok) break;
+                    if (leader) commit_both(bar(C::B_SFULL), both);
+                    __syncwarp();
+                    if (j > 0) pv(j - 1);
                 }
-                if (!ok) break;
-                if (leader) commit_both(bar(C::B_SFULL), both);
-                __syncwarp();
-                if (j > 0) pv(j - 1);
-            }
-            look();
-            if (ok && (!LOOP || nsteps > 0)) pv(nsteps - 1);
+                look();
+                if (ok && (!LOOP || nsteps > 0)) pv(nsteps - 1);
             } while (ok && enter());
             // LOOP: the last arrives of both CTAs are here
             if (LOOP && ok && g0 + nsteps > 0)
@@ -848,383 +848,383 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             owed = false;
         };
         do {
-        peek();
-        // this row's query token and its mask
-        const int mg = mt * BM + RM * rank + row;
-        const bool vrow = mg < p.M;
-        const int nt = p.T * tpl;  // query tokens of the request
-        const int t = t_row + list % tpl, draft = L - nt;
-        uint64_t tree = 0;
-        if (p.tree) {
-            tree = p.tree[(size_t)(list / tpl) * nt + t];
-            if (nt < 64) tree &= (1ull << nt) - 1;
-        }
-        // WIN: the row's first position, and the last of its CTA pair's rows' first ones
-        auto from = [&](int at) { return (int)max((long long)draft + at - p.window + 1, 0ll); };
-        const int low = WIN ? from(p.tree ? __popcll(tree) - 1 : t) : 0;
-        const int low_max = WIN ? from(p.tree ? nt - 1 : t_end) : 0;
-        float m2 = -INFINITY, l = 0.f;
-        float cref = 0.f, fac = 0.f;  // FP8: the scales' reference, a power of two, and 2^10 over it
-        const uint32_t wm = base + C::OFF_WM + 4u * (uint32_t)row;
-        if (FP8 && tid < RM) st_shared_f1(wm, 0.f);  // read behind a barrier
-        const float row_scale = p.scale_log2 * q_back;
-        for (int j = 0; j < nsteps; ++j) {
-            const int gj = g0 + j, ti = gj % NTI;
-            float s[KT];
-            const uint32_t sc_at = base + C::OFF_SC + ti * 512 + kh * 256 + hf * 128;
-            if (ok)
-                ok = __all_sync(0xffffffffu, mbar_wait_inline(bar((FP8 ? C::B_TREADY : C::B_TFULL) + ti), (uint32_t)(gj / NTI) & 1u) &&
-                                                 mbar_wait_inline(bar(C::B_SFULL), (uint32_t)gj & 1u));
-            if (ok) {
-                tc_fence_after();
-                uint32_t ra[32];
-                HS_TMEM_LD32(tmem + lane_off + TM_S + 32u * hf, ra);
-                HS_TMEM_WAIT_LD32(ra);
-#pragma unroll
-                for (int e = 0; e < KT; e += 4) {
-                    float4 f = FP8 ? ld_shared_f4(sc_at + 4 * e) : make_float4(p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) s[e + i] = __uint_as_float(ra[e + i]);
-                    if (FP8) {
-                        // the two scales first: the codes' sum, up to 2^27, times a large
-                        // row's alone may be beyond f32 where the score is not
-                        mul2(f.x, f.y, row_scale, row_scale);
-                        mul2(f.z, f.w, row_scale, row_scale);
-                    }
-                    mul2(s[e], s[e + 1], f.x, f.y);
-                    mul2(s[e + 2], s[e + 3], f.z, f.w);
-                }
+            peek();
+            // this row's query token and its mask
+            const int mg = mt * BM + RM * rank + row;
+            const bool vrow = mg < p.M;
+            const int nt = p.T * tpl;  // query tokens of the request
+            const int t = t_row + list % tpl, draft = L - nt;
+            uint64_t tree = 0;
+            if (p.tree) {
+                tree = p.tree[(size_t)(list / tpl) * nt + t];
+                if (nt < 64) tree &= (1ull << nt) - 1;
             }
-            tc_fence_before();
-            if (LOOP || j + 1 < nsteps) arrive_lead(lead(C::B_SFREE));  // S_{j+1} may be written
-            if (j == 0) pay();
-            const int pg = ok ? (int)ld_shared_b32(base + C::OFF_PG + 4 * (2 * ti + kh)) : -1;
-            // the keys that this row sees, as bits
-            const int d = draft - max(pg, 0) * kPage;  // the first query token's position in the page
-            // WIN: some row's window may begin in the page
-            const bool head = WIN && pg >= 0 && low_max > pg * kPage && p.n_sink - kPage < pg * kPage;
-            const bool tail = (pg >= 0 && d < kPage) || head;  // some row may not see some key
-            float tmax = -INFINITY, cmax = 0.f;
-            uint32_t mine = ~0u;
-            if (pg < 0) {
-                mine = 0;
-            } else if (tail) {
-                uint64_t seen;
-                if (p.tree) {
-                    if (WIN && d >= 64)
-                        seen = ~0ull;
-                    else if (d >= 0)
-                        seen = ((1ull << d) - 1) | (tree << d);
-                    else
-                        seen = d > -64 ? tree >> -d : 0ull;
-                } else {
-                    const int n = d + t + 1;
-                    seen = n >= 64 ? ~0ull : (n <= 0 ? 0ull : (1ull << n) - 1);
-                }
-                if (WIN && head) {
-                    const int a = low - pg * kPage, n = p.n_sink - pg * kPage;
-                    const uint64_t on = a >= 64 ? 0ull : (a <= 0 ? ~0ull : ~0ull << a);
-                    seen &= on | (n <= 0 ? 0ull : (1ull << n) - 1);  // n is below 64 here
-                }
-                mine = (uint32_t)(seen >> (KT * hf));
-            }
-            const bool hide = !__all_sync(0xffffffffu, mine == ~0u);
-            // BF16: a key that holds an infinity or NaN has no finite score, with any query
-            bool odd = false;
-            if (!FP8 && ok && tail) {
-                float z0 = 0.f, z1 = 0.f;
+            // WIN: the row's first position, and the last of its CTA pair's rows' first ones
+            auto from = [&](int at) { return (int)max((long long)draft + at - p.window + 1, 0ll); };
+            const int low = WIN ? from(p.tree ? __popcll(tree) - 1 : t) : 0;
+            const int low_max = WIN ? from(p.tree ? nt - 1 : t_end) : 0;
+            float m2 = -INFINITY, l = 0.f;
+            float cref = 0.f, fac = 0.f;  // FP8: the scales' reference, a power of two, and 2^10 over it
+            const uint32_t wm = base + C::OFF_WM + 4u * (uint32_t)row;
+            if (FP8 && tid < RM) st_shared_f1(wm, 0.f);  // read behind a barrier
+            const float row_scale = p.scale_log2 * q_back;
+            for (int j = 0; j < nsteps; ++j) {
+                const int gj = g0 + j, ti = gj % NTI;
+                float s[KT];
+                const uint32_t sc_at = base + C::OFF_SC + ti * 512 + kh * 256 + hf * 128;
+                if (ok)
+                    ok = __all_sync(0xffffffffu, mbar_wait_inline(bar((FP8 ? C::B_TREADY : C::B_TFULL) + ti), (uint32_t)(gj / NTI) & 1u) &&
+                                                     mbar_wait_inline(bar(C::B_SFULL), (uint32_t)gj & 1u));
+                if (ok) {
+                    tc_fence_after();
+                    uint32_t ra[32];
+                    HS_TMEM_LD32(tmem + lane_off + TM_S + 32u * hf, ra);
+                    HS_TMEM_WAIT_LD32(ra);
 #pragma unroll
-                for (int e = 0; e < KT; e += 2) zeros_of(z0, z1, s[e], s[e + 1]);
-                odd = !(z0 + z1 == 0.f);
-            }
-            if (ok) {
-                if (hide) {
+                    for (int e = 0; e < KT; e += 4) {
+                        float4 f = FP8 ? ld_shared_f4(sc_at + 4 * e) : make_float4(p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2);
 #pragma unroll
-                    for (int e = 0; e < KT; ++e) s[e] = (mine >> e) & 1u ? s[e] : -INFINITY;
-                }
-                float mx[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    mx[e] = max3(s[e], s[e + 4], s[e + 8]);
-                    mx[e] = max3(mx[e], s[e + 12], s[e + 16]);
-                    mx[e] = max3(mx[e], s[e + 20], s[e + 24]);
-                    mx[e] = fmaxf(mx[e], s[e + 28]);
-                }
-                tmax = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-                if (FP8) {
-                    cmax = ld_shared_f1(base + C::OFF_SP + 4 * (4 * ti + 2 * kh + hf));
-                    if (hide) {  // a hidden row's scale may be anything
-                        cmax = 0.f;
-#pragma unroll
-                        for (int e = 0; e < KT; e += 4) {
-                            const float4 f = ld_shared_f4(sc_at + 4 * e);
-                            cmax = fmaxf(cmax, (mine >> e) & 1u ? fabsf(f.x) : 0.f);
-                            cmax = fmaxf(cmax, (mine >> (e + 1)) & 1u ? fabsf(f.y) : 0.f);
-                            cmax = fmaxf(cmax, (mine >> (e + 2)) & 1u ? fabsf(f.z) : 0.f);
-                            cmax = fmaxf(cmax, (mine >> (e + 3)) & 1u ? fabsf(f.w) : 0.f);
+                        for (int i = 0; i < 4; ++i) s[e + i] = __uint_as_float(ra[e + i]);
+                        if (FP8) {
+                            // the two scales first: the codes' sum, up to 2^27, times a large
+                            // row's alone may be beyond f32 where the score is not
+                            mul2(f.x, f.y, row_scale, row_scale);
+                            mul2(f.z, f.w, row_scale, row_scale);
                         }
+                        mul2(s[e], s[e + 1], f.x, f.y);
+                        mul2(s[e + 2], s[e + 3], f.z, f.w);
                     }
                 }
-            }
-            // A row's four threads share its references: where some row of the CTA may
-            // outgrow its own, the rows' four maxima meet in shared memory.
-            float alpha = 1.f;
-            auto outgrown = [](float x, float ref) { return x > ref + TAU2<FP8> || (ref == -INFINITY && x != -INFINITY); };
-            const bool grow = any_softmax(outgrown(tmax, m2) || (FP8 && cmax > 2.f * cref) || odd);
-            if (grow) {
-                if (!FP8) odd = any_softmax(odd);  // either half of the keys
-                st_shared_f1(xm + 4 * tid, tmax);
-                if (FP8) st_shared_f1(xm + 4 * (32 * NSW + tid), cmax);
-                named_bar_sync(1, 32 * NSW);
-                auto of_row = [&](int o) {
-                    return fmaxf(fmaxf(ld_shared_f1(xm_row(o)), ld_shared_f1(xm_row(o + 64))),
-                                 fmaxf(ld_shared_f1(xm_row(o + 128)), ld_shared_f1(xm_row(o + 192))));
-                };
-                const float tall = of_row(0), call = FP8 ? of_row(32 * NSW) : 0.f;
-                named_bar_sync(1, 32 * NSW);  // read before the next writes
-                if (outgrown(tall, m2)) {
-                    alpha = exp2f(m2 - tall);  // 0 where the row had seen nothing
-                    l *= alpha;
-                    m2 = tall;
-                }
-                if (FP8) {
-                    float w = 0.f;  // the largest weight times scale (NaN drops out)
-                    if (ok) {
-                        const float mneg = m2 == -INFINITY ? 0.f : -m2;
-#pragma unroll
-                        for (int e = 0; e < KT; e += 4) {
-                            const float4 f = ld_shared_f4(sc_at + 4 * e);
-                            w = max3(w, ex2(s[e] + mneg) * fabsf(f.x), ex2(s[e + 1] + mneg) * fabsf(f.y));
-                            w = max3(w, ex2(s[e + 2] + mneg) * fabsf(f.z), ex2(s[e + 3] + mneg) * fabsf(f.w));
-                        }
-                    }
-                    st_shared_f1(xm + 4 * tid, w);
-                    named_bar_sync(1, 32 * NSW);
-                    const float most = fmaxf(of_row(0), ld_shared_f1(wm) * alpha);
-                    named_bar_sync(1, 32 * NSW);
-                    if (hf == 0 && kh == 0) st_shared_f1(wm, most);
-                    const float want = fminf(fmaxf(call, most), C_MOST * most);
-                    if (want > 2.f * cref || cref > C_MOST * most) {
-                        // at least 2^-107: its inverse, and the epilogue's factor, are normal
-                        const uint32_t e = max(__float_as_uint(want) >> 23, 20u);
-                        fac = __uint_as_float((254u + P_EXP - e) << 23);
-                        alpha = alpha * cref * fac * (1.f / (1 << P_EXP));
-                        cref = __uint_as_float(e << 23);
-                    }
-                }
-            }
-            uint32_t pk[KT / 2];
-            if (ok) {
-                const float mneg = m2 == -INFINITY ? 0.f : -m2;
-                float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
-#pragma unroll
-                for (int e = 0; e < KT; e += 4) {
-                    float a0 = s[e], a1 = s[e + 1], a2 = s[e + 2], a3 = s[e + 3];
-                    add2(a0, a1, mneg, mneg);
-                    add2(a2, a3, mneg, mneg);
-                    a0 = ex2(a0);
-                    a1 = ex2(a1);
-                    a2 = ex2(a2);
-                    a3 = ex2(a3);
-                    add2(l0, l1, a0, a1);
-                    add2(l2, l3, a2, a3);
-                    if (FP8) {
-                        float4 f = ld_shared_f4(sc_at + 4 * e);
-                        mul2(f.x, f.y, fac, fac);
-                        mul2(f.z, f.w, fac, fac);
-                        mul2(a0, a1, f.x, f.y);
-                        mul2(a2, a3, f.z, f.w);
-                        pk[e / 2] = pack_f16(a0, a1);
-                        pk[e / 2 + 1] = pack_f16(a2, a3);
+                tc_fence_before();
+                if (LOOP || j + 1 < nsteps) arrive_lead(lead(C::B_SFREE));  // S_{j+1} may be written
+                if (j == 0) pay();
+                const int pg = ok ? (int)ld_shared_b32(base + C::OFF_PG + 4 * (2 * ti + kh)) : -1;
+                // the keys that this row sees, as bits
+                const int d = draft - max(pg, 0) * kPage;  // the first query token's position in the page
+                // WIN: some row's window may begin in the page
+                const bool head = WIN && pg >= 0 && low_max > pg * kPage && p.n_sink - kPage < pg * kPage;
+                const bool tail = (pg >= 0 && d < kPage) || head;  // some row may not see some key
+                float tmax = -INFINITY, cmax = 0.f;
+                uint32_t mine = ~0u;
+                if (pg < 0) {
+                    mine = 0;
+                } else if (tail) {
+                    uint64_t seen;
+                    if (p.tree) {
+                        if (WIN && d >= 64)
+                            seen = ~0ull;
+                        else if (d >= 0)
+                            seen = ((1ull << d) - 1) | (tree << d);
+                        else
+                            seen = d > -64 ? tree >> -d : 0ull;
                     } else {
-                        pk[e / 2] = pack_bf16(a0, a1);
-                        pk[e / 2 + 1] = pack_bf16(a2, a3);
+                        const int n = d + t + 1;
+                        seen = n >= 64 ? ~0ull : (n <= 0 ? 0ull : (1ull << n) - 1);
                     }
+                    if (WIN && head) {
+                        const int a = low - pg * kPage, n = p.n_sink - pg * kPage;
+                        const uint64_t on = a >= 64 ? 0ull : (a <= 0 ? ~0ull : ~0ull << a);
+                        seen &= on | (n <= 0 ? 0ull : (1ull << n) - 1);  // n is below 64 here
+                    }
+                    mine = (uint32_t)(seen >> (KT * hf));
                 }
-                l += (l0 + l1) + (l2 + l3);
-                if (FP8 && hide) {
-                    // a hidden row's scale may be NaN
+                const bool hide = !__all_sync(0xffffffffu, mine == ~0u);
+                // BF16: a key that holds an infinity or NaN has no finite score, with any query
+                bool odd = false;
+                if (!FP8 && ok && tail) {
+                    float z0 = 0.f, z1 = 0.f;
 #pragma unroll
-                    for (int e = 0; e < KT / 2; ++e)
-                        pk[e] &= ((mine >> (2 * e)) & 1u ? 0xffffu : 0u) | ((mine >> (2 * e + 1)) & 1u ? 0xffff0000u : 0u);
+                    for (int e = 0; e < KT; e += 2) zeros_of(z0, z1, s[e], s[e + 1]);
+                    odd = !(z0 + z1 == 0.f);
                 }
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(C::B_TFREE + ti));
-            // P and O are free once the previous PV is done; BF16: this CTA's V has
-            // landed (FP8: its converters tell the MMA issuer themselves)
-            if (ok && j > 0) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_PVDONE), (uint32_t)(gj - 1) & 1u));
-            if (ok && !FP8)
-                ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_VFULL + gj % C::NV), (uint32_t)(gj / C::NV) & 1u));
-            if (ok) {
-                tc_fence_after();
-                const uint32_t pr = base + C::OFF_P + kh * CH + row * 128;
+                if (ok) {
+                    if (hide) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    st_shared_v4(pr + (((c + 4 * hf) ^ (row & 7)) << 4), pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
-                if (!FP8 && tail && odd) {
-                    // A row that some query does not see may hold infinities or
-                    // NaN, and 0 x NaN would reach that query's sum: in V they
-                    // become zeros (a query that does see them has them in its
-                    // scores). The page's 32 KB, by its 128 threads, where a score says so
-                    // (on every page that some query does not see all of, 4 of the 19 of
-                    // a window of 1,024, 2 x 1,999 tokens of 16 heads took 206 us instead of 145).
-                    const uint32_t v0 = base + C::OFF_V + (gj % C::NV) * 2 * NVC * CH + kh * NVC * CH + (row + 64 * hf) * 16;
-#pragma unroll 4
-                    for (int u = 0; u < 16; ++u) {
-                        const uint4 v = ld_shared_v4(v0 + 2048 * u);
-                        uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                        bool hit = false;
+                        for (int e = 0; e < KT; ++e) s[e] = (mine >> e) & 1u ? s[e] : -INFINITY;
+                    }
+                    float mx[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const bool a = (w[e] & 0x7f80u) == 0x7f80u, c = (w[e] & 0x7f800000u) == 0x7f800000u;
-                            hit = hit || a || c;
-                            w[e] = (a ? 0u : w[e] & 0xffffu) | (c ? 0u : w[e] & 0xffff0000u);
+                    for (int e = 0; e < 4; ++e) {
+                        mx[e] = max3(s[e], s[e + 4], s[e + 8]);
+                        mx[e] = max3(mx[e], s[e + 12], s[e + 16]);
+                        mx[e] = max3(mx[e], s[e + 20], s[e + 24]);
+                        mx[e] = fmaxf(mx[e], s[e + 28]);
+                    }
+                    tmax = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+                    if (FP8) {
+                        cmax = ld_shared_f1(base + C::OFF_SP + 4 * (4 * ti + 2 * kh + hf));
+                        if (hide) {  // a hidden row's scale may be anything
+                            cmax = 0.f;
+#pragma unroll
+                            for (int e = 0; e < KT; e += 4) {
+                                const float4 f = ld_shared_f4(sc_at + 4 * e);
+                                cmax = fmaxf(cmax, (mine >> e) & 1u ? fabsf(f.x) : 0.f);
+                                cmax = fmaxf(cmax, (mine >> (e + 1)) & 1u ? fabsf(f.y) : 0.f);
+                                cmax = fmaxf(cmax, (mine >> (e + 2)) & 1u ? fabsf(f.z) : 0.f);
+                                cmax = fmaxf(cmax, (mine >> (e + 3)) & 1u ? fabsf(f.w) : 0.f);
+                            }
                         }
-                        if (hit) st_shared_v4(v0 + 2048 * u, w[0], w[1], w[2], w[3]);
                     }
                 }
-                fence_proxy_async();
-                if (grow && j > 0 && __any_sync(0xffffffffu, alpha != 1.f))
-                    rescale_o(tmem + lane_off + TM_O + 128u * hf, alpha);
+                // A row's four threads share its references: where some row of the CTA may
+                // outgrow its own, the rows' four maxima meet in shared memory.
+                float alpha = 1.f;
+                auto outgrown = [](float x, float ref) { return x > ref + TAU2<FP8> || (ref == -INFINITY && x != -INFINITY); };
+                const bool grow = any_softmax(outgrown(tmax, m2) || (FP8 && cmax > 2.f * cref) || odd);
+                if (grow) {
+                    if (!FP8) odd = any_softmax(odd);  // either half of the keys
+                    st_shared_f1(xm + 4 * tid, tmax);
+                    if (FP8) st_shared_f1(xm + 4 * (32 * NSW + tid), cmax);
+                    named_bar_sync(1, 32 * NSW);
+                    auto of_row = [&](int o) {
+                        return fmaxf(fmaxf(ld_shared_f1(xm_row(o)), ld_shared_f1(xm_row(o + 64))),
+                                     fmaxf(ld_shared_f1(xm_row(o + 128)), ld_shared_f1(xm_row(o + 192))));
+                    };
+                    const float tall = of_row(0), call = FP8 ? of_row(32 * NSW) : 0.f;
+                    named_bar_sync(1, 32 * NSW);  // read before the next writes
+                    if (outgrown(tall, m2)) {
+                        alpha = exp2f(m2 - tall);  // 0 where the row had seen nothing
+                        l *= alpha;
+                        m2 = tall;
+                    }
+                    if (FP8) {
+                        float w = 0.f;  // the largest weight times scale (NaN drops out)
+                        if (ok) {
+                            const float mneg = m2 == -INFINITY ? 0.f : -m2;
+#pragma unroll
+                            for (int e = 0; e < KT; e += 4) {
+                                const float4 f = ld_shared_f4(sc_at + 4 * e);
+                                w = max3(w, ex2(s[e] + mneg) * fabsf(f.x), ex2(s[e + 1] + mneg) * fabsf(f.y));
+                                w = max3(w, ex2(s[e + 2] + mneg) * fabsf(f.z), ex2(s[e + 3] + mneg) * fabsf(f.w));
+                            }
+                        }
+                        st_shared_f1(xm + 4 * tid, w);
+                        named_bar_sync(1, 32 * NSW);
+                        const float most = fmaxf(of_row(0), ld_shared_f1(wm) * alpha);
+                        named_bar_sync(1, 32 * NSW);
+                        if (hf == 0 && kh == 0) st_shared_f1(wm, most);
+                        const float want = fminf(fmaxf(call, most), C_MOST * most);
+                        if (want > 2.f * cref || cref > C_MOST * most) {
+                            // at least 2^-107: its inverse, and the epilogue's factor, are normal
+                            const uint32_t e = max(__float_as_uint(want) >> 23, 20u);
+                            fac = __uint_as_float((254u + P_EXP - e) << 23);
+                            alpha = alpha * cref * fac * (1.f / (1 << P_EXP));
+                            cref = __uint_as_float(e << 23);
+                        }
+                    }
+                }
+                uint32_t pk[KT / 2];
+                if (ok) {
+                    const float mneg = m2 == -INFINITY ? 0.f : -m2;
+                    float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+#pragma unroll
+                    for (int e = 0; e < KT; e += 4) {
+                        float a0 = s[e], a1 = s[e + 1], a2 = s[e + 2], a3 = s[e + 3];
+                        add2(a0, a1, mneg, mneg);
+                        add2(a2, a3, mneg, mneg);
+                        a0 = ex2(a0);
+                        a1 = ex2(a1);
+                        a2 = ex2(a2);
+                        a3 = ex2(a3);
+                        add2(l0, l1, a0, a1);
+                        add2(l2, l3, a2, a3);
+                        if (FP8) {
+                            float4 f = ld_shared_f4(sc_at + 4 * e);
+                            mul2(f.x, f.y, fac, fac);
+                            mul2(f.z, f.w, fac, fac);
+                            mul2(a0, a1, f.x, f.y);
+                            mul2(a2, a3, f.z, f.w);
+                            pk[e / 2] = pack_f16(a0, a1);
+                            pk[e / 2 + 1] = pack_f16(a2, a3);
+                        } else {
+                            pk[e / 2] = pack_bf16(a0, a1);
+                            pk[e / 2 + 1] = pack_bf16(a2, a3);
+                        }
+                    }
+                    l += (l0 + l1) + (l2 + l3);
+                    if (FP8 && hide) {
+                        // a hidden row's scale may be NaN
+#pragma unroll
+                        for (int e = 0; e < KT / 2; ++e)
+                            pk[e] &= ((mine >> (2 * e)) & 1u ? 0xffffu : 0u) | ((mine >> (2 * e + 1)) & 1u ? 0xffff0000u : 0u);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::B_TFREE + ti));
+                // P and O are free once the previous PV is done; BF16: this CTA's V has
+                // landed (FP8: its converters tell the MMA issuer themselves)
+                if (ok && j > 0) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_PVDONE), (uint32_t)(gj - 1) & 1u));
+                if (ok && !FP8)
+                    ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_VFULL + gj % C::NV), (uint32_t)(gj / C::NV) & 1u));
+                if (ok) {
+                    tc_fence_after();
+                    const uint32_t pr = base + C::OFF_P + kh * CH + row * 128;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        st_shared_v4(pr + (((c + 4 * hf) ^ (row & 7)) << 4), pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+                    if (!FP8 && tail && odd) {
+                        // A row that some query does not see may hold infinities or
+                        // NaN, and 0 x NaN would reach that query's sum: in V they
+                        // become zeros (a query that does see them has them in its
+                        // scores). The page's 32 KB, by its 128 threads, where a score says so
+                        // (on every page that some query does not see all of, 4 of the 19 of
+                        // a window of 1,024, 2 x 1,999 tokens of 16 heads took 206 us instead of 145).
+                        const uint32_t v0 = base + C::OFF_V + (gj % C::NV) * 2 * NVC * CH + kh * NVC * CH + (row + 64 * hf) * 16;
+#pragma unroll 4
+                        for (int u = 0; u < 16; ++u) {
+                            const uint4 v = ld_shared_v4(v0 + 2048 * u);
+                            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                            bool hit = false;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const bool a = (w[e] & 0x7f80u) == 0x7f80u, c = (w[e] & 0x7f800000u) == 0x7f800000u;
+                                hit = hit || a || c;
+                                w[e] = (a ? 0u : w[e] & 0xffffu) | (c ? 0u : w[e] & 0xffff0000u);
+                            }
+                            if (hit) st_shared_v4(v0 + 2048 * u, w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                    fence_proxy_async();
+                    if (grow && j > 0 && __any_sync(0xffffffffu, alpha != 1.f))
+                        rescale_o(tmem + lane_off + TM_O + 128u * hf, alpha);
+                }
+                tc_fence_before();
+                arrive_lead(lead(C::B_PFULL));
             }
-            tc_fence_before();
-            arrive_lead(lead(C::B_PFULL));
-        }
-        // LOOP: the next unit's Q into tensor memory while the last PV runs, so that its first
-        // scores are multiplied during this unit's epilogue
-        const int g1 = g0 + nsteps;
-        pay();
-        if (LOOP && nx.there) {
-            look();
-            t_row = token_of(nx.mt * BM + RM * rank + row);
-            t_end = (min(p.M, nx.mt * BM + BM) - 1) / p.H;
-            if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_QFULL), (uint32_t)(it + 1) & 1u));
-            if (ok) {
+            // LOOP: the next unit's Q into tensor memory while the last PV runs, so that its first
+            // scores are multiplied during this unit's epilogue
+            const int g1 = g0 + nsteps;
+            pay();
+            if (LOOP && nx.there) {
+                look();
+                t_row = token_of(nx.mt * BM + RM * rank + row);
+                t_end = (min(p.M, nx.mt * BM + BM) - 1) / p.H;
+                if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_QFULL), (uint32_t)(it + 1) & 1u));
+                if (ok) {
 #pragma unroll 1
-                for (int i = hf; i < NQT; i += 2) {
-                    uint32_t w[32];
+                    for (int i = hf; i < NQT; i += 2) {
+                        uint32_t w[32];
 #pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        const uint4 v = ld_shared_v4(base + C::OFF_V + (g1 % C::NV) * 2 * NVC * CH + i * CH + row * 128 + ((u ^ (row & 7)) << 4));
-                        w[4 * u] = v.x;
-                        w[4 * u + 1] = v.y;
-                        w[4 * u + 2] = v.z;
-                        w[4 * u + 3] = v.w;
+                        for (int u = 0; u < 8; ++u) {
+                            const uint4 v = ld_shared_v4(base + C::OFF_V + (g1 % C::NV) * 2 * NVC * CH + i * CH + row * 128 + ((u ^ (row & 7)) << 4));
+                            w[4 * u] = v.x;
+                            w[4 * u + 1] = v.y;
+                            w[4 * u + 2] = v.z;
+                            w[4 * u + 3] = v.w;
+                        }
+                        HS_TMEM_ST32(tmem + lane_off + TM_Q + 32u * i, w);
                     }
-                    HS_TMEM_ST32(tmem + lane_off + TM_Q + 32u * i, w);
+                    tmem_wait_st();
                 }
-                tmem_wait_st();
+                q_moved();
             }
-            q_moved();
-        }
-        if (ok && nsteps > 0) {
-            ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_PVDONE), (uint32_t)(g1 - 1) & 1u));
-            tc_fence_after();
-        }
-        if (!ok && lane == 0) fail();
-        __syncwarp();
-        if (p.inside) cluster_arrive_relaxed();  // what this warp needed of this CTA's memory is used
-        // the row's sum over its four threads' keys
-        st_shared_f1(xm + 4 * tid, l);
-        named_bar_sync(1, 32 * NSW);
-        l = (ld_shared_f1(xm_row(0)) + ld_shared_f1(xm_row(64))) + (ld_shared_f1(xm_row(128)) + ld_shared_f1(xm_row(192)));
-        // rows that see nothing: out 0, lse -inf
-        const float inv = l == 0.f ? 0.f : __fdividef(FP8 ? cref * (1.f / (1 << P_EXP)) : 1.f, l);
-        const bool one = nsplit == 1;
-        // The columns that the other split joins go there as they are staged, once all
-        // CTAs are done with the memory they land in (where nothing was computed, what
-        // is sent is not used).
-        const uint32_t other = crank ^ 2u;
-        uint32_t theirs = 0;
-        if (p.inside) {
-            cluster_wait();
-            theirs = cluster_address(bar(C::B_JOIN), other);
-        }
-        if (p.inside || (ok && (one || nsteps > 0))) {
-            // O / l through shared memory, idle by now, in 32-row boxes of 128
-            // swizzled bytes per row: this thread's value columns are
-            // 256 hf + 128 kh + (0..127). Rows past M are clipped by the map.
-            const int wr = wq & 1;  // which 32 rows
-            // LOOP: the buffer that the next unit's Q and first V are not in
-            const uint32_t stage = base + C::OFF_V + (LOOP ? ((g1 + 1) % C::NV) * 2 * NVC * CH : 0);
-            const uint32_t st0 = stage + wr * 4096 + (uint32_t)(row & 31) * 128u;
+            if (ok && nsteps > 0) {
+                ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_PVDONE), (uint32_t)(g1 - 1) & 1u));
+                tc_fence_after();
+            }
+            if (!ok && lane == 0) fail();
+            __syncwarp();
+            if (p.inside) cluster_arrive_relaxed();  // what this warp needed of this CTA's memory is used
+            // the row's sum over its four threads' keys
+            st_shared_f1(xm + 4 * tid, l);
+            named_bar_sync(1, 32 * NSW);
+            l = (ld_shared_f1(xm_row(0)) + ld_shared_f1(xm_row(64))) + (ld_shared_f1(xm_row(128)) + ld_shared_f1(xm_row(192)));
+            // rows that see nothing: out 0, lse -inf
+            const float inv = l == 0.f ? 0.f : __fdividef(FP8 ? cref * (1.f / (1 << P_EXP)) : 1.f, l);
+            const bool one = nsplit == 1;
+            // The columns that the other split joins go there as they are staged, once all
+            // CTAs are done with the memory they land in (where nothing was computed, what
+            // is sent is not used).
+            const uint32_t other = crank ^ 2u;
+            uint32_t theirs = 0;
+            if (p.inside) {
+                cluster_wait();
+                theirs = cluster_address(bar(C::B_JOIN), other);
+            }
+            if (p.inside || (ok && (one || nsteps > 0))) {
+                // O / l through shared memory, idle by now, in 32-row boxes of 128
+                // swizzled bytes per row: this thread's value columns are
+                // 256 hf + 128 kh + (0..127). Rows past M are clipped by the map.
+                const int wr = wq & 1;  // which 32 rows
+                // LOOP: the buffer that the next unit's Q and first V are not in
+                const uint32_t stage = base + C::OFF_V + (LOOP ? ((g1 + 1) % C::NV) * 2 * NVC * CH : 0);
+                const uint32_t st0 = stage + wr * 4096 + (uint32_t)(row & 31) * 128u;
 #pragma unroll 1
-            for (int cc = 0; cc < 4; ++cc) {
-                uint32_t o[32];
-                if (nsteps > 0) {
-                    HS_TMEM_LD32(tmem + lane_off + TM_O + 128 * hf + 32 * cc, o);
-                    HS_TMEM_WAIT_LD32(o);
-                } else {
+                for (int cc = 0; cc < 4; ++cc) {
+                    uint32_t o[32];
+                    if (nsteps > 0) {
+                        HS_TMEM_LD32(tmem + lane_off + TM_O + 128 * hf + 32 * cc, o);
+                        HS_TMEM_WAIT_LD32(o);
+                    } else {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = 0u;
-                }
-                const int col = 256 * hf + 128 * kh + 32 * cc;
-                if (one) {
-                    const uint32_t at = st0 + (uint32_t)(col >> 6) * 8192u;
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            w[e] = pack_bf16(__uint_as_float(o[8 * u + 2 * e]) * inv,
-                                             __uint_as_float(o[8 * u + 2 * e + 1]) * inv);
-                        const int c = ((col & 32) >> 3) + u;
-                        st_shared_v4(at + (uint32_t)((c ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
+                        for (int e = 0; e < 32; ++e) o[e] = 0u;
                     }
-                } else {
-                    // partials stay f32: a third rounding to BF16 would show next to
-                    // those of P and of the output
-                    const uint32_t at = st0 + (uint32_t)(col >> 5) * 8192u;
+                    const int col = 256 * hf + 128 * kh + 32 * cc;
+                    if (one) {
+                        const uint32_t at = st0 + (uint32_t)(col >> 6) * 8192u;
 #pragma unroll
-                    for (int u = 0; u < 8; ++u)
-                        st_shared_v4(at + (uint32_t)((u ^ (row & 7)) << 4), __float_as_uint(__uint_as_float(o[4 * u]) * inv),
-                                     __float_as_uint(__uint_as_float(o[4 * u + 1]) * inv),
-                                     __float_as_uint(__uint_as_float(o[4 * u + 2]) * inv),
-                                     __float_as_uint(__uint_as_float(o[4 * u + 3]) * inv));
-                    if (p.inside && hf != split) {
+                        for (int u = 0; u < 4; ++u) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                w[e] = pack_bf16(__uint_as_float(o[8 * u + 2 * e]) * inv,
+                                                 __uint_as_float(o[8 * u + 2 * e + 1]) * inv);
+                            const int c = ((col & 32) >> 3) + u;
+                            st_shared_v4(at + (uint32_t)((c ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
+                        }
+                    } else {
+                        // partials stay f32: a third rounding to BF16 would show next to
+                        // those of P and of the output
+                        const uint32_t at = st0 + (uint32_t)(col >> 5) * 8192u;
+#pragma unroll
+                        for (int u = 0; u < 8; ++u)
+                            st_shared_v4(at + (uint32_t)((u ^ (row & 7)) << 4), __float_as_uint(__uint_as_float(o[4 * u]) * inv),
+                                         __float_as_uint(__uint_as_float(o[4 * u + 1]) * inv),
+                                         __float_as_uint(__uint_as_float(o[4 * u + 2]) * inv),
+                                         __float_as_uint(__uint_as_float(o[4 * u + 3]) * inv));
+                        if (p.inside && hf != split) {
+                            fence_proxy_async();
+                            __syncwarp();
+                            const int box = 4 * kh + cc;
+                            if (lane == 0)
+                                bulk_push(cluster_address(base + C::join_box(box) + wr * 4096, other),
+                                          base + C::OFF_V + (uint32_t)(8 * hf + box) * 8192u + wr * 4096, 4096, theirs);
+                        }
+                    }
+                    if (!p.inside && (!one || (cc & 1))) {  // a box is staged: its store runs behind the next one's
                         fence_proxy_async();
                         __syncwarp();
-                        const int box = 4 * kh + cc;
-                        if (lane == 0)
-                            bulk_push(cluster_address(base + C::join_box(box) + wr * 4096, other),
-                                      base + C::OFF_V + (uint32_t)(8 * hf + box) * 8192u + wr * 4096, 4096, theirs);
+                        if (lane == 0) {
+                            const int box = one ? col >> 6 : col >> 5;
+                            tma_store_3d(one ? &tm_o : &tm_w, stage + (uint32_t)box * 8192u + wr * 4096,
+                                         one ? 64 * box : 32 * box, mt * BM + RM * rank + 32 * wr,
+                                         one ? list : split * p.ws_lists + list - p.ws_list0);
+                            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                        }
                     }
                 }
-                if (!p.inside && (!one || (cc & 1))) {  // a box is staged: its store runs behind the next one's
-                    fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) {
-                        const int box = one ? col >> 6 : col >> 5;
-                        tma_store_3d(one ? &tm_o : &tm_w, stage + (uint32_t)box * 8192u + wr * 4096,
-                                     one ? 64 * box : 32 * box, mt * BM + RM * rank + 32 * wr,
-                                     one ? list : split * p.ws_lists + list - p.ws_list0);
-                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                    }
-                }
+                // the stores have read shared memory before the CTA may end
+                if (!LOOP && lane == 0 && !p.inside) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                __syncwarp();
             }
-            // the stores have read shared memory before the CTA may end
-            if (!LOOP && lane == 0 && !p.inside) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-            __syncwarp();
-        }
-        if (kh == 0 && hf == 0 && (vrow || p.inside)) {
-            const float lse = (!ok || l == 0.f) ? -INFINITY : (m2 + __log2f(l)) * 0.69314718055994531f;
-            if (one)
-                p.lse[(size_t)list * p.M + mg] = lse;
-            else if (!p.inside)
-                p.ws_lse[((size_t)split * p.ws_lists + list - p.ws_list0) * p.M + mg] = lse;
-            else
-                st_shared_f1(base + C::OFF_P + 4 * row, lse);  // P is done with
-        }
-        owed = LOOP;
-        if (p.inside && kh == 0 && hf == 0) {
-            fence_proxy_async();
-            __syncwarp();
-            const int wr = wq & 1;
-            if (lane == 0)
-                bulk_push(cluster_address(base + C::OFF_P + 1024 + wr * 128, other), base + C::OFF_P + wr * 128, 128, theirs);
-            __syncwarp();
-        }
+            if (kh == 0 && hf == 0 && (vrow || p.inside)) {
+                const float lse = (!ok || l == 0.f) ? -INFINITY : (m2 + __log2f(l)) * 0.69314718055994531f;
+                if (one)
+                    p.lse[(size_t)list * p.M + mg] = lse;
+                else if (!p.inside)
+                    p.ws_lse[((size_t)split * p.ws_lists + list - p.ws_list0) * p.M + mg] = lse;
+                else
+                    st_shared_f1(base + C::OFF_P + 4 * row, lse);  // P is done with
+            }
+            owed = LOOP;
+            if (p.inside && kh == 0 && hf == 0) {
+                fence_proxy_async();
+                __syncwarp();
+                const int wr = wq & 1;
+                if (lane == 0)
+                    bulk_push(cluster_address(base + C::OFF_P + 1024 + wr * 128, other), base + C::OFF_P + wr * 128, 128, theirs);
+                __syncwarp();
+            }
         } while (enter());
         pay();
     } else if (FP8 && warp >= 4 + NSW) {
@@ -1586,8 +1586,8 @@ int64_t window_pages(const hs_pool *pool, int64_t T, int64_t H, int64_t window, 
 // Windows over BF16 rows with two units or more for each pair of CTAs: a pair takes them one
 // after the other and none is split. The next unit's queries and keys come, and its first
 // scores are multiplied, during the last one's end: 2 x 1,999 tokens of 16 heads, windows of
-// 1,024, LOOP_US against 145 us with a launch of its own for each unit (which takes 3 of a
-// unit's 20 us, and nothing runs while it ends).
+// 1,024, 124 us against 145 with a launch of its own for each unit (which takes 3 of a unit's
+// 20 us, and nothing runs while it ends).
 PagePlan window_plan(bool fp8, int64_t lists, int64_t T, int64_t H, int64_t N, bool &loop) {
     const int64_t mtiles = (T * H + BM - 1) / BM;
     loop = !fp8 && lists * mtiles >= 2 * pairs_at_once();
