@@ -483,6 +483,8 @@ size_t hs_weights_workspace_bytes(hs_pool_t pool, int32_t B, int32_t T, int32_t 
  *   d_freed / d_n_freed: the freed GPU blocks, [n][max_pages] and [n], in ascending page order
  *   flags     HS_EVICT_SAVED_ONLY: pages without a host copy are kept, as the first are;
  *             HS_EVICT_PLAN: the lists are written and nothing is released
+ * Rows of an evicted page without a host copy are gone; a block that several pages name is
+ * listed as often as it is freed, and counting its uses is the caller's.
  * One launch, asynchronous on `stream`; order it with what reads the same requests' pages. The
  * request ids are distinct. A bad one frees nothing and keeps no page (HS_DEVERR_BAD_REQUEST); a
  * negative budget frees nothing (HS_DEVERR_BAD_PAGE). */

@@ -19,7 +19,11 @@
 // power of two, which brings the row's largest to (224, 448], is the sum of two codes: exact
 // from 2^-9.8 of that largest on, off by at most 2^-17.8 of it below. The powers of all
 // rows are told to both CTAs.
-// Bound: the keys' bytes, or for 256 rows 36 MMAs of 128 clocks per tile.
+// Bound: the keys' bytes, or for 256 rows of codes 36 MMAs of 128 clocks per tile. 4 x 74,160 BF16
+// keys, 256 rows: 67 us, tiles at the copy rate from 8 us on; 8 x 131,072 FP8 keys, 512 rows: 316 to
+// 405 us with the clock, 1.93 to 1.52 PFLOP/s. The ring's place is divided out at each chunk
+// (counting it on instead changed nothing); pages asked into L2 two tiles ahead: 85 instead of
+// 67 us.
 // Every wait is bounded; on expiry the kernel sets HS_DEVERR_TIMEOUT, drains its own
 // copies and MMAs and returns.
 #include <cuda_bf16.h>
