@@ -500,6 +500,12 @@ _prob_dtypes: dict = {}
 def _prob_rows(name: str, t, B: int, rows: int, V: int):
     """Pointer, distance of rows and hs_prob_dtype of probabilities [B][rows][V], whose rows may
     lie further apart than V values, all equally far."""
+    try:  # one look, as in _arg
+        if (t.shape == (B, rows, V) and t.get_device() == _only_device and t.is_contiguous()
+                and B * rows > 0):
+            return t.data_ptr(), V, _prob_dtypes[t.dtype]
+    except (AttributeError, KeyError):
+        pass
     import torch
     if not _prob_dtypes:
         _prob_dtypes.update({torch.float32: HS_PROB_F32, torch.bfloat16: HS_PROB_BF16})

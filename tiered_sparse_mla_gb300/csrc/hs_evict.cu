@@ -10,9 +10,10 @@
 //   keys are in, added over the cluster, gives the bin that the border is in; as soon as
 //   a bin has no more than CANDS keys all CTAs take them and count (mostly after one
 //   histogram). With g pages above the border and e on it before a page, min(e, room) + g
-//   kept ones are before that page, so one exchange of the slices' counts places every page
-//   in the two lists. 16 requests of 16,384 pages: 14 us (one CTA of 1,024 threads for everything
-//   27 us; histograms of 2,048 bins, whose exchange takes 3 us each, 23 us). 64 pages: 3 us.
+//   kept ones are before that page; the histograms say g and e of the slices before.
+// 64 pages: 3.0 us; 16 requests of 16,384 pages: 12.2 us (one CTA of 1,024 threads for everything
+// 27; histograms of 2,048 bins, whose exchange takes 3 each, 23; the slices' counts in an
+// exchange of their own and loads behind the length 14.2).
 #include <atomic>
 #include <cstdint>
 
@@ -27,7 +28,7 @@ constexpr int ET = 512;        // threads per CTA
 constexpr int NW = ET / 32;
 constexpr int BINS = 512;      // one per thread
 constexpr int CANDS = 512;
-constexpr int CAP = 32768;     // keys of a slice that are kept in shared memory
+constexpr int CAP = 20480;     // keys of a slice that are kept in shared memory, with their blocks
 constexpr int MAXG = 8;
 constexpr uint32_t ABSENT = 0u, MUST = 0xffffffffu;
 
@@ -144,26 +145,42 @@ evict_few_kernel(const EvictParams p) {
     }
 }
 
-// A cluster of G CTAs per request, a slice of the pages each.
+// A cluster of G CTAs per request, a slice of the pages each: the same for any length, so that
+// its first pages are on their way before the length is known.
+constexpr int EARLY = 4;
+
 __global__ void __launch_bounds__(ET)
 evict_kernel(const EvictParams p, const int G) {
     hs::tc::grid_dep_wait();
     hs::tc::grid_dep_launch();
-    extern __shared__ uint32_t keys[];  // [cap] of the slice
+    extern __shared__ uint32_t keys[];  // [cap] of the slice, and their blocks
     __shared__ uint32_t hist[2][BINS];  // one is read by the others while the next is filled
     __shared__ uint32_t own[CANDS];     // the slice's candidates
     __shared__ __align__(16) uint32_t cands[CANDS];
-    __shared__ int32_t wsum[NW][3], s_bin, s_over, s_n;
+    __shared__ int32_t wsum[NW][3], s_bin, s_over, s_n, s_same;
     __shared__ uint32_t s_border, s_room, wkey[NW][2];
-    __shared__ int32_t counts[MAXG][4], parts[MAXG][3], lists[MAXG];  // of all CTAs
+    __shared__ int32_t counts[MAXG][4], lists[MAXG];  // of all CTAs
     const int i = blockIdx.x / G, rank = (int)hs::cluster_ctarank(), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int32_t *blocks = reinterpret_cast<int32_t *>(keys) + p.cap;
+    const int per = ((p.max_pages + 32 * G - 1) / (32 * G)) * 32, p0 = min(rank * per, p.max_pages), slots = min(per, p.max_pages - p0);
+    const int maybe = p.req[i], at_r = maybe >= 0 && maybe < p.max_req ? maybe : 0;
+    int2 *table = p.table + (size_t)at_r * p.max_pages;
+    const float *weights = p.weights + (size_t)at_r * p.max_pages;
+    float w_early[EARLY];
+    int2 t_early[EARLY];
+#pragma unroll
+    for (int u = 0; u < EARLY; ++u) {
+        const int k = tid + u * ET;
+        if (k < slots) {
+            w_early[u] = weights[p0 + k];
+            t_early[u] = table[p0 + k];
+        }
+    }
     int P, budget;
     const int r = request_of(p, i, rank == 0, P, budget);
     if (r < 0) return;  // the whole cluster
-    int2 *table = p.table + (size_t)r * p.max_pages;
-    const float *weights = p.weights + (size_t)r * p.max_pages;
     int32_t *kept = p.kept + (size_t)i * p.N, *freed = p.freed + (size_t)i * p.max_pages;
-    const int per = ((P + 32 * G - 1) / (32 * G)) * 32, p0 = min(rank * per, P), n = min(per, P - p0);
+    const int n = max(min(P - p0, slots), 0);
     auto key = [&](int k) {
         return k < p.cap ? keys[k] : key_at(p, p0 + k, P, weights[p0 + k], table[p0 + k]);
     };
@@ -171,17 +188,24 @@ evict_kernel(const EvictParams p, const int G) {
     if (tid == 0) s_n = 0;
     int cand = 0, must = 0;
     uint32_t lo = MUST, hi = ABSENT;  // of the keys that need not stay
-#pragma unroll 4
-    for (int k = tid; k < n; k += ET) {
-        const uint32_t x = key_at(p, p0 + k, P, weights[p0 + k], table[p0 + k]);
-        if (k < p.cap) keys[k] = x;
+    auto take = [&](int k, float w, int2 where) {
+        const uint32_t x = key_at(p, p0 + k, P, w, where);
+        if (k < p.cap) {
+            keys[k] = x;
+            blocks[k] = where.x;
+        }
         cand += x != ABSENT;
         must += x == MUST;
         if (x != ABSENT && x != MUST) {
             lo = min(lo, x);
             hi = max(hi, x);
         }
-    }
+    };
+#pragma unroll
+    for (int u = 0; u < EARLY; ++u)
+        if (tid + u * ET < n) take(tid + u * ET, w_early[u], t_early[u]);
+#pragma unroll 4
+    for (int k = tid + EARLY * ET; k < n; k += ET) take(k, weights[p0 + k], table[p0 + k]);
     cand = __reduce_add_sync(0xffffffffu, cand);
     must = __reduce_add_sync(0xffffffffu, must);
     lo = __reduce_min_sync(0xffffffffu, lo);
@@ -207,10 +231,16 @@ evict_kernel(const EvictParams p, const int G) {
     }
     hs::cluster_arrive();
     hs::cluster_wait();
+    // of all slices, and (..0) of those before this one
     cand = must = 0;
+    int cand0 = 0, must0 = 0;
     lo = MUST;
     hi = ABSENT;
     for (int g = 0; g < G; ++g) {
+        if (g == rank) {
+            cand0 = cand;
+            must0 = must;
+        }
         cand += counts[g][0];
         must += counts[g][1];
         lo = min(lo, (uint32_t)counts[g][2]);
@@ -218,13 +248,17 @@ evict_kernel(const EvictParams p, const int G) {
     }
     // of the pages that need not stay, the `need` of the largest keys do; a negative budget
     // frees nothing
-    const int others = cand - must, need = budget < 0 ? others : max(budget - must, 0);
+    const int others = cand - must, need = budget < 0 ? others : min(max(budget - must, 0), others);
     uint32_t border = ABSENT;  // keys above it stay, and of those equal to it the first `room`
     int room = 0;
+    int g0 = cand0, e0 = 0;  // keys above the border, and on it, before this slice
     if (need == 0) {
         border = MUST - 1;
+        g0 = must0;
     } else if (need < others) {
         int left = need, inside = others;  // of the keys in lo .. hi
+        int above = 0;                     // this thread's share of those above it before this slice
+        int same = cand0 - must0;          // before this slice, in lo .. hi
 #pragma unroll 1
         for (int d = 0; lo < hi && inside > CANDS; ++d) {
             const int wide = 32 - __clz((int)(hi - lo)), shift = wide > 9 ? wide - 9 : 0;
@@ -236,10 +270,15 @@ evict_kernel(const EvictParams p, const int G) {
             hs::cluster_arrive();
             hs::cluster_wait();
             // bins from the top, one a thread, over all slices
-            int mine = 0;
+            const int bin = BINS - 1 - tid;
+            int mine = 0, before = 0;
 #pragma unroll
             for (int g = 0; g < MAXG; ++g)
-                if (g < G) mine += hs::dsmem_ld(hs::dsmem_map(&h[BINS - 1 - tid], (uint32_t)g));
+                if (g < G) {
+                    const int x = hs::dsmem_ld(hs::dsmem_map(&h[bin], (uint32_t)g));
+                    mine += x;
+                    before += g < rank ? x : 0;
+                }
             int incl = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -251,19 +290,23 @@ evict_kernel(const EvictParams p, const int G) {
             __syncthreads();
             const int over = __reduce_add_sync(0xffffffffu, lane < warp ? wsum[lane][0] : 0) + incl - mine;  // in higher bins
             if (over < left && over + mine >= left) {
-                s_bin = BINS - 1 - tid;
+                s_bin = bin;
                 s_over = over;
                 s_n = mine;
+                s_same = before;
             }
             __syncthreads();
+            above += bin > s_bin ? before : 0;
             lo += (uint32_t)s_bin << shift;
             hi = min(hi, lo + ((1u << shift) - 1u));
             left -= s_over;
             inside = s_n;
+            same = s_same;
             __syncthreads();
         }
         border = lo;  // where one key is left
         room = left;
+        int on = 0;
         if (lo < hi) {
             if (tid == 0) s_n = 0;
             __syncthreads();
@@ -275,7 +318,7 @@ evict_kernel(const EvictParams p, const int G) {
             if (tid < G) hs::dsmem_st(hs::dsmem_map(&lists[rank], (uint32_t)tid), s_n);
             hs::cluster_arrive();
             hs::cluster_wait();
-            // all slices' candidates: any order, the border is a value
+            // all slices' candidates, slice by slice; within one in any order
             cands[tid] = ABSENT;
             __syncthreads();
             int at = 0;
@@ -285,16 +328,17 @@ evict_kernel(const EvictParams p, const int G) {
                 at += m;
             }
             __syncthreads();
+            uint32_t x = ABSENT;
             if (tid < inside) {
-                const uint32_t x = cands[tid];
+                x = cands[tid];
                 const uint4 *c4 = reinterpret_cast<const uint4 *>(cands);
-                int more = 0, same = 0;
+                int more = 0, equal = 0;
                 for (int k = 0; k < inside; k += 4) {
                     const uint4 v = c4[k >> 2];
                     more += (v.x > x) + (v.y > x) + (v.z > x) + (v.w > x);
-                    same += (v.x == x) + (v.y == x) + (v.z == x) + (v.w == x);
+                    equal += (v.x == x) + (v.y == x) + (v.z == x) + (v.w == x);
                 }
-                if (more < left && more + same >= left) {  // equal ones write the same
+                if (more < left && more + equal >= left) {  // equal ones write the same
                     s_border = x;
                     s_room = (uint32_t)(left - more);
                 }
@@ -302,8 +346,24 @@ evict_kernel(const EvictParams p, const int G) {
             __syncthreads();
             border = s_border;
             room = (int)s_room;
+            if (tid < same) {  // those of the slices before this one come first
+                above += x > border;
+                on = x == border;
+            }
         }
+        above = __reduce_add_sync(0xffffffffu, above);
+        on = __reduce_add_sync(0xffffffffu, on);
+        if (lane == 0) {
+            wsum[warp][0] = above;
+            wsum[warp][1] = on;
+        }
+        __syncthreads();
+        above = __reduce_add_sync(0xffffffffu, lane < NW ? wsum[lane][0] : 0);
+        on = __reduce_add_sync(0xffffffffu, lane < NW ? wsum[lane][1] : 0);
+        g0 = must0 + above;
+        e0 = lo < hi ? on : same;
     }
+    hs::cluster_arrive();  // the last that this CTA reads of another
 
     // each warp a run of rows of 32 pages: how many are above the border, on it, there at all
     const int rows = (n + 31) / 32, row0 = rows * warp / NW, row1 = rows * (warp + 1) / NW;
@@ -318,18 +378,7 @@ evict_kernel(const EvictParams p, const int G) {
     __syncthreads();  // wsum has been read
     if (lane < 3) wsum[warp][lane] = lane == 0 ? g_n : (lane == 1 ? e_n : a_n);
     __syncthreads();
-    if (tid < 3 * G) {
-        int sum = 0;
-        for (int w = 0; w < NW; ++w) sum += wsum[w][tid % 3];
-        hs::dsmem_st(hs::dsmem_map(&parts[rank][tid % 3], (uint32_t)(tid / 3)), sum);
-    }
-    hs::cluster_arrive();
-    hs::cluster_wait();  // the last that any CTA reads or writes of another
-    int g = 0, e = 0, a = 0, g_all = 0, e_all = 0, a_all = 0;
-    for (int c = 0; c < G; ++c) {
-        if (c < rank) g += parts[c][0], e += parts[c][1], a += parts[c][2];
-        g_all += parts[c][0], e_all += parts[c][1], a_all += parts[c][2];
-    }
+    int g = g0, e = e0, a = cand0;
     for (int w = 0; w < warp; ++w) g += wsum[w][0], e += wsum[w][1], a += wsum[w][2];
     for (int row = row0; row < row1; ++row) {
         const int k = 32 * row + lane, page = p0 + k;
@@ -340,19 +389,20 @@ evict_kernel(const EvictParams p, const int G) {
         if (isg || (ise && on < room)) {
             if (before < p.N) kept[before] = page;
         } else if (isa) {
-            freed[a + __popc(ba & lower) - before] = table[page].x;
+            freed[a + __popc(ba & lower) - before] = k < p.cap ? blocks[k] : table[page].x;
             if (!p.plan) table[page].x = -1;
         }
         g += __popc(bg);
         e += __popc(be);
         a += __popc(ba);
     }
-    const int stay = g_all + min(e_all, room);
+    const int stay = must + need;
     for (int k = stay + rank * ET + tid; k < p.N; k += G * ET) kept[k] = -1;
     if (rank == 0 && tid == 0) {
-        p.n_freed[i] = a_all - stay;
+        p.n_freed[i] = cand - stay;
         if (stay > p.N) atomicOr(p.err, HS_DEVERR_CAPACITY);
     }
+    hs::cluster_wait();  // nobody reads this CTA's memory any more
 }
 
 }  // namespace
@@ -371,7 +421,7 @@ extern "C" hs_status hs_evict_pages(hs_pool_t pool, int32_t n, int32_t N, int32_
     static std::atomic<int> state[64];
     if (dev < 0 || dev >= 64) return HS_ERR_UNSUPPORTED;
     if (state[dev].load(std::memory_order_acquire) != 1) {
-        HS_CUDA_TRY(cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, CAP * 4));
+        HS_CUDA_TRY(cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, CAP * 8));
         state[dev].store(1, std::memory_order_release);
     }
     EvictParams p{};
@@ -401,7 +451,7 @@ extern "C" hs_status hs_evict_pages(hs_pool_t pool, int32_t n, int32_t N, int32_
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(few ? n : n * G), 1, 1);
     cfg.blockDim = dim3(ET, 1, 1);
-    cfg.dynamicSmemBytes = few ? 0 : (size_t)p.cap * 4;
+    cfg.dynamicSmemBytes = few ? 0 : (size_t)p.cap * 8;
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
