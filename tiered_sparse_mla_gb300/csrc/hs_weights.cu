@@ -10,7 +10,10 @@
 // key's sum runs along the registers of the threads that own it, and query rows its N
 // columns, half of them supplied by either CTA. The queries stay in shared memory (up to
 // 144 KB a CTA), the keys stream past once, and one tile's exponentials run while the next
-// is multiplied (two accumulators). Several groups' sums meet in a second grid.
+// is multiplied (two accumulators). Several groups' sums meet in a second grid. Up to 128
+// query rows leave room for two requests' queries: where a range goes on to another request
+// these come, and are made codes of, during the tiles before (16 x 3,000 FP8 keys, 16 rows
+// each: 19.6 -> 15.2 us; 40 x 1,000, 32 rows: 19.8 -> 14.9).
 //   warp 0      producer: queries where the range comes to another request, key chunks;
 //   warp 1      (CTA 0) MMA issuer;
 //   warps 2-9   per request: the columns' terms (FP8: the queries as codes); per tile:
@@ -54,24 +57,24 @@ constexpr int SMEM_MOST = 232448;
 template <bool FP8>
 struct WCfg {
     static constexpr int STAGE = FP8 ? 128 * 64 : 128 * 128;
-    static constexpr int OFF_B = 0;                               // f32 [256]: -lse, in log2 units
-    static constexpr int OFF_A = OFF_B + MAXN * 4;                // FP8 f32 [2][256]: scale over the row's power
-    static constexpr int OFF_X = OFF_A + (FP8 ? 2 * MAXN * 4 : 0);  // FP8 u32 [256]: halves of the rows' maxima
+    static constexpr int OFF_A = 0;                               // FP8 f32 [3][256]: scale over the row's power
+    static constexpr int OFF_X = OFF_A + (FP8 ? 3 * MAXN * 4 : 0);  // FP8 u32 [256]: parts of the rows' maxima
     static constexpr int OFF_PS = OFF_X + (FP8 ? MAXN * 4 : 0);   // f32 [2][8]: sums of a tile, by warp
-    static constexpr int OFF_DEAD = OFF_PS + 2 * NEW * 4;         // u32 [8]: columns that add nothing
-    static constexpr int OFF_MISC = OFF_DEAD + 32;                // TMEM base, abort flag
+    static constexpr int OFF_DEAD = OFF_PS + 2 * NEW * 4;         // u32 [2][8]: columns that add nothing
+    static constexpr int OFF_MISC = OFF_DEAD + 64;                // TMEM base, abort flag
     static constexpr int OFF_BAR = OFF_MISC + 16;
-    static constexpr int B_QFULL = 0, B_QREADY = 1, B_QFREE = 2, B_TAB = 3, B_DRAIN = 4, B_DFULL = 5, B_DFREE = 7,
-                         B_FULL = 9, B_FREE = B_FULL + MAXST, NBAR = B_FREE + MAXST;
-    static constexpr int HEAD = (OFF_BAR + 8 * NBAR + 15) & ~15;
-    __host__ __device__ static int stages(int N) {
-        const int room = SMEM_MOST - 1024 - HEAD - NCH * (N / 2) * 128, n = room / STAGE;
+    static constexpr int B_QFULL = 0, B_QREADY = 2, B_QFREE = 4, B_TAB = 5, B_DRAIN = 6, B_DFULL = 7, B_DFREE = 9,
+                         B_FULL = 11, B_FREE = B_FULL + MAXST, NBAR = B_FREE + MAXST;
+    static constexpr int OFF_B = (OFF_BAR + 8 * NBAR + 15) & ~15;  // f32 [1, deep: 2][256]: -lse, in log2 units
+    __host__ __device__ static int head(bool deep) { return OFF_B + (deep ? 2 : 1) * MAXN * 4; }
+    __host__ __device__ static int stages(int N, bool deep) {
+        const int room = SMEM_MOST - 1024 - head(deep) - (deep ? 2 : 1) * NCH * (N / 2) * 128, n = room / STAGE;
         return n < MAXST ? n : MAXST;
     }
     static_assert(OFF_BAR % 8 == 0 && OFF_A % 16 == 0, "alignment");
 };
-static_assert((SMEM_MOST - 1024 - WCfg<false>::HEAD - NCH * 128 * 128) / WCfg<false>::STAGE >= 4, "ring");
-static_assert((SMEM_MOST - 1024 - WCfg<true>::HEAD - NCH * 128 * 128) / WCfg<true>::STAGE >= 8, "ring");
+static_assert((SMEM_MOST - 1024 - WCfg<false>::OFF_B - 2048 - NCH * 128 * 128) / WCfg<false>::STAGE >= 4, "ring");
+static_assert((SMEM_MOST - 1024 - WCfg<true>::OFF_B - 2048 - NCH * 128 * 128) / WCfg<true>::STAGE >= 8, "ring");
 
 struct WeightParams {
     const int32_t *req, *ctx;
@@ -86,6 +89,7 @@ struct WeightParams {
     int B, T, H, M, groups, parts, N, nst;
     int max_req, max_pages, max_ctx, zero_block;
     float scale_log2, decay;
+    bool deep;                    // two requests' queries have room: the next one's come and are made codes of ahead
 };
 
 __device__ __forceinline__ int pages_of(int tokens) { return tokens <= 0 ? 0 : (tokens - 1) / kPage + 1; }
@@ -145,7 +149,8 @@ weight_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t raw = hs::smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;  // queries, ring, then the small things
-    const uint32_t ring = base + NCH * (uint32_t)(p.N / 2) * 128u, head = ring + (uint32_t)(p.nst * C::STAGE);
+    const uint32_t qall = NCH * (uint32_t)(p.N / 2) * 128u;
+    const uint32_t ring = base + (p.deep ? 2u : 1u) * qall, head = ring + (uint32_t)(p.nst * C::STAGE);
     uint8_t *small = smem_raw + (head - raw);
     volatile int32_t *misc = reinterpret_cast<volatile int32_t *>(small + C::OFF_MISC);
     auto bar = [&](int i) { return head + C::OFF_BAR + 8u * (uint32_t)i; };
@@ -161,7 +166,7 @@ weight_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::NBAR; ++i) {
             uint32_t n = 1;
-            if (i == C::B_QREADY || i == C::B_DFREE || i == C::B_DFREE + 1 || i == C::B_TAB) n = 2 * NEW;  // both CTAs'
+            if (i == C::B_QREADY || i == C::B_QREADY + 1 || i == C::B_DFREE || i == C::B_DFREE + 1 || i == C::B_TAB) n = 2 * NEW;  // both CTAs'
             mbar_init(bar(i), n);
         }
         misc[1] = 0;
@@ -265,15 +270,18 @@ weight_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             next(nx);
             const int2 *table = p.table + (size_t)w.r * p.max_pages;
             const int pages = pages_of(w.L);
+            // request b's, segment x of the range, into its place
+            auto queries = [&](int b, uint32_t x) {
+                const uint32_t at = base + (p.deep ? (x & 1u) * qall : 0u);
+                mbar_expect_tx(bar(C::B_QFULL + (int)(x & 1u)), qall);
+                for (int c = 0; c < NCH; ++c)
+                    tma_load_3d(at + c * qch, &tm_q, 64 * c, g * MAXN + rank * (p.N / 2), b, bar(C::B_QFULL + (int)(x & 1u)));
+                qn = x + 1;
+            };
             if (lane == 0) {
                 // the MMAs of the request before are done with the queries' place
-                if (seg > 0) ok = mbar_wait_inline(bar(C::B_QFREE), (seg - 1) & 1u);
-                if (ok) {
-                    mbar_expect_tx(bar(C::B_QFULL), NCH * qch);
-                    for (int c = 0; c < NCH; ++c)
-                        tma_load_3d(base + c * qch, &tm_q, 64 * c, g * MAXN + rank * (p.N / 2), w.b, bar(C::B_QFULL));
-                    ++qn;
-                }
+                if (!p.deep && seg > 0) ok = mbar_wait_inline(bar(C::B_QFREE), (seg - 1) & 1u);
+                if (ok && (!p.deep || seg == 0)) queries(w.b, seg);
             }
             int blk = 0;
             for (int i = 0; i < w.n; ++i) {
@@ -295,6 +303,10 @@ weight_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                         tma_load_pair(ring + s * C::STAGE, &tm_k, 0, row0, c, lead(C::B_FULL + (int)s));
                         tma_load_pair(ring + s * C::STAGE + C::STAGE / 2, &tm_k, 0, row1, c, lead(C::B_FULL + (int)s));
                     }
+                    if (p.deep && i == 0 && ok) {
+                        if (seg > 0) ok = mbar_wait_inline(bar(C::B_QFREE), (seg - 1) & 1u);
+                        if (ok && nx.n > 0) queries(nx.b, seg + 1);
+                    }
                 }
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok) break;
@@ -304,7 +316,7 @@ weight_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         }
         if (lane == 0) {
             // the copies begun have landed before the CTA may end
-            if (qn > 0) mbar_wait_inline(bar(C::B_QFULL), (qn - 1) & 1u);
+            for (uint32_t k = qn > 2 ? qn - 2 : 0; k < qn; ++k) mbar_wait_inline(bar(C::B_QFULL + (int)(k & 1u)), (k >> 1) & 1u);
             if (!ok) {
                 fail();
                 for (uint32_t k = 0, v = u; rank == 0 && k < nst && v > 0; ++k) {
@@ -325,8 +337,12 @@ weight_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             uint32_t u = 0, i = 0, seg = 0;
             const uint32_t last_u = tiles * NCH;
             for (Walk w = begin; w.n > 0 && ok; ++seg) {
-                ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_QREADY), seg & 1u));
+                ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_QREADY + (int)(seg & 1u)), (seg >> 1) & 1u));
                 if (!ok) break;
+                // the last request's place: given back only now, so that no query barrier is two
+                // phases ahead of those who wait for it
+                if (p.deep && seg > 0 && leader) commit_both(bar(C::B_QFREE));
+                const uint32_t q0 = lo + ((p.deep ? (seg & 1u) * qall : 0u) >> 4);
                 for (int j = 0; j < w.n && ok; ++j, ++i) {
                     if (i >= 2)
                         ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_DFREE + (int)(i & 1)), ((i >> 1) & 1u) ^ 1u));
@@ -338,7 +354,7 @@ weight_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                         if (!ok) break;
                         tc_fence_after();
                         if (leader) {
-                            const uint32_t a = lo + ((ring - base + s * C::STAGE) >> 4), q = lo + ((c * qch) >> 4);
+                            const uint32_t a = lo + ((ring - base + s * C::STAGE) >> 4), q = q0 + ((c * qch) >> 4);
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 if (FP8)  // both codes of the queries with the same 32 codes of the keys
@@ -355,7 +371,7 @@ weight_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                     __syncwarp();
                 }
                 next(w);
-                if (ok && w.n > 0 && leader) commit_both(bar(C::B_QFREE));
+                if (!p.deep && ok && w.n > 0 && leader) commit_both(bar(C::B_QFREE));
                 __syncwarp();
             }
             if (!ok && lane == 0) fail();
@@ -376,81 +392,97 @@ weight_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         volatile uint32_t *dead = reinterpret_cast<volatile uint32_t *>(small + C::OFF_DEAD);
         const bool writer = hf == 0 && (wq & 1) == 0 && lane == 0;  // of one page of the tile
         bool ok = true;
-        uint32_t i = 0, seg = 0;
-        for (Walk w = begin; w.n > 0; next(w), ++seg) {
-            // columns' terms; all warps are done with those of the request before
-            {
+        uint32_t i = 0, seg = 0, ready = 0, tabs = 0;  // segments begun, made ready; tables of both CTAs seen
+        auto see_tables = [&](uint32_t upto) {
+            for (; FP8 && tabs <= upto; ++tabs)
+                if (ok) ok = __all_sync(0xffffffffu, mbar_wait_cluster(bar(C::B_TAB), tabs & 1u));
+        };
+        Walk w = begin, nx = begin;  // nx: the next to make ready
+        while (w.n > 0) {
+            if (nx.n > 0 && ready <= seg + (p.deep ? 1u : 0u)) {
+                // A request's columns: the terms of its lse, and (FP8) its queries as codes. All
+                // warps are done with the tiles before this segment's; the peer has made this
+                // one ready, so it is done with the tables of the one before the last.
+                if (ready > 0) see_tables(ready - 1);
                 const int m = g * MAXN + tid;
-                float v = tid < p.N && m < p.M ? p.lse[(size_t)w.b * p.M + m] : 0.f;
+                const float v = tid < p.N && m < p.M ? p.lse[(size_t)nx.b * p.M + m] : 0.f;
                 const bool fin = fabsf(v) < INFINITY;
-                const uint32_t out = __ballot_sync(0xffffffffu, !fin);
-                if (seg > 0) named_bar_sync(1, 32 * NEW);
-                if (tid < p.N) st_shared_f1(head + C::OFF_B + 4 * tid, fin && m < p.M ? -v * 1.4426950408889634f : -INFINITY);
-                if (lane == 0) dead[warp - 2] = out;
-            }
-            if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_QFULL), seg & 1u));
-            const uint32_t tab = head + C::OFF_A + (seg & 1u) * MAXN * 4;
-            if (FP8) {
-                // thread = (row of this CTA's half, half of its chunks)
-                const int row = tid & 127, half = tid >> 7;
-                const bool in = row < p.N / 2;
-                auto q_at = [&](int c) { return base + c * qch + row * 128; };
-                uint32_t m = 0;  // the row's largest magnitude; NaN if there is one
-                if (ok && in) {
+                const uint32_t out = __ballot_sync(0xffffffffu, !fin), odd = p.deep ? ready & 1u : 0u;
+                if (tid < p.N)
+                    st_shared_f1(head + C::OFF_B + 4 * (odd * MAXN + tid), fin && m < p.M ? -v * 1.4426950408889634f : -INFINITY);
+                if (lane == 0) dead[8 * odd + warp - 2] = out;
+                if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_QFULL + (int)(ready & 1u)), (ready >> 1) & 1u));
+                if (FP8) {
+                    // thread = (row of this CTA's half, part of its chunks): as many parts as the
+                    // threads allow
+                    const int rows = p.N / 2, parts = 32 * NEW / rows, row = tid % rows, part = tid / rows;
+                    const bool in = part < parts;
+                    const uint32_t q0 = base + odd * qall + row * 128;
+                    auto q_at = [&](int c) { return q0 + c * qch; };
+                    uint32_t top = 0;  // the row's largest magnitude; NaN if there is one
+                    if (ok && in) {
 #pragma unroll 1
-                    for (int c = half; c < NCH; c += 2)
+                        for (int c = part; c < NCH; c += parts)
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const uint4 v = ld_shared_v4(q_at(c) + ((k ^ (row & 7)) << 4));
-                            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+                            for (int k = 0; k < 8; ++k) {
+                                const uint4 x4 = ld_shared_v4(q_at(c) + ((k ^ (row & 7)) << 4));
+                                const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w};
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(x[e] & 0x7fff7fffu));
-                        }
-                }
-                // bits of magnitudes are in their order, infinities and NaN above all
-                st_shared_b32(head + C::OFF_X + 4 * tid, max(m & 0xffffu, m >> 16));
-                named_bar_sync(1, 32 * NEW);
-                const uint32_t top = max(ld_shared_b32(head + C::OFF_X + 4 * row), ld_shared_b32(head + C::OFF_X + 4 * (row + 128)));
-                // times 2^k it lies in (224, 448]; a row that is not finite becomes NaN
-                const int k2 = min(135 - (int)(top >> 7) - ((top & 0x7fu) > 0x60u), 126);
-                const uint32_t pow2 = top >= 0x7f80u ? 0x7fc07fc0u : (uint32_t)(k2 + 127) * 0x00800080u;
-                if (ok && in) {
+                                for (int e = 0; e < 4; ++e) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(top) : "r"(x[e] & 0x7fff7fffu));
+                            }
+                    }
+                    // bits of magnitudes are in their order, infinities and NaN above all
+                    named_bar_sync(1, 32 * NEW);  // the last request's have been read
+                    st_shared_b32(head + C::OFF_X + 4 * tid, max(top & 0xffffu, top >> 16));
+                    named_bar_sync(1, 32 * NEW);
+                    top = 0;
+                    for (int k = 0; k < parts; ++k) top = max(top, ld_shared_b32(head + C::OFF_X + 4 * (k * rows + row)));
+                    // times 2^k it lies in (224, 448]; a row that is not finite becomes NaN
+                    const int k2 = min(135 - (int)(top >> 7) - ((top & 0x7fu) > 0x60u), 126);
+                    const uint32_t pow2 = top >= 0x7f80u ? 0x7fc07fc0u : (uint32_t)(k2 + 127) * 0x00800080u;
+                    if (ok && in) {
 #pragma unroll 1
-                    for (int c = half; c < NCH; c += 2) {
-                        uint32_t r[16];  // first codes go where values have been read
+                        for (int c = part; c < NCH; c += parts) {
+                            uint32_t r[16];  // first codes go where values have been read
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint4 x = ld_shared_v4(q_at(c) + (((2 * k) ^ (row & 7)) << 4));
-                            const uint4 y = ld_shared_v4(q_at(c) + (((2 * k + 1) ^ (row & 7)) << 4));
-                            uint32_t z[4];
-                            four_codes(x.x, x.y, pow2, z[0], r[4 * k]);
-                            four_codes(x.z, x.w, pow2, z[1], r[4 * k + 1]);
-                            four_codes(y.x, y.y, pow2, z[2], r[4 * k + 2]);
-                            four_codes(y.z, y.w, pow2, z[3], r[4 * k + 3]);
-                            st_shared_v4(q_at(c) + ((k ^ (row & 7)) << 4), z[0], z[1], z[2], z[3]);
+                            for (int k = 0; k < 4; ++k) {
+                                const uint4 x = ld_shared_v4(q_at(c) + (((2 * k) ^ (row & 7)) << 4));
+                                const uint4 y = ld_shared_v4(q_at(c) + (((2 * k + 1) ^ (row & 7)) << 4));
+                                uint32_t z[4];
+                                four_codes(x.x, x.y, pow2, z[0], r[4 * k]);
+                                four_codes(x.z, x.w, pow2, z[1], r[4 * k + 1]);
+                                four_codes(y.x, y.y, pow2, z[2], r[4 * k + 2]);
+                                four_codes(y.z, y.w, pow2, z[3], r[4 * k + 3]);
+                                st_shared_v4(q_at(c) + ((k ^ (row & 7)) << 4), z[0], z[1], z[2], z[3]);
+                            }
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                st_shared_v4(q_at(c) + (((4 + k) ^ (row & 7)) << 4), r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
                         }
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            st_shared_v4(q_at(c) + (((4 + k) ^ (row & 7)) << 4), r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+                    }
+                    if (part == 0) {
+                        const float a = p.scale_log2 * __uint_as_float((uint32_t)(127 - k2) << 23);
+                        const uint32_t at = head + C::OFF_A + 4 * ((ready % 3u) * MAXN + (uint32_t)(rank * rows + row));
+                        st_shared_f1(at, a);
+                        st_cluster_f1(cluster_address(at, (uint32_t)rank ^ 1u), a);
+                    }
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive_remote(cluster_address(bar(C::B_TAB), 0));
+                        mbar_arrive_remote(cluster_address(bar(C::B_TAB), 1));
                     }
                 }
-                if (in && half == 0) {
-                    const float a = p.scale_log2 * __uint_as_float((uint32_t)(127 - k2) << 23);
-                    const uint32_t at = tab + 4 * (uint32_t)(rank * (p.N / 2) + row);
-                    st_shared_f1(at, a);
-                    st_cluster_f1(cluster_address(at, (uint32_t)rank ^ 1u), a);
-                }
-                fence_proxy_async();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive_remote(cluster_address(bar(C::B_TAB), 0));
-                    mbar_arrive_remote(cluster_address(bar(C::B_TAB), 1));
-                }
+                if (lane == 0) mbar_arrive_peer(lead(C::B_QREADY + (int)(ready & 1u)));
+                next(nx);
+                ++ready;
+                if (p.deep && ready == 1 && nx.n > 0) continue;  // the first two
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive_peer(lead(C::B_QREADY));
-            if (FP8 && ok) ok = __all_sync(0xffffffffu, mbar_wait_cluster(bar(C::B_TAB), seg & 1u));
+            see_tables(seg);
             named_bar_sync(1, 32 * NEW);  // the columns' terms are there
+            const uint32_t odd = p.deep ? seg & 1u : 0u, tab = head + C::OFF_A + (seg % 3u) * MAXN * 4;
+            const uint32_t terms = head + C::OFF_B + odd * MAXN * 4;
 
             const int pages = pages_of(w.L), draft = w.L - p.T;
             const int2 *table = p.table + (size_t)w.r * p.max_pages;
@@ -479,13 +511,13 @@ weight_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                         uint32_t d[32];
                         HS_TMEM_LD32(tmem + lane_off + (i & 1) * (uint32_t)p.N + c0, d);
                         HS_TMEM_WAIT_LD32(d);
-                        const uint32_t gone = dead[c0 >> 5];
+                        const uint32_t gone = dead[8 * odd + (c0 >> 5)];
                         // the columns that count: with a key that is not finite the others hold NaN
                         const uint32_t live = ~gone & (c_hi - c0 < 32 ? (1u << (c_hi - c0)) - 1u : ~0u);
                         auto sums = [&](auto whole) {
 #pragma unroll
                             for (int e = 0; e < 32; e += 4) {
-                                const float4 b = ld_shared_f4(head + C::OFF_B + 4 * (c0 + e));
+                                const float4 b = ld_shared_f4(terms + 4 * (c0 + e));
                                 float a0 = ks, a1 = ks, a2 = ks, a3 = ks;
                                 if (FP8) {  // the two scales first: their product with a sum may be the only one in range
                                     const float4 a = ld_shared_f4(tab + 4 * (c0 + e));
@@ -522,7 +554,7 @@ weight_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                             bool seen = sees(t);
 #pragma unroll
                             for (int e = 0; e < 32; ++e) {
-                                const float b = ld_shared_f1(head + C::OFF_B + 4 * (c0 + e));
+                                const float b = ld_shared_f1(terms + 4 * (c0 + e));
                                 const float a = FP8 ? ks * ld_shared_f1(tab + 4 * (c0 + e)) : ks;
                                 const float y = ex2(fmaf(__uint_as_float(d[e]), a, b));
                                 s0 += seen && ((live >> e) & 1u) ? y : 0.f;
@@ -552,6 +584,8 @@ weight_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 }
                 blk = blk_next;
             }
+            next(w);
+            ++seg;
         }
         if (!ok && lane == 0) fail();
     }
@@ -633,7 +667,8 @@ hs_status launch_weights(int dev, cudaStream_t s, const CUtensorMap &tk, const C
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * p.groups * p.parts), 1, 1);
     cfg.blockDim = dim3(WT, 1, 1);
-    cfg.dynamicSmemBytes = (size_t)(1024 + NCH * (p.N / 2) * 128 + p.nst * WCfg<FP8>::STAGE + WCfg<FP8>::HEAD);
+    cfg.dynamicSmemBytes =
+        (size_t)(1024 + (p.deep ? 2 : 1) * NCH * (p.N / 2) * 128 + p.nst * WCfg<FP8>::STAGE + WCfg<FP8>::head(p.deep));
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -685,7 +720,8 @@ extern "C" hs_status hs_page_weights(hs_pool_t pool, int32_t B, int32_t T, int32
     p.M = T * H;
     p.groups = groups_of(p.M);
     p.N = p.M < MAXN ? (p.M + 63) & ~63 : MAXN;
-    p.nst = fp8 ? WCfg<true>::stages(p.N) : WCfg<false>::stages(p.N);
+    p.deep = B > 1 && p.N <= MAXN / 2;
+    p.nst = fp8 ? WCfg<true>::stages(p.N, p.deep) : WCfg<false>::stages(p.N, p.deep);
     const int64_t tiles = (int64_t)B * ((pool->max_pages + TP - 1) / TP);
     // the keys' bytes at the card's rate, or the products
     const double us_mma = 2.5 * p.N / 256, us_bytes = (fp8 ? 148e3 : 295e3) / 85e3;
