@@ -10,23 +10,28 @@
 // key's sum runs along the registers of the threads that own it, and query rows its N
 // columns, half of them supplied by either CTA. The queries stay in shared memory (up to
 // 144 KB a CTA), the keys stream past once, and one tile's exponentials run while the next
-// is multiplied (two accumulators). Several groups' sums meet in a second grid. Up to 128
-// query rows leave room for two requests' queries: where a range goes on to another request
-// these come, and are made codes of, during the tiles before (16 x 3,000 FP8 keys, 16 rows
-// each: 19.6 -> 15.2 us; 40 x 1,000, 32 rows: 19.8 -> 14.9).
-//   warp 0      producer: queries where the range comes to another request, key chunks;
-//   warp 1      (CTA 0) MMA issuer;
-//   warps 2-9   per request: the columns' terms (FP8: the queries as codes); per tile:
-//               the sums, thread = key and half of the columns.
+// is multiplied (two accumulators). Several groups' sums meet in a second grid; the rows are
+// dealt to them evenly (12 x 27,929 FP8 keys, 264 rows: 64 us with 160 columns each, 79 with 192;
+// 16 rows of 16 x 3,000: 11.4 with 32 columns, 12.7 with 64). Where a
+// range goes on to another request, each chunk of its queries comes as soon as the last tile's
+// MMAs have read that chunk of the one before (8 x 8,000 BF16 keys, 512 rows: 34.2 -> 30.7 us
+// against all chunks after the last tile; a second place for them, up to 128 rows, changes nothing).
+//   warp 0      producer: key chunks;
+//   warp 1      (CTA 0) MMA issuer: one lane, waits and all. With the warp's 32 lanes agreeing on each wait
+//               it cannot keep up with chunks of 192 or fewer columns (4 x 20,000 BF16 keys, 528 rows: 48 us
+//               instead of 39);
+//   warps 2-9   per request: the columns' terms; per tile: the sums, thread = key and half of
+//               the columns;
+//   warp 10     producer: queries.
 // FP8: scores from the e4m3 codes themselves (kind::f8f6f4). A query value times its row's
 // power of two, which brings the row's largest to (224, 448], is the sum of two codes: exact
-// from 2^-9.8 of that largest on, off by at most 2^-17.8 of it below. The powers of all
-// rows are told to both CTAs.
+// from 2^-9.8 of that largest on, off by at most 2^-17.8 of it below. A grid of its own makes the
+// codes of each row once, in the workspace; pairs that did so for themselves at each request took
+// 4 to 5 us each time (30 x 6,000 keys, 256 rows: 46 -> 37 us; 40 x 1,000, 32 rows: 15.0 -> 12.8).
+// Only 64 x 500 keys, 256 rows, where every pair has one request, were faster so (22 against 24).
 // Bound: the keys' bytes, or for 256 rows of codes 36 MMAs of 128 clocks per tile. 4 x 74,160 BF16
-// keys, 256 rows: 67 us, tiles at the copy rate from 8 us on; 8 x 131,072 FP8 keys, 512 rows: 316 to
-// 405 us with the clock, 1.93 to 1.52 PFLOP/s. The ring's place is divided out at each chunk
-// (counting it on instead changed nothing); pages asked into L2 two tiles ahead: 85 instead of
-// 67 us.
+// keys, 256 rows: 64 us, tiles at the copy rate from 8 us on; 8 x 131,072 FP8 keys, 512 rows: 312 to
+// 405 us with the clock, 1.94 to 1.52 PFLOP/s. Pages asked into L2 two tiles ahead: 85 instead of 67 us.
 // Every wait is bounded; on expiry the kernel sets HS_DEVERR_TIMEOUT, drains its own
 // copies and MMAs and returns.
 #include <cuda_bf16.h>
@@ -50,35 +55,35 @@ constexpr int TP = 4;            // pages per tile (two CTAs)
 constexpr int NCH = kDim / 64;   // depth chunks
 constexpr int MAXN = 256;        // query rows per group
 constexpr int NEW = 8;           // warps for the sums
-constexpr int WT = 64 + 32 * NEW;
+constexpr int WT = 96 + 32 * NEW;
 constexpr int MAXST = 16;        // ring stages, one chunk of 128 keys each
 constexpr int SMEM_MOST = 232448;
 
 template <bool FP8>
 struct WCfg {
     static constexpr int STAGE = FP8 ? 128 * 64 : 128 * 128;
-    static constexpr int OFF_A = 0;                               // FP8 f32 [3][256]: scale over the row's power
-    static constexpr int OFF_X = OFF_A + (FP8 ? 3 * MAXN * 4 : 0);  // FP8 u32 [256]: parts of the rows' maxima
-    static constexpr int OFF_PS = OFF_X + (FP8 ? MAXN * 4 : 0);   // f32 [2][8]: sums of a tile, by warp
-    static constexpr int OFF_DEAD = OFF_PS + 2 * NEW * 4;         // u32 [2][8]: columns that add nothing
-    static constexpr int OFF_MISC = OFF_DEAD + 64;                // TMEM base, abort flag
+    static constexpr int OFF_A = 0;                               // FP8 f32 [256]: scale over the rows' powers
+    static constexpr int OFF_B = OFF_A + (FP8 ? MAXN * 4 : 0);    // f32 [256]: -lse, in log2 units
+    static constexpr int OFF_PS = OFF_B + MAXN * 4;               // f32 [2][8]: sums of a tile, by warp
+    static constexpr int OFF_DEAD = OFF_PS + 2 * NEW * 4;         // u32 [8]: columns that add nothing
+    static constexpr int OFF_MISC = OFF_DEAD + 32;                // TMEM base, abort flag
     static constexpr int OFF_BAR = OFF_MISC + 16;
-    static constexpr int B_QFULL = 0, B_QREADY = 2, B_QFREE = 4, B_TAB = 5, B_DRAIN = 6, B_DFULL = 7, B_DFREE = 9,
-                         B_FULL = 11, B_FREE = B_FULL + MAXST, NBAR = B_FREE + MAXST;
-    static constexpr int OFF_B = (OFF_BAR + 8 * NBAR + 15) & ~15;  // f32 [1, deep: 2][256]: -lse, in log2 units
-    __host__ __device__ static int head(bool deep) { return OFF_B + (deep ? 2 : 1) * MAXN * 4; }
-    __host__ __device__ static int stages(int N, bool deep) {
-        const int room = SMEM_MOST - 1024 - head(deep) - (deep ? 2 : 1) * NCH * (N / 2) * 128, n = room / STAGE;
+    static constexpr int B_QFULL = 0, B_QFREE = NCH, B_DRAIN = 2 * NCH, B_DFULL = B_DRAIN + 1, B_DFREE = B_DFULL + 2,
+                         B_FULL = B_DFREE + 2, B_FREE = B_FULL + MAXST, NBAR = B_FREE + MAXST;
+    static constexpr int HEAD = OFF_BAR + 8 * NBAR;
+    __host__ __device__ static int stages(int N) {
+        const int room = SMEM_MOST - 1024 - HEAD - NCH * (N / 2) * 128, n = room / STAGE;
         return n < MAXST ? n : MAXST;
     }
-    static_assert(OFF_BAR % 8 == 0 && OFF_A % 16 == 0, "alignment");
+    static_assert(OFF_BAR % 8 == 0 && OFF_B % 16 == 0, "alignment");
 };
-static_assert((SMEM_MOST - 1024 - WCfg<false>::OFF_B - 2048 - NCH * 128 * 128) / WCfg<false>::STAGE >= 4, "ring");
-static_assert((SMEM_MOST - 1024 - WCfg<true>::OFF_B - 2048 - NCH * 128 * 128) / WCfg<true>::STAGE >= 8, "ring");
+static_assert((SMEM_MOST - 1024 - WCfg<false>::HEAD - NCH * 128 * 128) / WCfg<false>::STAGE >= 5, "ring");
+static_assert((SMEM_MOST - 1024 - WCfg<true>::HEAD - NCH * 128 * 128) / WCfg<true>::STAGE >= 9, "ring");
 
 struct WeightParams {
     const int32_t *req, *ctx;
     const int2 *table;
+    const float *powers;          // FP8 [B][T*H]: the query rows' powers of two, inverted
     const uint64_t *tree;         // [B][T] or null
     const float *lse;             // [B][T*H]
     const float *scales;          // FP8: the pool's row scales
@@ -89,7 +94,6 @@ struct WeightParams {
     int B, T, H, M, groups, parts, N, nst;
     int max_req, max_pages, max_ctx, zero_block;
     float scale_log2, decay;
-    bool deep;                    // two requests' queries have room: the next one's come and are made codes of ahead
 };
 
 __device__ __forceinline__ int pages_of(int tokens) { return tokens <= 0 ? 0 : (tokens - 1) / kPage + 1; }
@@ -133,8 +137,46 @@ __device__ __forceinline__ void four_codes(uint32_t w0, uint32_t w1, uint32_t po
     asm("mov.b32 %0, {%1, %2};" : "=r"(p) : "h"(p0), "h"(p1));
     asm("mov.b32 %0, {%1, %2};" : "=r"(r) : "h"(r0), "h"(r1));
 }
-__device__ __forceinline__ void st_cluster_f1(uint32_t a, float x) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(x) : "memory");
+// FP8: the query rows' codes, laid out as the rows were: per chunk of 64 values the first codes,
+// then the second ones; and the inverses of their powers of two. One warp per row.
+__global__ void __launch_bounds__(256)
+weight_codes_kernel(const uint4 *q, uint2 *codes, float *powers, int64_t rows) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const int64_t m = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (m >= rows) return;
+    constexpr int UNITS = kDim / 8;
+    uint4 y[3];
+    uint32_t top = 0;  // the largest magnitude; NaN if there is one
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        const int u = lane + 32 * k;
+        y[k] = u < UNITS ? q[m * UNITS + u] : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        const uint32_t z[4] = {y[k].x, y[k].y, y[k].z, y[k].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(top) : "r"(z[e] & 0x7fff7fffu));
+    }
+    // bits of magnitudes are in their order, infinities and NaN above all
+    top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+    // times 2^k it lies in (224, 448]; a row that is not finite becomes NaN
+    const int k2 = min(135 - (int)(top >> 7) - ((top & 0x7fu) > 0x60u), 126);
+    const uint32_t pow2 = top >= 0x7f80u ? 0x7fc07fc0u : (uint32_t)(k2 + 127) * 0x00800080u;
+    if (lane == 0) powers[m] = __uint_as_float((uint32_t)(127 - k2) << 23);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        const int u = lane + 32 * k;
+        if (u >= UNITS) break;
+        uint2 z, r;
+        four_codes(y[k].x, y[k].y, pow2, z.x, r.x);
+        four_codes(y[k].z, y[k].w, pow2, z.y, r.y);
+        uint2 *to = codes + m * (2 * UNITS) + (u >> 3) * 16 + (u & 7);
+        to[0] = z;
+        to[8] = r;
+    }
 }
 
 template <bool FP8>
@@ -142,7 +184,9 @@ __global__ void __launch_bounds__(WT, 1)
 weight_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q, const WeightParams p) {
     using C = WCfg<FP8>;
     extern __shared__ uint8_t smem_raw[];
-    grid_dep_wait();
+    // FP8: the launch before is the one that makes the codes, begun when all before it had ended;
+    // those who read codes or powers wait for it.
+    if (!FP8) grid_dep_wait();
     grid_dep_launch();
     const int rank = static_cast<int>(hs::cluster_ctarank());
     const int unit = blockIdx.x >> 1, g = unit % p.groups, part = unit / p.groups;
@@ -150,7 +194,7 @@ weight_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     const uint32_t raw = hs::smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;  // queries, ring, then the small things
     const uint32_t qall = NCH * (uint32_t)(p.N / 2) * 128u;
-    const uint32_t ring = base + (p.deep ? 2u : 1u) * qall, head = ring + (uint32_t)(p.nst * C::STAGE);
+    const uint32_t ring = base + qall, head = ring + (uint32_t)(p.nst * C::STAGE);
     uint8_t *small = smem_raw + (head - raw);
     volatile int32_t *misc = reinterpret_cast<volatile int32_t *>(small + C::OFF_MISC);
     auto bar = [&](int i) { return head + C::OFF_BAR + 8u * (uint32_t)i; };
@@ -166,7 +210,7 @@ weight_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::NBAR; ++i) {
             uint32_t n = 1;
-            if (i == C::B_QREADY || i == C::B_QREADY + 1 || i == C::B_DFREE || i == C::B_DFREE + 1 || i == C::B_TAB) n = 2 * NEW;  // both CTAs'
+            if (i == C::B_DFREE || i == C::B_DFREE + 1) n = 2 * NEW;  // both CTAs'
             mbar_init(bar(i), n);
         }
         misc[1] = 0;
@@ -263,26 +307,11 @@ weight_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
         Walk w = begin;
-        uint32_t u = 0, seg = 0, qn = 0;
+        uint32_t u = 0, s = 0, turn = 1;  // chunks asked for; ring stage and the phase before its own
         bool ok = true;
         while (w.n > 0 && ok) {
-            Walk nx = w;
-            next(nx);
             const int2 *table = p.table + (size_t)w.r * p.max_pages;
             const int pages = pages_of(w.L);
-            // request b's, segment x of the range, into its place
-            auto queries = [&](int b, uint32_t x) {
-                const uint32_t at = base + (p.deep ? (x & 1u) * qall : 0u);
-                mbar_expect_tx(bar(C::B_QFULL + (int)(x & 1u)), qall);
-                for (int c = 0; c < NCH; ++c)
-                    tma_load_3d(at + c * qch, &tm_q, 64 * c, g * MAXN + rank * (p.N / 2), b, bar(C::B_QFULL + (int)(x & 1u)));
-                qn = x + 1;
-            };
-            if (lane == 0) {
-                // the MMAs of the request before are done with the queries' place
-                if (!p.deep && seg > 0) ok = mbar_wait_inline(bar(C::B_QFREE), (seg - 1) & 1u);
-                if (ok && (!p.deep || seg == 0)) queries(w.b, seg);
-            }
             int blk = 0;
             for (int i = 0; i < w.n; ++i) {
                 // blocks of this CTA's pages, 16 tiles ahead
@@ -295,35 +324,55 @@ weight_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 const int row1 = __shfl_sync(0xffffffffu, blk, 2 * (i % 16) + 1) * kPage;
                 if (lane == 0) {
                     for (int c = 0; c < NCH && ok; ++c, ++u) {
-                        const uint32_t s = u % nst;
-                        ok = mbar_wait_inline(bar(C::B_FREE + (int)s), ((u / nst) & 1u) ^ 1u);
+                        ok = mbar_wait_inline(bar(C::B_FREE + (int)s), turn);
                         if (!ok) break;
                         // both CTAs' bytes complete on CTA 0's barrier
                         if (rank == 0) mbar_expect_tx(bar(C::B_FULL + (int)s), 2 * C::STAGE);
                         tma_load_pair(ring + s * C::STAGE, &tm_k, 0, row0, c, lead(C::B_FULL + (int)s));
                         tma_load_pair(ring + s * C::STAGE + C::STAGE / 2, &tm_k, 0, row1, c, lead(C::B_FULL + (int)s));
-                    }
-                    if (p.deep && i == 0 && ok) {
-                        if (seg > 0) ok = mbar_wait_inline(bar(C::B_QFREE), (seg - 1) & 1u);
-                        if (ok && nx.n > 0) queries(nx.b, seg + 1);
+                        if (++s == nst) {
+                            s = 0;
+                            turn ^= 1u;
+                        }
                     }
                 }
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok) break;
             }
-            w = nx;
-            ++seg;
+            next(w);
         }
-        if (lane == 0) {
-            // the copies begun have landed before the CTA may end
-            for (uint32_t k = qn > 2 ? qn - 2 : 0; k < qn; ++k) mbar_wait_inline(bar(C::B_QFULL + (int)(k & 1u)), (k >> 1) & 1u);
-            if (!ok) {
-                fail();
-                for (uint32_t k = 0, v = u; rank == 0 && k < nst && v > 0; ++k) {
-                    --v;
-                    mbar_wait_inline(bar(C::B_FULL + (int)(v % nst)), (v / nst) & 1u);
+        if (lane == 0 && !ok) {
+            fail();
+            for (uint32_t k = 0, v = u; rank == 0 && k < nst && v > 0; ++k) {
+                --v;
+                mbar_wait_inline(bar(C::B_FULL + (int)(v % nst)), (v / nst) & 1u);
+            }
+        }
+    } else if (warp == 2 + NEW) {
+        // ------------------------------------------------------------ queries' producer
+        uint32_t n = 0;  // chunks asked for
+        bool ok = true;
+        uint32_t x = 0;
+        if (FP8) grid_dep_wait();
+        for (Walk w = begin; w.n > 0 && ok; next(w), ++x) {
+            if (lane == 0) {
+                for (int c = 0; c < NCH && ok; ++c) {
+                    // the MMAs of the request before are done with the chunk's place
+                    if (x > 0) ok = mbar_wait_inline(bar(C::B_QFREE + c), (x - 1) & 1u);
+                    if (!ok) break;
+                    if (rank == 0) mbar_expect_tx(bar(C::B_QFULL + c), 2 * qch);  // both CTAs' bytes
+                    tma_load_pair(base + c * qch, &tm_q, 64 * c, g * p.N + rank * (p.N / 2), w.b, lead(C::B_QFULL + c));
+                    ++n;
                 }
             }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+        }
+        if (lane == 0) {
+            if (!ok) fail();
+            // the copies begun have landed before the CTA may end
+            for (uint32_t k = n > NCH ? n - NCH : 0; k < n && rank == 0; ++k)
+                mbar_wait_inline(bar(C::B_QFULL + (int)(k % NCH)), (k / NCH) & 1u);
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer (CTA 0)
@@ -334,27 +383,22 @@ weight_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             const uint32_t khi = FP8 ? (uint32_t)(desc_sw64(base, 16, 512) >> 32) : hi;
             const uint32_t leader = elect_one();
             bool ok = true;
-            uint32_t u = 0, i = 0, seg = 0;
-            const uint32_t last_u = tiles * NCH;
+            uint32_t i = 0, seg = 0, s = 0, turn = 0;  // ring stage and its phase
+            uint32_t keep = tiles * NCH > nst ? tiles * NCH - nst : 0;  // chunks whose stages are filled again
             for (Walk w = begin; w.n > 0 && ok; ++seg) {
-                ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_QREADY + (int)(seg & 1u)), (seg >> 1) & 1u));
-                if (!ok) break;
-                // the last request's place: given back only now, so that no query barrier is two
-                // phases ahead of those who wait for it
-                if (p.deep && seg > 0 && leader) commit_both(bar(C::B_QFREE));
-                const uint32_t q0 = lo + ((p.deep ? (seg & 1u) * qall : 0u) >> 4);
-                for (int j = 0; j < w.n && ok; ++j, ++i) {
-                    if (i >= 2)
-                        ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_DFREE + (int)(i & 1)), ((i >> 1) & 1u) ^ 1u));
-                    if (!ok) break;
-                    const uint32_t d = tmem + (i & 1) * (uint32_t)p.N;
-                    for (int c = 0; c < NCH && ok; ++c, ++u) {
-                        const uint32_t s = u % nst;
-                        ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_FULL + (int)s), (u / nst) & 1u));
-                        if (!ok) break;
-                        tc_fence_after();
-                        if (leader) {
-                            const uint32_t a = lo + ((ring - base + s * C::STAGE) >> 4), q = q0 + ((c * qch) >> 4);
+                Walk nx = w;
+                next(nx);
+                if (leader) {
+                    for (int j = 0; j < w.n && ok; ++j) {
+                        const uint32_t k = i + (uint32_t)j, d = tmem + (k & 1u) * (uint32_t)p.N;
+                        if (k >= 2) ok = mbar_wait_inline(bar(C::B_DFREE + (int)(k & 1u)), ((k >> 1) & 1u) ^ 1u);
+#pragma unroll 1
+                        for (int c = 0; c < NCH && ok; ++c) {
+                            if (j == 0) ok = mbar_wait_inline(bar(C::B_QFULL + c), seg & 1u);
+                            if (ok) ok = mbar_wait_inline(bar(C::B_FULL + (int)s), turn);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint32_t a = lo + ((ring - base + s * C::STAGE) >> 4), q = lo + ((c * qch) >> 4);
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 if (FP8)  // both codes of the queries with the same 32 codes of the keys
@@ -362,17 +406,23 @@ weight_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                                 else
                                     mma2_ss(d, a + 2 * e, q + 2 * e, hi, idesc, (c | e) != 0);
                             }
-                            if (u + nst < last_u) commit_both(bar(C::B_FREE + (int)s));
+                            if (keep > 0) {
+                                commit_both(bar(C::B_FREE + (int)s));
+                                --keep;
+                            }
+                            // the next request's queries take the place of these
+                            if (j == w.n - 1 && nx.n > 0) commit_both(bar(C::B_QFREE + c));
+                            if (++s == nst) {
+                                s = 0;
+                                turn ^= 1u;
+                            }
                         }
-                        __syncwarp();
+                        if (ok) commit_both(bar(C::B_DFULL + (int)(k & 1u)));
                     }
-                    if (!ok) break;
-                    if (leader) commit_both(bar(C::B_DFULL + (int)(i & 1)));
-                    __syncwarp();
                 }
-                next(w);
-                if (!p.deep && ok && w.n > 0 && leader) commit_both(bar(C::B_QFREE));
-                __syncwarp();
+                ok = __all_sync(0xffffffffu, ok);
+                i += (uint32_t)w.n;
+                w = nx;
             }
             if (!ok && lane == 0) fail();
             if (leader) {
@@ -387,102 +437,34 @@ weight_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         // ------------------------------------------------------------ the sums
         const int wq = warp & 3, hf = (warp - 2) >> 2, tid = (warp - 2) * 32 + lane;
         const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
-        const int c_lo = hf * (p.N / 2), c_hi = min(c_lo + p.N / 2, p.M - g * MAXN);
+        const int mid = (p.N / 2 + 31) & ~31, c_lo = hf * mid, c_hi = min(hf ? p.N : mid, p.M - g * p.N);
         volatile float *psum = reinterpret_cast<volatile float *>(small + C::OFF_PS);
         volatile uint32_t *dead = reinterpret_cast<volatile uint32_t *>(small + C::OFF_DEAD);
         const bool writer = hf == 0 && (wq & 1) == 0 && lane == 0;  // of one page of the tile
         bool ok = true;
-        uint32_t i = 0, seg = 0, ready = 0, tabs = 0;  // segments begun, made ready; tables of both CTAs seen
-        auto see_tables = [&](uint32_t upto) {
-            for (; FP8 && tabs <= upto; ++tabs)
-                if (ok) ok = __all_sync(0xffffffffu, mbar_wait_cluster(bar(C::B_TAB), tabs & 1u));
+        uint32_t i = 0;
+        const int m_own = g * p.N + tid;  // this thread's column
+        float lse = 0.f, pw = 0.f;
+        auto fetch = [&](const Walk &v) {  // its terms
+            if (tid >= p.N || m_own >= p.M || v.n <= 0) return;
+            lse = p.lse[(size_t)v.b * p.M + m_own];
+            if (FP8) pw = p.powers[(size_t)v.b * p.M + m_own];
         };
-        Walk w = begin, nx = begin;  // nx: the next to make ready
-        while (w.n > 0) {
-            if (nx.n > 0 && ready <= seg + (p.deep ? 1u : 0u)) {
-                // A request's columns: the terms of its lse, and (FP8) its queries as codes. All
-                // warps are done with the tiles before this segment's; the peer has made this
-                // one ready, so it is done with the tables of the one before the last.
-                if (ready > 0) see_tables(ready - 1);
-                const int m = g * MAXN + tid;
-                const float v = tid < p.N && m < p.M ? p.lse[(size_t)nx.b * p.M + m] : 0.f;
-                const bool fin = fabsf(v) < INFINITY;
-                const uint32_t out = __ballot_sync(0xffffffffu, !fin), odd = p.deep ? ready & 1u : 0u;
-                if (tid < p.N)
-                    st_shared_f1(head + C::OFF_B + 4 * (odd * MAXN + tid), fin && m < p.M ? -v * 1.4426950408889634f : -INFINITY);
-                if (lane == 0) dead[8 * odd + warp - 2] = out;
-                if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_QFULL + (int)(ready & 1u)), (ready >> 1) & 1u));
-                if (FP8) {
-                    // thread = (row of this CTA's half, part of its chunks): as many parts as the
-                    // threads allow
-                    const int rows = p.N / 2, parts = 32 * NEW / rows, row = tid % rows, part = tid / rows;
-                    const bool in = part < parts;
-                    const uint32_t q0 = base + odd * qall + row * 128;
-                    auto q_at = [&](int c) { return q0 + c * qch; };
-                    uint32_t top = 0;  // the row's largest magnitude; NaN if there is one
-                    if (ok && in) {
-#pragma unroll 1
-                        for (int c = part; c < NCH; c += parts)
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                const uint4 x4 = ld_shared_v4(q_at(c) + ((k ^ (row & 7)) << 4));
-                                const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w};
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(top) : "r"(x[e] & 0x7fff7fffu));
-                            }
-                    }
-                    // bits of magnitudes are in their order, infinities and NaN above all
-                    named_bar_sync(1, 32 * NEW);  // the last request's have been read
-                    st_shared_b32(head + C::OFF_X + 4 * tid, max(top & 0xffffu, top >> 16));
-                    named_bar_sync(1, 32 * NEW);
-                    top = 0;
-                    for (int k = 0; k < parts; ++k) top = max(top, ld_shared_b32(head + C::OFF_X + 4 * (k * rows + row)));
-                    // times 2^k it lies in (224, 448]; a row that is not finite becomes NaN
-                    const int k2 = min(135 - (int)(top >> 7) - ((top & 0x7fu) > 0x60u), 126);
-                    const uint32_t pow2 = top >= 0x7f80u ? 0x7fc07fc0u : (uint32_t)(k2 + 127) * 0x00800080u;
-                    if (ok && in) {
-#pragma unroll 1
-                        for (int c = part; c < NCH; c += parts) {
-                            uint32_t r[16];  // first codes go where values have been read
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const uint4 x = ld_shared_v4(q_at(c) + (((2 * k) ^ (row & 7)) << 4));
-                                const uint4 y = ld_shared_v4(q_at(c) + (((2 * k + 1) ^ (row & 7)) << 4));
-                                uint32_t z[4];
-                                four_codes(x.x, x.y, pow2, z[0], r[4 * k]);
-                                four_codes(x.z, x.w, pow2, z[1], r[4 * k + 1]);
-                                four_codes(y.x, y.y, pow2, z[2], r[4 * k + 2]);
-                                four_codes(y.z, y.w, pow2, z[3], r[4 * k + 3]);
-                                st_shared_v4(q_at(c) + ((k ^ (row & 7)) << 4), z[0], z[1], z[2], z[3]);
-                            }
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                st_shared_v4(q_at(c) + (((4 + k) ^ (row & 7)) << 4), r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
-                        }
-                    }
-                    if (part == 0) {
-                        const float a = p.scale_log2 * __uint_as_float((uint32_t)(127 - k2) << 23);
-                        const uint32_t at = head + C::OFF_A + 4 * ((ready % 3u) * MAXN + (uint32_t)(rank * rows + row));
-                        st_shared_f1(at, a);
-                        st_cluster_f1(cluster_address(at, (uint32_t)rank ^ 1u), a);
-                    }
-                    fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive_remote(cluster_address(bar(C::B_TAB), 0));
-                        mbar_arrive_remote(cluster_address(bar(C::B_TAB), 1));
-                    }
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive_peer(lead(C::B_QREADY + (int)(ready & 1u)));
-                next(nx);
-                ++ready;
-                if (p.deep && ready == 1 && nx.n > 0) continue;  // the first two
-            }
-            see_tables(seg);
-            named_bar_sync(1, 32 * NEW);  // the columns' terms are there
-            const uint32_t odd = p.deep ? seg & 1u : 0u, tab = head + C::OFF_A + (seg % 3u) * MAXN * 4;
-            const uint32_t terms = head + C::OFF_B + odd * MAXN * 4;
+        if (FP8) grid_dep_wait();
+        fetch(begin);
+        for (Walk w = begin, nx; w.n > 0; w = nx) {
+            nx = w;
+            next(nx);
+            // The columns' terms. All warps are done with the last segment's.
+            const bool fin = fabsf(lse) < INFINITY;
+            const uint32_t out = __ballot_sync(0xffffffffu, !fin);
+            if (tid < p.N)
+                st_shared_f1(head + C::OFF_B + 4 * tid, fin && m_own < p.M ? -lse * 1.4426950408889634f : -INFINITY);
+            if (FP8 && tid < p.N) st_shared_f1(head + C::OFF_A + 4 * tid, p.scale_log2 * pw);
+            if (lane == 0) dead[warp - 2] = out;
+            fetch(nx);
+            named_bar_sync(1, 32 * NEW);
+            const uint32_t terms = head + C::OFF_B, tab = head + C::OFF_A;
 
             const int pages = pages_of(w.L), draft = w.L - p.T;
             const int2 *table = p.table + (size_t)w.r * p.max_pages;
@@ -511,7 +493,7 @@ weight_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                         uint32_t d[32];
                         HS_TMEM_LD32(tmem + lane_off + (i & 1) * (uint32_t)p.N + c0, d);
                         HS_TMEM_WAIT_LD32(d);
-                        const uint32_t gone = dead[8 * odd + (c0 >> 5)];
+                        const uint32_t gone = dead[c0 >> 5];
                         // the columns that count: with a key that is not finite the others hold NaN
                         const uint32_t live = ~gone & (c_hi - c0 < 32 ? (1u << (c_hi - c0)) - 1u : ~0u);
                         auto sums = [&](auto whole) {
@@ -544,7 +526,7 @@ weight_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                         } else if (all) {
                             sums(std::false_type{});
                         } else {
-                            int m = g * MAXN + c0, t = m / p.H, h = m - t * p.H;
+                            int m = g * p.N + c0, t = m / p.H, h = m - t * p.H;
                             auto sees = [&](int tt) {
                                 if (tt >= p.T || pos >= w.L) return false;
                                 if (!p.tree) return pos <= draft + tt;
@@ -584,8 +566,6 @@ weight_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 }
                 blk = blk_next;
             }
-            next(w);
-            ++seg;
         }
         if (!ok && lane == 0) fail();
     }
@@ -619,7 +599,12 @@ weight_join_kernel(const float *part, const int32_t *req, const int32_t *ctx, co
 bool takes(int64_t B, int64_t T, int64_t H) {
     return B >= 0 && B <= 65535 && T >= 1 && T <= 32767 && H >= 1 && T * H <= (1 << 22);
 }
-int groups_of(int64_t M) { return (int)((M + MAXN - 1) / MAXN); }
+// The query rows are dealt evenly to as few groups as hold them: rows of a group, a multiple of 32.
+int rows_of(int64_t M) {
+    const int64_t groups = (M + MAXN - 1) / MAXN;
+    return (int)((M + groups - 1) / groups + 31) & ~31;
+}
+int groups_of(int64_t M) { return (int)((M + rows_of(M) - 1) / rows_of(M)); }
 
 // Parts that the key tiles of all requests are cut into, each worked through by one pair of
 // CTAs per group: the count that a model of the launch makes shortest. A tile takes a
@@ -668,7 +653,7 @@ hs_status launch_weights(int dev, cudaStream_t s, const CUtensorMap &tk, const C
     cfg.gridDim = dim3((unsigned)(2 * p.groups * p.parts), 1, 1);
     cfg.blockDim = dim3(WT, 1, 1);
     cfg.dynamicSmemBytes =
-        (size_t)(1024 + (p.deep ? 2 : 1) * NCH * (p.N / 2) * 128 + p.nst * WCfg<FP8>::STAGE + WCfg<FP8>::head(p.deep));
+        (size_t)(1024 + NCH * (p.N / 2) * 128 + p.nst * WCfg<FP8>::STAGE + WCfg<FP8>::HEAD);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -681,12 +666,20 @@ hs_status launch_weights(int dev, cudaStream_t s, const CUtensorMap &tk, const C
     return cudaLaunchKernelEx(&cfg, weight_kernel<FP8>, tk, tq, p) == cudaSuccess ? HS_OK : HS_ERR_CUDA;
 }
 
+size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+// FP8: the queries' codes and powers, before the groups' sums in the workspace
+size_t code_bytes(int64_t B, int64_t T, int64_t H) {
+    const size_t rows = (size_t)B * T * H;
+    return up256(rows * 2 * kDim) + up256(rows * 4);
+}
+
 }  // namespace
 
 extern "C" size_t hs_weights_workspace_bytes(hs_pool_t pool, int32_t B, int32_t T, int32_t H) {
     if (!pool || B < 1 || !takes(B, T, H)) return 0;
     const int groups = groups_of((int64_t)T * H);
-    return groups == 1 ? 0 : ((size_t)groups * B * pool->max_pages * 4 + 255) & ~(size_t)255;
+    const size_t parts = groups == 1 ? 0 : (size_t)groups * B * pool->max_pages * 4;
+    return up256(parts) + (pool->cfg.dtype == HS_FP8_E4M3_ROWSCALE ? code_bytes(B, T, H) : 0);
 }
 
 extern "C" hs_status hs_page_weights(hs_pool_t pool, int32_t B, int32_t T, int32_t H, const void *d_q,
@@ -712,21 +705,24 @@ extern "C" hs_status hs_page_weights(hs_pool_t pool, int32_t B, int32_t T, int32
     p.scales = pool->d_scales;
     p.prior = d_prior;
     p.weights = d_weights;
-    p.part = need ? static_cast<float *>(d_workspace) : nullptr;
+    const int64_t rows = (int64_t)B * T * H;
+    uint8_t *ws = static_cast<uint8_t *>(d_workspace);
+    float *powers = fp8 ? reinterpret_cast<float *>(ws + up256((size_t)rows * 2 * kDim)) : nullptr;
+    p.powers = powers;
+    p.part = reinterpret_cast<float *>(ws + (fp8 ? code_bytes(B, T, H) : 0));  // read with several groups only
     p.err = pool->d_err;
     p.B = B;
     p.T = T;
     p.H = H;
     p.M = T * H;
     p.groups = groups_of(p.M);
-    p.N = p.M < MAXN ? (p.M + 63) & ~63 : MAXN;
-    p.deep = B > 1 && p.N <= MAXN / 2;
-    p.nst = fp8 ? WCfg<true>::stages(p.N, p.deep) : WCfg<false>::stages(p.N, p.deep);
+    p.N = rows_of(p.M);
+    p.nst = fp8 ? WCfg<true>::stages(p.N) : WCfg<false>::stages(p.N);
     const int64_t tiles = (int64_t)B * ((pool->max_pages + TP - 1) / TP);
     // the keys' bytes at the card's rate, or the products
     const double us_mma = 2.5 * p.N / 256, us_bytes = (fp8 ? 148e3 : 295e3) / 85e3;
     p.parts = parts_of(p.groups, tiles, us_mma > us_bytes ? us_mma : us_bytes);
-    if (2ll * p.groups * p.parts > INT32_MAX || tiles > INT32_MAX / 32) return HS_ERR_INVALID_ARG;
+    if (2ll * p.groups * p.parts > INT32_MAX || rows > 8ll * INT32_MAX || tiles > INT32_MAX / 32) return HS_ERR_INVALID_ARG;
     p.max_req = pool->cfg.max_requests;
     p.max_pages = pool->max_pages;
     p.max_ctx = pool->cfg.max_ctx;
@@ -735,9 +731,23 @@ extern "C" hs_status hs_page_weights(hs_pool_t pool, int32_t B, int32_t T, int32
     p.decay = decay;
     CUtensorMap tk, tq;
     if (!make_key_map(&tk, fp8, pool->d_rows, (uint64_t)(pool->cfg.n_gpu_blocks + 1) * kPage) ||
-        !make_map(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d_q, kDim, (uint64_t)p.M, B, 2 * kDim, 64, p.N / 2,
+        !make_map(&tq, CU_TENSOR_MAP_DATA_TYPE_UINT16, fp8 ? ws : d_q, kDim, (uint64_t)p.M, B, 2 * kDim, 64, p.N / 2,
                   CU_TENSOR_MAP_SWIZZLE_128B))
         return HS_ERR_CUDA;
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    if (fp8) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)((rows + 7) / 8), 1, 1);
+        cfg.blockDim = dim3(256, 1, 1);
+        cfg.stream = s;
+        cfg.attrs = pdl;
+        cfg.numAttrs = 1;
+        if (cudaLaunchKernelEx(&cfg, weight_codes_kernel, static_cast<const uint4 *>(d_q), reinterpret_cast<uint2 *>(ws), powers,
+                               rows) != cudaSuccess)
+            return HS_ERR_CUDA;
+    }
     const hs_status st = fp8 ? launch_weights<true>(dev, s, tk, tq, p) : launch_weights<false>(dev, s, tk, tq, p);
     if (st != HS_OK || p.groups == 1) return st;
     cudaLaunchConfig_t cfg = {};
@@ -745,10 +755,7 @@ extern "C" hs_status hs_page_weights(hs_pool_t pool, int32_t B, int32_t T, int32
     cfg.gridDim = dim3((unsigned)(blocks < 1024 ? blocks : 1024), (unsigned)B, 1);
     cfg.blockDim = dim3(256, 1, 1);
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
+    cfg.attrs = pdl;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, weight_join_kernel, (const float *)p.part, d_req_ids, (const int32_t *)pool->d_ctx,
                               d_prior, d_weights, (int)B, p.groups, p.max_req, p.max_pages, p.max_ctx, decay) == cudaSuccess
