@@ -30,8 +30,8 @@
 // 4 to 5 us each time (30 x 6,000 keys, 256 rows: 46 -> 37 us; 40 x 1,000, 32 rows: 15.0 -> 12.8).
 // Only 64 x 500 keys, 256 rows, where every pair has one request, were faster so (22 against 24).
 // Bound: the keys' bytes, or for 256 rows of codes 36 MMAs of 128 clocks per tile. 4 x 74,160 BF16
-// keys, 256 rows: 64 us, tiles at the copy rate from 8 us on; 8 x 131,072 FP8 keys, 512 rows: 312 to
-// 405 us with the clock, 1.94 to 1.52 PFLOP/s. Pages asked into L2 two tiles ahead: 85 instead of 67 us.
+// keys, 256 rows: 62 us, tiles at the copy rate from 7 us on; 8 x 131,072 FP8 keys, 512 rows: 310 to
+// 400 us with the clock, 1.96 to 1.52 PFLOP/s. Pages asked into L2 two tiles ahead: 85 instead of 67 us.
 // Every wait is bounded; on expiry the kernel sets HS_DEVERR_TIMEOUT, drains its own
 // copies and MMAs and returns.
 #include <cuda_bf16.h>
@@ -484,6 +484,23 @@ weight_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 if (writer && page < pages && p.groups == 1 && p.prior && p.decay != 0.f)
                     before = p.decay * p.prior[(size_t)w.r * p.max_pages + page];
                 const bool all = (pos | 31) < draft;  // every query token sees these keys
+                const int node = pos - draft;
+                // Which of the query rows m .. m + 31 see this key. A word of them ahead of the sums: asked at
+                // each row, the tiles at a context's end took 5 us more (13 x 304 keys, 512 rows: 14.3 -> 9.9 us).
+                auto sees = [&](int m) {
+                    if (!p.tree) {  // the tokens from the key's own on
+                        const int first = max(node, 0) * p.H - m;
+                        return first <= 0 ? ~0u : first < 32 ? ~0u << first : 0u;
+                    }
+                    if (node < 0) return ~0u;
+                    uint32_t x = 0;
+                    if (node < p.T)
+                        for (int t = m / p.H; t < p.T && t * p.H < m + 32; ++t) {
+                            const int lo = max(t * p.H - m, 0), n = min((t + 1) * p.H - m, 32) - lo;
+                            if ((p.tree[(size_t)w.b * p.T + t] >> node) & 1) x |= (n < 32 ? (1u << n) - 1u : ~0u) << lo;
+                        }
+                    return x;
+                };
                 if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_DFULL + (int)(i & 1)), (i >> 1) & 1u));
                 float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
                 if (ok && live) {
@@ -495,7 +512,8 @@ weight_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                         HS_TMEM_WAIT_LD32(d);
                         const uint32_t gone = dead[c0 >> 5];
                         // the columns that count: with a key that is not finite the others hold NaN
-                        const uint32_t live = ~gone & (c_hi - c0 < 32 ? (1u << (c_hi - c0)) - 1u : ~0u);
+                        uint32_t live = ~gone & (c_hi - c0 < 32 ? (1u << (c_hi - c0)) - 1u : ~0u);
+                        if (!all) live &= sees(g * p.N + c0);
                         auto sums = [&](auto whole) {
 #pragma unroll
                             for (int e = 0; e < 32; e += 4) {
@@ -521,31 +539,10 @@ weight_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                                 add2(s2, s3, y2, y3);
                             }
                         };
-                        if (all && live == ~0u) {
+                        if (__all_sync(0xffffffffu, live == ~0u))
                             sums(std::true_type{});
-                        } else if (all) {
+                        else
                             sums(std::false_type{});
-                        } else {
-                            int m = g * p.N + c0, t = m / p.H, h = m - t * p.H;
-                            auto sees = [&](int tt) {
-                                if (tt >= p.T || pos >= w.L) return false;
-                                if (!p.tree) return pos <= draft + tt;
-                                const int node = pos - draft;
-                                return node < 0 || ((p.tree[(size_t)w.b * p.T + tt] >> node) & 1) != 0;
-                            };
-                            bool seen = sees(t);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const float b = ld_shared_f1(terms + 4 * (c0 + e));
-                                const float a = FP8 ? ks * ld_shared_f1(tab + 4 * (c0 + e)) : ks;
-                                const float y = ex2(fmaf(__uint_as_float(d[e]), a, b));
-                                s0 += seen && ((live >> e) & 1u) ? y : 0.f;
-                                if (++h == p.H) {
-                                    h = 0;
-                                    seen = sees(++t);
-                                }
-                            }
-                        }
                     }
                 }
                 tc_fence_before();
