@@ -751,36 +751,49 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         };
         bool ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_QFULL), 0));
         auto q_at = [&](int i) { return base + (i < NQT ? C::OFF_QST + i * CH : C::OFF_Q + (i - NQT) * CH) + row * 128; };
-        uint32_t q_pow = 0;   // FP8: the row's power of two, a pair of BF16
         float q_back = 1.f;
         if (FP8) {
+            // Q's values become codes in place. thread = (row, quarter of each chunk), so that a row
+            // is in one warp and is read once: the two pieces of each value, 64 first ones and then
+            // 64 second ones, lie where they are read as 128 bytes of a row of A.
+            const int crow = tid >> 2, part = 2 * (tid & 3);
+            auto at = [&](int i, int u) {
+                return base + (i < NQT ? C::OFF_QST + i * CH : C::OFF_Q + (i - NQT) * CH) + crow * 128 + ((u ^ (crow & 7)) << 4);
+            };
+            uint4 v[NK][2];
             uint32_t m = 0;  // the row's largest magnitude; NaN if there is one
-            if (ok) {
 #pragma unroll
-                for (int n = 0; n < 3; ++n) {
-                    const int i = 2 * hf + kh + 4 * n;
-                    if (i < NK) {
+            for (int i = 0; i < NK; ++i)
 #pragma unroll
-                        for (int u = 0; u < 8; ++u) {
-                            const uint4 v = ld_shared_v4(q_at(i) + ((u ^ (row & 7)) << 4));
-                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                for (int u = 0; u < 2; ++u) {
+                    v[i][u] = ok ? ld_shared_v4(at(i, part + u)) : make_uint4(0, 0, 0, 0);
+                    const uint32_t w[4] = {v[i][u].x, v[i][u].y, v[i][u].z, v[i][u].w};
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[e] & 0x7fff7fffu));
-                        }
-                    }
+                    for (int e = 0; e < 4; ++e) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[e] & 0x7fff7fffu));
                 }
-            }
             // bits of magnitudes are in their order, infinities and NaN above all
-            st_shared_b32(xm + 4 * tid, max(m & 0xffffu, m >> 16));
-            named_bar_sync(1, 32 * NSW);
-            const uint32_t top = max(max(ld_shared_b32(xm_row(0)), ld_shared_b32(xm_row(64))),
-                                     max(ld_shared_b32(xm_row(128)), ld_shared_b32(xm_row(192))));
-            named_bar_sync(1, 32 * NSW);
+            uint32_t top = max(m & 0xffffu, m >> 16);
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));  // all have read
             // times 2^k it lies in (224, 448]; a row that is not finite becomes NaN
             const int k = min(135 - (int)(top >> 7) - ((top & 0x7fu) > 0x60u), 126);
-            q_pow = top >= 0x7f80u ? 0x7fc07fc0u : (uint32_t)(k + 127) * 0x00800080u;
-            q_back = __uint_as_float((uint32_t)(127 - k) << 23);
+            const uint32_t q_pow = top >= 0x7f80u ? 0x7fc07fc0u : (uint32_t)(k + 127) * 0x00800080u;
+            if (part == 0) st_shared_f1(xm + 4 * crow, __uint_as_float((uint32_t)(127 - k) << 23));
+#pragma unroll
+            for (int i = 0; i < NK; ++i) {
+                uint32_t w[4], r[4];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    bf16x4_to_e4m3(v[i][u].x, v[i][u].y, q_pow, w[2 * u], r[2 * u]);
+                    bf16x4_to_e4m3(v[i][u].z, v[i][u].w, q_pow, w[2 * u + 1], r[2 * u + 1]);
+                }
+                if (ok) {
+                    st_shared_v4(at(i, part >> 1), w[0], w[1], w[2], w[3]);
+                    st_shared_v4(at(i, 4 + (part >> 1)), r[0], r[1], r[2], r[3]);
+                }
+            }
+            named_bar_sync(1, 32 * NSW);
+            q_back = ld_shared_f1(xm_row(0));
         }
         if (ok && nsteps > 0) {
 #pragma unroll 1
@@ -789,39 +802,12 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
                     const uint4 v = ld_shared_v4(q_at(i) + ((u ^ (row & 7)) << 4));
-                    if (FP8) {
-                        bf16x4_to_e4m3(v.x, v.y, q_pow, w[2 * u], w[16 + 2 * u]);
-                        bf16x4_to_e4m3(v.z, v.w, q_pow, w[2 * u + 1], w[17 + 2 * u]);
-                    } else {
-                        w[4 * u] = v.x;
-                        w[4 * u + 1] = v.y;
-                        w[4 * u + 2] = v.z;
-                        w[4 * u + 3] = v.w;
-                    }
+                    w[4 * u] = v.x;
+                    w[4 * u + 1] = v.y;
+                    w[4 * u + 2] = v.z;
+                    w[4 * u + 3] = v.w;
                 }
                 HS_TMEM_ST32(tmem + lane_off + TM_Q + 32u * i, w);
-            }
-            if (FP8) {
-                // the chunks that stay in shared memory, in place: three of a row's
-                // four threads take one each
-                const int i = NQT + 2 * hf + kh;
-                if (i < NK) {
-                    uint32_t r[16];  // first pieces go where values have been read
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const uint4 x = ld_shared_v4(q_at(i) + (((2 * u) ^ (row & 7)) << 4));
-                        const uint4 y = ld_shared_v4(q_at(i) + (((2 * u + 1) ^ (row & 7)) << 4));
-                        uint32_t w[4];
-                        bf16x4_to_e4m3(x.x, x.y, q_pow, w[0], r[4 * u]);
-                        bf16x4_to_e4m3(x.z, x.w, q_pow, w[1], r[4 * u + 1]);
-                        bf16x4_to_e4m3(y.x, y.y, q_pow, w[2], r[4 * u + 2]);
-                        bf16x4_to_e4m3(y.z, y.w, q_pow, w[3], r[4 * u + 3]);
-                        st_shared_v4(q_at(i) + ((u ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
-                    }
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        st_shared_v4(q_at(i) + (((4 + u) ^ (row & 7)) << 4), r[4 * u], r[4 * u + 1], r[4 * u + 2], r[4 * u + 3]);
-                }
             }
             tmem_wait_st();
         }
