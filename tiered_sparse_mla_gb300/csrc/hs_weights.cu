@@ -184,10 +184,6 @@ __global__ void __launch_bounds__(WT, 1)
 weight_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q, const WeightParams p) {
     using C = WCfg<FP8>;
     extern __shared__ uint8_t smem_raw[];
-    // FP8: the launch before is the one that makes the codes, begun when all before it had ended;
-    // those who read codes or powers wait for it.
-    if (!FP8) grid_dep_wait();
-    grid_dep_launch();
     const int rank = static_cast<int>(hs::cluster_ctarank());
     const int unit = blockIdx.x >> 1, g = unit % p.groups, part = unit / p.groups;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -207,19 +203,26 @@ weight_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     };
     uint32_t cols = 32;
     while ((int)cols < 2 * p.N) cols <<= 1;
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < C::NBAR; ++i) {
+    if (warp == 0) {
+        for (int i = lane; i < C::NBAR; i += 32) {
             uint32_t n = 1;
             if (i == C::B_DFREE || i == C::B_DFREE + 1) n = 2 * NEW;  // both CTAs'
             mbar_init(bar(i), n);
         }
-        misc[1] = 0;
         fence_mbar_init();
         fence_proxy_async();
-        prefetch_tmap(&tm_k);
-        prefetch_tmap(&tm_q);
+        if (lane == 0) {
+            misc[1] = 0;
+            prefetch_tmap(&tm_k);
+            prefetch_tmap(&tm_q);
+        }
+        __syncwarp();
     }
     if (warp == 1) tmem_alloc2(head + C::OFF_MISC, cols);
+    // FP8: the launch before is the one that makes the codes, begun when all before it had ended;
+    // those who read codes or powers wait for it.
+    if (!FP8) grid_dep_wait();
+    grid_dep_launch();
 
     // The requests' tiles laid end to end: how many, and where this pair's range begins.
     // Every warp finds that, and walks the range, for itself.
