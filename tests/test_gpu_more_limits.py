@@ -220,3 +220,48 @@ def test_plans_captured_with_one_workspace_and_replayed_in_turn():
         for j in range(2):
             assert all(torch.equal(a, b) for a, b in zip(outs[j], want[j]))
     c.close()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("T,H", [(1, 33), (2, 40), (1, 129), (1, 257), (33, 8), (3, 107), (5, 104), (33, 20), (2, 449)])
+def test_weights_of_rows_dealt_to_uneven_groups(dtype, T, H):
+    """Groups of 64, 96, 160, 192, 224 columns, the last one not full, over ranges that come to
+    several requests; with a tree too."""
+    B = 40
+    g = torch.Generator().manual_seed(31)
+    ctx = [T + int(x) for x in torch.randint(0, 900, (B,), generator=g)]
+    ctx[7] = 0
+    c = Cache(dtype, ctx)
+    q = normal(32, B, T, H, P.DIM)
+    for tree in (None, a_tree(33, B, T)):
+        lse = lse_of(c, q, tree)
+        w = run_weights(c, q, lse, tree)
+        check_weights(c, w, q, lse, tree, which=[0, 7, 8, 21, B - 1])
+        total, seen = torch.where(w == -7.0, 0.0, w).sum(1), torch.isfinite(lse).sum((1, 2)).float()
+        assert bool(((total - seen).abs() <= 2.0 ** -10 * seen).all())
+        assert torch.equal(w, run_weights(c, q, lse, tree))
+    c.close()
+
+
+@pytest.mark.parametrize("pages", [31, 33, 64, 255, 511, 512, 513, 537, 2049, 4097])
+@pytest.mark.parametrize("kind", ["one value", "two values", "narrow", "a few apart"])
+def test_evict_where_many_pages_are_near_the_border(pages, kind):
+    """Equal weights in one warp and in several, and bins of the border that hold hundreds of pages."""
+    g = torch.Generator().manual_seed(34)
+    c = Tables([64 * pages - 5] * 4, seed=35, holes=0.05)
+    x = torch.rand(c.R, c.P, generator=g)
+    if kind == "one value":
+        x.fill_(0.25)
+    elif kind == "two values":
+        x = (x > 0.5).float()
+    elif kind == "narrow":  # 512 values next to each other
+        x = (0x3F800000 + (x * 512).int()).view(torch.float32)
+    else:  # most pages alike, few of other magnitudes
+        x = torch.where(x < 0.02, x * 1e30, torch.where(x < 0.04, x * 1e-30, 1.0 + 2.0 ** -23 * (x * 4).floor()))
+    budget = [2, pages // 3, pages - 1, pages // 2 + 1]
+    kept, freed, count = run_evict(c, range(4), budget, x.cuda(), c.P, plan=True)
+    for r in range(4):
+        stay, gone = M.evict(c.table[r], c.saved[r], x[r].tolist(), c.ctx[r], budget[r], 1, 1, False)
+        assert kept[r] == stay + [-1] * (c.P - len(stay)) and count[r] == len(gone)
+        assert freed[r][:len(gone)] == [int(c.table[r, p]) for p in gone]
+    c.close()
