@@ -3,6 +3,7 @@ offsets past 32 bits, lengths past max_ctx, rows that are not finite beside ones
 long vocabularies, many requests."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -264,4 +265,50 @@ def test_evict_where_many_pages_are_near_the_border(pages, kind):
         stay, gone = M.evict(c.table[r], c.saved[r], x[r].tolist(), c.ctx[r], budget[r], 1, 1, False)
         assert kept[r] == stay + [-1] * (c.P - len(stay)) and count[r] == len(gone)
         assert freed[r][:len(gone)] == [int(c.table[r, p]) for p in gone]
+    c.close()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+def test_weights_see_what_was_written_just_before(dtype):
+    """Rows appended, lengths set, queries and pages changed directly before each call in the same
+    stream, one workspace for all: eager, and as one graph."""
+    B, T, H, new = 3, 2, 40, 2000
+    lens = [i32(9000, 7000, 8000), i32(8500, 9000, 6001)]
+    c = Cache(dtype, [9000, 7000, 8000], max_ctx=9000)
+    c.pool.page_map_range(1, 0, np.resize(c.table[1][c.table[1] >= 0], c.P).astype(np.int32), np.full(c.P, -1, np.int32))
+    hs, req = c.hs, torch.arange(B, **I32)
+    rows = [normal(41 + i, B, new, P.DIM) for i in range(2)]
+    q = [normal(43 + i, B, T, H, P.DIM) for i in range(2)]
+    c.set_ctx([9000, 7000, 8000])
+    lse = torch.full((B, T, H), 3.0, device="cuda")
+    ws = workspace(hs.hs_weights_workspace_bytes(c.pool.handle, B, T, H))
+    now = torch.empty_like(q[0])
+
+    def step(i, w, sync):
+        for call in (lambda: c.pool.set_ctx_lens(lens[i]), lambda: c.pool.append_rows(rows[i], req), lambda: now.copy_(q[i]),
+                     lambda: c.pool.page_weights(now, lse, req, None, SCALE, w, None, 1.0, ws)):
+            call()
+            if sync:
+                torch.cuda.synchronize()
+
+    blank = torch.full((c.R, c.P), -7.0, device="cuda")
+    want = [blank.clone() for _ in range(2)]
+    for i in (0, 1, 0, 1):
+        want[i].fill_(-7.0)
+        step(i, want[i], True)
+    assert not torch.equal(want[0], want[1])
+    outs = [blank.clone() for _ in range(12)]
+    for i in range(12):
+        step(i % 2, outs[i], False)
+    torch.cuda.synchronize()
+    assert all(torch.equal(outs[i], want[i % 2]) for i in range(2, 12))
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=side):
+        for i in range(12):
+            step(i % 2, outs[i], False)
+    for w in outs:
+        w.fill_(-7.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(outs[i], want[i % 2]) for i in range(2, 12))
     c.close()
