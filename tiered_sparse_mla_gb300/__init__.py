@@ -471,11 +471,12 @@ def hs_page_weights(pool: int, q, lse, req_ids, tree, sm_scale: float, weights, 
     B, T, H = q.shape[:3]
     shape = table_shape or _table_shape(pool)
     ws, wp = _ws(workspace)
+    out = _arg("weights", weights, "float32", *shape)
+    old = out if prior is weights else _arg("prior", prior, "float32", *shape, optional=True)
     _check("hs_page_weights", load().hs_page_weights(
         pool, B, T, H, _arg("q", q, "bfloat16", B, T, H, 576), _arg("lse", lse, "float32", B, T, H),
         _arg("req_ids", req_ids, "int32", B), _arg("tree", tree, "int64", B, T, optional=True),
-        float(sm_scale), float(decay), _arg("prior", prior, "float32", *shape, optional=True),
-        _arg("weights", weights, "float32", *shape), wp, ws, _stream(stream)))
+        float(sm_scale), float(decay), old, out, wp, ws, _stream(stream)))
 
 
 def hs_evict_pages(pool: int, req, budget, weights, kept, freed, n_freed, n_first: int = 1,
