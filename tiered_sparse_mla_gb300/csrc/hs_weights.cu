@@ -32,6 +32,8 @@
 // Bound: the keys' bytes, or for 256 rows of codes 36 MMAs of 128 clocks per tile. 4 x 74,160 BF16
 // keys, 256 rows: 62 us, tiles at the copy rate from 7 us on; 8 x 131,072 FP8 keys, 512 rows: 310 to
 // 400 us with the clock, 1.96 to 1.52 PFLOP/s. Pages asked into L2 two tiles ahead: 85 instead of 67 us.
+// Ranges cut at half tiles or at pages, whose last tiles are not full: 8 x 8,000 BF16 keys, 512 rows
+// 28.1 instead of 26.1 us, 4 x 74,160 the same.
 // Every wait is bounded; on expiry the kernel sets HS_DEVERR_TIMEOUT, drains its own
 // copies and MMAs and returns.
 #include <cuda_bf16.h>
