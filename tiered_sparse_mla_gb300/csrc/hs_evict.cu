@@ -157,6 +157,10 @@ constexpr int EARLY = 4;
 
 __global__ void __launch_bounds__(ET)
 evict_kernel(const EvictParams p, const int G) {
+    // Once all CTAs of the cluster have come here, each may write to the others' shared memory: a
+    // CTA that has not begun has none. The wait is directly before the first such write, behind the
+    // loads that lead to it.
+    hs::tc::cluster_arrive_relaxed();
     hs::tc::grid_dep_wait();
     hs::tc::grid_dep_launch();
     extern __shared__ uint32_t keys[];  // [cap] of the slice, and their blocks
@@ -184,7 +188,10 @@ evict_kernel(const EvictParams p, const int G) {
     }
     int P, budget;
     const int r = request_of(p, i, rank == 0, P, budget);
-    if (r < 0) return;  // the whole cluster
+    if (r < 0) {  // the whole cluster
+        hs::cluster_wait();
+        return;
+    }
     int32_t *kept = p.kept + (size_t)i * p.N, *freed = p.freed + (size_t)i * p.max_pages;
     const int n = max(min(P - p0, slots), 0);
     auto key = [&](int k) {
@@ -223,6 +230,7 @@ evict_kernel(const EvictParams p, const int G) {
         wkey[warp][1] = hi;
     }
     __syncthreads();
+    hs::cluster_wait();
     if (warp == 0) {
         cand = __reduce_add_sync(0xffffffffu, lane < NW ? wsum[lane][0] : 0);
         must = __reduce_add_sync(0xffffffffu, lane < NW ? wsum[lane][1] : 0);
