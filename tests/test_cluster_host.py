@@ -15,12 +15,15 @@ WAIT = re.compile(r"\bcluster_(?:wait|sync_all|sync_relaxed)\(|barrier\.cluster\
 def kernels(source):
     with open(os.path.join(CSRC, source)) as f:
         text = re.sub(r"//[^\n]*", "", f.read())
-    for kernel in text.split("__global__")[1:]:
+    for kernel in re.split(r"__global__|__device__ __forceinline__ void (?=\w+_body\()", text)[1:]:
         name = re.search(r"(\w+)\s*\((?!\()", re.sub(r"__launch_bounds__\([^;{]*?\)\s*\n?", "", kernel)).group(1)
         yield name, kernel[kernel.index("{"):]
 
 
-@pytest.mark.parametrize("source", ["hs_evict.cu"])
+SOURCES = sorted(f for f in os.listdir(CSRC) if f.endswith(".cu"))
+
+
+@pytest.mark.parametrize("source", SOURCES)
 def test_no_cta_reaches_another_before_all_of_the_cluster_run(source):
     """A CTA's shared memory is there from when the CTA has begun: a cluster barrier has to lie before the
     first access from another one."""
@@ -35,4 +38,4 @@ def test_no_cta_reaches_another_before_all_of_the_cluster_run(source):
         while wait and re.match(r"[^{}]*\breturn;", body[wait.end():]):
             wait = WAIT.search(body, wait.end())
         assert wait and wait.start() < remote.start(), f"{source}: {name}"
-    assert found
+    assert found or source not in ("hs_resolve.cu", "hs_select.cu", "hs_page_decode.cu", "hs_weights.cu", "hs_evict.cu", "hs_verify.cu")

@@ -148,6 +148,10 @@ __device__ __forceinline__ uint64_t part_of(float u, uint64_t total) {
 template <typename P>
 __global__ void __launch_bounds__(VT, 4)
 verify_kernel(const VerifyParams p) {
+    // Once all CTAs of the cluster have come here, each may write to the others' shared memory: a
+    // CTA that has not begun has none. The wait is directly before the first such write, behind the
+    // row's sums.
+    hs::tc::cluster_arrive_relaxed();
     hs::tc::grid_dep_wait();
     hs::tc::grid_dep_launch();
     __shared__ uint64_t sums[NW][UNITS][33];   // of a warp's units, by lane
@@ -375,6 +379,7 @@ verify_kernel(const VerifyParams p) {
         uint64_t all = total_lane;
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) all = add_sat(all, (uint64_t)__shfl_xor_sync(0xffffffffu, (unsigned long long)all, o));
+        if (attempt == 0) hs::cluster_wait();
         if (lane < G) {
             const uint32_t at = hs::dsmem_map(&totals[me], lane);
             asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(all) : "memory");
