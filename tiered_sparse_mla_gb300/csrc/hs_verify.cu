@@ -15,10 +15,11 @@
 // behind them the slowest CTA and the search. (The whole runs asked into L2 at the start:
 // 19.7 us. Copies of 16 bytes through shared memory, 30 us: twice the instructions.)
 //
-// A search by sums has to add the same way each time. Here sums are integers of 2^-58: eight
-// values of a lane are cut into digits of f32, multiples of 2^-20 (to which adding and
-// taking away 12 rounds a value in [0, 1]), then of 2^-41, whose sums of eight are exact, and a
-// rest below 2^-42, whose sum is off by less than 2^-60. (Integer shifts, at half
+// A search by sums has to add the same way each time. Here a value counts in whole steps of
+// 2^-58, what is below them is cut off, and sums are integers: eight values of a lane are cut into
+// digits of f32, multiples of 2^-20 (to which adding and taking away 12 rounds a value in [0, 1]),
+// then of 2^-41, whose sums of eight are exact, and a rest below 2^-42, which an addition rounded
+// down leaves as an integer in the low bits. (Integer shifts, at half
 // the rate of additions and twice as many, made 64 requests of 128,000 values 22.7 us.)
 // Integer sums saturate at 64, which those of probabilities do not reach.
 #include <cuda_bf16.h>
@@ -98,17 +99,25 @@ __device__ __forceinline__ uint64_t less(uint64_t a, uint64_t b) {  // a - b
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(c) : "l"(b), "l"(0xbf800000bf800000ull), "l"(a));
     return c;
 }
-// Two values' digits: the multiples of 2^-20 and 2^-41, and the rest.
+__device__ __forceinline__ uint64_t plus_down(uint64_t a, uint64_t b) {
+    uint64_t c;
+    asm("add.rm.f32x2 %0, %1, %2;" : "=l"(c) : "l"(a), "l"(b));
+    return c;
+}
+// Two values' digits: the multiples of 2^-20 and 2^-41, and the rest's whole steps of 2^-58 above
+// the bits of 1.5 2^-35, whose last bit is one step.
+constexpr uint32_t C3 = 0x2e400000u;
 struct Digits {
     uint64_t h, m, l;
 };
+__device__ __forceinline__ uint32_t steps_of(uint64_t l) { return (uint32_t)l + (uint32_t)(l >> 32); }  // of both values, and twice C3
 __device__ __forceinline__ Digits digits_of(uint64_t x) {
     constexpr uint64_t C1 = 0x4140000041400000ull, C2 = 0x36c0000036c00000ull, SIGNS = 0x8000000080000000ull;  // 12, 1.5 2^-18
     Digits d;
     d.h = plus(plus(x, C1), C1 ^ SIGNS);
     x = less(x, d.h);
     d.m = plus(plus(x, C2), C2 ^ SIGNS);
-    d.l = less(x, d.m);
+    d.l = plus_down(less(x, d.m), (uint64_t)C3 << 32 | C3);
     return d;
 }
 // In units of 2^-58, the rest cut off.
@@ -309,35 +318,37 @@ verify_kernel(const VerifyParams p) {
                 }
             }
         };
-        auto sum_of = [&](const Digits &all) {  // the lane's, at most 8; the digits' signs differ, their sum has none
-            const int h = __float2int_rn(both_of(all.h) * 0x1p20f), m = __float2int_rn(both_of(all.m) * 0x1p41f);
-            const int l = __float2int_rn(both_of(all.l) * 0x1p58f);
-            return (uint64_t)max(((int64_t)h << 38) + ((int64_t)m << 17) + l, (int64_t)0);
+        // the lane's, at most 8; the digits' signs differ, their sum has none
+        auto sum_of = [&](uint64_t hs, uint64_t ms, uint32_t ls) {
+            const int h = __float2int_rn(both_of(hs) * 0x1p20f), m = __float2int_rn(both_of(ms) * 0x1p41f);
+            return (uint64_t)(((int64_t)h << 38) + ((int64_t)m << 17) + (int32_t)ls);
         };
         auto plain = [&](const uint32_t (&x)[8]) {
-            Digits all = {0, 0, 0};
+            uint64_t h = 0, m = 0;
+            uint32_t l = 0u - 8u * C3;
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
                 const Digits d = digits_of(pair(within(__uint_as_float(x[e])), within(__uint_as_float(x[e + 1]))));
-                all.h = plus(all.h, d.h);
-                all.m = plus(all.m, d.m);
-                all.l = plus(all.l, d.l);
+                h = plus(h, d.h);
+                m = plus(m, d.m);
+                l += steps_of(d.l);
             }
-            return sum_of(all);
+            return sum_of(h, m, l);
         };
         auto beside = [&](const uint32_t (&x)[8], const uint32_t (&y)[8]) {
-            Digits all = {0, 0, 0};
+            uint64_t h = 0, m = 0;
+            uint32_t l = 0;
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
                 const float x0 = within(__uint_as_float(x[e])), x1 = within(__uint_as_float(x[e + 1]));
                 const Digits d = digits_of(pair(x0, x1));
                 // where the draft's is the larger, nothing is left: the same digits
                 const Digits f = digits_of(pair(fminf(within(__uint_as_float(y[e])), x0), fminf(within(__uint_as_float(y[e + 1])), x1)));
-                all.h = less(plus(all.h, d.h), f.h);
-                all.m = less(plus(all.m, d.m), f.m);
-                all.l = less(plus(all.l, d.l), f.l);
+                h = less(plus(h, d.h), f.h);
+                m = less(plus(m, d.m), f.m);
+                l += steps_of(d.l) - steps_of(f.l);
             }
-            return sum_of(all);
+            return sum_of(h, m, l);
         };
         uint32_t x[8], y[8];
         auto keep = [&](int i, uint64_t sum) {
@@ -461,18 +472,11 @@ verify_kernel(const VerifyParams p) {
                 sum += r[e];
             }
             sum = sum_up(sum, lane);
-            int at = locate(sum);
-            if (at < 0 && k + 1 < p.per) {  // a later batch: all of this one lies before the border
-                rest -= min(rest, shuffle64(sum, 31));
+            const int at = locate(sum);
+            if (at < 0) {  // a later batch: all of this one lies before the border
+                rest -= shuffle64(sum, 31);
                 continue;
             }
-            // The values by themselves are cut off at 2^-58 where their sum was not: behind all
-            // of them it is the last one that is there.
-            const bool behind = at < 0;
-            uint32_t some_left = 0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) some_left |= clean(x[e]) > clean(y[e]) ? 1u << e : 0u;
-            if (behind) at = 31 - __clz((int)__ballot_sync(0xffffffffu, some_left != 0));
             if (lane == at) {
                 int e = 0;
 #pragma unroll
@@ -481,7 +485,7 @@ verify_kernel(const VerifyParams p) {
                         rest -= r[j];
                         ++e;
                     }
-                p.next[b] = (int32_t)(v0 + (behind ? 31 - __clz((int)some_left) : e));
+                p.next[b] = (int32_t)(v0 + e);
             }
             return;
         }
