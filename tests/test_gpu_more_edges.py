@@ -69,3 +69,54 @@ def test_verify_values_near_a_step_of_the_sums(pool, V, kind, draft):
     want = [M.draw(fixed, float(v)) for v in u0]
     assert got[1] == [1] * B and got[2] == want
     assert pool.get_error() == (0 if sum(fixed) else pool.hs.HS_DEVERR_INDEX_RANGE)
+
+
+def test_verify_decides_small_probabilities_exactly(pool):
+    """u q < p and u s < p, on both sides of equality, for values whose last bits are below any step of the
+    sums and for products below f32's normal numbers."""
+    ulp = lambda x: float(np.spacing(np.float32(x)))
+    chain, draft = [], []  # (u, p) and (u, q, p)
+    for e in (-30, -34, -35, -40, -57, -58, -59, -70, -100, -126, -127, -140, -149):
+        for m in (1.0, 1.25, 1.9999):
+            x = float(np.float32(m * 2.0 ** e))
+            if x == 0:
+                continue
+            chain += [(x, x), (x, x + ulp(x)), (x + ulp(x), x), (max(x - ulp(x), 0.0), x)]
+            for q in (1.0, 0.75, 2.0 ** -20, 1.1 * 2.0 ** -60):
+                q = float(np.float32(q))
+                y = x / q
+                for u in (y, y + ulp(y), y - ulp(y), y + 2 * ulp(y)):
+                    u = float(np.float32(u))
+                    if 0 <= u < 1:
+                        draft += [(u, q, x)]
+    for cases in (chain, draft):
+        B, V = len(cases), 9
+        p = torch.zeros(B, 2, V)
+        p[:, :, 0] = 0.5
+        p[:, 0, 3] = torch.tensor([c[-1] for c in cases], dtype=torch.float64).float()
+        tokens = torch.full((B, 2), 3, dtype=torch.int32)
+        u = torch.full((B, 2), 0.25)
+        u[:, 1] = torch.tensor([c[0] for c in cases], dtype=torch.float64).float()
+        q = None
+        if cases is draft:
+            q = torch.zeros(B, 1, V)
+            q[:, 0, 3] = torch.tensor([c[1] for c in cases], dtype=torch.float64).float()
+        x = (tokens.cuda(), p.cuda(), None if q is None else q.cuda(), None, u.cuda())
+        got = run_verify(pool, *x)
+        assert 0.2 * B < got[1].count(2) < 0.9 * B
+        check_verify(got, *x)
+    # a tree: what an earlier child had is gone first
+    cases = [(w, r) for w in (0.5, 0.75, 0.9375) for r in chain]
+    B = len(cases)
+    p = torch.zeros(B, 3, V)
+    p[:, :, 0] = torch.tensor([c[0] for c in cases])[:, None]
+    p[:, 0, 3] = torch.tensor([c[1][1] for c in cases], dtype=torch.float64).float()
+    tokens = torch.tensor([0, 0, 3], dtype=torch.int32).expand(B, 3).contiguous()
+    u = torch.full((B, 3), 0.99)
+    u[:, 2] = torch.tensor([min(c[1][0] / (1 - c[0]), 0.9) for c in cases], dtype=torch.float64).float()
+    star = torch.tensor([1, 3, 5]).expand(B, 3).contiguous()
+    x = (tokens.cuda(), p.cuda(), None, star.cuda(), u.cuda())
+    got = run_verify(pool, *x)
+    assert 0.2 * B < got[1].count(2) < 0.9 * B
+    check_verify(got, *x)
+    assert pool.get_error() == 0

@@ -127,10 +127,28 @@ __device__ __forceinline__ uint64_t fixed(uint32_t b) {
     asm("shr.u64 %0, %1, %2;" : "=l"(r) : "l"((uint64_t)top << 32), "r"(127u - (b >> 23)));  // beyond 63: 0
     return r;
 }
-// A draft's test, u q < p, on u q's two 32-bit words (products below 2^-100 may count as zero).
-__device__ __forceinline__ bool below(float u, float q, float p) {
-    const float hi = __fmul_rn(u, q), lo = __fmaf_rn(u, q, -hi);
-    return hi < p || (hi == p && lo < 0.f);
+// A value that is not negative as m 2^e.
+__device__ __forceinline__ uint32_t parts(float x, int &e) {
+    const uint32_t b = __float_as_uint(x), ex = b >> 23;
+    e = (int)max(ex, 1u) - 150;
+    return (b & 0x7fffffu) | (ex ? 0x800000u : 0u);
+}
+// u b 2^eb < p, exactly, for b below 2^60: the integers u's times b and p's times 2^k.
+__device__ __forceinline__ bool below(float u, uint64_t b, int eb, float p) {
+    int eu, ep;
+    const uint64_t mu = parts(u, eu), mp = parts(p, ep), lo = mu * b, hi = __umul64hi(mu, b);
+    const int k = min(max(ep - eu - eb, -24), 100);  // further on nothing changes: u's times b is below 2^84
+    uint64_t plo, phi = 0;
+    if (k <= 0) {
+        plo = (mp + (1u << -k) - 1) >> -k;  // rounded up: the other side is a whole number
+    } else if (k < 64) {
+        plo = mp << k;
+        phi = mp >> (64 - k);
+    } else {
+        plo = 0;
+        phi = mp << (k - 64);
+    }
+    return hi < phi || (hi == phi && lo < plo);
 }
 template <typename P>
 __device__ __forceinline__ uint32_t bits_at(const void *row, int64_t i);
@@ -200,7 +218,7 @@ verify_kernel(const VerifyParams p) {
                             static_cast<const P *>(p.draft) + ((int64_t)b * (T - 1) + t - 1) * p.draft_ld, x)));
                 }
             }
-            u[k] = u[k] > 0.f ? fminf(u[k], 0x1.fffffep-1f) : 0.f;
+            u[k] = __uint_as_float(min(clean(__float_as_uint(u[k])), 0x3f7fffffu));  // on bits: arithmetic makes subnormal numbers 0
         }
         auto both = [&](bool lo, bool hi) {
             return (uint64_t)__ballot_sync(0xffffffffu, lo) | (uint64_t)__ballot_sync(0xffffffffu, hi) << 32;
@@ -208,8 +226,10 @@ verify_kernel(const VerifyParams p) {
         uint64_t path = 1;
         int end = 0, minus = 0, ngone = 0;
         if (p.draft) {  // a chain: up to the first that has no token or is refused
-            const bool s0 = tok[0] >= 0 && below(u[0], qx[0], px[0]);
-            const bool s1 = tok[1] >= 0 && below(u[1], qx[1], px[1]);
+            int e0, e1;
+            const uint32_t q0 = parts(qx[0], e0), q1 = parts(qx[1], e1);
+            const bool s0 = tok[0] >= 0 && below(u[0], q0, e0, px[0]);
+            const bool s1 = tok[1] >= 0 && below(u[1], q1, e1, px[1]);
             const uint64_t stop = both(lane > 0 && !s0, !s1);  // nodes from T on have no token
             const uint64_t there = both(tok[0] >= 0, tok[1] >= 0);
             const int n = stop ? __ffsll((long long)stop) - 1 : MAXT;
@@ -258,10 +278,7 @@ verify_kernel(const VerifyParams p) {
                         if (j < lane + 32 * k && par[k] == pj) left[k] -= min(left[k], mj);
                 }
             }
-            // probabilities below one step by themselves: 0 < p(x) stays
-            auto stays = [&](int k) {
-                return tok[k] >= 0 && (mine[k] ? part_of(u[k], left[k]) < mine[k] : u[k] * ((float)left[k] * 0x1p-58f) < px[k]);
-            };
+            auto stays = [&](int k) { return tok[k] >= 0 && below(u[k], left[k], -58, px[k]); };
             const bool t0 = stays(0), t1 = stays(1);
             for (;;) {  // down the first of each node's children that stays
                 const uint64_t kids = both(par[0] == end && t0, par[1] == end && t1);
