@@ -120,3 +120,59 @@ def test_verify_decides_small_probabilities_exactly(pool):
     assert 0.2 * B < got[1].count(2) < 0.9 * B
     check_verify(got, *x)
     assert pool.get_error() == 0
+
+
+# ------------------------------------------------------------------ window
+def signed(x):
+    return x - (1 << 64) if x >= 1 << 63 else x
+
+
+def only_seen_pages(c, L, T, trees, window, n_sink):
+    """Takes the blocks of all pages away that no query token sees, and fills their rows with NaN."""
+    rows, scales = c.pool.gpu_rows(), c.pool.gpu_scales()
+    gone = 0
+    for b in range(len(L)):
+        seen = torch.zeros(L[b], dtype=torch.bool)
+        for t in range(T):
+            seen |= M.window_mask(L[b], T, trees[b], t, window, n_sink)
+        table = c.table[b].copy()
+        for page in range(-(-L[b] // 64)):
+            if bool(seen[64 * page:64 * page + 64].any()):
+                continue
+            gone += 1
+            block = int(table[page])
+            rows[64 * block:64 * block + 64] = 0xFF
+            if scales is not None:
+                scales[64 * block:64 * block + 64] = math.nan
+            table[page] = -1
+        c.pool.page_map_range(b, 0, table, table * 0 - 1)
+    return gone
+
+
+@pytest.mark.parametrize("dtype,units", [("bf16", 1), ("fp8", 1), ("bf16", 3)])
+@pytest.mark.parametrize("T,window,n_sink,kind", [(4, 100, 0, "tree"), (7, 100, 5, "tree"), (4, 4, 1, "path"), (4, 64, 0, "path"),
+                                                  (5, 70, 3, "star"), (6, 80, 0, "empty"), (6, 80, 0, "low"), (63, 64, 0, "path"),
+                                                  (64, 64, 0, "tree"), (40, 50, 64, "high"), (3, 2 ** 31 - 1, 0, "path")])
+def test_window_of_a_tree_needs_no_page_that_it_does_not_see(dtype, units, T, window, n_sink, kind):
+    """At every alignment of the context's end; with pages of few nodes, and nodes that nobody sees."""
+    L = [200 + T + i for i in range(64)] + [T, T + 1, max(1, T - 2), T + 63]
+    # 16 heads and more where units are to be taken one after the other
+    H = 16 if units == 1 else -(-152 * 2 * 128 // (len(L) * T))
+    c = Cache(dtype, L)
+    one = (1 << T) - 1
+    if kind in ("tree", "path"):
+        tree = a_tree(9, len(L), T) if kind == "tree" else torch.tensor(
+            [[signed((2 << t) - 1) for t in range(T)]] * len(L)).cuda()
+    elif kind == "star":
+        tree = torch.tensor([[1 | 1 << t for t in range(T)]] * len(L)).cuda()
+    else:  # some see no node, or none sees the last nodes, or none the first ones
+        bits = {"empty": [0 if t % 2 else 1 << t for t in range(T)], "low": [1] * T, "high": [(1 << t) & ~7 for t in range(T)]}[kind]
+        tree = torch.tensor([[x & one for x in bits]] * len(L)).cuda()
+    trees = tree.tolist()
+    gone = only_seen_pages(c, L, T, trees, window, n_sink)
+    assert gone > 30 or window > 200
+    q = normal(6, len(L), T, H, P.DIM)
+    out, lse = attend_window(c, q, window, n_sink, tree)
+    assert c.pool.get_error() == 0
+    check_window(c, q, out, lse, window, n_sink, tree, tokens=sorted({0, T // 2, T - 1}))
+    c.close()

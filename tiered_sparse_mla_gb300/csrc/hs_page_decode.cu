@@ -361,13 +361,26 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
     };
     // WIN: a unit's entries, of the context's pages `e`; the others are left out
-    auto window_pages = [&](int len_u, int mt_u, int &e, int &sinks_u, int &skip_u) {
+    auto window_pages = [&](int len_u, int mt_u, int list_u, int &e, int &sinks_u, int &skip_u) {
         sinks_u = INT_MAX;
         skip_u = 0;
         if (e <= 0) return;
-        // The positions that some row sees: up to its last token's, and from its first
-        // token's window on (a tree's node may be as high up as the context's end).
-        const int t0 = p.tree ? -1 : mt_u * BM / p.H, t1 = p.tree ? p.T - 1 : (min(p.M, mt_u * BM + BM) - 1) / p.H;
+        // The positions that some row sees: up to its last token's, and from its first token's
+        // window on. A tree: up to the last node that some token sees (-1: none sees any), and from the
+        // window of the token that sees the fewest on. No page in between is without a row
+        // that some token sees: where the context's last ones are in no window, all tokens see all nodes.
+        int t0 = mt_u * BM / p.H, t1 = (min(p.M, mt_u * BM + BM) - 1) / p.H;
+        if (p.tree) {
+            const uint64_t *masks = p.tree + (size_t)list_u * p.T, nodes = p.T < 64 ? (1ull << p.T) - 1 : ~0ull;
+            int few = 64, last = -1;
+            for (int t = lane; t < p.T; t += 32) {
+                const uint64_t m = masks[t] & nodes;
+                few = min(few, __popcll(m));
+                last = max(last, 63 - __clzll((long long)m));
+            }
+            t0 = __reduce_min_sync(0xffffffffu, few) - 1;
+            t1 = __reduce_max_sync(0xffffffffu, last);
+        }
         const int top = len_u - p.T + t1, low = (int)max((long long)len_u - p.T + t0 - p.window + 1, 0ll);
         e = top < 0 ? 0 : top / kPage + 1;
         const int sinks = min((int)(((long long)p.n_sink + kPage - 1) / kPage), e);
@@ -401,7 +414,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         if (len_next > p.max_ctx) bad |= HS_DEVERR_INDEX_RANGE;
         nx.L = hs::context_within(len_next, p.max_ctx);
         nx.npages = nx.end = nx.L <= 0 ? 0 : (nx.L - 1) / kPage + 1;
-        window_pages(nx.L, nx.mt, nx.end, nx.sinks, nx.skip);
+        window_pages(nx.L, nx.mt, nx.list, nx.end, nx.sinks, nx.skip);
     };
     auto enter = [&]() {  // false: there is no next one
         if (!nx.there) return false;
@@ -430,7 +443,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         } else {
             end = L <= 0 ? 0 : (L - 1) / kPage + 1;
         }
-        if (WIN) window_pages(L, mt, end, wsinks, wskip);
+        if (WIN) window_pages(L, mt, list, end, wsinks, wskip);
         // splits begin at even entries: a step is two pages
         const long long steps = (end + 1) / 2;
         const int z = (int)(steps * (split + 1) / nsplit);
