@@ -176,3 +176,25 @@ def test_window_of_a_tree_needs_no_page_that_it_does_not_see(dtype, units, T, wi
     assert c.pool.get_error() == 0
     check_window(c, q, out, lse, window, n_sink, tree, tokens=sorted({0, T // 2, T - 1}))
     c.close()
+
+
+@pytest.mark.parametrize("kind", ["empty", "unknown"])
+def test_window_units_that_end_with_empty_ones(kind):
+    """Units one after the other whose last ones have no step: the sums of the unit before are read before
+    the empty one's are written. (A race does not show in every run: the results have to be right, and
+    the same each time.)"""
+    pairs = torch.cuda.get_device_properties(0).multi_processor_count // 2
+    g = torch.Generator().manual_seed(13)
+    ctx = [int(x) for x in torch.randint(1, 300, (2 * pairs,), generator=g)] + [0] * pairs
+    c = Cache("bf16", ctx)
+    q = normal(14, 3 * pairs, 1, 128, P.DIM)
+    req = torch.arange(3 * pairs, **I32)
+    if kind == "unknown":
+        req[2 * pairs:] = -1
+    out, lse = attend_window(c, q, 200, 1, req=req)
+    check_window(c, q[:2 * pairs], out[:2 * pairs], lse[:2 * pairs], 200, 1)
+    assert not out[2 * pairs:].any() and bool((lse[2 * pairs:] == -math.inf).all())
+    for _ in range(50):
+        again = attend_window(c, q, 200, 1, req=req)
+        assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    c.close(0 if kind == "empty" else c.hs.HS_DEVERR_BAD_REQUEST)

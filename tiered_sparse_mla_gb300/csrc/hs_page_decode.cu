@@ -1124,7 +1124,9 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (!ok && lane == 0) fail();
             __syncwarp();
             if (p.inside) cluster_arrive_relaxed();  // what this warp needed of this CTA's memory is used
-            // the row's sum over its four threads' keys
+            // The row's sum over its four threads' keys. LOOP: the last unit's have been read: before a unit's
+            // steps its barriers say so, a unit without steps has this one.
+            if (LOOP && nsteps == 0) named_bar_sync(1, 32 * NSW);
             st_shared_f1(xm + 4 * tid, l);
             named_bar_sync(1, 32 * NSW);
             l = (ld_shared_f1(xm_row(0)) + ld_shared_f1(xm_row(64))) + (ld_shared_f1(xm_row(128)) + ld_shared_f1(xm_row(192)));
