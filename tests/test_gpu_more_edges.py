@@ -198,3 +198,49 @@ def test_window_units_that_end_with_empty_ones(kind):
         again = attend_window(c, q, 200, 1, req=req)
         assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
     c.close(0 if kind == "empty" else c.hs.HS_DEVERR_BAD_REQUEST)
+
+
+# ------------------------------------------------------------------ eviction
+@pytest.mark.parametrize("saved_only", [False, True])
+@pytest.mark.parametrize("pages", [513, 2049, 4097, 5000, 8193, 32769, 270000])
+def test_evict_releases_pages_of_long_contexts(pages, saved_only):
+    """Requests whose pages are dealt to clusters of 1, 2, 4 and 8, and more than fit in their shared
+    memory: the table, the host copies and the lists after the call itself."""
+    ctx = [pages * 64, pages * 64 - 64 * 17 - 3, 64 * (pages // 3) + 1]
+    c = Tables(ctx, seed=pages)
+    g = torch.Generator().manual_seed(23)
+    w = torch.rand(c.R, c.P, generator=g)
+    w[1] = (w[1] * 50).floor()
+    want = c.table.copy()
+    for budget in (pages - pages // 3, pages // 5, 7):
+        kept, freed, count = run_evict(c, [2, 0, 1], [budget] * 3, w.cuda(), c.P, 2, 3, saved_only)
+        for i, r in enumerate((2, 0, 1)):
+            stay, gone = M.evict(want[r], c.saved[r], w[r].tolist(), ctx[r], budget, 2, 3, saved_only)
+            assert kept[i] == stay + [-1] * (c.P - len(stay))
+            assert count[i] == len(gone) and freed[i][:len(gone)] == want[r, gone].tolist()
+            assert set(freed[i][len(gone):]) <= {-7}
+            want[r, gone] = -1
+        now = c.now()
+        assert np.array_equal(now[..., 0], want) and np.array_equal(now[..., 1], c.saved)
+    c.close()
+
+
+@pytest.mark.parametrize("max_pages", [512, 513, 3000, 16384])
+def test_evict_short_requests_of_long_pools(max_pages):
+    """The kernel goes by the pool's pages, not by a request's: the same result in any pool."""
+    ctx = [0, 1, 64, 65, 2000, 63 * 64, 64 * 64, 300 * 64 + 7]
+    c = Tables(ctx, max_ctx=max_pages * 64, seed=3)
+    g = torch.Generator().manual_seed(24)
+    w = torch.exp(torch.randn(c.R, c.P, generator=g))
+    w[4] = 0.5
+    for budget in ([0] * 8, [1, 1, 1, 1, 9, 20, 64, 100], [10 ** 9] * 8):
+        for plan in (True, False):
+            kept, freed, count = run_evict(c, list(range(8)), budget, w.cuda(), 400, 1, 2, False, plan)
+            for r in range(8):
+                stay, gone = M.evict(c.table[r], c.saved[r], w[r].tolist(), ctx[r], budget[r], 1, 2, False)
+                assert kept[r] == stay + [-1] * (400 - len(stay))
+                assert count[r] == len(gone) and freed[r][:len(gone)] == c.table[r, gone].tolist()
+                if not plan:
+                    c.table[r, gone] = -1
+            assert np.array_equal(c.now()[..., 0], c.table)
+    c.close()
