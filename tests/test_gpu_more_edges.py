@@ -8,7 +8,7 @@ import torch
 
 import _more as M
 import _pages as P
-from test_gpu_more import (I32, SCALE, Cache, Tables, a_draft, a_tree, attend_window, check_verify, check_window, i32,
+from test_gpu_more import (I32, SCALE, Cache, Tables, a_draft, a_tree, attend_window, check_verify, check_weights, check_window, i32,
                            normal, pool, run_evict, run_verify)
 
 pytestmark = pytest.mark.gpu
@@ -243,4 +243,67 @@ def test_evict_short_requests_of_long_pools(max_pages):
                 if not plan:
                     c.table[r, gone] = -1
             assert np.array_equal(c.now()[..., 0], c.table)
+    c.close()
+
+
+# ------------------------------------------------------------------ the documents' step
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+def test_the_readme_step_of_drafts(dtype):
+    """README.md's step of drafts in a cache that must not grow, as it stands there: a tree whose accepted
+    rows do not lie where they were drafted, from a list of pages that an earlier step kept."""
+    import os
+    with open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")) as f:
+        blocks = f.read().split("```")[1::2]
+    code, = [b for b in blocks if "verify_drafts" in b]
+    B, T, H, V = 3, 8, 16, 300
+    ctx = [700, 64 * 10 + 3, 640]  # one has just come to a new page
+    c = Cache(dtype, ctx, host=2, garbage=False)
+    hs = c.hs
+    tokens, probs, _, tree, uniform = a_draft(91, B, T, V, torch.float32, "tree", sharp=2.0)
+    new_rows, q = normal(92, B, T, P.DIM), normal(93, B, T, H, P.DIM)
+    req_ids = torch.arange(B, **I32)
+    pages = [[0, 2, 3, 7, 8, 9, 10], [0, 1, 5, 9, 10], [0, 4, 8, 9]]  # the earlier step's, and new ones behind them
+    kept = torch.full((B, c.P), -1, **I32)
+    for b in range(B):
+        kept[b, :len(pages[b])] = i32(*pages[b])
+    weights = torch.rand(c.R, c.P, generator=torch.Generator().manual_seed(94)).cuda()
+    for b in range(B):
+        weights[b, -(-ctx[b] // 64):] = -7.0
+    before = weights.clone()
+    space = lambda n: torch.empty(max(n, 1), dtype=torch.uint8, device="cuda")
+    names = dict(
+        pool=c.pool, new_rows=new_rows, req_ids=req_ids, q=q, tree_masks=tree, sm_scale=SCALE, tokens=tokens, probs=probs,
+        uniform=uniform, kept=kept, weights=weights, budget=i32(4, 4, 4),
+        out=torch.empty(B, T, H, 512, dtype=torch.bfloat16, device="cuda"), lse=torch.empty(B, T, H, device="cuda"),
+        index=torch.empty(B, T, **I32), count=torch.empty(B, **I32), next_token=torch.empty(B, **I32),
+        freed=torch.empty(B, c.P, **I32), n_freed=torch.empty(B, **I32),
+        ws1=space(hs.hs_window_workspace_bytes(c.pool.handle, B, T, H, 4096, 4)),
+        ws2=space(hs.hs_page_decode_workspace_bytes(B, T, H, c.P)),
+        ws3=space(hs.hs_weights_workspace_bytes(c.pool.handle, B, T, H)))
+    rows = c.pool.gpu_rows().clone()
+    scales = None if dtype == "bf16" else c.pool.gpu_scales().clone()
+    exec(code, names)
+    torch.cuda.synchronize()
+    assert c.pool.get_error() == 0
+    moved = 0
+    for b in range(B):
+        path, token = M.verify(tokens[b].tolist(), probs[b].tolist(), None, tree[b].tolist(), uniform[b].tolist())
+        assert names["index"][b].tolist() == path + [-1] * (T - len(path)) and int(names["next_token"][b]) == token
+        moved += path != list(range(len(path)))
+        stay, gone = M.evict(c.table[b], [-1] * c.P, weights[b].tolist(), ctx[b], 4, 1, 2, False)
+        assert [x for x in kept[b].tolist() if x >= 0] == stay and int(names["n_freed"][b]) == len(gone)
+    assert moved  # otherwise the order of the calls makes no difference
+    # what the attention and the weights saw: the draft's rows where its masks say
+    c.pool.gpu_rows().copy_(rows)
+    if scales is not None:
+        c.pool.gpu_scales().copy_(scales)
+    c.pool.append_rows(new_rows, req_ids)
+    torch.cuda.synchronize()
+    for b in range(B):
+        for t in range(T):
+            pos = torch.cat([torch.arange(x * 64, min(ctx[b], x * 64 + 64)) for x in pages[b]])
+            pos = pos[P.seen_mask(ctx[b], T, tree[b].tolist(), t)[pos]]
+            ref = P.attention(q[b, t].double(), c.kv(b, pos), torch.ones(len(pos), dtype=torch.bool, device="cuda"), SCALE)
+            P.check_attention(names["out"][b, t], names["lse"][b, t], *ref, what=f"request {b} token {t}")
+    check_weights(c, weights, q, names["lse"], tree, prior=before, decay=0.99)
     c.close()
