@@ -73,6 +73,7 @@
 #include <type_traits>
 
 #include "hs_internal.cuh"
+#include "hs_pages.cuh"
 #include "hs_tc.cuh"
 #include "hs_tmap.cuh"
 
@@ -170,33 +171,9 @@ __device__ __forceinline__ void bulk_push(uint32_t dst, uint32_t src, uint32_t b
                  "r"(src), "r"(bytes), "r"(bar)
                  : "memory");
 }
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
-}
-// Two BF16 values times 2^k (a pair of BF16; at most 448, or NaN) as the sums of two
-// e4m3 codes each. F16 holds the products' eight bits down to 2^-17, the codes'
-// smallest step is 2^-9.
-__device__ __forceinline__ void e4m3_pieces(uint32_t w, uint32_t pow2, uint16_t &p, uint16_t &r) {
-    uint32_t x, h;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(w), "r"(pow2));
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(x) : "f"(__uint_as_float(x & 0xffff0000u)), "f"(__uint_as_float(x << 16)));
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(p) : "r"(x));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(p));
-    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(h));
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
-}
-__device__ __forceinline__ void bf16x4_to_e4m3(uint32_t w0, uint32_t w1, uint32_t pow2, uint32_t &p, uint32_t &r) {
-    uint16_t p0, p1, r0, r1;
-    e4m3_pieces(w0, pow2, p0, r0);
-    e4m3_pieces(w1, pow2, p1, r1);
-    asm("mov.b32 %0, {%1, %2};" : "=r"(p) : "h"(p0), "h"(p1));
-    asm("mov.b32 %0, {%1, %2};" : "=r"(r) : "h"(r0), "h"(r1));
 }
 // Four e4m3 codes to F16, exactly; the NaN codes (rows that no query sees may hold
 // any byte) become a finite value.
@@ -214,17 +191,6 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
         "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
         "l"(src), "r"(bytes), "r"(bar)
         : "memory");
-}
-// Two f32 operations in one instruction.
-__device__ __forceinline__ void mul2(float &a, float &b, float c, float d) {
-    asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n mul.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
-        : "+f"(a), "+f"(b)
-        : "f"(c), "f"(d));
-}
-__device__ __forceinline__ void add2(float &a, float &b, float c, float d) {
-    asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
-        : "+f"(a), "+f"(b)
-        : "f"(c), "f"(d));
 }
 // a and b plus 0 times c and d: NaN where one is not finite
 __device__ __forceinline__ void zeros_of(float &a, float &b, float c, float d) {
@@ -788,10 +754,8 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             uint32_t top = max(m & 0xffffu, m >> 16);
 #pragma unroll
             for (int o = 1; o < 4; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));  // all have read
-            // times 2^k it lies in (224, 448]; a row that is not finite becomes NaN
-            const int k = min(135 - (int)(top >> 7) - ((top & 0x7fu) > 0x60u), 126);
-            const uint32_t q_pow = top >= 0x7f80u ? 0x7fc07fc0u : (uint32_t)(k + 127) * 0x00800080u;
-            if (part == 0) st_shared_f1(xm + 4 * crow, __uint_as_float((uint32_t)(127 - k) << 23));
+            const uint32_t q_pow = query_power(top);
+            if (part == 0) st_shared_f1(xm + 4 * crow, query_back(top));
 #pragma unroll
             for (int i = 0; i < NK; ++i) {
                 uint32_t w[4], r[4];
@@ -1457,21 +1421,6 @@ PagePlan page_plan(int64_t lists, int64_t T, int64_t H, int64_t N) {
         pl.ws_bytes = pl.ws_o_bytes + ((rows * sizeof(float) + 255) & ~size_t(255));
     }
     return pl;
-}
-
-// [rows][9 chunks][64] seen as (element, row, chunk), boxes of 64 x 64 x n
-bool make_page_map(CUtensorMap *m, bool fp8, const void *rows, uint64_t n_rows, uint32_t nchunks, CUtensorMapSwizzle sw) {
-    auto fn = encode_fn();
-    if (!fn) return false;
-    const cuuint64_t rb = fp8 ? kDim : 2 * kDim;
-    cuuint64_t dims[3] = {64, n_rows, 9};
-    cuuint64_t strides[2] = {rb, rb / 9};
-    cuuint32_t box[3] = {64, (cuuint32_t)kPage, nchunks};
-    cuuint32_t es[3] = {1, 1, 1};
-    return fn(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-              const_cast<void *>(rows), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              sw,
-              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // How many clusters of two pairs of CTAs the device holds at once.

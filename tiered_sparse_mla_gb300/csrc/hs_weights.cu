@@ -44,6 +44,7 @@
 #include <type_traits>
 
 #include "hs_internal.cuh"
+#include "hs_pages.cuh"
 #include "hs_tc.cuh"
 #include "hs_tmap.cuh"
 
@@ -98,46 +99,12 @@ struct WeightParams {
     float scale_log2, decay;
 };
 
-__device__ __forceinline__ int pages_of(int tokens) { return tokens <= 0 ? 0 : (tokens - 1) / kPage + 1; }
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ void mul2(float &a, float &b, float c, float d) {
-    asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n mul.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
-        : "+f"(a), "+f"(b)
-        : "f"(c), "f"(d));
-}
-__device__ __forceinline__ void add2(float &a, float &b, float c, float d) {
-    asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
-        : "+f"(a), "+f"(b)
-        : "f"(c), "f"(d));
-}
 // a = a c + e, b = b d + f
 __device__ __forceinline__ void fma2(float &a, float &b, float c, float d, float e, float f) {
     asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n mov.b64 z, {%4, %5};\n"
         " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}\n"
         : "+f"(a), "+f"(b)
         : "f"(c), "f"(d), "f"(e), "f"(f));
-}
-// Two BF16 values times 2^k (at most 448, or NaN) as the sums of two e4m3 codes each: F16
-// holds the products' eight bits down to 2^-17, the codes' smallest step is 2^-9.
-__device__ __forceinline__ void two_codes(uint32_t w, uint32_t pow2, uint16_t &p, uint16_t &r) {
-    uint32_t x, h;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(w), "r"(pow2));
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(x) : "f"(__uint_as_float(x & 0xffff0000u)), "f"(__uint_as_float(x << 16)));
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(p) : "r"(x));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(p));
-    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(h));
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
-}
-__device__ __forceinline__ void four_codes(uint32_t w0, uint32_t w1, uint32_t pow2, uint32_t &p, uint32_t &r) {
-    uint16_t p0, p1, r0, r1;
-    two_codes(w0, pow2, p0, r0);
-    two_codes(w1, pow2, p1, r1);
-    asm("mov.b32 %0, {%1, %2};" : "=r"(p) : "h"(p0), "h"(p1));
-    asm("mov.b32 %0, {%1, %2};" : "=r"(r) : "h"(r0), "h"(r1));
 }
 // FP8: the query rows' codes, laid out as the rows were: per chunk of 64 values the first codes,
 // then the second ones; and the inverses of their powers of two. One warp per row.
@@ -164,17 +131,15 @@ weight_codes_kernel(const uint4 *q, uint2 *codes, float *powers, int64_t rows) {
     }
     // bits of magnitudes are in their order, infinities and NaN above all
     top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
-    // times 2^k it lies in (224, 448]; a row that is not finite becomes NaN
-    const int k2 = min(135 - (int)(top >> 7) - ((top & 0x7fu) > 0x60u), 126);
-    const uint32_t pow2 = top >= 0x7f80u ? 0x7fc07fc0u : (uint32_t)(k2 + 127) * 0x00800080u;
-    if (lane == 0) powers[m] = __uint_as_float((uint32_t)(127 - k2) << 23);
+    const uint32_t pow2 = query_power(top);
+    if (lane == 0) powers[m] = query_back(top);
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
         const int u = lane + 32 * k;
         if (u >= UNITS) break;
         uint2 z, r;
-        four_codes(y[k].x, y[k].y, pow2, z.x, r.x);
-        four_codes(y[k].z, y[k].w, pow2, z.y, r.y);
+        bf16x4_to_e4m3(y[k].x, y[k].y, pow2, z.x, r.x);
+        bf16x4_to_e4m3(y[k].z, y[k].w, pow2, z.y, r.y);
         uint2 *to = codes + m * (2 * UNITS) + (u >> 3) * 16 + (u & 7);
         to[0] = z;
         to[8] = r;
@@ -628,21 +593,6 @@ int parts_of(int64_t groups, int64_t tiles, double us_tile) {
     return (int)parts;
 }
 
-// [rows][9 chunks][64] seen as (element, row, chunk), boxes of one page's chunk
-bool make_key_map(CUtensorMap *m, bool fp8, const void *rows, uint64_t n_rows) {
-    auto fn = encode_fn();
-    if (!fn) return false;
-    const cuuint64_t rb = fp8 ? kDim : 2 * kDim;
-    cuuint64_t dims[3] = {64, n_rows, 9};
-    cuuint64_t strides[2] = {rb, rb / 9};
-    cuuint32_t box[3] = {64, (cuuint32_t)kPage, 1};
-    cuuint32_t es[3] = {1, 1, 1};
-    return fn(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(rows),
-              dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              fp8 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <bool FP8>
 hs_status launch_weights(int dev, cudaStream_t s, const CUtensorMap &tk, const CUtensorMap &tq, const WeightParams &p) {
     static std::atomic<int> state[64];
@@ -732,7 +682,8 @@ extern "C" hs_status hs_page_weights(hs_pool_t pool, int32_t B, int32_t T, int32
     p.scale_log2 = sm_scale * 1.4426950408889634f;
     p.decay = decay;
     CUtensorMap tk, tq;
-    if (!make_key_map(&tk, fp8, pool->d_rows, (uint64_t)(pool->cfg.n_gpu_blocks + 1) * kPage) ||
+    if (!make_page_map(&tk, fp8, pool->d_rows, (uint64_t)(pool->cfg.n_gpu_blocks + 1) * kPage, 1,
+                       fp8 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B) ||
         !make_map(&tq, CU_TENSOR_MAP_DATA_TYPE_UINT16, fp8 ? ws : d_q, kDim, (uint64_t)p.M, B, 2 * kDim, 64, p.N / 2,
                   CU_TENSOR_MAP_SWIZZLE_128B))
         return HS_ERR_CUDA;
