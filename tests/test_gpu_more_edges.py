@@ -200,6 +200,31 @@ def test_window_units_that_end_with_empty_ones(kind):
     c.close(0 if kind == "empty" else c.hs.HS_DEVERR_BAD_REQUEST)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("T,window,n_sink", [(200, 16, 64), (130, 1, 130), (70, 16, 300)])
+def test_window_of_sinks_that_are_query_tokens(dtype, T, window, n_sink):
+    """Contexts that begin inside the query tokens (a whole prompt, say): the first positions stay visible to
+    the later tokens, those among them that are query tokens themselves too; the same by the plain form of
+    the measured cases."""
+    from perf import more_operators as plain
+    case = {"op": "window", "dtype": dtype, "B": 2, "T": T, "H": 16, "ctx": T + 10, "window": window, "sink": n_sink, "tree": False}
+    c = Cache(dtype, [T + 10, T], garbage=False)
+    q = normal(15, 2, T, 16, P.DIM)
+    out, lse = attend_window(c, q, window, n_sink)
+    check_window(c, q, out, lse, window, n_sink)
+    L = T + 10
+    kv = M.window_mask(L, T, None, T - 1, window, n_sink)
+    assert int(kv.sum()) == min(L, n_sink + window)  # the last token: none of the sinks is left out
+    rows = c.pool.gpu_rows()
+    state = {"case": case, "lens": torch.tensor(c.ctx, **I32), "table": torch.from_numpy(c.table).cuda(), "q": q, "tree": None,
+             "rows": rows.view(torch.bfloat16) if dtype == "bf16" else rows.view(torch.float8_e4m3fn),
+             "scales": None if dtype == "bf16" else c.pool.gpu_scales()}
+    assert plain.SCALE == SCALE
+    o2, l2 = plain._window(state)
+    check_window(c, q, o2, l2, window, n_sink)
+    c.close()
+
+
 # ------------------------------------------------------------------ eviction
 @pytest.mark.parametrize("saved_only", [False, True])
 @pytest.mark.parametrize("pages", [513, 2049, 4097, 5000, 8193, 32769, 270000])
