@@ -200,6 +200,21 @@ def test_window_units_that_end_with_empty_ones(kind):
     c.close(0 if kind == "empty" else c.hs.HS_DEVERR_BAD_REQUEST)
 
 
+@pytest.mark.parametrize("B,T,H,window", [(160, 1, 128, 4096), (160, 1, 128, 100), (157, 3, 80, 1500), (10, 500, 16, 4096), (3, 1300, 16, 1000)])
+def test_window_units_of_uneven_requests(B, T, H, window):
+    """Twice as many units as pairs of CTAs and more, of requests of very different lengths: those taken one
+    after the other, and those that get CTAs of their own and of which the last are split."""
+    g = torch.Generator().manual_seed(16)
+    ctx = [T + int(math.exp(x)) for x in (9 * torch.rand(B, generator=g)).tolist()]
+    c = Cache("bf16", ctx)
+    q = normal(17, B, T, H, P.DIM)
+    out, lse = attend_window(c, q, window, 3)
+    check_window(c, q, out, lse, window, 3, tokens=sorted({0, T // 3, T // 2, T - 1}))
+    again = attend_window(c, q, window, 3)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    c.close()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp8"])
 @pytest.mark.parametrize("T,window,n_sink", [(200, 16, 64), (130, 1, 130), (70, 16, 300)])
 def test_window_of_sinks_that_are_query_tokens(dtype, T, window, n_sink):

@@ -1533,18 +1533,28 @@ int64_t window_pages(const hs_pool *pool, int64_t T, int64_t H, int64_t window, 
     return n < pool->max_pages ? n : pool->max_pages;
 }
 
-// Windows over BF16 rows with two units or more for each pair of CTAs: a pair takes them one
-// after the other and none is split. The next unit's queries and keys come, and its first
-// scores are multiplied, during the last one's end: 2 x 1,999 tokens of 16 heads, windows of
-// 1,024, 124 us against 145 with a launch of its own for each unit (which takes 3 of a unit's
-// 20 us, and nothing runs while it ends).
+// Windows over BF16 rows with two units or more for each pair of CTAs may be taken one after the
+// other by a pair, none of them split: the next unit's queries and keys come, and its first
+// scores are multiplied, during the last one's end, so that a unit's ends take 4 us instead of 7
+// (2 x 1,999 tokens of 16 heads, windows of 1,024: 127 us against 148 with a launch's CTAs for each
+// unit). But units are dealt out beforehand, and those of requests of other lengths are not
+// evened out: requests of one unit lose about a unit's time, less the more units a request
+// has, since its own are alike and go to all pairs. Measured one after the other / each by itself, contexts
+// spread over 1 to 8,192: 608 requests of one unit, windows of 512 97-105 / 108-111, of 4,096
+// 258-295 / 202-217; 38 of 16, windows of 4,096 192-231 / 150-186; 9 of 63, 95-197 / 115-203.
+// Equal contexts of 8,192 and windows of 4,096: 160 requests 216 / 181 (the last 8 units split), 608 592 / 614.
+constexpr double US_NEXT = 4.0;
+
 PagePlan window_plan(bool fp8, int64_t lists, int64_t T, int64_t H, int64_t N, bool &loop) {
-    const int64_t mtiles = (T * H + BM - 1) / BM;
-    loop = !fp8 && lists * mtiles >= 2 * pairs_at_once();
-    if (!loop) return page_plan(lists, T, H, N);
+    const PagePlan each = page_plan(lists, T, H, N);
+    const int64_t mtiles = each.mtiles, pairs = pairs_at_once(), units = lists * mtiles;
+    const double steps = (double)((N + 1) / 2) * US_STEP, uneven = 1.0 - 2.0 * (double)mtiles / (double)pairs;
+    loop = !fp8 && units >= 2 * pairs &&
+           (double)((units + pairs - 1) / pairs) * (steps + US_NEXT) + (uneven > 0 ? uneven * steps : 0.0) < each.us;
+    if (!loop) return each;
     PagePlan pl{};
-    pl.M = (int)(T * H);
-    pl.mtiles = (int)mtiles;
+    pl.M = each.M;
+    pl.mtiles = each.mtiles;
     pl.nsplit = 1;
     return pl;
 }
