@@ -152,7 +152,8 @@ def only_seen_pages(c, L, T, trees, window, n_sink):
 @pytest.mark.parametrize("dtype,units", [("bf16", 1), ("fp8", 1), ("bf16", 3)])
 @pytest.mark.parametrize("T,window,n_sink,kind", [(4, 100, 0, "tree"), (7, 100, 5, "tree"), (4, 4, 1, "path"), (4, 64, 0, "path"),
                                                   (5, 70, 3, "star"), (6, 80, 0, "empty"), (6, 80, 0, "low"), (63, 64, 0, "path"),
-                                                  (64, 64, 0, "tree"), (40, 50, 64, "high"), (3, 2 ** 31 - 1, 0, "path")])
+                                                  (64, 64, 0, "tree"), (40, 50, 64, "high"), (3, 2 ** 31 - 1, 0, "path"),
+                                                  (9, 20, 0, "random"), (40, 41, 7, "random")])
 def test_window_of_a_tree_needs_no_page_that_it_does_not_see(dtype, units, T, window, n_sink, kind):
     """At every alignment of the context's end; with pages of few nodes, and nodes that nobody sees."""
     L = [200 + T + i for i in range(64)] + [T, T + 1, max(1, T - 2), T + 63]
@@ -165,6 +166,9 @@ def test_window_of_a_tree_needs_no_page_that_it_does_not_see(dtype, units, T, wi
             [[signed((2 << t) - 1) for t in range(T)]] * len(L)).cuda()
     elif kind == "star":
         tree = torch.tensor([[1 | 1 << t for t in range(T)]] * len(L)).cuda()
+    elif kind == "random":
+        g = torch.Generator().manual_seed(18)
+        tree = (torch.randint(0, 1 << 62, (len(L), T), generator=g) & torch.randint(0, 1 << 62, (len(L), T), generator=g)).cuda()
     else:  # some see no node, or none sees the last nodes, or none the first ones
         bits = {"empty": [0 if t % 2 else 1 << t for t in range(T)], "low": [1] * T, "high": [(1 << t) & ~7 for t in range(T)]}[kind]
         tree = torch.tensor([[x & one for x in bits]] * len(L)).cuda()
