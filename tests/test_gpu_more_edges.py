@@ -219,6 +219,26 @@ def test_window_units_of_uneven_requests(B, T, H, window):
     c.close()
 
 
+@pytest.mark.parametrize("ctx,T,H,window", [([0, 66, 65, 66, 70, 66, 0, 67, 1, 3], 65, 64, 16),
+                                            ([0, 1, 53, 55, 1, 1, 52, 80, 52, 81, 159, 1, 53, 112, 53, 1, 79, 53, 58, 53, 645], 52, 40, 818),
+                                            ([0] * 100 + [40] * 60 + [0] * 100 + [100] * 100, 1, 128, 64)])
+def test_window_units_without_steps_beside_other_work(ctx, T, H, window):
+    """Units without steps before and between others, while another stream keeps the GPU busy: no role of a
+    pair of CTAs misses what another says (it would wait until the limit: HS_DEVERR_TIMEOUT)."""
+    c = Cache("bf16", ctx)
+    q = normal(19, len(ctx), T, H, P.DIM)
+    out, lse = attend_window(c, q, window, 0)
+    check_window(c, q, out, lse, window, 0, tokens=sorted({0, T // 2, T - 1}))
+    side, x = torch.cuda.Stream(), torch.randn(4096, 4096, device="cuda")
+    for k in range(30):
+        with torch.cuda.stream(side):
+            for _ in range(1 + k % 3):
+                torch.mm(x[:256 << (k % 4)], x)
+        again = attend_window(c, q, window, 0)
+        assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    c.close()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp8"])
 @pytest.mark.parametrize("T,window,n_sink", [(200, 16, 64), (130, 1, 130), (70, 16, 300)])
 def test_window_of_sinks_that_are_query_tokens(dtype, T, window, n_sink):

@@ -621,10 +621,10 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             };
             constexpr int PER = FP8 ? NK / C::GK : 8 / C::GK;  // groups of K chunks per step
             int s = 0;
-            uint32_t ph = 0;
+            uint32_t ph = 0, ready = 0;  // units with steps so far
             do {
                 peek();
-                ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_QREADY), (uint32_t)it & 1u));
+                if (!LOOP || nsteps > 0) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_QREADY), ready++ & 1u));
                 tc_fence_after();
                 for (int j = 0; j < nsteps && ok; ++j) {
                     const int gj = g0 + j;
@@ -788,14 +788,16 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
             tmem_wait_st();
         }
-        auto q_moved = [&]() {
+        // A unit without steps is not announced to the MMA issuer: nothing would hold the softmax back until the
+        // issuer has looked, and a phase missed is waited for without end.
+        auto q_moved = [&](bool steps) {
             fence_proxy_async();  // the staging space is refilled next
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::B_QDONE));
-            if (LOOP || nsteps > 0) arrive_lead(lead(C::B_QREADY));
+            if (steps) arrive_lead(lead(C::B_QREADY));
         };
-        q_moved();
+        q_moved(nsteps > 0);
 
         const int tpl = LOOP ? 1 : p.tpl;
         auto token_of = [&](int g) { return g < p.M ? g / p.H : 0; };
@@ -1079,7 +1081,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     }
                     tmem_wait_st();
                 }
-                q_moved();
+                q_moved(nx.end > 0);
             }
             if (ok && nsteps > 0) {
                 ok = __all_sync(0xffffffffu, mbar_wait_inline(bar(C::B_PVDONE), (uint32_t)(g1 - 1) & 1u));
