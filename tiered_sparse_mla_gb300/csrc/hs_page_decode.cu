@@ -294,6 +294,17 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     // length) and the length.
     const int32_t *entries = p.pages ? p.pages + (size_t)list * p.N : nullptr;
     const bool loader = warp == 0 || warp == 3;
+    // WIN, a tree: of this lane's tokens, the fewest nodes that one sees, and the last node
+    auto tree_nodes = [&](int list_u, int &few, int &last) {
+        const uint64_t *masks = p.tree + (size_t)list_u * p.T, nodes = p.T < 64 ? (1ull << p.T) - 1 : ~0ull;
+        for (int t = lane; t < p.T; t += 32) {
+            const uint64_t m = masks[t] & nodes;
+            few = min(few, __popcll(m));
+            last = max(last, 63 - __clzll((long long)m));
+        }
+    };
+    int few = 64, last = -1;
+    if (WIN && loader && p.tree) tree_nodes(list, few, last);
     int e0 = -1;  // entry `lane`
     if (loader && entries && lane < p.N) e0 = entries[lane];
     const int req = p.req[list / p.tpl];
@@ -327,7 +338,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
     };
     // WIN: a unit's entries, of the context's pages `e`; the others are left out
-    auto window_pages = [&](int len_u, int mt_u, int list_u, int &e, int &sinks_u, int &skip_u) {
+    auto window_pages = [&](int len_u, int mt_u, int few_u, int last_u, int &e, int &sinks_u, int &skip_u) {
         sinks_u = INT_MAX;
         skip_u = 0;
         if (e <= 0) return;
@@ -337,15 +348,8 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         // that some token sees: where the context's last ones are in no window, all tokens see all nodes.
         int t0 = mt_u * BM / p.H, t1 = (min(p.M, mt_u * BM + BM) - 1) / p.H;
         if (p.tree) {
-            const uint64_t *masks = p.tree + (size_t)list_u * p.T, nodes = p.T < 64 ? (1ull << p.T) - 1 : ~0ull;
-            int few = 64, last = -1;
-            for (int t = lane; t < p.T; t += 32) {
-                const uint64_t m = masks[t] & nodes;
-                few = min(few, __popcll(m));
-                last = max(last, 63 - __clzll((long long)m));
-            }
-            t0 = __reduce_min_sync(0xffffffffu, few) - 1;
-            t1 = __reduce_max_sync(0xffffffffu, last);
+            t0 = __reduce_min_sync(0xffffffffu, few_u) - 1;
+            t1 = __reduce_max_sync(0xffffffffu, last_u);
         }
         const int top = len_u - p.T + t1, low = (int)max((long long)len_u - p.T + t0 - p.window + 1, 0ll);
         e = top < 0 ? 0 : top / kPage + 1;
@@ -380,7 +384,9 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         if (len_next > p.max_ctx) bad |= HS_DEVERR_INDEX_RANGE;
         nx.L = hs::context_within(len_next, p.max_ctx);
         nx.npages = nx.end = nx.L <= 0 ? 0 : (nx.L - 1) / kPage + 1;
-        window_pages(nx.L, nx.mt, nx.list, nx.end, nx.sinks, nx.skip);
+        int few_u = 64, last_u = -1;
+        if (p.tree) tree_nodes(nx.list, few_u, last_u);
+        window_pages(nx.L, nx.mt, few_u, last_u, nx.end, nx.sinks, nx.skip);
     };
     auto enter = [&]() {  // false: there is no next one
         if (!nx.there) return false;
@@ -409,7 +415,7 @@ page_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         } else {
             end = L <= 0 ? 0 : (L - 1) / kPage + 1;
         }
-        if (WIN) window_pages(L, mt, list, end, wsinks, wskip);
+        if (WIN) window_pages(L, mt, few, last, end, wsinks, wskip);
         // splits begin at even entries: a step is two pages
         const long long steps = (end + 1) / 2;
         const int z = (int)(steps * (split + 1) / nsplit);
