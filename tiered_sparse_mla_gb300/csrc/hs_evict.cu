@@ -11,7 +11,9 @@
 //   a bin has no more than CANDS keys all CTAs take them and count (mostly after one
 //   histogram). With g pages above the border and e on it before a page, min(e, room) + g
 //   kept ones are before that page; the histograms say g and e of the slices before.
-// 64 pages: 3.0 us, 500 pages 7.6 (13.7 with equal keys' places looked at one by one); 16 requests of 16,384 pages: 12.2 us (one CTA of 1,024 threads for everything
+// The pool's pages say which, a request's own are known on the device alone: 64 pages take 3.0 us in a
+// pool of up to 512 pages a request, 5.4 to 5.7 in one of 513 to 16,384. 500 pages 7.6 (13.7 with equal keys'
+// places looked at one by one); 16 requests of 16,384 pages: 12.2 us (one CTA of 1,024 threads for everything
 // 27; histograms of 2,048 bins, whose exchange takes 3 each, 23; the slices' counts in an
 // exchange of their own and loads behind the length 14.2).
 #include <atomic>

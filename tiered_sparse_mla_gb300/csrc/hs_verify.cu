@@ -9,11 +9,14 @@
 // refused children. The drawn token is the first v whose r(0) + .. + r(v) passes u_0 times
 // the sum of all.
 //
-// Only one row of V values (two with a draft's) is read in full for a request, a run of it
-// by each warp of a cluster: 64 requests of 128,000 values, 65.5 MB, 17 us, 10 of them the
-// bytes at the copy rate, 1.5 before them two dependent loads that say which row it is, 4
-// behind them the slowest CTA and the search. (The whole runs asked into L2 at the start:
-// 19.7 us. Copies of 16 bytes through shared memory, 30 us: twice the instructions.)
+// Only one row of V values (two where a draft's probabilities refuse a token) is read in full for
+// a request, a run of it by each warp of a cluster. 64 requests of 128,000 F32 values, 29 of which
+// read two rows: 47.7 MB, 7.2 us at the copy rate, take 17. Two dependent loads say which row it is
+// (1.5 us); the rows then come until 12, at about 4.5 TB/s: a warp asks for a batch or two by loads of
+// one value each, and adds them up before it asks again; the slowest CTA, the barrier and the search take the
+// rest. BF16, half the bytes, takes as long (18.6 with 31 such requests): loads are as many. (The
+// whole runs asked into L2 at the start: 19.7 us. Copies of 16 bytes through shared memory, 30 us: twice
+// the instructions.)
 //
 // A search by sums has to add the same way each time. Here a value counts in whole steps of
 // 2^-58, what is below them is cut off, and sums are integers: eight values of a lane are cut into
