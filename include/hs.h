@@ -521,10 +521,10 @@ typedef enum { HS_PROB_F32 = 0, HS_PROB_BF16 = 1 } hs_prob_dtype;
  *            them, as hs_append_rows takes them
  *   d_count  int32 [B] out: how many they are;  d_next int32 [B] out: the next token, -1 (and
  *            HS_DEVERR_INDEX_RANGE) where all of p is below 2^-58
- * Values outside [0, 1] and NaN count as the nearest of them and as 0. Both tests are exact. In what the next token is
- * drawn from, and in s, a probability counts in whole steps of 2^-58 (what is below a step is cut
- * off); sums of these are exact and end at 64. A token outside [-1, V) counts as -1
- * (HS_DEVERR_INDEX_RANGE).
+ * Values outside [0, 1] and NaN count as the nearest of them and as 0. Both tests are exact. In
+ * what the next token is drawn from, and in s, a probability counts in whole steps of 2^-58 (what
+ * is below a step is cut off); sums of these are exact and end at 64. A token outside [-1, V)
+ * counts as -1 (HS_DEVERR_INDEX_RANGE).
  * Requires B <= 65535, 1 <= T <= 64, V >= 1, rows at least V apart, pointers aligned to
  * their elements. The pool gives the device and takes the errors. */
 hs_status hs_verify_drafts(hs_pool_t pool, int32_t B, int32_t T, int32_t V, int32_t dtype,

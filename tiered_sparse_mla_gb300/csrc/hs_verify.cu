@@ -339,9 +339,9 @@ verify_kernel(const VerifyParams p) {
             }
         };
         // the lane's, at most 8; the digits' signs differ, their sum has none
-        auto sum_of = [&](uint64_t hs, uint64_t ms, uint32_t ls) {
-            const int h = __float2int_rn(both_of(hs) * 0x1p20f), m = __float2int_rn(both_of(ms) * 0x1p41f);
-            return (uint64_t)(((int64_t)h << 38) + ((int64_t)m << 17) + (int32_t)ls);
+        auto sum_of = [&](uint64_t high, uint64_t middle, uint32_t low) {
+            const int h = __float2int_rn(both_of(high) * 0x1p20f), m = __float2int_rn(both_of(middle) * 0x1p41f);
+            return (uint64_t)(((int64_t)h << 38) + ((int64_t)m << 17) + (int32_t)low);
         };
         auto plain = [&](const uint32_t (&x)[8]) {
             uint64_t h = 0, m = 0;
